@@ -412,6 +412,140 @@ dsb_status dsb_attention_decode_multi_noalloc(const float* q, int n_q_heads, con
                                               const int32_t* batch_index, int n_seq, int tokens_per_seq,
                                               const int32_t* seq_lens, float* out, void* stream);
 
+/* ---- rotary layouts, the paged append, and the 4-bit paged KV cache -----------
+ *
+ * A decode step at long contexts is bound by the bytes of its KV cache.  These
+ * calls keep K and V in 4 bits (0.27 of a 16-bit cache at head_dim 128) on the
+ * page geometry of dsb_kv_pages, write them straight from the [q | k | v] rows
+ * of a projection with the rotation on the way, attend over them, and read them
+ * back.  Batches are ragged: every sequence brings its own number of new tokens
+ * (none, one, a draft, a prompt).  They are no restatement of the pages above.
+ *
+ * Metadata of up to 960 words rides in the launch itself; such a call can be
+ * captured into a CUDA graph, which then replays that metadata.  A longer one
+ * is staged through the workspace and is DSB_ERR_UNSUPPORTED on a capturing
+ * stream.  The words of a call: rope_rotary one a token; append 3 a sequence + 2
+ * + the pages its new tokens touch; attention 8 a sequence + 1 + the pages it
+ * visits; gather 5 a sequence + 1 + the pages it reads.  The workspace must
+ * belong to the current device. */
+
+/* Scaling of the rotation's frequencies f_i = theta^(-2i/r) for contexts longer
+ * than the trained one, with s = scale_factor >= 1:
+ *   LINEAR  f_i / s
+ *   NTK     theta s^(r/(r-2)) in place of theta
+ *   BANDS   f_i keep + (f_i / s) (1 - keep) with keep =
+ *           clamp((n_i - scale_low) / (scale_high - scale_low), 0, 1) and
+ *           n_i = scale_orig_ctx f_i / (2 pi), the turns of pair i over the
+ *           original context
+ * YaRN is chosen by rope.yarn_factor > 1 and excludes these. */
+typedef enum { DSB_ROPE_UNSCALED = 0, DSB_ROPE_LINEAR = 1, DSB_ROPE_NTK = 2, DSB_ROPE_BANDS = 3 } dsb_rope_scaling;
+
+/* Rotary positions on the first r = rotary_dim dimensions of each head (0: all;
+ * even), the others unchanged.  interleaved = 0: pairs (i, i + r/2); 1: pairs
+ * (2i, 2i + 1).  rope: theta and the YaRN parameters, whose head_dim is r here. */
+typedef struct {
+  dsb_rope rope;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t scaling; /* dsb_rope_scaling */
+  float scale_factor;
+  int32_t scale_orig_ctx;
+  float scale_low;
+  float scale_high;
+} dsb_rotary;
+
+/* Rotates q and k rows in place, row t at position pos[t] (host int32[n_tok],
+ * each in [0, 2^24)).  q: device float32, row t at q + t * q_stride, heads of
+ * head_dim side by side; k alike (NULL with n_kv_heads = 0).  q and k may be
+ * parts of the same rows (the strides of a fused projection) but share no
+ * value.  head_dim even in [2, 1024].  Angles modulo one turn in 64-bit integer
+ * arithmetic, sine, cosine and rotation in float32.  Row t is bitwise equal to
+ * an n_tok = 1 call. */
+dsb_status dsb_rope_rotary(float* q, int64_t q_stride, int n_q_heads, float* k, int64_t k_stride, int n_kv_heads,
+                           int head_dim, int n_tok, const int32_t* pos, const dsb_rotary* rotary, dsb_workspace* ws,
+                           void* stream);
+
+/* The sequences of a paged call (host arrays, read during the call only).
+ * Sequence s has seq_lens[s] keys after the call, of which new_tokens[s] >= 0 are
+ * new: its token rows follow those of the sequences before it, and its token j
+ * sits at position seq_lens[s] - new_tokens[s] + j.  block_table
+ * [n_seq][max_blocks], n_blocks and window as in dsb_attention_decode_paged
+ * (window[s] > 0: a ring, which must hold window[s] + new_tokens[s] - 1 keys;
+ * n_blocks[s] may be 0 where seq_lens[s] is).  At most DSB_MAX_TOKENS new tokens
+ * in all. */
+typedef struct {
+  const int32_t* block_table;
+  int32_t max_blocks;
+  const int32_t* n_blocks;
+  const int32_t* window;
+  int32_t n_seq;
+  const int32_t* new_tokens;
+  const int32_t* seq_lens;
+} dsb_paged_batch;
+
+/* Appends the new tokens to 16-bit pages.  qkv: device float32, token row t at
+ * qkv + t * row_stride (a multiple of 4, >= (n_q_heads + 2 n_kv_heads) head_dim),
+ * holding the query heads, the key heads and the value heads.  Per-head RMS
+ * norm of q / k first where q_norm / k_norm (device float32 [head_dim]) is
+ * given, as dsb_head_rmsnorm_rope; then q is rotated in place, and k rotated and
+ * v as it is are converted (round to nearest even) and written at their
+ * positions' page rows.  The k and v parts of qkv and all other page rows keep
+ * their values.  n_q_heads may be 0.  head_dim 64 or 128.  Positions below 2^24.
+ * Two tokens of a call on one page row are DSB_ERR_INVALID_ARG. */
+dsb_status dsb_kv_append_paged(float* qkv, int64_t row_stride, int n_q_heads, const dsb_kv_pages* kv,
+                               const dsb_paged_batch* batch, const dsb_rotary* rotary, const float* q_norm,
+                               const float* k_norm, float eps, dsb_workspace* ws, void* stream);
+
+/* A pool of 4-bit pages of DSB_KV_PAGE keys (device, 16-byte aligned): n_pages *
+ * dsb_kv_q4_page_bytes(n_kv_heads, head_dim) bytes, per page and kv head one
+ * block of 128 (D + 8) bytes:
+ *   K codes   [128 keys][D/2]; dimension 2i in the low half of byte i
+ *   K (d, z)  [128 keys] two fp16
+ *   V codes   [64 key pairs][D/4 words][2 keys] 16-bit; word i of a key holds
+ *             dimensions 4i .. 4i+3, the lowest four bits first
+ *   V (d, z)  [128 keys] two fp16
+ * Each head vector has its own scale and centre, d = fp16((max - min) / 15) and
+ * z = fp16(min + 8 d); code = clamp(round-half-even((x - z) / d) + 8, 0, 15) in
+ * float32 (8 where d = 0), and the value is z + d (code - 8).  A vector that
+ * holds a NaN or an infinity is stored as NaN in every dimension; values must
+ * otherwise lie within fp16's range.  head_dim 64 or 128. */
+typedef struct {
+  void* blocks;
+  int32_t n_pages;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} dsb_kv_q4_pages;
+
+/* Bytes of one page; 0 for arguments out of range. */
+size_t dsb_kv_q4_page_bytes(int n_kv_heads, int head_dim);
+
+/* dsb_kv_append_paged into 4-bit pages. */
+dsb_status dsb_kv_append_q4(float* qkv, int64_t row_stride, int n_q_heads, const dsb_kv_q4_pages* kv,
+                            const dsb_paged_batch* batch, const dsb_rotary* rotary, const float* q_norm,
+                            const float* k_norm, float eps, dsb_workspace* ws, void* stream);
+
+/* Multi-sequence GQA decode attention over 4-bit pages, after the call's new
+ * tokens have been appended: new token j of sequence s at position p =
+ * seq_lens[s] - new_tokens[s] + j sees keys max(0, p - window[s] + 1) .. p (all
+ * up to p without a window); score = q.k / sqrt(head_dim), out = softmax(score) V
+ * with the pages' values, float32 accuracy.  q: device float32, row t at
+ * q + t * q_stride (a multiple of 4; the query part of qkv rows will do); out:
+ * device float32 [tokens][n_q_heads][head_dim].  A sequence without new tokens
+ * has no rows.  Any number of new tokens.  Partial sums of long sequences go to
+ * the workspace: dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest
+ * seq_lens) is enough.  No atomics; a sequence's rows are bitwise the same alone
+ * and in any batch. */
+dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_q4_pages* kv,
+                                   const dsb_paged_batch* batch, float* out, dsb_workspace* ws, void* stream);
+
+/* Reads keys first[s] .. first[s] + count[s] - 1 of every sequence back (host
+ * int32[n_seq]; within seq_lens[s], under a window also within what the ring
+ * still holds; new_tokens is not used) as the values they stand for, rounded to
+ * nearest even in dtype (dsb_dtype): k_out and v_out device 16-bit
+ * [sum of count][n_kv_heads][head_dim], the sequences one after the other. */
+dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* batch, const int32_t* first,
+                            const int32_t* count, int dtype, void* k_out, void* v_out, dsb_workspace* ws, void* stream);
+
 /* ---- measurement probe -------------------------------------------------------
  * The issue rate and latency of the four-way int8 dot product (__dp4a) the
  * narrow q8_0 matmul is built on, so that its arithmetic ceiling comes from a

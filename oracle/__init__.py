@@ -26,6 +26,8 @@ Modules
 q8_0       block codec (quantise / unpack / dequantise)
 matmul     narrow-batch q8_0 matmul and its int32 block dot products
 rope       pos-vector rotary embedding
+rotary     rotary pair layouts, partial heads, long-context frequency scalings
+kv_q4      the paged 4-bit KV cache: codec, page blocks, append, attention
 kv         fp32 -> fp16 / bf16 round-to-nearest-even and the batch_index scatter
 attention  multi-sequence GQA decode attention (unsplit softmax)
 glue       RMSNorm, SiLU-gate, residual add, embedding gather

@@ -1,0 +1,568 @@
+// Decode attention over the paged 4-bit KV cache (sm_103a).
+//
+// For query row r (token j of the sequence's new ones, head gi of the kv head's
+// group) and the keys k it sees (k <= len - new + j, and k > that - window under
+// a window), with K_k = z + d (c - 8) and V alike:
+//     out = sum_k softmax_k(q . K_k / sqrt D) V_k
+//
+// The codes enter both products as small signed integers, exact in fp16, and
+// the scale and offset of a key are applied outside them, in float32:
+//     q . K_k = d (sum_i q_i (c_i - 8)) + z (sum_i q_i)
+//     sum_k p_k V_k = sum_k (p_k d_k) (c_k - 8) + sum_k p_k z_k
+// q and the weights w_k = p_k d_k are split into two fp16 (hi + lo: 22 bits), and
+// the two parts are the two halves of one m16n8k16's rows: 8 query rows fill
+// the tensor product exactly, and the float32 accuracy costs nothing more.
+//
+// Work: a CTA of four warps takes units of a few pages of one (sequence, kv
+// head, tile of 8 query rows); how many pages a unit has depends on the
+// sequence's own length alone, so a sequence's rows are bitwise the same alone
+// and in a batch.  A warp takes 32 of a page's 128 keys and carries its own
+// maximum, sum and output tile through the unit: inside a unit the warps meet at
+// no barrier but those of the copies.  Pages arrive as bulk copies of whole
+// blocks, two ahead.  The four warps' results are joined at the unit's end, the
+// units' by a second kernel in unit order (a sequence of one unit needs none).
+//
+// The maximum is kept over s_k + log2 d_k (of V), so that the weights that enter
+// the fp16 split are at most 2^14 whatever the scales are, and the largest at
+// least 2^10; p_k itself and the sums over it are float32.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "dsb_kernels.h"
+#include "dsb_ptx.cuh"
+#include "dsb_q4.cuh"
+
+namespace dsbk {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 3;
+
+__device__ unsigned int g_err_attention_q4 = 0;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], __half2 b0, __half2 b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(*reinterpret_cast<const uint32_t*>(&b0)),
+        "r"(*reinterpret_cast<const uint32_t*>(&b1)));
+}
+
+// x0, x1 as hi + lo fp16 pairs.
+__device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Where a CTA is in its list of items: one unit of one (sequence, kv head, row
+// tile), and the page inside it.
+struct Cursor {
+  int item, s, h, rt, u, units, pg, pg_end;
+  Q4Seq q;
+
+  __device__ __forceinline__ void load(const int32_t* meta) {
+    const int32_t* p = meta + s * kQ4SeqWords;
+    q.item_off = p[0];
+    q.tok0 = p[1];
+    q.n_new = p[2];
+    q.len = p[3];
+    q.window = p[4];
+    q.chunk0 = p[5];
+    q.pg_at = p[6];
+    q.u_pages = p[7];
+  }
+  __device__ __forceinline__ void place(int G) {
+    const int pages = ((q.len - 1) >> 7) - q.chunk0 + 1;
+    units = (pages + q.u_pages - 1) / q.u_pages;
+    const int tiles = (G * q.n_new + kQ4Rows - 1) / kQ4Rows;
+    const int rel = item - q.item_off, x = rel / units;
+    u = rel - x * units;
+    h = x / tiles;
+    rt = x - h * tiles;
+    pg = u * q.u_pages;
+    pg_end = min(pg + q.u_pages, pages);
+  }
+  __device__ __forceinline__ void start(const int32_t* meta, int n_seq, int G, int first) {
+    item = first;
+    int lo = 0, hi = n_seq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (meta[mid * kQ4SeqWords] <= item)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s = lo;
+    load(meta);
+    place(G);
+  }
+  // The next item (one that exists).
+  __device__ __forceinline__ void next(const int32_t* meta, int n_seq, int G) {
+    ++item;
+    if (s + 1 < n_seq && item >= meta[(s + 1) * kQ4SeqWords]) {
+      ++s;
+      load(meta);
+    }
+    place(G);
+  }
+};
+
+template <int D>
+struct Q4Smem {
+  static constexpr int rows = D + 16;  // floats between the joined rows: two rows' quads on different banks
+  static constexpr int join = kStages * Q4Block<D>::bytes;
+  static constexpr int stat = join + kWarps * kQ4Rows * rows * 4;
+  static constexpr int bars = stat + 2 * kWarps * kQ4Rows * 4;
+  static constexpr int bytes = bars + 2 * kStages * 8;
+};
+
+// One thread requests the page the cursor is at: its block's four parts up to
+// the sequence's last key (rounded up to four keys: 16-byte pieces), or, where
+// the page is full, the block in one piece.
+template <int D>
+__device__ __forceinline__ void request(const Cursor& c, const int32_t* meta, const uint8_t* pool, int hkv, uint8_t* dst,
+                                        uint64_t* bar) {
+  using B = Q4Block<D>;
+  const int page = meta[c.q.pg_at + c.pg];
+  const uint8_t* src = pool + ((size_t)page * hkv + c.h) * B::bytes;
+  const int keys = min(kQ4Page, (c.q.len - ((c.q.chunk0 + c.pg) << 7) + 3) & ~3);
+  if (keys == kQ4Page) {
+    mbar_arrive_expect_tx(bar, B::bytes);
+    bulk_g2s(dst, src, B::bytes, bar);
+  } else {
+    const uint32_t codes = keys * (D / 2), nums = keys * 4;
+    mbar_arrive_expect_tx(bar, 2 * (codes + nums));
+    bulk_g2s(dst, src, codes, bar);
+    bulk_g2s(dst + B::kz, src + B::kz, nums, bar);
+    bulk_g2s(dst + B::v, src + B::v, codes, bar);
+    bulk_g2s(dst + B::vz, src + B::vz, nums, bar);
+  }
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
+    const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint8_t* __restrict__ pool, int n_seq,
+    float scale_log2e, int max_units, float* __restrict__ partials, float* __restrict__ out,
+    const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+  using B = Q4Block<D>;
+  using S = Q4Smem<D>;
+  constexpr int KS = D / 16;   // 16-dimension steps of q . K
+  constexpr int W = D / 32;    // 32-bit words of a thread's piece of a K row, and of a V key pair
+  constexpr int NT = D / 8;    // 8-dimension tiles of the output
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* join = reinterpret_cast<float*>(smem + S::join);
+  float* stat = reinterpret_cast<float*>(smem + S::stat);  // [warp][8] maxima, then [warp][8] sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bars);
+  uint64_t* empty = full + kStages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int G = hq / hkv;
+  const int32_t* meta = N > 1 ? words.w : meta_dev;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const long long total = meta[n_seq * kQ4SeqWords];
+  const int i0 = (int)(total * blockIdx.x / gridDim.x), i1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  if (i0 >= i1) return;
+
+  // Thread 0 runs kStages - 1 pages ahead of the others.
+  Cursor ahead;
+  int asked = 0;
+  bool more = true;
+  auto ask = [&]() {
+    const int st = asked % kStages, use = asked / kStages;
+    if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1)) g_err_attention_q4 = 1u;
+    request<D>(ahead, meta, pool, hkv, smem + st * B::bytes, &full[st]);
+    ++asked;
+    if (++ahead.pg == ahead.pg_end) {
+      if (ahead.item + 1 < i1)
+        ahead.next(meta, n_seq, G);
+      else
+        more = false;
+    }
+  };
+  if (tid == 0) {
+    ahead.start(meta, n_seq, G, i0);
+    for (int i = 0; i < kStages - 1 && more; ++i) ask();
+  }
+
+  Cursor cur;
+  cur.start(meta, n_seq, G, i0);
+  uint32_t qf[KS][4];            // q of row g as the products' left operand: rows 0..7 hi, 8..15 lo
+  float row_scale = 1.0f, row_sum = 0.0f;
+  int key_hi = 0, key_lo = 0;    // the keys row g sees
+  int old_s = -1, old_h = -1, old_rt = -1;
+  int n = 0;                     // pages done
+  for (;;) {
+    const Q4Seq& sq = cur.q;
+    const int R = G * sq.n_new;
+    if (cur.s != old_s || cur.h != old_h || cur.rt != old_rt) {
+      old_s = cur.s, old_h = cur.h, old_rt = cur.rt;
+      const int r = cur.rt * kQ4Rows + g, j = r / G, gi = r - j * G;
+      const bool live = r < R;
+      // a row past the last: q = 0, the keys of the last token; never written
+      key_hi = live ? sq.len - sq.n_new + j : sq.len - 1;
+      key_lo = sq.window > 0 ? key_hi - sq.window + 1 : 0;
+      float x[D / 4];
+      const float* src = q + (size_t)(sq.tok0 + j) * q_stride + (size_t)(cur.h * G + gi) * D + c * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const float4 v = live ? __ldcg(reinterpret_cast<const float4*>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
+        x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
+      }
+      // the row over a power of two that brings its largest value to [1, 2): the
+      // split keeps its 22 bits whatever q's size
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
+      row_scale = __uint_as_float((uint32_t)e << 23);
+      const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      row_sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) {
+        x[i] *= inv;
+        row_sum += x[i];
+      }
+      row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 1);
+      row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
+      // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4)
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          split(x[8 * w + 2 * b], x[8 * w + 2 * b + 4], qf[2 * w + b][0], qf[2 * w + b][1]);
+          split(x[8 * w + 2 * b + 1], x[8 * w + 2 * b + 5], qf[2 * w + b][2], qf[2 * w + b][3]);
+        }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
+    float M = -INFINITY, lsum = 0.0f, zsum = 0.0f;
+    // what any row of the tile can see, and what every row sees
+    const int j0 = cur.rt * kQ4Rows / G, j1 = min(cur.rt * kQ4Rows + kQ4Rows - 1, R - 1) / G;
+    const int first_hi = sq.len - sq.n_new + j0, last_hi = sq.len - sq.n_new + j1;
+    const int any_lo = sq.window > 0 ? first_hi - sq.window + 1 : 0, all_lo = sq.window > 0 ? sq.len - sq.window : 0;
+
+    for (int pg = cur.pg; pg < cur.pg_end; ++pg, ++n) {
+      const int st = n % kStages;
+      if (!mbar_wait(&full[st], (n / kStages) & 1)) g_err_attention_q4 = 1u;
+      __syncwarp();
+      const uint8_t* blk = smem + st * B::bytes;
+      const int key0 = ((sq.chunk0 + pg) << 7) + 32 * warp;
+      if (key0 <= last_hi && key0 + 31 >= any_lo) {
+        const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
+        // ---- scores of 32 keys, four tiles of eight
+        float sc[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
+          uint32_t kw[W];
+          const uint8_t* kp = blk + (32 * warp + 8 * t + g) * (D / 2) + c * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kp);
+            kw[0] = v.x, kw[1] = v.y, kw[2] = v.z, kw[3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(kp);
+            kw[0] = v.x, kw[1] = v.y;
+          }
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            __half2 h[4];
+            q4_unpack(kw[w], h);
+            mma(sc[t], qf[2 * w], h[0], h[1]);
+            mma(sc[t], qf[2 * w + 1], h[2], h[3]);
+          }
+        }
+        // s = d acc + z sum(q) for keys 8t + 2c, + 1 of row g; t = s + log2 d(V)
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int at = (32 * warp + 8 * t + 2 * c) * 4;
+          const uint2 kz = *reinterpret_cast<const uint2*>(blk + B::kz + at);
+          const uint2 vz = *reinterpret_cast<const uint2*>(blk + B::vz + at);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 dz = __half22float2(*reinterpret_cast<const __half2*>(e ? &kz.y : &kz.x));
+            const float vd = __low2float(*reinterpret_cast<const __half2*>(e ? &vz.y : &vz.x));
+            const float s = __fmaf_rn(dz.x, sc[t][e] + sc[t][2 + e], dz.y * row_sum);
+            x[2 * t + e] = s;
+            float w = __fmaf_rn(row_scale, s, fmaxf(lg2(vd), -24.0f));
+            if (!whole) {
+              const int key = key0 + 8 * t + 2 * c + e;
+              if (key > key_hi || key < key_lo) w = -INFINITY;
+            }
+            top = fmaxf(top, w);
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // The reference is set 2^10 below the largest weight and moves only when
+        // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
+        // coarser than 2^-35 of the largest weight.
+        if (__any_sync(0xFFFFFFFFu, top > M + 14.0f)) {
+          const float to = top > M + 14.0f ? top - 10.0f : M;
+          const float f = M == -INFINITY ? 0.0f : ex2(M - to);
+          M = to;
+          lsum *= f;
+          zsum *= f;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][e] *= f;
+        }
+        // ---- weights, and 16 keys at a time their product with V
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          uint32_t a[4];
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) {
+            const int t = 2 * p + tt;
+            const uint2 vz = *reinterpret_cast<const uint2*>(blk + B::vz + (32 * warp + 8 * t + 2 * c) * 4);
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2 dz = __half22float2(*reinterpret_cast<const __half2*>(e ? &vz.y : &vz.x));
+              float pr = ex2(__fmaf_rn(row_scale, x[2 * t + e], -M));
+              if (!whole) {
+                const int key = key0 + 8 * t + 2 * c + e;
+                if (key > key_hi || key < key_lo) pr = dz.x = dz.y = 0.0f;  // its numbers may be anything
+              }
+              lsum += pr;
+              zsum = __fmaf_rn(pr, dz.y, zsum);
+              w[e] = pr * dz.x;
+            }
+            split(w[0], w[1], a[2 * tt], a[2 * tt + 1]);
+          }
+          uint32_t v0[W], v1[W];
+          const uint8_t* vp = blk + B::v + (16 * warp + 8 * p + c) * D + g * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 u0 = *reinterpret_cast<const uint4*>(vp), u1 = *reinterpret_cast<const uint4*>(vp + 4 * D);
+            v0[0] = u0.x, v0[1] = u0.y, v0[2] = u0.z, v0[3] = u0.w;
+            v1[0] = u1.x, v1[1] = u1.y, v1[2] = u1.z, v1[3] = u1.w;
+          } else {
+            const uint2 u0 = *reinterpret_cast<const uint2*>(vp), u1 = *reinterpret_cast<const uint2*>(vp + 4 * D);
+            v0[0] = u0.x, v0[1] = u0.y;
+            v1[0] = u1.x, v1[1] = u1.y;
+          }
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            __half2 h0[4], h1[4];
+            q4_unpack(v0[w], h0);
+            q4_unpack(v1[w], h1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, h0[i], h1[i]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (tid == 0 && more) ask();
+    }
+
+    // ---- the unit's end: join the four warps' rows
+    lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 1);
+    lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 2);
+    zsum += __shfl_xor_sync(0xFFFFFFFFu, zsum, 1);
+    zsum += __shfl_xor_sync(0xFFFFFFFFu, zsum, 2);
+    if (c == 0) {
+      stat[warp * kQ4Rows + g] = M;
+      stat[(kWarps + warp) * kQ4Rows + g] = lsum;
+    }
+    {
+      // tile t, element e of this thread is dimension D/8 (2c + e) + t; four tiles
+      // make a 16-byte piece, and the pieces of a c are swizzled so that the four
+      // c's of a row hit different banks
+      float* dst = join + (warp * kQ4Rows + g) * S::rows + c * (D / 4);
+      const int sw = D == 128 ? c : c >> 1;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < NT / 4; ++i) {
+          const int piece = e * (NT / 4) + i;
+          *reinterpret_cast<float4*>(dst + 4 * (piece ^ sw)) =
+              make_float4(o[4 * i][e] + o[4 * i][2 + e] + zsum, o[4 * i + 1][e] + o[4 * i + 1][2 + e] + zsum,
+                          o[4 * i + 2][e] + o[4 * i + 2][2 + e] + zsum, o[4 * i + 3][e] + o[4 * i + 3][2 + e] + zsum);
+        }
+    }
+    __syncthreads();
+    {
+      const int dim = tid % D, cc = dim / (D / 4), in = dim % (D / 4);
+      const int place = cc * (D / 4) + 4 * ((in >> 2) ^ (D == 128 ? cc : cc >> 1)) + (in & 3);
+#pragma unroll
+      for (int i = tid / D; i < kQ4Rows; i += kThreads / D) {
+        const int r = cur.rt * kQ4Rows + i;
+        if (r >= R) break;
+        float top = stat[i];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, stat[w * kQ4Rows + i]);
+        float l = 0.0f, acc = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = stat[w * kQ4Rows + i];
+          // a warp whose keys were all NaN has no maximum but a NaN sum
+          const float f = mw == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : ex2(mw - top);
+          const float lw = stat[(kWarps + w) * kQ4Rows + i];
+          l = __fmaf_rn(f, lw, l);
+          acc = __fmaf_rn(f, join[(w * kQ4Rows + i) * S::rows + place], acc);
+        }
+        const int j = r / G, head = cur.h * G + r - j * G;
+        const size_t row = (size_t)(sq.tok0 + j) * hq + head;
+        if (cur.units == 1) {
+          out[row * D + dim] = __fdiv_rn(acc, l);
+        } else {
+          float* dst = partials + (row * max_units + cur.u) * (D + 2);
+          dst[2 + dim] = acc;
+          if (dim == 0) {
+            dst[0] = top;
+            dst[1] = l;
+          }
+        }
+      }
+    }
+    if (cur.item + 1 >= i1) break;
+    cur.next(meta, n_seq, G);
+    __syncthreads();
+  }
+}
+
+// One CTA of D threads per (token row, query head): the units' (maximum, sum,
+// row) joined in unit order.  Sequences of one unit are done already.
+template <int D, int N>
+__global__ void __launch_bounds__(D) attention_q4_merge_kernel(const float* __restrict__ partials, int hq, int n_seq,
+                                                               int max_units, float* __restrict__ out,
+                                                               const __grid_constant__ ParamWords<N> words,
+                                                               const int32_t* __restrict__ meta_dev) {
+  const int32_t* meta = N > 1 ? words.w : meta_dev;
+  const int t = blockIdx.x, head = blockIdx.y, dim = threadIdx.x, lane = dim & 31;
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (meta[mid * kQ4SeqWords + 1] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int32_t* p = meta + lo * kQ4SeqWords;
+  const int pages = ((p[3] - 1) >> 7) - p[5] + 1, units = (pages + p[7] - 1) / p[7];
+  pdl_wait();
+  pdl_trigger();
+  if (units == 1) return;
+  const size_t row = (size_t)t * hq + head;
+  const float* base = partials + row * max_units * (D + 2);
+  float M = -INFINITY;
+  for (int u = lane; u < units; u += 32) M = fmaxf(M, __ldcg(base + (size_t)u * (D + 2)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float l = 0.0f, acc = 0.0f;
+#pragma unroll 8
+  for (int u = 0; u < units; ++u) {
+    const float* b = base + (size_t)u * (D + 2);
+    const float mu = __ldcg(b), lu = __ldcg(b + 1), v = __ldcg(b + 2 + dim);
+    const float f = mu == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2(mu - M);
+    l = __fmaf_rn(f, lu, l);
+    acc = __fmaf_rn(f, v, acc);
+  }
+  out[row * D + dim] = __fdiv_rn(acc, l);
+}
+
+template <int D, int N>
+cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
+  constexpr int smem = Q4Smem<D>::bytes;
+  auto kern = attention_q4_kernel<D, N>;
+  int resident = 0;
+  {
+    static std::mutex mu;
+    static int cache[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64) resident = cache[dev];
+    if (resident == 0) {
+      int per_sm = 0, sms = 0;
+      if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+      if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem)) != cudaSuccess) return e;
+      if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+      resident = (per_sm > 0 ? per_sm : 1) * sms;
+      if (dev >= 0 && dev < 64) cache[dev] = resident;
+    }
+  }
+  ParamWords<N> w;
+  for (int i = 0; i < N; ++i) w.w[i] = N > 1 && i < meta.n_words ? meta.host[i] : 0;
+  const unsigned grid = (unsigned)(a.items < resident ? a.items : resident);
+  const float scale = (float)(1.4426950408889634 / sqrt((double)D));
+  cudaError_t e = launch_kernel(kern, dim3(grid), dim3(kThreads), smem, st, a.q, a.q_stride, a.hq, a.hkv,
+                                static_cast<const uint8_t*>(a.pool), a.n_seq, scale, a.max_units, a.partials, a.out, w,
+                                meta.dev);
+  if (e != cudaSuccess || a.max_units == 1) return e;
+  // the join's CTAs may start while the last units run (they wait for them)
+  const bool was = pdl();
+  set_pdl(true);
+  e = launch_kernel(attention_q4_merge_kernel<D, N>, dim3((unsigned)a.n_tok, (unsigned)a.hq), dim3(D), 0, st, a.partials,
+                    a.hq, a.n_seq, a.max_units, a.out, w, meta.dev);
+  set_pdl(was);
+  return e;
+}
+
+}  // namespace
+
+// Long units cost less joining, short ones fill the GPU with few sequences.  A
+// sequence of many row tiles fills it without being cut.
+int q4_unit_pages(int n, int tiles) {
+  if (n <= 2 || tiles >= 64) return n;
+  if (n <= 16) return 1;
+  if (n <= 128) return 2;
+  return n <= 512 ? 4 : (n + 127) / 128;
+}
+
+cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st) {
+  if (a.items == 0) return cudaSuccess;
+  if (head_dim == 128) return meta.dev ? attention_go<128, 1>(a, meta, st) : attention_go<128, kParamWords>(a, meta, st);
+  if (head_dim == 64) return meta.dev ? attention_go<64, 1>(a, meta, st) : attention_go<64, kParamWords>(a, meta, st);
+  return cudaErrorInvalidValue;
+}
+
+unsigned int read_clear_error_attention_q4() {
+  unsigned int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_attention_q4, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  cudaMemcpyToSymbol(g_err_attention_q4, &z, sizeof z);
+  return v;
+}
+
+}  // namespace dsbk

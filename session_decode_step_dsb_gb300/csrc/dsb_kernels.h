@@ -202,4 +202,85 @@ cudaError_t launch_noalloc_table(const int32_t* batch_index, const int32_t* seq_
 unsigned int read_clear_error_matmul();
 unsigned int read_clear_error_attention();
 
+// ---- rotary layouts, paged append, 4-bit KV (csrc/rotary.cu, csrc/attention_q4.cu, csrc/gather_q4.cu)
+
+// A call's metadata words: up to kParamWords of them ride in the kernel's
+// parameters (no copy, and a captured launch keeps its own), more are staged in
+// device memory.  Kernels take both forms; ParamWords<1> means the staged one.
+constexpr int kParamWords = 960;
+template <int N>
+struct ParamWords {
+  int32_t w[N];
+};
+struct MetaArg {
+  const int32_t* dev = nullptr;   // staged words, or NULL:
+  const int32_t* host = nullptr;  // words for the parameters
+  int n_words = 0;
+};
+
+// Rotation of the first rd dimensions of a head: turns per position of each
+// pair as 64-bit fractions of a turn, the pair layout, the factor on the result.
+struct RotaryTable {
+  unsigned long long turns[kRopeMaxPairs];
+  int rd;
+  int interleaved;
+  float gain;
+};
+// freq: rd / 2 angles per position, in radians.
+void rotary_table(const double* freq, int rd, bool interleaved, float gain, RotaryTable* out);
+
+// Metadata: pos[n_tok].
+cudaError_t launch_rope_rotary(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,
+                               int n_tok, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st);
+
+enum class KvStore { kF16, kBF16, kQ4 };
+struct AppendArgs {
+  float* qkv;
+  long long stride;  // floats between token rows
+  int hq, hkv;
+  void* kc;          // page pool (K and V of a 4-bit pool)
+  void* vc;          // V pool of 16-bit pages
+  const float* q_norm;
+  const float* k_norm;
+  float eps;
+  int n_seq, n_tok;
+};
+// Metadata: tok_off[n_seq + 1] | pos0[n_seq] | pg_off[n_seq + 1] | pages.
+cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, const RotaryTable& rot,
+                             const MetaArg& meta, cudaStream_t st);
+
+// One sequence of a 4-bit attention call, in its metadata; n_seq of them, then
+// the total item count, then the visited pages of all sequences.  A sequence's
+// work items are (kv head, tile of 8 query rows, unit of u_pages pages).
+struct Q4Seq {
+  int32_t item_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
+};
+constexpr int kQ4SeqWords = 8;
+constexpr int kQ4Rows = 8;  // query rows of an item
+// Pages per unit of a sequence that visits n of them with `tiles` tiles of rows.
+int q4_unit_pages(int n, int tiles);
+struct Q4AttnArgs {
+  const float* q;
+  long long q_stride;
+  int hq, hkv;
+  const void* pool;
+  int n_seq, n_tok;
+  long long items;
+  int max_units;    // units of the sequence with the most of them
+  float* partials;  // [n_tok][hq][max_units][head_dim + 2]
+  float* out;       // [n_tok][hq][head_dim]
+};
+cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st);
+unsigned int read_clear_error_attention_q4();
+
+// One sequence of a read-back; n_seq of them, then the total page count, then
+// the pages of all sequences.
+struct Q4Span {
+  int32_t page_off, first, count, row0, pg_at;
+};
+constexpr int kQ4SpanWords = 5;
+// dtype: DSB_F16 or DSB_BF16; k, v: [rows][hkv][head_dim].
+cudaError_t launch_gather_q4(const void* pool, int hkv, int head_dim, int n_seq, long long pages, int dtype, void* k,
+                             void* v, const MetaArg& meta, cudaStream_t st);
+
 }  // namespace dsbk

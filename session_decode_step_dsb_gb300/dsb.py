@@ -56,6 +56,24 @@ class RopeC(ctypes.Structure):
                 ("yarn_beta_fast", ctypes.c_float), ("yarn_beta_slow", ctypes.c_float)]
 
 
+class RotaryC(ctypes.Structure):
+    _fields_ = [("rope", RopeC), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("scale_factor", ctypes.c_float), ("scale_orig_ctx", ctypes.c_int32),
+                ("scale_low", ctypes.c_float), ("scale_high", ctypes.c_float)]
+
+
+class KVQ4Pages(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class PagedBatchC(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.POINTER(ctypes.c_int32)), ("max_blocks", ctypes.c_int32),
+                ("n_blocks", ctypes.POINTER(ctypes.c_int32)), ("window", ctypes.POINTER(ctypes.c_int32)),
+                ("n_seq", ctypes.c_int32), ("new_tokens", ctypes.POINTER(ctypes.c_int32)),
+                ("seq_lens", ctypes.POINTER(ctypes.c_int32))]
+
+
 class Yarn(NamedTuple):
     """YaRN RoPE parameters: scale ``factor`` > 1 over the original context
     ``orig_ctx``, ramp bounds ``beta_fast`` / ``beta_slow`` (rotation counts)."""
@@ -563,6 +581,205 @@ def rope_kv_write(qkv, n_q_heads: int, kv: KVCache, batch_index, tokens_per_seq:
                                    ctypes.byref(r), _ptr(q_norm), _ptr(k_norm), float(eps), ws.handle,
                                    _stream(stream)))
     return qkv
+
+
+# ------------------------------- rotary layouts, paged append, 4-bit paged KV
+SIGNATURES.update({
+    "dsb_rope_rotary": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _I, _PI32, ctypes.POINTER(RotaryC), _P, _P]),
+    "dsb_kv_append_paged": (_I, [_P, _I64, _I, ctypes.POINTER(KVPages), ctypes.POINTER(PagedBatchC),
+                                 ctypes.POINTER(RotaryC), _P, _P, _F, _P, _P]),
+    "dsb_kv_q4_page_bytes": (ctypes.c_size_t, [_I, _I]),
+    "dsb_kv_append_q4": (_I, [_P, _I64, _I, ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC),
+                              ctypes.POINTER(RotaryC), _P, _P, _F, _P, _P]),
+    "dsb_attention_decode_q4": (_I, [_P, _I64, _I, ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC), _P, _P,
+                                     _P]),
+    "dsb_kv_gather_q4": (_I, [ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC), _PI32, _PI32, _I, _P, _P, _P,
+                              _P]),
+})
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "bands": 3}
+
+
+class Rotary:
+    """Description of a rotary position embedding (``dsb_rotary``): base
+    ``theta``, the first ``rotary_dim`` dimensions of each head (0: all) in
+    pairs (i, i + r/2) or, ``interleaved``, (2i, 2i + 1).  ``scaling``: None,
+    ``"linear"`` or ``"ntk"`` with ``factor``, ``"bands"`` with ``factor``,
+    ``orig_ctx``, ``low``, ``high``; or ``yarn`` (a :class:`Yarn`)."""
+
+    def __init__(self, theta: float = 10000.0, rotary_dim: int = 0, interleaved: bool = False, scaling=None,
+                 factor: float = 1.0, orig_ctx: int = 0, low: float = 0.0, high: float = 0.0, yarn=None):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+        self.c = RotaryC(rope_params(theta, yarn), int(rotary_dim), int(bool(interleaved)), ROPE_SCALINGS[scaling],
+                         float(factor), int(orig_ctx), float(low), float(high))
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedBatch:
+    """The sequences of one paged call or of every layer of one step
+    (``dsb_paged_batch``; host arrays, copied): block tables ``[n_seq,
+    max_blocks]``, block counts, windows, new tokens and lengths after the
+    call, one entry for each sequence."""
+
+    def __init__(self, block_table, n_blocks, window, new_tokens, seq_lens):
+        bt = np.array(block_table, dtype=np.int32, order="C")
+        if bt.ndim != 2:
+            raise ValueError("block_table is [n_seq, max_blocks]")
+        n = bt.shape[0]
+        self._arrays = [bt]
+        ptrs = [bt.ctypes.data_as(_PI32)]
+        for name, a in (("n_blocks", n_blocks), ("window", window), ("new_tokens", new_tokens),
+                        ("seq_lens", seq_lens)):
+            arr = np.array(a, dtype=np.int32).reshape(-1)
+            if arr.size != n:
+                raise ValueError(f"{name} has {arr.size} entries, needs {n}")
+            self._arrays.append(arr)
+            ptrs.append(arr.ctypes.data_as(_PI32))
+        self.n_seq = n
+        self.n_tok = int(self._arrays[3].sum())
+        self.c = PagedBatchC(ptrs[0], bt.shape[1], ptrs[1], ptrs[2], n, ptrs[3], ptrs[4])
+        self.ref = ctypes.byref(self.c)
+
+
+def _rows(t, rows: int, width: int, name: str):
+    """Row stride of float32 ``t`` seen as ``rows`` rows of ``width`` values,
+    contiguous in a row (rows may lie further apart)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32, got {t.dtype}")
+    if t.dim() < 2 or t.shape[0] != rows or t[0:1].numel() != min(rows, 1) * width:
+        raise ValueError(f"{name} must be {rows} rows of {width} values, got {tuple(t.shape)}")
+    if rows and not t[0].is_contiguous():
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return t.stride(0) if rows > 1 else width
+
+
+def _dev_ptr(t, device, name: str):
+    """Data pointer of ``t``, which must live on ``device``."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must live on {device}, a CUDA device, got {t.device}")
+    return t.data_ptr()
+
+
+def _current_device(t, name: str):
+    """Device of ``t``; it must be the current CUDA device, on which the
+    library launches."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def rope_rotary(q, k, pos, rotary: Rotary, ws: Workspace, stream=None):
+    """Rotates ``q[n_tok, Hq, D]`` and ``k[n_tok, Hkv, D]`` (k may be None) in
+    place by ``pos``; rows may lie apart (parts of a fused projection)."""
+    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
+        raise ValueError("q is [n_tok, Hq, D] and k [n_tok, Hkv, D]")
+    n_tok, hq, d = q.shape
+    hkv = 0 if k is None else k.shape[1]
+    qs = _rows(q, n_tok, hq * d, "q")
+    ks = 0 if k is None else _rows(k, n_tok, hkv * d, "k")
+    arr, p = _i32(pos, n_tok, "pos")
+    dev = _current_device(q, "q")
+    _check(lib().dsb_rope_rotary(q.data_ptr(), qs, hq, None if k is None else _dev_ptr(k, dev, "k"), ks, hkv, d, n_tok,
+                                 p, rotary.ref, ws.handle, _stream(stream)))
+
+
+def _append(fn, qkv, n_q_heads: int, kv, batch: PagedBatch, rotary: Rotary, ws: Workspace, q_norm, k_norm, eps, stream):
+    stride = _rows(qkv, batch.n_tok, (n_q_heads + 2 * kv.n_kv_heads) * kv.head_dim, "qkv")
+    dev = _current_device(qkv, "qkv")
+    norms = []
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        _need_opt(w, 4 * kv.head_dim, name, "f32")
+        if w is not None and not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        norms.append(None if w is None else _dev_ptr(w, dev, name))
+    for t in kv._tensors:
+        _dev_ptr(t, dev, "the page pool")
+    _check(fn(qkv.data_ptr(), stride, n_q_heads, ctypes.byref(kv), batch.ref, rotary.ref, norms[0], norms[1],
+              float(eps), ws.handle, _stream(stream)))
+    return qkv
+
+
+def kv_append_paged(qkv, n_q_heads: int, kv: KVPages, batch: PagedBatch, rotary: Rotary, ws: Workspace, q_norm=None,
+                    k_norm=None, eps: float = 0.0, stream=None):
+    """Appends the new tokens' ``qkv[n_tok, (Hq + 2 Hkv) * D]`` rows to 16-bit
+    pages: (optional per-head RMS norm,) q rotated in place, k rotated and v
+    converted and written to their page rows."""
+    return _append(lib().dsb_kv_append_paged, qkv, n_q_heads, kv, batch, rotary, ws, q_norm, k_norm, eps, stream)
+
+
+def kv_q4_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one 4-bit page of 128 keys (0: not served)."""
+    return lib().dsb_kv_q4_page_bytes(n_kv_heads, head_dim)
+
+
+def kv_q4_pages(pool, head_dim: int) -> KVQ4Pages:
+    """Describe a device pool of 4-bit pages, uint8 ``[n_pages, Hkv, 128 * (D +
+    8)]``; the returned struct keeps the tensor alive for as long as it lives."""
+    _need(pool, 0, "pool", "u8")
+    if pool.dim() != 3 or pool.shape[2] != KV_PAGE * (head_dim + 8):
+        raise ValueError(f"pool must be [n_pages, Hkv, {KV_PAGE * (head_dim + 8)}], got {tuple(pool.shape)}")
+    kv = KVQ4Pages(_ptr(pool), pool.shape[0], pool.shape[1], head_dim)
+    kv._tensors = (pool,)
+    return kv
+
+
+def kv_append_q4(qkv, n_q_heads: int, kv: KVQ4Pages, batch: PagedBatch, rotary: Rotary, ws: Workspace, q_norm=None,
+                 k_norm=None, eps: float = 0.0, stream=None):
+    """:func:`kv_append_paged` into 4-bit pages."""
+    return _append(lib().dsb_kv_append_q4, qkv, n_q_heads, kv, batch, rotary, ws, q_norm, k_norm, eps, stream)
+
+
+def attention_decode_q4(q, kv: KVQ4Pages, batch: PagedBatch, ws: Workspace, out=None, stream=None):
+    """Decode attention over 4-bit pages: float32 ``out[n_tok, Hq, D]`` of
+    ``q[n_tok, Hq, D]`` (rows may lie apart), the batch's new tokens in order."""
+    import torch
+    if q.dim() != 3 or q.shape[2] != kv.head_dim:
+        raise ValueError(f"q must be [n_tok, Hq, head_dim={kv.head_dim}], got {tuple(q.shape)}")
+    n_tok, hq, d = q.shape
+    stride = _rows(q, batch.n_tok, hq * d, "q")
+    dev = _current_device(q, "q")
+    if out is None:
+        out = torch.empty((n_tok, hq, d), dtype=torch.float32, device=dev)
+    _need(out, 4 * n_tok * hq * d, "out", "f32")
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _dev_ptr(kv._tensors[0], dev, "the page pool")
+    _check(lib().dsb_attention_decode_q4(q.data_ptr(), stride, hq, ctypes.byref(kv), batch.ref,
+                                         _dev_ptr(out, dev, "out"), ws.handle, _stream(stream)))
+    return out
+
+
+def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws: Workspace, k=None, v=None,
+                 stream=None):
+    """Keys ``first[s] .. first[s] + count[s] - 1`` of every sequence read back:
+    ``(k, v)``, each 16-bit ``[sum(count), Hkv, D]`` of ``dtype`` (DSB_F16 or
+    DSB_BF16), the values the 4-bit rows stand for."""
+    import torch
+    fa, pf = _i32(first, batch.n_seq, "first")
+    ca, pc = _i32(count, batch.n_seq, "count")
+    kinds = {DSB_F16: torch.float16, DSB_BF16: torch.bfloat16}
+    if dtype not in kinds:
+        raise ValueError(f"dtype must be DSB_F16 or DSB_BF16, got {dtype}")
+    dev = _current_device(kv._tensors[0], "the page pool")
+    shape = (max(int(ca.sum()), 0), kv.n_kv_heads, kv.head_dim)
+    outs = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            t = torch.empty(shape, dtype=kinds[dtype], device=dev)
+        _need(t, 2 * shape[0] * shape[1] * shape[2], name)
+        if t.dtype != kinds[dtype] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {kinds[dtype]}")
+        outs.append(t)
+    _check(lib().dsb_kv_gather_q4(ctypes.byref(kv), batch.ref, pf, pc, dtype, _dev_ptr(outs[0], dev, "k"),
+                                  _dev_ptr(outs[1], dev, "v"), ws.handle, _stream(stream)))
+    return outs[0], outs[1]
 
 
 # ---------------------------------------------------------------- decode step
