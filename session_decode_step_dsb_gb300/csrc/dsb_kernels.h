@@ -224,10 +224,10 @@ struct RotaryTable {
   unsigned long long turns[kRopeMaxPairs];
   int rd;
   int interleaved;
-  float gain;
+  double gain;
 };
 // freq: rd / 2 angles per position, in radians.
-void rotary_table(const double* freq, int rd, bool interleaved, float gain, RotaryTable* out);
+void rotary_table(const double* freq, int rd, bool interleaved, double gain, RotaryTable* out);
 
 // Metadata: pos[n_tok].
 cudaError_t launch_rope_rotary(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,

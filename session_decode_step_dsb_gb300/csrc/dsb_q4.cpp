@@ -78,7 +78,8 @@ void build_rotary(const dsb_rotary& r, int head_dim, dsbk::RotaryTable* out) {
       f.f[i] = f.f[i] * keep + f.f[i] / s * (1.0 - keep);
     }
   }
-  dsbk::rotary_table(f.f, rd, r.interleaved != 0, f.mscale, out);
+  const double gain = r.rope.yarn_factor > 1.0f ? 0.1 * std::log((double)r.rope.yarn_factor) + 1.0 : 1.0;
+  dsbk::rotary_table(f.f, rd, r.interleaved != 0, gain, out);
 }
 
 dsb_status check_workspace(const dsb_workspace* ws) {

@@ -2,7 +2,7 @@
 // write and read it.
 //
 // A head vector x of D values is stored as D codes in 0..15 and two fp16
-// numbers, one pair per key and head: d = fp16((max - min) / 15),
+// numbers, one pair per key and head: d = fp16((max - min) * fl(1/15)),
 // z = fp16(min + 8 d), code = clamp(round-half-even((x - z) / d) + 8, 0, 15)
 // (8 where d is 0), and stands for z + d (code - 8).  Centring the codes on 8
 // lets a matrix product run on small signed integers (exact in fp16) with the

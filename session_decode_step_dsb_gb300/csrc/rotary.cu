@@ -7,12 +7,17 @@
 //
 // The angle.  f_i / 2 pi, the turns per position, is kept as a 64-bit fraction
 // of a turn: p times it modulo 2^64 is the angle modulo one turn, exactly, so
-// that the wrap-around of an integer product is the whole range reduction (no
-// float64 work, which this GPU does at a small part of its float32 rate).  The frequency is
-// a float64 rounded to that fraction: the angle of position 2^24 is off by at
-// most 2^24 * 2^-53 turns.  The nearest quarter turn is taken off as an
-// integer, and the sine and cosine of the remaining eighth of a turn at most
-// are a float32 sincospif.
+// that the wrap-around of an integer product is the whole range reduction.  The
+// frequency is a float64 rounded to that fraction: the angle of position 2^24
+// is off by at most 2^24 * 2^-53 turns.  The nearest quarter turn is taken off
+// as an integer; sine and cosine of the eighth of a turn at most that remains
+// are their Taylor sums in pairs of float32 (about 46 bits; this GPU does
+// float64 at a small part of its float32 rate), so that the float32 factors are
+// the ones nearest to the true values but for one in some thousands.
+//
+// The rotation and the head norm round every step once, in the order written
+// in include/dsb.h, with no fused multiply-add: a 4-bit code next to a border
+// is then the code that these steps define, on whatever path they are taken.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,27 +38,71 @@ namespace {
 template <int NP>
 struct Turns {
   unsigned long long f[NP];  // turns per position of pair i, times 2^64
-  float gain;                // every rotated value is multiplied by it
+  float gain, gain_lo;       // every rotated value is multiplied by gain + gain_lo
   int rd;                    // rotated dimensions
   int interleaved;
 };
 
-__device__ __forceinline__ float2 turn_cs(unsigned long long f, int pos, float gain) {
+// A value as the unevaluated sum of two float32, hi the nearest to it.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_mul(Two a, Two b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  float e = __fmaf_rn(a.hi, b.hi, -p);
+  e = __fmaf_rn(a.hi, b.lo, e);
+  e = __fmaf_rn(a.lo, b.hi, e);
+  const float s = __fadd_rn(p, e);
+  return Two{s, __fsub_rn(e, __fsub_rn(s, p))};
+}
+// c + x, |c| >= |x|
+__device__ __forceinline__ Two two_add(Two c, Two x) {
+  const float s = __fadd_rn(c.hi, x.hi);
+  const float e = __fadd_rn(__fsub_rn(x.hi, __fsub_rn(s, c.hi)), __fadd_rn(c.lo, x.lo));
+  const float r = __fadd_rn(s, e);
+  return Two{r, __fsub_rn(e, __fsub_rn(r, s))};
+}
+
+__device__ __forceinline__ float2 turn_cs(unsigned long long f, int pos, float gain, float gain_lo) {
   const unsigned long long p = f * (unsigned long long)(unsigned)pos;
   const unsigned quarter = (unsigned)((p + (1ull << 61)) >> 62);
   const long long r = (long long)(p - ((unsigned long long)quarter << 62));  // [-2^61, 2^61)
-  float s, c;
-  sincospif((float)(int)(r >> 30) * 0x1p-33f, &s, &c);
-  float2 o = make_float2(c, s);
-  if (quarter & 1) o = make_float2(-s, c);
-  if (quarter & 2) o = make_float2(-o.x, -o.y);
-  return make_float2(__fmul_rn(o.x, gain), __fmul_rn(o.y, gain));
+  // t: the rest in half turns, at most 1/4; u = t^2
+  Two t;
+  t.hi = __ll2float_rn(r);
+  t.lo = __fmul_rn(__ll2float_rn(r - __float2ll_rn(t.hi)), 0x1p-63f);
+  t.hi = __fmul_rn(t.hi, 0x1p-63f);
+  const Two u = two_mul(t, t);
+  // sin(pi t) = t (pi - pi^3/3! u + pi^5/5! u^2 - ...), cos(pi t) alike; the terms
+  // from u^3 on, below 2^-12 of the sum, in one float32
+  float a = __fmaf_rn(0x1.e8f434p-12f, u.hi, -0x1.e30750p-8f);
+  a = __fmaf_rn(a, u.hi, 0x1.507834p-4f);
+  a = __fmaf_rn(a, u.hi, -0x1.32d2ccp-1f);
+  Two s = two_add(Two{0x1.466bc6p+1f, 0x1.dd6ab8p-25f}, two_mul(u, Two{a, 0.0f}));
+  s = two_add(Two{-0x1.4abbcep+2f, -0x1.896f94p-24f}, two_mul(u, s));
+  s = two_add(Two{0x1.921fb6p+1f, -0x1.777a5cp-24f}, two_mul(u, s));
+  s = two_mul(t, s);
+  float b = __fmaf_rn(-0x1.b6e250p-14f, u.hi, 0x1.f9d38ap-10f);
+  b = __fmaf_rn(b, u.hi, -0x1.a6d1f2p-6f);
+  b = __fmaf_rn(b, u.hi, 0x1.e1f506p-3f);
+  Two c = two_add(Two{-0x1.55d3c8p+0f, 0x1.c34006p-28f}, two_mul(u, Two{b, 0.0f}));
+  c = two_add(Two{0x1.03c1f0p+2f, 0x1.036b58p-23f}, two_mul(u, c));
+  c = two_add(Two{-0x1.3bd3ccp+2f, -0x1.37c8bcp-23f}, two_mul(u, c));
+  c = two_add(Two{1.0f, 0.0f}, two_mul(u, c));
+  if (quarter & 1) {
+    const Two x = c;
+    c = Two{-s.hi, -s.lo};
+    s = x;
+  }
+  const float sign = quarter & 2 ? -1.0f : 1.0f;
+  const Two g{__fmul_rn(sign, gain), __fmul_rn(sign, gain_lo)};
+  return make_float2(two_mul(c, g).hi, two_mul(s, g).hi);
 }
 
 __device__ __forceinline__ void turn_pair(float& a, float& b, float2 cs) {
   const float x = a, y = b;
-  a = __fmaf_rn(x, cs.x, __fmul_rn(-y, cs.y));
-  b = __fmaf_rn(x, cs.y, __fmul_rn(y, cs.x));
+  a = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, cs.y));
+  b = __fadd_rn(__fmul_rn(x, cs.y), __fmul_rn(y, cs.x));
 }
 
 constexpr int kRotThreads = 256;
@@ -105,7 +154,7 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
     }
   }
   const int pos = N > 1 ? words.w[t] : pos_dev[t];
-  for (int i = threadIdx.x; i < half; i += kRotThreads) cs[i] = turn_cs(tab.f[i], pos, tab.gain);
+  for (int i = threadIdx.x; i < half; i += kRotThreads) cs[i] = turn_cs(tab.f[i], pos, tab.gain, tab.gain_lo);
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kRotUnroll; ++u) {
@@ -150,6 +199,49 @@ template <>
 __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Sum of the squares of a head's D values, lane l of its D/4 holding values
+// 4l .. 4l+3.  The order is that of 32 running sums, the i-th over dimensions i,
+// i + 32, ..., added pairwise, neighbours first.  D = 128: the four terms of a
+// running sum sit 8 lanes apart; a transpose of the 4 x 4 (lane group, element)
+// brings them into one lane, the i-th group taking element i.  D = 64: two terms,
+// half of the elements to each group.
+template <int D>
+__device__ __forceinline__ float sum_squares(const float (&y)[4], int lane) {
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(y[e], y[e]);
+  float ss;
+  if constexpr (D == 128) {
+    const bool up = lane & 16, odd = lane & 8;
+    const float a = __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+    const float b = __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : v[3], 16);
+    if (up) {
+      v[0] = a, v[1] = b;
+    } else {
+      v[2] = a, v[3] = b;
+    }
+    const float c = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 8);
+    const float d = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2] : v[3], 8);
+    if (odd) {
+      v[0] = c, v[2] = d;
+    } else {
+      v[1] = c, v[3] = d;
+    }
+    ss = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), v[2]), v[3]);
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 16));
+  } else {
+    const bool odd = lane & 8;
+    const float a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 8);
+    const float b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 8);
+    ss = odd ? __fadd_rn(__fadd_rn(v[2], a), __fadd_rn(v[3], b)) : __fadd_rn(__fadd_rn(v[0], a), __fadd_rn(v[1], b));
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+  return ss;
 }
 
 // How the cache rows are stored.
@@ -202,7 +294,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
   const int32_t* pg_off = meta + 2 * n_seq + 1;
   const int page = pg_off[n_seq + 1 + pg_off[lo] + (pos >> 7) - (pos0 >> 7)];
   const int r = pos & 127;
-  if (tid < half) cs[tid] = turn_cs(tab.f[tid], pos, tab.gain);
+  if (tid < half) cs[tid] = turn_cs(tab.f[tid], pos, tab.gain, tab.gain_lo);
   __syncthreads();
   float c[4], s[4];  // of this lane's four dimensions; s with the sign its term takes
   int partner[4];
@@ -227,13 +319,9 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
     float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
     const float* w = !live ? nullptr : is_q ? q_norm : is_k ? k_norm : nullptr;
     if (__any_sync(0xFFFFFFFFu, w != nullptr)) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ss = __fmaf_rn(y[e], y[e], ss);
-#pragma unroll
-      for (int o = LPH >> 1; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+      const float ss = sum_squares<D>(y, tid & 31);
       if (w) {
-        const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)D), eps)));
+        const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
         const float4 wv = __ldg(reinterpret_cast<const float4*>(w) + l);
         y[0] = __fmul_rn(__fmul_rn(y[0], inv), wv.x);
         y[1] = __fmul_rn(__fmul_rn(y[1], inv), wv.y);
@@ -260,7 +348,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
       if (is_q || is_k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (4 * l + e < rd) y[e] = __fmaf_rn(y[e], c[e], __fmul_rn(p[e], s[e]));
+          if (4 * l + e < rd) y[e] = __fadd_rn(__fmul_rn(y[e], c[e]), __fmul_rn(p[e], s[e]));
       }
     }
     if (live && is_q && (q_norm || 4 * l < rd))
@@ -275,7 +363,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
                        !(fabsf(y[3]) <= FLT_MAX);
       const uint32_t seen = __ballot_sync(0xFFFFFFFFu, odd);
       const uint32_t group = LPH == 32 ? 0xFFFFFFFFu : 0xFFFFu << (tid & 16);
-      __half dh = __float2half_rn(__fdiv_rn(__fsub_rn(most, least), 15.0f));
+      __half dh = __float2half_rn(__fmul_rn(__fsub_rn(most, least), 1.0f / 15.0f));
       __half zh = __float2half_rn(__fadd_rn(least, __fmul_rn(8.0f, __half2float(dh))));
       if (seen & group) {  // a vector with a NaN or an infinity is stored as NaN
         dh = __ushort_as_half(0);
@@ -308,7 +396,8 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
 template <int NP>
 void fill_turns(const RotaryTable& rot, Turns<NP>* out) {
   for (int i = 0; i < NP; ++i) out->f[i] = i < rot.rd / 2 ? rot.turns[i] : 0;
-  out->gain = rot.gain;
+  out->gain = (float)rot.gain;
+  out->gain_lo = (float)(rot.gain - (double)out->gain);
   out->rd = rot.rd;
   out->interleaved = rot.interleaved;
 }
@@ -396,7 +485,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, c
 
 // Turns per position as 64-bit fractions; only the fraction of a turn counts,
 // because positions are whole numbers.
-void rotary_table(const double* freq, int rd, bool interleaved, float gain, RotaryTable* out) {
+void rotary_table(const double* freq, int rd, bool interleaved, double gain, RotaryTable* out) {
   out->rd = rd;
   out->interleaved = interleaved ? 1 : 0;
   out->gain = gain;
