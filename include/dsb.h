@@ -459,8 +459,10 @@ typedef struct {
  * head_dim side by side; k alike (NULL with n_kv_heads = 0).  q and k may be
  * parts of the same rows (the strides of a fused projection) but share no
  * value.  head_dim even in [2, 1024].  Angles modulo one turn in 64-bit integer
- * arithmetic, sine, cosine and rotation in float32.  Row t is bitwise equal to
- * an n_tok = 1 call. */
+ * arithmetic; c and s the float32 nearest to the cosine and the sine times the
+ * gain (but for one in some thousands); x c - y s and x s + y c with every
+ * product and sum rounded to float32.  Row t is bitwise equal to an n_tok = 1
+ * call. */
 dsb_status dsb_rope_rotary(float* q, int64_t q_stride, int n_q_heads, float* k, int64_t k_stride, int n_kv_heads,
                            int head_dim, int n_tok, const int32_t* pos, const dsb_rotary* rotary, dsb_workspace* ws,
                            void* stream);
@@ -487,9 +489,11 @@ typedef struct {
  * qkv + t * row_stride (a multiple of 4, >= (n_q_heads + 2 n_kv_heads) head_dim),
  * holding the query heads, the key heads and the value heads.  Per-head RMS
  * norm of q / k first where q_norm / k_norm (device float32 [head_dim]) is
- * given, as dsb_head_rmsnorm_rope; then q is rotated in place, and k rotated and
- * v as it is are converted (round to nearest even) and written at their
- * positions' page rows.  The k and v parts of qkv and all other page rows keep
+ * given: x rsqrt(mean + eps) w, the squares summed as 32 running sums (the i-th
+ * over dimensions i, i + 32, ...) that are then added pairwise, neighbours first,
+ * every step rounded to float32.  Then q is rotated in place as by
+ * dsb_rope_rotary, and k so rotated and v as it is are converted (round to
+ * nearest even) and written at their positions' page rows.  The k and v parts of qkv and all other page rows keep
  * their values.  n_q_heads may be 0.  head_dim 64 or 128.  Positions below 2^24.
  * Two tokens of a call on one page row are DSB_ERR_INVALID_ARG. */
 dsb_status dsb_kv_append_paged(float* qkv, int64_t row_stride, int n_q_heads, const dsb_kv_pages* kv,
@@ -504,8 +508,8 @@ dsb_status dsb_kv_append_paged(float* qkv, int64_t row_stride, int n_q_heads, co
  *   V codes   [64 key pairs][D/4 words][2 keys] 16-bit; word i of a key holds
  *             dimensions 4i .. 4i+3, the lowest four bits first
  *   V (d, z)  [128 keys] two fp16
- * Each head vector has its own scale and centre, d = fp16((max - min) / 15) and
- * z = fp16(min + 8 d); code = clamp(round-half-even((x - z) / d) + 8, 0, 15) in
+ * Each head vector has its own scale and centre, d = fp16((max - min) r), r the
+ * float32 nearest 1/15, and z = fp16(min + 8 d); code = clamp(round-half-even((x - z) / d) + 8, 0, 15) in
  * float32 (8 where d = 0), and the value is z + d (code - 8).  A vector that
  * holds a NaN or an infinity is stored as NaN in every dimension; values must
  * otherwise lie within fp16's range.  head_dim 64 or 128. */

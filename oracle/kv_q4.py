@@ -3,7 +3,7 @@
 A head vector x of D float32 values is stored as D codes and two fp16 numbers,
 every step a single rounding:
 
-    d = fp16((max x - min x) / 15),  z = fp16(min x + 8 d)
+    d = fp16((max x - min x) * float32(1/15)),  z = fp16(min x + 8 d)
     code = clamp(round-half-even((x - z) / d) + 8, 0, 15), 8 where d = 0
     value = z + d (code - 8)
 
@@ -27,7 +27,7 @@ def quantise(x):
     x = np.asarray(x, dtype=np.float32)
     lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
     with np.errstate(all="ignore"):
-        d16 = ((hi - lo) / np.float32(15)).astype(np.float16)
+        d16 = ((hi - lo) * np.float32(1 / 15)).astype(np.float16)
         d = d16.astype(np.float32)
         z16 = (lo + np.float32(8) * d).astype(np.float16)
         z = z16.astype(np.float32)
