@@ -585,7 +585,7 @@ def rope_kv_write(qkv, n_q_heads: int, kv: KVCache, batch_index, tokens_per_seq:
 
 # ------------------------------- rotary layouts, paged append, 4-bit paged KV
 SIGNATURES.update({
-    "dsb_rope_rotary": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _I, _PI32, ctypes.POINTER(RotaryC), _P, _P]),
+    "dsb_rope_rotary": (_I, [_P, _I64, _I, _P, _I64, _I, _I, _I, _P, ctypes.POINTER(RotaryC), _P, _P]),
     "dsb_kv_append_paged": (_I, [_P, _I64, _I, ctypes.POINTER(KVPages), ctypes.POINTER(PagedBatchC),
                                  ctypes.POINTER(RotaryC), _P, _P, _F, _P, _P]),
     "dsb_kv_q4_page_bytes": (ctypes.c_size_t, [_I, _I]),
@@ -593,8 +593,7 @@ SIGNATURES.update({
                               ctypes.POINTER(RotaryC), _P, _P, _F, _P, _P]),
     "dsb_attention_decode_q4": (_I, [_P, _I64, _I, ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC), _P, _P,
                                      _P]),
-    "dsb_kv_gather_q4": (_I, [ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC), _PI32, _PI32, _I, _P, _P, _P,
-                              _P]),
+    "dsb_kv_gather_q4": (_I, [ctypes.POINTER(KVQ4Pages), ctypes.POINTER(PagedBatchC), _P, _P, _I, _P, _P, _P, _P]),
 })
 
 ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "bands": 3}
@@ -642,37 +641,61 @@ class PagedBatch:
         self.ref = ctypes.byref(self.c)
 
 
-def _rows(t, rows: int, width: int, name: str):
-    """Row stride of float32 ``t`` seen as ``rows`` rows of ``width`` values,
-    contiguous in a row (rows may lie further apart)."""
+def _row_stride(t, rows: int, inner, name: str):
+    """Row stride of float32 ``t`` of shape ``(rows, *inner)``, whose values are
+    contiguous in a row (rows may lie further apart).  Shapes and strides only:
+    a step makes these calls for every layer, and tensor views cost more on the
+    host than the launch."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be float32, got {t.dtype}")
-    if t.dim() < 2 or t.shape[0] != rows or t[0:1].numel() != min(rows, 1) * width:
-        raise ValueError(f"{name} must be {rows} rows of {width} values, got {tuple(t.shape)}")
-    if rows and not t[0].is_contiguous():
-        raise ValueError(f"{name}: the values of a row must be contiguous")
-    return t.stride(0) if rows > 1 else width
+    shape = tuple(t.shape)
+    if shape != (rows, *inner):
+        raise ValueError(f"{name} must be {rows} rows of {' x '.join(map(str, inner))} values, got {shape}")
+    strides, width = t.stride(), 1
+    for n, step in zip(reversed(inner), reversed(strides)):
+        if n != 1 and step != width:
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+        width *= n
+    return strides[0] if rows > 1 else width
 
 
-def _dev_ptr(t, device, name: str):
-    """Data pointer of ``t``, which must live on ``device``."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must live on {device}, a CUDA device, got {t.device}")
+def _dev_ptr(t, device: int, name: str):
+    """Data pointer of ``t``, which must live on CUDA device ``device``."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must live on cuda:{device}, got {t.device}")
     return t.data_ptr()
 
 
-def _current_device(t, name: str):
-    """Device of ``t``; it must be the current CUDA device, on which the
+def _current_device(t, name: str) -> int:
+    """Index of ``t``'s device; it must be the current CUDA device, on which the
     library launches."""
     import torch
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    return dev
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The cudaStream_t of ``stream``, or of the device's current stream."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _host_i32(a, n: int, name: str):
+    """``a`` as a contiguous int32 array of ``n`` entries, and its address."""
+    if not (type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous):
+        a = np.ascontiguousarray(np.asarray(a, dtype=np.int32)).reshape(-1)
+    if a.size != n:
+        raise ValueError(f"{name} has {a.size} entries, needs {n}")
+    return a, a.__array_interface__["data"][0]
 
 
 def rope_rotary(q, k, pos, rotary: Rotary, ws: Workspace, stream=None):
@@ -682,27 +705,28 @@ def rope_rotary(q, k, pos, rotary: Rotary, ws: Workspace, stream=None):
         raise ValueError("q is [n_tok, Hq, D] and k [n_tok, Hkv, D]")
     n_tok, hq, d = q.shape
     hkv = 0 if k is None else k.shape[1]
-    qs = _rows(q, n_tok, hq * d, "q")
-    ks = 0 if k is None else _rows(k, n_tok, hkv * d, "k")
-    arr, p = _i32(pos, n_tok, "pos")
+    qs = _row_stride(q, n_tok, (hq, d), "q")
+    ks = 0 if k is None else _row_stride(k, n_tok, (hkv, d), "k")
+    arr, p = _host_i32(pos, n_tok, "pos")
     dev = _current_device(q, "q")
     _check(lib().dsb_rope_rotary(q.data_ptr(), qs, hq, None if k is None else _dev_ptr(k, dev, "k"), ks, hkv, d, n_tok,
-                                 p, rotary.ref, ws.handle, _stream(stream)))
+                                 p, rotary.ref, ws.handle, _raw_stream(stream, dev)))
 
 
 def _append(fn, qkv, n_q_heads: int, kv, batch: PagedBatch, rotary: Rotary, ws: Workspace, q_norm, k_norm, eps, stream):
-    stride = _rows(qkv, batch.n_tok, (n_q_heads + 2 * kv.n_kv_heads) * kv.head_dim, "qkv")
+    stride = _row_stride(qkv, batch.n_tok, ((n_q_heads + 2 * kv.n_kv_heads) * kv.head_dim,), "qkv")
     dev = _current_device(qkv, "qkv")
-    norms = []
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        _need_opt(w, 4 * kv.head_dim, name, "f32")
-        if w is not None and not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        norms.append(None if w is None else _dev_ptr(w, dev, name))
+    norms = [None, None]
+    for i, (w, name) in enumerate(((q_norm, "q_norm"), (k_norm, "k_norm"))):
+        if w is not None:
+            _need(w, 4 * kv.head_dim, name, "f32")
+            if not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            norms[i] = _dev_ptr(w, dev, name)
     for t in kv._tensors:
         _dev_ptr(t, dev, "the page pool")
     _check(fn(qkv.data_ptr(), stride, n_q_heads, ctypes.byref(kv), batch.ref, rotary.ref, norms[0], norms[1],
-              float(eps), ws.handle, _stream(stream)))
+              float(eps), ws.handle, _raw_stream(stream, dev)))
     return qkv
 
 
@@ -743,16 +767,17 @@ def attention_decode_q4(q, kv: KVQ4Pages, batch: PagedBatch, ws: Workspace, out=
     if q.dim() != 3 or q.shape[2] != kv.head_dim:
         raise ValueError(f"q must be [n_tok, Hq, head_dim={kv.head_dim}], got {tuple(q.shape)}")
     n_tok, hq, d = q.shape
-    stride = _rows(q, batch.n_tok, hq * d, "q")
+    stride = _row_stride(q, batch.n_tok, (hq, d), "q")
     dev = _current_device(q, "q")
     if out is None:
-        out = torch.empty((n_tok, hq, d), dtype=torch.float32, device=dev)
-    _need(out, 4 * n_tok * hq * d, "out", "f32")
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
+        out = torch.empty((n_tok, hq, d), dtype=torch.float32, device=q.device)
+    else:
+        _need(out, 4 * n_tok * hq * d, "out", "f32")
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
     _dev_ptr(kv._tensors[0], dev, "the page pool")
     _check(lib().dsb_attention_decode_q4(q.data_ptr(), stride, hq, ctypes.byref(kv), batch.ref,
-                                         _dev_ptr(out, dev, "out"), ws.handle, _stream(stream)))
+                                         _dev_ptr(out, dev, "out"), ws.handle, _raw_stream(stream, dev)))
     return out
 
 
@@ -762,23 +787,24 @@ def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws:
     ``(k, v)``, each 16-bit ``[sum(count), Hkv, D]`` of ``dtype`` (DSB_F16 or
     DSB_BF16), the values the 4-bit rows stand for."""
     import torch
-    fa, pf = _i32(first, batch.n_seq, "first")
-    ca, pc = _i32(count, batch.n_seq, "count")
-    kinds = {DSB_F16: torch.float16, DSB_BF16: torch.bfloat16}
-    if dtype not in kinds:
+    fa, pf = _host_i32(first, batch.n_seq, "first")
+    ca, pc = _host_i32(count, batch.n_seq, "count")
+    if dtype not in (DSB_F16, DSB_BF16):
         raise ValueError(f"dtype must be DSB_F16 or DSB_BF16, got {dtype}")
-    dev = _current_device(kv._tensors[0], "the page pool")
+    kind = torch.float16 if dtype == DSB_F16 else torch.bfloat16
+    pool = kv._tensors[0]
+    dev = _current_device(pool, "the page pool")
     shape = (max(int(ca.sum()), 0), kv.n_kv_heads, kv.head_dim)
-    outs = []
-    for t, name in ((k, "k"), (v, "v")):
-        if t is None:
-            t = torch.empty(shape, dtype=kinds[dtype], device=dev)
-        _need(t, 2 * shape[0] * shape[1] * shape[2], name)
-        if t.dtype != kinds[dtype] or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {kinds[dtype]}")
-        outs.append(t)
+    outs = [k, v]
+    for i, name in enumerate("kv"):
+        if outs[i] is None:
+            outs[i] = torch.empty(shape, dtype=kind, device=pool.device)
+            continue
+        _need(outs[i], 2 * shape[0] * shape[1] * shape[2], name)
+        if outs[i].dtype != kind or not outs[i].is_contiguous():
+            raise ValueError(f"{name} must be contiguous {kind}")
     _check(lib().dsb_kv_gather_q4(ctypes.byref(kv), batch.ref, pf, pc, dtype, _dev_ptr(outs[0], dev, "k"),
-                                  _dev_ptr(outs[1], dev, "v"), ws.handle, _stream(stream)))
+                                  _dev_ptr(outs[1], dev, "v"), ws.handle, _raw_stream(stream, dev)))
     return outs[0], outs[1]
 
 
