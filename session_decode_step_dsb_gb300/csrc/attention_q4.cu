@@ -64,6 +64,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], __hal
         "r"(*reinterpret_cast<const uint32_t*>(&b1)));
 }
 
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], __half2 b0, __half2 b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(*reinterpret_cast<const uint32_t*>(&b0)),
+        "r"(*reinterpret_cast<const uint32_t*>(&b1)), "f"(0.0f));
+}
+
 // x0, x1 as hi + lo fp16 pairs.
 __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x0, x1);
@@ -78,14 +87,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // Where a CTA is in its list of items: one unit of one (sequence, kv head, row
-// tile), and the page inside it.
+// tile), and the page inside it.  Divides once, at its start; then it counts.
 struct Cursor {
-  int item, s, h, rt, u, units, pg, pg_end;
+  int at;  // pages of work before this item
+  int s, h, rt, u, units, tiles, pages, pg, pg_end;
   Q4Seq q;
 
-  __device__ __forceinline__ void load(const int32_t* meta) {
+  __device__ __forceinline__ void load(const int32_t* meta, int G) {
     const int32_t* p = meta + s * kQ4SeqWords;
-    q.item_off = p[0];
+    q.work_off = p[0];
     q.tok0 = p[1];
     q.n_new = p[2];
     q.len = p[3];
@@ -93,41 +103,58 @@ struct Cursor {
     q.chunk0 = p[5];
     q.pg_at = p[6];
     q.u_pages = p[7];
-  }
-  __device__ __forceinline__ void place(int G) {
-    const int pages = ((q.len - 1) >> 7) - q.chunk0 + 1;
+    pages = ((q.len - 1) >> 7) - q.chunk0 + 1;
     units = (pages + q.u_pages - 1) / q.u_pages;
-    const int tiles = (G * q.n_new + kQ4Rows - 1) / kQ4Rows;
-    const int rel = item - q.item_off, x = rel / units;
-    u = rel - x * units;
-    h = x / tiles;
-    rt = x - h * tiles;
+    tiles = (G * q.n_new + kQ4Rows - 1) / kQ4Rows;
+  }
+  __device__ __forceinline__ void place() {
     pg = u * q.u_pages;
     pg_end = min(pg + q.u_pages, pages);
   }
-  __device__ __forceinline__ void start(const int32_t* meta, int n_seq, int G, int first) {
-    item = first;
+  // The first item that starts at or after `from` pages of work; false if none.
+  __device__ __forceinline__ bool start(const int32_t* meta, int n_seq, int hkv, int G, int from) {
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (meta[mid * kQ4SeqWords] <= item)
+      if (meta[mid * kQ4SeqWords] <= from)
         lo = mid;
       else
         hi = mid - 1;
     }
     s = lo;
-    load(meta);
-    place(G);
+    load(meta, G);
+    const int rel = from - q.work_off;
+    int x = rel / pages;
+    u = (rel - x * pages + q.u_pages - 1) / q.u_pages;
+    if (u == units) u = 0, ++x;
+    h = x / tiles;
+    rt = x - h * tiles;
+    if (h == hkv) {
+      if (++s == n_seq) return false;
+      h = 0;
+      load(meta, G);
+    }
+    place();
+    at = q.work_off + (h * tiles + rt) * pages + pg;
+    return true;
   }
   // The next item (one that exists).
-  __device__ __forceinline__ void next(const int32_t* meta, int n_seq, int G) {
-    ++item;
-    if (s + 1 < n_seq && item >= meta[(s + 1) * kQ4SeqWords]) {
-      ++s;
-      load(meta);
+  __device__ __forceinline__ void next(const int32_t* meta, int hkv, int G) {
+    at += pg_end - u * q.u_pages;
+    if (++u == units) {
+      u = 0;
+      if (++rt == tiles) {
+        rt = 0;
+        if (++h == hkv) {
+          h = 0;
+          ++s;
+          load(meta, G);
+        }
+      }
     }
-    place(G);
+    place();
   }
+  __device__ __forceinline__ int end() const { return at + pg_end - u * q.u_pages; }  // pages before the next item
 };
 
 template <int D>
@@ -190,12 +217,14 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  // this CTA's items: those that start in its share of the pages
   const long long total = meta[n_seq * kQ4SeqWords];
-  const int i0 = (int)(total * blockIdx.x / gridDim.x), i1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  if (i0 >= i1) return;
+  const int w0 = (int)(total * blockIdx.x / gridDim.x), w1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  Cursor cur;
+  if (w0 >= w1 || !cur.start(meta, n_seq, hkv, G, w0) || cur.at >= w1) return;
 
   // Thread 0 runs kStages - 1 pages ahead of the others.
-  Cursor ahead;
+  Cursor ahead = cur;
   int asked = 0;
   bool more = true;
   auto ask = [&]() {
@@ -204,19 +233,16 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     request<D>(ahead, meta, pool, hkv, smem + st * B::bytes, &full[st]);
     ++asked;
     if (++ahead.pg == ahead.pg_end) {
-      if (ahead.item + 1 < i1)
-        ahead.next(meta, n_seq, G);
+      if (ahead.end() < w1)
+        ahead.next(meta, hkv, G);
       else
         more = false;
     }
   };
   if (tid == 0) {
-    ahead.start(meta, n_seq, G, i0);
     for (int i = 0; i < kStages - 1 && more; ++i) ask();
   }
 
-  Cursor cur;
-  cur.start(meta, n_seq, G, i0);
   uint32_t qf[KS][4];            // q of row g as the products' left operand: rows 0..7 hi, 8..15 lo
   float row_scale = 1.0f, row_sum = 0.0f;
   int key_hi = 0, key_lo = 0;    // the keys row g sees
@@ -290,8 +316,6 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
         float sc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][e] = 0.0f;
           uint32_t kw[W];
           const uint8_t* kp = blk + (32 * warp + 8 * t + g) * (D / 2) + c * (D / 8);
           if constexpr (D == 128) {
@@ -305,7 +329,10 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
           for (int w = 0; w < W; ++w) {
             __half2 h[4];
             q4_unpack(kw[w], h);
-            mma(sc[t], qf[2 * w], h[0], h[1]);
+            if (w == 0)
+              mma_new(sc[t], qf[0], h[0], h[1]);
+            else
+              mma(sc[t], qf[2 * w], h[0], h[1]);
             mma(sc[t], qf[2 * w + 1], h[2], h[3]);
           }
         }
@@ -337,14 +364,16 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
         // coarser than 2^-35 of the largest weight.
         if (__any_sync(0xFFFFFFFFu, top > M + 14.0f)) {
           const float to = top > M + 14.0f ? top - 10.0f : M;
-          const float f = M == -INFINITY ? 0.0f : ex2(M - to);
+          if (__any_sync(0xFFFFFFFFu, M != -INFINITY)) {  // else nothing has been summed yet
+            const float f = M == -INFINITY ? 0.0f : ex2(M - to);
+            lsum *= f;
+            zsum *= f;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[t][e] *= f;
+          }
           M = to;
-          lsum *= f;
-          zsum *= f;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][e] *= f;
         }
         // ---- weights, and 16 keys at a time their product with V
 #pragma unroll
@@ -424,10 +453,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     {
       const int dim = tid % D, cc = dim / (D / 4), in = dim % (D / 4);
       const int place = cc * (D / 4) + 4 * ((in >> 2) ^ (D == 128 ? cc : cc >> 1)) + (in & 3);
-#pragma unroll
-      for (int i = tid / D; i < kQ4Rows; i += kThreads / D) {
-        const int r = cur.rt * kQ4Rows + i;
-        if (r >= R) break;
+      const int rows = min(kQ4Rows, R - cur.rt * kQ4Rows);
+      int i = tid / D, r = cur.rt * kQ4Rows + i, j = r / G, gi = r - j * G;
+      for (; i < rows; i += kThreads / D) {
         float top = stat[i];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, stat[w * kQ4Rows + i]);
@@ -441,8 +469,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
           l = __fmaf_rn(f, lw, l);
           acc = __fmaf_rn(f, join[(w * kQ4Rows + i) * S::rows + place], acc);
         }
-        const int j = r / G, head = cur.h * G + r - j * G;
-        const size_t row = (size_t)(sq.tok0 + j) * hq + head;
+        const size_t row = (size_t)(sq.tok0 + j) * hq + cur.h * G + gi;
+        gi += kThreads / D;
+        while (gi >= G) gi -= G, ++j;
         if (cur.units == 1) {
           out[row * D + dim] = __fdiv_rn(acc, l);
         } else {
@@ -455,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
         }
       }
     }
-    if (cur.item + 1 >= i1) break;
-    cur.next(meta, n_seq, G);
+    if (cur.end() >= w1) break;
+    cur.next(meta, hkv, G);
     __syncthreads();
   }
 }
@@ -542,13 +571,15 @@ cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t 
 
 }  // namespace
 
-// Long units cost less joining, short ones fill the GPU with few sequences.  A
-// sequence of many row tiles fills it without being cut.
-int q4_unit_pages(int n, int tiles) {
-  if (n <= 2 || tiles >= 64) return n;
-  if (n <= 16) return 1;
-  if (n <= 128) return 2;
-  return n <= 512 ? 4 : (n + 127) / 128;
+// Long units cost less joining, short ones fill the GPU with few sequences: the
+// sequence alone makes up to kAlone items (heads and row tiles included), of two
+// pages at least where it has many.
+int q4_unit_pages(int n, int lanes) {
+  constexpr long long kAlone = 512;
+  if (n <= 2) return n;
+  const int least = n <= 16 ? 1 : 2;
+  const long long u = ((long long)n * lanes + kAlone - 1) / kAlone;
+  return u < least ? least : u > n ? n : (int)u;
 }
 
 cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st) {

@@ -250,15 +250,17 @@ cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, c
                              const MetaArg& meta, cudaStream_t st);
 
 // One sequence of a 4-bit attention call, in its metadata; n_seq of them, then
-// the total item count, then the visited pages of all sequences.  A sequence's
-// work items are (kv head, tile of 8 query rows, unit of u_pages pages).
+// the pages of work in all, then the visited pages of all sequences.  A
+// sequence's work items are (kv head, tile of 8 query rows, unit of u_pages
+// pages); work_off: pages of work of the sequences before it.
 struct Q4Seq {
-  int32_t item_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
+  int32_t work_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
 };
 constexpr int kQ4SeqWords = 8;
 constexpr int kQ4Rows = 8;  // query rows of an item
-// Pages per unit of a sequence that visits n of them with `tiles` tiles of rows.
-int q4_unit_pages(int n, int tiles);
+// Pages per unit of a sequence that visits n of them, with `lanes` pairs of a kv
+// head and a tile of rows: a rule on the sequence alone, not on the batch.
+int q4_unit_pages(int n, int lanes);
 struct Q4AttnArgs {
   const float* q;
   long long q_stride;

@@ -376,7 +376,7 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     if ((st = cut_groups(b->n_seq, 1, dsbk::kQ4SeqWords, pages, &groups)) != DSB_OK) return st;
     struct Plan {
       int live = 0, max_units = 1;
-      long long items = 0;
+      long long items = 0, work = 0;
     };
     std::vector<Plan> plans(groups.size());
     int tok0 = 0;
@@ -391,8 +391,8 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
         const int n = b->new_tokens[s];
         if (n == 0) continue;
         const int np = pages(s), tiles = (int)(((long long)G * n + dsbk::kQ4Rows - 1) / dsbk::kQ4Rows);
-        const int u = dsbk::q4_unit_pages(np, tiles), units = (np + u - 1) / u;
-        const int32_t rec[dsbk::kQ4SeqWords] = {(int32_t)p.items,
+        const int u = dsbk::q4_unit_pages(np, kv->n_kv_heads * tiles), units = (np + u - 1) / u;
+        const int32_t rec[dsbk::kQ4SeqWords] = {(int32_t)p.work,
                                                 g.n_tok,
                                                 n,
                                                 b->seq_lens[s],
@@ -403,12 +403,13 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
         g.words.insert(g.words.end(), rec, rec + dsbk::kQ4SeqWords);
         for (int i = 0; i < np; ++i) list.push_back(page_of(b, s, chunk0(s) + i));
         p.items += (long long)kv->n_kv_heads * tiles * units;
+        p.work += (long long)kv->n_kv_heads * tiles * np;
         p.max_units = std::max(p.max_units, units);
         g.n_tok += n;
-        if (p.items > INT_MAX) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+        if (p.work > INT_MAX) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
       }
       tok0 += g.n_tok;
-      g.words.push_back((int32_t)p.items);
+      g.words.push_back((int32_t)p.work);
       g.words.insert(g.words.end(), list.begin(), list.end());
       most = std::max(most, g.words.size());
       if (p.max_units > 1)
