@@ -22,9 +22,10 @@
 // blocks, two ahead.  The four warps' results are joined at the unit's end, the
 // units' by a second kernel in unit order (a sequence of one unit needs none).
 //
-// The maximum is kept over s_k + log2 d_k (of V), so that the weights that enter
-// the fp16 split are at most 2^14 whatever the scales are, and the largest at
-// least 2^10; p_k itself and the sums over it are float32.
+// The running reference of the exponentials is the largest s_k plus the log of
+// the largest d_k (of V) of the same 32 keys, so that the weights that enter the
+// fp16 split are at most 2^14 whatever the scales are; p_k itself and the sums
+// over it are float32.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -64,20 +65,62 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], __hal
         "r"(*reinterpret_cast<const uint32_t*>(&b1)));
 }
 
-// The same with a zero accumulator.
-__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], __half2 b0, __half2 b1) {
+// The same on words that hold the half2, and from the accumulator (hi, hi, 0, 0).
+__device__ __forceinline__ void mma_w(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float hi) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %11, %11};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(*reinterpret_cast<const uint32_t*>(&b0)),
-        "r"(*reinterpret_cast<const uint32_t*>(&b1)), "f"(0.0f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(hi), "f"(0.0f));
+}
+
+// Two float32 at once.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// The (d, z) of two neighbouring keys as (d, d) and (z, z).
+__device__ __forceinline__ void numbers(uint2 w, f2& d, f2& z) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  d = pack(a.x, b.x);
+  z = pack(a.y, b.y);
 }
 
 // x0, x1 as hi + lo fp16 pairs.
-__device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x0, x1);
+__device__ __forceinline__ void split(f2 x, uint32_t& hi, uint32_t& lo) {
+  const float2 v = unpack(x);
+  const __half2 h = __floats2half2_rn(v.x, v.y);
   const float2 f = __half22float2(h);
-  const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  const float2 t = unpack(add2(x, pack(-f.x, -f.y)));
+  const __half2 r = __floats2half2_rn(t.x, t.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -266,16 +309,16 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
         x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
         x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
       }
-      // the row over a power of two that brings its largest value to [1, 2): the
-      // split keeps its 22 bits whatever q's size
+      // the row over a power of two that brings its largest value to [2^10, 2^11):
+      // the split keeps its 22 bits whatever q's size
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
-      row_scale = __uint_as_float((uint32_t)e << 23);
-      const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+      const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
+      row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
+      const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
       row_sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) {
@@ -284,13 +327,16 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       }
       row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 1);
       row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
-      // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4)
+      row_sum *= 0x1p-24f;
+      // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
+      // nibbles stand 16 times as high in their word
 #pragma unroll
       for (int w = 0; w < W; ++w)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          split(x[8 * w + 2 * b], x[8 * w + 2 * b + 4], qf[2 * w + b][0], qf[2 * w + b][1]);
-          split(x[8 * w + 2 * b + 1], x[8 * w + 2 * b + 5], qf[2 * w + b][2], qf[2 * w + b][3]);
+          split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), qf[2 * w + b][0], qf[2 * w + b][1]);
+          split(pack(x[8 * w + 2 * b + 1] * 0.0625f, x[8 * w + 2 * b + 5] * 0.0625f), qf[2 * w + b][2],
+                qf[2 * w + b][3]);
         }
     }
     float o[NT][4];
@@ -298,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
-    float M = -INFINITY, lsum = 0.0f, zsum = 0.0f;
+    float M = -INFINITY;
+    f2 lsum = 0, zsum = 0;  // over even and odd keys
     // what any row of the tile can see, and what every row sees
     const int j0 = cur.rt * kQ4Rows / G, j1 = min(cur.rt * kQ4Rows + kQ4Rows - 1, R - 1) / G;
     const int first_hi = sq.len - sq.n_new + j0, last_hi = sq.len - sq.n_new + j1;
@@ -312,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       const int key0 = ((sq.chunk0 + pg) << 7) + 32 * warp;
       if (key0 <= last_hi && key0 + 31 >= any_lo) {
         const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
-        // ---- scores of 32 keys, four tiles of eight
+        // ---- scores of 32 keys, four tiles of eight.  A code masked out of its word
+        // is an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the
+        // product: no conversion; -8 sum(q) starts the sums.
         float sc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -327,38 +376,39 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
           }
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            __half2 h[4];
-            q4_unpack(kw[w], h);
+            const uint32_t k8 = kw[w] >> 8;
             if (w == 0)
-              mma_new(sc[t], qf[0], h[0], h[1]);
+              mma_from(sc[t], qf[0], kw[0] & 0x000F000Fu, kw[0] & 0x00F000F0u, -8.0f * row_sum);
             else
-              mma(sc[t], qf[2 * w], h[0], h[1]);
-            mma(sc[t], qf[2 * w + 1], h[2], h[3]);
+              mma_w(sc[t], qf[2 * w], kw[w] & 0x000F000Fu, kw[w] & 0x00F000F0u);
+            mma_w(sc[t], qf[2 * w + 1], k8 & 0x000F000Fu, k8 & 0x00F000F0u);
           }
         }
-        // s = d acc + z sum(q) for keys 8t + 2c, + 1 of row g; t = s + log2 d(V)
-        float x[8], top = -INFINITY;
+        // the largest scale of V among the 32 keys (bits of an fp16 that is not negative)
+        uint32_t vd = *reinterpret_cast<const uint16_t*>(blk + B::vz + (32 * warp + lane) * 4);
+        if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
+        vd = __reduce_max_sync(0xFFFFFFFFu, vd);
+        const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
+        // s = d acc + z sum(q) for keys 8t + 2c, + 1 of row g, times 2^-24
+        f2 x[4];
+        float top = -INFINITY;
+        const f2 rsum = pack(row_sum, row_sum);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int at = (32 * warp + 8 * t + 2 * c) * 4;
-          const uint2 kz = *reinterpret_cast<const uint2*>(blk + B::kz + at);
-          const uint2 vz = *reinterpret_cast<const uint2*>(blk + B::vz + at);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 dz = __half22float2(*reinterpret_cast<const __half2*>(e ? &kz.y : &kz.x));
-            const float vd = __low2float(*reinterpret_cast<const __half2*>(e ? &vz.y : &vz.x));
-            const float s = __fmaf_rn(dz.x, sc[t][e] + sc[t][2 + e], dz.y * row_sum);
-            x[2 * t + e] = s;
-            float w = __fmaf_rn(row_scale, s, fmaxf(lg2(vd), -24.0f));
-            if (!whole) {
-              const int key = key0 + 8 * t + 2 * c + e;
-              if (key > key_hi || key < key_lo) w = -INFINITY;
-            }
-            top = fmaxf(top, w);
+          f2 d, z;
+          numbers(*reinterpret_cast<const uint2*>(blk + B::kz + (32 * warp + 8 * t + 2 * c) * 4), d, z);
+          x[t] = fma2(d, add2(pack(sc[t][0], sc[t][1]), pack(sc[t][2], sc[t][3])), mul2(z, rsum));
+          float2 v = unpack(x[t]);
+          if (!whole) {
+            const int key = key0 + 8 * t + 2 * c;
+            if (key > key_hi || key < key_lo) v.x = -INFINITY;
+            if (key + 1 > key_hi || key + 1 < key_lo) v.y = -INFINITY;
           }
+          top = fmaxf(top, fmaxf(v.x, v.y));
         }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        top = __fmaf_rn(row_scale, top, vd_log);
         // The reference is set 2^10 below the largest weight and moves only when
         // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
         // coarser than 2^-35 of the largest weight.
@@ -366,8 +416,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
           const float to = top > M + 14.0f ? top - 10.0f : M;
           if (__any_sync(0xFFFFFFFFu, M != -INFINITY)) {  // else nothing has been summed yet
             const float f = M == -INFINITY ? 0.0f : ex2(M - to);
-            lsum *= f;
-            zsum *= f;
+            const f2 ff = pack(f, f);
+            lsum = mul2(lsum, ff);
+            zsum = mul2(zsum, ff);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -376,27 +427,29 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
           M = to;
         }
         // ---- weights, and 16 keys at a time their product with V
+        const f2 rs2 = pack(row_scale, row_scale), nm2 = pack(-M, -M);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           uint32_t a[4];
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt) {
             const int t = 2 * p + tt;
-            const uint2 vz = *reinterpret_cast<const uint2*>(blk + B::vz + (32 * warp + 8 * t + 2 * c) * 4);
-            float w[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float2 dz = __half22float2(*reinterpret_cast<const __half2*>(e ? &vz.y : &vz.x));
-              float pr = ex2(__fmaf_rn(row_scale, x[2 * t + e], -M));
-              if (!whole) {
-                const int key = key0 + 8 * t + 2 * c + e;
-                if (key > key_hi || key < key_lo) pr = dz.x = dz.y = 0.0f;  // its numbers may be anything
-              }
-              lsum += pr;
-              zsum = __fmaf_rn(pr, dz.y, zsum);
-              w[e] = pr * dz.x;
+            f2 d, z;
+            numbers(*reinterpret_cast<const uint2*>(blk + B::vz + (32 * warp + 8 * t + 2 * c) * 4), d, z);
+            const float2 v = unpack(fma2(rs2, x[t], nm2));
+            float2 pr = make_float2(ex2(v.x), ex2(v.y));
+            if (!whole) {  // a hidden key's numbers may be anything
+              const int key = key0 + 8 * t + 2 * c;
+              float2 dd = unpack(d), zz = unpack(z);
+              if (key > key_hi || key < key_lo) pr.x = dd.x = zz.x = 0.0f;
+              if (key + 1 > key_hi || key + 1 < key_lo) pr.y = dd.y = zz.y = 0.0f;
+              d = pack(dd.x, dd.y);
+              z = pack(zz.x, zz.y);
             }
-            split(w[0], w[1], a[2 * tt], a[2 * tt + 1]);
+            const f2 pp = pack(pr.x, pr.y);
+            lsum = add2(lsum, pp);
+            zsum = fma2(pp, z, zsum);
+            split(mul2(pp, d), a[2 * tt], a[2 * tt + 1]);
           }
           uint32_t v0[W], v1[W];
           const uint8_t* vp = blk + B::v + (16 * warp + 8 * p + c) * D + g * (D / 8);
@@ -425,13 +478,14 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     }
 
     // ---- the unit's end: join the four warps' rows
-    lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 1);
-    lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 2);
-    zsum += __shfl_xor_sync(0xFFFFFFFFu, zsum, 1);
-    zsum += __shfl_xor_sync(0xFFFFFFFFu, zsum, 2);
+    float l = unpack(lsum).x + unpack(lsum).y, zs = unpack(zsum).x + unpack(zsum).y;
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    zs += __shfl_xor_sync(0xFFFFFFFFu, zs, 1);
+    zs += __shfl_xor_sync(0xFFFFFFFFu, zs, 2);
     if (c == 0) {
       stat[warp * kQ4Rows + g] = M;
-      stat[(kWarps + warp) * kQ4Rows + g] = lsum;
+      stat[(kWarps + warp) * kQ4Rows + g] = l;
     }
     {
       // tile t, element e of this thread is dimension D/8 (2c + e) + t; four tiles
@@ -445,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
         for (int i = 0; i < NT / 4; ++i) {
           const int piece = e * (NT / 4) + i;
           *reinterpret_cast<float4*>(dst + 4 * (piece ^ sw)) =
-              make_float4(o[4 * i][e] + o[4 * i][2 + e] + zsum, o[4 * i + 1][e] + o[4 * i + 1][2 + e] + zsum,
-                          o[4 * i + 2][e] + o[4 * i + 2][2 + e] + zsum, o[4 * i + 3][e] + o[4 * i + 3][2 + e] + zsum);
+              make_float4(o[4 * i][e] + o[4 * i][2 + e] + zs, o[4 * i + 1][e] + o[4 * i + 1][2 + e] + zs,
+                          o[4 * i + 2][e] + o[4 * i + 2][2 + e] + zs, o[4 * i + 3][e] + o[4 * i + 3][2 + e] + zs);
         }
     }
     __syncthreads();
