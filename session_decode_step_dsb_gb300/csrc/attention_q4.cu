@@ -5,13 +5,16 @@
 // a window), with K_k = z + d (c - 8) and V alike:
 //     out = sum_k softmax_k(q . K_k / sqrt D) V_k
 //
-// The codes enter both products as small signed integers, exact in fp16, and
-// the scale and offset of a key are applied outside them, in float32:
+// The codes enter both products as small integers, exact in fp16, and the scale
+// and offset of a key are applied outside them, in float32:
 //     q . K_k = d (sum_i q_i (c_i - 8)) + z (sum_i q_i)
 //     sum_k p_k V_k = sum_k (p_k d_k) (c_k - 8) + sum_k p_k z_k
-// q and the weights w_k = p_k d_k are split into two fp16 (hi + lo: 22 bits), and
-// the two parts are the two halves of one m16n8k16's rows: 8 query rows fill
-// the tensor product exactly, and the float32 accuracy costs nothing more.
+// q and the weights w_k = p_k d_k are split into two fp16 (hi + lo: 22 bits), two
+// products into one float32 sum.  Both products have the 8 query rows as their
+// columns, S^T = K Q^T (keys x rows) and O^T = V^T P^T (dimensions x rows), so that
+// m16n8k16 carries no padding at 8 rows and a warp's output tile is D/4 registers
+// a thread; the weights turn from the first product's result layout into the
+// second's operand layout by an 8 x 8 transpose in the warp.
 //
 // Work: a CTA of four warps takes units of a few pages of one (sequence, kv
 // head, tile of 8 query rows); how many pages a unit has depends on the
@@ -19,7 +22,7 @@
 // and in a batch.  A warp takes 32 of a page's 128 keys and carries its own
 // maximum, sum and output tile through the unit: inside a unit the warps meet at
 // no barrier but those of the copies.  Pages arrive as bulk copies of whole
-// blocks, two ahead.  The four warps' results are joined at the unit's end, the
+// blocks, one ahead.  The four warps' results are joined at the unit's end, the
 // units' by a second kernel in unit order (a sequence of one unit needs none).
 //
 // The running reference of the exponentials is the largest s_k plus the log of
@@ -57,27 +60,28 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], __half2 b0, __half2 b1) {
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(*reinterpret_cast<const uint32_t*>(&b0)),
-        "r"(*reinterpret_cast<const uint32_t*>(&b1)));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// The same on words that hold the half2, and from the accumulator (hi, hi, 0, 0).
-__device__ __forceinline__ void mma_w(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// The same from an accumulator whose rows hold (c0, c1).
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float hi) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %11, %11};"
+      "{%10, %11, %10, %11};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(hi), "f"(0.0f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
+// An 8 x 8 tile of 16-bit values, a row of two to each thread, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // Two float32 at once.
 using f2 = unsigned long long;
@@ -106,14 +110,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-// The (d, z) of two neighbouring keys as (d, d) and (z, z).
-__device__ __forceinline__ void numbers(uint2 w, f2& d, f2& z) {
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-  d = pack(a.x, b.x);
-  z = pack(a.y, b.y);
-}
-
 // x0, x1 as hi + lo fp16 pairs.
 __device__ __forceinline__ void split(f2 x, uint32_t& hi, uint32_t& lo) {
   const float2 v = unpack(x);
@@ -202,7 +198,7 @@ struct Cursor {
 
 template <int D>
 struct Q4Smem {
-  static constexpr int rows = D + 16;  // floats between the joined rows: two rows' quads on different banks
+  static constexpr int rows = D + 4;  // floats between the joined rows: two rows' quads on different banks
   static constexpr int join = kStages * Q4Block<D>::bytes;
   static constexpr int stat = join + kWarps * kQ4Rows * rows * 4;
   static constexpr int bars = stat + 2 * kWarps * kQ4Rows * 4;
@@ -241,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
   using S = Q4Smem<D>;
   constexpr int KS = D / 16;   // 16-dimension steps of q . K
   constexpr int W = D / 32;    // 32-bit words of a thread's piece of a K row, and of a V key pair
-  constexpr int NT = D / 8;    // 8-dimension tiles of the output
+  constexpr int NT = D / 16;   // 16-dimension tiles of the output
   extern __shared__ __align__(128) uint8_t smem[];
   float* join = reinterpret_cast<float*>(smem + S::join);
   float* stat = reinterpret_cast<float*>(smem + S::stat);  // [warp][8] maxima, then [warp][8] sums
@@ -286,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     for (int i = 0; i < kStages - 1 && more; ++i) ask();
   }
 
-  uint32_t qf[KS][4];            // q of row g as the products' left operand: rows 0..7 hi, 8..15 lo
-  float row_scale = 1.0f, row_sum = 0.0f;
-  int key_hi = 0, key_lo = 0;    // the keys row g sees
+  uint32_t qf[KS][4];               // q of row g as the product's right operand: hi, lo, hi, lo
+  f2 scale2 = 0, sum2 = 0;          // of rows 2c and 2c + 1: the scale taken out of q, and sum(q)
+  int hi0 = 0, hi1 = 0, lo0 = 0, lo1 = 0;  // the keys these two rows see
   int old_s = -1, old_h = -1, old_rt = -1;
   int n = 0;                     // pages done
   for (;;) {
@@ -299,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       const int r = cur.rt * kQ4Rows + g, j = r / G, gi = r - j * G;
       const bool live = r < R;
       // a row past the last: q = 0, the keys of the last token; never written
-      key_hi = live ? sq.len - sq.n_new + j : sq.len - 1;
-      key_lo = sq.window > 0 ? key_hi - sq.window + 1 : 0;
+      const int key_hi = live ? sq.len - sq.n_new + j : sq.len - 1;
+      const int key_lo = sq.window > 0 ? key_hi - sq.window + 1 : 0;
       float x[D / 4];
       const float* src = q + (size_t)(sq.tok0 + j) * q_stride + (size_t)(cur.h * G + gi) * D + c * (D / 4);
 #pragma unroll
@@ -317,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
-      row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
+      const float row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
       const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
-      row_sum = 0.0f;
+      float row_sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 4; ++i) {
         x[i] *= inv;
@@ -328,6 +324,11 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 1);
       row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
       row_sum *= 0x1p-24f;
+      const int r0 = 8 * c, r1 = 8 * c + 4;  // lanes of rows 2c and 2c + 1
+      scale2 = pack(__shfl_sync(0xFFFFFFFFu, row_scale, r0), __shfl_sync(0xFFFFFFFFu, row_scale, r1));
+      sum2 = pack(__shfl_sync(0xFFFFFFFFu, row_sum, r0), __shfl_sync(0xFFFFFFFFu, row_sum, r1));
+      hi0 = __shfl_sync(0xFFFFFFFFu, key_hi, r0), hi1 = __shfl_sync(0xFFFFFFFFu, key_hi, r1);
+      lo0 = __shfl_sync(0xFFFFFFFFu, key_lo, r0), lo1 = __shfl_sync(0xFFFFFFFFu, key_lo, r1);
       // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
       // nibbles stand 16 times as high in their word
 #pragma unroll
@@ -344,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
-    float M = -INFINITY;
-    f2 lsum = 0, zsum = 0;  // over even and odd keys
+    float M0 = -INFINITY, M1 = -INFINITY;
+    f2 lsum = 0, zsum = 0;
     // what any row of the tile can see, and what every row sees
     const int j0 = cur.rt * kQ4Rows / G, j1 = min(cur.rt * kQ4Rows + kQ4Rows - 1, R - 1) / G;
     const int first_hi = sq.len - sq.n_new + j0, last_hi = sq.len - sq.n_new + j1;
@@ -359,100 +360,125 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
       const int key0 = ((sq.chunk0 + pg) << 7) + 32 * warp;
       if (key0 <= last_hi && key0 + 31 >= any_lo) {
         const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
-        // ---- scores of 32 keys, four tiles of eight.  A code masked out of its word
-        // is an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the
-        // product: no conversion; -8 sum(q) starts the sums.
-        float sc[4][4];
+        // ---- scores of 32 keys, two tiles of 16.  A code masked out of its word is
+        // an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the product:
+        // no conversion; -8 sum(q) starts the sums.
+        float sc[2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
+        {
+          uint32_t kw[2][2][W];  // [tile][key g, g + 8]
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t kw[W];
-          const uint8_t* kp = blk + (32 * warp + 8 * t + g) * (D / 2) + c * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kp);
-            kw[0] = v.x, kw[1] = v.y, kw[2] = v.z, kw[3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kp);
-            kw[0] = v.x, kw[1] = v.y;
-          }
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const uint32_t k8 = kw[w] >> 8;
-            if (w == 0)
-              mma_from(sc[t], qf[0], kw[0] & 0x000F000Fu, kw[0] & 0x00F000F0u, -8.0f * row_sum);
-            else
-              mma_w(sc[t], qf[2 * w], kw[w] & 0x000F000Fu, kw[w] & 0x00F000F0u);
-            mma_w(sc[t], qf[2 * w + 1], k8 & 0x000F000Fu, k8 & 0x00F000F0u);
-          }
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* kp = blk + (32 * warp + 16 * t + 8 * h + g) * (D / 2) + c * (D / 8);
+              if constexpr (D == 128) {
+                const uint4 v = *reinterpret_cast<const uint4*>(kp);
+                kw[t][h][0] = v.x, kw[t][h][1] = v.y, kw[t][h][2] = v.z, kw[t][h][3] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(kp);
+                kw[t][h][0] = v.x, kw[t][h][1] = v.y;
+              }
+            }
+          const float2 start = unpack(mul2(sum2, pack(-8.0f, -8.0f)));
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t x = kw[t][0][w] >> (8 * b), y = kw[t][1][w] >> (8 * b);
+                const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
+                const uint32_t(&q4)[4] = qf[2 * w + b];
+                if (w == 0 && b == 0) {
+                  mma_from(sc[t][0], a0, a1, a2, a3, q4[0], q4[2], start.x, start.y);
+                  mma_from(sc[t][1], a0, a1, a2, a3, q4[1], q4[3], 0.0f, 0.0f);
+                } else {
+                  mma(sc[t][0], a0, a1, a2, a3, q4[0], q4[2]);
+                  mma(sc[t][1], a0, a1, a2, a3, q4[1], q4[3]);
+                }
+              }
         }
         // the largest scale of V among the 32 keys (bits of an fp16 that is not negative)
         uint32_t vd = *reinterpret_cast<const uint16_t*>(blk + B::vz + (32 * warp + lane) * 4);
         if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
         vd = __reduce_max_sync(0xFFFFFFFFu, vd);
         const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
-        // s = d acc + z sum(q) for keys 8t + 2c, + 1 of row g, times 2^-24
-        f2 x[4];
-        float top = -INFINITY;
-        const f2 rsum = pack(row_sum, row_sum);
+        // s = d acc + z sum(q) of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
+        f2 x[2][2];
+        float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          f2 d, z;
-          numbers(*reinterpret_cast<const uint2*>(blk + B::kz + (32 * warp + 8 * t + 2 * c) * 4), d, z);
-          x[t] = fma2(d, add2(pack(sc[t][0], sc[t][1]), pack(sc[t][2], sc[t][3])), mul2(z, rsum));
-          float2 v = unpack(x[t]);
-          if (!whole) {
-            const int key = key0 + 8 * t + 2 * c;
-            if (key > key_hi || key < key_lo) v.x = -INFINITY;
-            if (key + 1 > key_hi || key + 1 < key_lo) v.y = -INFINITY;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 dz =
+                __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
+            const f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]), pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
+            x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
+            float2 v = unpack(x[t][h]);
+            if (!whole) {
+              const int key = key0 + 16 * t + 8 * h + g;
+              if (key > hi0 || key < lo0) v.x = -INFINITY;
+              if (key > hi1 || key < lo1) v.y = -INFINITY;
+            }
+            top0 = fmaxf(top0, v.x);
+            top1 = fmaxf(top1, v.y);
           }
-          top = fmaxf(top, fmaxf(v.x, v.y));
+#pragma unroll
+        for (int s4 = 4; s4 < 32; s4 <<= 1) {
+          top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, s4));
+          top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, s4));
         }
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        top = __fmaf_rn(row_scale, top, vd_log);
+        {
+          const float2 sc2 = unpack(scale2);
+          top0 = __fmaf_rn(sc2.x, top0, vd_log);
+          top1 = __fmaf_rn(sc2.y, top1, vd_log);
+        }
         // The reference is set 2^10 below the largest weight and moves only when
         // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
         // coarser than 2^-35 of the largest weight.
-        if (__any_sync(0xFFFFFFFFu, top > M + 14.0f)) {
-          const float to = top > M + 14.0f ? top - 10.0f : M;
-          if (__any_sync(0xFFFFFFFFu, M != -INFINITY)) {  // else nothing has been summed yet
-            const float f = M == -INFINITY ? 0.0f : ex2(M - to);
-            const f2 ff = pack(f, f);
-            lsum = mul2(lsum, ff);
-            zsum = mul2(zsum, ff);
+        if (__any_sync(0xFFFFFFFFu, top0 > M0 + 14.0f || top1 > M1 + 14.0f)) {
+          const float to0 = top0 > M0 + 14.0f ? top0 - 10.0f : M0, to1 = top1 > M1 + 14.0f ? top1 - 10.0f : M1;
+          if (__any_sync(0xFFFFFFFFu, M0 != -INFINITY || M1 != -INFINITY)) {  // else nothing has been summed yet
+            const float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - to0), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - to1);
+            lsum = mul2(lsum, pack(f0, f1));
+            zsum = mul2(zsum, pack(f0, f1));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[t][e] *= f;
+            for (int t = 0; t < NT; ++t) {
+              o[t][0] *= f0, o[t][1] *= f1;
+              o[t][2] *= f0, o[t][3] *= f1;
+            }
           }
-          M = to;
+          M0 = to0, M1 = to1;
         }
         // ---- weights, and 16 keys at a time their product with V
-        const f2 rs2 = pack(row_scale, row_scale), nm2 = pack(-M, -M);
+        const f2 minus = pack(-M0, -M1);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          uint32_t a[4];
+        for (int t = 0; t < 2; ++t) {
+          uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
 #pragma unroll
-          for (int tt = 0; tt < 2; ++tt) {
-            const int t = 2 * p + tt;
-            f2 d, z;
-            numbers(*reinterpret_cast<const uint2*>(blk + B::vz + (32 * warp + 8 * t + 2 * c) * 4), d, z);
-            const float2 v = unpack(fma2(rs2, x[t], nm2));
+          for (int h = 0; h < 2; ++h) {
+            const float2 dz =
+                __half22float2(*reinterpret_cast<const __half2*>(blk + B::vz + (32 * warp + 16 * t + 8 * h + g) * 4));
+            f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
+            const float2 v = unpack(fma2(scale2, x[t][h], minus));
             float2 pr = make_float2(ex2(v.x), ex2(v.y));
             if (!whole) {  // a hidden key's numbers may be anything
-              const int key = key0 + 8 * t + 2 * c;
-              float2 dd = unpack(d), zz = unpack(z);
-              if (key > key_hi || key < key_lo) pr.x = dd.x = zz.x = 0.0f;
-              if (key + 1 > key_hi || key + 1 < key_lo) pr.y = dd.y = zz.y = 0.0f;
-              d = pack(dd.x, dd.y);
-              z = pack(zz.x, zz.y);
+              const int key = key0 + 16 * t + 8 * h + g;
+              const bool no0 = key > hi0 || key < lo0, no1 = key > hi1 || key < lo1;
+              if (no0) pr.x = 0.0f;
+              if (no1) pr.y = 0.0f;
+              d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
+              z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
             }
             const f2 pp = pack(pr.x, pr.y);
             lsum = add2(lsum, pp);
             zsum = fma2(pp, z, zsum);
-            split(mul2(pp, d), a[2 * tt], a[2 * tt + 1]);
+            split(mul2(pp, d), ph[h], pl[h]);
+            ph[h] = transpose8(ph[h]);
+            pl[h] = transpose8(pl[h]);
           }
           uint32_t v0[W], v1[W];
-          const uint8_t* vp = blk + B::v + (16 * warp + 8 * p + c) * D + g * (D / 8);
+          const uint8_t* vp = blk + B::v + (16 * warp + 8 * t + c) * D + g * (D / 8);
           if constexpr (D == 128) {
             const uint4 u0 = *reinterpret_cast<const uint4*>(vp), u1 = *reinterpret_cast<const uint4*>(vp + 4 * D);
             v0[0] = u0.x, v0[1] = u0.y, v0[2] = u0.z, v0[3] = u0.w;
@@ -462,13 +488,18 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
             v0[0] = u0.x, v0[1] = u0.y;
             v1[0] = u1.x, v1[1] = u1.y;
           }
+          // tile j: its rows g and g + 8 are dimensions D/8 g + 2j and + 1
 #pragma unroll
           for (int w = 0; w < W; ++w) {
             __half2 h0[4], h1[4];
             q4_unpack(v0[w], h0);
             q4_unpack(v1[w], h1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma(o[4 * w + i], a, h0[i], h1[i]);
+            for (int i = 0; i < 2; ++i)
+              mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]), ph[0], ph[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]), pl[0], pl[1]);
           }
         }
       }
@@ -478,35 +509,34 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
     }
 
     // ---- the unit's end: join the four warps' rows
-    float l = unpack(lsum).x + unpack(lsum).y, zs = unpack(zsum).x + unpack(zsum).y;
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    zs += __shfl_xor_sync(0xFFFFFFFFu, zs, 1);
-    zs += __shfl_xor_sync(0xFFFFFFFFu, zs, 2);
-    if (c == 0) {
-      stat[warp * kQ4Rows + g] = M;
-      stat[(kWarps + warp) * kQ4Rows + g] = l;
+#pragma unroll
+    for (int s4 = 4; s4 < 32; s4 <<= 1) {
+      const float2 l = unpack(lsum), z = unpack(zsum);
+      lsum = add2(lsum, pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
+      zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
+    }
+    const float2 l2 = unpack(lsum), z2 = unpack(zsum);
+    if (g == 0) {
+      *reinterpret_cast<float2*>(stat + warp * kQ4Rows + 2 * c) = make_float2(M0, M1);
+      *reinterpret_cast<float2*>(stat + (kWarps + warp) * kQ4Rows + 2 * c) = l2;
     }
     {
-      // tile t, element e of this thread is dimension D/8 (2c + e) + t; four tiles
-      // make a 16-byte piece, and the pieces of a c are swizzled so that the four
-      // c's of a row hit different banks
-      float* dst = join + (warp * kQ4Rows + g) * S::rows + c * (D / 4);
-      const int sw = D == 128 ? c : c >> 1;
+      // this thread's dimensions D/8 g .. of rows 2c and 2c + 1, in 16-byte pieces;
+      // neighbouring g's swap theirs, so that 8 threads hit different banks
+      float* dst = join + (warp * kQ4Rows + 2 * c) * S::rows + g * (D / 8);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < NT / 4; ++i) {
-          const int piece = e * (NT / 4) + i;
-          *reinterpret_cast<float4*>(dst + 4 * (piece ^ sw)) =
-              make_float4(o[4 * i][e] + o[4 * i][2 + e] + zs, o[4 * i + 1][e] + o[4 * i + 1][2 + e] + zs,
-                          o[4 * i + 2][e] + o[4 * i + 2][2 + e] + zs, o[4 * i + 3][e] + o[4 * i + 3][2 + e] + zs);
-        }
+      for (int i = 0; i < NT / 2; ++i) {
+        float* at = dst + 4 * (i ^ (g & 1));
+        *reinterpret_cast<float4*>(at) = make_float4(o[2 * i][0] + z2.x, o[2 * i][2] + z2.x, o[2 * i + 1][0] + z2.x,
+                                                     o[2 * i + 1][2] + z2.x);
+        *reinterpret_cast<float4*>(at + S::rows) = make_float4(o[2 * i][1] + z2.y, o[2 * i][3] + z2.y,
+                                                               o[2 * i + 1][1] + z2.y, o[2 * i + 1][3] + z2.y);
+      }
     }
     __syncthreads();
     {
-      const int dim = tid % D, cc = dim / (D / 4), in = dim % (D / 4);
-      const int place = cc * (D / 4) + 4 * ((in >> 2) ^ (D == 128 ? cc : cc >> 1)) + (in & 3);
+      const int dim = tid % D, gg = dim / (D / 8), in = dim % (D / 8);
+      const int place = gg * (D / 8) + 4 * ((in >> 2) ^ (gg & 1)) + (in & 3);
       const int rows = min(kQ4Rows, R - cur.rt * kQ4Rows);
       int i = tid / D, r = cur.rt * kQ4Rows + i, j = r / G, gi = r - j * G;
       for (; i < rows; i += kThreads / D) {

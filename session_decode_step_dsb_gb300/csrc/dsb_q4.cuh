@@ -38,10 +38,16 @@ struct Q4Block {
 // half) and nibble n + 4 (high half).  A nibble at bits 0..3 of an fp16 with
 // exponent bits 0x6400 is 1024 + q; at bits 4..7 it is 1024 + 16 q.  Both steps
 // are exact.
+// (w & mask) | 0x64006400 in one instruction.
+__device__ __forceinline__ uint32_t q4_biased(uint32_t w, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+  return r;
+}
 __device__ __forceinline__ void q4_unpack(uint32_t w, __half2 (&h)[4]) {
-  const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (w & 0x00F000F0u) | 0x64006400u;
   const uint32_t w8 = w >> 8;
-  const uint32_t c = (w8 & 0x000F000Fu) | 0x64006400u, d = (w8 & 0x00F000F0u) | 0x64006400u;
+  const uint32_t a = q4_biased(w, 0x000F000Fu), b = q4_biased(w, 0x00F000F0u);
+  const uint32_t c = q4_biased(w8, 0x000F000Fu), d = q4_biased(w8, 0x00F000F0u);
   const __half2 bias = __float2half2_rn(1032.0f), s = __float2half2_rn(0.0625f), o = __float2half2_rn(-72.0f);
   h[0] = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
   h[1] = __hfma2(*reinterpret_cast<const __half2*>(&b), s, o);
