@@ -45,7 +45,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;
 
 __device__ unsigned int g_err_attention_q4 = 0;
 
@@ -127,11 +126,14 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // Where a CTA is in its list of items: one unit of one (sequence, kv head, row
 // tile), and the page inside it.  Divides once, at its start; then it counts.
+// Kept in shared memory by thread 0; the others read what they need of it.
 struct Cursor {
+  int fresh;  // another sequence, head or row tile than the item before
   int at;  // pages of work before this item
   int s, h, rt, u, units, tiles, pages, pg, pg_end;
   Q4Seq q;
 
+  template <int NR>
   __device__ __forceinline__ void load(const int32_t* meta, int G) {
     const int32_t* p = meta + s * kQ4SeqWords;
     q.work_off = p[0];
@@ -144,13 +146,14 @@ struct Cursor {
     q.u_pages = p[7];
     pages = ((q.len - 1) >> 7) - q.chunk0 + 1;
     units = (pages + q.u_pages - 1) / q.u_pages;
-    tiles = (G * q.n_new + kQ4Rows - 1) / kQ4Rows;
+    tiles = (G * q.n_new + 8 * NR - 1) / (8 * NR);
   }
   __device__ __forceinline__ void place() {
     pg = u * q.u_pages;
     pg_end = min(pg + q.u_pages, pages);
   }
   // The first item that starts at or after `from` pages of work; false if none.
+  template <int NR>
   __device__ __forceinline__ bool start(const int32_t* meta, int n_seq, int hkv, int G, int from) {
     int lo = 0, hi = n_seq - 1;
     while (lo < hi) {
@@ -161,7 +164,7 @@ struct Cursor {
         hi = mid - 1;
     }
     s = lo;
-    load(meta, G);
+    load<NR>(meta, G);
     const int rel = from - q.work_off;
     int x = rel / pages;
     u = (rel - x * pages + q.u_pages - 1) / q.u_pages;
@@ -171,23 +174,27 @@ struct Cursor {
     if (h == hkv) {
       if (++s == n_seq) return false;
       h = 0;
-      load(meta, G);
+      load<NR>(meta, G);
     }
     place();
     at = q.work_off + (h * tiles + rt) * pages + pg;
+    fresh = 1;
     return true;
   }
   // The next item (one that exists).
+  template <int NR>
   __device__ __forceinline__ void next(const int32_t* meta, int hkv, int G) {
     at += pg_end - u * q.u_pages;
+    fresh = 0;
     if (++u == units) {
       u = 0;
+      fresh = 1;
       if (++rt == tiles) {
         rt = 0;
         if (++h == hkv) {
           h = 0;
           ++s;
-          load(meta, G);
+          load<NR>(meta, G);
         }
       }
     }
@@ -196,58 +203,64 @@ struct Cursor {
   __device__ __forceinline__ int end() const { return at + pg_end - u * q.u_pages; }  // pages before the next item
 };
 
-template <int D>
+constexpr int kSlots = 5;  // half pages (K or V) on their way or in use
+
+// NR: tiles of 8 query rows that a CTA works on together.
+template <int D, int NR>
 struct Q4Smem {
-  static constexpr int rows = D + 4;  // floats between the joined rows: two rows' quads on different banks
-  static constexpr int join = kStages * Q4Block<D>::bytes;
-  static constexpr int stat = join + kWarps * kQ4Rows * rows * 4;
-  static constexpr int bars = stat + 2 * kWarps * kQ4Rows * 4;
-  static constexpr int bytes = bars + 2 * kStages * 8;
+  static constexpr int half = Q4Block<D>::v;                // K codes and numbers; V's are as many bytes
+  static constexpr int q = kSlots * half;                   // [D/16][NR][32 lanes] uint4: q as right operand
+  static constexpr int rows = q + D / 16 * NR * 512;        // [8 NR] float4: scale, sum, last key, -
+  static constexpr int join = rows + 8 * NR * 16;           // [2 warps][NR * D/16][32 lanes] float4
+  static constexpr int stat = join + 2 * NR * (D / 16) * 512;  // [2 warps][NR][4] float4: M, M, sum, sum
+  static constexpr int bars = stat + 2 * NR * 64;
+  static constexpr int cursors = bars + 2 * kSlots * 8;     // the item in work, the next to ask for, "done"
+  static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
 };
 
-// One thread requests the page the cursor is at: its block's four parts up to
-// the sequence's last key (rounded up to four keys: 16-byte pieces), or, where
-// the page is full, the block in one piece.
+// One thread requests the K (which = 0) or V half of the page the cursor is at:
+// codes and numbers up to the sequence's last key (rounded up to four keys:
+// 16-byte pieces), or, where the page is full, the half in one piece.
 template <int D>
-__device__ __forceinline__ void request(const Cursor& c, const int32_t* meta, const uint8_t* pool, int hkv, uint8_t* dst,
-                                        uint64_t* bar) {
+__device__ __forceinline__ void request(const Cursor& c, int which, const int32_t* meta, const uint8_t* pool, int hkv,
+                                        uint8_t* dst, uint64_t* bar) {
   using B = Q4Block<D>;
   const int page = meta[c.q.pg_at + c.pg];
-  const uint8_t* src = pool + ((size_t)page * hkv + c.h) * B::bytes;
+  const uint8_t* src = pool + ((size_t)page * hkv + c.h) * B::bytes + (which ? B::v : 0);
   const int keys = min(kQ4Page, (c.q.len - ((c.q.chunk0 + c.pg) << 7) + 3) & ~3);
   if (keys == kQ4Page) {
-    mbar_arrive_expect_tx(bar, B::bytes);
-    bulk_g2s(dst, src, B::bytes, bar);
+    mbar_arrive_expect_tx(bar, B::v);
+    bulk_g2s(dst, src, B::v, bar);
   } else {
     const uint32_t codes = keys * (D / 2), nums = keys * 4;
-    mbar_arrive_expect_tx(bar, 2 * (codes + nums));
+    mbar_arrive_expect_tx(bar, codes + nums);
     bulk_g2s(dst, src, codes, bar);
     bulk_g2s(dst + B::kz, src + B::kz, nums, bar);
-    bulk_g2s(dst + B::v, src + B::v, codes, bar);
-    bulk_g2s(dst + B::vz, src + B::vz, nums, bar);
   }
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
+template <int D, int NR, int N>
+__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel(
     const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint8_t* __restrict__ pool, int n_seq,
     float scale_log2e, int max_units, float* __restrict__ partials, float* __restrict__ out,
     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using B = Q4Block<D>;
-  using S = Q4Smem<D>;
-  constexpr int KS = D / 16;   // 16-dimension steps of q . K
+  using S = Q4Smem<D, NR>;
   constexpr int W = D / 32;    // 32-bit words of a thread's piece of a K row, and of a V key pair
   constexpr int NT = D / 16;   // 16-dimension tiles of the output
+  constexpr int ROWS = 8 * NR;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* join = reinterpret_cast<float*>(smem + S::join);
-  float* stat = reinterpret_cast<float*>(smem + S::stat);  // [warp][8] maxima, then [warp][8] sums
+  uint4* qs = reinterpret_cast<uint4*>(smem + S::q);
+  float4* rowp = reinterpret_cast<float4*>(smem + S::rows);
+  float4* join = reinterpret_cast<float4*>(smem + S::join);
+  float4* stat = reinterpret_cast<float4*>(smem + S::stat);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bars);
-  uint64_t* empty = full + kStages;
+  uint64_t* empty = full + kSlots;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int G = hq / hkv;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kWarps);
     }
@@ -256,229 +269,281 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  // this CTA's items: those that start in its share of the pages
+  // This CTA's items: those that start in its share of the pages.  Thread 0 asks
+  // for the half pages, kSlots - 1 ahead: after its warp has left one, for the slot
+  // of the one before, which the other warps have left long since.
+  Cursor* cur = reinterpret_cast<Cursor*>(smem + S::cursors);
+  Cursor* ahead = cur + 1;
+  int* done = reinterpret_cast<int*>(cur + 2);
   const long long total = meta[n_seq * kQ4SeqWords];
-  const int w0 = (int)(total * blockIdx.x / gridDim.x), w1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  Cursor cur;
-  if (w0 >= w1 || !cur.start(meta, n_seq, hkv, G, w0) || cur.at >= w1) return;
-
-  // Thread 0 runs kStages - 1 pages ahead of the others.
-  Cursor ahead = cur;
-  int asked = 0;
-  bool more = true;
+  const int w1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
+  int ask_slot = 0, ask_which = 0;
+  uint32_t ask_phase = 1;  // parity of the slot's last release; the first round waits for none
+  bool more = false;
   auto ask = [&]() {
-    const int st = asked % kStages, use = asked / kStages;
-    if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1)) g_err_attention_q4 = 1u;
-    request<D>(ahead, meta, pool, hkv, smem + st * B::bytes, &full[st]);
-    ++asked;
-    if (++ahead.pg == ahead.pg_end) {
-      if (ahead.end() < w1)
-        ahead.next(meta, hkv, G);
+    if (!mbar_wait(&empty[ask_slot], ask_phase)) g_err_attention_q4 = 1u;
+    request<D>(*ahead, ask_which, meta, pool, hkv, smem + ask_slot * S::half, &full[ask_slot]);
+    if (++ask_slot == kSlots) ask_slot = 0, ask_phase ^= 1;
+    if ((ask_which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
+      if (ahead->end() < w1)
+        ahead->next<NR>(meta, hkv, G);
       else
         more = false;
     }
   };
   if (tid == 0) {
-    for (int i = 0; i < kStages - 1 && more; ++i) ask();
-  }
-
-  uint32_t qf[KS][4];               // q of row g as the product's right operand: hi, lo, hi, lo
-  f2 scale2 = 0, sum2 = 0;          // of rows 2c and 2c + 1: the scale taken out of q, and sum(q)
-  int hi0 = 0, hi1 = 0, lo0 = 0, lo1 = 0;  // the keys these two rows see
-  int old_s = -1, old_h = -1, old_rt = -1;
-  int n = 0;                     // pages done
-  for (;;) {
-    const Q4Seq& sq = cur.q;
-    const int R = G * sq.n_new;
-    if (cur.s != old_s || cur.h != old_h || cur.rt != old_rt) {
-      old_s = cur.s, old_h = cur.h, old_rt = cur.rt;
-      const int r = cur.rt * kQ4Rows + g, j = r / G, gi = r - j * G;
-      const bool live = r < R;
-      // a row past the last: q = 0, the keys of the last token; never written
-      const int key_hi = live ? sq.len - sq.n_new + j : sq.len - 1;
-      const int key_lo = sq.window > 0 ? key_hi - sq.window + 1 : 0;
-      float x[D / 4];
-      const float* src = q + (size_t)(sq.tok0 + j) * q_stride + (size_t)(cur.h * G + gi) * D + c * (D / 4);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const float4 v = live ? __ldcg(reinterpret_cast<const float4*>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
-        x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
-      }
-      // the row over a power of two that brings its largest value to [2^10, 2^11):
-      // the split keeps its 22 bits whatever q's size
-      float m = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
-      const float row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
-      const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
-      float row_sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) {
-        x[i] *= inv;
-        row_sum += x[i];
-      }
-      row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 1);
-      row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
-      row_sum *= 0x1p-24f;
-      const int r0 = 8 * c, r1 = 8 * c + 4;  // lanes of rows 2c and 2c + 1
-      scale2 = pack(__shfl_sync(0xFFFFFFFFu, row_scale, r0), __shfl_sync(0xFFFFFFFFu, row_scale, r1));
-      sum2 = pack(__shfl_sync(0xFFFFFFFFu, row_sum, r0), __shfl_sync(0xFFFFFFFFu, row_sum, r1));
-      hi0 = __shfl_sync(0xFFFFFFFFu, key_hi, r0), hi1 = __shfl_sync(0xFFFFFFFFu, key_hi, r1);
-      lo0 = __shfl_sync(0xFFFFFFFFu, key_lo, r0), lo1 = __shfl_sync(0xFFFFFFFFu, key_lo, r1);
-      // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
-      // nibbles stand 16 times as high in their word
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), qf[2 * w + b][0], qf[2 * w + b][1]);
-          split(pack(x[8 * w + 2 * b + 1] * 0.0625f, x[8 * w + 2 * b + 5] * 0.0625f), qf[2 * w + b][2],
-                qf[2 * w + b][3]);
-        }
+    const int w0 = (int)(total * blockIdx.x / gridDim.x);
+    Cursor first;
+    more = w0 < w1 && first.start<NR>(meta, n_seq, hkv, G, w0) && first.at < w1;
+    *done = !more;
+    if (more) {
+      *cur = first;
+      *ahead = first;
+      for (int i = 0; i < kSlots - 1 && more; ++i) ask();
     }
-    float o[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
-    float M0 = -INFINITY, M1 = -INFINITY;
-    f2 lsum = 0, zsum = 0;
-    // what any row of the tile can see, and what every row sees
-    const int j0 = cur.rt * kQ4Rows / G, j1 = min(cur.rt * kQ4Rows + kQ4Rows - 1, R - 1) / G;
-    const int first_hi = sq.len - sq.n_new + j0, last_hi = sq.len - sq.n_new + j1;
-    const int any_lo = sq.window > 0 ? first_hi - sq.window + 1 : 0, all_lo = sq.window > 0 ? sq.len - sq.window : 0;
+  }
+  __syncthreads();
+  if (*done) return;
 
-    for (int pg = cur.pg; pg < cur.pg_end; ++pg, ++n) {
-      const int st = n % kStages;
-      if (!mbar_wait(&full[st], (n / kStages) & 1)) g_err_attention_q4 = 1u;
+  int slot = 0;
+  uint32_t phase = 0;
+  auto release = [&]() {  // this warp is done with the slot
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == kSlots) slot = 0, phase ^= 1;
+  };
+  for (;;) {
+    const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * ROWS, R = G * n_new;
+    if (cur->fresh) {
+      if (warp < NR) {  // a warp for each tile of 8 rows: row g, dimensions D/4 c ..
+        const int r = row0 + 8 * warp + g, j = r / G, gi = r - j * G;
+        const bool live = r < R;
+        float x[D / 4];
+        const float* src = q + (size_t)(cur->q.tok0 + j) * q_stride + (size_t)(cur->h * G + gi) * D + c * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const float4 v = live ? __ldcg(reinterpret_cast<const float4*>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
+          x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
+        }
+        // the row over a power of two that brings its largest value to [2^10, 2^11):
+        // the split keeps its 22 bits whatever q's size
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
+        const float row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
+        const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
+        float row_sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+          x[i] *= inv;
+          row_sum += x[i];
+        }
+        row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 1);
+        row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
+        // a row past the last: q = 0, the keys of the last token; never written
+        if (c == 0)
+          rowp[8 * warp + g] = make_float4(row_scale, row_sum * 0x1p-24f,
+                                           __int_as_float(live ? len - n_new + j : len - 1), 0.0f);
+        // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
+        // nibbles stand 16 times as high in their word
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint4 v;  // hi of the step's two halves, then lo
+            split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), v.x, v.z);
+            split(pack(x[8 * w + 2 * b + 1] * 0.0625f, x[8 * w + 2 * b + 5] * 0.0625f), v.y, v.w);
+            qs[((2 * w + b) * NR + warp) * 32 + lane] = v;
+          }
+      }
+      __syncthreads();
+    }
+    // rows 2c and 2c + 1 of each tile: the scale taken out of q, sum(q), the last key seen
+    f2 scale2[NR], sum2[NR];
+    int hi0[NR], hi1[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float4 a = rowp[8 * n + 2 * c], b = rowp[8 * n + 2 * c + 1];
+      scale2[n] = pack(a.x, b.x);
+      sum2[n] = pack(a.y, b.y);
+      hi0[n] = __float_as_int(a.z), hi1[n] = __float_as_int(b.z);
+    }
+    const int back = window > 0 ? window - 1 : 0x7FFFFFFF;  // keys seen before the last
+    float o[NR][NT][4];
+    float M0[NR], M1[NR];
+    f2 lsum[NR], zsum[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][t][e] = 0.0f;
+      M0[n] = M1[n] = -INFINITY;
+      lsum[n] = zsum[n] = 0;
+    }
+    // what any row of the item can see, and what every row sees
+    const int j0 = row0 / G, j1 = min(row0 + ROWS - 1, R - 1) / G;
+    const int first_hi = len - n_new + j0, last_hi = len - n_new + j1;
+    const int any_lo = first_hi - back, all_lo = window > 0 ? len - window : 0;
+
+    int key0 = ((cur->q.chunk0 + cur->pg) << 7) + 32 * warp;  // this warp's first key of the page
+    for (int left = cur->pg_end - cur->pg; left > 0; --left, key0 += kQ4Page) {
+      const bool some = key0 <= last_hi && key0 + 31 >= any_lo;
+      const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
+      const auto hidden = [&](int key, int last) { return key > last || last - key > back; };
+      // ---- scores of 32 keys, two tiles of 16.  A code masked out of its word is
+      // an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the product:
+      // no conversion; -8 sum(q) starts the sums.
+      if (!mbar_wait(&full[slot], phase)) g_err_attention_q4 = 1u;
       __syncwarp();
-      const uint8_t* blk = smem + st * B::bytes;
-      const int key0 = ((sq.chunk0 + pg) << 7) + 32 * warp;
-      if (key0 <= last_hi && key0 + 31 >= any_lo) {
-        const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
-        // ---- scores of 32 keys, two tiles of 16.  A code masked out of its word is
-        // an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the product:
-        // no conversion; -8 sum(q) starts the sums.
-        float sc[2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
-        {
-          uint32_t kw[2][2][W];  // [tile][key g, g + 8]
+      f2 x[NR][2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
+      if (some) {
+        const uint8_t* blk = smem + slot * S::half;
+        float sc[NR][2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
+        uint32_t kw[2][2][W];   // [tile][key g, g + 8]
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint8_t* kp = blk + (32 * warp + 16 * t + 8 * h + g) * (D / 2) + c * (D / 8);
-              if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4*>(kp);
-                kw[t][h][0] = v.x, kw[t][h][1] = v.y, kw[t][h][2] = v.z, kw[t][h][3] = v.w;
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(kp);
-                kw[t][h][0] = v.x, kw[t][h][1] = v.y;
-              }
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* kp = blk + (32 * warp + 16 * t + 8 * h + g) * (D / 2) + c * (D / 8);
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kp);
+              kw[t][h][0] = v.x, kw[t][h][1] = v.y, kw[t][h][2] = v.z, kw[t][h][3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(kp);
+              kw[t][h][0] = v.x, kw[t][h][1] = v.y;
             }
-          const float2 start = unpack(mul2(sum2, pack(-8.0f, -8.0f)));
+          }
 #pragma unroll
-          for (int w = 0; w < W; ++w)
+        for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < 2; ++b) {
+            uint4 q4[NR];
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t x = kw[t][0][w] >> (8 * b), y = kw[t][1][w] >> (8 * b);
-                const uint32_t a0 = x & 0x000F000Fu, a1 = y & 0x000F000Fu, a2 = x & 0x00F000F0u, a3 = y & 0x00F000F0u;
-                const uint32_t(&q4)[4] = qf[2 * w + b];
+            for (int n = 0; n < NR; ++n) q4[n] = qs[((2 * w + b) * NR + n) * 32 + lane];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t u = kw[t][0][w] >> (8 * b), v = kw[t][1][w] >> (8 * b);
+              const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
                 if (w == 0 && b == 0) {
-                  mma_from(sc[t][0], a0, a1, a2, a3, q4[0], q4[2], start.x, start.y);
-                  mma_from(sc[t][1], a0, a1, a2, a3, q4[1], q4[3], 0.0f, 0.0f);
+                  const float2 start = unpack(mul2(sum2[n], pack(-8.0f, -8.0f)));
+                  mma_from(sc[n][t][0], a0, a1, a2, a3, q4[n].x, q4[n].y, start.x, start.y);
+                  mma_from(sc[n][t][1], a0, a1, a2, a3, q4[n].z, q4[n].w, 0.0f, 0.0f);
                 } else {
-                  mma(sc[t][0], a0, a1, a2, a3, q4[0], q4[2]);
-                  mma(sc[t][1], a0, a1, a2, a3, q4[1], q4[3]);
+                  mma(sc[n][t][0], a0, a1, a2, a3, q4[n].x, q4[n].y);
+                  mma(sc[n][t][1], a0, a1, a2, a3, q4[n].z, q4[n].w);
                 }
               }
-        }
-        // the largest scale of V among the 32 keys (bits of an fp16 that is not negative)
-        uint32_t vd = *reinterpret_cast<const uint16_t*>(blk + B::vz + (32 * warp + lane) * 4);
-        if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
-        vd = __reduce_max_sync(0xFFFFFFFFu, vd);
-        const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
-        // s = d acc + z sum(q) of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
-        f2 x[2][2];
-        float top0 = -INFINITY, top1 = -INFINITY;
+            }
+          }
+        // s = d acc + z sum(q)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
-            const f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]), pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
-            x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
-            float2 v = unpack(x[t][h]);
-            if (!whole) {
-              const int key = key0 + 16 * t + 8 * h + g;
-              if (key > hi0 || key < lo0) v.x = -INFINITY;
-              if (key > hi1 || key < lo1) v.y = -INFINITY;
-            }
-            top0 = fmaxf(top0, v.x);
-            top1 = fmaxf(top1, v.y);
-          }
 #pragma unroll
-        for (int s4 = 4; s4 < 32; s4 <<= 1) {
-          top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, s4));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, s4));
-        }
-        {
-          const float2 sc2 = unpack(scale2);
+            for (int n = 0; n < NR; ++n) {
+              const f2 acc = add2(pack(sc[n][t][0][2 * h], sc[n][t][0][2 * h + 1]),
+                                  pack(sc[n][t][1][2 * h], sc[n][t][1][2 * h + 1]));
+              x[n][t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2[n]));
+            }
+          }
+      }
+      release();
+      if (tid == 0 && more) ask();
+
+      if (!mbar_wait(&full[slot], phase)) g_err_attention_q4 = 1u;
+      __syncwarp();
+      if (some) {
+        const uint8_t* blk = smem + slot * S::half;
+        // the largest scale of V among the 32 keys (bits of an fp16 that is not negative)
+        uint32_t vd = *reinterpret_cast<const uint16_t*>(blk + B::kz + (32 * warp + lane) * 4);
+        if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
+        vd = __reduce_max_sync(0xFFFFFFFFu, vd);
+        const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2 v = unpack(x[n][t][h]);
+              if (!whole) {
+                const int key = key0 + 16 * t + 8 * h + g;
+                if (hidden(key, hi0[n])) v.x = -INFINITY;
+                if (hidden(key, hi1[n])) v.y = -INFINITY;
+              }
+              top0 = fmaxf(top0, v.x);
+              top1 = fmaxf(top1, v.y);
+            }
+#pragma unroll
+          for (int s4 = 4; s4 < 32; s4 <<= 1) {
+            top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, s4));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, s4));
+          }
+          const float2 sc2 = unpack(scale2[n]);
           top0 = __fmaf_rn(sc2.x, top0, vd_log);
           top1 = __fmaf_rn(sc2.y, top1, vd_log);
-        }
-        // The reference is set 2^10 below the largest weight and moves only when
-        // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
-        // coarser than 2^-35 of the largest weight.
-        if (__any_sync(0xFFFFFFFFu, top0 > M0 + 14.0f || top1 > M1 + 14.0f)) {
-          const float to0 = top0 > M0 + 14.0f ? top0 - 10.0f : M0, to1 = top1 > M1 + 14.0f ? top1 - 10.0f : M1;
-          if (__any_sync(0xFFFFFFFFu, M0 != -INFINITY || M1 != -INFINITY)) {  // else nothing has been summed yet
-            const float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - to0), f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - to1);
-            lsum = mul2(lsum, pack(f0, f1));
-            zsum = mul2(zsum, pack(f0, f1));
+          // The reference is set 2^10 below the largest weight and moves only when
+          // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
+          // coarser than 2^-35 of the largest weight.
+          if (__any_sync(0xFFFFFFFFu, top0 > M0[n] + 14.0f || top1 > M1[n] + 14.0f)) {
+            const float to0 = top0 > M0[n] + 14.0f ? top0 - 10.0f : M0[n];
+            const float to1 = top1 > M1[n] + 14.0f ? top1 - 10.0f : M1[n];
+            if (__any_sync(0xFFFFFFFFu, M0[n] != -INFINITY || M1[n] != -INFINITY)) {  // else nothing is summed yet
+              const float f0 = M0[n] == -INFINITY ? 0.0f : ex2(M0[n] - to0);
+              const float f1 = M1[n] == -INFINITY ? 0.0f : ex2(M1[n] - to1);
+              lsum[n] = mul2(lsum[n], pack(f0, f1));
+              zsum[n] = mul2(zsum[n], pack(f0, f1));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              o[t][0] *= f0, o[t][1] *= f1;
-              o[t][2] *= f0, o[t][3] *= f1;
+              for (int t = 0; t < NT; ++t) {
+                o[n][t][0] *= f0, o[n][t][1] *= f1;
+                o[n][t][2] *= f0, o[n][t][3] *= f1;
+              }
             }
+            M0[n] = to0, M1[n] = to1;
           }
-          M0 = to0, M1 = to1;
         }
         // ---- weights, and 16 keys at a time their product with V
-        const f2 minus = pack(-M0, -M1);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
+          uint32_t ph[NR][2], pl[NR][2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
-                __half22float2(*reinterpret_cast<const __half2*>(blk + B::vz + (32 * warp + 16 * t + 8 * h + g) * 4));
-            f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
-            const float2 v = unpack(fma2(scale2, x[t][h], minus));
-            float2 pr = make_float2(ex2(v.x), ex2(v.y));
-            if (!whole) {  // a hidden key's numbers may be anything
-              const int key = key0 + 16 * t + 8 * h + g;
-              const bool no0 = key > hi0 || key < lo0, no1 = key > hi1 || key < lo1;
-              if (no0) pr.x = 0.0f;
-              if (no1) pr.y = 0.0f;
-              d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
-              z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
+                __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
+              const float2 v = unpack(fma2(scale2[n], x[n][t][h], pack(-M0[n], -M1[n])));
+              float2 pr = make_float2(ex2(v.x), ex2(v.y));
+              if (!whole) {  // a hidden key's numbers may be anything
+                const int key = key0 + 16 * t + 8 * h + g;
+                const bool no0 = hidden(key, hi0[n]), no1 = hidden(key, hi1[n]);
+                if (no0) pr.x = 0.0f;
+                if (no1) pr.y = 0.0f;
+                d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
+                z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
+              }
+              const f2 pp = pack(pr.x, pr.y);
+              lsum[n] = add2(lsum[n], pp);
+              zsum[n] = fma2(pp, z, zsum[n]);
+              split(mul2(pp, d), ph[n][h], pl[n][h]);
+              ph[n][h] = transpose8(ph[n][h]);
+              pl[n][h] = transpose8(pl[n][h]);
             }
-            const f2 pp = pack(pr.x, pr.y);
-            lsum = add2(lsum, pp);
-            zsum = fma2(pp, z, zsum);
-            split(mul2(pp, d), ph[h], pl[h]);
-            ph[h] = transpose8(ph[h]);
-            pl[h] = transpose8(pl[h]);
           }
           uint32_t v0[W], v1[W];
-          const uint8_t* vp = blk + B::v + (16 * warp + 8 * t + c) * D + g * (D / 8);
+          const uint8_t* vp = blk + (16 * warp + 8 * t + c) * D + g * (D / 8);
           if constexpr (D == 128) {
             const uint4 u0 = *reinterpret_cast<const uint4*>(vp), u1 = *reinterpret_cast<const uint4*>(vp + 4 * D);
             v0[0] = u0.x, v0[1] = u0.y, v0[2] = u0.z, v0[3] = u0.w;
@@ -495,82 +560,113 @@ __global__ void __launch_bounds__(kThreads, 3) attention_q4_kernel(
             q4_unpack(v0[w], h0);
             q4_unpack(v1[w], h1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]), ph[0], ph[1]);
+            for (int n = 0; n < NR; ++n) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]), pl[0], pl[1]);
+              for (int i = 0; i < 2; ++i)
+                mma(o[n][2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                    ph[n][0], ph[n][1]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                mma(o[n][2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                    pl[n][0], pl[n][1]);
+            }
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      release();
       if (tid == 0 && more) ask();
     }
 
-    // ---- the unit's end: join the four warps' rows
+    // ---- the unit's end: warps 2 and 3 hand their rows to 0 and 1, then 1 to 0;
+    // a thread's rows and dimensions are the same in every warp
 #pragma unroll
-    for (int s4 = 4; s4 < 32; s4 <<= 1) {
-      const float2 l = unpack(lsum), z = unpack(zsum);
-      lsum = add2(lsum, pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
-      zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
-    }
-    const float2 l2 = unpack(lsum), z2 = unpack(zsum);
-    if (g == 0) {
-      *reinterpret_cast<float2*>(stat + warp * kQ4Rows + 2 * c) = make_float2(M0, M1);
-      *reinterpret_cast<float2*>(stat + (kWarps + warp) * kQ4Rows + 2 * c) = l2;
-    }
-    {
-      // this thread's dimensions D/8 g .. of rows 2c and 2c + 1, in 16-byte pieces;
-      // neighbouring g's swap theirs, so that 8 threads hit different banks
-      float* dst = join + (warp * kQ4Rows + 2 * c) * S::rows + g * (D / 8);
+    for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int i = 0; i < NT / 2; ++i) {
-        float* at = dst + 4 * (i ^ (g & 1));
-        *reinterpret_cast<float4*>(at) = make_float4(o[2 * i][0] + z2.x, o[2 * i][2] + z2.x, o[2 * i + 1][0] + z2.x,
-                                                     o[2 * i + 1][2] + z2.x);
-        *reinterpret_cast<float4*>(at + S::rows) = make_float4(o[2 * i][1] + z2.y, o[2 * i][3] + z2.y,
-                                                               o[2 * i + 1][1] + z2.y, o[2 * i + 1][3] + z2.y);
+      for (int s4 = 4; s4 < 32; s4 <<= 1) {
+        const float2 l = unpack(lsum[n]), z = unpack(zsum[n]);
+        lsum[n] = add2(lsum[n], pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
+        zsum[n] = add2(zsum[n], pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
+      }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const float2 z = unpack(zsum[n]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        o[n][t][0] += z.x, o[n][t][1] += z.y;
+        o[n][t][2] += z.x, o[n][t][3] += z.y;
       }
     }
-    __syncthreads();
-    {
-      const int dim = tid % D, gg = dim / (D / 8), in = dim % (D / 8);
-      const int place = gg * (D / 8) + 4 * ((in >> 2) ^ (gg & 1)) + (in & 3);
-      const int rows = min(kQ4Rows, R - cur.rt * kQ4Rows);
-      int i = tid / D, r = cur.rt * kQ4Rows + i, j = r / G, gi = r - j * G;
-      for (; i < rows; i += kThreads / D) {
-        float top = stat[i];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, stat[w * kQ4Rows + i]);
-        float l = 0.0f, acc = 0.0f;
+    for (int from = 2; from > 0; from >>= 1) {
+      if (warp >= from && warp < 2 * from) {
+        float4* dst = join + (warp - from) * (NR * NT * 32) + lane;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = stat[w * kQ4Rows + i];
-          // a warp whose keys were all NaN has no maximum but a NaN sum
-          const float f = mw == -INFINITY ? (top == -INFINITY ? 1.0f : 0.0f) : ex2(mw - top);
-          const float lw = stat[(kWarps + w) * kQ4Rows + i];
-          l = __fmaf_rn(f, lw, l);
-          acc = __fmaf_rn(f, join[(w * kQ4Rows + i) * S::rows + place], acc);
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) dst[(n * NT + t) * 32] = make_float4(o[n][t][0], o[n][t][1], o[n][t][2], o[n][t][3]);
+          const float2 l = unpack(lsum[n]);
+          if (g == 0) stat[((warp - from) * NR + n) * 4 + c] = make_float4(M0[n], M1[n], l.x, l.y);
         }
-        const size_t row = (size_t)(sq.tok0 + j) * hq + cur.h * G + gi;
-        gi += kThreads / D;
-        while (gi >= G) gi -= G, ++j;
-        if (cur.units == 1) {
-          out[row * D + dim] = __fdiv_rn(acc, l);
-        } else {
-          float* dst = partials + (row * max_units + cur.u) * (D + 2);
-          dst[2 + dim] = acc;
-          if (dim == 0) {
-            dst[0] = top;
-            dst[1] = l;
+      }
+      __syncthreads();
+      if (warp < from) {
+        const float4* src = join + warp * (NR * NT * 32) + lane;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const float4 b = stat[(warp * NR + n) * 4 + c];
+          const float2 l = unpack(lsum[n]);
+          const float t0 = fmaxf(M0[n], b.x), t1 = fmaxf(M1[n], b.y);
+          // no maximum: nothing was seen, or only NaN scores, which the sums carry
+          const float a0 = M0[n] == t0 ? 1.0f : ex2(M0[n] - t0), a1 = M1[n] == t1 ? 1.0f : ex2(M1[n] - t1);
+          const float b0 = b.x == t0 ? 1.0f : ex2(b.x - t0), b1 = b.y == t1 ? 1.0f : ex2(b.y - t1);
+          M0[n] = t0, M1[n] = t1;
+          lsum[n] = pack(__fmaf_rn(b0, b.z, a0 * l.x), __fmaf_rn(b1, b.w, a1 * l.y));
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float4 v = src[(n * NT + t) * 32];
+            o[n][t][0] = __fmaf_rn(b0, v.x, a0 * o[n][t][0]);
+            o[n][t][1] = __fmaf_rn(b1, v.y, a1 * o[n][t][1]);
+            o[n][t][2] = __fmaf_rn(b0, v.z, a0 * o[n][t][2]);
+            o[n][t][3] = __fmaf_rn(b1, v.w, a1 * o[n][t][3]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float2 l = unpack(lsum[n]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = row0 + 8 * n + 2 * c + e;
+          if (r >= R) continue;
+          const int j = r / G;
+          const size_t row = (size_t)(cur->q.tok0 + j) * hq + cur->h * G + r - j * G;
+          const float le = e ? l.y : l.x;
+          if (cur->units == 1) {
+            float4* dst = reinterpret_cast<float4*>(out + row * D + g * (D / 8));
+#pragma unroll
+            for (int t = 0; t < NT; t += 2)
+              dst[t / 2] = make_float4(__fdiv_rn(o[n][t][e], le), __fdiv_rn(o[n][t][2 + e], le),
+                                       __fdiv_rn(o[n][t + 1][e], le), __fdiv_rn(o[n][t + 1][2 + e], le));
+          } else {
+            float* at = partials + (row * max_units + cur->u) * (D + 2);
+            float2* dst = reinterpret_cast<float2*>(at + 2 + g * (D / 8));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) dst[t] = make_float2(o[n][t][e], o[n][t][2 + e]);
+            if (g == 0) *reinterpret_cast<float2*>(at) = make_float2(e ? M1[n] : M0[n], le);
           }
         }
       }
     }
-    if (cur.end() >= w1) break;
-    cur.next(meta, hkv, G);
+    __syncwarp();
+    if (tid == 0) {
+      *done = cur->end() >= w1;
+      if (!*done) cur->next<NR>(meta, hkv, G);
+    }
     __syncthreads();
+    if (*done) break;
   }
 }
 
@@ -593,31 +689,61 @@ __global__ void __launch_bounds__(D) attention_q4_merge_kernel(const float* __re
   }
   const int32_t* p = meta + lo * kQ4SeqWords;
   const int pages = ((p[3] - 1) >> 7) - p[5] + 1, units = (pages + p[7] - 1) / p[7];
+  const bool listed = t >= p[1] && t < p[1] + p[2];  // the launch may be for some of the sequences
   pdl_wait();
   pdl_trigger();
-  if (units == 1) return;
+  if (units == 1 || !listed) return;
   const size_t row = (size_t)t * hq + head;
   const float* base = partials + row * max_units * (D + 2);
-  float M = -INFINITY;
-  for (int u = lane; u < units; u += 32) M = fmaxf(M, __ldcg(base + (size_t)u * (D + 2)));
+  // 32 units at a time: their maxima and sums in the lanes, their rows all on the
+  // way before the first is used
+  constexpr int kBatch = 16;
+  float M = -INFINITY, m0 = -INFINITY, l0 = 0.0f, v[kBatch];
+  if (lane < units) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + (size_t)lane * (D + 2)));
+    m0 = ml.x, l0 = ml.y;
+  }
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (i < units) v[i] = __ldcg(base + (size_t)i * (D + 2) + 2 + dim);
+  M = m0;
+  for (int u = lane + 32; u < units; u += 32) M = fmaxf(M, __ldcg(base + (size_t)u * (D + 2)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float l = 0.0f, acc = 0.0f;
-#pragma unroll 8
-  for (int u = 0; u < units; ++u) {
-    const float* b = base + (size_t)u * (D + 2);
-    const float mu = __ldcg(b), lu = __ldcg(b + 1), v = __ldcg(b + 2 + dim);
-    const float f = mu == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2(mu - M);
-    l = __fmaf_rn(f, lu, l);
-    acc = __fmaf_rn(f, v, acc);
+  for (int u0 = 0; u0 < units; u0 += 32) {
+    if (u0 > 0) {
+      m0 = -INFINITY, l0 = 0.0f;
+      if (u0 + lane < units) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + (size_t)(u0 + lane) * (D + 2)));
+        m0 = ml.x, l0 = ml.y;
+      }
+    }
+    const float f = m0 == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2(m0 - M);
+    l = __fmaf_rn(f, l0, l);
+    const int n = min(32, units - u0);
+    for (int b = 0; b < n; b += kBatch) {
+      if (u0 + b > 0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (b + i < n) v[i] = __ldcg(base + (size_t)(u0 + b + i) * (D + 2) + 2 + dim);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, (b + i) & 31);
+        if (b + i < n) acc = __fmaf_rn(w, v[i], acc);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, o));
   out[row * D + dim] = __fdiv_rn(acc, l);
 }
 
-template <int D, int N>
+template <int D, int NR, int N>
 cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  constexpr int smem = Q4Smem<D>::bytes;
-  auto kern = attention_q4_kernel<D, N>;
+  constexpr int smem = Q4Smem<D, NR>::bytes;
+  auto kern = attention_q4_kernel<D, NR, N>;
   int resident = 0;
   {
     static std::mutex mu;
@@ -653,13 +779,19 @@ cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t 
   return e;
 }
 
+template <int D>
+cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
+  if (a.row_tiles == 1) return meta.dev ? attention_go<D, 1, 1>(a, meta, st) : attention_go<D, 1, kParamWords>(a, meta, st);
+  return meta.dev ? attention_go<D, 2, 1>(a, meta, st) : attention_go<D, 2, kParamWords>(a, meta, st);
+}
+
 }  // namespace
 
 // Long units cost less joining, short ones fill the GPU with few sequences: the
 // sequence alone makes up to kAlone items (heads and row tiles included), of two
 // pages at least where it has many.
 int q4_unit_pages(int n, int lanes) {
-  constexpr long long kAlone = 512;
+  constexpr long long kAlone = 2048;
   if (n <= 2) return n;
   const int least = n <= 16 ? 1 : 2;
   const long long u = ((long long)n * lanes + kAlone - 1) / kAlone;
@@ -668,8 +800,8 @@ int q4_unit_pages(int n, int lanes) {
 
 cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st) {
   if (a.items == 0) return cudaSuccess;
-  if (head_dim == 128) return meta.dev ? attention_go<128, 1>(a, meta, st) : attention_go<128, kParamWords>(a, meta, st);
-  if (head_dim == 64) return meta.dev ? attention_go<64, 1>(a, meta, st) : attention_go<64, kParamWords>(a, meta, st);
+  if (head_dim == 128) return attention_pick<128>(a, meta, st);
+  if (head_dim == 64) return attention_pick<64>(a, meta, st);
   return cudaErrorInvalidValue;
 }
 

@@ -251,13 +251,15 @@ cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, c
 
 // One sequence of a 4-bit attention call, in its metadata; n_seq of them, then
 // the pages of work in all, then the visited pages of all sequences.  A
-// sequence's work items are (kv head, tile of 8 query rows, unit of u_pages
+// sequence's work items are (kv head, tile of 8 row_tiles query rows, unit of u_pages
 // pages); work_off: pages of work of the sequences before it.
 struct Q4Seq {
   int32_t work_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
 };
 constexpr int kQ4SeqWords = 8;
-constexpr int kQ4Rows = 8;  // query rows of an item
+// Tiles of 8 query rows in an item of a sequence with `rows` of them on a kv
+// head: a rule on the sequence alone, as the one on its units.
+inline int q4_row_tiles(long long rows) { return rows < 0 ? 2 : 1; }
 // Pages per unit of a sequence that visits n of them, with `lanes` pairs of a kv
 // head and a tile of rows: a rule on the sequence alone, not on the batch.
 int q4_unit_pages(int n, int lanes);
@@ -267,6 +269,7 @@ struct Q4AttnArgs {
   int hq, hkv;
   const void* pool;
   int n_seq, n_tok;
+  int row_tiles;    // of every listed sequence
   long long items;
   int max_units;    // units of the sequence with the most of them
   float* partials;  // [n_tok][hq][max_units][head_dim + 2]

@@ -374,68 +374,79 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     auto pages = [&](int s) { return b->new_tokens[s] == 0 ? 0 : (b->seq_lens[s] - 1) / DSB_KV_PAGE - chunk0(s) + 1; };
     std::vector<Group> groups;
     if ((st = cut_groups(b->n_seq, 1, dsbk::kQ4SeqWords, pages, &groups)) != DSB_OK) return st;
+    // One launch for each group and number of row tiles: that, like the units,
+    // depends on a sequence's own rows, not on its neighbours.
     struct Plan {
-      int live = 0, max_units = 1;
+      std::vector<int32_t> words;
+      int live = 0, max_units = 1, tok0 = 0, n_tok = 0, row_tiles = 1;
       long long items = 0, work = 0;
     };
-    std::vector<Plan> plans(groups.size());
+    std::vector<Plan> plans;
     int tok0 = 0;
     size_t most = 0, need = 0;
-    for (size_t gi = 0; gi < groups.size(); ++gi) {
-      Group& g = groups[gi];
-      Plan& p = plans[gi];
-      std::vector<int32_t> list;
-      g.tok0 = tok0;
-      for (int s = g.s0; s < g.s1; ++s) p.live += b->new_tokens[s] > 0;
-      for (int s = g.s0; s < g.s1; ++s) {
-        const int n = b->new_tokens[s];
-        if (n == 0) continue;
-        const int np = pages(s), tiles = (int)(((long long)G * n + dsbk::kQ4Rows - 1) / dsbk::kQ4Rows);
-        const int u = dsbk::q4_unit_pages(np, kv->n_kv_heads * tiles), units = (np + u - 1) / u;
-        const int32_t rec[dsbk::kQ4SeqWords] = {(int32_t)p.work,
-                                                g.n_tok,
-                                                n,
-                                                b->seq_lens[s],
-                                                b->window[s],
-                                                chunk0(s),
-                                                (int32_t)((size_t)p.live * dsbk::kQ4SeqWords + 1 + list.size()),
-                                                u};
-        g.words.insert(g.words.end(), rec, rec + dsbk::kQ4SeqWords);
-        for (int i = 0; i < np; ++i) list.push_back(page_of(b, s, chunk0(s) + i));
-        p.items += (long long)kv->n_kv_heads * tiles * units;
-        p.work += (long long)kv->n_kv_heads * tiles * np;
-        p.max_units = std::max(p.max_units, units);
-        g.n_tok += n;
-        if (p.work > INT_MAX) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+    for (const Group& g : groups) {
+      int tok1 = tok0;
+      for (int tiles_of = 1; tiles_of <= 2; ++tiles_of) {
+        Plan p;
+        std::vector<int32_t> list;
+        p.tok0 = tok0;
+        p.row_tiles = tiles_of;
+        auto mine = [&](int s) {
+          return b->new_tokens[s] > 0 && dsbk::q4_row_tiles((long long)G * b->new_tokens[s]) == tiles_of;
+        };
+        for (int s = g.s0; s < g.s1; ++s) p.live += mine(s);
+        int tok = 0;
+        for (int s = g.s0; s < g.s1; tok += b->new_tokens[s], ++s) {
+          if (!mine(s)) continue;
+          const int n = b->new_tokens[s], np = pages(s), rows = 8 * tiles_of;
+          const int tiles = (int)(((long long)G * n + rows - 1) / rows);
+          const int u = dsbk::q4_unit_pages(np, kv->n_kv_heads * tiles), units = (np + u - 1) / u;
+          const int32_t rec[dsbk::kQ4SeqWords] = {(int32_t)p.work,
+                                                  tok,
+                                                  n,
+                                                  b->seq_lens[s],
+                                                  b->window[s],
+                                                  chunk0(s),
+                                                  (int32_t)((size_t)p.live * dsbk::kQ4SeqWords + 1 + list.size()),
+                                                  u};
+          p.words.insert(p.words.end(), rec, rec + dsbk::kQ4SeqWords);
+          for (int i = 0; i < np; ++i) list.push_back(page_of(b, s, chunk0(s) + i));
+          p.items += (long long)kv->n_kv_heads * tiles * units;
+          p.work += (long long)kv->n_kv_heads * tiles * np;
+          p.max_units = std::max(p.max_units, units);
+          p.n_tok = tok + n;
+          if (p.work > INT_MAX) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+        }
+        tok1 = tok0 + tok;
+        if (p.live == 0) continue;
+        p.words.push_back((int32_t)p.work);
+        p.words.insert(p.words.end(), list.begin(), list.end());
+        most = std::max(most, p.words.size());
+        if (p.max_units > 1) need = std::max(need, (size_t)p.n_tok * n_q_heads * p.max_units * (D + 2) * sizeof(float));
+        plans.push_back(std::move(p));
       }
-      tok0 += g.n_tok;
-      g.words.push_back((int32_t)p.work);
-      g.words.insert(g.words.end(), list.begin(), list.end());
-      most = std::max(most, g.words.size());
-      if (p.max_units > 1)
-        need = std::max(need, (size_t)g.n_tok * n_q_heads * p.max_units * (D + 2) * sizeof(float));
+      tok0 = tok1;
     }
     if (need > partial_capacity(ws))
       return fail(DSB_ERR_WORKSPACE, "attention needs %zu workspace bytes for partials, have %zu", need, partial_capacity(ws));
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     if ((st = check_capture(most, cs)) != DSB_OK) return st;
-    for (size_t gi = 0; gi < groups.size(); ++gi) {
-      const Group& g = groups[gi];
-      if (g.n_tok == 0) continue;
+    for (const Plan& p : plans) {
       dsbk::MetaArg meta;
-      if ((st = meta_arg(ws, g.words, cs, &meta)) != DSB_OK) return st;
-      const dsbk::Q4AttnArgs a{q + (size_t)g.tok0 * q_stride,
+      if ((st = meta_arg(ws, p.words, cs, &meta)) != DSB_OK) return st;
+      const dsbk::Q4AttnArgs a{q + (size_t)p.tok0 * q_stride,
                                q_stride,
                                n_q_heads,
                                kv->n_kv_heads,
                                kv->blocks,
-                               plans[gi].live,
-                               g.n_tok,
-                               plans[gi].items,
-                               plans[gi].max_units,
+                               p.live,
+                               p.n_tok,
+                               p.row_tiles,
+                               p.items,
+                               p.max_units,
                                reinterpret_cast<float*>(partial_base(ws)),
-                               out + (size_t)g.tok0 * n_q_heads * D};
+                               out + (size_t)p.tok0 * n_q_heads * D};
       const cudaError_t e = dsbk::launch_attention_q4(a, D, meta, cs);
       if (e != cudaSuccess) return cuda_fail(e, "attention_decode_q4 launch");
     }
