@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -183,9 +184,50 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
 
 constexpr int kAppThreads = 256;
 
-__device__ __forceinline__ float lanes_max(float v, int width) {
-  for (int o = width >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+// Two float32 products or sums at once, each rounded as by itself.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Largest of a and b; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Over the D/4 lanes that hold a head.
+template <int D>
+__device__ __forceinline__ float head_max_nan(float v) {
+  if constexpr (D == 128) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  } else {
+#pragma unroll
+    for (int o = D / 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  }
+}
+// Whether any head of the warp is concerned; a warp holds one head at D = 128.
+template <int D>
+__device__ __forceinline__ bool warp_any(bool x) {
+  return D == 128 ? x : __any_sync(0xFFFFFFFFu, x);
 }
 
 template <typename T>
@@ -210,8 +252,8 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
 template <int D>
 __device__ __forceinline__ float sum_squares(const float (&y)[4], int lane) {
   float v[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(y[e], y[e]);
+  unpack2(mul2(pack2(y[0], y[1]), pack2(y[0], y[1])), v[0], v[1]);
+  unpack2(mul2(pack2(y[2], y[3]), pack2(y[2], y[3])), v[2], v[3]);
   float ss;
   if constexpr (D == 128) {
     const bool up = lane & 16, odd = lane & 8;
@@ -247,15 +289,19 @@ __device__ __forceinline__ float sum_squares(const float (&y)[4], int lane) {
 // How the cache rows are stored.
 struct StoreQ4 {};
 
-// grid (n_tok, groups of heads), 256 threads: D/4 lanes hold one head's vector,
+// grid (n_tok, shares of the heads), 256 threads: D/4 lanes hold one head's vector,
 // four values each, so that its norm, its extremes and the partner of a rotated
-// value stay inside a warp.  A lane handles the same four dimensions of HPS
-// heads, all loaded before the first is used, with one set of sines and cosines.
-// Head h of the row: query heads, then key heads, then value heads.
+// value stay inside a warp.  A lane handles the same four dimensions of one head
+// after the other, HPS of them loaded before the first is used, with one set of
+// sines and cosines.  Head h of the row: query heads, then key heads, then value
+// heads.  With many tokens one CTA takes all heads of its token: the kernel is
+// bound by instruction issue (a prompt of 5178 tokens of 56 heads: 254 MB, 78 us
+// and 253 instructions a head before, see the launch for the time now), so the
+// token's set-up is paid once.
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
 template <int D, typename Store, int HPS, int N>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restrict__ qkv, long long stride, int hq,
+__global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __restrict__ qkv, long long stride, int hq,
                                                                 int hkv, uint8_t* __restrict__ kc,
                                                                 uint8_t* __restrict__ vc,
                                                                 const __grid_constant__ Turns<64> tab,
@@ -270,17 +316,18 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
   pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x, l = tid & (LPH - 1), slot = tid / LPH;
   const int heads = hq + 2 * hkv, rd = tab.rd, half = rd >> 1;
-  float* row = qkv + (size_t)t * stride;
+  const bool touched = q_norm || 4 * l < rd;  // query values past the rotated part stay where they are
+  float* row = qkv + (size_t)t * stride + 4 * l;
   float4 x[HPS];
-  const int h0 = blockIdx.y * (HPS * SLOTS) + slot;
+  auto fetch = [&](int h0) {
 #pragma unroll
-  for (int u = 0; u < HPS; ++u) {
-    const int h = h0 + u * SLOTS;
-    x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    // query values past the rotated part stay where they are
-    if (h < heads && (h >= hq || q_norm || 4 * l < rd))
-      x[u] = __ldcg(reinterpret_cast<const float4*>(row + (size_t)h * D) + l);
-  }
+    for (int u = 0; u < HPS; ++u) {
+      const int h = h0 + u * SLOTS;
+      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (h < heads && (h >= hq || touched)) x[u] = __ldcg(reinterpret_cast<const float4*>(row + h * D));
+    }
+  };
+  fetch(blockIdx.y * (HPS * SLOTS) + slot);
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   int lo = 0, hi = n_seq - 1;  // the sequence of token t
   while (lo < hi) {
@@ -297,6 +344,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
   if (tid < half) cs[tid] = turn_cs(tab.f[tid], pos, tab.gain, tab.gain_lo);
   __syncthreads();
   float c[4], s[4];  // of this lane's four dimensions; s with the sign its term takes
+  bool turned[4];
   int partner[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -304,7 +352,8 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
     c[e] = 1.0f;
     s[e] = 0.0f;
     partner[e] = dim;
-    if (dim < rd) {
+    turned[e] = dim < rd;
+    if (turned[e]) {
       const bool second = tab.interleaved ? (dim & 1) : dim >= half;
       const float2 v = cs[tab.interleaved ? dim >> 1 : second ? dim - half : dim];
       c[e] = v.x;
@@ -312,84 +361,107 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(float* __restric
       partner[e] = tab.interleaved ? dim ^ 1 : second ? dim - half : dim + half;
     }
   }
+  const int src = (tid & 31 & ~(LPH - 1)) + (partner[0] >> 2);  // lane of the partners, half layout in whole lanes
+  const bool lanes = (rd & 7) == 0, all = rd == D;
+  const float4 qw = q_norm ? __ldg(reinterpret_cast<const float4*>(q_norm) + l) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 kw = k_norm ? __ldg(reinterpret_cast<const float4*>(k_norm) + l) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int h0 = blockIdx.y * (HPS * SLOTS) + slot;; ) {
 #pragma unroll
-  for (int u = 0; u < HPS; ++u) {
-    const int h = h0 + u * SLOTS;
-    const bool live = h < heads, is_q = h < hq, is_k = !is_q && h < hq + hkv;
-    float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    const float* w = !live ? nullptr : is_q ? q_norm : is_k ? k_norm : nullptr;
-    if (__any_sync(0xFFFFFFFFu, w != nullptr)) {
-      const float ss = sum_squares<D>(y, tid & 31);
-      if (w) {
-        const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
-        const float4 wv = __ldg(reinterpret_cast<const float4*>(w) + l);
-        y[0] = __fmul_rn(__fmul_rn(y[0], inv), wv.x);
-        y[1] = __fmul_rn(__fmul_rn(y[1], inv), wv.y);
-        y[2] = __fmul_rn(__fmul_rn(y[2], inv), wv.z);
-        y[3] = __fmul_rn(__fmul_rn(y[3], inv), wv.w);
+    for (int u = 0; u < HPS; ++u) {
+      const int h = h0 + u * SLOTS;
+      if (D == 128 && h >= heads) break;
+      const bool live = h < heads, is_q = h < hq, is_k = !is_q && h < hq + hkv, is_v = live && !is_q && !is_k;
+      float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      const bool normed = (is_q && q_norm) || (is_k && k_norm);
+      if (warp_any<D>(normed)) {
+        const float ss = sum_squares<D>(y, tid & 31);
+        if (normed) {
+          const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
+          const float4 wv = is_q ? qw : kw;
+          const f2 inv2 = pack2(inv, inv);
+          unpack2(mul2(mul2(pack2(y[0], y[1]), inv2), pack2(wv.x, wv.y)), y[0], y[1]);
+          unpack2(mul2(mul2(pack2(y[2], y[3]), inv2), pack2(wv.z, wv.w)), y[2], y[3]);
+        }
       }
-    }
-    if (__any_sync(0xFFFFFFFFu, live && (is_q || is_k))) {
-      float p[4];
-      if (tab.interleaved) {
-        p[0] = y[1], p[1] = y[0], p[2] = y[3], p[3] = y[2];
-      } else if ((rd & 7) == 0) {  // the partners are another lane's four values
-        const int src = (tid & 31 & ~(LPH - 1)) + (partner[0] >> 2);
+      if (warp_any<D>(live && !is_v)) {
+        float p[4];
+        if (tab.interleaved) {
+          p[0] = y[1], p[1] = y[0], p[2] = y[3], p[3] = y[2];
+        } else if (lanes) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], src);
+          for (int e = 0; e < 4; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], src);
+        } else {
+          float* mine = swap + slot * D;
+          __syncwarp();
+          *reinterpret_cast<float4*>(mine + 4 * l) = make_float4(y[0], y[1], y[2], y[3]);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = mine[partner[e]];
+        }
+        if (!is_v) {
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float z0, z1;
+            unpack2(add2(mul2(pack2(y[e], y[e + 1]), pack2(c[e], c[e + 1])),
+                         mul2(pack2(p[e], p[e + 1]), pack2(s[e], s[e + 1]))),
+                    z0, z1);
+            y[e] = all || turned[e] ? z0 : y[e];
+            y[e + 1] = all || turned[e + 1] ? z1 : y[e + 1];
+          }
+        }
+      }
+      if (is_q && touched) *reinterpret_cast<float4*>(row + h * D) = make_float4(y[0], y[1], y[2], y[3]);
+      const int g = h - hq - (is_k ? 0 : hkv);  // kv head
+      if constexpr (std::is_same<Store, StoreQ4>::value) {
+        if (!warp_any<D>(live && !is_q)) continue;
+        const float most = head_max_nan<D>(max_nan(max_nan(y[0], y[1]), max_nan(y[2], y[3])));
+        const float least = -head_max_nan<D>(max_nan(max_nan(-y[0], -y[1]), max_nan(-y[2], -y[3])));
+        const float span = __fsub_rn(most, least);
+        __half dh = __float2half_rn(__fmul_rn(span, 1.0f / 15.0f));
+        __half zh = __float2half_rn(__fadd_rn(least, __fmul_rn(8.0f, __half2float(dh))));
+        if (!(span <= FLT_MAX)) {  // a vector with a NaN or an infinity is stored as NaN
+          dh = __ushort_as_half(0);
+          zh = __ushort_as_half(0x7FFF);
+        }
+        const float d = __half2float(dh), z = __half2float(zh);
+        // The quotient by the reciprocal, at most 8, is within 2^-20 of the rounded
+        // quotient; only where it lies closer than that to a half does the code
+        // need the division itself.
+        const float inv = __frcp_rn(d);
+        uint32_t code = 0;
+        bool near = false;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = __fmul_rn(__fsub_rn(y[e], z), inv);
+          const float n = rintf(v[e]);
+          near |= !(fabsf(fabsf(v[e] - n) - 0.5f) > 0x1p-18f);
+          v[e] = n;
+        }
+        if (near) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = rintf(__fdiv_rn(__fsub_rn(y[e], z), d));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) code |= (uint32_t)(int)fminf(fmaxf(v[e] + 8.0f, 0.0f), 15.0f) << (4 * e);
+        if (d == 0.0f) code = 0x8888u;
+        if (live && !is_q) {
+          using B = Q4Block<D>;
+          uint8_t* blk = kc + ((size_t)page * hkv + g) * B::bytes;
+          uint8_t* dst = is_k ? blk + r * (D / 2) + 2 * l : blk + B::v + (r >> 1) * D + 4 * l + 2 * (r & 1);
+          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+          if (l == 0) *reinterpret_cast<__half2*>(blk + (is_k ? B::kz : B::vz) + 4 * r) = __halves2half2(dh, zh);
+        }
       } else {
-        float* mine = swap + slot * D;
-        __syncwarp();
-        *reinterpret_cast<float4*>(mine + 4 * l) = make_float4(y[0], y[1], y[2], y[3]);
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = mine[partner[e]];
-      }
-      if (is_q || is_k) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (4 * l + e < rd) y[e] = __fadd_rn(__fmul_rn(y[e], c[e]), __fmul_rn(p[e], s[e]));
+        if (live && !is_q) {
+          uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + 4 * l) * 2;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]));
+        }
       }
     }
-    if (live && is_q && (q_norm || 4 * l < rd))
-      *(reinterpret_cast<float4*>(row + (size_t)h * D) + l) = make_float4(y[0], y[1], y[2], y[3]);
-    const int g = h - hq - (is_k ? 0 : hkv);  // kv head
-    if constexpr (std::is_same<Store, StoreQ4>::value) {
-      if (!__any_sync(0xFFFFFFFFu, live && !is_q)) continue;
-      float least = fminf(fminf(y[0], y[1]), fminf(y[2], y[3])), most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-      most = lanes_max(most, LPH);
-      least = -lanes_max(-least, LPH);
-      const bool odd = !(fabsf(y[0]) <= FLT_MAX) || !(fabsf(y[1]) <= FLT_MAX) || !(fabsf(y[2]) <= FLT_MAX) ||
-                       !(fabsf(y[3]) <= FLT_MAX);
-      const uint32_t seen = __ballot_sync(0xFFFFFFFFu, odd);
-      const uint32_t group = LPH == 32 ? 0xFFFFFFFFu : 0xFFFFu << (tid & 16);
-      __half dh = __float2half_rn(__fmul_rn(__fsub_rn(most, least), 1.0f / 15.0f));
-      __half zh = __float2half_rn(__fadd_rn(least, __fmul_rn(8.0f, __half2float(dh))));
-      if (seen & group) {  // a vector with a NaN or an infinity is stored as NaN
-        dh = __ushort_as_half(0);
-        zh = __ushort_as_half(0x7FFF);
-      }
-      const float d = __half2float(dh), z = __half2float(zh);
-      uint32_t code = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = rintf(__fdiv_rn(__fsub_rn(y[e], z), d)) + 8.0f;
-        const int n = d == 0.0f ? 8 : (int)fminf(fmaxf(v, 0.0f), 15.0f);
-        code |= (uint32_t)n << (4 * e);
-      }
-      if (live && !is_q) {
-        using B = Q4Block<D>;
-        uint8_t* blk = kc + ((size_t)page * hkv + g) * B::bytes;
-        uint8_t* dst = is_k ? blk + r * (D / 2) + 2 * l : blk + B::v + (r >> 1) * D + 4 * l + 2 * (r & 1);
-        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
-        if (l == 0) *reinterpret_cast<__half2*>(blk + (is_k ? B::kz : B::vz) + 4 * r) = __halves2half2(dh, zh);
-      }
-    } else {
-      if (live && !is_q) {
-        uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + 4 * l) * 2;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]));
-      }
-    }
+    h0 += gridDim.y * (HPS * SLOTS);
+    if (h0 - slot >= heads) break;
+    fetch(h0);
   }
 }
 
@@ -438,8 +510,11 @@ cudaError_t append_go(const AppendArgs& a, const RotaryTable& rot, const MetaArg
   fill_turns(rot, &tab);
   ParamWords<N> w;
   fill_words(meta, &w);
-  const int slots = kAppThreads / (D / 4) * HPS;
-  const dim3 grid((unsigned)a.n_tok, (unsigned)((a.hq + 2 * a.hkv + slots - 1) / slots));
+  // as many shares of a token's heads as fill the GPU (8 CTAs on each of some 150
+  // SMs), no more than there are
+  const int slots = kAppThreads / (D / 4) * HPS, most = (a.hq + 2 * a.hkv + slots - 1) / slots;
+  const int shares = std::min(most, std::max(1, 1200 / a.n_tok));
+  const dim3 grid((unsigned)a.n_tok, (unsigned)shares);
   return launch_kernel(kv_append_kernel<D, Store, HPS, N>, grid, dim3(kAppThreads), 0, st, a.qkv, a.stride, a.hq, a.hkv,
                        static_cast<uint8_t*>(a.kc), static_cast<uint8_t*>(a.vc), tab, a.q_norm, a.k_norm, a.eps, a.n_seq,
                        w, meta.dev);
