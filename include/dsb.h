@@ -424,7 +424,8 @@ dsb_status dsb_attention_decode_multi_noalloc(const float* q, int n_q_heads, con
  * Metadata of up to 960 words rides in the launch itself; such a call can be
  * captured into a CUDA graph, which then replays that metadata.  A longer one
  * is staged through the workspace and is DSB_ERR_UNSUPPORTED on a capturing
- * stream.  The words of a call: rope_rotary one a token; append 3 a sequence + 2
+ * stream.  The words of a call: rope_rotary one a
+ * token, or two for each run of consecutive positions; append 3 a sequence + 2
  * + the pages its new tokens touch; attention 8 a sequence + 1 + the pages it
  * visits; gather 5 a sequence + 1 + the pages it reads.  The workspace must
  * belong to the current device. */

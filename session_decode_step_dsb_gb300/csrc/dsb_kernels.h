@@ -229,9 +229,10 @@ struct RotaryTable {
 // freq: rd / 2 angles per position, in radians.
 void rotary_table(const double* freq, int rd, bool interleaved, double gain, RotaryTable* out);
 
-// Metadata: pos[n_tok].
+// Metadata: the first token of each of `runs` runs of consecutive positions, then
+// the runs' first positions; or, with runs = 0, pos[n_tok].
 cudaError_t launch_rope_rotary(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,
-                               int n_tok, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st);
+                               int n_tok, const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st);
 
 enum class KvStore { kF16, kBF16, kQ4 };
 struct AppendArgs {

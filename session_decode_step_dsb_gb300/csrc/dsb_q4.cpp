@@ -305,14 +305,27 @@ dsb_status dsb_rope_rotary(float* q, int64_t q_stride, int n_q_heads, float* k, 
       if (pos[t] < 0 || pos[t] >= kMaxPos) return fail(DSB_ERR_INVALID_ARG, "pos[%d]=%d out of [0, 2^24)", t, pos[t]);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if ((st = check_capture((size_t)n_tok, cs)) != DSB_OK) return st;
+    // runs of consecutive positions (a prompt is one), or the positions themselves
+    // where they are fewer words
+    std::vector<int32_t> words, first;
+    for (int t = 0; t < n_tok; ++t)
+      if (t == 0 || pos[t] != pos[t - 1] + 1) {
+        words.push_back(t);
+        first.push_back(pos[t]);
+      }
+    int runs = (int)first.size();
+    words.insert(words.end(), first.begin(), first.end());
+    if (words.size() > (size_t)n_tok) {
+      runs = 0;
+      words.assign(pos, pos + n_tok);
+    }
+    if ((st = check_capture(words.size(), cs)) != DSB_OK) return st;
     dsbk::RotaryTable rot;
     build_rotary(*rotary, head_dim, &rot);
-    const std::vector<int32_t> words(pos, pos + n_tok);
     dsbk::MetaArg meta;
     if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
     const cudaError_t e =
-        dsbk::launch_rope_rotary(q, q_stride, n_q_heads, k, k ? k_stride : 0, n_kv_heads, head_dim, n_tok, rot, meta, cs);
+        dsbk::launch_rope_rotary(q, q_stride, n_q_heads, k, k ? k_stride : 0, n_kv_heads, head_dim, n_tok, rot, runs, meta, cs);
     return e == cudaSuccess ? DSB_OK : cuda_fail(e, "rope_rotary launch");
   });
 }

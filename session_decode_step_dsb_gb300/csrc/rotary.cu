@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
                                                                   float* __restrict__ k, long long k_stride, int hkv,
                                                                   int head_dim,
                                                                   const __grid_constant__ Turns<NP> tab,
+                                                                  int runs,
                                                                   const __grid_constant__ ParamWords<N> words,
-                                                                  const int32_t* __restrict__ pos_dev) {
+                                                                  const int32_t* __restrict__ meta_dev) {
   __shared__ float2 cs[NP];
   pdl_wait();
   pdl_trigger();
@@ -154,7 +155,17 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
       }
     }
   }
-  const int pos = N > 1 ? words.w[t] : pos_dev[t];
+  // the run of consecutive positions that token t is in
+  const int32_t* meta = N > 1 ? words.w : meta_dev;
+  int lo = 0, hi = runs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (meta[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int pos = runs == 0 ? meta[t] : meta[runs + lo] + t - meta[lo];
   for (int i = threadIdx.x; i < half; i += kRotThreads) cs[i] = turn_cs(tab.f[i], pos, tab.gain, tab.gain_lo);
   __syncthreads();
 #pragma unroll
@@ -481,7 +492,7 @@ void fill_words(const MetaArg& m, ParamWords<N>* out) {
 
 template <int NP, bool VEC, int N>
 cudaError_t rope_go(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim, int n_tok,
-                    const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
+                    const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st) {
   Turns<NP> tab;
   fill_turns(rot, &tab);
   ParamWords<N> w;
@@ -490,18 +501,18 @@ cudaError_t rope_go(float* q, long long q_stride, int hq, float* k, long long k_
   const long long pieces = (long long)(hq + hkv) * per_head;
   const unsigned gy = (unsigned)((pieces + kRotThreads * kRotUnroll - 1) / (kRotThreads * kRotUnroll));
   return launch_kernel(rope_rotary_kernel<NP, VEC, N>, dim3((unsigned)n_tok, gy), dim3(kRotThreads), 0, st, q, q_stride,
-                       hq, k, k_stride, hkv, head_dim, tab, w, meta.dev);
+                       hq, k, k_stride, hkv, head_dim, tab, runs, w, meta.dev);
 }
 
 template <int NP, int N>
 cudaError_t rope_vec(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,
-                     int n_tok, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
+                     int n_tok, const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st) {
   // 16-byte pieces where every head starts on 16 bytes and the rotated part is
   // a whole number of pieces
   const bool vec = head_dim % 4 == 0 && q_stride % 4 == 0 && k_stride % 4 == 0 &&
                    rot.rd % (rot.interleaved ? 4 : 8) == 0;
-  return vec ? rope_go<NP, true, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta, st)
-             : rope_go<NP, false, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta, st);
+  return vec ? rope_go<NP, true, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
+             : rope_go<NP, false, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st);
 }
 
 template <int D, typename Store, int HPS, int N>
@@ -532,14 +543,14 @@ cudaError_t append_pick(const AppendArgs& a, const RotaryTable& rot, const MetaA
 }  // namespace
 
 cudaError_t launch_rope_rotary(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,
-                               int n_tok, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
+                               int n_tok, const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st) {
   if (n_tok == 0) return cudaSuccess;
   if (rot.rd <= 128)
-    return meta.dev ? rope_vec<64, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta, st)
-                    : rope_vec<64, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta, st);
-  return meta.dev ? rope_vec<kRopeMaxPairs, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta, st)
-                  : rope_vec<kRopeMaxPairs, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, meta,
-                                                         st);
+    return meta.dev ? rope_vec<64, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
+                    : rope_vec<64, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st);
+  return meta.dev ? rope_vec<kRopeMaxPairs, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
+                  : rope_vec<kRopeMaxPairs, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs,
+                                                         meta, st);
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, const RotaryTable& rot,

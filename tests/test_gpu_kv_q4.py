@@ -63,7 +63,7 @@ def test_rope_rotary(cuda_device, n, hq, hkv, D, rd, inter, scale, pos0):
     d = _dsb()
     rng = np.random.default_rng(n + rd)
     rows = rng.standard_normal((n, hq + 2 * hkv + 1, D)).astype(np.float32)      # parts of wider rows
-    pos = pos0 + np.arange(n)[::-1]
+    pos = pos0 + (np.arange(n)[::-1] if n % 2 else (np.arange(n) + n // 4) % n)   # backwards, or in two runs
     rot, f, gain = _rot(scale, rd, inter)
     t = to_dev(rows)
     q, k = t[:, :hq], t[:, hq:hq + hkv] if hkv else None
@@ -440,7 +440,7 @@ def test_captured_and_replayed(cuda_device):
             torch.cuda.synchronize()
             for a, b in zip((qkv, out, k, v, pool), want):
                 assert torch.equal(a, b)
-    # 1000 positions are staged: not in a graph
+    # 1000 positions apart are staged: not in a graph
     q = torch.zeros((1000, 2, D), device="cuda")
     big = d.Workspace(1000, 2, D, P)
     s = torch.cuda.Stream()
@@ -448,8 +448,8 @@ def test_captured_and_replayed(cuda_device):
     with torch.cuda.graph(g, stream=s):
         q.add_(0.0)
         with pytest.raises(d.DsbError, match="captured"):
-            d.rope_rotary(q, None, np.arange(1000), rot, big)
-    d.rope_rotary(q, None, np.arange(1000), rot, big)
+            d.rope_rotary(q, None, np.arange(0, 2000, 2), rot, big)
+    d.rope_rotary(q, None, np.arange(0, 2000, 2), rot, big)
     torch.cuda.synchronize()
 
 
