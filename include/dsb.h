@@ -421,7 +421,7 @@ dsb_status dsb_attention_decode_multi_noalloc(const float* q, int n_q_heads, con
  * back.  Batches are ragged: every sequence brings its own number of new tokens
  * (none, one, a draft, a prompt).  They are no restatement of the pages above.
  *
- * Metadata of up to 960 words rides in the launch itself; such a call can be
+ * Metadata of up to 4032 words rides in the launch itself; such a call can be
  * captured into a CUDA graph, which then replays that metadata.  A longer one
  * is staged through the workspace and is DSB_ERR_UNSUPPORTED on a capturing
  * stream.  The words of a call: rope_rotary one a

@@ -35,6 +35,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attention_q4.cuh"
 #include "dsb_kernels.h"
 #include "dsb_ptx.cuh"
 #include "dsb_q4.cuh"
@@ -47,17 +48,6 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 __device__ unsigned int g_err_attention_q4 = 0;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -82,173 +72,34 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// Two float32 at once.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-// x0, x1 as hi + lo fp16 pairs.
-__device__ __forceinline__ void split(f2 x, uint32_t& hi, uint32_t& lo) {
-  const float2 v = unpack(x);
-  const __half2 h = __floats2half2_rn(v.x, v.y);
-  const float2 f = __half22float2(h);
-  const float2 t = unpack(add2(x, pack(-f.x, -f.y)));
-  const __half2 r = __floats2half2_rn(t.x, t.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&r);
-}
-
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Where a CTA is in its list of items: one unit of one (sequence, kv head, row
-// tile), and the page inside it.  Divides once, at its start; then it counts.
-// Kept in shared memory by thread 0; the others read what they need of it.
-struct Cursor {
-  int fresh;  // another sequence, head or row tile than the item before
-  int at;  // pages of work before this item
-  int s, h, rt, u, units, tiles, pages, pg, pg_end;
-  Q4Seq q;
-
-  template <int NR>
-  __device__ __forceinline__ void load(const int32_t* meta, int G) {
-    const int32_t* p = meta + s * kQ4SeqWords;
-    q.work_off = p[0];
-    q.tok0 = p[1];
-    q.n_new = p[2];
-    q.len = p[3];
-    q.window = p[4];
-    q.chunk0 = p[5];
-    q.pg_at = p[6];
-    q.u_pages = p[7];
-    pages = ((q.len - 1) >> 7) - q.chunk0 + 1;
-    units = (pages + q.u_pages - 1) / q.u_pages;
-    tiles = (G * q.n_new + 8 * NR - 1) / (8 * NR);
-  }
-  __device__ __forceinline__ void place() {
-    pg = u * q.u_pages;
-    pg_end = min(pg + q.u_pages, pages);
-  }
-  // The first item that starts at or after `from` pages of work; false if none.
-  template <int NR>
-  __device__ __forceinline__ bool start(const int32_t* meta, int n_seq, int hkv, int G, int from) {
-    int lo = 0, hi = n_seq - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (meta[mid * kQ4SeqWords] <= from)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    s = lo;
-    load<NR>(meta, G);
-    const int rel = from - q.work_off;
-    int x = rel / pages;
-    u = (rel - x * pages + q.u_pages - 1) / q.u_pages;
-    if (u == units) u = 0, ++x;
-    h = x / tiles;
-    rt = x - h * tiles;
-    if (h == hkv) {
-      if (++s == n_seq) return false;
-      h = 0;
-      load<NR>(meta, G);
-    }
-    place();
-    at = q.work_off + (h * tiles + rt) * pages + pg;
-    fresh = 1;
-    return true;
-  }
-  // The next item (one that exists).
-  template <int NR>
-  __device__ __forceinline__ void next(const int32_t* meta, int hkv, int G) {
-    at += pg_end - u * q.u_pages;
-    fresh = 0;
-    if (++u == units) {
-      u = 0;
-      fresh = 1;
-      if (++rt == tiles) {
-        rt = 0;
-        if (++h == hkv) {
-          h = 0;
-          ++s;
-          load<NR>(meta, G);
-        }
-      }
-    }
-    place();
-  }
-  __device__ __forceinline__ int end() const { return at + pg_end - u * q.u_pages; }  // pages before the next item
-};
-
+constexpr int kRows = 8;   // query rows of an item
 constexpr int kSlots = 5;  // half pages (K or V) on their way or in use
 
-// NR: tiles of 8 query rows that a CTA works on together.
-template <int D, int NR>
+template <int D>
 struct Q4Smem {
   static constexpr int half = Q4Block<D>::v;                // K codes and numbers; V's are as many bytes
-  static constexpr int q = kSlots * half;                   // [D/16][NR][32 lanes] uint4: q as right operand
-  static constexpr int rows = q + D / 16 * NR * 512;        // [8 NR] float4: scale, sum, last key, -
-  static constexpr int join = rows + 8 * NR * 16;           // [2 warps][NR * D/16][32 lanes] float4
-  static constexpr int stat = join + 2 * NR * (D / 16) * 512;  // [2 warps][NR][4] float4: M, M, sum, sum
-  static constexpr int bars = stat + 2 * NR * 64;
+  static constexpr int q = kSlots * half;                   // [D/16][32 lanes] uint4: q as right operand
+  static constexpr int rows = q + D / 16 * 512;             // [8] float4: scale, sum, last key, -
+  static constexpr int join = rows + kRows * 16;            // [2 warps][D/16][32 lanes] float4
+  static constexpr int stat = join + 2 * (D / 16) * 512;    // [2 warps][4] float4: M, M, sum, sum
+  static constexpr int bars = stat + 2 * 64;
   static constexpr int cursors = bars + 2 * kSlots * 8;     // the item in work, the next to ask for, "done"
   static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
 };
 
-// One thread requests the K (which = 0) or V half of the page the cursor is at:
-// codes and numbers up to the sequence's last key (rounded up to four keys:
-// 16-byte pieces), or, where the page is full, the half in one piece.
-template <int D>
-__device__ __forceinline__ void request(const Cursor& c, int which, const int32_t* meta, const uint8_t* pool, int hkv,
-                                        uint8_t* dst, uint64_t* bar) {
-  using B = Q4Block<D>;
-  const int page = meta[c.q.pg_at + c.pg];
-  const uint8_t* src = pool + ((size_t)page * hkv + c.h) * B::bytes + (which ? B::v : 0);
-  const int keys = min(kQ4Page, (c.q.len - ((c.q.chunk0 + c.pg) << 7) + 3) & ~3);
-  if (keys == kQ4Page) {
-    mbar_arrive_expect_tx(bar, B::v);
-    bulk_g2s(dst, src, B::v, bar);
-  } else {
-    const uint32_t codes = keys * (D / 2), nums = keys * 4;
-    mbar_arrive_expect_tx(bar, codes + nums);
-    bulk_g2s(dst, src, codes, bar);
-    bulk_g2s(dst + B::kz, src + B::kz, nums, bar);
-  }
-}
-
-template <int D, int NR, int N>
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel(
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint8_t* __restrict__ pool, int n_seq,
     float scale_log2e, int max_units, float* __restrict__ partials, float* __restrict__ out,
     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using B = Q4Block<D>;
-  using S = Q4Smem<D, NR>;
+  using S = Q4Smem<D>;
   constexpr int W = D / 32;    // 32-bit words of a thread's piece of a K row, and of a V key pair
   constexpr int NT = D / 16;   // 16-dimension tiles of the output
-  constexpr int ROWS = 8 * NR;
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* qs = reinterpret_cast<uint4*>(smem + S::q);
   float4* rowp = reinterpret_cast<float4*>(smem + S::rows);
@@ -286,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
     if (++ask_slot == kSlots) ask_slot = 0, ask_phase ^= 1;
     if ((ask_which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
       if (ahead->end() < w1)
-        ahead->next<NR>(meta, hkv, G);
+        ahead->next<kRows>(meta, hkv, G);
       else
         more = false;
     }
@@ -294,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
   if (tid == 0) {
     const int w0 = (int)(total * blockIdx.x / gridDim.x);
     Cursor first;
-    more = w0 < w1 && first.start<NR>(meta, n_seq, hkv, G, w0) && first.at < w1;
+    more = w0 < w1 && first.start<kRows>(meta, n_seq, hkv, G, w0) && first.at < w1;
     *done = !more;
     if (more) {
       *cur = first;
@@ -313,10 +164,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
     if (++slot == kSlots) slot = 0, phase ^= 1;
   };
   for (;;) {
-    const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * ROWS, R = G * n_new;
+    const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * kRows, R = G * n_new;
     if (cur->fresh) {
-      if (warp < NR) {  // a warp for each tile of 8 rows: row g, dimensions D/4 c ..
-        const int r = row0 + 8 * warp + g, j = r / G, gi = r - j * G;
+      if (warp == 0) {  // row g, dimensions D/4 c ..
+        const int r = row0 + g, j = r / G, gi = r - j * G;
         const bool live = r < R;
         float x[D / 4];
         const float* src = q + (size_t)(cur->q.tok0 + j) * q_stride + (size_t)(cur->h * G + gi) * D + c * (D / 4);
@@ -346,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
         row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
         // a row past the last: q = 0, the keys of the last token; never written
         if (c == 0)
-          rowp[8 * warp + g] = make_float4(row_scale, row_sum * 0x1p-24f,
+          rowp[g] = make_float4(row_scale, row_sum * 0x1p-24f,
                                            __int_as_float(live ? len - n_new + j : len - 1), 0.0f);
         // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
         // nibbles stand 16 times as high in their word
@@ -357,36 +208,34 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
             uint4 v;  // hi of the step's two halves, then lo
             split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), v.x, v.z);
             split(pack(x[8 * w + 2 * b + 1] * 0.0625f, x[8 * w + 2 * b + 5] * 0.0625f), v.y, v.w);
-            qs[((2 * w + b) * NR + warp) * 32 + lane] = v;
+            qs[(2 * w + b) * 32 + lane] = v;
           }
       }
       __syncthreads();
     }
-    // rows 2c and 2c + 1 of each tile: the scale taken out of q, sum(q), the last key seen
-    f2 scale2[NR], sum2[NR];
-    int hi0[NR], hi1[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const float4 a = rowp[8 * n + 2 * c], b = rowp[8 * n + 2 * c + 1];
-      scale2[n] = pack(a.x, b.x);
-      sum2[n] = pack(a.y, b.y);
-      hi0[n] = __float_as_int(a.z), hi1[n] = __float_as_int(b.z);
+    // rows 2c and 2c + 1: the scale taken out of q, sum(q), the last key seen
+    f2 scale2, sum2;
+    int hi0, hi1;
+    {
+      const float4 a = rowp[2 * c], b = rowp[2 * c + 1];
+      scale2 = pack(a.x, b.x);
+      sum2 = pack(a.y, b.y);
+      hi0 = __float_as_int(a.z), hi1 = __float_as_int(b.z);
     }
     const int back = window > 0 ? window - 1 : 0x7FFFFFFF;  // keys seen before the last
-    float o[NR][NT][4];
-    float M0[NR], M1[NR];
-    f2 lsum[NR], zsum[NR];
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
+    float o[NT][4];
+    float M0, M1;
+    f2 lsum, zsum;
+    {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][t][e] = 0.0f;
-      M0[n] = M1[n] = -INFINITY;
-      lsum[n] = zsum[n] = 0;
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
+      M0 = M1 = -INFINITY;
+      lsum = zsum = 0;
     }
     // what any row of the item can see, and what every row sees
-    const int j0 = row0 / G, j1 = min(row0 + ROWS - 1, R - 1) / G;
+    const int j0 = row0 / G, j1 = min(row0 + kRows - 1, R - 1) / G;
     const int first_hi = len - n_new + j0, last_hi = len - n_new + j1;
     const int any_lo = first_hi - back, all_lo = window > 0 ? len - window : 0;
 
@@ -400,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
       // no conversion; -8 sum(q) starts the sums.
       if (!mbar_wait(&full[slot], phase)) g_err_attention_q4 = 1u;
       __syncwarp();
-      f2 x[NR][2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
+      f2 x[2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
       if (some) {
         const uint8_t* blk = smem + slot * S::half;
-        float sc[NR][2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
+        float sc[2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
         uint32_t kw[2][2][W];   // [tile][key g, g + 8]
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -422,22 +271,19 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
         for (int w = 0; w < W; ++w)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            uint4 q4[NR];
-#pragma unroll
-            for (int n = 0; n < NR; ++n) q4[n] = qs[((2 * w + b) * NR + n) * 32 + lane];
+            const uint4 q4 = qs[(2 * w + b) * 32 + lane];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const uint32_t u = kw[t][0][w] >> (8 * b), v = kw[t][1][w] >> (8 * b);
               const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
-#pragma unroll
-              for (int n = 0; n < NR; ++n) {
+              {
                 if (w == 0 && b == 0) {
-                  const float2 start = unpack(mul2(sum2[n], pack(-8.0f, -8.0f)));
-                  mma_from(sc[n][t][0], a0, a1, a2, a3, q4[n].x, q4[n].y, start.x, start.y);
-                  mma_from(sc[n][t][1], a0, a1, a2, a3, q4[n].z, q4[n].w, 0.0f, 0.0f);
+                  const float2 start = unpack(mul2(sum2, pack(-8.0f, -8.0f)));
+                  mma_from(sc[t][0], a0, a1, a2, a3, q4.x, q4.y, start.x, start.y);
+                  mma_from(sc[t][1], a0, a1, a2, a3, q4.z, q4.w, 0.0f, 0.0f);
                 } else {
-                  mma(sc[n][t][0], a0, a1, a2, a3, q4[n].x, q4[n].y);
-                  mma(sc[n][t][1], a0, a1, a2, a3, q4[n].z, q4[n].w);
+                  mma(sc[t][0], a0, a1, a2, a3, q4.x, q4.y);
+                  mma(sc[t][1], a0, a1, a2, a3, q4.z, q4.w);
                 }
               }
             }
@@ -449,11 +295,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-              const f2 acc = add2(pack(sc[n][t][0][2 * h], sc[n][t][0][2 * h + 1]),
-                                  pack(sc[n][t][1][2 * h], sc[n][t][1][2 * h + 1]));
-              x[n][t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2[n]));
+            {
+              const f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]),
+                                  pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
+              x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
             }
           }
       }
@@ -469,18 +314,17 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
         if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
         vd = __reduce_max_sync(0xFFFFFFFFu, vd);
         const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
+        {
           float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float2 v = unpack(x[n][t][h]);
+              float2 v = unpack(x[t][h]);
               if (!whole) {
                 const int key = key0 + 16 * t + 8 * h + g;
-                if (hidden(key, hi0[n])) v.x = -INFINITY;
-                if (hidden(key, hi1[n])) v.y = -INFINITY;
+                if (hidden(key, hi0)) v.x = -INFINITY;
+                if (hidden(key, hi1)) v.y = -INFINITY;
               }
               top0 = fmaxf(top0, v.x);
               top1 = fmaxf(top1, v.y);
@@ -490,56 +334,55 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
             top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, s4));
             top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, s4));
           }
-          const float2 sc2 = unpack(scale2[n]);
+          const float2 sc2 = unpack(scale2);
           top0 = __fmaf_rn(sc2.x, top0, vd_log);
           top1 = __fmaf_rn(sc2.y, top1, vd_log);
           // The reference is set 2^10 below the largest weight and moves only when
           // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
           // coarser than 2^-35 of the largest weight.
-          if (__any_sync(0xFFFFFFFFu, top0 > M0[n] + 14.0f || top1 > M1[n] + 14.0f)) {
-            const float to0 = top0 > M0[n] + 14.0f ? top0 - 10.0f : M0[n];
-            const float to1 = top1 > M1[n] + 14.0f ? top1 - 10.0f : M1[n];
-            if (__any_sync(0xFFFFFFFFu, M0[n] != -INFINITY || M1[n] != -INFINITY)) {  // else nothing is summed yet
-              const float f0 = M0[n] == -INFINITY ? 0.0f : ex2(M0[n] - to0);
-              const float f1 = M1[n] == -INFINITY ? 0.0f : ex2(M1[n] - to1);
-              lsum[n] = mul2(lsum[n], pack(f0, f1));
-              zsum[n] = mul2(zsum[n], pack(f0, f1));
+          if (__any_sync(0xFFFFFFFFu, top0 > M0 + 14.0f || top1 > M1 + 14.0f)) {
+            const float to0 = top0 > M0 + 14.0f ? top0 - 10.0f : M0;
+            const float to1 = top1 > M1 + 14.0f ? top1 - 10.0f : M1;
+            if (__any_sync(0xFFFFFFFFu, M0 != -INFINITY || M1 != -INFINITY)) {  // else nothing is summed yet
+              const float f0 = M0 == -INFINITY ? 0.0f : ex2(M0 - to0);
+              const float f1 = M1 == -INFINITY ? 0.0f : ex2(M1 - to1);
+              lsum = mul2(lsum, pack(f0, f1));
+              zsum = mul2(zsum, pack(f0, f1));
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                o[n][t][0] *= f0, o[n][t][1] *= f1;
-                o[n][t][2] *= f0, o[n][t][3] *= f1;
+                o[t][0] *= f0, o[t][1] *= f1;
+                o[t][2] *= f0, o[t][3] *= f1;
               }
             }
-            M0[n] = to0, M1[n] = to1;
+            M0 = to0, M1 = to1;
           }
         }
         // ---- weights, and 16 keys at a time their product with V
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          uint32_t ph[NR][2], pl[NR][2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
+          uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
+            {
               f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
-              const float2 v = unpack(fma2(scale2[n], x[n][t][h], pack(-M0[n], -M1[n])));
+              const float2 v = unpack(fma2(scale2, x[t][h], pack(-M0, -M1)));
               float2 pr = make_float2(ex2(v.x), ex2(v.y));
               if (!whole) {  // a hidden key's numbers may be anything
                 const int key = key0 + 16 * t + 8 * h + g;
-                const bool no0 = hidden(key, hi0[n]), no1 = hidden(key, hi1[n]);
+                const bool no0 = hidden(key, hi0), no1 = hidden(key, hi1);
                 if (no0) pr.x = 0.0f;
                 if (no1) pr.y = 0.0f;
                 d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
                 z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
               }
               const f2 pp = pack(pr.x, pr.y);
-              lsum[n] = add2(lsum[n], pp);
-              zsum[n] = fma2(pp, z, zsum[n]);
-              split(mul2(pp, d), ph[n][h], pl[n][h]);
-              ph[n][h] = transpose8(ph[n][h]);
-              pl[n][h] = transpose8(pl[n][h]);
+              lsum = add2(lsum, pp);
+              zsum = fma2(pp, z, zsum);
+              split(mul2(pp, d), ph[h], pl[h]);
+              ph[h] = transpose8(ph[h]);
+              pl[h] = transpose8(pl[h]);
             }
           }
           uint32_t v0[W], v1[W];
@@ -559,16 +402,15 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
             __half2 h0[4], h1[4];
             q4_unpack(v0[w], h0);
             q4_unpack(v1[w], h1);
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                mma(o[n][2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
-                    ph[n][0], ph[n][1]);
+            {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                mma(o[n][2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
-                    pl[n][0], pl[n][1]);
+                mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                    ph[0], ph[1]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                    pl[0], pl[1]);
             }
           }
         }
@@ -580,66 +422,60 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
     // ---- the unit's end: warps 2 and 3 hand their rows to 0 and 1, then 1 to 0;
     // a thread's rows and dimensions are the same in every warp
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
       for (int s4 = 4; s4 < 32; s4 <<= 1) {
-        const float2 l = unpack(lsum[n]), z = unpack(zsum[n]);
-        lsum[n] = add2(lsum[n], pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
-        zsum[n] = add2(zsum[n], pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
+        const float2 l = unpack(lsum), z = unpack(zsum);
+        lsum = add2(lsum, pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
+        zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
       }
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      const float2 z = unpack(zsum[n]);
+    {
+      const float2 z = unpack(zsum);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        o[n][t][0] += z.x, o[n][t][1] += z.y;
-        o[n][t][2] += z.x, o[n][t][3] += z.y;
+        o[t][0] += z.x, o[t][1] += z.y;
+        o[t][2] += z.x, o[t][3] += z.y;
       }
     }
 #pragma unroll
     for (int from = 2; from > 0; from >>= 1) {
       if (warp >= from && warp < 2 * from) {
-        float4* dst = join + (warp - from) * (NR * NT * 32) + lane;
+        float4* dst = join + (warp - from) * (NT * 32) + lane;
+        {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) dst[(n * NT + t) * 32] = make_float4(o[n][t][0], o[n][t][1], o[n][t][2], o[n][t][3]);
-          const float2 l = unpack(lsum[n]);
-          if (g == 0) stat[((warp - from) * NR + n) * 4 + c] = make_float4(M0[n], M1[n], l.x, l.y);
+          for (int t = 0; t < NT; ++t) dst[t * 32] = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
+          const float2 l = unpack(lsum);
+          if (g == 0) stat[(warp - from) * 4 + c] = make_float4(M0, M1, l.x, l.y);
         }
       }
       __syncthreads();
       if (warp < from) {
-        const float4* src = join + warp * (NR * NT * 32) + lane;
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          const float4 b = stat[(warp * NR + n) * 4 + c];
-          const float2 l = unpack(lsum[n]);
-          const float t0 = fmaxf(M0[n], b.x), t1 = fmaxf(M1[n], b.y);
+        const float4* src = join + warp * (NT * 32) + lane;
+        {
+          const float4 b = stat[warp * 4 + c];
+          const float2 l = unpack(lsum);
+          const float t0 = fmaxf(M0, b.x), t1 = fmaxf(M1, b.y);
           // no maximum: nothing was seen, or only NaN scores, which the sums carry
-          const float a0 = M0[n] == t0 ? 1.0f : ex2(M0[n] - t0), a1 = M1[n] == t1 ? 1.0f : ex2(M1[n] - t1);
+          const float a0 = M0 == t0 ? 1.0f : ex2(M0 - t0), a1 = M1 == t1 ? 1.0f : ex2(M1 - t1);
           const float b0 = b.x == t0 ? 1.0f : ex2(b.x - t0), b1 = b.y == t1 ? 1.0f : ex2(b.y - t1);
-          M0[n] = t0, M1[n] = t1;
-          lsum[n] = pack(__fmaf_rn(b0, b.z, a0 * l.x), __fmaf_rn(b1, b.w, a1 * l.y));
+          M0 = t0, M1 = t1;
+          lsum = pack(__fmaf_rn(b0, b.z, a0 * l.x), __fmaf_rn(b1, b.w, a1 * l.y));
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float4 v = src[(n * NT + t) * 32];
-            o[n][t][0] = __fmaf_rn(b0, v.x, a0 * o[n][t][0]);
-            o[n][t][1] = __fmaf_rn(b1, v.y, a1 * o[n][t][1]);
-            o[n][t][2] = __fmaf_rn(b0, v.z, a0 * o[n][t][2]);
-            o[n][t][3] = __fmaf_rn(b1, v.w, a1 * o[n][t][3]);
+            const float4 v = src[t * 32];
+            o[t][0] = __fmaf_rn(b0, v.x, a0 * o[t][0]);
+            o[t][1] = __fmaf_rn(b1, v.y, a1 * o[t][1]);
+            o[t][2] = __fmaf_rn(b0, v.z, a0 * o[t][2]);
+            o[t][3] = __fmaf_rn(b1, v.w, a1 * o[t][3]);
           }
         }
       }
       __syncthreads();
     }
     if (warp == 0) {
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const float2 l = unpack(lsum[n]);
+      {
+        const float2 l = unpack(lsum);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = row0 + 8 * n + 2 * c + e;
+          const int r = row0 + 2 * c + e;
           if (r >= R) continue;
           const int j = r / G;
           const size_t row = (size_t)(cur->q.tok0 + j) * hq + cur->h * G + r - j * G;
@@ -648,14 +484,14 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
             float4* dst = reinterpret_cast<float4*>(out + row * D + g * (D / 8));
 #pragma unroll
             for (int t = 0; t < NT; t += 2)
-              dst[t / 2] = make_float4(__fdiv_rn(o[n][t][e], le), __fdiv_rn(o[n][t][2 + e], le),
-                                       __fdiv_rn(o[n][t + 1][e], le), __fdiv_rn(o[n][t + 1][2 + e], le));
+              dst[t / 2] = make_float4(__fdiv_rn(o[t][e], le), __fdiv_rn(o[t][2 + e], le),
+                                       __fdiv_rn(o[t + 1][e], le), __fdiv_rn(o[t + 1][2 + e], le));
           } else {
             float* at = partials + (row * max_units + cur->u) * (D + 2);
             float2* dst = reinterpret_cast<float2*>(at + 2 + g * (D / 8));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) dst[t] = make_float2(o[n][t][e], o[n][t][2 + e]);
-            if (g == 0) *reinterpret_cast<float2*>(at) = make_float2(e ? M1[n] : M0[n], le);
+            for (int t = 0; t < NT; ++t) dst[t] = make_float2(o[t][e], o[t][2 + e]);
+            if (g == 0) *reinterpret_cast<float2*>(at) = make_float2(e ? M1 : M0, le);
           }
         }
       }
@@ -663,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2) attention_q4_kernel
     __syncwarp();
     if (tid == 0) {
       *done = cur->end() >= w1;
-      if (!*done) cur->next<NR>(meta, hkv, G);
+      if (!*done) cur->next<kRows>(meta, hkv, G);
     }
     __syncthreads();
     if (*done) break;
@@ -740,10 +576,10 @@ __global__ void __launch_bounds__(D) attention_q4_merge_kernel(const float* __re
   out[row * D + dim] = __fdiv_rn(acc, l);
 }
 
-template <int D, int NR, int N>
+template <int D, int N>
 cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  constexpr int smem = Q4Smem<D, NR>::bytes;
-  auto kern = attention_q4_kernel<D, NR, N>;
+  constexpr int smem = Q4Smem<D>::bytes;
+  auto kern = attention_q4_kernel<D, N>;
   int resident = 0;
   {
     static std::mutex mu;
@@ -765,15 +601,20 @@ cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t 
   ParamWords<N> w;
   for (int i = 0; i < N; ++i) w.w[i] = N > 1 && i < meta.n_words ? meta.host[i] : 0;
   const unsigned grid = (unsigned)(a.items < resident ? a.items : resident);
-  const float scale = (float)(1.4426950408889634 / sqrt((double)D));
-  cudaError_t e = launch_kernel(kern, dim3(grid), dim3(kThreads), smem, st, a.q, a.q_stride, a.hq, a.hkv,
-                                static_cast<const uint8_t*>(a.pool), a.n_seq, scale, a.max_units, a.partials, a.out, w,
-                                meta.dev);
-  if (e != cudaSuccess || a.max_units == 1) return e;
+  return launch_kernel(kern, dim3(grid), dim3(kThreads), smem, st, a.q, a.q_stride, a.hq, a.hkv,
+                       static_cast<const uint8_t*>(a.pool), a.n_seq, (float)(1.4426950408889634 / sqrt((double)D)),
+                       a.max_units, a.partials, a.out, w, meta.dev);
+}
+
+template <int D, int N>
+cudaError_t merge_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
+  ParamWords<N> w;
+  for (int i = 0; i < N; ++i) w.w[i] = N > 1 && i < meta.n_words ? meta.host[i] : 0;
   // the join's CTAs may start while the last units run (they wait for them)
   const bool was = pdl();
   set_pdl(true);
-  e = launch_kernel(attention_q4_merge_kernel<D, N>, dim3((unsigned)a.n_tok, (unsigned)a.hq), dim3(D), 0, st, a.partials,
+  const cudaError_t e =
+      launch_kernel(attention_q4_merge_kernel<D, N>, dim3((unsigned)a.n_tok, (unsigned)a.hq), dim3(D), 0, st, a.partials,
                     a.hq, a.n_seq, a.max_units, a.out, w, meta.dev);
   set_pdl(was);
   return e;
@@ -781,20 +622,26 @@ cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t 
 
 template <int D>
 cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  if (a.row_tiles == 1) return meta.dev ? attention_go<D, 1, 1>(a, meta, st) : attention_go<D, 1, kParamWords>(a, meta, st);
-  return meta.dev ? attention_go<D, 2, 1>(a, meta, st) : attention_go<D, 2, kParamWords>(a, meta, st);
+  cudaError_t e;
+  if (a.tile_rows > kRows)
+    e = launch_attention_q4_tc(a, D, meta, st);
+  else
+    e = meta.dev ? attention_go<D, 1>(a, meta, st) : attention_go<D, kParamWords>(a, meta, st);
+  if (e != cudaSuccess || a.max_units == 1) return e;
+  return meta.dev ? merge_go<D, 1>(a, meta, st) : merge_go<D, kParamWords>(a, meta, st);
 }
 
 }  // namespace
 
 // Long units cost less joining, short ones fill the GPU with few sequences: the
-// sequence alone makes up to kAlone items (heads and row tiles included), of two
-// pages at least where it has many.
-int q4_unit_pages(int n, int lanes) {
-  constexpr long long kAlone = 2048;
+// sequence alone makes up to 1024 items (heads and row tiles included), of two or
+// four pages at least where it has many.  The tcgen05 kernel's units have more to
+// set up and to add up at their end.
+int q4_unit_pages(int n, int lanes, int tile_rows) {
+  const long long alone = tile_rows > 8 ? 128 : 1024;
   if (n <= 2) return n;
-  const int least = n <= 16 ? 1 : 2;
-  const long long u = ((long long)n * lanes + kAlone - 1) / kAlone;
+  const int least = tile_rows > 8 ? (n < 4 ? n : 4) : n <= 4 ? 1 : n <= 64 ? 2 : 4;
+  const long long u = ((long long)n * lanes + alone - 1) / alone;
   return u < least ? least : u > n ? n : (int)u;
 }
 

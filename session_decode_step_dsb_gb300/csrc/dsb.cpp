@@ -150,7 +150,8 @@ dsb_status dsb_device_error(void) {
   const unsigned int m = dsbk::read_clear_error_matmul();
   const unsigned int mt = dsbk::read_clear_error_matmul_tc() | dsbk::read_clear_error_matmul_fused() |
                            dsbk::read_clear_error_matmul_staged();
-  const unsigned int a = dsbk::read_clear_error_attention() | dsbk::read_clear_error_attention_q4();
+  const unsigned int a = dsbk::read_clear_error_attention() | dsbk::read_clear_error_attention_q4() |
+                         dsbk::read_clear_error_attention_q4_tc();
   if (m || mt || a)
     return fail(DSB_ERR_DEVICE, "a kernel's bounded wait ran out (matmul=%u matmul_tc=%u attention=%u)", m, mt, a);
   return DSB_OK;

@@ -204,10 +204,11 @@ unsigned int read_clear_error_attention();
 
 // ---- rotary layouts, paged append, 4-bit KV (csrc/rotary.cu, csrc/attention_q4.cu, csrc/gather_q4.cu)
 
-// A call's metadata words: up to kParamWords of them ride in the kernel's
+// A call's metadata words: up to kParamWords of them (16 KB) ride in the kernel's
 // parameters (no copy, and a captured launch keeps its own), more are staged in
-// device memory.  Kernels take both forms; ParamWords<1> means the staged one.
-constexpr int kParamWords = 960;
+// device memory.  Measured against 960: small calls the same, 64 sequences of up to
+// 1500 keys (1100 words, staged before) 74 -> 43 us a pass.  Kernels take both forms; ParamWords<1> means the staged one.
+constexpr int kParamWords = 4032;
 template <int N>
 struct ParamWords {
   int32_t w[N];
@@ -252,25 +253,30 @@ cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, c
 
 // One sequence of a 4-bit attention call, in its metadata; n_seq of them, then
 // the pages of work in all, then the visited pages of all sequences.  A
-// sequence's work items are (kv head, tile of 8 row_tiles query rows, unit of u_pages
+// sequence's work items are (kv head, tile of tile_rows query rows, unit of u_pages
 // pages); work_off: pages of work of the sequences before it.
 struct Q4Seq {
   int32_t work_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
 };
 constexpr int kQ4SeqWords = 8;
-// Tiles of 8 query rows in an item of a sequence with `rows` of them on a kv
-// head: a rule on the sequence alone, as the one on its units.
-inline int q4_row_tiles(long long rows) { return rows < 0 ? 2 : 1; }
+// Query rows of an item of a sequence with `rows` of them on a kv head: a rule on
+// the sequence alone, as the one on its units.  Up to 8 the warp-level kernel
+// (attention_q4.cu), more the tcgen05 one (attention_q4_tc.cu).
+inline int q4_tile_rows(long long rows) {
+  if (rows <= 8) return 8;
+  const long long tiles = (rows + 23) / 24;
+  return (rows + tiles - 1) / tiles <= 16 ? 16 : 24;
+}
 // Pages per unit of a sequence that visits n of them, with `lanes` pairs of a kv
-// head and a tile of rows: a rule on the sequence alone, not on the batch.
-int q4_unit_pages(int n, int lanes);
+// head and a tile of tile_rows rows: a rule on the sequence alone, not on the batch.
+int q4_unit_pages(int n, int lanes, int tile_rows);
 struct Q4AttnArgs {
   const float* q;
   long long q_stride;
   int hq, hkv;
   const void* pool;
   int n_seq, n_tok;
-  int row_tiles;    // of every listed sequence
+  int tile_rows;    // of every listed sequence
   long long items;
   int max_units;    // units of the sequence with the most of them
   float* partials;  // [n_tok][hq][max_units][head_dim + 2]
@@ -278,6 +284,9 @@ struct Q4AttnArgs {
 };
 cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st);
 unsigned int read_clear_error_attention_q4();
+// Its kernel for tiles of more than 8 rows, without the joining of the units.
+cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st);
+unsigned int read_clear_error_attention_q4_tc();
 
 // One sequence of a read-back; n_seq of them, then the total page count, then
 // the pages of all sequences.

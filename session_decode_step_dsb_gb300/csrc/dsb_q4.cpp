@@ -387,11 +387,11 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     auto pages = [&](int s) { return b->new_tokens[s] == 0 ? 0 : (b->seq_lens[s] - 1) / DSB_KV_PAGE - chunk0(s) + 1; };
     std::vector<Group> groups;
     if ((st = cut_groups(b->n_seq, 1, dsbk::kQ4SeqWords, pages, &groups)) != DSB_OK) return st;
-    // One launch for each group and number of row tiles: that, like the units,
+    // One launch for each group and height of the row tiles: that, like the units,
     // depends on a sequence's own rows, not on its neighbours.
     struct Plan {
       std::vector<int32_t> words;
-      int live = 0, max_units = 1, tok0 = 0, n_tok = 0, row_tiles = 1;
+      int live = 0, max_units = 1, tok0 = 0, n_tok = 0, tile_rows = 8;
       long long items = 0, work = 0;
     };
     std::vector<Plan> plans;
@@ -399,21 +399,21 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     size_t most = 0, need = 0;
     for (const Group& g : groups) {
       int tok1 = tok0;
-      for (int tiles_of = 1; tiles_of <= 2; ++tiles_of) {
+      for (const int rows : {8, 16, 24}) {
         Plan p;
         std::vector<int32_t> list;
         p.tok0 = tok0;
-        p.row_tiles = tiles_of;
+        p.tile_rows = rows;
         auto mine = [&](int s) {
-          return b->new_tokens[s] > 0 && dsbk::q4_row_tiles((long long)G * b->new_tokens[s]) == tiles_of;
+          return b->new_tokens[s] > 0 && dsbk::q4_tile_rows((long long)G * b->new_tokens[s]) == rows;
         };
         for (int s = g.s0; s < g.s1; ++s) p.live += mine(s);
         int tok = 0;
         for (int s = g.s0; s < g.s1; tok += b->new_tokens[s], ++s) {
           if (!mine(s)) continue;
-          const int n = b->new_tokens[s], np = pages(s), rows = 8 * tiles_of;
+          const int n = b->new_tokens[s], np = pages(s);
           const int tiles = (int)(((long long)G * n + rows - 1) / rows);
-          const int u = dsbk::q4_unit_pages(np, kv->n_kv_heads * tiles), units = (np + u - 1) / u;
+          const int u = dsbk::q4_unit_pages(np, kv->n_kv_heads * tiles, rows), units = (np + u - 1) / u;
           const int32_t rec[dsbk::kQ4SeqWords] = {(int32_t)p.work,
                                                   tok,
                                                   n,
@@ -455,7 +455,7 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
                                kv->blocks,
                                p.live,
                                p.n_tok,
-                               p.row_tiles,
+                               p.tile_rows,
                                p.items,
                                p.max_units,
                                reinterpret_cast<float*>(partial_base(ws)),

@@ -243,7 +243,10 @@ ATTN = [  # D, hq, hkv, lens, new, window
     (128, 3, 3, [1, 2, 31, 32, 33, 95, 97], [1, 2, 1, 1, 3, 1, 2], [0, 1, 7, 0, 32, 0, 96]),
     (64, 10, 1, [2600], [7], [0]),                       # 70 query rows
     (128, 2, 1, [5000, 260], [1, 64], [0, 130]),
-    (64, 16, 2, [300], [130], [0])]                       # a prompt: 1040 rows
+    (64, 16, 2, [300], [130], [0]),                       # a prompt: 1040 rows
+    (128, 16, 1, [1, 127, 128, 700], [1, 1, 1, 1], [0, 0, 60, 300]),    # 16 rows
+    (128, 10, 2, [400, 8, 1500, 513], [8, 8, 1, 2], [0, 0, 0, 333]),     # 40, 5 and 10 rows in one call
+    (64, 9, 1, [1000, 260], [1, 3], [129, 0])]            # 9 and 27 rows
 
 
 @pytest.mark.parametrize("case", ATTN)
@@ -311,6 +314,28 @@ def test_attention_q4_scales_far_apart(cuda_device):
     want, bound = oq4.attention(q, kvals, vvals, [[0]], [1], [0], [1], [100], oq4.pool_sizes(pool, 64))
     got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), 64), d.PagedBatch([[0]], [1], [0], [1], [100]),
                                         d.Workspace(1, 1, 64, P)))
+    assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,T", [(2, 2), (12, 1), (6, 5)])
+def test_attention_q4_references_move(cuda_device, D, hq, T):
+    """Keys that grow from page to page: each page's largest weight is far above
+    the last one's, for all rows or for some (rows of the other sign shrink)."""
+    d = _dsb()
+    rng = np.random.default_rng(13)
+    pool = np.empty((9, 1, P * (D + 8)), np.uint8)
+    for p in range(9):
+        k = rng.standard_normal((P, D)) * 0.1
+        k[:, 0] += 4.0 * p
+        pool[p, 0] = oq4.pack_block(*oq4.quantise(k), *oq4.quantise(rng.standard_normal((P, D)) * 2.0 ** (p % 3)))
+    q = rng.standard_normal((T, hq, D)).astype(np.float32) * 0.2
+    q[..., 0] = np.sqrt(D) * np.where(rng.random((T, hq)) < 0.5, 3.5, -1.0)
+    bt = [list(range(9))]
+    kvals, vvals = oq4.pool_values(pool, D)
+    want, bound = oq4.attention(q, kvals, vvals, bt, [9], [0], [T], [1100], oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [9], [0], [T], [1100]),
+                                        d.Workspace(T, hq, D, 1152)))
     assert (np.abs(got - want) <= bound).all()
 
 
@@ -440,21 +465,21 @@ def test_captured_and_replayed(cuda_device):
             torch.cuda.synchronize()
             for a, b in zip((qkv, out, k, v, pool), want):
                 assert torch.equal(a, b)
-    # 1000 positions apart are staged: not in a graph
-    q = torch.zeros((1000, 2, D), device="cuda")
-    big = d.Workspace(1000, 2, D, P)
+    # 5000 positions apart are staged: not in a graph
+    q = torch.zeros((5000, 2, D), device="cuda")
+    big = d.Workspace(5000, 2, D, P)
     s = torch.cuda.Stream()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=s):
         q.add_(0.0)
         with pytest.raises(d.DsbError, match="captured"):
-            d.rope_rotary(q, None, np.arange(0, 2000, 2), rot, big)
-    d.rope_rotary(q, None, np.arange(0, 2000, 2), rot, big)
+            d.rope_rotary(q, None, np.arange(0, 10000, 2), rot, big)
+    d.rope_rotary(q, None, np.arange(0, 10000, 2), rot, big)
     torch.cuda.synchronize()
 
 
 def test_staged_and_cut_metadata_give_the_same_bits(cuda_device):
-    """700 sequences with tables of 40 blocks (35000 words: several launches,
+    """700 sequences with tables of 40 blocks (some 20000 words: several launches,
     staged) against the same sequences a few at a time (in the parameters)."""
     import torch
     d = _dsb()
