@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
 
 constexpr int kAppThreads = 256;
 
-// Two float32 products or sums at once, each rounded as by itself.
+// Two float32 products at once, each rounded as by itself.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float a, float b) {
   f2 r;
@@ -208,11 +208,6 @@ __device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   f2 d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
@@ -412,10 +407,12 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __rest
         if (!is_v) {
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            float z0, z1;
-            unpack2(add2(mul2(pack2(y[e], y[e + 1]), pack2(c[e], c[e + 1])),
-                         mul2(pack2(p[e], p[e + 1]), pack2(s[e], s[e + 1]))),
-                    z0, z1);
+            // the sums one by one: a packed sum of packed products is compiled to a
+            // fused multiply-add, which rounds once less
+            float a0, a1, b0, b1;
+            unpack2(mul2(pack2(y[e], y[e + 1]), pack2(c[e], c[e + 1])), a0, a1);
+            unpack2(mul2(pack2(p[e], p[e + 1]), pack2(s[e], s[e + 1])), b0, b1);
+            const float z0 = __fadd_rn(a0, b0), z1 = __fadd_rn(a1, b1);
             y[e] = all || turned[e] ? z0 : y[e];
             y[e + 1] = all || turned[e + 1] ? z1 : y[e + 1];
           }

@@ -195,6 +195,29 @@ def test_append(cuda_device, case, store):
     assert flips <= 3 + 1e-3 * n_tok * hkv * D
 
 
+@pytest.mark.parametrize("D,rd,inter,scale,n", [(128, 128, False, "yarn", 300), (64, 48, True, "linear", 5),
+                                               (128, 34, True, "none", 70), (64, 18, False, "ntk", 40)])
+def test_the_append_turns_as_the_rotary_call_does(cuda_device, D, rd, inter, scale, n):
+    """The same steps, each rounded once: the same bits on both paths."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(D + rd)
+    hq, hkv = 6, 2
+    x = to_dev(rng.standard_normal((n, hq + 2 * hkv, D)).astype(np.float32))
+    rot = _rot(scale, rd, inter)[0]
+    turned = x.clone()
+    ws = d.Workspace(n, hq, D, 4096)
+    d.rope_rotary(turned[:, :hq], turned[:, hq:hq + hkv], np.arange(700, 700 + n), rot, ws)
+    blocks = -(-(700 + n) // P)
+    batch = d.PagedBatch(np.arange(blocks, dtype=np.int32)[None], [blocks], [0], [n], [700 + n])
+    k = torch.zeros((blocks, hkv, P, D), device="cuda", dtype=torch.float16)
+    got = x.clone()
+    d.kv_append_paged(got.view(n, -1), hq, d.kv_pages(k, torch.zeros_like(k), d.DSB_F16), batch, rot, ws)
+    assert torch.equal(got[:, :hq], turned[:, :hq]) and torch.equal(got[:, hq:], x[:, hq:])
+    rows = k.permute(0, 2, 1, 3).reshape(-1, hkv, D)[700:700 + n]
+    assert torch.equal(rows, turned[:, hq:hq + hkv].half())
+
+
 def test_append_stores_bad_vectors_as_nan(cuda_device):
     d = _dsb()
     x = np.random.default_rng(0).standard_normal((4, 3 * 64)).astype(np.float32)
