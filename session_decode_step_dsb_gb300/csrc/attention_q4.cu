@@ -34,6 +34,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "attention_q4.cuh"
 #include "dsb_kernels.h"
@@ -84,9 +85,9 @@ struct Q4Smem {
   static constexpr int half = Q4Block<D>::v;                // K codes and numbers; V's are as many bytes
   static constexpr int q = kSlots * half;                   // [D/16][32 lanes] uint4: q as right operand
   static constexpr int rows = q + D / 16 * 512;             // [8] float4: scale, sum, last key, -
-  static constexpr int join = rows + kRows * 16;            // [2 warps][D/16][32 lanes] float4
-  static constexpr int stat = join + 2 * (D / 16) * 512;    // [2 warps][4] float4: M, M, sum, sum
-  static constexpr int bars = stat + 2 * 64;
+  static constexpr int join = rows + kRows * 16;            // [4 warps][D/32][32 lanes] float4
+  static constexpr int stat = join + 4 * (D / 32) * 512;    // [4 warps][4] float4: M, M, sum, sum
+  static constexpr int bars = stat + 4 * 64;
   static constexpr int cursors = bars + 2 * kSlots * 8;     // the item in work, the next to ask for, "done"
   static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
 };
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
-        const float row_scale = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 240);
+        const float row_scale = __uint_as_float((uint32_t)(e - 10) << 23);  // 2^-10 of that
         const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
         float row_sum = 0.0f;
 #pragma unroll
@@ -197,17 +198,16 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         row_sum += __shfl_xor_sync(0xFFFFFFFFu, row_sum, 2);
         // a row past the last: q = 0, the keys of the last token; never written
         if (c == 0)
-          rowp[g] = make_float4(row_scale, row_sum * 0x1p-24f,
+          rowp[g] = make_float4(row_scale, row_sum,
                                            __int_as_float(live ? len - n_new + j : len - 1), 0.0f);
-        // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4); the odd
-        // nibbles stand 16 times as high in their word
+        // word w holds dimensions 8w .. 8w+7 of the piece, paired (n, n + 4)
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint4 v;  // hi of the step's two halves, then lo
             split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), v.x, v.z);
-            split(pack(x[8 * w + 2 * b + 1] * 0.0625f, x[8 * w + 2 * b + 5] * 0.0625f), v.y, v.w);
+            split(pack(x[8 * w + 2 * b + 1], x[8 * w + 2 * b + 5]), v.y, v.w);
             qs[(2 * w + b) * 32 + lane] = v;
           }
       }
@@ -244,12 +244,13 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       const bool some = key0 <= last_hi && key0 + 31 >= any_lo;
       const bool whole = key0 + 31 <= first_hi && key0 >= all_lo;  // no row hides a key
       const auto hidden = [&](int key, int last) { return key > last || last - key > back; };
-      // ---- scores of 32 keys, two tiles of 16.  A code masked out of its word is
-      // an fp16 below the normal range, q 2^-24 (or q 2^-20), exact in the product:
-      // no conversion; -8 sum(q) starts the sums.
+      // ---- scores of 32 keys, two tiles of 16, from centred codes.  (The bare codes,
+      // below fp16's normal range, would need no conversion and took 5% off the time
+      // at 65536 keys; but the tensor cores drop low bits of such products: the
+      // output was off by 4e-6 of its size, against 5e-7.)
       if (!mbar_wait(&full[slot], phase)) g_err_attention_q4 = 1u;
       __syncwarp();
-      f2 x[2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, times 2^-24
+      f2 x[2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, over the row's scale
       if (some) {
         const uint8_t* blk = smem + slot * S::half;
         float sc[2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
@@ -268,26 +269,27 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
             }
           }
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+        for (int w = 0; w < W; ++w) {
+          __half2 u[2][4], v[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) q4_unpack(kw[t][0][w], u[t]), q4_unpack(kw[t][1][w], v[t]);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const uint4 q4 = qs[(2 * w + b) * 32 + lane];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const uint32_t u = kw[t][0][w] >> (8 * b), v = kw[t][1][w] >> (8 * b);
-              const uint32_t a0 = u & 0x000F000Fu, a1 = v & 0x000F000Fu, a2 = u & 0x00F000F0u, a3 = v & 0x00F000F0u;
-              {
-                if (w == 0 && b == 0) {
-                  const float2 start = unpack(mul2(sum2, pack(-8.0f, -8.0f)));
-                  mma_from(sc[t][0], a0, a1, a2, a3, q4.x, q4.y, start.x, start.y);
-                  mma_from(sc[t][1], a0, a1, a2, a3, q4.z, q4.w, 0.0f, 0.0f);
-                } else {
-                  mma(sc[t][0], a0, a1, a2, a3, q4.x, q4.y);
-                  mma(sc[t][1], a0, a1, a2, a3, q4.z, q4.w);
-                }
+              const uint32_t a0 = bits(u[t][2 * b]), a1 = bits(v[t][2 * b]), a2 = bits(u[t][2 * b + 1]),
+                             a3 = bits(v[t][2 * b + 1]);
+              if (w == 0 && b == 0) {
+                mma_from(sc[t][0], a0, a1, a2, a3, q4.x, q4.y, 0.0f, 0.0f);
+                mma_from(sc[t][1], a0, a1, a2, a3, q4.z, q4.w, 0.0f, 0.0f);
+              } else {
+                mma(sc[t][0], a0, a1, a2, a3, q4.x, q4.y);
+                mma(sc[t][1], a0, a1, a2, a3, q4.z, q4.w);
               }
             }
           }
+        }
         // s = d acc + z sum(q)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -419,14 +421,16 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       if (tid == 0 && more) ask();
     }
 
-    // ---- the unit's end: warps 2 and 3 hand their rows to 0 and 1, then 1 to 0;
-    // a thread's rows and dimensions are the same in every warp
+    // ---- the unit's end.  A thread's rows and dimensions are the same in every
+    // warp: warps two apart swap halves of their tiles and add the ones they keep,
+    // then neighbours halves of those, so that warp w ends with the sums of the
+    // w-th quarter of the tiles.
 #pragma unroll
-      for (int s4 = 4; s4 < 32; s4 <<= 1) {
-        const float2 l = unpack(lsum), z = unpack(zsum);
-        lsum = add2(lsum, pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
-        zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
-      }
+    for (int s4 = 4; s4 < 32; s4 <<= 1) {
+      const float2 l = unpack(lsum), z = unpack(zsum);
+      lsum = add2(lsum, pack(__shfl_xor_sync(0xFFFFFFFFu, l.x, s4), __shfl_xor_sync(0xFFFFFFFFu, l.y, s4)));
+      zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
+    }
     {
       const float2 z = unpack(zsum);
 #pragma unroll
@@ -435,68 +439,72 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         o[t][2] += z.x, o[t][3] += z.y;
       }
     }
+    const bool mine = row0 + 2 * c < R;  // else the thread's rows are nobody's
+    // The region and statistics that a warp reads in the first round are the ones it
+    // writes in the second: nobody else reads them between.
+    const auto swap = [&](auto upper, auto tiles, int to, int from) {
+      constexpr int n = decltype(tiles)::value / 2, keep = decltype(upper)::value ? n : 0, give = n - keep;
+      float4* dst = join + to * (NT / 2 * 32) + lane;
+      if (mine) {
 #pragma unroll
-    for (int from = 2; from > 0; from >>= 1) {
-      if (warp >= from && warp < 2 * from) {
-        float4* dst = join + (warp - from) * (NT * 32) + lane;
-        {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) dst[t * 32] = make_float4(o[t][0], o[t][1], o[t][2], o[t][3]);
-          const float2 l = unpack(lsum);
-          if (g == 0) stat[(warp - from) * 4 + c] = make_float4(M0, M1, l.x, l.y);
-        }
-      }
-      __syncthreads();
-      if (warp < from) {
-        const float4* src = join + warp * (NT * 32) + lane;
-        {
-          const float4 b = stat[warp * 4 + c];
-          const float2 l = unpack(lsum);
-          const float t0 = fmaxf(M0, b.x), t1 = fmaxf(M1, b.y);
-          // no maximum: nothing was seen, or only NaN scores, which the sums carry
-          const float a0 = M0 == t0 ? 1.0f : ex2(M0 - t0), a1 = M1 == t1 ? 1.0f : ex2(M1 - t1);
-          const float b0 = b.x == t0 ? 1.0f : ex2(b.x - t0), b1 = b.y == t1 ? 1.0f : ex2(b.y - t1);
-          M0 = t0, M1 = t1;
-          lsum = pack(__fmaf_rn(b0, b.z, a0 * l.x), __fmaf_rn(b1, b.w, a1 * l.y));
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float4 v = src[t * 32];
-            o[t][0] = __fmaf_rn(b0, v.x, a0 * o[t][0]);
-            o[t][1] = __fmaf_rn(b1, v.y, a1 * o[t][1]);
-            o[t][2] = __fmaf_rn(b0, v.z, a0 * o[t][2]);
-            o[t][3] = __fmaf_rn(b1, v.w, a1 * o[t][3]);
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (warp == 0) {
-      {
+        for (int t = 0; t < n; ++t)
+          dst[t * 32] = make_float4(o[give + t][0], o[give + t][1], o[give + t][2], o[give + t][3]);
         const float2 l = unpack(lsum);
+        if (g == 0) stat[to * 4 + c] = make_float4(M0, M1, l.x, l.y);
+      }
+      __syncthreads();
+      if (mine) {
+        const float4* src = join + from * (NT / 2 * 32) + lane;
+        const float4 b = stat[from * 4 + c];
+        const float2 l = unpack(lsum);
+        const float t0 = fmaxf(M0, b.x), t1 = fmaxf(M1, b.y);
+        // no maximum: nothing was seen, or only NaN scores, which the sums carry
+        const float a0 = M0 == t0 ? 1.0f : ex2(M0 - t0), a1 = M1 == t1 ? 1.0f : ex2(M1 - t1);
+        const float b0 = b.x == t0 ? 1.0f : ex2(b.x - t0), b1 = b.y == t1 ? 1.0f : ex2(b.y - t1);
+        M0 = t0, M1 = t1;
+        lsum = pack(__fadd_rn(__fmul_rn(a0, l.x), __fmul_rn(b0, b.z)), __fadd_rn(__fmul_rn(a1, l.y), __fmul_rn(b1, b.w)));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = row0 + 2 * c + e;
-          if (r >= R) continue;
-          const int j = r / G;
-          const size_t row = (size_t)(cur->q.tok0 + j) * hq + cur->h * G + r - j * G;
-          const float le = e ? l.y : l.x;
-          if (cur->units == 1) {
-            float4* dst = reinterpret_cast<float4*>(out + row * D + g * (D / 8));
+        for (int t = 0; t < n; ++t) {
+          const float4 v = src[t * 32];
+          o[t][0] = __fmaf_rn(b0, v.x, a0 * o[keep + t][0]);
+          o[t][1] = __fmaf_rn(b1, v.y, a1 * o[keep + t][1]);
+          o[t][2] = __fmaf_rn(b0, v.z, a0 * o[keep + t][2]);
+          o[t][3] = __fmaf_rn(b1, v.w, a1 * o[keep + t][3]);
+        }
+      }
+    };
+    if (warp & 2)
+      swap(std::true_type{}, std::integral_constant<int, NT>{}, warp, warp ^ 2);
+    else
+      swap(std::false_type{}, std::integral_constant<int, NT>{}, warp, warp ^ 2);
+    const int units = cur->units, u = cur->u, tok0 = cur->q.tok0, head0 = cur->h * G;  // thread 0 moves on after the barrier
+    if (warp & 1)
+      swap(std::true_type{}, std::integral_constant<int, NT / 2>{}, warp ^ 2, warp ^ 3);
+    else
+      swap(std::false_type{}, std::integral_constant<int, NT / 2>{}, warp ^ 2, warp ^ 3);
+    {
+      constexpr int Q = NT / 4;  // tiles of this warp
+      const float2 l = unpack(lsum);
 #pragma unroll
-            for (int t = 0; t < NT; t += 2)
-              dst[t / 2] = make_float4(__fdiv_rn(o[t][e], le), __fdiv_rn(o[t][2 + e], le),
-                                       __fdiv_rn(o[t + 1][e], le), __fdiv_rn(o[t + 1][2 + e], le));
-          } else {
-            float* at = partials + (row * max_units + cur->u) * (D + 2);
-            float2* dst = reinterpret_cast<float2*>(at + 2 + g * (D / 8));
+      for (int e = 0; e < 2; ++e) {
+        const int r = row0 + 2 * c + e;
+        if (r >= R) continue;
+        const int j = r / G, dim = g * (D / 8) + warp * (2 * Q);
+        const size_t row = (size_t)(tok0 + j) * hq + head0 + r - j * G;
+        const float le = e ? l.y : l.x;
+        if (units == 1) {
+          float2* dst = reinterpret_cast<float2*>(out + row * D + dim);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) dst[t] = make_float2(o[t][e], o[t][2 + e]);
-            if (g == 0) *reinterpret_cast<float2*>(at) = make_float2(e ? M1 : M0, le);
-          }
+          for (int t = 0; t < Q; ++t) dst[t] = make_float2(__fdiv_rn(o[t][e], le), __fdiv_rn(o[t][2 + e], le));
+        } else {
+          float* at = partials + (row * max_units + u) * (D + 2);
+          float2* dst = reinterpret_cast<float2*>(at + 2 + dim);
+#pragma unroll
+          for (int t = 0; t < Q; ++t) dst[t] = make_float2(o[t][e], o[t][2 + e]);
+          if (warp == 0 && g == 0) *reinterpret_cast<float2*>(at) = make_float2(e ? M1 : M0, le);
         }
       }
     }
-    __syncwarp();
     if (tid == 0) {
       *done = cur->end() >= w1;
       if (!*done) cur->next<kRows>(meta, hkv, G);
@@ -623,8 +631,8 @@ cudaError_t merge_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) 
 template <int D>
 cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
   cudaError_t e;
-  if (a.tile_rows > kRows)
-    e = launch_attention_q4_tc(a, D, meta, st);
+  if (D == 128 && a.tile_rows > kRows)
+    e = launch_attention_q4_tc(a, meta, st);
   else
     e = meta.dev ? attention_go<D, 1>(a, meta, st) : attention_go<D, kParamWords>(a, meta, st);
   if (e != cudaSuccess || a.max_units == 1) return e;
@@ -635,14 +643,21 @@ cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_
 
 // Long units cost less joining, short ones fill the GPU with few sequences: the
 // sequence alone makes up to 1024 items (heads and row tiles included), of two or
-// four pages at least where it has many.  The tcgen05 kernel's units have more to
-// set up and to add up at their end.
+// four pages at least where it has many.  At most eight: the tensor cores' sums
+// drop the bits below their last, toward zero, and over units of 16 pages that
+// made the output of 65536 keys 1.1e-6 of its size off, over eight 0.9e-6 (210 and
+// 214 us).  The tcgen05 kernel's units, whose sums are float32's from page to page,
+// have more to set up and to add up at their end: up to 128 items, of at most 16
+// pages (one sequence of 32768 keys, 40 rows: 85 us with the 32 pages that makes,
+// 65 with 16).
 int q4_unit_pages(int n, int lanes, int tile_rows) {
-  const long long alone = tile_rows > 8 ? 128 : 1024;
+  const bool tc = tile_rows > 8;
+  const long long alone = tc ? 128 : 1024;
   if (n <= 2) return n;
-  const int least = tile_rows > 8 ? (n < 4 ? n : 4) : n <= 4 ? 1 : n <= 64 ? 2 : 4;
+  const int least = tc ? 4 : n <= 4 ? 1 : n <= 64 ? 2 : 4;  // tc: n is more than 16
+  const int most = tc ? 16 : n < 8 ? n : 8;
   const long long u = ((long long)n * lanes + alone - 1) / alone;
-  return u < least ? least : u > n ? n : (int)u;
+  return u < least ? least : u > most ? most : (int)u;
 }
 
 cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st) {

@@ -1,23 +1,21 @@
-// Decode attention over the paged 4-bit KV cache for more than 8 query rows on a
-// kv head (draft tokens, wide groups, prompts), on the 5th-generation tensor cores
+// Decode attention over the paged 4-bit KV cache for more than 16 query rows on a
+// kv head (draft tokens, wide groups, prompts) over long sequences, on the 5th-generation tensor cores
 // (sm_103a).  The mathematics is that of attention_q4.cu; what differs is who
 // multiplies.  With many rows the warp-level products there unpack every code
 // once for each 8 rows and are bound by instruction issue and the warp-level
-// tensor pipe; here a page is unpacked once for up to 32 rows and two MMAs of
+// tensor pipe; here a page is unpacked once for up to 24 rows and two MMAs of
 // 128 x N x 128 do the rest, N = 2 rows (hi and lo parts of q, and of the weights,
 // as columns of their own).
 //
 // A CTA of 256 threads, two for each key (K, softmax) and each dimension (output),
 // which share out the dimensions of K, the keys of V and the rows of the softmax:
 //   K codes   the threads' row of 64 bytes becomes 64 columns of tensor memory
-//             (A operand): a code masked out of its word is an fp16 below the
-//             normal range, exact in the product; 8 columns more hold a constant
-//             that brings in -8 sum(q) first, so that the sums stay small
+//             (A operand), (c - 8) as fp16
 //   S^T       128 keys x N in tensor memory: thread k reads its key's scores of
 //             half of the rows, applies the key's numbers and the row's reference,
 //             and writes the weights' hi and lo parts as B operand of the second
 //             product
-//   V codes   (c - 8) as fp16 into shared memory, K-major, eight keys a store
+//   V codes   likewise into shared memory, K-major, eight keys a store
 //   O^T       D dimensions x N of one page in tensor memory, then added to float32
 //             registers: the tensor core's sums round toward zero, which would tell
 //             over a unit's pages
@@ -35,6 +33,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "attention_q4.cuh"
 #include "dsb_kernels.h"
@@ -45,6 +44,9 @@ namespace dsbk {
 
 namespace {
 
+constexpr int D = 128;    // head dimension
+constexpr int ROWS = 24;  // query rows of an item
+using B = Q4Block<D>;
 constexpr int kWorkers = 256;
 constexpr int kThreads = kWorkers + 32;  // and a warp that asks for the pages and issues the products
 constexpr int kRing = 3;  // half pages asked for at a time
@@ -123,15 +125,12 @@ __device__ __forceinline__ void st_b16(uint32_t at, uint32_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
 }
 
-template <int D, int ROWS>
 struct TcSmem {
-  using B = Q4Block<D>;
   static constexpr int NT = 2 * ROWS;                     // columns at most: hi and lo
   static constexpr int v_k = D / 8 * 144;                 // V: core matrices along the keys, and along the dimensions
   static constexpr int v_m = 144;
   static constexpr int p_k = 144, p_n = 16 * 144;         // weights: along the keys, along the rows
-  static constexpr int q_k = 128, q_n = (D / 8 + 2) * 128;  // q: along the dimensions (16 more, see -8 sum(q)), the rows
-  // the product reads 128 rows of V also where D is 64: what follows them
+  static constexpr int q_k = 128, q_n = D / 8 * 128;        // q: along the dimensions, the rows
   static constexpr int v = 0, v_bytes = 15 * v_k + 16 * v_m;
   static constexpr int p = v + v_bytes, p_bytes = NT / 8 * p_n;
   static constexpr int q = p + p_bytes, q_bytes = NT / 8 * q_n;
@@ -147,8 +146,8 @@ struct TcSmem {
   static constexpr int base = bars + (kRing + 4) * 8;     // tensor memory's address
   static constexpr int cursors = base + 8;
   static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
-  static constexpr int a_col = 0, c_col = D / 2, s_col = c_col + 8, o_col = s_col + NT;
-  static constexpr int cols = o_col + NT <= 128 ? 128 : 256;  // a power of two; two CTAs an SM
+  static constexpr int a_col = 0, s_col = D / 2, o_col = s_col + NT;
+  static constexpr int cols = 256;  // a power of two; two CTAs an SM
   static_assert(o_col + NT <= 256, "tensor memory");
   static_assert(v_bytes % 16 == 0 && raw % 128 == 0 && p % 16 == 0 && q % 16 == 0, "operand alignment");
 };
@@ -157,7 +156,7 @@ struct TcSmem {
 // and the lanes that share one.  Lane i ends with value i COUNT / 32.
 template <int COUNT>
 __device__ __forceinline__ float lane_sums(float (&v)[COUNT], int lane) {
-  constexpr int STEPS = COUNT == 16 ? 4 : 3;
+  constexpr int STEPS = 4;
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int mask = 16 >> s, n = COUNT >> (s + 1);
@@ -173,13 +172,12 @@ __device__ __forceinline__ float lane_sums(float (&v)[COUNT], int lane) {
   return v[0];
 }
 
-template <int D, int ROWS, int N>
+template <int N>
 __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
     const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint8_t* __restrict__ pool, int n_seq,
     float scale_log2e, int max_units, float* __restrict__ partials, float* __restrict__ out,
     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
-  using B = Q4Block<D>;
-  using S = TcSmem<D, ROWS>;
+  using S = TcSmem;
   extern __shared__ __align__(128) uint8_t smem[];
   float4* pairs = reinterpret_cast<float4*>(smem + S::pairs);
   float* minus = reinterpret_cast<float*>(smem + S::minus);
@@ -216,11 +214,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
   __syncthreads();
   fence_after();
   const uint32_t tm = *base, mine = tm + ((uint32_t)(32 * quarter) << 16);
-  if (part == 0 && warp < 8) {  // 2^-14 three times, against the three parts of -8 sum(q) 2^-10
-    const uint32_t c[8] = {0x04000400u, 0x00000400u, 0, 0, 0, 0, 0, 0};
-    tm_st8(mine + S::c_col, c);
-    tm_st_wait();
-  }
   pdl_wait();
   pdl_trigger();
 
@@ -259,10 +252,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       for (int n = 0; more || 2 * n < asked; ++n) {
         if (!mbar_wait(keys, n & 1)) g_err_attention_q4_tc = 1u;
         fence_after();
-        mma_ta(tm + S::s_col, tm + S::c_col, qd + (uint64_t)(D / 8 * S::q_k >> 4), id, 0);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ta(tm + S::s_col, tm + S::a_col + 8 * k, qd + (uint64_t)(k * (2 * S::q_k >> 4)), id, 1);
+          mma_ta(tm + S::s_col, tm + S::a_col + 8 * k, qd + (uint64_t)(k * (2 * S::q_k >> 4)), id, k > 0);
         commit(scores);
         if (more) ask();
         if (!mbar_wait(weights, n & 1)) g_err_attention_q4_tc = 1u;
@@ -307,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
         for (int k = 0; k < D / 8; ++k) m = fmaxf(m, fabsf(x[k]));
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const int e = min(max((int)(__float_as_uint(m) >> 23), 10), 240);
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 240);
         const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
         float sum = 0.0f;
 #pragma unroll
@@ -321,33 +313,20 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
         uint8_t* lo = hi + ROWS / 8 * S::q_n;
         if (c == 0) {
           float* to = reinterpret_cast<float*>(&pairs[i >> 1]) + (i & 1);
-          to[0] = __uint_as_float((uint32_t)(e + 14) << 23);  // 2^-10 of that, 2^24 of the codes
-          to[2] = sum * 0x1p-24f;
+          to[0] = __uint_as_float((uint32_t)(e - 10) << 23);
+          to[2] = sum;
           last[i] = live ? len - n_new + j : len - 1;
           where[i] = (cur->q.tok0 + j) * hq + cur->h * G + gi;
-          {
-            const float v = sum * -0x1p-7f;
-            const __half a = __float2half_rn(v), b = __float2half_rn(v - __half2float(a));
-            const __half d = __float2half_rn(v - __half2float(a) - __half2float(b));
-            uint4 w = make_uint4((uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16,
-                                 (uint32_t)__half_as_ushort(d), 0, 0);
-            *reinterpret_cast<uint4*>(hi + D / 8 * S::q_k) = w;
-            w = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(hi + (D / 8 + 1) * S::q_k) = w;
-            *reinterpret_cast<uint4*>(lo + D / 8 * S::q_k) = w;
-            *reinterpret_cast<uint4*>(lo + (D / 8 + 1) * S::q_k) = w;
-          }
         }
         {
-          // eight dimensions in the order of their nibbles, (0, 4), (1, 5), ..; the odd
-          // ones stand 16 times as high in their word
+          // eight dimensions in the order of their nibbles, (0, 4), (1, 5), ..
 #pragma unroll
           for (int w = 0; w < D / 64; ++w) {
             uint4 a, b;
             split(pack(x[8 * w], x[8 * w + 4]), a.x, b.x);
-            split(pack(x[8 * w + 1] * 0.0625f, x[8 * w + 5] * 0.0625f), a.y, b.y);
+            split(pack(x[8 * w + 1], x[8 * w + 5]), a.y, b.y);
             split(pack(x[8 * w + 2], x[8 * w + 6]), a.z, b.z);
-            split(pack(x[8 * w + 3] * 0.0625f, x[8 * w + 7] * 0.0625f), a.w, b.w);
+            split(pack(x[8 * w + 3], x[8 * w + 7]), a.w, b.w);
             *reinterpret_cast<uint4*>(hi + (c * (D / 64) + w) * S::q_k) = a;
             *reinterpret_cast<uint4*>(lo + (c * (D / 64) + w) * S::q_k) = b;
           }
@@ -395,18 +374,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       f2 kd, kz;
       {
         const uint8_t* raw = smem + S::raw + slot * B::v;
-        constexpr int NP = D / 64;  // 16-byte pieces
+        constexpr int NP = 2;  // 16-byte pieces
         uint4 w[NP];
-        // two pieces in an order that turns with the lane (so that rows hit other banks), put right by selects
-        const int turn = NP == 2 ? (lane >> 1) & 1 : 0;
+        // in an order that turns with the lane (so that rows hit other banks), put right by selects
+        const int turn = (lane >> 1) & 1;
 #pragma unroll
         for (int k = 0; k < NP; ++k)
           w[k] = *reinterpret_cast<const uint4*>(raw + at * (D / 2) + part * (D / 4) + (k ^ turn) * 16);
-        if constexpr (NP == 2) {
-          const uint4 a = w[0], b = w[1];
-          w[0] = turn ? b : a;
-          w[1] = turn ? a : b;
-        }
+        const uint4 first_w = w[0], second_w = w[1];
+        w[0] = turn ? second_w : first_w;
+        w[1] = turn ? first_w : second_w;
         const float2 dz = __half22float2(*reinterpret_cast<const __half2*>(raw + B::kz + at * 4));
         kd = pack(dz.x, dz.x);
         kz = pack(dz.y, dz.y);
@@ -416,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
           const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            c[4 * i] = v[i] & 0x000F000Fu;
-            c[4 * i + 1] = v[i] & 0x00F000F0u;
-            c[4 * i + 2] = (v[i] >> 8) & 0x000F000Fu;
-            c[4 * i + 3] = (v[i] >> 8) & 0x00F000F0u;
+            __half2 h[4];
+            q4_unpack(v[i], h);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) c[4 * i + n] = *reinterpret_cast<const uint32_t*>(&h[n]);
           }
           tm_st16(mine + S::a_col + 16 * (NP * part + k), c);
         }
@@ -438,17 +415,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       float vd, vz;
       {
         const uint8_t* raw = smem + S::raw + slot * B::v;
-        constexpr int WORDS = D / 4;             // words of a key pair
-        constexpr int AT_ONCE = 32 / WORDS;      // groups of eight keys a warp takes at once
-        const int i = lane % WORDS;
 #pragma unroll
-        for (int it = 0; it < 2 / AT_ONCE; ++it) {
-          const int kg = (warp + 8 * it) * AT_ONCE + lane / WORDS;
+        for (int it = 0; it < 2; ++it) {  // word `lane` of the key pairs of eight keys
+          const int kg = warp + 8 * it;
           __half2 h[4][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            q4_unpack(*reinterpret_cast<const uint32_t*>(raw + (4 * kg + j) * D + 4 * i), h[j]);
-          uint8_t* dst = smem + S::v + kg * S::v_k + (i >> 1) * S::v_m + (i & 1) * 64;
+            q4_unpack(*reinterpret_cast<const uint32_t*>(raw + (4 * kg + j) * D + 4 * lane), h[j]);
+          uint8_t* dst = smem + S::v + kg * S::v_k + (lane >> 1) * S::v_m + (lane & 1) * 64;
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             uint4 v;
@@ -474,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
         const int l = last[row];
         return key > l || l - key > back;
       };
-      // s of this thread's rows (times 2^-24 over the row's scale), and then p
+      // s of this thread's rows over the row's scale, then p
       f2 x[PAIRS], p[PAIRS];
       {
         float hi[ROWS / 8][4], lo[ROWS / 8][4];
@@ -542,18 +516,19 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
             }
           }
         }
-        // weights of this key into the second product's operand
+        // weights of this key into the second product's operand; pages that every row
+        // sees whole take a path of their own, free of the masks' predicates
         float most = -INFINITY;
+        const auto weigh = [&](auto all) {
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-          const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
-          {
+          for (int i = 0; i < PAIRS; ++i) {
+            const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
             const float4 pr = pairs[row / 2];
             const float2 mm = *reinterpret_cast<const float2*>(&minus[row]);
             const float2 a = unpack(fma2(pack(pr.x, pr.y), x[i], pack(mm.x, mm.y)));
             float2 w = make_float2(ex2(a.x), ex2(a.y));
             f2 d = vd2;
-            if (whole) {
+            if constexpr (decltype(all)::value) {
               most = fmaxf(most, fmaxf(a.x, a.y));
             } else {  // a hidden key's numbers may be anything
               const bool no0 = hidden(row), no1 = hidden(row + 1);
@@ -575,7 +550,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
             st_b16(p_lo + to, lb);
             st_b16(p_lo + to + 16, lb >> 16);
           }
-        }
+        };
+        if (whole)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
         fence_proxy_async_smem();  // V and the weights precede the product
         fence_before();
         if (!meet_or(pass == 0 && !first && most > limit)) break;
@@ -583,21 +562,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       if (tid == 0) arrive(weights);
       multiplied = true;
       if (++slot == kRing) slot = 0, phase ^= 1;
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) {
-        const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
-        {
-          lsum[i] = add2(lsum[i], p[i]);
-          const f2 z = whole ? pack(vz, vz) : pack(hidden(row) ? 0.0f : vz, hidden(row + 1) ? 0.0f : vz);
-          zsum[i] = fma2(p[i], z, zsum[i]);
+        for (int i = 0; i < PAIRS; ++i) zsum[i] = fma2(p[i], pack(vz, vz), zsum[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
+          zsum[i] = fma2(p[i], pack(hidden(row) ? 0.0f : vz, hidden(row + 1) ? 0.0f : vz), zsum[i]);
         }
       }
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) lsum[i] = add2(lsum[i], p[i]);
     }
 
     // ---- the unit's end: sums over the keys, then the output by dimension
     drain();
     {
-      constexpr int COUNT = ROWS == 16 ? 8 : 16;
+      constexpr int COUNT = 16;  // two for each pair, rounded up to a power of two
       float l[COUNT], z[COUNT];
 #pragma unroll
       for (int i = 0; i < COUNT / 2; ++i) {
@@ -614,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       }
     }
     meet();
-    if (at < D) {
+    {
       const int units = cur->units, u = cur->u;
 #pragma unroll
       for (int i = 0; i < 2 * PAIRS; ++i) {
@@ -648,11 +630,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
   }
 }
 
-template <int D, int ROWS, int N>
+template <int N>
 cudaError_t tc_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  constexpr int smem = TcSmem<D, ROWS>::bytes;
+  constexpr int smem = TcSmem::bytes;
   static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
-  auto kern = attention_q4_tc_kernel<D, ROWS, N>;
+  auto kern = attention_q4_tc_kernel<N>;
   int resident = 0;
   {
     static std::mutex mu;
@@ -678,17 +660,10 @@ cudaError_t tc_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
                        a.max_units, a.partials, a.out, w, meta.dev);
 }
 
-template <int D, int ROWS>
-cudaError_t tc_meta(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  return meta.dev ? tc_go<D, ROWS, 1>(a, meta, st) : tc_go<D, ROWS, kParamWords>(a, meta, st);
-}
-
 }  // namespace
 
-cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st) {
-  if (head_dim == 128)
-    return a.tile_rows == 16 ? tc_meta<128, 16>(a, meta, st) : tc_meta<128, 24>(a, meta, st);
-  return a.tile_rows == 16 ? tc_meta<64, 16>(a, meta, st) : tc_meta<64, 24>(a, meta, st);
+cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
+  return meta.dev ? tc_go<1>(a, meta, st) : tc_go<kParamWords>(a, meta, st);
 }
 
 unsigned int read_clear_error_attention_q4_tc() {

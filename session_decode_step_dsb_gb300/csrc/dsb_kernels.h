@@ -259,13 +259,17 @@ struct Q4Seq {
   int32_t work_off, tok0, n_new, len, window, chunk0, pg_at, u_pages;
 };
 constexpr int kQ4SeqWords = 8;
-// Query rows of an item of a sequence with `rows` of them on a kv head: a rule on
-// the sequence alone, as the one on its units.  Up to 8 the warp-level kernel
-// (attention_q4.cu), more the tcgen05 one (attention_q4_tc.cu).
-inline int q4_tile_rows(long long rows) {
-  if (rows <= 8) return 8;
-  const long long tiles = (rows + 23) / 24;
-  return (rows + tiles - 1) / tiles <= 16 ? 16 : 24;
+// Query rows of an item of a sequence with `rows` of them on a kv head and n pages to
+// visit: a rule on the sequence alone, as the one on its units.  8: the warp-level
+// kernel (attention_q4.cu); 24: the tcgen05 one (attention_q4_tc.cu), whose items
+// unpack a page once for three times the rows but take longer to start and to end.
+// Measured at 8 kv heads of 128, warp-level and tcgen05: one sequence of 2048 keys and
+// 64 rows 19 and 24 us; 8 sequences of 4096 to 16384 keys, 16 rows 82 and 82 us, 24 rows
+// 117 and 98, 40 rows 177 and 161, 64 rows 255 and 237.  At heads of 64 (12 kv heads),
+// where a page holds half the work, the tcgen05 kernel took longer for all of them
+// (same sequences, 24 rows 120 and 122 us, 40 rows 187 and 207) and is not built.
+inline int q4_tile_rows(long long rows, int n, int head_dim) {
+  return head_dim == 128 && rows > 16 && n > 16 ? 24 : 8;
 }
 // Pages per unit of a sequence that visits n of them, with `lanes` pairs of a kv
 // head and a tile of tile_rows rows: a rule on the sequence alone, not on the batch.
@@ -285,7 +289,7 @@ struct Q4AttnArgs {
 cudaError_t launch_attention_q4(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st);
 unsigned int read_clear_error_attention_q4();
 // Its kernel for tiles of more than 8 rows, without the joining of the units.
-cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, int head_dim, const MetaArg& meta, cudaStream_t st);
+cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st);
 unsigned int read_clear_error_attention_q4_tc();
 
 // One sequence of a read-back; n_seq of them, then the total page count, then

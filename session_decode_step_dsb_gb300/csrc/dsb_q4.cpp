@@ -399,13 +399,13 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     size_t most = 0, need = 0;
     for (const Group& g : groups) {
       int tok1 = tok0;
-      for (const int rows : {8, 16, 24}) {
+      for (const int rows : {8, 24}) {
         Plan p;
         std::vector<int32_t> list;
         p.tok0 = tok0;
         p.tile_rows = rows;
         auto mine = [&](int s) {
-          return b->new_tokens[s] > 0 && dsbk::q4_tile_rows((long long)G * b->new_tokens[s]) == rows;
+          return b->new_tokens[s] > 0 && dsbk::q4_tile_rows((long long)G * b->new_tokens[s], pages(s), D) == rows;
         };
         for (int s = g.s0; s < g.s1; ++s) p.live += mine(s);
         int tok = 0;

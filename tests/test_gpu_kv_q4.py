@@ -269,7 +269,10 @@ ATTN = [  # D, hq, hkv, lens, new, window
     (64, 16, 2, [300], [130], [0]),                       # a prompt: 1040 rows
     (128, 16, 1, [1, 127, 128, 700], [1, 1, 1, 1], [0, 0, 60, 300]),    # 16 rows
     (128, 10, 2, [400, 8, 1500, 513], [8, 8, 1, 2], [0, 0, 0, 333]),     # 40, 5 and 10 rows in one call
-    (64, 9, 1, [1000, 260], [1, 3], [129, 0])]            # 9 and 27 rows
+    (64, 9, 1, [1000, 260], [1, 3], [129, 0]),            # 9 and 27 rows
+    (128, 20, 2, [2300, 40, 2177, 2500, 0], [2, 2, 3, 1, 0], [0, 0, 2100, 0, 0]),   # 20 and 30 rows on long caches, 20 on a short
+    (128, 40, 1, [4100, 2500], [2, 1], [0, 0]),           # 80 and 40 rows
+    (128, 2, 2, [3000, 2049], [49, 17], [2200, 0])]       # 49 rows in a window; the shortest of the kind, 17 rows
 
 
 @pytest.mark.parametrize("case", ATTN)
@@ -321,6 +324,34 @@ def test_attention_q4_at_odd_sizes_of_values(cuda_device, vsize, qsize):
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("hq,T,L", [(4, 1, 3000), (10, 4, 700), (2, 8, 200), (10, 4, 2200)])
+def test_attention_q4_as_exact_as_float32(cuda_device, hq, T, L):
+    """Vectors with a few wide dimensions, as a trained model's.  Every operand and
+    sum of the kernel keeps 22 bits or more, so its error may be twice that of a
+    float32 evaluation with numpy's blocked sums, and 2^-22 for the split."""
+    d = _dsb()
+    rng = np.random.default_rng(hq + T)
+    D, n_pages = 128, -(-L // P)
+    wide = np.where(rng.random((2, D)) < 0.05, 7.0, 1.0)
+    pool = np.stack([oq4.pack_block(*oq4.quantise(rng.standard_normal((P, D)) * wide[0]),
+                                    *oq4.quantise(rng.standard_normal((P, D)) * wide[1])) for _ in range(n_pages)])[:, None]
+    q = (rng.standard_normal((T, hq, D)) * wide[0]).astype(np.float32)
+    kvals, vvals = oq4.pool_values(pool, D)
+    bt = np.arange(n_pages)[None]
+    want, _ = oq4.attention(q, kvals, vvals, bt, [n_pages], [0], [T], [L], oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D),
+                                        d.PagedBatch(bt, [n_pages], [0], [T], [L]), d.Workspace(T, hq, D, L)))
+    k32, v32 = (np.asarray(x).reshape(-1, D).astype(np.float32)[:L] for x in (kvals, vvals))
+    plain = np.empty_like(q)
+    for j in range(T):
+        seen = L - T + j + 1
+        s = (q[j] @ k32[:seen].T) * np.float32(D ** -0.5)
+        w = np.exp(s - s.max(-1, keepdims=True))
+        plain[j] = (w @ v32[:seen]) / w.sum(-1, keepdims=True)
+    size = np.linalg.norm(want)
+    assert np.linalg.norm(got - want) <= 2 * np.linalg.norm(plain - want) + 2.0 ** -22 * size
+
+
 def test_attention_q4_scales_far_apart(cuda_device):
     """The keys that carry the weight have values 2^-13 of the others': the
     reference is kept over weight times scale, so they lose no bits."""
@@ -340,25 +371,27 @@ def test_attention_q4_scales_far_apart(cuda_device):
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("pages", [9, 19])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("hq,T", [(2, 2), (12, 1), (6, 5)])
-def test_attention_q4_references_move(cuda_device, D, hq, T):
+def test_attention_q4_references_move(cuda_device, D, hq, T, pages):
     """Keys that grow from page to page: each page's largest weight is far above
     the last one's, for all rows or for some (rows of the other sign shrink)."""
     d = _dsb()
     rng = np.random.default_rng(13)
-    pool = np.empty((9, 1, P * (D + 8)), np.uint8)
-    for p in range(9):
+    pool = np.empty((pages, 1, P * (D + 8)), np.uint8)
+    for p in range(pages):
         k = rng.standard_normal((P, D)) * 0.1
         k[:, 0] += 4.0 * p
         pool[p, 0] = oq4.pack_block(*oq4.quantise(k), *oq4.quantise(rng.standard_normal((P, D)) * 2.0 ** (p % 3)))
     q = rng.standard_normal((T, hq, D)).astype(np.float32) * 0.2
     q[..., 0] = np.sqrt(D) * np.where(rng.random((T, hq)) < 0.5, 3.5, -1.0)
-    bt = [list(range(9))]
+    L = pages * P - 52
+    bt = [list(range(pages))]
     kvals, vvals = oq4.pool_values(pool, D)
-    want, bound = oq4.attention(q, kvals, vvals, bt, [9], [0], [T], [1100], oq4.pool_sizes(pool, D))
-    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [9], [0], [T], [1100]),
-                                        d.Workspace(T, hq, D, 1152)))
+    want, bound = oq4.attention(q, kvals, vvals, bt, [pages], [0], [T], [L], oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [pages], [0], [T], [L]),
+                                        d.Workspace(T, hq, D, pages * P)))
     assert (np.abs(got - want) <= bound).all()
 
 
