@@ -653,7 +653,7 @@ cudaError_t tc_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
     }
   }
   ParamWords<N> w;
-  for (int i = 0; i < N; ++i) w.w[i] = N > 1 && i < meta.n_words ? meta.host[i] : 0;
+  fill_words(meta, &w);
   const unsigned grid = (unsigned)(a.items < resident ? a.items : resident);
   return launch_kernel(kern, dim3(grid), dim3(kThreads), smem, st, a.q, a.q_stride, a.hq, a.hkv,
                        static_cast<const uint8_t*>(a.pool), a.n_seq, (float)(1.4426950408889634 / sqrt((double)D)),

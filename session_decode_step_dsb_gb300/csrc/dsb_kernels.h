@@ -5,6 +5,10 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
+#include <memory>
+#include <tuple>
+#include <type_traits>
 
 namespace dsbk {
 
@@ -21,9 +25,14 @@ bool dry_run();
 void set_pdl(bool on);
 bool pdl();
 
+// An argument of a launch: itself where it has the parameter's type (some
+// parameters are 16 KB and are not to be copied on the way), else converted.
+template <typename K, typename A>
+using LaunchArg = std::conditional_t<std::is_same_v<K, A>, const K&, const K>;
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                 Args... args) {
+                                 const Args&... args) {
   if (dry_run()) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -37,7 +46,13 @@ inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  const std::tuple<LaunchArg<KArgs, Args>...> held(static_cast<LaunchArg<KArgs, Args>>(args)...);
+  return std::apply(
+      [&](const auto&... a) {
+        void* at[] = {const_cast<void*>(static_cast<const void*>(std::addressof(a)))...};
+        return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), at);
+      },
+      held);
 }
 
 // Per-call metadata staged in device memory (workspace), int32 words:
@@ -218,6 +233,11 @@ struct MetaArg {
   const int32_t* host = nullptr;  // words for the parameters
   int n_words = 0;
 };
+// The words behind the last are never read.
+template <int N>
+inline void fill_words(const MetaArg& m, ParamWords<N>* out) {
+  if (N > 1) std::memcpy(out->w, m.host, (size_t)m.n_words * sizeof(int32_t));
+}
 
 // Rotation of the first rd dimensions of a head: turns per position of each
 // pair as 64-bit fractions of a turn, the pair layout, the factor on the result.

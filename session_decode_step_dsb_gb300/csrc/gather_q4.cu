@@ -18,6 +18,7 @@ namespace dsbk {
 namespace {
 
 constexpr int kGatherThreads = 256;
+constexpr unsigned kGatherPages = 32768;  // in one plane of the grid
 
 template <typename T>
 __device__ __forceinline__ uint32_t two16(float a, float b);
@@ -44,6 +45,7 @@ __device__ __forceinline__ uint4 eight(uint32_t w, float2 dz) {
 
 template <int D, typename T, int N>
 __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(const uint8_t* __restrict__ pool, int hkv, int n_seq,
+                                                                   int pages,
                                                                    T* __restrict__ k, T* __restrict__ v,
                                                                    const __grid_constant__ ParamWords<N> words,
                                                                    const int32_t* __restrict__ meta_dev) {
@@ -51,7 +53,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(const uint8_t
   pdl_wait();
   pdl_trigger();
   const int32_t* meta = N > 1 ? words.w : meta_dev;
-  const int item = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+  const int item = (int)(blockIdx.z * kGatherPages + blockIdx.y), g = blockIdx.x, tid = threadIdx.x;
+  if (item >= pages) return;
   int lo = 0, hi = n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -70,47 +73,61 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(const uint8_t
   const size_t stride = (size_t)hkv * D;
   const long long base = (long long)sp[3] + key0 - first;
   constexpr int W = D / 8;  // words of a K row, and of a V row
-#pragma unroll 4
-  for (int e = tid; e < kQ4Page * W; e += kGatherThreads) {
-    const int r = e / W, w = e % W;
+  // everything is on its way before the first value is stored
+  constexpr int NK = kQ4Page * W / kGatherThreads, NV = NK / 2;
+  uint32_t kc[NK];
+  uint2 vc[NV], vdz[NV];
+  __half2 kdz[NK];
+#pragma unroll
+  for (int n = 0; n < NK; ++n) {
+    const int e = tid + n * kGatherThreads, r = e / W;
     if (r >= r0 && r < r1) {
-      const float2 dz = __half22float2(__ldg(reinterpret_cast<const __half2*>(blk + B::kz) + r));
-      const uint32_t c = __ldcg(reinterpret_cast<const uint32_t*>(blk) + e);
-      *reinterpret_cast<uint4*>(k + (size_t)(base + r) * stride + (size_t)g * D + 8 * w) = eight<T>(c, dz);
+      kc[n] = __ldcg(reinterpret_cast<const uint32_t*>(blk) + e);
+      kdz[n] = __ldg(reinterpret_cast<const __half2*>(blk + B::kz) + r);
     }
   }
-#pragma unroll 4
-  for (int e = tid; e < kQ4Page / 2 * W; e += kGatherThreads) {  // eight dimensions of a key pair
-    const int r = e / W * 2, w = e % W;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {  // eight dimensions of a key pair
+    const int e = tid + n * kGatherThreads, r = e / W * 2;
     if (r + 1 >= r0 && r < r1) {
-      const float4 dz = [&] {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(blk + B::vz) + (r >> 1));
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-        return make_float4(a.x, a.y, b.x, b.y);
-      }();
-      const uint2 c = __ldcg(reinterpret_cast<const uint2*>(blk + B::v) + e);
-      T* dst = v + (size_t)(base + r) * stride + (size_t)g * D + 8 * w;
-      if (r >= r0)
-        *reinterpret_cast<uint4*>(dst) = eight<T>(__byte_perm(c.x, c.y, 0x5410), make_float2(dz.x, dz.y));
-      if (r + 1 >= r0 && r + 1 < r1)
-        *reinterpret_cast<uint4*>(dst + stride) = eight<T>(__byte_perm(c.x, c.y, 0x7632), make_float2(dz.z, dz.w));
+      vc[n] = __ldcg(reinterpret_cast<const uint2*>(blk + B::v) + e);
+      vdz[n] = __ldg(reinterpret_cast<const uint2*>(blk + B::vz) + (r >> 1));
     }
+  }
+#pragma unroll
+  for (int n = 0; n < NK; ++n) {
+    const int e = tid + n * kGatherThreads, r = e / W, w = e % W;
+    if (r >= r0 && r < r1)
+      *reinterpret_cast<uint4*>(k + (size_t)(base + r) * stride + (size_t)g * D + 8 * w) =
+          eight<T>(kc[n], __half22float2(kdz[n]));
+  }
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int e = tid + n * kGatherThreads, r = e / W * 2, w = e % W;
+    T* dst = v + (size_t)(base + r) * stride + (size_t)g * D + 8 * w;
+    if (r >= r0 && r < r1)
+      *reinterpret_cast<uint4*>(dst) = eight<T>(__byte_perm(vc[n].x, vc[n].y, 0x5410),
+                                                __half22float2(*reinterpret_cast<const __half2*>(&vdz[n].x)));
+    if (r + 1 >= r0 && r + 1 < r1)
+      *reinterpret_cast<uint4*>(dst + stride) = eight<T>(__byte_perm(vc[n].x, vc[n].y, 0x7632),
+                                                         __half22float2(*reinterpret_cast<const __half2*>(&vdz[n].y)));
   }
 }
 
 template <int D, typename T>
 cudaError_t gather_go(const void* pool, int hkv, int n_seq, long long pages, void* k, void* v, const MetaArg& meta,
                       cudaStream_t st) {
-  const dim3 grid((unsigned)pages, (unsigned)hkv);
+  // the heads of a page side by side: together they write whole rows of the output
+  const dim3 grid((unsigned)hkv, (unsigned)(pages < kGatherPages ? pages : kGatherPages),
+                  (unsigned)((pages + kGatherPages - 1) / kGatherPages));
   if (meta.dev)
     return launch_kernel(gather_q4_kernel<D, T, 1>, grid, dim3(kGatherThreads), 0, st,
-                         static_cast<const uint8_t*>(pool), hkv, n_seq, static_cast<T*>(k), static_cast<T*>(v),
+                         static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k), static_cast<T*>(v),
                          ParamWords<1>{}, meta.dev);
   ParamWords<kParamWords> w;
-  for (int i = 0; i < kParamWords; ++i) w.w[i] = i < meta.n_words ? meta.host[i] : 0;
+  fill_words(meta, &w);
   return launch_kernel(gather_q4_kernel<D, T, kParamWords>, grid, dim3(kGatherThreads), 0, st,
-                       static_cast<const uint8_t*>(pool), hkv, n_seq, static_cast<T*>(k), static_cast<T*>(v), w,
+                       static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k), static_cast<T*>(v), w,
                        meta.dev);
 }
 

@@ -482,11 +482,6 @@ void fill_turns(const RotaryTable& rot, Turns<NP>* out) {
   out->interleaved = rot.interleaved;
 }
 
-template <int N>
-void fill_words(const MetaArg& m, ParamWords<N>* out) {
-  for (int i = 0; i < N; ++i) out->w[i] = N > 1 && i < m.n_words ? m.host[i] : 0;
-}
-
 template <int NP, bool VEC, int N>
 cudaError_t rope_go(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim, int n_tok,
                     const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st) {
