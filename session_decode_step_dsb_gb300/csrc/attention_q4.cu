@@ -634,9 +634,9 @@ cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_
   if (D == 128 && a.tile_rows > kRows)
     e = launch_attention_q4_tc(a, meta, st);
   else
-    e = meta.dev ? attention_go<D, 1>(a, meta, st) : attention_go<D, kParamWords>(a, meta, st);
+    e = with_words(meta, [&](auto n) { return attention_go<D, decltype(n)::value>(a, meta, st); });
   if (e != cudaSuccess || a.max_units == 1) return e;
-  return meta.dev ? merge_go<D, 1>(a, meta, st) : merge_go<D, kParamWords>(a, meta, st);
+  return with_words(meta, [&](auto n) { return merge_go<D, decltype(n)::value>(a, meta, st); });
 }
 
 }  // namespace

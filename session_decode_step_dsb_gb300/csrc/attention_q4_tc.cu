@@ -663,7 +663,7 @@ cudaError_t tc_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  return meta.dev ? tc_go<1>(a, meta, st) : tc_go<kParamWords>(a, meta, st);
+  return with_words(meta, [&](auto n) { return tc_go<decltype(n)::value>(a, meta, st); });
 }
 
 unsigned int read_clear_error_attention_q4_tc() {

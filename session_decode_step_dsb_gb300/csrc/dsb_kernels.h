@@ -221,9 +221,11 @@ unsigned int read_clear_error_attention();
 
 // A call's metadata words: up to kParamWords of them (16 KB) ride in the kernel's
 // parameters (no copy, and a captured launch keeps its own), more are staged in
-// device memory.  Measured against 960: small calls the same, 64 sequences of up to
-// 1500 keys (1100 words, staged before) 74 -> 43 us a pass.  Kernels take both forms; ParamWords<1> means the staged one.
-constexpr int kParamWords = 4032;
+// device memory.  Measured against at most 960 in the parameters: 64 sequences of up
+// to 1500 keys (1100 words, staged before) 74 -> 43 us a pass.  A call of few words
+// has a kernel of 1 KB of them: the launch copies them all (3.7 us of host time back
+// to back against 3.9, 6.2 against 7.4 among other work).  ParamWords<1>: staged.
+constexpr int kParamWords = 4032, kParamFew = 240;
 template <int N>
 struct ParamWords {
   int32_t w[N];
@@ -237,6 +239,13 @@ struct MetaArg {
 template <int N>
 inline void fill_words(const MetaArg& m, ParamWords<N>* out) {
   if (N > 1) std::memcpy(out->w, m.host, (size_t)m.n_words * sizeof(int32_t));
+}
+// go(std::integral_constant<int, N>) with the N that the metadata takes.
+template <typename Go>
+inline cudaError_t with_words(const MetaArg& m, Go go) {
+  if (m.dev) return go(std::integral_constant<int, 1>{});
+  if (m.n_words <= kParamFew) return go(std::integral_constant<int, kParamFew>{});
+  return go(std::integral_constant<int, kParamWords>{});
 }
 
 // Rotation of the first rd dimensions of a head: turns per position of each

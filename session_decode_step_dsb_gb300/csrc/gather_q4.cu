@@ -120,15 +120,13 @@ cudaError_t gather_go(const void* pool, int hkv, int n_seq, long long pages, voi
   // the heads of a page side by side: together they write whole rows of the output
   const dim3 grid((unsigned)hkv, (unsigned)(pages < kGatherPages ? pages : kGatherPages),
                   (unsigned)((pages + kGatherPages - 1) / kGatherPages));
-  if (meta.dev)
-    return launch_kernel(gather_q4_kernel<D, T, 1>, grid, dim3(kGatherThreads), 0, st,
-                         static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k), static_cast<T*>(v),
-                         ParamWords<1>{}, meta.dev);
-  ParamWords<kParamWords> w;
-  fill_words(meta, &w);
-  return launch_kernel(gather_q4_kernel<D, T, kParamWords>, grid, dim3(kGatherThreads), 0, st,
-                       static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k), static_cast<T*>(v), w,
-                       meta.dev);
+  return with_words(meta, [&](auto n) {
+    ParamWords<decltype(n)::value> w;
+    fill_words(meta, &w);
+    return launch_kernel(gather_q4_kernel<D, T, decltype(n)::value>, grid, dim3(kGatherThreads), 0, st,
+                         static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k),
+                         static_cast<T*>(v), w, meta.dev);
+  });
 }
 
 }  // namespace

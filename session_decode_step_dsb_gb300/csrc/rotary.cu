@@ -527,9 +527,10 @@ template <int D, typename Store>
 cudaError_t append_pick(const AppendArgs& a, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
   // few tokens: one head per lane group, the most CTAs; else four
   const bool few = a.n_tok <= 64;
-  if (meta.dev) return few ? append_go<D, Store, 1, 1>(a, rot, meta, st) : append_go<D, Store, 4, 1>(a, rot, meta, st);
-  return few ? append_go<D, Store, 1, kParamWords>(a, rot, meta, st)
-             : append_go<D, Store, 4, kParamWords>(a, rot, meta, st);
+  return with_words(meta, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return few ? append_go<D, Store, 1, N>(a, rot, meta, st) : append_go<D, Store, 4, N>(a, rot, meta, st);
+  });
 }
 
 }  // namespace
@@ -537,12 +538,11 @@ cudaError_t append_pick(const AppendArgs& a, const RotaryTable& rot, const MetaA
 cudaError_t launch_rope_rotary(float* q, long long q_stride, int hq, float* k, long long k_stride, int hkv, int head_dim,
                                int n_tok, const RotaryTable& rot, int runs, const MetaArg& meta, cudaStream_t st) {
   if (n_tok == 0) return cudaSuccess;
-  if (rot.rd <= 128)
-    return meta.dev ? rope_vec<64, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
-                    : rope_vec<64, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st);
-  return meta.dev ? rope_vec<kRopeMaxPairs, 1>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
-                  : rope_vec<kRopeMaxPairs, kParamWords>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs,
-                                                         meta, st);
+  return with_words(meta, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    return rot.rd <= 128 ? rope_vec<64, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st)
+                         : rope_vec<kRopeMaxPairs, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st);
+  });
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, const RotaryTable& rot,

@@ -676,7 +676,7 @@ def _current_device(t, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
@@ -794,7 +794,7 @@ def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws:
     kind = torch.float16 if dtype == DSB_F16 else torch.bfloat16
     pool = kv._tensors[0]
     dev = _current_device(pool, "the page pool")
-    shape = (max(int(ca.sum()), 0), kv.n_kv_heads, kv.head_dim)
+    shape = (max(sum(ca.tolist()), 0), kv.n_kv_heads, kv.head_dim)
     outs = [k, v]
     for i, name in enumerate("kv"):
         if outs[i] is None:
