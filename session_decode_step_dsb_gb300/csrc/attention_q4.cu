@@ -143,19 +143,19 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         more = false;
     }
   };
-  if (tid == 0) {
+  if (warp == 0) {
     const int w0 = (int)(total * blockIdx.x / gridDim.x);
     Cursor first;
     more = w0 < w1 && first.start<kRows>(meta, n_seq, hkv, G, w0) && first.at < w1;
-    *done = !more;
-    if (more) {
-      *cur = first;
-      *ahead = first;
-      for (int i = 0; i < kSlots - 1 && more; ++i) ask();
+    if (lane == 0) {
+      *done = !more;
+      if (more) *cur = *ahead = first;
     }
   }
   __syncthreads();
   if (*done) return;
+  if (tid == 0)  // meanwhile warp 1 stages the rows
+    for (int i = 0; i < kSlots - 1 && more; ++i) ask();
 
   int slot = 0;
   uint32_t phase = 0;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
   for (;;) {
     const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * kRows, R = G * n_new;
     if (cur->fresh) {
-      if (warp == 0) {  // row g, dimensions D/4 c ..
+      if (warp == 1) {  // row g, dimensions D/4 c ..
         const int r = row0 + g, j = r / G, gi = r - j * G;
         const bool live = r < R;
         float x[D / 4];

@@ -89,18 +89,18 @@ struct Cursor {
     pg = u * q.u_pages;
     pg_end = min(pg + q.u_pages, pages);
   }
-  // The first item that starts at or after `from` pages of work; false if none.
+  // The first item that starts at or after `from` pages of work; false if none.  The
+  // 32 lanes of a warp call it alike: they search 32 sequences at once (a search by
+  // halves waits for one word after the other).
   template <int ROWS>
   __device__ __forceinline__ bool start(const int32_t* meta, int n_seq, int hkv, int G, int from) {
-    int lo = 0, hi = n_seq - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (meta[mid * kQ4SeqWords] <= from)
-        lo = mid;
-      else
-        hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    s = -1;
+    for (int i = lane; i - lane < n_seq; i += 32) {
+      const unsigned before = __ballot_sync(0xFFFFFFFFu, i < n_seq && meta[i * kQ4SeqWords] <= from);
+      s += __popc(before);
+      if (before != 0xFFFFFFFFu) break;
     }
-    s = lo;
     load<ROWS>(meta, G);
     const int rel = from - q.work_off;
     int x = rel / pages;

@@ -220,12 +220,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
   // This CTA's items: those that start in its share of the pages.
   const long long total = meta[n_seq * kQ4SeqWords];
   const int w1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  if (tid == 0) {
+  if (warp == 0) {
     const int w0 = (int)(total * blockIdx.x / gridDim.x);
     Cursor first;
     const bool any = w0 < w1 && first.start<ROWS>(meta, n_seq, hkv, G, w0) && first.at < w1;
-    *done = !any;
-    if (any) *cur = *ahead = first;
+    if (lane == 0) {
+      *done = !any;
+      if (any) *cur = *ahead = first;
+    }
   }
   __syncthreads();
   if (warp == 8) {

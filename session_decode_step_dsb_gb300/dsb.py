@@ -651,14 +651,14 @@ def _row_stride(t, rows: int, inner, name: str):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be float32, got {t.dtype}")
-    shape = tuple(t.shape)
+    shape = t.shape
     if shape != (rows, *inner):
-        raise ValueError(f"{name} must be {rows} rows of {' x '.join(map(str, inner))} values, got {shape}")
+        raise ValueError(f"{name} must be {rows} rows of {' x '.join(map(str, inner))} values, got {tuple(shape)}")
     strides, width = t.stride(), 1
-    for n, step in zip(reversed(inner), reversed(strides)):
-        if n != 1 and step != width:
+    for i in range(len(inner), 0, -1):
+        if strides[i] != width and shape[i] != 1:
             raise ValueError(f"{name}: the values of a row must be contiguous")
-        width *= n
+        width *= shape[i]
     return strides[0] if rows > 1 else width
 
 
@@ -689,9 +689,12 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_INT32 = np.dtype(np.int32)
+
+
 def _host_i32(a, n: int, name: str):
     """``a`` as a contiguous int32 array of ``n`` entries, and its address."""
-    if not (type(a) is np.ndarray and a.dtype == np.int32 and a.ndim == 1 and a.flags.c_contiguous):
+    if not (type(a) is np.ndarray and a.dtype is _INT32 and a.ndim == 1 and a.flags.c_contiguous):
         a = np.ascontiguousarray(np.asarray(a, dtype=np.int32)).reshape(-1)
     if a.size != n:
         raise ValueError(f"{name} has {a.size} entries, needs {n}")
