@@ -193,9 +193,12 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
 
 // ---- append --------------------------------------------------------------------
 
-constexpr int kAppThreads = 256;
+// Small CTAs: a token's set-up (its sequence, page, sines and cosines) is a chain
+// that others hide.  5178 tokens of 56 heads, append and read-back: 32 threads 75 us,
+// 64 65, 128 with 7 CTAs an SM (72 registers) 62, with 8 63, 256 68.
+constexpr int kAppThreads = 128, kAppPerSm = 7;
 
-// Two float32 products at once, each rounded as by itself.
+// Two float32 operations at once, each rounded as by itself.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float a, float b) {
   f2 r;
@@ -210,6 +213,13 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// Not of two packed products: that would be compiled to a fused multiply-add, which
+// rounds once less.
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // Largest of a and b; NaN where either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -217,23 +227,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Over the D/4 lanes that hold a head.
+// Largest and smallest value over the D/8 lanes that hold a head (NaN where any is).
+// Neighbours share the work: after the first exchange even lanes carry the largest,
+// odd ones the smallest negated.
 template <int D>
-__device__ __forceinline__ float head_max_nan(float v) {
-  if constexpr (D == 128) {
-    float r;
-    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-  } else {
+__device__ __forceinline__ void head_range(float& most, float& least, int lane) {
+  const bool odd = lane & 1;
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? most : -least, 1);
+  float v = max_nan(odd ? -least : most, other);
 #pragma unroll
-    for (int o = D / 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-  }
-}
-// Whether any head of the warp is concerned; a warp holds one head at D = 128.
-template <int D>
-__device__ __forceinline__ bool warp_any(bool x) {
-  return D == 128 ? x : __any_sync(0xFFFFFFFFu, x);
+  for (int o = 2; o < D / 8; o <<= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+  most = odd ? w : v;
+  least = odd ? -v : -w;
 }
 
 template <typename T>
@@ -249,65 +255,104 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Sum of the squares of a head's D values, lane l of its D/4 holding values
-// 4l .. 4l+3.  The order is that of 32 running sums, the i-th over dimensions i,
-// i + 32, ..., added pairwise, neighbours first.  D = 128: the four terms of a
-// running sum sit 8 lanes apart; a transpose of the 4 x 4 (lane group, element)
-// brings them into one lane, the i-th group taking element i.  D = 64: two terms,
-// half of the elements to each group.
+// Sum of the squares of a head's D values, lane l of its D/8 holding values
+// 8l .. 8l+7.  The order is that of 32 running sums, the i-th over dimensions i,
+// i + 32, ..., added pairwise, neighbours first.  The terms of a running sum sit
+// four lanes apart; exchanges bring them into one lane.
 template <int D>
-__device__ __forceinline__ float sum_squares(const float (&y)[4], int lane) {
-  float v[4];
-  unpack2(mul2(pack2(y[0], y[1]), pack2(y[0], y[1])), v[0], v[1]);
-  unpack2(mul2(pack2(y[2], y[3]), pack2(y[2], y[3])), v[2], v[3]);
+__device__ __forceinline__ float sum_squares(const float (&y)[8], int lane) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), pack2(y[e], y[e + 1])), v[e], v[e + 1]);
   float ss;
   if constexpr (D == 128) {
-    const bool up = lane & 16, odd = lane & 8;
-    const float a = __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
-    const float b = __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : v[3], 16);
-    if (up) {
-      v[0] = a, v[1] = b;
-    } else {
-      v[2] = a, v[3] = b;
-    }
-    const float c = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 8);
-    const float d = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2] : v[3], 8);
-    if (odd) {
-      v[0] = c, v[2] = d;
-    } else {
-      v[1] = c, v[3] = d;
-    }
-    ss = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), v[2]), v[3]);
-    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
-    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 16));
-  } else {
-    const bool odd = lane & 8;
-    const float a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[2], 8);
-    const float b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[1] : v[3], 8);
-    ss = odd ? __fadd_rn(__fadd_rn(v[2], a), __fadd_rn(v[3], b)) : __fadd_rn(__fadd_rn(v[0], a), __fadd_rn(v[1], b));
-    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
-  }
+    // lane group j = 0 .. 3 holds the j-th terms and ends with elements 2j, 2j + 1
+    const bool up = lane & 8, odd = lane & 4;
+    float a[4], b[4];  // elements 4 (j / 2) ..: the terms of this group's half, of the other
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
-  return ss;
+    for (int e = 0; e < 4; ++e) {
+      a[e] = up ? v[e + 4] : v[e];
+      b[e] = __shfl_xor_sync(0xFFFFFFFFu, up ? v[e] : v[e + 4], 8);
+    }
+    float t[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a0 = odd ? a[e + 2] : a[e], b0 = odd ? b[e + 2] : b[e];
+      const float a1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a[e] : a[e + 2], 4);
+      const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? b[e] : b[e + 2], 4);
+      // terms 0 .. 3: (a0, a1) are 0 and 1 in the lower half, 2 and 3 in the upper
+      const float x0 = up ? b0 : a0, x1 = up ? b1 : a1, y0 = up ? a0 : b0, y1 = up ? a1 : b1;
+      t[e] = __fadd_rn(__fadd_rn(__fadd_rn(x0, x1), odd ? y1 : y0), odd ? y0 : y1);
+    }
+    ss = __fadd_rn(t[0], t[1]);
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 4));
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
+  } else {
+    const bool up = lane & 4;
+    float t[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      t[e] = __fadd_rn(up ? v[e + 4] : v[e], __shfl_xor_sync(0xFFFFFFFFu, up ? v[e] : v[e + 4], 4));
+    ss = __fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3]));
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 4));
+  }
+  ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 1));
+  return __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 2));
 }
 
 // How the cache rows are stored.
 struct StoreQ4 {};
 
-// grid (n_tok, shares of the heads), 256 threads: D/4 lanes hold one head's vector,
-// four values each, so that its norm, its extremes and the partner of a rotated
-// value stay inside a warp.  A lane handles the same four dimensions of one head
-// after the other, HPS of them loaded before the first is used, with one set of
-// sines and cosines.  Head h of the row: query heads, then key heads, then value
-// heads.  With many tokens one CTA takes all heads of its token: the kernel is
-// bound by instruction issue (a prompt of 5178 tokens of 56 heads: 254 MB, 78 us
-// and 253 instructions a head before, see the launch for the time now), so the
-// token's set-up is paid once.
+// The eight 4-bit codes of y / d about z.  The quotient by the reciprocal, held to
+// the codes' range, is within 2^-20 of the rounded quotient; only where it lies
+// closer than that to a half does the code need the division itself.  Adding 1.5 2^23
+// (and the code's 8) rounds to the nearest integer, ties to even, and leaves the code
+// in the low bits.
+__device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float z) {
+  constexpr float kRound = 12582920.0f;
+  const float inv = __frcp_rn(d);
+  const f2 inv2 = pack2(inv, inv), z2 = pack2(-z, -z), up = pack2(kRound, kRound), down = pack2(-kRound, -kRound);
+  uint32_t code = 0;
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float v0, v1, t0, t1, r0, r1;
+    unpack2(mul2(add2(pack2(y[e], y[e + 1]), z2), inv2), v0, v1);
+    v0 = fminf(fmaxf(v0, -8.0f), 7.0f);
+    v1 = fminf(fmaxf(v1, -8.0f), 7.0f);
+    const f2 t = add2(pack2(v0, v1), up);
+    const f2 n = add2(t, down);
+    unpack2(t, t0, t1);
+    unpack2(n, r0, r1);
+    near |= !(fabsf(fabsf(v0 - r0) - 0.5f) > 0x1p-18f) || !(fabsf(fabsf(v1 - r1) - 0.5f) > 0x1p-18f);
+    code += __float_as_uint(t0) << (4 * e);
+    code += __float_as_uint(t1) << (4 * e + 4);
+  }
+  // the bits above the codes, the same in each
+  constexpr uint32_t kBits = 0x4B400000u;
+  code -= kBits * 0x11111111u;
+  if (near) {
+    code = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float n = rintf(__fdiv_rn(__fsub_rn(y[e], z), d));
+      code |= (uint32_t)(int)fminf(fmaxf(n + 8.0f, 0.0f), 15.0f) << (4 * e);
+    }
+  }
+  return d == 0.0f ? 0x88888888u : code;
+}
+
+// grid (n_tok, shares of the heads): D/8 lanes hold one head's vector, eight values
+// each, so that its norm, its extremes and the partner of a rotated value stay inside
+// a warp.  A lane handles the same dimensions of one head after the other, the next
+// one's values on their way, with one set of sines and cosines.  Head h of the row:
+// query heads, then key heads, then value heads.  With many tokens one CTA takes all
+// heads of its token, so the token's set-up is paid once.  Bound by instruction
+// issue: those 5178 tokens move 205 MB (30 us at the copy rate).
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
-template <int D, typename Store, int HPS, int N>
-__global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __restrict__ qkv, long long stride, int hq,
+template <int D, typename Store, int N>
+__global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float* __restrict__ qkv, long long stride, int hq,
                                                                 int hkv, uint8_t* __restrict__ kc,
                                                                 uint8_t* __restrict__ vc,
                                                                 const __grid_constant__ Turns<64> tab,
@@ -315,25 +360,25 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __rest
                                                                 const float* __restrict__ k_norm, float eps, int n_seq,
                                                                 const __grid_constant__ ParamWords<N> words,
                                                                 const int32_t* __restrict__ meta_dev) {
-  constexpr int LPH = D / 4, SLOTS = kAppThreads / LPH;
-  __shared__ float2 cs[D / 2];
-  __shared__ float swap[kAppThreads * 4];
+  constexpr int LPH = D / 8, SLOTS = kAppThreads / LPH;
+  __shared__ __align__(16) float cosines[D], sines[D];  // of every dimension; a sine with the sign its term takes
+  __shared__ __align__(16) float swap[kAppThreads * 8];
   pdl_wait();
   pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x, l = tid & (LPH - 1), slot = tid / LPH;
   const int heads = hq + 2 * hkv, rd = tab.rd, half = rd >> 1;
-  const bool touched = q_norm || 4 * l < rd;  // query values past the rotated part stay where they are
-  float* row = qkv + (size_t)t * stride + 4 * l;
-  float4 x[HPS];
-  auto fetch = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < HPS; ++u) {
-      const int h = h0 + u * SLOTS;
-      x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (h < heads && (h >= hq || touched)) x[u] = __ldcg(reinterpret_cast<const float4*>(row + h * D));
+  const bool touched = q_norm || 8 * l < rd;  // query values past the rotated part stay where they are
+  float* row = qkv + (size_t)t * stride + 8 * l;
+  float4 x[2];
+  auto fetch = [&](int h) {
+    x[0] = x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (h < heads && (h >= hq || touched)) {
+      x[0] = __ldcg(reinterpret_cast<const float4*>(row + h * D));
+      x[1] = __ldcg(reinterpret_cast<const float4*>(row + h * D) + 1);
     }
   };
-  fetch(blockIdx.y * (HPS * SLOTS) + slot);
+  int h = blockIdx.y * SLOTS + slot;
+  fetch(h);
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   int lo = 0, hi = n_seq - 1;  // the sequence of token t
   while (lo < hi) {
@@ -347,83 +392,98 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __rest
   const int32_t* pg_off = meta + 2 * n_seq + 1;
   const int page = pg_off[n_seq + 1 + pg_off[lo] + (pos >> 7) - (pos0 >> 7)];
   const int r = pos & 127;
-  if (tid < half) cs[tid] = turn_cs(tab.f[tid], pos, tab.gain, tab.gain_lo);
-  __syncthreads();
-  float c[4], s[4];  // of this lane's four dimensions; s with the sign its term takes
-  bool turned[4];
-  int partner[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int dim = 4 * l + e;
-    c[e] = 1.0f;
-    s[e] = 0.0f;
-    partner[e] = dim;
-    turned[e] = dim < rd;
-    if (turned[e]) {
-      const bool second = tab.interleaved ? (dim & 1) : dim >= half;
-      const float2 v = cs[tab.interleaved ? dim >> 1 : second ? dim - half : dim];
-      c[e] = v.x;
-      s[e] = second ? v.y : -v.y;
-      partner[e] = tab.interleaved ? dim ^ 1 : second ? dim - half : dim + half;
-    }
+  for (int i = tid; i < half; i += kAppThreads) {
+    const float2 v = turn_cs(tab.f[i], pos, tab.gain, tab.gain_lo);
+    const int a = tab.interleaved ? 2 * i : i, b = tab.interleaved ? a + 1 : a + half;
+    cosines[a] = cosines[b] = v.x;
+    sines[a] = -v.y;
+    sines[b] = v.y;
   }
-  const int src = (tid & 31 & ~(LPH - 1)) + (partner[0] >> 2);  // lane of the partners, half layout in whole lanes
-  const bool lanes = (rd & 7) == 0, all = rd == D;
-  const float4 qw = q_norm ? __ldg(reinterpret_cast<const float4*>(q_norm) + l) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 kw = k_norm ? __ldg(reinterpret_cast<const float4*>(k_norm) + l) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int h0 = blockIdx.y * (HPS * SLOTS) + slot;; ) {
+  for (int i = rd + tid; i < D; i += kAppThreads) {
+    cosines[i] = 1.0f;
+    sines[i] = 0.0f;
+  }
+  __syncthreads();
+  const int turned = min(max(rd - 8 * l, 0), 8);  // of this lane's eight dimensions
+  // The partners of a whole lane's values are a whole lane's where half the rotated
+  // part is lanes; else they are fetched one by one.
+  const bool lanes = (rd & 15) == 0;
+  const int src = (tid & 31 & ~(LPH - 1)) + (turned == 0 ? l : 8 * l >= half ? l - half / 8 : l + half / 8);
+  float4 c[2], s[2];
 #pragma unroll
-    for (int u = 0; u < HPS; ++u) {
-      const int h = h0 + u * SLOTS;
-      if (D == 128 && h >= heads) break;
-      const bool live = h < heads, is_q = h < hq, is_k = !is_q && h < hq + hkv, is_v = live && !is_q && !is_k;
-      float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      const bool normed = (is_q && q_norm) || (is_k && k_norm);
-      if (warp_any<D>(normed)) {
-        const float ss = sum_squares<D>(y, tid & 31);
-        if (normed) {
-          const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
-          const float4 wv = is_q ? qw : kw;
-          const f2 inv2 = pack2(inv, inv);
-          unpack2(mul2(mul2(pack2(y[0], y[1]), inv2), pack2(wv.x, wv.y)), y[0], y[1]);
-          unpack2(mul2(mul2(pack2(y[2], y[3]), inv2), pack2(wv.z, wv.w)), y[2], y[3]);
+  for (int e = 0; e < 2; ++e) {
+    c[e] = *reinterpret_cast<const float4*>(&cosines[8 * l + 4 * e]);
+    s[e] = *reinterpret_cast<const float4*>(&sines[8 * l + 4 * e]);
+  }
+  for (;;) {
+    const bool live = h < heads, is_q = h < hq, is_k = !is_q && h < hq + hkv, is_v = live && !is_q && !is_k;
+    float y[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    const int next = h + gridDim.y * SLOTS;
+    if (next - slot < heads) fetch(next);
+    const float* norm = is_q ? q_norm : is_k ? k_norm : nullptr;
+    if (__any_sync(0xFFFFFFFFu, norm != nullptr)) {
+      const float ss = sum_squares<D>(y, tid & 31);
+      if (norm) {
+        const float inv = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
+        const f2 inv2 = pack2(inv, inv);
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(norm + 8 * l + e));
+          unpack2(mul2(mul2(pack2(y[e], y[e + 1]), inv2), pack2(w.x, w.y)), y[e], y[e + 1]);
+          unpack2(mul2(mul2(pack2(y[e + 2], y[e + 3]), inv2), pack2(w.z, w.w)), y[e + 2], y[e + 3]);
         }
       }
-      if (warp_any<D>(live && !is_v)) {
-        float p[4];
-        if (tab.interleaved) {
-          p[0] = y[1], p[1] = y[0], p[2] = y[3], p[3] = y[2];
-        } else if (lanes) {
+    }
+    if (__any_sync(0xFFFFFFFFu, live && !is_v)) {
+      float p[8];
+      if (tab.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], src);
-        } else {
-          float* mine = swap + slot * D;
-          __syncwarp();
-          *reinterpret_cast<float4*>(mine + 4 * l) = make_float4(y[0], y[1], y[2], y[3]);
-          __syncwarp();
+        for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
+      } else if (lanes) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = mine[partner[e]];
+        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], src);
+      } else {
+        float* mine = swap + slot * D;
+        __syncwarp();
+        *reinterpret_cast<float4*>(mine + 8 * l) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(mine + 8 * l + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int dim = 8 * l + e;
+          p[e] = mine[e >= turned ? dim : dim >= half ? dim - half : dim + half];
         }
-        if (!is_v) {
+      }
+      if (!is_v) {
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            // the sums one by one: a packed sum of packed products is compiled to a
-            // fused multiply-add, which rounds once less
-            float a0, a1, b0, b1;
-            unpack2(mul2(pack2(y[e], y[e + 1]), pack2(c[e], c[e + 1])), a0, a1);
-            unpack2(mul2(pack2(p[e], p[e + 1]), pack2(s[e], s[e + 1])), b0, b1);
-            const float z0 = __fadd_rn(a0, b0), z1 = __fadd_rn(a1, b1);
-            y[e] = all || turned[e] ? z0 : y[e];
-            y[e + 1] = all || turned[e + 1] ? z1 : y[e + 1];
+        for (int i = 0; i < 2; ++i) {
+          float a[4], b[4];
+          unpack2(mul2(pack2(y[4 * i], y[4 * i + 1]), pack2(c[i].x, c[i].y)), a[0], a[1]);
+          unpack2(mul2(pack2(y[4 * i + 2], y[4 * i + 3]), pack2(c[i].z, c[i].w)), a[2], a[3]);
+          unpack2(mul2(pack2(p[4 * i], p[4 * i + 1]), pack2(s[i].x, s[i].y)), b[0], b[1]);
+          unpack2(mul2(pack2(p[4 * i + 2], p[4 * i + 3]), pack2(s[i].z, s[i].w)), b[2], b[3]);
+          if (turned == 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[4 * i + e] = __fadd_rn(a[e], b[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[4 * i + e] = 4 * i + e < turned ? __fadd_rn(a[e], b[e]) : y[4 * i + e];
           }
         }
       }
-      if (is_q && touched) *reinterpret_cast<float4*>(row + h * D) = make_float4(y[0], y[1], y[2], y[3]);
-      const int g = h - hq - (is_k ? 0 : hkv);  // kv head
-      if constexpr (std::is_same<Store, StoreQ4>::value) {
-        if (!warp_any<D>(live && !is_q)) continue;
-        const float most = head_max_nan<D>(max_nan(max_nan(y[0], y[1]), max_nan(y[2], y[3])));
-        const float least = -head_max_nan<D>(max_nan(max_nan(-y[0], -y[1]), max_nan(-y[2], -y[3])));
+    }
+    if (is_q && touched) {
+      *reinterpret_cast<float4*>(row + h * D) = make_float4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<float4*>(row + h * D + 4) = make_float4(y[4], y[5], y[6], y[7]);
+    }
+    const int g = h - hq - (is_k ? 0 : hkv);  // kv head
+    if constexpr (std::is_same<Store, StoreQ4>::value) {
+      if (__any_sync(0xFFFFFFFFu, live && !is_q)) {
+        float most = max_nan(max_nan(max_nan(y[0], y[1]), max_nan(y[2], y[3])),
+                             max_nan(max_nan(y[4], y[5]), max_nan(y[6], y[7])));
+        float least = -max_nan(max_nan(max_nan(-y[0], -y[1]), max_nan(-y[2], -y[3])),
+                               max_nan(max_nan(-y[4], -y[5]), max_nan(-y[6], -y[7])));
+        head_range<D>(most, least, tid & 31);
         const float span = __fsub_rn(most, least);
         __half dh = __float2half_rn(__fmul_rn(span, 1.0f / 15.0f));
         __half zh = __float2half_rn(__fadd_rn(least, __fmul_rn(8.0f, __half2float(dh))));
@@ -431,45 +491,29 @@ __global__ void __launch_bounds__(kAppThreads, 4) kv_append_kernel(float* __rest
           dh = __ushort_as_half(0);
           zh = __ushort_as_half(0x7FFF);
         }
-        const float d = __half2float(dh), z = __half2float(zh);
-        // The quotient by the reciprocal, at most 8, is within 2^-20 of the rounded
-        // quotient; only where it lies closer than that to a half does the code
-        // need the division itself.
-        const float inv = __frcp_rn(d);
-        uint32_t code = 0;
-        bool near = false;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = __fmul_rn(__fsub_rn(y[e], z), inv);
-          const float n = rintf(v[e]);
-          near |= !(fabsf(fabsf(v[e] - n) - 0.5f) > 0x1p-18f);
-          v[e] = n;
-        }
-        if (near) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = rintf(__fdiv_rn(__fsub_rn(y[e], z), d));
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) code |= (uint32_t)(int)fminf(fmaxf(v[e] + 8.0f, 0.0f), 15.0f) << (4 * e);
-        if (d == 0.0f) code = 0x8888u;
         if (live && !is_q) {
+          const uint32_t code = q4_codes(y, __half2float(dh), __half2float(zh));
           using B = Q4Block<D>;
           uint8_t* blk = kc + ((size_t)page * hkv + g) * B::bytes;
-          uint8_t* dst = is_k ? blk + r * (D / 2) + 2 * l : blk + B::v + (r >> 1) * D + 4 * l + 2 * (r & 1);
-          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+          if (is_k) {
+            *reinterpret_cast<uint32_t*>(blk + r * (D / 2) + 4 * l) = code;
+          } else {
+            uint8_t* dst = blk + B::v + (r >> 1) * D + 8 * l + 2 * (r & 1);
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+            *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)(code >> 16);
+          }
           if (l == 0) *reinterpret_cast<__half2*>(blk + (is_k ? B::kz : B::vz) + 4 * r) = __halves2half2(dh, zh);
         }
-      } else {
-        if (live && !is_q) {
-          uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + 4 * l) * 2;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]));
-        }
+      }
+    } else {
+      if (live && !is_q) {
+        uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + 8 * l) * 2;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]),
+                                                    pack16<Store>(y[4], y[5]), pack16<Store>(y[6], y[7]));
       }
     }
-    h0 += gridDim.y * (HPS * SLOTS);
-    if (h0 - slot >= heads) break;
-    fetch(h0);
+    h = next;
+    if (h - slot >= heads) break;
   }
 }
 
@@ -507,30 +551,25 @@ cudaError_t rope_vec(float* q, long long q_stride, int hq, float* k, long long k
              : rope_go<NP, false, N>(q, q_stride, hq, k, k_stride, hkv, head_dim, n_tok, rot, runs, meta, st);
 }
 
-template <int D, typename Store, int HPS, int N>
+template <int D, typename Store, int N>
 cudaError_t append_go(const AppendArgs& a, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
   Turns<64> tab;
   fill_turns(rot, &tab);
   ParamWords<N> w;
   fill_words(meta, &w);
-  // as many shares of a token's heads as fill the GPU (8 CTAs on each of some 150
+  // as many shares of a token's heads as fill the GPU (7 CTAs on each of some 150
   // SMs), no more than there are
-  const int slots = kAppThreads / (D / 4) * HPS, most = (a.hq + 2 * a.hkv + slots - 1) / slots;
-  const int shares = std::min(most, std::max(1, 1200 / a.n_tok));
+  const int slots = kAppThreads / (D / 8), most = (a.hq + 2 * a.hkv + slots - 1) / slots;
+  const int shares = std::min(most, std::max(1, 7 * 150 / a.n_tok));
   const dim3 grid((unsigned)a.n_tok, (unsigned)shares);
-  return launch_kernel(kv_append_kernel<D, Store, HPS, N>, grid, dim3(kAppThreads), 0, st, a.qkv, a.stride, a.hq, a.hkv,
+  return launch_kernel(kv_append_kernel<D, Store, N>, grid, dim3(kAppThreads), 0, st, a.qkv, a.stride, a.hq, a.hkv,
                        static_cast<uint8_t*>(a.kc), static_cast<uint8_t*>(a.vc), tab, a.q_norm, a.k_norm, a.eps, a.n_seq,
                        w, meta.dev);
 }
 
 template <int D, typename Store>
 cudaError_t append_pick(const AppendArgs& a, const RotaryTable& rot, const MetaArg& meta, cudaStream_t st) {
-  // few tokens: one head per lane group, the most CTAs; else four
-  const bool few = a.n_tok <= 64;
-  return with_words(meta, [&](auto n) {
-    constexpr int N = decltype(n)::value;
-    return few ? append_go<D, Store, 1, N>(a, rot, meta, st) : append_go<D, Store, 4, N>(a, rot, meta, st);
-  });
+  return with_words(meta, [&](auto n) { return append_go<D, Store, decltype(n)::value>(a, rot, meta, st); });
 }
 
 }  // namespace
