@@ -458,8 +458,8 @@ typedef struct {
 /* Rotates q and k rows in place, row t at position pos[t] (host int32[n_tok],
  * each in [0, 2^24)).  q: device float32, row t at q + t * q_stride, heads of
  * head_dim side by side; k alike (NULL with n_kv_heads = 0).  q and k may be
- * parts of the same rows (the strides of a fused projection) but share no
- * value.  head_dim even in [2, 1024].  Angles modulo one turn in 64-bit integer
+ * parts of the same rows (the strides of a fused projection, q_stride = k_stride
+ * then) but share no value.  head_dim even in [2, 1024].  Angles modulo one turn in 64-bit integer
  * arithmetic; c and s the float32 nearest to the cosine and the sine times the
  * gain (but for one in some thousands); x c - y s and x s + y c with every
  * product and sum rounded to float32.  Row t is bitwise equal to an n_tok = 1
@@ -535,7 +535,7 @@ dsb_status dsb_kv_append_q4(float* qkv, int64_t row_stride, int n_q_heads, const
  * up to p without a window); score = q.k / sqrt(head_dim), out = softmax(score) V
  * with the pages' values, float32 accuracy.  q: device float32, row t at
  * q + t * q_stride (a multiple of 4; the query part of qkv rows will do); out:
- * device float32 [tokens][n_q_heads][head_dim].  A sequence without new tokens
+ * device float32 [tokens][n_q_heads][head_dim], apart from q's rows.  A sequence without new tokens
  * has no rows.  Any number of new tokens.  Partial sums of long sequences go to
  * the workspace: dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest
  * seq_lens) is enough.  No atomics; a sequence's rows are bitwise the same alone
@@ -547,7 +547,7 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
  * int32[n_seq]; within seq_lens[s], under a window also within what the ring
  * still holds; new_tokens is not used) as the values they stand for, rounded to
  * nearest even in dtype (dsb_dtype): k_out and v_out device 16-bit
- * [sum of count][n_kv_heads][head_dim], the sequences one after the other. */
+ * [sum of count][n_kv_heads][head_dim], apart, the sequences one after the other. */
 dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* batch, const int32_t* first,
                             const int32_t* count, int dtype, void* k_out, void* v_out, dsb_workspace* ws, void* stream);
 

@@ -82,6 +82,23 @@ void build_rotary(const dsb_rotary& r, int head_dim, dsbk::RotaryTable* out) {
   dsbk::rotary_table(f.f, rd, r.interleaved != 0, gain, out);
 }
 
+// Whether two ranges of device memory share a byte.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+// The same of n rows of `width` floats each, a stride apart; rows of two strides in
+// one range count as shared.
+bool rows_overlap(const float* a, int64_t a_stride, int64_t a_width, const float* b, int64_t b_stride, int64_t b_width,
+                  int n) {
+  if (!overlap(a, ((n - 1) * a_stride + a_width) * sizeof(float), b, ((n - 1) * b_stride + b_width) * sizeof(float)))
+    return false;
+  if (a_stride != b_stride) return true;
+  const int64_t bytes = a_stride * (int64_t)sizeof(float);
+  const int64_t off = ((reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % bytes + bytes) % bytes;
+  return off < a_width * (int64_t)sizeof(float) || off + b_width * (int64_t)sizeof(float) > bytes;
+}
+
 dsb_status check_workspace(const dsb_workspace* ws) {
   if (!ws) return fail(DSB_ERR_WORKSPACE, "workspace is NULL");
   int dev = -1;
@@ -303,6 +320,8 @@ dsb_status dsb_rope_rotary(float* q, int64_t q_stride, int n_q_heads, float* k, 
     if (!aligned16(q) || (k && !aligned16(k))) return fail(DSB_ERR_INVALID_ARG, "q / k not 16-byte aligned");
     for (int t = 0; t < n_tok; ++t)
       if (pos[t] < 0 || pos[t] >= kMaxPos) return fail(DSB_ERR_INVALID_ARG, "pos[%d]=%d out of [0, 2^24)", t, pos[t]);
+    if (k && rows_overlap(q, q_stride, (int64_t)n_q_heads * head_dim, k, k_stride, (int64_t)n_kv_heads * head_dim, n_tok))
+      return fail(DSB_ERR_INVALID_ARG, "q and k share values: they would be rotated twice");
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // runs of consecutive positions (a prompt is one), or the positions themselves
@@ -442,6 +461,9 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     }
     if (need > partial_capacity(ws))
       return fail(DSB_ERR_WORKSPACE, "attention needs %zu workspace bytes for partials, have %zu", need, partial_capacity(ws));
+    const int64_t width = (int64_t)n_q_heads * D;
+    if (overlap(q, ((n_tok - 1) * q_stride + width) * sizeof(float), out, n_tok * width * sizeof(float)))
+      return fail(DSB_ERR_INVALID_ARG, "out overlaps the rows of q");
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     if ((st = check_capture(most, cs)) != DSB_OK) return st;
@@ -515,6 +537,8 @@ dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* b,
       g.words.insert(g.words.end(), list.begin(), list.end());
       most = std::max(most, g.words.size());
     }
+    const size_t out_bytes = (size_t)rows * kv->n_kv_heads * kv->head_dim * 2;
+    if (overlap(k_out, out_bytes, v_out, out_bytes)) return fail(DSB_ERR_INVALID_ARG, "k_out and v_out overlap");
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     if ((st = check_capture(most, cs)) != DSB_OK) return st;

@@ -692,6 +692,18 @@ def _raw_stream(stream, device: int) -> int:
 _INT32 = np.dtype(np.int32)
 
 
+def _empty_on(stream, shape, dtype, device):
+    """``torch.empty`` for a call on ``stream``: memory of that stream's, since
+    what the current stream has freed may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _host_i32(a, n: int, name: str):
     """``a`` as a contiguous int32 array of ``n`` entries, and its address."""
     if not (type(a) is np.ndarray and a.dtype is _INT32 and a.ndim == 1 and a.flags.c_contiguous):
@@ -773,7 +785,7 @@ def attention_decode_q4(q, kv: KVQ4Pages, batch: PagedBatch, ws: Workspace, out=
     stride = _row_stride(q, batch.n_tok, (hq, d), "q")
     dev = _current_device(q, "q")
     if out is None:
-        out = torch.empty((n_tok, hq, d), dtype=torch.float32, device=q.device)
+        out = _empty_on(stream, (n_tok, hq, d), torch.float32, q.device)
     else:
         _need(out, 4 * n_tok * hq * d, "out", "f32")
         if not out.is_contiguous():
@@ -801,7 +813,7 @@ def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws:
     outs = [k, v]
     for i, name in enumerate("kv"):
         if outs[i] is None:
-            outs[i] = torch.empty(shape, dtype=kind, device=pool.device)
+            outs[i] = _empty_on(stream, shape, kind, pool.device)
             continue
         _need(outs[i], 2 * shape[0] * shape[1] * shape[2], name)
         if outs[i].dtype != kind or not outs[i].is_contiguous():

@@ -630,3 +630,83 @@ def test_a_short_workspace_is_refused(cuda_device):
     b = d.PagedBatch([list(range(32))], [32], [0], [1], [4096])
     with pytest.raises(d.DsbError, match="partials"):
         d.attention_decode_q4(torch.zeros((1, 4, 64), device="cuda"), d.kv_q4_pages(pool, 64), b, d.Workspace(1, 4, 64, 128))
+
+
+def test_a_nan_key_on_a_long_cache_of_many_rows(cuda_device):
+    d = _dsb()
+    rng = np.random.default_rng(8)
+    L, T, hq = 2400, 3, 8
+    pool = _pool(rng, 19, 1, 128)
+    c = 64 * 128
+    key = L - T + 1                                       # the second new token's: the first does not see it
+    page, r = divmod(key, P)
+    q = to_dev(rng.standard_normal((T, hq, 128)).astype(np.float32))
+    b = d.PagedBatch([list(range(19))], [19], [0], [T], [L])
+    for at in (c + 4 * r, 2 * c + 4 * P + 4 * r):          # its K numbers, its V numbers
+        bad = pool.copy()
+        bad[page, 0, at:at + 4] = 255
+        got = to_host(d.attention_decode_q4(q, d.kv_q4_pages(to_dev(bad), 128), b, d.Workspace(T, hq, 128, L)))
+        assert np.isfinite(got[0]).all() and np.isnan(got[1:]).all()
+
+
+def test_a_thousand_sequences(cuda_device):
+    """As many as a call may have: their metadata is staged, and every CTA looks
+    its first one up among them."""
+    d = _dsb()
+    n, D, hq, hkv = 1024, 64, 2, 1
+    rng = np.random.default_rng(21)
+    lens = rng.integers(1, 300, n)
+    new = np.where(rng.random(n) < 0.1, 0, 1)
+    bt = rng.integers(0, 40, (n, 3))                      # pages shared by many: they are only read
+    pool = _pool(rng, 40, hkv, D)
+    q = rng.standard_normal((int(new.sum()), hq, D)).astype(np.float32)
+    kv = d.kv_q4_pages(to_dev(pool), D)
+    got = to_host(d.attention_decode_q4(to_dev(q), kv, d.PagedBatch(bt, [3] * n, [0] * n, new, lens),
+                                        d.Workspace(n, hq, D, 384)))
+    kvals, vvals = oq4.pool_values(pool, D)
+    want, bound = oq4.attention(q, kvals, vvals, bt, [3] * n, [0] * n, new, lens, oq4.pool_sizes(pool, D))
+    assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("n", [1, 240, 241, 4032, 4033])
+def test_positions_in_and_beside_the_launch(cuda_device, n):
+    """Metadata at the sizes where its way to the kernel changes."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(n)
+    pos = rng.permutation(3 * n)[:n] * 2                  # no two in a row
+    x = to_dev(rng.standard_normal((n, 1, 64)).astype(np.float32))
+    rot, ws = d.Rotary(interleaved=True), d.Workspace(n, 1, 64, P)
+    got = x.clone()
+    d.rope_rotary(got, None, pos, rot, ws)
+    order = np.argsort(pos)                               # one call for each half
+    for part in (order[:n // 2], order[n // 2:]):
+        if len(part):
+            y = x[torch.from_numpy(part).cuda()].contiguous()
+            d.rope_rotary(y, None, pos[part], rot, ws)
+            assert torch.equal(y, got[torch.from_numpy(part).cuda()])
+
+
+def test_a_given_stream_owns_what_the_call_makes(cuda_device):
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(31)
+    pool = to_dev(_pool(rng, 3, 2, 64))
+    q = to_dev(rng.standard_normal((1, 4, 64)).astype(np.float32))
+    kv, b = d.kv_q4_pages(pool, 64), d.PagedBatch([[2, 0, 1]], [3], [0], [1], [333])
+    want = d.attention_decode_q4(q, kv, b, d.Workspace(1, 4, 64, 384))
+    wk, wv = d.kv_gather_q4(kv, b, [5], [300], d.DSB_BF16, d.Workspace(1, 4, 64, 384))
+    torch.cuda.synchronize()
+    side, ws = torch.cuda.Stream(), d.Workspace(1, 4, 64, 384)
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        # memory that the current stream still writes is freed and must not be handed out
+        busy = [torch.full_like(t, 7.0) for t in (want, wk, wv)]
+        torch.cuda._sleep(20_000_000)
+        for t in busy:
+            t.fill_(9.0)
+        del busy, t
+        out = d.attention_decode_q4(q, kv, b, ws, stream=stream)
+        k, v = d.kv_gather_q4(kv, b, [5], [300], d.DSB_BF16, ws, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)

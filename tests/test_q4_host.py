@@ -156,6 +156,43 @@ def test_pool_and_buffer_refusals(d):
     assert gather([743, 0], [10, 0], batch=ring) == INVALID and "ring" in lib.dsb_last_error().decode()
 
 
+def test_memory_shared_between_arguments_is_refused(d):
+    """Before any device work: the workspace is not looked at either."""
+    lib, b, rot, kv = d.lib(), _batch(d), d.Rotary(), _pages(d)
+    base = 1 << 20
+    ws = ctypes.create_string_buffer(4096)          # stands for a workspace: only its size is read
+    pos = np.arange(3, dtype=np.int32)
+    pp = pos.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+
+    def rope(k, qs, ks, n=3):
+        st = lib.dsb_rope_rotary(base, qs, 2, k, ks, 1, 64, n, pp, rot.ref, ws, None)
+        return st, lib.dsb_last_error().decode()
+
+    for k, qs, ks in ((base, 128, 64), (base, 192, 192), (base + 4 * 64, 192, 192), (base + 4 * 160, 192, 192),
+                      (base + 4 * 128, 192, 256), (base - 4 * 32, 128, 64)):
+        st, why = rope(k, qs, ks)
+        assert st == INVALID and "share" in why, (k - base, qs, ks)
+    st, why = rope(base, 128, 64, 1)
+    assert st == INVALID and "share" in why
+
+    def gather(k, v):
+        f, c = np.array([0, 0], np.int32), np.array([100, 2], np.int32)
+        p = [a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)) for a in (f, c)]
+        return lib.dsb_kv_gather_q4(ctypes.byref(kv), b.ref, p[0], p[1], 0, k, v, ws, None), lib.dsb_last_error().decode()
+
+    for v in (base, base + 102 * 2 * 64 * 2 - 16, base - 102 * 2 * 64 * 2 + 16):
+        st, why = gather(base, v)
+        assert st == INVALID and "overlap" in why
+
+    def attn(out, stride=256):
+        return (lib.dsb_attention_decode_q4(base, stride, 4, ctypes.byref(kv), b.ref, out, ws, None),
+                lib.dsb_last_error().decode())
+
+    for out, stride in ((base, 256), (base + 4 * 256 * 3 - 16, 256), (base - 4 * 256 * 3 + 16, 256), (base + 4 * 300, 512)):
+        st, why = attn(out, stride)
+        assert st == INVALID and "overlap" in why
+
+
 def test_a_block_table_past_the_staging_slot_is_refused(d):
     kv = _pages(d)
     b = d.PagedBatch(np.zeros((1, 12000)), [12000], [0], [1], [12000 * 128])
