@@ -21,14 +21,22 @@
 // sequence's own length alone, so a sequence's rows are bitwise the same alone
 // and in a batch.  A warp takes 32 of a page's 128 keys and carries its own
 // maximum, sum and output tile through the unit: inside a unit the warps meet at
-// no barrier but those of the copies.  Pages arrive as bulk copies of whole
-// blocks, one ahead.  The four warps' results are joined at the unit's end, the
-// units' by a second kernel in unit order (a sequence of one unit needs none).
+// no barrier but those of the copies.  The K and V halves of the pages arrive as
+// bulk copies, four halves ahead.  The four warps' results are joined at the unit's
+// end, the units' by a second kernel in unit order (a sequence of one unit needs
+// none).
 //
 // The running reference of the exponentials is the largest s_k plus the log of
 // the largest d_k (of V) of the same 32 keys, so that the weights that enter the
 // fp16 split are at most 2^14 whatever the scales are; p_k itself and the sums
 // over it are float32.
+//
+// Measured: 4 sequences of 16384 to 65536 keys, 32 kv heads of 128, one row each
+// (820 MB of pages): 202 us, 4.1 TB/s, 0.60 of the copy rate.  Bound by instruction
+// issue and its latencies: some 690 instructions a warp and page, 290 of them the
+// unpacking of the codes, at 16 warps an SM (128 registers); the warp-level tensor
+// pipe is busy 0.4 of the time.  16 sequences of up to 4096 keys, 8 kv heads of 128,
+// 5 rows each (39 MB): 20 us for 2 or 4 pages a CTA.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -515,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
 }
 
 // One CTA of D threads per (token row, query head): the units' (maximum, sum,
-// row) joined in unit order.  Sequences of one unit are done already.
+// row) joined in unit order.  Sequences of one unit are done already.  Bound by
+// latency: 640 rows of up to 16 units 4.3 us, 128 rows of up to 64 units 7.6 us.
 template <int D, int N>
 __global__ void __launch_bounds__(D) attention_q4_merge_kernel(const float* __restrict__ partials, int hq, int n_seq,
                                                                int max_units, float* __restrict__ out,

@@ -112,7 +112,9 @@ constexpr int kRotUnroll = 4;  // pieces per thread, all loaded before the first
 // grid (n_tok, pieces / (256 * 4)).  A piece is four pairs (half layout: four
 // values from each half), two pairs (interleaved) or, without VEC, one pair.
 // In place: a pair is read and written by one thread.  The pairs' sines and
-// cosines are worked out once per CTA while the loads are on their way.
+// cosines are worked out once per CTA while the loads are on their way.  Bound by
+// memory: 6000 rows of 48 heads, 64 dimensions turned (147 MB): 25 us, 5.9 TB/s, 0.87
+// of the copy rate.  One row: 4 us, a launch's latency.
 template <int NP, bool VEC, int N>
 __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restrict__ q, long long q_stride, int hq,
                                                                   float* __restrict__ k, long long k_stride, int hkv,
@@ -348,7 +350,8 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float
 // one's values on their way, with one set of sines and cosines.  Head h of the row:
 // query heads, then key heads, then value heads.  With many tokens one CTA takes all
 // heads of its token, so the token's set-up is paid once.  Bound by instruction
-// issue: those 5178 tokens move 205 MB (30 us at the copy rate).
+// issue: those 5178 tokens move 205 MB (30 us at the copy rate) in 51 us.  16 tokens:
+// 4.5 us, the latency of the chain.
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
 template <int D, typename Store, int N>
