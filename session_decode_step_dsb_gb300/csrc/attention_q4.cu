@@ -11,7 +11,8 @@
 //     sum_k p_k V_k = sum_k (p_k d_k) (c_k - 8) + sum_k p_k z_k
 // q and the weights w_k = p_k d_k are split into two fp16 (hi + lo: 22 bits), two
 // products into one float32 sum.  Both products have the 8 query rows as their
-// columns, S^T = K Q^T (keys x rows) and O^T = V^T P^T (dimensions x rows), so that
+// columns, S^T = K Q^T (keys x rows) and O^T = V^T P^T (dimensions x rows) (up to 4
+// rows: hi and lo as columns of one product), so that
 // m16n8k16 carries no padding at 8 rows and a warp's output tile is D/4 registers
 // a thread; the weights turn from the first product's result layout into the
 // second's operand layout by an 8 x 8 transpose in the warp.
@@ -32,11 +33,11 @@
 // over it are float32.
 //
 // Measured: 4 sequences of 16384 to 65536 keys, 32 kv heads of 128, one row each
-// (820 MB of pages): 202 us, 4.1 TB/s, 0.60 of the copy rate.  Bound by instruction
-// issue and its latencies: some 690 instructions a warp and page, 290 of them the
-// unpacking of the codes, at 16 warps an SM (128 registers); the warp-level tensor
-// pipe is busy 0.4 of the time.  16 sequences of up to 4096 keys, 8 kv heads of 128,
-// 5 rows each (39 MB): 20 us for 2 or 4 pages a CTA.
+// (820 MB of pages): 193 us with the join, 4.3 TB/s, 0.63 of the copy rate.  Bound by
+// instruction issue and its latencies: some 650 instructions a warp and page, 290 of
+// them the unpacking of the codes, at 16 warps an SM (123 registers), issued in 0.6 of
+// the cycles; an eighth of the waiting is at the units' ends.  16 sequences of up to
+// 4096 keys, 8 kv heads of 128, 5 rows each (39 MB): 20 us for 2 or 4 pages a CTA.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -85,7 +86,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-constexpr int kRows = 8;   // query rows of an item
 constexpr int kSlots = 5;  // half pages (K or V) on their way or in use
 
 template <int D>
@@ -93,14 +93,16 @@ struct Q4Smem {
   static constexpr int half = Q4Block<D>::v;                // K codes and numbers; V's are as many bytes
   static constexpr int q = kSlots * half;                   // [D/16][32 lanes] uint4: q as right operand
   static constexpr int rows = q + D / 16 * 512;             // [8] float4: scale, sum, last key, -
-  static constexpr int join = rows + kRows * 16;            // [4 warps][D/32][32 lanes] float4
+  static constexpr int join = rows + 8 * 16;                // [4 warps][D/32][32 lanes] float4
   static constexpr int stat = join + 4 * (D / 32) * 512;    // [4 warps][4] float4: M, M, sum, sum
   static constexpr int bars = stat + 4 * 64;
   static constexpr int cursors = bars + 2 * kSlots * 8;     // the item in work, the next to ask for, "done"
   static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
 };
 
-template <int D, int N>
+// ROWS, the query rows of an item: 8, or 4, whose hi and lo parts then share a
+// product as columns 0 .. 3 and 4 .. 7.
+template <int D, int ROWS, int N>
 __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint8_t* __restrict__ pool, int n_seq,
     float scale_log2e, int max_units, float* __restrict__ partials, float* __restrict__ out,
@@ -109,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
   using S = Q4Smem<D>;
   constexpr int W = D / 32;    // 32-bit words of a thread's piece of a K row, and of a V key pair
   constexpr int NT = D / 16;   // 16-dimension tiles of the output
+  constexpr bool kFew = ROWS == 4;
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* qs = reinterpret_cast<uint4*>(smem + S::q);
   float4* rowp = reinterpret_cast<float4*>(smem + S::rows);
@@ -117,6 +120,8 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::bars);
   uint64_t* empty = full + kSlots;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int pair = kFew ? c & 1 : c;   // the thread's rows are 2 pair and 2 pair + 1
+  const bool first_half = !kFew || c < 2;  // its columns are those of the hi parts
   const int G = hq / hkv;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   if (tid == 0) {
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     if (++ask_slot == kSlots) ask_slot = 0, ask_phase ^= 1;
     if ((ask_which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
       if (ahead->end() < w1)
-        ahead->next<kRows>(meta, hkv, G);
+        ahead->next<ROWS>(meta, hkv, G);
       else
         more = false;
     }
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
   if (warp == 0) {
     const int w0 = (int)(total * blockIdx.x / gridDim.x);
     Cursor first;
-    more = w0 < w1 && first.start<kRows>(meta, n_seq, hkv, G, w0) && first.at < w1;
+    more = w0 < w1 && first.start<ROWS>(meta, n_seq, hkv, G, w0) && first.at < w1;
     if (lane == 0) {
       *done = !more;
       if (more) *cur = *ahead = first;
@@ -173,10 +178,10 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     if (++slot == kSlots) slot = 0, phase ^= 1;
   };
   for (;;) {
-    const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * kRows, R = G * n_new;
+    const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * ROWS, R = G * n_new;
     if (cur->fresh) {
-      if (warp == 1) {  // row g, dimensions D/4 c ..
-        const int r = row0 + g, j = r / G, gi = r - j * G;
+      if (warp == 1) {  // column g, dimensions D/4 c ..
+        const int r = row0 + (g & (ROWS - 1)), j = r / G, gi = r - j * G;
         const bool live = r < R;
         float x[D / 4];
         const float* src = q + (size_t)(cur->q.tok0 + j) * q_stride + (size_t)(cur->h * G + gi) * D + c * (D / 4);
@@ -216,16 +221,19 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
             uint4 v;  // hi of the step's two halves, then lo
             split(pack(x[8 * w + 2 * b], x[8 * w + 2 * b + 4]), v.x, v.z);
             split(pack(x[8 * w + 2 * b + 1], x[8 * w + 2 * b + 5]), v.y, v.w);
-            qs[(2 * w + b) * 32 + lane] = v;
+            if constexpr (kFew)
+              reinterpret_cast<uint2*>(qs)[(2 * w + b) * 32 + lane] = g < 4 ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w);
+            else
+              qs[(2 * w + b) * 32 + lane] = v;
           }
       }
       __syncthreads();
     }
-    // rows 2c and 2c + 1: the scale taken out of q, sum(q), the last key seen
+    // the two rows: the scale taken out of q, sum(q), the last key seen
     f2 scale2, sum2;
     int hi0, hi1;
     {
-      const float4 a = rowp[2 * c], b = rowp[2 * c + 1];
+      const float4 a = rowp[2 * pair], b = rowp[2 * pair + 1];
       scale2 = pack(a.x, b.x);
       sum2 = pack(a.y, b.y);
       hi0 = __float_as_int(a.z), hi1 = __float_as_int(b.z);
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       lsum = zsum = 0;
     }
     // what any row of the item can see, and what every row sees
-    const int j0 = row0 / G, j1 = min(row0 + kRows - 1, R - 1) / G;
+    const int j0 = row0 / G, j1 = min(row0 + ROWS - 1, R - 1) / G;
     const int first_hi = len - n_new + j0, last_hi = len - n_new + j1;
     const int any_lo = first_hi - back, all_lo = window > 0 ? len - window : 0;
 
@@ -258,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       // output was off by 4e-6 of its size, against 5e-7.)
       if (!mbar_wait(&full[slot], phase)) g_err_attention_q4 = 1u;
       __syncwarp();
-      f2 x[2][2];  // [tile][half]: s of keys 16t + 8h + g, rows 2c and 2c + 1, over the row's scale
+      f2 x[2][2];  // [tile][half]: s of keys 16t + 8h + g and the two rows, over the row's scale
       if (some) {
         const uint8_t* blk = smem + slot * S::half;
-        float sc[2][2][4];  // [tile][hi, lo of q]: keys g, g, g + 8, g + 8 of rows 2c, 2c + 1
+        float sc[2][2][4];  // [tile][hi, lo of q; or halves of the sum]: keys g, g, g + 8, g + 8 of columns 2c, 2c + 1
         uint32_t kw[2][2][W];   // [tile][key g, g + 8]
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -283,12 +291,23 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
           for (int t = 0; t < 2; ++t) q4_unpack(kw[t][0][w], u[t]), q4_unpack(kw[t][1][w], v[t]);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const uint4 q4 = qs[(2 * w + b) * 32 + lane];
+            uint4 q4;
+            if constexpr (kFew) {
+              const uint2 q2 = reinterpret_cast<const uint2*>(qs)[(2 * w + b) * 32 + lane];
+              q4 = make_uint4(q2.x, q2.y, 0, 0);
+            } else {
+              q4 = qs[(2 * w + b) * 32 + lane];
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const uint32_t a0 = bits(u[t][2 * b]), a1 = bits(v[t][2 * b]), a2 = bits(u[t][2 * b + 1]),
                              a3 = bits(v[t][2 * b + 1]);
-              if (w == 0 && b == 0) {
+              if constexpr (kFew) {
+                if (w == 0)
+                  mma_from(sc[t][b], a0, a1, a2, a3, q4.x, q4.y, 0.0f, 0.0f);
+                else
+                  mma(sc[t][b], a0, a1, a2, a3, q4.x, q4.y);
+              } else if (w == 0 && b == 0) {
                 mma_from(sc[t][0], a0, a1, a2, a3, q4.x, q4.y, 0.0f, 0.0f);
                 mma_from(sc[t][1], a0, a1, a2, a3, q4.z, q4.w, 0.0f, 0.0f);
               } else {
@@ -306,8 +325,11 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
             {
-              const f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]),
-                                  pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
+              f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]), pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
+              if constexpr (kFew) {  // hi parts' and lo parts' columns
+                const float2 v = unpack(acc);
+                acc = add2(acc, pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, 2), __shfl_xor_sync(0xFFFFFFFFu, v.y, 2)));
+              }
               x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
             }
           }
@@ -370,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         // ---- weights, and 16 keys at a time their product with V
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves
+          uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves; of column g
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
@@ -391,8 +413,12 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
               lsum = add2(lsum, pp);
               zsum = fma2(pp, z, zsum);
               split(mul2(pp, d), ph[h], pl[h]);
-              ph[h] = transpose8(ph[h]);
-              pl[h] = transpose8(pl[h]);
+              if constexpr (kFew) {
+                ph[h] = transpose8(first_half ? ph[h] : pl[h]);
+              } else {
+                ph[h] = transpose8(ph[h]);
+                pl[h] = transpose8(pl[h]);
+              }
             }
           }
           uint32_t v0[W], v1[W];
@@ -417,10 +443,12 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
               for (int i = 0; i < 2; ++i)
                 mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
                     ph[0], ph[1]);
+              if constexpr (!kFew) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
-                    pl[0], pl[1]);
+                for (int i = 0; i < 2; ++i)
+                  mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                      pl[0], pl[1]);
+              }
             }
           }
         }
@@ -440,14 +468,14 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       zsum = add2(zsum, pack(__shfl_xor_sync(0xFFFFFFFFu, z.x, s4), __shfl_xor_sync(0xFFFFFFFFu, z.y, s4)));
     }
     {
-      const float2 z = unpack(zsum);
+      const float2 z = first_half ? unpack(zsum) : make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         o[t][0] += z.x, o[t][1] += z.y;
         o[t][2] += z.x, o[t][3] += z.y;
       }
     }
-    const bool mine = row0 + 2 * c < R;  // else the thread's rows are nobody's
+    const bool mine = row0 + 2 * pair < R;  // else the thread's rows are nobody's
     // The region and statistics that a warp reads in the first round are the ones it
     // writes in the second: nobody else reads them between.
     const auto swap = [&](auto upper, auto tiles, int to, int from) {
@@ -493,10 +521,16 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     {
       constexpr int Q = NT / 4;  // tiles of this warp
       const float2 l = unpack(lsum);
+      if constexpr (kFew) {
+#pragma unroll
+        for (int t = 0; t < Q; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][i] += __shfl_xor_sync(0xFFFFFFFFu, o[t][i], 2);
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = row0 + 2 * c + e;
-        if (r >= R) continue;
+        const int r = row0 + 2 * pair + e;
+        if (r >= R || !first_half) continue;
         const int j = r / G, dim = g * (D / 8) + warp * (2 * Q);
         const size_t row = (size_t)(tok0 + j) * hq + head0 + r - j * G;
         const float le = e ? l.y : l.x;
@@ -515,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     }
     if (tid == 0) {
       *done = cur->end() >= w1;
-      if (!*done) cur->next<kRows>(meta, hkv, G);
+      if (!*done) cur->next<ROWS>(meta, hkv, G);
     }
     __syncthreads();
     if (*done) break;
@@ -593,10 +627,10 @@ __global__ void __launch_bounds__(D) attention_q4_merge_kernel(const float* __re
   out[row * D + dim] = __fdiv_rn(acc, l);
 }
 
-template <int D, int N>
+template <int D, int ROWS, int N>
 cudaError_t attention_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
   constexpr int smem = Q4Smem<D>::bytes;
-  auto kern = attention_q4_kernel<D, N>;
+  auto kern = attention_q4_kernel<D, ROWS, N>;
   int resident = 0;
   {
     static std::mutex mu;
@@ -639,11 +673,9 @@ cudaError_t merge_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) 
 
 template <int D>
 cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  cudaError_t e;
-  if (D == 128 && a.tile_rows > kRows)
-    e = launch_attention_q4_tc(a, meta, st);
-  else
-    e = with_words(meta, [&](auto n) { return attention_go<D, decltype(n)::value>(a, meta, st); });
+  const cudaError_t e = a.tile_rows == 4   ? with_words(meta, [&](auto n) { return attention_go<D, 4, decltype(n)::value>(a, meta, st); })
+                        : a.tile_rows == 8 ? with_words(meta, [&](auto n) { return attention_go<D, 8, decltype(n)::value>(a, meta, st); })
+                                           : launch_attention_q4_tc(a, meta, st);
   if (e != cudaSuccess || a.max_units == 1) return e;
   return with_words(meta, [&](auto n) { return merge_go<D, decltype(n)::value>(a, meta, st); });
 }
@@ -654,8 +686,9 @@ cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_
 // sequence alone makes up to 1024 items (heads and row tiles included), of two or
 // four pages at least where it has many.  At most eight: the tensor cores' sums
 // drop the bits below their last, toward zero, and over units of 16 pages that
-// made the output of 65536 keys 1.1e-6 of its size off, over eight 0.9e-6 (210 and
-// 214 us).  The tcgen05 kernel's units, whose sums are float32's from page to page,
+// made the output of 65536 keys 1.1e-6 of its size off, over eight 0.9e-6 (191 and
+// 193 us).  One unit for up to 8 pages, without a join, is faster for many sequences at
+// once (64 of 12 heads: 29 us, not 33) and slower for few (one of 1000 keys: 19, not 13).  The tcgen05 kernel's units, whose sums are float32's from page to page,
 // have more to set up and to add up at their end: up to 128 items, of at most 16
 // pages (one sequence of 32768 keys, 40 rows: 85 us with the 32 pages that makes,
 // 65 with 16).
@@ -664,7 +697,7 @@ int q4_unit_pages(int n, int lanes, int tile_rows) {
   const long long alone = tc ? 128 : 1024;
   if (n <= 2) return n;
   const int least = tc ? 4 : n <= 4 ? 1 : n <= 64 ? 2 : 4;  // tc: n is more than 16
-  const int most = tc ? 16 : n < 8 ? n : 8;
+  const int cap = tc ? 16 : 8, most = n < cap ? n : cap;
   const long long u = ((long long)n * lanes + alone - 1) / alone;
   return u < least ? least : u > most ? most : (int)u;
 }

@@ -418,7 +418,7 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     size_t most = 0, need = 0;
     for (const Group& g : groups) {
       int tok1 = tok0;
-      for (const int rows : {8, 24}) {
+      for (const int rows : {4, 8, 24}) {
         Plan p;
         std::vector<int32_t> list;
         p.tok0 = tok0;
