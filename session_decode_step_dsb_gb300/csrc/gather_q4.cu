@@ -20,7 +20,6 @@ namespace dsbk {
 namespace {
 
 constexpr int kGatherThreads = 256;
-constexpr unsigned kGatherPages = 32768;  // in one plane of the grid
 
 template <typename T>
 __device__ __forceinline__ uint32_t two16(float a, float b);
@@ -47,7 +46,6 @@ __device__ __forceinline__ uint4 eight(uint32_t w, float2 dz) {
 
 template <int D, typename T, int N>
 __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(const uint8_t* __restrict__ pool, int hkv, int n_seq,
-                                                                   int pages,
                                                                    T* __restrict__ k, T* __restrict__ v,
                                                                    const __grid_constant__ ParamWords<N> words,
                                                                    const int32_t* __restrict__ meta_dev) {
@@ -55,8 +53,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_q4_kernel(const uint8_t
   pdl_wait();
   pdl_trigger();
   const int32_t* meta = N > 1 ? words.w : meta_dev;
-  const int item = (int)(blockIdx.z * kGatherPages + blockIdx.y), g = blockIdx.x, tid = threadIdx.x;
-  if (item >= pages) return;
+  const int item = blockIdx.y, g = blockIdx.x, tid = threadIdx.x;
   int lo = 0, hi = n_seq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -120,13 +117,12 @@ template <int D, typename T>
 cudaError_t gather_go(const void* pool, int hkv, int n_seq, long long pages, void* k, void* v, const MetaArg& meta,
                       cudaStream_t st) {
   // the heads of a page side by side: together they write whole rows of the output
-  const dim3 grid((unsigned)hkv, (unsigned)(pages < kGatherPages ? pages : kGatherPages),
-                  (unsigned)((pages + kGatherPages - 1) / kGatherPages));
+  const dim3 grid((unsigned)hkv, (unsigned)pages);
   return with_words(meta, [&](auto n) {
     ParamWords<decltype(n)::value> w;
     fill_words(meta, &w);
     return launch_kernel(gather_q4_kernel<D, T, decltype(n)::value>, grid, dim3(kGatherThreads), 0, st,
-                         static_cast<const uint8_t*>(pool), hkv, n_seq, (int)pages, static_cast<T*>(k),
+                         static_cast<const uint8_t*>(pool), hkv, n_seq, static_cast<T*>(k),
                          static_cast<T*>(v), w, meta.dev);
   });
 }

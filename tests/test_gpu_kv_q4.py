@@ -272,7 +272,8 @@ ATTN = [  # D, hq, hkv, lens, new, window
     (64, 9, 1, [1000, 260], [1, 3], [129, 0]),            # 9 and 27 rows
     (128, 20, 2, [2300, 40, 2177, 2500, 0], [2, 2, 3, 1, 0], [0, 0, 2100, 0, 0]),   # 20 and 30 rows on long caches, 20 on a short
     (128, 40, 1, [4100, 2500], [2, 1], [0, 0]),           # 80 and 40 rows
-    (128, 2, 2, [3000, 2049], [49, 17], [2200, 0])]       # 49 rows in a window; the shortest of the kind, 17 rows
+    (128, 2, 2, [3000, 2049], [49, 17], [2200, 0]),       # 49 rows in a window; the shortest of the kind, 17 rows
+    (128, 4, 1, [2300, 700, 900, 2500], [5, 1, 2, 1], [0, 0, 300, 0])]    # 20, 4, 8 and 4 rows in one call
 
 
 @pytest.mark.parametrize("case", ATTN)
