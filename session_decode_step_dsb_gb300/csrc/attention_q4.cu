@@ -87,6 +87,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 constexpr int kSlots = 5;  // half pages (K or V) on their way or in use
+constexpr int kAhead = 8;  // items known at a time: a power of two, above the halves' reach of units of a page
 
 template <int D>
 struct Q4Smem {
@@ -96,8 +97,8 @@ struct Q4Smem {
   static constexpr int join = rows + 8 * 16;                // [4 warps][D/32][32 lanes] float4
   static constexpr int stat = join + 4 * (D / 32) * 512;    // [4 warps][4] float4: M, M, sum, sum
   static constexpr int bars = stat + 4 * 64;
-  static constexpr int cursors = bars + 2 * kSlots * 8;     // the item in work, the next to ask for, "done"
-  static constexpr int bytes = cursors + 2 * (int)sizeof(Cursor) + 8;
+  static constexpr int cursors = bars + 2 * kSlots * 8;     // the items asked for, and how many those are
+  static constexpr int bytes = cursors + kAhead * (int)sizeof(Cursor) + 8;
 };
 
 // ROWS, the query rows of an item: 8, or 4, whose hi and lo parts then share a
@@ -137,36 +138,44 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
   // This CTA's items: those that start in its share of the pages.  Thread 0 asks
   // for the half pages, kSlots - 1 ahead: after its warp has left one, for the slot
   // of the one before, which the other warps have left long since.
-  Cursor* cur = reinterpret_cast<Cursor*>(smem + S::cursors);
-  Cursor* ahead = cur + 1;
-  int* done = reinterpret_cast<int*>(cur + 2);
+  Cursor* items = reinterpret_cast<Cursor*>(smem + S::cursors);  // item i of this CTA at i % kAhead
+  volatile int* known = reinterpret_cast<volatile int*>(items + kAhead);
   const long long total = meta[n_seq * kQ4SeqWords];
   const int w1 = (int)(total * (blockIdx.x + 1) / gridDim.x);
-  int ask_slot = 0, ask_which = 0;
+  int ask_slot = 0, ask_which = 0, ask_item = 0, ask_pg = 0, ask_page = 0;
   uint32_t ask_phase = 1;  // parity of the slot's last release; the first round waits for none
   bool more = false;
   auto ask = [&]() {
     if (!mbar_wait(&empty[ask_slot], ask_phase)) g_err_attention_q4 = 1u;
-    request<D>(*ahead, ask_which, meta, pool, hkv, smem + ask_slot * S::half, &full[ask_slot]);
+    Cursor* it = items + (ask_item & (kAhead - 1));
+    request<D>(*it, ask_pg, ask_page, ask_which, pool, hkv, smem + ask_slot * S::half, &full[ask_slot]);
     if (++ask_slot == kSlots) ask_slot = 0, ask_phase ^= 1;
-    if ((ask_which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
-      if (ahead->end() < w1)
-        ahead->next<ROWS>(meta, hkv, G);
-      else
-        more = false;
+    if ((ask_which ^= 1) != 0) return;
+    if (++ask_pg == it->pg_end) {
+      more = it->end() < w1;
+      if (!more) return;
+      Cursor* then = items + (++ask_item & (kAhead - 1));
+      *then = *it;
+      then->next<ROWS>(meta, hkv, G);
+      ask_pg = then->pg;
+      *known = ask_item + 1;
+      it = then;
     }
+    ask_page = meta[it->q.pg_at + ask_pg];  // not waited for before the next call
   };
   if (warp == 0) {
     const int w0 = (int)(total * blockIdx.x / gridDim.x);
     Cursor first;
     more = w0 < w1 && first.start<ROWS>(meta, n_seq, hkv, G, w0) && first.at < w1;
     if (lane == 0) {
-      *done = !more;
-      if (more) *cur = *ahead = first;
+      *known = more;
+      if (more) *items = first;
     }
+    ask_pg = first.pg;
+    if (more) ask_page = meta[first.q.pg_at + ask_pg];
   }
   __syncthreads();
-  if (*done) return;
+  if (*known == 0) return;
   if (tid == 0)  // meanwhile warp 1 stages the rows
     for (int i = 0; i < kSlots - 1 && more; ++i) ask();
 
@@ -177,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     if (lane == 0) mbar_arrive(&empty[slot]);
     if (++slot == kSlots) slot = 0, phase ^= 1;
   };
-  for (;;) {
+  for (int item = 0;; ++item) {
+    const Cursor* cur = items + (item & (kAhead - 1));
     const int len = cur->q.len, n_new = cur->q.n_new, window = cur->q.window, row0 = cur->rt * ROWS, R = G * n_new;
     if (cur->fresh) {
       if (warp == 1) {  // column g, dimensions D/4 c ..
@@ -476,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       }
     }
     const bool mine = row0 + 2 * pair < R;  // else the thread's rows are nobody's
-    // The region and statistics that a warp reads in the first round are the ones it
-    // writes in the second: nobody else reads them between.
+    // The region and statistics that a warp reads in one round are the ones it writes
+    // in the next, be it the next item's: nobody else reads them, so that the two
+    // barriers are enough.
     const auto swap = [&](auto upper, auto tiles, int to, int from) {
       constexpr int n = decltype(tiles)::value / 2, keep = decltype(upper)::value ? n : 0, give = n - keep;
       float4* dst = join + to * (NT / 2 * 32) + lane;
@@ -509,15 +520,17 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         }
       }
     };
+    const int me = item & 1 ? warp ^ 3 : warp;
     if (warp & 2)
-      swap(std::true_type{}, std::integral_constant<int, NT>{}, warp, warp ^ 2);
+      swap(std::true_type{}, std::integral_constant<int, NT>{}, me, me ^ 2);
     else
-      swap(std::false_type{}, std::integral_constant<int, NT>{}, warp, warp ^ 2);
-    const int units = cur->units, u = cur->u, tok0 = cur->q.tok0, head0 = cur->h * G;  // thread 0 moves on after the barrier
+      swap(std::false_type{}, std::integral_constant<int, NT>{}, me, me ^ 2);
+    // thread 0 may write over the item once it has passed the next barrier
+    const int units = cur->units, u = cur->u, tok0 = cur->q.tok0, head0 = cur->h * G;
     if (warp & 1)
-      swap(std::true_type{}, std::integral_constant<int, NT / 2>{}, warp ^ 2, warp ^ 3);
+      swap(std::true_type{}, std::integral_constant<int, NT / 2>{}, me ^ 2, me ^ 3);
     else
-      swap(std::false_type{}, std::integral_constant<int, NT / 2>{}, warp ^ 2, warp ^ 3);
+      swap(std::false_type{}, std::integral_constant<int, NT / 2>{}, me ^ 2, me ^ 3);
     {
       constexpr int Q = NT / 4;  // tiles of this warp
       const float2 l = unpack(lsum);
@@ -547,12 +560,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         }
       }
     }
-    if (tid == 0) {
-      *done = cur->end() >= w1;
-      if (!*done) cur->next<ROWS>(meta, hkv, G);
-    }
-    __syncthreads();
-    if (*done) break;
+    if (*known <= item + 1) break;  // the last half page was asked for long ago: no more items will be known
   }
 }
 

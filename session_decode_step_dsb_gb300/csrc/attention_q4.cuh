@@ -140,16 +140,16 @@ struct Cursor {
   __device__ __forceinline__ int end() const { return at + pg_end - u * q.u_pages; }  // pages before the next item
 };
 
-// One thread requests the K (which = 0) or V half of the page the cursor is at:
+// One thread requests the K (which = 0) or V half of page pg of the cursor's unit,
+// page `page` of the pool:
 // codes and numbers up to the sequence's last key (rounded up to four keys:
 // 16-byte pieces), or, where the page is full, the half in one piece.
 template <int D>
-__device__ __forceinline__ void request(const Cursor& c, int which, const int32_t* meta, const uint8_t* pool, int hkv,
+__device__ __forceinline__ void request(const Cursor& c, int pg, int page, int which, const uint8_t* pool, int hkv,
                                         uint8_t* dst, uint64_t* bar) {
   using B = Q4Block<D>;
-  const int page = meta[c.q.pg_at + c.pg];
   const uint8_t* src = pool + ((size_t)page * hkv + c.h) * B::bytes + (which ? B::v : 0);
-  const int keys = min(kQ4Page, (c.q.len - ((c.q.chunk0 + c.pg) << 7) + 3) & ~3);
+  const int keys = min(kQ4Page, (c.q.len - ((c.q.chunk0 + pg) << 7) + 3) & ~3);
   if (keys == kQ4Page) {
     mbar_arrive_expect_tx(bar, B::v);
     bulk_g2s(dst, src, B::v, bar);

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       int slot = 0, which = 0, asked = 0;
       bool more = true;
       auto ask = [&]() {
-        request<D>(*ahead, which, meta, pool, hkv, smem + S::raw + slot * B::v, &full[slot]);
+        request<D>(*ahead, ahead->pg, meta[ahead->q.pg_at + ahead->pg], which, pool, hkv, smem + S::raw + slot * B::v, &full[slot]);
         ++asked;
         if (++slot == kRing) slot = 0;
         if ((which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
