@@ -1,6 +1,7 @@
-// Decode attention over the paged 4-bit KV cache for more than 16 query rows on a
-// kv head (draft tokens, wide groups, prompts) over long sequences, on the 5th-generation tensor cores
-// (sm_103a).  The mathematics is that of attention_q4.cu; what differs is who
+// Decode attention over the paged 4-bit KV cache for many query rows on a kv head
+// (more than 16, but for 25 to 32: draft tokens, wide groups) over long sequences, on
+// the 5th-generation tensor cores (sm_103a).  The mathematics is that of
+// attention_q4.cu; what differs is who
 // multiplies.  With many rows the warp-level products there unpack every code
 // once for each 8 rows and are bound by instruction issue and the warp-level
 // tensor pipe; here a page is unpacked once for up to 24 rows and two MMAs of

@@ -292,16 +292,18 @@ constexpr int kQ4SeqWords = 8;
 // visit: a rule on the sequence alone, as the one on its units.  4 and 8: the warp-level
 // kernel (attention_q4.cu), whose 4-row form has half of the products (one row of 32 kv
 // heads of 128 over 4 sequences of up to 65536 keys: 193 us, in the 8-row form 214; four
-// rows of 12 heads of 64 over up to 8 pages: 33 us in both); 24: the tcgen05 one (attention_q4_tc.cu), whose items
-// unpack a page once for three times the rows but take longer to start and to end.
+// rows of 12 heads of 64 over up to 8 pages: 33 us in both).  24: the tcgen05 one
+// (attention_q4_tc.cu), whose items unpack a page once for three times the rows but take
+// longer to start and to end.
 // Measured at 8 kv heads of 128, warp-level and tcgen05: one sequence of 2048 keys and
-// 64 rows 19 and 24 us; 8 sequences of 4096 to 16384 keys, 16 rows 82 and 82 us, 24 rows
-// 117 and 98, 40 rows 177 and 161, 64 rows 255 and 237.  At heads of 64 (12 kv heads),
-// where a page holds half the work, the tcgen05 kernel took longer for all of them
-// (same sequences, 24 rows 120 and 122 us, 40 rows 187 and 207) and is not built.
+// 64 rows 19 and 24 us; 8 sequences of 4096 to 16384 keys, 16 rows 81 and 82 us, 24 rows
+// 117 and 98, 32 rows 147 and 161, 40 rows 177 and 162, 64 rows 255 and 228: a tile of 24
+// costs 2.2 tiles of 8.  At heads of 64 (12 kv heads), where a page holds half the work,
+// the tcgen05 kernel took longer for all of them (same sequences, 24 rows 120 and 122 us,
+// 40 rows 187 and 207) and is not built.
 inline int q4_tile_rows(long long rows, int n, int head_dim) {
   if (rows <= 4) return 4;
-  return head_dim == 128 && rows > 16 && n > 16 ? 24 : 8;
+  return head_dim == 128 && n > 16 && 9 * ((rows + 7) / 8) > 20 * ((rows + 23) / 24) ? 24 : 8;
 }
 // Pages per unit of a sequence that visits n of them, with `lanes` pairs of a kv
 // head and a tile of tile_rows rows: a rule on the sequence alone, not on the batch.
