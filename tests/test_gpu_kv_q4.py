@@ -711,3 +711,79 @@ def test_a_given_stream_owns_what_the_call_makes(cuda_device):
         k, v = d.kv_gather_q4(kv, b, [5], [300], d.DSB_BF16, ws, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)
+
+
+def test_two_graphs_on_one_workspace(cuda_device):
+    """Captured calls carry their metadata; partial sums in the workspace they
+    share are each replay's own, one replay after the other."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(41)
+    D, hq, hkv = 128, 8, 2
+    pool = to_dev(_pool(rng, 40, hkv, D))
+    kv = d.kv_q4_pages(pool, D)
+    calls = []
+    for lens, new in (([2000, 77], [1, 2]), ([2500, 300], [6, 1])):
+        bt, blocks, _ = _geometry(lens, new, [0, 0], rng)
+        q = to_dev(rng.standard_normal((sum(new), hq, D)).astype(np.float32))
+        calls.append((q, d.PagedBatch(bt, blocks, [0, 0], new, lens)))
+    want = [d.attention_decode_q4(q, kv, b, d.Workspace(7, hq, D, 2560)).clone() for q, b in calls]
+    ws = d.Workspace(7, hq, D, 2560)
+    outs = [torch.empty_like(w) for w in want]
+    graphs = []
+    for (q, b), o in zip(calls, outs):
+        d.attention_decode_q4(q, kv, b, ws, out=o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.attention_decode_q4(q, kv, b, ws, out=o)
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(float("nan"))
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_threads_with_their_own_workspaces(cuda_device):
+    """Four host threads on four streams, all four calls, the bits of one thread."""
+    import threading
+
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(43)
+    D, hq, hkv = 64, 6, 2
+    lens, new = [700, 200], [1, 3]
+    bt, blocks, n_pages = _geometry(lens, new, [0, 0], rng)
+    host_pool, rows = _pool(rng, n_pages, hkv, D), rng.standard_normal((4, (hq + 2 * hkv) * D)).astype(np.float32)
+    batch, rot = d.PagedBatch(bt, blocks, [0, 0], new, lens), d.Rotary()
+
+    def job(n, out):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            ws = d.Workspace(4, hq, D, 768)
+            pool = to_dev(host_pool)
+            kv = d.kv_q4_pages(pool, D)
+            for _ in range(n):
+                qkv = to_dev(rows)
+                d.kv_append_q4(qkv, hq, kv, batch, rot, ws)
+                q = qkv[:, :hq * D].unflatten(1, (hq, D))
+                att = d.attention_decode_q4(q, kv, batch, ws)
+                k, v = d.kv_gather_q4(kv, batch, [0, 0], lens, d.DSB_F16, ws)
+                d.rope_rotary(q, None, np.arange(4), rot, ws)
+            stream.synchronize()
+            out.append([x.clone() for x in (att, k, v, qkv)])
+            stream.synchronize()
+
+    want, got = [], []
+    job(1, want)
+    threads = [threading.Thread(target=job, args=(25, got)) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want[0]))
