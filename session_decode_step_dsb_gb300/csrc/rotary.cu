@@ -257,10 +257,11 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Sum of the squares of a head's D values, lane l of its D/8 holding values
-// 8l .. 8l+7.  The order is that of 32 running sums, the i-th over dimensions i,
-// i + 32, ..., added pairwise, neighbours first.  The terms of a running sum sit
-// four lanes apart; exchanges bring them into one lane.
+// Sum of the squares of a head's D values, lane l of its D/8 holding values 4l ..
+// and D/2 + 4l ...  The order is that of 32 running sums, the i-th over dimensions i,
+// i + 32, ..., added pairwise, neighbours first.  D = 64: a lane holds both terms of
+// four running sums; D = 128: two of the four terms, and an exchange with the lane
+// that holds the others leaves two running sums to each.
 template <int D>
 __device__ __forceinline__ float sum_squares(const float (&y)[8], int lane) {
   float v[8];
@@ -268,38 +269,24 @@ __device__ __forceinline__ float sum_squares(const float (&y)[8], int lane) {
   for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), pack2(y[e], y[e + 1])), v[e], v[e + 1]);
   float ss;
   if constexpr (D == 128) {
-    // lane group j = 0 .. 3 holds the j-th terms and ends with elements 2j, 2j + 1
-    const bool up = lane & 8, odd = lane & 4;
-    float a[4], b[4];  // elements 4 (j / 2) ..: the terms of this group's half, of the other
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      a[e] = up ? v[e + 4] : v[e];
-      b[e] = __shfl_xor_sync(0xFFFFFFFFu, up ? v[e] : v[e + 4], 8);
-    }
+    const bool up = lane & 8;
     float t[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float a0 = odd ? a[e + 2] : a[e], b0 = odd ? b[e + 2] : b[e];
-      const float a1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? a[e] : a[e + 2], 4);
-      const float b1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? b[e] : b[e + 2], 4);
-      // terms 0 .. 3: (a0, a1) are 0 and 1 in the lower half, 2 and 3 in the upper
-      const float x0 = up ? b0 : a0, x1 = up ? b1 : a1, y0 = up ? a0 : b0, y1 = up ? a1 : b1;
-      t[e] = __fadd_rn(__fadd_rn(__fadd_rn(x0, x1), odd ? y1 : y0), odd ? y0 : y1);
+      const float a = up ? v[e + 2] : v[e], b = up ? v[e + 6] : v[e + 4];
+      const float a1 = __shfl_xor_sync(0xFFFFFFFFu, up ? v[e] : v[e + 2], 8);
+      const float b1 = __shfl_xor_sync(0xFFFFFFFFu, up ? v[e + 4] : v[e + 6], 8);
+      t[e] = __fadd_rn(__fadd_rn(__fadd_rn(a, a1), up ? b1 : b), up ? b : b1);
     }
     ss = __fadd_rn(t[0], t[1]);
-    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 4));
     ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 8));
   } else {
-    const bool up = lane & 4;
-    float t[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      t[e] = __fadd_rn(up ? v[e + 4] : v[e], __shfl_xor_sync(0xFFFFFFFFu, up ? v[e] : v[e + 4], 4));
-    ss = __fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3]));
-    ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 4));
+    ss = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[4]), __fadd_rn(v[1], v[5])),
+                   __fadd_rn(__fadd_rn(v[2], v[6]), __fadd_rn(v[3], v[7])));
   }
-  ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 1));
-  return __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, 2));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xFFFFFFFFu, ss, o));
+  return ss;
 }
 
 // How the cache rows are stored.
@@ -345,8 +332,9 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float
 }
 
 // grid (n_tok, shares of the heads): D/8 lanes hold one head's vector, eight values
-// each, so that its norm, its extremes and the partner of a rotated value stay inside
-// a warp.  A lane handles the same dimensions of one head after the other, the next
+// each: four of its first half and the four at the same place of its second, so that a
+// rotated value's partner is in the lane (both pair layouts, the whole head rotated; else
+// it is fetched from shared memory) and norm and extremes stay inside a warp.  A lane handles the same dimensions of one head after the other, the next
 // one's values on their way, with one set of sines and cosines.  Head h of the row:
 // query heads, then key heads, then value heads.  With many tokens one CTA takes all
 // heads of its token, so the token's set-up is paid once.  Bound by instruction
@@ -370,15 +358,15 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
   pdl_trigger();
   const int t = blockIdx.x, tid = threadIdx.x, l = tid & (LPH - 1), slot = tid / LPH;
   const int heads = hq + 2 * hkv, rd = tab.rd, half = rd >> 1;
-  const bool touched = q_norm || 8 * l < rd;  // query values past the rotated part stay where they are
-  float* row = qkv + (size_t)t * stride + 8 * l;
+  const int d0 = 4 * l, d1 = D / 2 + 4 * l;  // the lane's dimensions
+  // query values past the rotated part stay where they are
+  const bool touched0 = q_norm || d0 < rd, touched1 = q_norm || d1 < rd;
+  float* row = qkv + (size_t)t * stride;
   float4 x[2];
   auto fetch = [&](int h) {
     x[0] = x[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (h < heads && (h >= hq || touched)) {
-      x[0] = __ldcg(reinterpret_cast<const float4*>(row + h * D));
-      x[1] = __ldcg(reinterpret_cast<const float4*>(row + h * D) + 1);
-    }
+    if (h < heads && (h >= hq || touched0)) x[0] = __ldcg(reinterpret_cast<const float4*>(row + h * D + d0));
+    if (h < heads && (h >= hq || touched1)) x[1] = __ldcg(reinterpret_cast<const float4*>(row + h * D + d1));
   };
   int h = blockIdx.y * SLOTS + slot;
   fetch(h);
@@ -407,17 +395,10 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
     sines[i] = 0.0f;
   }
   __syncthreads();
-  const int turned = min(max(rd - 8 * l, 0), 8);  // of this lane's eight dimensions
-  // The partners of a whole lane's values are a whole lane's where half the rotated
-  // part is lanes; else they are fetched one by one.
-  const bool lanes = (rd & 15) == 0;
-  const int src = (tid & 31 & ~(LPH - 1)) + (turned == 0 ? l : 8 * l >= half ? l - half / 8 : l + half / 8);
-  float4 c[2], s[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    c[e] = *reinterpret_cast<const float4*>(&cosines[8 * l + 4 * e]);
-    s[e] = *reinterpret_cast<const float4*>(&sines[8 * l + 4 * e]);
-  }
+  const int turned0 = min(max(rd - d0, 0), 4), turned1 = min(max(rd - d1, 0), 4);  // of its dimensions
+  const bool whole = rd == D;
+  const float4 c[2] = {*reinterpret_cast<const float4*>(&cosines[d0]), *reinterpret_cast<const float4*>(&cosines[d1])};
+  const float4 s[2] = {*reinterpret_cast<const float4*>(&sines[d0]), *reinterpret_cast<const float4*>(&sines[d1])};
   for (;;) {
     const bool live = h < heads, is_q = h < hq, is_k = !is_q && h < hq + hkv, is_v = live && !is_q && !is_k;
     float y[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -431,7 +412,7 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
         const f2 inv2 = pack2(inv, inv);
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(norm + 8 * l + e));
+          const float4 w = __ldg(reinterpret_cast<const float4*>(norm + (e ? d1 : d0)));
           unpack2(mul2(mul2(pack2(y[e], y[e + 1]), inv2), pack2(w.x, w.y)), y[e], y[e + 1]);
           unpack2(mul2(mul2(pack2(y[e + 2], y[e + 3]), inv2), pack2(w.z, w.w)), y[e + 2], y[e + 3]);
         }
@@ -442,19 +423,19 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
       if (tab.interleaved) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
-      } else if (lanes) {
+      } else if (whole) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], src);
+        for (int e = 0; e < 8; ++e) p[e] = y[e ^ 4];
       } else {
         float* mine = swap + slot * D;
         __syncwarp();
-        *reinterpret_cast<float4*>(mine + 8 * l) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4*>(mine + 8 * l + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<float4*>(mine + d0) = make_float4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<float4*>(mine + d1) = make_float4(y[4], y[5], y[6], y[7]);
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int dim = 8 * l + e;
-          p[e] = mine[e >= turned ? dim : dim >= half ? dim - half : dim + half];
+          const int dim = e < 4 ? d0 + e : d1 + e - 4;
+          p[e] = mine[dim >= rd ? dim : dim >= half ? dim - half : dim + half];
         }
       }
       if (!is_v) {
@@ -465,20 +446,18 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
           unpack2(mul2(pack2(y[4 * i + 2], y[4 * i + 3]), pack2(c[i].z, c[i].w)), a[2], a[3]);
           unpack2(mul2(pack2(p[4 * i], p[4 * i + 1]), pack2(s[i].x, s[i].y)), b[0], b[1]);
           unpack2(mul2(pack2(p[4 * i + 2], p[4 * i + 3]), pack2(s[i].z, s[i].w)), b[2], b[3]);
-          if (turned == 8) {
+          if (whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[4 * i + e] = __fadd_rn(a[e], b[e]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[4 * i + e] = 4 * i + e < turned ? __fadd_rn(a[e], b[e]) : y[4 * i + e];
+            for (int e = 0; e < 4; ++e) y[4 * i + e] = e < (i ? turned1 : turned0) ? __fadd_rn(a[e], b[e]) : y[4 * i + e];
           }
         }
       }
     }
-    if (is_q && touched) {
-      *reinterpret_cast<float4*>(row + h * D) = make_float4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<float4*>(row + h * D + 4) = make_float4(y[4], y[5], y[6], y[7]);
-    }
+    if (is_q && touched0) *reinterpret_cast<float4*>(row + h * D + d0) = make_float4(y[0], y[1], y[2], y[3]);
+    if (is_q && touched1) *reinterpret_cast<float4*>(row + h * D + d1) = make_float4(y[4], y[5], y[6], y[7]);
     const int g = h - hq - (is_k ? 0 : hkv);  // kv head
     if constexpr (std::is_same<Store, StoreQ4>::value) {
       if (__any_sync(0xFFFFFFFFu, live && !is_q)) {
@@ -498,21 +477,18 @@ __global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float
           const uint32_t code = q4_codes(y, __half2float(dh), __half2float(zh));
           using B = Q4Block<D>;
           uint8_t* blk = kc + ((size_t)page * hkv + g) * B::bytes;
-          if (is_k) {
-            *reinterpret_cast<uint32_t*>(blk + r * (D / 2) + 4 * l) = code;
-          } else {
-            uint8_t* dst = blk + B::v + (r >> 1) * D + 8 * l + 2 * (r & 1);
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
-            *reinterpret_cast<uint16_t*>(dst + 4) = (uint16_t)(code >> 16);
-          }
+          // 16 bits of codes for four dimensions; V's words hold a key pair's
+          uint8_t* dst = is_k ? blk + r * (D / 2) + d0 / 2 : blk + B::v + (r >> 1) * D + d0 + 2 * (r & 1);
+          *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+          *reinterpret_cast<uint16_t*>(dst + (is_k ? D / 4 : D / 2)) = (uint16_t)(code >> 16);
           if (l == 0) *reinterpret_cast<__half2*>(blk + (is_k ? B::kz : B::vz) + 4 * r) = __halves2half2(dh, zh);
         }
       }
     } else {
       if (live && !is_q) {
-        uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + 8 * l) * 2;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]),
-                                                    pack16<Store>(y[4], y[5]), pack16<Store>(y[6], y[7]));
+        uint8_t* dst = (is_k ? kc : vc) + ((((size_t)page * hkv + g) * kQ4Page + r) * D + d0) * 2;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<Store>(y[0], y[1]), pack16<Store>(y[2], y[3]));
+        *reinterpret_cast<uint2*>(dst + D) = make_uint2(pack16<Store>(y[4], y[5]), pack16<Store>(y[6], y[7]));
       }
     }
     h = next;
