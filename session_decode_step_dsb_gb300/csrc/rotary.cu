@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kRotThreads) rope_rotary_kernel(float* __restr
 // ---- append --------------------------------------------------------------------
 
 // Small CTAs: a token's set-up (its sequence, page, sines and cosines) is a chain
-// that others hide.  5178 tokens of 56 heads, append and read-back: 32 threads 75 us,
-// 64 65, 128 with 7 CTAs an SM (72 registers) 62, with 8 63, 256 68.
+// that others hide.  5178 tokens of 56 heads, append and read-back: 64 threads 61 us,
+// 128 with 6, 7 or 8 CTAs an SM 62, 58 and 58, 256 62 (all as far as registers allow).
 constexpr int kAppThreads = 128, kAppPerSm = 7;
 
 // Two float32 operations at once, each rounded as by itself.
@@ -338,7 +338,7 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float
 // one's values on their way, with one set of sines and cosines.  Head h of the row:
 // query heads, then key heads, then value heads.  With many tokens one CTA takes all
 // heads of its token, so the token's set-up is paid once.  Bound by instruction
-// issue: those 5178 tokens move 205 MB (30 us at the copy rate) in 51 us.  16 tokens:
+// issue: those 5178 tokens move 205 MB (30 us at the copy rate) in 45 us.  16 tokens:
 // 4.5 us, the latency of the chain.
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
