@@ -697,7 +697,7 @@ def _empty_on(stream, shape, dtype, device):
     what the current stream has freed may still be in use there."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)      # the current stream's
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
@@ -810,17 +810,18 @@ def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws:
     pool = kv._tensors[0]
     dev = _current_device(pool, "the page pool")
     shape = (max(sum(ca.tolist()), 0), kv.n_kv_heads, kv.head_dim)
-    outs = [k, v]
-    for i, name in enumerate("kv"):
-        if outs[i] is None:
-            outs[i] = _empty_on(stream, shape, kind, pool.device)
-            continue
-        _need(outs[i], 2 * shape[0] * shape[1] * shape[2], name)
-        if outs[i].dtype != kind or not outs[i].is_contiguous():
-            raise ValueError(f"{name} must be contiguous {kind}")
-    _check(lib().dsb_kv_gather_q4(ctypes.byref(kv), batch.ref, pf, pc, dtype, _dev_ptr(outs[0], dev, "k"),
-                                  _dev_ptr(outs[1], dev, "v"), ws.handle, _raw_stream(stream, dev)))
-    return outs[0], outs[1]
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _need(t, 2 * shape[0] * shape[1] * shape[2], name)
+            if t.dtype != kind or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {kind}")
+    if k is None:
+        k = _empty_on(stream, shape, kind, pool.device)
+    if v is None:
+        v = _empty_on(stream, shape, kind, pool.device)
+    _check(lib().dsb_kv_gather_q4(ctypes.byref(kv), batch.ref, pf, pc, dtype, _dev_ptr(k, dev, "k"),
+                                  _dev_ptr(v, dev, "v"), ws.handle, _raw_stream(stream, dev)))
+    return k, v
 
 
 # ---------------------------------------------------------------- decode step
