@@ -334,14 +334,12 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
-            {
-              f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]), pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
-              if constexpr (kFew) {  // hi parts' and lo parts' columns
-                const float2 v = unpack(acc);
-                acc = add2(acc, pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, 2), __shfl_xor_sync(0xFFFFFFFFu, v.y, 2)));
-              }
-              x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
+            f2 acc = add2(pack(sc[t][0][2 * h], sc[t][0][2 * h + 1]), pack(sc[t][1][2 * h], sc[t][1][2 * h + 1]));
+            if constexpr (kFew) {  // hi parts' and lo parts' columns
+              const float2 v = unpack(acc);
+              acc = add2(acc, pack(__shfl_xor_sync(0xFFFFFFFFu, v.x, 2), __shfl_xor_sync(0xFFFFFFFFu, v.y, 2)));
             }
+            x[t][h] = fma2(pack(dz.x, dz.x), acc, mul2(pack(dz.y, dz.y), sum2));
           }
       }
       release();
@@ -407,28 +405,26 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
           for (int h = 0; h < 2; ++h) {
             const float2 dz =
                 __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
-            {
-              f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
-              const float2 v = unpack(fma2(scale2, x[t][h], pack(-M0, -M1)));
-              float2 pr = make_float2(ex2(v.x), ex2(v.y));
-              if (!whole) {  // a hidden key's numbers may be anything
-                const int key = key0 + 16 * t + 8 * h + g;
-                const bool no0 = hidden(key, hi0), no1 = hidden(key, hi1);
-                if (no0) pr.x = 0.0f;
-                if (no1) pr.y = 0.0f;
-                d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
-                z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
-              }
-              const f2 pp = pack(pr.x, pr.y);
-              lsum = add2(lsum, pp);
-              zsum = fma2(pp, z, zsum);
-              split(mul2(pp, d), ph[h], pl[h]);
-              if constexpr (kFew) {
-                ph[h] = transpose8(first_half ? ph[h] : pl[h]);
-              } else {
-                ph[h] = transpose8(ph[h]);
-                pl[h] = transpose8(pl[h]);
-              }
+            f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
+            const float2 v = unpack(fma2(scale2, x[t][h], pack(-M0, -M1)));
+            float2 pr = make_float2(ex2(v.x), ex2(v.y));
+            if (!whole) {  // a hidden key's numbers may be anything
+              const int key = key0 + 16 * t + 8 * h + g;
+              const bool no0 = hidden(key, hi0), no1 = hidden(key, hi1);
+              if (no0) pr.x = 0.0f;
+              if (no1) pr.y = 0.0f;
+              d = pack(no0 ? 0.0f : dz.x, no1 ? 0.0f : dz.x);
+              z = pack(no0 ? 0.0f : dz.y, no1 ? 0.0f : dz.y);
+            }
+            const f2 pp = pack(pr.x, pr.y);
+            lsum = add2(lsum, pp);
+            zsum = fma2(pp, z, zsum);
+            split(mul2(pp, d), ph[h], pl[h]);
+            if constexpr (kFew) {
+              ph[h] = transpose8(first_half ? ph[h] : pl[h]);
+            } else {
+              ph[h] = transpose8(ph[h]);
+              pl[h] = transpose8(pl[h]);
             }
           }
           uint32_t v0[W], v1[W];
@@ -448,17 +444,15 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
             __half2 h0[4], h1[4];
             q4_unpack(v0[w], h0);
             q4_unpack(v1[w], h1);
-            {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
+                  ph[0], ph[1]);
+            if constexpr (!kFew) {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
-                    ph[0], ph[1]);
-              if constexpr (!kFew) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  mma(o[2 * w + i], bits(h0[2 * i]), bits(h0[2 * i + 1]), bits(h1[2 * i]), bits(h1[2 * i + 1]),
-                      pl[0], pl[1]);
-              }
+                    pl[0], pl[1]);
             }
           }
         }
@@ -681,9 +675,13 @@ cudaError_t merge_go(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) 
 
 template <int D>
 cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st) {
-  const cudaError_t e = a.tile_rows == 4   ? with_words(meta, [&](auto n) { return attention_go<D, 4, decltype(n)::value>(a, meta, st); })
-                        : a.tile_rows == 8 ? with_words(meta, [&](auto n) { return attention_go<D, 8, decltype(n)::value>(a, meta, st); })
-                                           : launch_attention_q4_tc(a, meta, st);
+  cudaError_t e;
+  if (a.tile_rows == 4)
+    e = with_words(meta, [&](auto n) { return attention_go<D, 4, decltype(n)::value>(a, meta, st); });
+  else if (a.tile_rows == 8)
+    e = with_words(meta, [&](auto n) { return attention_go<D, 8, decltype(n)::value>(a, meta, st); });
+  else
+    e = launch_attention_q4_tc(a, meta, st);
   if (e != cudaSuccess || a.max_units == 1) return e;
   return with_words(meta, [&](auto n) { return merge_go<D, decltype(n)::value>(a, meta, st); });
 }
@@ -696,10 +694,10 @@ cudaError_t attention_pick(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_
 // drop the bits below their last, toward zero, and over units of 16 pages that
 // made the output of 65536 keys 1.1e-6 of its size off, over eight 0.9e-6 (191 and
 // 193 us).  One unit for up to 8 pages, without a join, is faster for many sequences at
-// once (64 of 12 heads: 29 us, not 33) and slower for few (one of 1000 keys: 19, not 13).  The tcgen05 kernel's units, whose sums are float32's from page to page,
-// have more to set up and to add up at their end: up to 128 items, of at most 16
-// pages (one sequence of 32768 keys, 40 rows: 85 us with the 32 pages that makes,
-// 65 with 16).
+// once (64 of 12 heads: 29 us, not 33) and slower for few (one of 1000 keys: 19, not 13).
+// The tcgen05 kernel's units, whose sums are float32's from page to page, have more to
+// set up and to add up at their end: up to 128 items, of at most 16 pages (one sequence
+// of 32768 keys, 40 rows: 85 us with the 32 pages that makes, 65 with 16).
 int q4_unit_pages(int n, int lanes, int tile_rows) {
   const bool tc = tile_rows > 8;
   const long long alone = tc ? 128 : 1024;

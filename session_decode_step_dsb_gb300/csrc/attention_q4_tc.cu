@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
       int slot = 0, which = 0, asked = 0;
       bool more = true;
       auto ask = [&]() {
-        request<D>(*ahead, ahead->pg, meta[ahead->q.pg_at + ahead->pg], which, pool, hkv, smem + S::raw + slot * B::v, &full[slot]);
+        request<D>(*ahead, ahead->pg, meta[ahead->q.pg_at + ahead->pg], which, pool, hkv, smem + S::raw + slot * B::v,
+                   &full[slot]);
         ++asked;
         if (++slot == kRing) slot = 0;
         if ((which ^= 1) == 0 && ++ahead->pg == ahead->pg_end) {
@@ -327,18 +328,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
           last[i] = live ? len - n_new + j : len - 1;
           where[i] = (cur->q.tok0 + j) * hq + cur->h * G + gi;
         }
-        {
-          // eight dimensions in the order of their nibbles, (0, 4), (1, 5), ..
+        // eight dimensions in the order of their nibbles, (0, 4), (1, 5), ..
 #pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            uint4 a, b;
-            split(pack(x[8 * w], x[8 * w + 4]), a.x, b.x);
-            split(pack(x[8 * w + 1], x[8 * w + 5]), a.y, b.y);
-            split(pack(x[8 * w + 2], x[8 * w + 6]), a.z, b.z);
-            split(pack(x[8 * w + 3], x[8 * w + 7]), a.w, b.w);
-            *reinterpret_cast<uint4*>(hi + (c * (D / 64) + w) * S::q_k) = a;
-            *reinterpret_cast<uint4*>(lo + (c * (D / 64) + w) * S::q_k) = b;
-          }
+        for (int w = 0; w < D / 64; ++w) {
+          uint4 a, b;
+          split(pack(x[8 * w], x[8 * w + 4]), a.x, b.x);
+          split(pack(x[8 * w + 1], x[8 * w + 5]), a.y, b.y);
+          split(pack(x[8 * w + 2], x[8 * w + 6]), a.z, b.z);
+          split(pack(x[8 * w + 3], x[8 * w + 7]), a.w, b.w);
+          *reinterpret_cast<uint4*>(hi + (c * (D / 64) + w) * S::q_k) = a;
+          *reinterpret_cast<uint4*>(lo + (c * (D / 64) + w) * S::q_k) = b;
         }
       }
       fence_proxy_async_smem();  // q is the first product's operand
@@ -470,10 +469,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
           const int c = i >> 1, e = 2 * (i & 1);
-          {
-            const float4 pr = pairs[4 * c + 2 * part + (i & 1)];
-            x[i] = fma2(kd, add2(pack(hi[c][e], hi[c][e + 1]), pack(lo[c][e], lo[c][e + 1])), mul2(kz, pack(pr.z, pr.w)));
-          }
+          const float4 pr = pairs[4 * c + 2 * part + (i & 1)];
+          x[i] = fma2(kd, add2(pack(hi[c][e], hi[c][e + 1]), pack(lo[c][e], lo[c][e + 1])), mul2(kz, pack(pr.z, pr.w)));
         }
       }
       const float limit = 14.0f - vd_log;
@@ -487,17 +484,15 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
 #pragma unroll
           for (int i = 0; i < PAIRS; ++i) {
             const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
-            {
-              const float4 pr = pairs[row / 2];
-              float2 t = unpack(fma2(pack(pr.x, pr.y), x[i], pack(vd_log, vd_log)));
-              if (!whole) {
-                if (hidden(row)) t.x = -INFINITY;
-                if (hidden(row + 1)) t.y = -INFINITY;
-              }
-              t.x = warp_max(t.x);
-              t.y = warp_max(t.y);
-              if (lane == 0) *reinterpret_cast<float2*>(&top[quarter * ROWS + row]) = t;
+            const float4 pr = pairs[row / 2];
+            float2 t = unpack(fma2(pack(pr.x, pr.y), x[i], pack(vd_log, vd_log)));
+            if (!whole) {
+              if (hidden(row)) t.x = -INFINITY;
+              if (hidden(row + 1)) t.y = -INFINITY;
             }
+            t.x = warp_max(t.x);
+            t.y = warp_max(t.y);
+            if (lane == 0) *reinterpret_cast<float2*>(&top[quarter * ROWS + row]) = t;
           }
           meet();
           if (tid < ROWS) {
@@ -515,13 +510,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
               const int row = 8 * (i >> 1) + 4 * part + 2 * (i & 1);
-              {
-                const float2 f = *reinterpret_cast<const float2*>(&fac[row]);
-                lsum[i] = mul2(lsum[i], pack(f.x, f.y));
-                zsum[i] = mul2(zsum[i], pack(f.x, f.y));
-                acc[2 * i] *= f.x;
-                acc[2 * i + 1] *= f.y;
-              }
+              const float2 f = *reinterpret_cast<const float2*>(&fac[row]);
+              lsum[i] = mul2(lsum[i], pack(f.x, f.y));
+              zsum[i] = mul2(zsum[i], pack(f.x, f.y));
+              acc[2 * i] *= f.x;
+              acc[2 * i + 1] *= f.y;
             }
           }
         }

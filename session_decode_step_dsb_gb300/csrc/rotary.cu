@@ -334,23 +334,21 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float
 // grid (n_tok, shares of the heads): D/8 lanes hold one head's vector, eight values
 // each: four of its first half and the four at the same place of its second, so that a
 // rotated value's partner is in the lane (both pair layouts, the whole head rotated; else
-// it is fetched from shared memory) and norm and extremes stay inside a warp.  A lane handles the same dimensions of one head after the other, the next
-// one's values on their way, with one set of sines and cosines.  Head h of the row:
-// query heads, then key heads, then value heads.  With many tokens one CTA takes all
-// heads of its token, so the token's set-up is paid once.  Bound by instruction
-// issue: those 5178 tokens move 205 MB (30 us at the copy rate) in 45 us.  16 tokens:
-// 4.5 us, the latency of the chain.
+// it is fetched from shared memory) and norm and extremes stay inside a warp.  A lane
+// handles the same dimensions of one head after the other, the next one's values on
+// their way, with one set of sines and cosines.  Head h of the row: query heads, then
+// key heads, then value heads.  With many tokens one CTA takes all heads of its token,
+// so the token's set-up is paid once.  Bound by instruction issue: those 5178 tokens
+// move 205 MB (30 us at the copy rate) in 45 us.  16 tokens: 4.5 us, the latency of the
+// chain.
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
 template <int D, typename Store, int N>
-__global__ void __launch_bounds__(kAppThreads, kAppPerSm) kv_append_kernel(float* __restrict__ qkv, long long stride, int hq,
-                                                                int hkv, uint8_t* __restrict__ kc,
-                                                                uint8_t* __restrict__ vc,
-                                                                const __grid_constant__ Turns<64> tab,
-                                                                const float* __restrict__ q_norm,
-                                                                const float* __restrict__ k_norm, float eps, int n_seq,
-                                                                const __grid_constant__ ParamWords<N> words,
-                                                                const int32_t* __restrict__ meta_dev) {
+__global__ void __launch_bounds__(kAppThreads, kAppPerSm)
+    kv_append_kernel(float* __restrict__ qkv, long long stride, int hq, int hkv, uint8_t* __restrict__ kc,
+                     uint8_t* __restrict__ vc, const __grid_constant__ Turns<64> tab, const float* __restrict__ q_norm,
+                     const float* __restrict__ k_norm, float eps, int n_seq,
+                     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   constexpr int LPH = D / 8, SLOTS = kAppThreads / LPH;
   __shared__ __align__(16) float cosines[D], sines[D];  // of every dimension; a sine with the sign its term takes
   __shared__ __align__(16) float swap[kAppThreads * 8];
