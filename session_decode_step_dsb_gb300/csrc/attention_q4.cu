@@ -481,11 +481,14 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
     }
     const bool mine = row0 + 2 * pair < R;  // else the thread's rows are nobody's
     // The region and statistics that a warp reads in one round are the ones it writes
-    // in the next, be it the next item's: nobody else reads them, so that the two
-    // barriers are enough.
+    // in the next, be it the next item's: no other warp reads them, so that the two
+    // barriers are enough.  A lane writes the tiles that it has read itself, but the
+    // statistics that all lanes have read are written by the first of them: the warp
+    // meets before each round's writes.
     const auto swap = [&](auto upper, auto tiles, int to, int from) {
       constexpr int n = decltype(tiles)::value / 2, keep = decltype(upper)::value ? n : 0, give = n - keep;
       float4* dst = join + to * (NT / 2 * 32) + lane;
+      __syncwarp();
       if (mine) {
 #pragma unroll
         for (int t = 0; t < n; ++t)
