@@ -27,10 +27,10 @@
 // end, the units' by a second kernel in unit order (a sequence of one unit needs
 // none).
 //
-// The running reference of the exponentials is the largest s_k plus the log of
-// the largest d_k (of V) of the same 32 keys, so that the weights that enter the
-// fp16 split are at most 2^14 whatever the scales are; p_k itself and the sums
-// over it are float32.
+// The running reference of the exponentials is the largest s_k + log d_k (d_k: V's
+// scale of the same key) over the keys that the row sees, so that the weights that
+// enter the fp16 split are at most 2^14 whatever the scales are; p_k itself and the
+// sums over it are float32.
 //
 // Measured: 4 sequences of 16384 to 65536 keys, 32 kv heads of 128, one row each
 // (820 MB of pages): 193 us with the join, 4.3 TB/s, 0.63 of the copy rate.  Bound by
@@ -349,18 +349,19 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
       __syncwarp();
       if (some) {
         const uint8_t* blk = smem + slot * S::half;
-        // the largest scale of V among the 32 keys (bits of an fp16 that is not negative)
-        uint32_t vd = *reinterpret_cast<const uint16_t*>(blk + B::kz + (32 * warp + lane) * 4);
-        if (!whole && (key0 + lane > last_hi || key0 + lane < any_lo)) vd = 0;
-        vd = __reduce_max_sync(0xFFFFFFFFu, vd);
-        const float vd_log = lg2(fmaxf(__half2float(__ushort_as_half((unsigned short)vd)), 0x1p-24f));
+        __half2 vn[2][2];  // V's numbers of the thread's keys
         {
+          // score plus the log of the key's own V scale, for each row over the keys
+          // that it sees: what another row sees, or a key without weight, does not
+          // move a row's reference
           float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float2 v = unpack(x[t][h]);
+              vn[t][h] = *reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4);
+              const float vd_log = lg2(fmaxf(__low2float(vn[t][h]), 0x1p-24f));
+              float2 v = unpack(fma2(scale2, x[t][h], pack(vd_log, vd_log)));
               if (!whole) {
                 const int key = key0 + 16 * t + 8 * h + g;
                 if (hidden(key, hi0)) v.x = -INFINITY;
@@ -374,12 +375,9 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
             top0 = fmaxf(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, s4));
             top1 = fmaxf(top1, __shfl_xor_sync(0xFFFFFFFFu, top1, s4));
           }
-          const float2 sc2 = unpack(scale2);
-          top0 = __fmaf_rn(sc2.x, top0, vd_log);
-          top1 = __fmaf_rn(sc2.y, top1, vd_log);
-          // The reference is set 2^10 below the largest weight and moves only when
+          // The reference is set 2^10 below the largest weight times scale and moves only when
           // that has grown to 2^14 of it: fp16 ends at 2^16, and a low part is never
-          // coarser than 2^-35 of the largest weight.
+          // coarser than 2^-35 of the largest.
           if (__any_sync(0xFFFFFFFFu, top0 > M0 + 14.0f || top1 > M1 + 14.0f)) {
             const float to0 = top0 > M0 + 14.0f ? top0 - 10.0f : M0;
             const float to1 = top1 > M1 + 14.0f ? top1 - 10.0f : M1;
@@ -403,8 +401,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
           uint32_t ph[2], pl[2];  // P^T: keys 2c, 2c + 1 of row g, hi and lo, of the tile's halves; of column g
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float2 dz =
-                __half22float2(*reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4));
+            const float2 dz = __half22float2(vn[t][h]);
             f2 d = pack(dz.x, dz.x), z = pack(dz.y, dz.y);
             const float2 v = unpack(fma2(scale2, x[t][h], pack(-M0, -M1)));
             float2 pr = make_float2(ex2(v.x), ex2(v.y));

@@ -5,8 +5,9 @@ test_gpu_kv_q4."""
 import numpy as np
 import pytest
 
-from tests.gpu_util import to_dev
-from tests.test_gpu_kv_q4 import _dsb, _pool
+from oracle import kv_q4 as oq4
+from tests.gpu_util import to_dev, to_host
+from tests.test_gpu_kv_q4 import P, _dsb, _pool
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,71 @@ def test_one_cta_after_many_units(cuda_device, D, group, new):
     for _ in range(20):
         assert torch.equal(d.attention_decode_q4(q, kv, batch, ws), want)
     d.device_error()
+
+
+def _hidden_case(D, T, L, rng, vsize):
+    """A pool whose V vectors are of size ``vsize``, the last T keys new."""
+    n = -(-L // P)
+    return _pool(rng, n, 1, D, vsize), [list(range(n))]
+
+
+def _numbers(pool, key, D, which, d=None, z=None):
+    """Copy of the pool with key ``key``'s (d, z) of K (0) or V (1) replaced."""
+    out = pool.copy()
+    at = P * D // 2 + which * (P * D // 2 + 4 * P) + 4 * (key % P)
+    for i, x in ((0, d), (2, z)):
+        if x is not None:
+            out[key // P, :, at + i:at + i + 2] = np.frombuffer(np.float16(x).tobytes(), np.uint8)
+    return out
+
+
+FORMS = [(64, 1, 3, 200), (64, 4, 2, 135), (128, 2, 2, 129), (128, 3, 4, 300), (128, 8, 3, 2400)]  # D, hq, T, L
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+def test_a_row_does_not_depend_on_keys_it_does_not_see(cuda_device, D, hq, T, L):
+    """Whatever the numbers of a later draft's key are, the rows before it keep
+    their bits (both kernels, 4 and 8 rows a product)."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(D + L)
+    pool, bt = _hidden_case(D, T, L, rng, 1e-3)
+    q = to_dev(rng.standard_normal((T, hq, D)).astype(np.float32))
+    b, ws = d.PagedBatch(bt, [len(bt[0])], [0], [T], [L]), d.Workspace(T, hq, D, L)
+    clean = d.attention_decode_q4(q, d.kv_q4_pages(to_dev(pool), D), b, ws)
+    assert torch.isfinite(clean).all()
+    nan, inf = float("nan"), float("inf")
+    for key in (L - 1, L - T + 1):
+        first = key - (L - T)                # the row that is the first to see it
+        for which, dd, z in ((0, nan, nan), (0, 60000.0, 0.0), (1, nan, nan), (1, nan, 0.0), (1, inf, None), (1, 60000.0, 0.0),
+                             (1, 2.0 ** -24, 0.0), (1, 0.0, 0.0)):
+            got = d.attention_decode_q4(q, d.kv_q4_pages(to_dev(_numbers(pool, key, D, which, dd, z)), D), b, ws)
+            assert torch.equal(got[:first], clean[:first]), (key, which, dd)
+            if not np.isfinite(dd):
+                assert not torch.isfinite(got[first:]).any()
+    d.device_error()
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+@pytest.mark.parametrize("ratio", [16, 20, 25])
+def test_scales_far_apart(cuda_device, D, hq, T, L, ratio):
+    """Every 20th key has V vectors 2^ratio times the others' and a score 2^-(ratio
+    + 24) of theirs in weight, so that it does not count: the keys that do keep
+    their bits."""
+    d = _dsb()
+    rng = np.random.default_rng(ratio)
+    n = -(-L // P)
+    k = rng.standard_normal((n * P, D)) * 0.02
+    k[:, 0] = 0.0
+    v = rng.standard_normal((n * P, D)) * 2.0 ** -11
+    k[::20, 0], v[::20] = -20.0, v[::20] * 2.0 ** ratio
+    pool = np.stack([oq4.pack_block(*oq4.quantise(k[a:a + P]), *oq4.quantise(v[a:a + P])) for a in range(0, n * P, P)])[:, None]
+    q = (rng.standard_normal((T, hq, D)) * 0.1).astype(np.float32)
+    q[..., 0] = (ratio + 24) * np.log(2) * np.sqrt(D) / 20
+    kvals, vvals = oq4.pool_values(pool, D)
+    bt = [list(range(n))]
+    want, bound = oq4.attention(q, kvals, vvals, bt, [n], [0], [T], [L], oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [n], [0], [T], [L]),
+                                        d.Workspace(T, hq, D, L)))
+    worst = (np.abs(got - want) / bound).max()
+    assert worst <= 1, f"{worst:.2f} of the bound"
