@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               vn[t][h] = *reinterpret_cast<const __half2*>(blk + B::kz + (32 * warp + 16 * t + 8 * h + g) * 4);
-              const float vd_log = lg2(fmaxf(__low2float(vn[t][h]), 0x1p-24f));
+              const float vd_log = lg2(fmaxf(__low2float(vn[t][h]), kLeastScale));
               float2 v = unpack(fma2(scale2, x[t][h], pack(vd_log, vd_log)));
               if (!whole) {
                 const int key = key0 + 16 * t + 8 * h + g;

@@ -23,6 +23,11 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// What a V scale counts as at least in a row's reference.  Scales are fp16, 2^-24 or
+// more, or 0: then the weight p_k d_k is 0 and needs no room in fp16, only a p_k (at
+// most 2^14 over this) whose sums, of p_k z_k too, stay within float32.
+constexpr float kLeastScale = 0x1p-60f;
+
 // Two float32 at once.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack(float a, float b) {

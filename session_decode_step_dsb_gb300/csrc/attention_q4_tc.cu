@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
         vd = dz.x;
         vz = dz.y;
       }
-      const float vd_log = lg2(fmaxf(vd, 0x1p-24f));
+      const float vd_log = lg2(fmaxf(vd, kLeastScale));
 
       // ---- the scores
       if (!mbar_wait(scores, s_phase)) g_err_attention_q4_tc = 1u;

@@ -102,3 +102,27 @@ def test_scales_far_apart(cuda_device, D, hq, T, L, ratio):
                                         d.Workspace(T, hq, D, L)))
     worst = (np.abs(got - want) / bound).max()
     assert worst <= 1, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+def test_a_key_without_values_that_carries_the_weight(cuda_device, D, hq, T, L):
+    """A first key whose V vector is zero (its scale is 0) takes all but 2^-50 of
+    the weight: the output is that small, and as exact as ever."""
+    d = _dsb()
+    rng = np.random.default_rng(L)
+    n = -(-L // P)
+    k, v = rng.standard_normal((2, n * P, D)) * 0.02, rng.standard_normal((n * P, D))
+    k = k[0]
+    k[:, 0] = 0.0
+    k[0, 0], v[0] = 20.0, 0.0
+    pool = np.stack([oq4.pack_block(*oq4.quantise(k[a:a + P]), *oq4.quantise(v[a:a + P])) for a in range(0, n * P, P)])[:, None]
+    q = (rng.standard_normal((T, hq, D)) * 0.1).astype(np.float32)
+    q[..., 0] = 50 * np.log(2) * np.sqrt(D) / 20
+    kvals, vvals = oq4.pool_values(pool, D)
+    bt = [list(range(n))]
+    want, bound = oq4.attention(q, kvals, vvals, bt, [n], [0], [T], [L], oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [n], [0], [T], [L]),
+                                        d.Workspace(T, hq, D, L)))
+    assert 0 < np.abs(want).max() < 2.0 ** -40
+    worst = (np.abs(got - want) / bound).max()
+    assert worst <= 1, f"{worst:.2f} of the bound"
