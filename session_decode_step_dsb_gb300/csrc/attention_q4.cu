@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 4) attention_q4_kernel(
         for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 240);
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
         const float row_scale = __uint_as_float((uint32_t)(e - 10) << 23);  // 2^-10 of that
         const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
         float row_sum = 0.0f;

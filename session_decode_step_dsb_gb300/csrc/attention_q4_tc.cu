@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_q4_tc_kernel(
         for (int k = 0; k < D / 8; ++k) m = fmaxf(m, fabsf(x[k]));
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 240);
+        const int e = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
         const float inv = __uint_as_float((uint32_t)(264 - e) << 23);
         float sum = 0.0f;
 #pragma unroll

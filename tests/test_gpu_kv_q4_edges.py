@@ -126,3 +126,31 @@ def test_a_key_without_values_that_carries_the_weight(cuda_device, D, hq, T, L):
     assert 0 < np.abs(want).max() < 2.0 ** -40
     worst = (np.abs(got - want) / bound).max()
     assert worst <= 1, f"{worst:.2f} of the bound"
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+@pytest.mark.parametrize("size", [1e36, 1e37, 3e38])
+def test_query_rows_up_to_the_largest_float(cuda_device, D, hq, T, L, size):
+    """Scores that float32 holds: all keys alike (2^-20 in each dimension), the
+    output is the mean of the values that a row sees.  A weight is 1 up to the
+    exponential's 2^-22, each of up to L sums and the two-part products within
+    2^-22 of the terms' magnitudes: 2^-20 of the mean magnitude with room."""
+    d = _dsb()
+    rng = np.random.default_rng(L)
+    n = -(-L // P)
+    v = rng.standard_normal((n * P, D))
+    k = np.full((P, D), 2.0 ** -20)
+    pool = np.stack([oq4.pack_block(*oq4.quantise(k), *oq4.quantise(v[a:a + P])) for a in range(0, n * P, P)])[:, None]
+    q = np.zeros((T, hq, D), np.float32)
+    q[..., 3] = size
+    q[..., 5] = -size / 4
+    _, vvals = oq4.pool_values(pool, D)
+    _, vsize = oq4.pool_sizes(pool, D)
+    vvals, vsize = vvals.reshape(-1, D), vsize.reshape(-1, D)
+    bt = [list(range(n))]
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [n], [0], [T], [L]),
+                                        d.Workspace(T, hq, D, L)))
+    for j in range(T):
+        seen = L - T + j + 1
+        assert (np.abs(got[j] - vvals[:seen].mean(0)) <= 2.0 ** -20 * vsize[:seen].mean(0)).all()
+    d.device_error()
