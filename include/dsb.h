@@ -459,11 +459,11 @@ typedef struct {
  * each in [0, 2^24)).  q: device float32, row t at q + t * q_stride, heads of
  * head_dim side by side; k alike (NULL with n_kv_heads = 0).  q and k may be
  * parts of the same rows (the strides of a fused projection, q_stride = k_stride
- * then) but share no value.  head_dim even in [2, 1024].  Angles modulo one turn in 64-bit integer
- * arithmetic; c and s the float32 nearest to the cosine and the sine times the
- * gain (but for one in some thousands); x c - y s and x s + y c with every
- * product and sum rounded to float32.  Row t is bitwise equal to an n_tok = 1
- * call. */
+ * then) but share no value.  head_dim even in [2, 1024].  Angles pos[t] f_i, with
+ * f_i in float64, modulo one turn in 64-bit integer arithmetic; c and s the float32
+ * nearest to their cosine and sine times the gain (but for one in some thousands at
+ * most, at any position); x c - y s and x s + y c with every product and sum rounded
+ * to float32.  Row t is bitwise equal to an n_tok = 1 call. */
 dsb_status dsb_rope_rotary(float* q, int64_t q_stride, int n_q_heads, float* k, int64_t k_stride, int n_kv_heads,
                            int head_dim, int n_tok, const int32_t* pos, const dsb_rotary* rotary, dsb_workspace* ws,
                            void* stream);

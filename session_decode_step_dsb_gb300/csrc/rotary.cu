@@ -8,8 +8,8 @@
 // The angle.  f_i / 2 pi, the turns per position, is kept as a 64-bit fraction
 // of a turn: p times it modulo 2^64 is the angle modulo one turn, exactly, so
 // that the wrap-around of an integer product is the whole range reduction.  The
-// frequency is a float64 rounded to that fraction: the angle of position 2^24
-// is off by at most 2^24 * 2^-53 turns.  The nearest quarter turn is taken off
+// frequency is a float64, its turns rounded to that fraction: the angle of position
+// 2^24 is off by at most 2^24 * 2^-65 turns.  The nearest quarter turn is taken off
 // as an integer; sine and cosine of the eighth of a turn at most that remains
 // are their Taylor sums in pairs of float32 (about 46 bits; this GPU does
 // float64 at a small part of its float32 rate), so that the float32 factors are
@@ -577,17 +577,27 @@ cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, c
   return cudaErrorInvalidValue;
 }
 
-// Turns per position as 64-bit fractions; only the fraction of a turn counts,
-// because positions are whole numbers.
+// Turns per position as 64-bit fractions, the nearest to freq / 2 pi: that quotient
+// in two float64 (one is 2^-53 of it off, 2^-30 of a turn at position 2^24: there one
+// factor in a hundred would not be the nearest float32).  Only the fraction of a turn
+// counts, because positions are whole numbers.
 void rotary_table(const double* freq, int rd, bool interleaved, double gain, RotaryTable* out) {
+  constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLo = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
   out->rd = rd;
   out->interleaved = interleaved ? 1 : 0;
   out->gain = gain;
   for (int i = 0; i < rd / 2; ++i) {
-    double turns = freq[i] * 0.15915494309189533577;
-    turns -= std::floor(turns);
-    const double scaled = std::ldexp(turns, 64);
-    out->turns[i] = scaled >= 18446744073709551616.0 ? 0ull : (unsigned long long)scaled;
+    double hi = freq[i] * kTurn;
+    double lo = std::fma(freq[i], kTurn, -hi) + freq[i] * kTurnLo;
+    hi -= std::floor(hi);
+    lo -= std::rint(lo);  // of turns from 2^52 on
+    hi *= 0x1p64;
+    const double whole = std::floor(hi);
+    lo = lo * 0x1p64 + (hi - whole);
+    // whole < 2^64; |lo| <= 2^63, halved before its conversion where it is that large
+    const unsigned long long rest = std::fabs(lo) < 0x1p62 ? (unsigned long long)std::llrint(lo)
+                                                           : 2ull * (unsigned long long)std::llrint(0.5 * lo);
+    out->turns[i] = (unsigned long long)whole + rest;
   }
 }
 

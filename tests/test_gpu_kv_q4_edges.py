@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 
 from oracle import kv_q4 as oq4
+from oracle import rotary as orot
 from tests.gpu_util import to_dev, to_host
-from tests.test_gpu_kv_q4 import P, _dsb, _pool
+from tests.test_gpu_kv_q4 import P, _dsb, _partner, _pool, _rot
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,57 @@ def test_query_rows_up_to_the_largest_float(cuda_device, D, hq, T, L, size):
         seen = L - T + j + 1
         assert (np.abs(got[j] - vvals[:seen].mean(0)) <= 2.0 ** -20 * vsize[:seen].mean(0)).all()
     d.device_error()
+
+
+PI = 314159265358979323846264338327950288419716939937510582097494459230781640628620899
+
+
+def _turned(pos, f):
+    """float32 nearest to cos(pos f) and sin(pos f), f the float64 given: the angle
+    modulo a turn in integers (2^-160), its cosine in float64."""
+    one = 1 << 160
+    turn = 2 * PI * one // 10 ** 80
+    m, e = f.as_integer_ratio()
+    r = int(pos) * m * one // e % turn / one
+    return np.float32(np.cos(r)), np.float32(np.sin(r))
+
+
+@pytest.mark.parametrize("pos0", [0, 100000, 1 << 20, (1 << 24) - 300])
+def test_cosines_and_sines_are_the_nearest(cuda_device, pos0):
+    """Pairs (1, 0) turn to the factors themselves.  A turn's fraction is within
+    2^-65 for each position, 2^-38 radians at 2^24, and the sums within 2^-44: of
+    values spread over the circle less than one in a thousand lies as near to a
+    border between two float32 (some 13 octaves below 1, each with 2^-13.3 of its
+    share of about a third)."""
+    d = _dsb()
+    n, D = 300, 128
+    f = orot.frequencies(D, 10000.0)
+    x = np.zeros((n, 1, D), np.float32)
+    x[..., :D // 2] = 1.0
+    t = to_dev(x)
+    d.rope_rotary(t, None, np.arange(pos0, pos0 + n), d.Rotary(10000.0), d.Workspace(n, 1, D, P))
+    got = to_host(t)[:, 0]
+    want = np.array([np.array([_turned(pos0 + i, v) for v in f.tolist()]).T.reshape(-1) for i in range(n)], np.float32)
+    assert (np.abs(got.astype(np.float64) - want) <= np.spacing(np.abs(want)) + 2.0 ** -38).all()
+    off = int((got != want).sum())
+    assert off * 1000 <= want.size, f"{off} of {want.size}"
+
+
+@pytest.mark.parametrize("rd,inter,scale,pos0", [(128, False, "none", 0), (64, True, "bands", 131000), (48, False, "ntk", 77),
+                                                 (128, True, "yarn", 8000), (34, False, "linear", (1 << 24) - 400)])
+def test_rotated_values_keep_their_roundings(cuda_device, rd, inter, scale, pos0):
+    """x c + p s with c and s the nearest float32 (2^-24 of the gain's octave) and
+    three more roundings of at most 2^-24: 2^-24 for the factors, one for the two
+    products together and one for the sum, of (|x| + |p|) gain; and 4e-9 rad, what
+    float64 leaves of the oracle's own angle at 2^24."""
+    d = _dsb()
+    n, D = 400, 128
+    rng = np.random.default_rng(rd)
+    x = rng.standard_normal((n, 3, D)).astype(np.float32)
+    pos = pos0 + np.arange(n)
+    rot, f, gain = _rot(scale, rd, inter)
+    t = to_dev(x)
+    d.rope_rotary(t, None, pos, rot, d.Workspace(n, 3, D, P))
+    want = orot.rotate(x, pos, f, inter, gain)
+    tol = (3 * 2.0 ** -24 + 4e-9) * gain
+    assert (np.abs(to_host(t) - want) <= tol * _partner(x.astype(np.float64), rd, inter)).all()
