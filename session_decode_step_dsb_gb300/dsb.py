@@ -615,6 +615,24 @@ class Rotary:
         self.ref = ctypes.byref(self.c)
 
 
+_INT32 = np.dtype(np.int32)
+
+
+def _whole_i32(a, name: str):
+    """``a`` as an int32 array; values that int32 cannot hold (wider integers past
+    its range, fractions, NaN) are refused, not wrapped or cut."""
+    a = np.asarray(a)
+    if a.dtype == _INT32:
+        return a
+    if a.size == 0:
+        return a.astype(np.int32)
+    if a.dtype.kind not in "iubf":
+        raise ValueError(f"{name} must hold integers, got {a.dtype}")
+    if not (a.min() >= -2 ** 31 and a.max() < 2 ** 31) or (a.dtype.kind == "f" and (a != np.floor(a)).any()):
+        raise ValueError(f"{name} must hold integers that int32 can hold")
+    return a.astype(np.int32)
+
+
 class PagedBatch:
     """The sequences of one paged call or of every layer of one step
     (``dsb_paged_batch``; host arrays, copied): block tables ``[n_seq,
@@ -622,7 +640,7 @@ class PagedBatch:
     call, one entry for each sequence."""
 
     def __init__(self, block_table, n_blocks, window, new_tokens, seq_lens):
-        bt = np.array(block_table, dtype=np.int32, order="C")
+        bt = np.array(_whole_i32(block_table, "block_table"), order="C")
         if bt.ndim != 2:
             raise ValueError("block_table is [n_seq, max_blocks]")
         n = bt.shape[0]
@@ -630,7 +648,7 @@ class PagedBatch:
         ptrs = [bt.ctypes.data_as(_PI32)]
         for name, a in (("n_blocks", n_blocks), ("window", window), ("new_tokens", new_tokens),
                         ("seq_lens", seq_lens)):
-            arr = np.array(a, dtype=np.int32).reshape(-1)
+            arr = np.array(_whole_i32(a, name)).reshape(-1)
             if arr.size != n:
                 raise ValueError(f"{name} has {arr.size} entries, needs {n}")
             self._arrays.append(arr)
@@ -689,9 +707,6 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_INT32 = np.dtype(np.int32)
-
-
 def _empty_on(stream, shape, dtype, device):
     """``torch.empty`` for a call on ``stream``: memory of that stream's, since
     what the current stream has freed may still be in use there."""
@@ -707,7 +722,7 @@ def _empty_on(stream, shape, dtype, device):
 def _host_i32(a, n: int, name: str):
     """``a`` as a contiguous int32 array of ``n`` entries, and its address."""
     if not (type(a) is np.ndarray and a.dtype is _INT32 and a.ndim == 1 and a.flags.c_contiguous):
-        a = np.ascontiguousarray(np.asarray(a, dtype=np.int32)).reshape(-1)
+        a = np.ascontiguousarray(_whole_i32(a, name)).reshape(-1)
     if a.size != n:
         raise ValueError(f"{name} has {a.size} entries, needs {n}")
     return a, a.__array_interface__["data"][0]
