@@ -714,7 +714,8 @@ def _empty_on(stream, shape, dtype, device):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)      # the current stream's
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # handle 0 is the default stream; an ExternalStream of 0 would be a new one
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

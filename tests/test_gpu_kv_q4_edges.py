@@ -209,3 +209,28 @@ def test_rotated_values_keep_their_roundings(cuda_device, rd, inter, scale, pos0
     want = orot.rotate(x, pos, f, inter, gain)
     tol = (3 * 2.0 ** -24 + 4e-9) * gain
     assert (np.abs(to_host(t) - want) <= tol * _partner(x.astype(np.float64), rd, inter)).all()
+
+
+def test_results_on_the_default_stream_by_its_handle(cuda_device):
+    """Handle 0 given as the stream: the results come from the default stream's
+    memory, which a side stream still at work on freed memory cannot hold."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(3)
+    pool = to_dev(_pool(rng, 3, 2, 64))
+    q = to_dev(rng.standard_normal((1, 4, 64)).astype(np.float32))
+    kv, b, ws = d.kv_q4_pages(pool, 64), d.PagedBatch([[2, 0, 1]], [3], [0], [1], [333]), d.Workspace(1, 4, 64, 384)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    want, (wk, wv) = d.attention_decode_q4(q, kv, b, ws), d.kv_gather_q4(kv, b, [5], [300], d.DSB_F16, ws)
+    torch.cuda.synchronize()
+    for _ in range(40):                     # every stream of torch's pool has freed memory that it is yet to write
+        with torch.cuda.stream(torch.cuda.Stream()):
+            busy = [torch.full_like(t, 7.0) for t in (want, wk, wv)]
+            torch.cuda._sleep(10_000_000)
+            for t in busy:
+                t.fill_(9.0)
+            del busy, t
+    out = d.attention_decode_q4(q, kv, b, ws, stream=0)
+    k, v = d.kv_gather_q4(kv, b, [5], [300], d.DSB_F16, ws, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)

@@ -54,3 +54,27 @@ def test_whole_numbers_of_any_type_arrive(kind):
     arr, at = d._host_i32(own, 2, "x")
     assert arr is own and at == own.ctypes.data
     assert d._host_i32(np.array([3, 4, 5, 6])[::2], 2, "x")[0].tolist() == [3, 5]
+
+
+def test_what_a_call_makes_belongs_to_its_stream(monkeypatch):
+    """The handle 0 is the default stream's; other handles are wrapped, streams
+    taken as they are."""
+    import contextlib
+    d, entered = _dsb(), []
+
+    class Stream:
+        def __init__(self, name):
+            self.name = name
+
+    @contextlib.contextmanager
+    def on(stream):
+        entered.append(stream.name)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: Stream(("handle", handle, device)))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream(("default", device)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    for stream in (0, 77, Stream("given"), None):
+        assert d._empty_on(stream, (2, 3), torch.float32, "cpu").shape == (2, 3)
+    assert entered == [("default", "cpu"), ("handle", 77, "cpu"), "given"]
