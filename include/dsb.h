@@ -496,7 +496,8 @@ typedef struct {
  * dsb_rope_rotary, and k so rotated and v as it is are converted (round to
  * nearest even) and written at their positions' page rows.  The k and v parts of qkv and all other page rows keep
  * their values.  n_q_heads may be 0.  head_dim 64 or 128.  Positions below 2^24.
- * Two tokens of a call on one page row are DSB_ERR_INVALID_ARG. */
+ * Two tokens of a call on one page row are DSB_ERR_INVALID_ARG, and so are pools of
+ * K and V, rows of qkv and norm weights that share memory with each other. */
 dsb_status dsb_kv_append_paged(float* qkv, int64_t row_stride, int n_q_heads, const dsb_kv_pages* kv,
                                const dsb_paged_batch* batch, const dsb_rotary* rotary, const float* q_norm,
                                const float* k_norm, float eps, dsb_workspace* ws, void* stream);
@@ -535,8 +536,8 @@ dsb_status dsb_kv_append_q4(float* qkv, int64_t row_stride, int n_q_heads, const
  * up to p without a window); score = q.k / sqrt(head_dim), out = softmax(score) V
  * with the pages' values, float32 accuracy.  q: device float32, row t at
  * q + t * q_stride (a multiple of 4; the query part of qkv rows will do); out:
- * device float32 [tokens][n_q_heads][head_dim], apart from q's rows.  A sequence without new tokens
- * has no rows.  Any number of new tokens.  Partial sums of long sequences go to
+ * device float32 [tokens][n_q_heads][head_dim], apart from q's rows and from the
+ * pool.  A sequence without new tokens has no rows.  Any number of new tokens.  Partial sums of long sequences go to
  * the workspace: dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest
  * seq_lens) is enough.  No atomics; a sequence's rows are bitwise the same alone
  * and in any batch. */
@@ -547,7 +548,8 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
  * int32[n_seq]; within seq_lens[s], under a window also within what the ring
  * still holds; new_tokens is not used) as the values they stand for, rounded to
  * nearest even in dtype (dsb_dtype): k_out and v_out device 16-bit
- * [sum of count][n_kv_heads][head_dim], apart, the sequences one after the other. */
+ * [sum of count][n_kv_heads][head_dim], apart from each other and from the pool, the
+ * sequences one after the other. */
 dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* batch, const int32_t* first,
                             const int32_t* count, int dtype, void* k_out, void* v_out, dsb_workspace* ws, void* stream);
 

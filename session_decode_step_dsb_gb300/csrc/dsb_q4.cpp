@@ -99,6 +99,14 @@ bool rows_overlap(const float* a, int64_t a_stride, int64_t a_width, const float
   return off < a_width * (int64_t)sizeof(float) || off + b_width * (int64_t)sizeof(float) > bytes;
 }
 
+// Whether n rows of `width` floats, a stride apart, and a range share a byte.
+bool rows_touch(const float* a, int64_t stride, int64_t width, int n, const void* b, size_t bytes) {
+  if (!overlap(a, ((n - 1) * stride + width) * sizeof(float), b, bytes)) return false;
+  const int64_t step = stride * (int64_t)sizeof(float);
+  const int64_t off = ((reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) % step + step) % step;
+  return off < width * (int64_t)sizeof(float) || off + (int64_t)bytes > step;
+}
+
 dsb_status check_workspace(const dsb_workspace* ws) {
   if (!ws) return fail(DSB_ERR_WORKSPACE, "workspace is NULL");
   int dev = -1;
@@ -140,6 +148,10 @@ dsb_status check_q4_pages(const dsb_kv_q4_pages* kv) {
   if (kv->head_dim != 64 && kv->head_dim != 128)
     return fail(DSB_ERR_UNSUPPORTED, "head_dim=%d: 4-bit pages serve 64 and 128", kv->head_dim);
   return DSB_OK;
+}
+
+size_t pool_bytes(const dsb_kv_q4_pages* kv) {
+  return (size_t)kv->n_pages * kv->n_kv_heads * DSB_KV_PAGE * (kv->head_dim + 8);
 }
 
 // The batch's tables against a pool of n_pages; *n_tok: its new token rows.
@@ -222,8 +234,9 @@ dsb_status cut_groups(int n_seq, size_t fixed, size_t per_seq, Pages pages, std:
   return DSB_OK;
 }
 
+// vc: NULL where kc is the pool of both.
 dsb_status append_common(float* qkv, int64_t row_stride, int n_q_heads, int n_pages, int n_kv_heads, int head_dim,
-                         void* kc, void* vc, dsbk::KvStore store, const dsb_paged_batch* b, const dsb_rotary* rotary,
+                         void* kc, void* vc, size_t pool_bytes, dsbk::KvStore store, const dsb_paged_batch* b, const dsb_rotary* rotary,
                          const float* q_norm, const float* k_norm, float eps, dsb_workspace* ws, void* stream) {
   if (n_q_heads < 0 || n_q_heads > 65535 || n_kv_heads > 65535)
     return fail(DSB_ERR_INVALID_ARG, "n_q_heads=%d / n_kv_heads=%d out of range", n_q_heads, n_kv_heads);
@@ -242,6 +255,13 @@ dsb_status append_common(float* qkv, int64_t row_stride, int n_q_heads, int n_pa
   if ((st = check_writes(b)) != DSB_OK) return st;
   if (n_tok == 0) return DSB_OK;
   if (!qkv || !aligned16(qkv)) return fail(DSB_ERR_INVALID_ARG, "qkv is NULL or not 16-byte aligned");
+  if (vc && overlap(kc, pool_bytes, vc, pool_bytes)) return fail(DSB_ERR_INVALID_ARG, "the pools of K and V overlap");
+  for (const void* pool : {kc, vc})
+    if (pool && rows_touch(qkv, row_stride, width, n_tok, pool, pool_bytes))
+      return fail(DSB_ERR_INVALID_ARG, "qkv and a page pool overlap");
+  for (const float* w : {q_norm, k_norm})
+    if (w && rows_touch(qkv, row_stride, width, n_tok, w, head_dim * sizeof(float)))
+      return fail(DSB_ERR_INVALID_ARG, "qkv and the weights of a norm overlap");
   // blocks sequence s's new tokens touch
   auto pages = [&](int s) {
     if (b->new_tokens[s] == 0) return 0;
@@ -361,7 +381,7 @@ dsb_status dsb_kv_append_paged(float* qkv, int64_t row_stride, int n_q_heads, co
     if (kv->head_dim != 64 && kv->head_dim != 128)
       return fail(DSB_ERR_UNSUPPORTED, "head_dim=%d: the paged append serves 64 and 128", kv->head_dim);
     return append_common(qkv, row_stride, n_q_heads, kv->n_pages, kv->n_kv_heads, kv->head_dim, kv->k, kv->v,
-                         kv->dtype == DSB_F16 ? dsbk::KvStore::kF16 : dsbk::KvStore::kBF16, batch, rotary, q_norm, k_norm,
+                         (size_t)kv->n_pages * kv->n_kv_heads * DSB_KV_PAGE * kv->head_dim * 2, kv->dtype == DSB_F16 ? dsbk::KvStore::kF16 : dsbk::KvStore::kBF16, batch, rotary, q_norm, k_norm,
                          eps, ws, stream);
   });
 }
@@ -377,7 +397,7 @@ dsb_status dsb_kv_append_q4(float* qkv, int64_t row_stride, int n_q_heads, const
   return guarded([&]() -> dsb_status {
     const dsb_status st = check_q4_pages(kv);
     if (st != DSB_OK) return st;
-    return append_common(qkv, row_stride, n_q_heads, kv->n_pages, kv->n_kv_heads, kv->head_dim, kv->blocks, nullptr,
+    return append_common(qkv, row_stride, n_q_heads, kv->n_pages, kv->n_kv_heads, kv->head_dim, kv->blocks, nullptr, pool_bytes(kv),
                          dsbk::KvStore::kQ4, batch, rotary, q_norm, k_norm, eps, ws, stream);
   });
 }
@@ -464,6 +484,8 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
     const int64_t width = (int64_t)n_q_heads * D;
     if (overlap(q, ((n_tok - 1) * q_stride + width) * sizeof(float), out, n_tok * width * sizeof(float)))
       return fail(DSB_ERR_INVALID_ARG, "out overlaps the rows of q");
+    if (overlap(kv->blocks, pool_bytes(kv), out, n_tok * width * sizeof(float)))
+      return fail(DSB_ERR_INVALID_ARG, "out overlaps the page pool");
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     if ((st = check_capture(most, cs)) != DSB_OK) return st;
@@ -539,6 +561,9 @@ dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* b,
     }
     const size_t out_bytes = (size_t)rows * kv->n_kv_heads * kv->head_dim * 2;
     if (overlap(k_out, out_bytes, v_out, out_bytes)) return fail(DSB_ERR_INVALID_ARG, "k_out and v_out overlap");
+    for (const void* o : {k_out, v_out})
+      if (overlap(kv->blocks, pool_bytes(kv), o, out_bytes))
+        return fail(DSB_ERR_INVALID_ARG, "k_out / v_out and the page pool overlap");
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     if ((st = check_capture(most, cs)) != DSB_OK) return st;

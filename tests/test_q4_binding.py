@@ -78,3 +78,62 @@ def test_what_a_call_makes_belongs_to_its_stream(monkeypatch):
     for stream in (0, 77, Stream("given"), None):
         assert d._empty_on(stream, (2, 3), torch.float32, "cpu").shape == (2, 3)
     assert entered == [("default", "cpu"), ("handle", 77, "cpu"), "given"]
+
+
+def _lib():
+    import os
+    from session_decode_step_dsb_gb300 import build
+    d = _dsb()
+    if not os.path.exists(d.LIB_PATH):
+        build.build()
+    return d, d.lib()
+
+
+def test_memory_that_a_call_reads_and_writes_is_apart():
+    """Before any device work.  The workspace is a stand-in that belongs to no device:
+    a call that passed these checks would be refused for that."""
+    import ctypes
+    d, lib = _lib()
+    ws, rot, b = ctypes.create_string_buffer(b"\xff" * 4096), d.Rotary(), d.PagedBatch(**BATCH)
+    hq, hkv, D, n, pages, mb = 4, 2, 64, 3, 8, 1 << 20
+    width, pool = (hq + 2 * hkv) * D * 4, pages * hkv * 128 * (D + 8)
+    pool16 = pages * hkv * 128 * D * 2
+
+    def said(st):
+        assert st == d.DSB_ERR_INVALID_ARG
+        return lib.dsb_last_error().decode()
+
+    def append(k, v, qkv, stride=width // 4, qn=None, kn=None):
+        if v is None:
+            kv, fn = d.KVQ4Pages(k, pages, hkv, D), lib.dsb_kv_append_q4
+        else:
+            kv, fn = d.KVPages(k, v, 0, pages, hkv, D), lib.dsb_kv_append_paged
+        return said(fn(qkv, stride, hq, ctypes.byref(kv), b.ref, rot.ref, qn, kn, 1e-6, ws, None))
+
+    for v in (mb, mb + pool16 - 16, mb - pool16 + 16):
+        assert append(mb, v, 64 * mb) == "the pools of K and V overlap"
+    for k, v, end in ((mb, None, mb + pool), (mb, 16 * mb, mb + pool16), (16 * mb, mb, mb + pool16)):
+        for qkv in (mb, end - 16, mb - n * width + 16):
+            assert append(k, v, qkv) == "qkv and a page pool overlap"
+    rows = 64 * mb
+    for w in (rows, rows + 2 * width + 16, rows + width - 16, rows - D * 4 + 16):
+        assert append(mb, None, rows, qn=w) == "qkv and the weights of a norm overlap"
+        assert append(mb, 16 * mb, rows, kn=w) == "qkv and the weights of a norm overlap"
+    # between rows that lie far apart, at the last byte that a row leaves free
+    wide = width // 4 + D
+    assert append(mb, None, rows, stride=wide, qn=rows + width + 16) == "qkv and the weights of a norm overlap"
+    assert lib.dsb_kv_append_q4(rows, wide, hq, ctypes.byref(d.KVQ4Pages(mb, pages, hkv, D)), b.ref, rot.ref, rows + width,
+                                None, 1e-6, ws, None) != d.DSB_OK
+    assert "overlap" not in lib.dsb_last_error().decode()
+
+    kv = d.KVQ4Pages(mb, pages, hkv, D)
+    out = n * hq * D * 4
+    for o in (mb, mb + pool - 16, mb - out + 16):
+        assert said(lib.dsb_attention_decode_q4(rows, hq * D, hq, ctypes.byref(kv), b.ref, o, ws, None)) == \
+            "out overlaps the page pool"
+    f, c = np.array([0, 0], np.int32), np.array([100, 2], np.int32)
+    each = 102 * hkv * D * 2
+    for o in (mb, mb + pool - 16, mb - each + 16):
+        for k, v in ((o, rows), (rows, o)):
+            assert said(lib.dsb_kv_gather_q4(ctypes.byref(kv), b.ref, f.ctypes.data, c.ctypes.data, 0, k, v, ws, None)) == \
+                "k_out / v_out and the page pool overlap"
