@@ -212,7 +212,7 @@ dsb_status check_writes(const dsb_paged_batch* b) {
 
 // Sequences [s0, s1) whose metadata makes one launch.
 struct Group {
-  int s0, s1, tok0, n_tok;
+  int s0, s1;
   std::vector<int32_t> words;
 };
 
@@ -225,7 +225,7 @@ dsb_status cut_groups(int n_seq, size_t fixed, size_t per_seq, Pages pages, std:
     const size_t need = per_seq + (size_t)pages(s);
     if (fixed + need > kMetaWords) return fail(DSB_ERR_UNSUPPORTED, "sequence %d's block table exceeds the staging slot", s);
     if (out->empty() || have + need > kMetaWords) {
-      out->push_back(Group{s, s, 0, 0, {}});
+      out->push_back(Group{s, s, {}});
       have = fixed;
     }
     have += need;
@@ -262,56 +262,36 @@ dsb_status append_common(float* qkv, int64_t row_stride, int n_q_heads, int n_pa
   for (const float* w : {q_norm, k_norm})
     if (w && rows_touch(qkv, row_stride, width, n_tok, w, head_dim * sizeof(float)))
       return fail(DSB_ERR_INVALID_ARG, "qkv and the weights of a norm overlap");
-  // blocks sequence s's new tokens touch
-  auto pages = [&](int s) {
-    if (b->new_tokens[s] == 0) return 0;
-    return (b->seq_lens[s] - 1) / DSB_KV_PAGE - (b->seq_lens[s] - b->new_tokens[s]) / DSB_KV_PAGE + 1;
-  };
-  std::vector<Group> groups;
-  if ((st = cut_groups(b->n_seq, 2, 3, pages, &groups)) != DSB_OK) return st;
-  // tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages
-  int tok0 = 0;
-  size_t most = 0;
-  for (Group& g : groups) {
-    std::vector<int32_t> off, pos0, pg_off, list;
-    int tok = 0;
-    for (int s = g.s0; s < g.s1; ++s) {
-      if (b->new_tokens[s] == 0) continue;
-      off.push_back(tok);
-      pos0.push_back(b->seq_lens[s] - b->new_tokens[s]);
-      pg_off.push_back((int32_t)list.size());
-      const int i0 = pos0.back() / DSB_KV_PAGE;
-      for (int i = 0; i < pages(s); ++i) list.push_back(page_of(b, s, i0 + i));
-      tok += b->new_tokens[s];
-    }
-    off.push_back(tok);
+  // tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages, of the sequences with new tokens.
+  // A sequence of n touches at most (n - 2) / DSB_KV_PAGE + 2 pages, so that any call
+  // fits a staging slot.
+  static_assert(5 * (size_t)DSB_MAX_SEQS + 2 + DSB_MAX_TOKENS / DSB_KV_PAGE <= kMetaWords, "append metadata");
+  std::vector<int32_t> words, pos0, pg_off, list;
+  int tok = 0;
+  for (int s = 0; s < b->n_seq; ++s) {
+    if (b->new_tokens[s] == 0) continue;
+    words.push_back(tok);
+    pos0.push_back(b->seq_lens[s] - b->new_tokens[s]);
     pg_off.push_back((int32_t)list.size());
-    g.tok0 = tok0;
-    g.n_tok = tok;
-    tok0 += tok;
-    g.words = off;
-    g.words.insert(g.words.end(), pos0.begin(), pos0.end());
-    g.words.insert(g.words.end(), pg_off.begin(), pg_off.end());
-    g.words.insert(g.words.end(), list.begin(), list.end());
-    most = std::max(most, g.words.size());
+    for (int i = pos0.back() / DSB_KV_PAGE; i <= (b->seq_lens[s] - 1) / DSB_KV_PAGE; ++i) list.push_back(page_of(b, s, i));
+    tok += b->new_tokens[s];
   }
+  const int live = (int)pos0.size();
+  words.push_back(tok);
+  pg_off.push_back((int32_t)list.size());
+  words.insert(words.end(), pos0.begin(), pos0.end());
+  words.insert(words.end(), pg_off.begin(), pg_off.end());
+  words.insert(words.end(), list.begin(), list.end());
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if ((st = check_workspace(ws)) != DSB_OK) return st;
-  if ((st = check_capture(most, cs)) != DSB_OK) return st;
+  if ((st = check_capture(words.size(), cs)) != DSB_OK) return st;
   dsbk::RotaryTable rot;
   build_rotary(*rotary, head_dim, &rot);
-  for (const Group& g : groups) {
-    if (g.n_tok == 0) continue;
-    dsbk::MetaArg meta;
-    if ((st = meta_arg(ws, g.words, cs, &meta)) != DSB_OK) return st;
-    int live = 0;
-    for (int s = g.s0; s < g.s1; ++s) live += b->new_tokens[s] > 0;
-    const dsbk::AppendArgs a{qkv + (size_t)g.tok0 * row_stride, row_stride, n_q_heads, n_kv_heads, kc, vc, q_norm, k_norm,
-                             eps, live, g.n_tok};
-    const cudaError_t e = dsbk::launch_kv_append(a, head_dim, store, rot, meta, cs);
-    if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
-  }
-  return DSB_OK;
+  dsbk::MetaArg meta;
+  if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
+  const dsbk::AppendArgs a{qkv, row_stride, n_q_heads, n_kv_heads, kc, vc, q_norm, k_norm, eps, live, n_tok};
+  const cudaError_t e = dsbk::launch_kv_append(a, head_dim, store, rot, meta, cs);
+  return e == cudaSuccess ? DSB_OK : cuda_fail(e, "kv_append launch");
 }
 
 }  // namespace

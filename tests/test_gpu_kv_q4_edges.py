@@ -8,7 +8,7 @@ import pytest
 from oracle import kv_q4 as oq4
 from oracle import rotary as orot
 from tests.gpu_util import to_dev, to_host
-from tests.test_gpu_kv_q4 import P, _dsb, _partner, _pool, _rot
+from tests.test_gpu_kv_q4 import P, _dsb, _geometry, _partner, _pool, _rot
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +234,42 @@ def test_results_on_the_default_stream_by_its_handle(cuda_device):
     k, v = d.kv_gather_q4(kv, b, [5], [300], d.DSB_F16, ws, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)
+
+
+@pytest.mark.parametrize("n", [70, 1024])
+@pytest.mark.parametrize("store", ["q4", "f16", "bf16"])
+def test_appends_of_many_sessions(cuda_device, n, store):
+    """Metadata of some hundred words in the launch (70 sessions) and staged (1024):
+    the same bits as the sessions a few at a time, whose words are few."""
+    import torch
+    d = _dsb()
+    D, hq, hkv = 64, 3, 2
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, 400, n)
+    new = np.minimum(np.where(rng.random(n) < 0.05, 0, rng.integers(1, 6, n)), lens)
+    window = np.where(rng.random(n) < 0.3, 100, 0)
+    bt, blocks, n_pages = _geometry(lens, new, window, rng)
+    rot = d.Rotary(rotary_dim=48)
+    w = [to_dev((rng.standard_normal(D) * 0.1 + 1).astype(np.float32)) for _ in range(2)]
+    qkv = to_dev(rng.standard_normal((int(new.sum()), (hq + 2 * hkv) * D)).astype(np.float32))
+    ws = d.Workspace(len(qkv), hq, D, 512)
+
+    def run(cuts):
+        if store == "q4":
+            pools = [torch.full((n_pages, hkv, P * (D + 8)), 7, dtype=torch.uint8, device="cuda")]
+            kv, call = d.kv_q4_pages(pools[0], D), d.kv_append_q4
+        else:
+            pools = [torch.full((n_pages, hkv, P, D), 7, dtype=torch.int16, device="cuda") for _ in range(2)]
+            kv, call = d.kv_pages(*pools, d.DSB_F16 if store == "f16" else d.DSB_BF16), d.kv_append_paged
+        rows, at = qkv.clone(), 0
+        for a, b in cuts:
+            m = int(new[a:b].sum())
+            if m:
+                call(rows[at:at + m], hq, kv, d.PagedBatch(bt[a:b], blocks[a:b], window[a:b], new[a:b], lens[a:b]), rot, ws,
+                     q_norm=w[0], k_norm=w[1], eps=1e-6)
+            at += m
+        return [rows, *pools]
+
+    together, apart = run([(0, n)]), run([(a, min(a + 8, n)) for a in range(0, n, 8)])
+    for a, b in zip(together, apart):
+        assert torch.equal(a, b)
