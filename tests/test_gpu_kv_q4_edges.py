@@ -273,3 +273,70 @@ def test_appends_of_many_sessions(cuda_device, n, store):
     together, apart = run([(0, n)]), run([(a, min(a + 8, n)) for a in range(0, n, 8)])
     for a, b in zip(together, apart):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D,hq,hkv,lens,new,window", [
+    (128, 2, 1, [2300], [300], [0]), (128, 6, 2, [2500, 40, 2400], [90, 1, 130], [0, 0, 2200]), (64, 3, 1, [700], [260], [0])])
+def test_attention_of_a_prompts_rows(cuda_device, D, hq, hkv, lens, new, window):
+    """Hundreds of rows on a kv head, beside a single token's, on caches long enough
+    for the tcgen05 kernel and on a short one."""
+    d = _dsb()
+    rng = np.random.default_rng(sum(lens))
+    bt, blocks, n_pages = _geometry(lens, new, window, rng)
+    pool = _pool(rng, n_pages, hkv, D)
+    q = (rng.standard_normal((sum(new), hq, D)) * 2).astype(np.float32)
+    kvals, vvals = oq4.pool_values(pool, D)
+    want, bound = oq4.attention(q, kvals, vvals, bt, blocks, window, new, lens, oq4.pool_sizes(pool, D))
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, blocks, window, new, lens),
+                                        d.Workspace(sum(new), hq, D, max(lens))))
+    assert (np.abs(got - want) <= bound).all()
+    d.device_error()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,rd,inter,scale", [(128, 128, False, "yarn"), (64, 64, True, "none")])
+def test_a_long_prompt_into_16_bit_pages(cuda_device, dtype, D, rd, inter, scale):
+    """3000 rows at once: k as the rotary call turns it and v as it is, rounded once."""
+    import torch
+    d = _dsb()
+    n, past, hq, hkv = 3000, 90, 5, 2
+    rng = np.random.default_rng(D)
+    x = to_dev(rng.standard_normal((n, hq + 2 * hkv, D)).astype(np.float32))
+    rot, ws = _rot(scale, rd, inter)[0], d.Workspace(n, hq, D, 4096)
+    turned = x.clone()
+    d.rope_rotary(turned[:, :hq], turned[:, hq:hq + hkv], np.arange(past, past + n), rot, ws)
+    blocks = -(-(past + n) // P)
+    table = rng.permutation(blocks).astype(np.int32)
+    kind = torch.float16 if dtype == "f16" else torch.bfloat16
+    k, v = (torch.full((blocks, hkv, P, D), 7.0, device="cuda", dtype=kind) for _ in range(2))
+    got = x.clone()
+    d.kv_append_paged(got.view(n, -1), hq, d.kv_pages(k, v, d.DSB_F16 if dtype == "f16" else d.DSB_BF16),
+                      d.PagedBatch(table[None], [blocks], [0], [n], [past + n]), rot, ws)
+    assert torch.equal(got[:, :hq], turned[:, :hq]) and torch.equal(got[:, hq:], x[:, hq:])
+    order = torch.from_numpy(table).cuda().long()
+    for pages, rows in ((k, turned[:, hq:hq + hkv]), (v, x[:, hq + hkv:])):
+        flat = pages[order].permute(0, 2, 1, 3).reshape(-1, hkv, D)
+        assert torch.equal(flat[past:past + n], rows.to(kind))
+        assert (flat[:past] == 7.0).all() and (flat[past + n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3e38])
+def test_a_bad_query_row_is_its_own(cuda_device, D, hq, T, L, bad):
+    """A NaN, an infinity or a huge value in one row changes no bit of the others."""
+    import torch
+    d = _dsb()
+    rng = np.random.default_rng(L)
+    pool, bt = _hidden_case(D, T, L, rng, 1.0)
+    q = to_dev(rng.standard_normal((T, hq, D)).astype(np.float32))
+    kv, b, ws = d.kv_q4_pages(to_dev(pool), D), d.PagedBatch(bt, [len(bt[0])], [0], [T], [L]), d.Workspace(T, hq, D, L)
+    want = d.attention_decode_q4(q, kv, b, ws)
+    for j, h in ((0, 0), (T - 1, hq - 1)):
+        x = q.clone()
+        x[j, h, 17] = bad
+        got = d.attention_decode_q4(x, kv, b, ws)
+        keep = torch.ones((T, hq), dtype=torch.bool, device="cuda")
+        keep[j, h] = False
+        assert torch.equal(got[keep], want[keep])
+        if not np.isfinite(bad):
+            assert torch.isnan(got[j, h]).all()
