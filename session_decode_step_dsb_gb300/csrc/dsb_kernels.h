@@ -326,11 +326,9 @@ unsigned int read_clear_error_attention_q4();
 cudaError_t launch_attention_q4_tc(const Q4AttnArgs& a, const MetaArg& meta, cudaStream_t st);
 unsigned int read_clear_error_attention_q4_tc();
 
-// One sequence of a read-back; n_seq of them, then the total page count, then
-// the pages of all sequences.
-struct Q4Span {
-  int32_t page_off, first, count, row0, pg_at;
-};
+// Words of one sequence of a read-back: its first page in the call's count, first key,
+// keys, first output row, where its pages are.  n_seq of them, then the total page
+// count, then the pages of all sequences.
 constexpr int kQ4SpanWords = 5;
 // dtype: DSB_F16 or DSB_BF16; k, v: [rows][hkv][head_dim].
 cudaError_t launch_gather_q4(const void* pool, int hkv, int head_dim, int n_seq, long long pages, int dtype, void* k,
