@@ -275,6 +275,7 @@ struct AppendArgs {
   const float* k_norm;
   float eps;
   int n_seq, n_tok;
+  int sms;  // of the device
 };
 // Metadata: tok_off[n_seq + 1] | pos0[n_seq] | pg_off[n_seq + 1] | pages.
 cudaError_t launch_kv_append(const AppendArgs& a, int head_dim, KvStore store, const RotaryTable& rot,

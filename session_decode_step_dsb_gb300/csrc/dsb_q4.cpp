@@ -285,11 +285,14 @@ dsb_status append_common(float* qkv, int64_t row_stride, int n_q_heads, int n_pa
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if ((st = check_workspace(ws)) != DSB_OK) return st;
   if ((st = check_capture(words.size(), cs)) != DSB_OK) return st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != DSB_OK) return st;
   dsbk::RotaryTable rot;
   build_rotary(*rotary, head_dim, &rot);
   dsbk::MetaArg meta;
   if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
-  const dsbk::AppendArgs a{qkv, row_stride, n_q_heads, n_kv_heads, kc, vc, q_norm, k_norm, eps, live, n_tok};
+  const dsbk::AppendArgs a{qkv, row_stride, n_q_heads, n_kv_heads, kc, vc, q_norm, k_norm, eps, live, n_tok,
+                           dev.sms};
   const cudaError_t e = dsbk::launch_kv_append(a, head_dim, store, rot, meta, cs);
   return e == cudaSuccess ? DSB_OK : cuda_fail(e, "kv_append launch");
 }

@@ -534,10 +534,9 @@ cudaError_t append_go(const AppendArgs& a, const RotaryTable& rot, const MetaArg
   fill_turns(rot, &tab);
   ParamWords<N> w;
   fill_words(meta, &w);
-  // as many shares of a token's heads as fill the GPU (7 CTAs on each of some 150
-  // SMs), no more than there are
+  // as many shares of a token's heads as fill the GPU, no more than there are
   const int slots = kAppThreads / (D / 8), most = (a.hq + 2 * a.hkv + slots - 1) / slots;
-  const int shares = std::min(most, std::max(1, 7 * 150 / a.n_tok));
+  const int shares = std::min(most, std::max(1, kAppPerSm * a.sms / a.n_tok));
   const dim3 grid((unsigned)a.n_tok, (unsigned)shares);
   return launch_kernel(kv_append_kernel<D, Store, N>, grid, dim3(kAppThreads), 0, st, a.qkv, a.stride, a.hq, a.hkv,
                        static_cast<uint8_t*>(a.kc), static_cast<uint8_t*>(a.vc), tab, a.q_norm, a.k_norm, a.eps, a.n_seq,
