@@ -57,7 +57,7 @@ using B = Q4Block<D>;
 constexpr int kWorkers = 256;
 constexpr int kThreads = kWorkers + 32;  // and a warp that asks for the pages and issues the products
 constexpr int kRing = 3;  // half pages asked for at a time
-constexpr float kNoKey = -1e30f;
+constexpr float kNoKey = -0x1.fffffep127f;  // reference of a row that has seen no key: below any score
 
 __device__ unsigned int g_err_attention_q4_tc = 0;
 

@@ -340,3 +340,28 @@ def test_a_bad_query_row_is_its_own(cuda_device, D, hq, T, L, bad):
         assert torch.equal(got[keep], want[keep])
         if not np.isfinite(bad):
             assert torch.isnan(got[j, h]).all()
+
+
+@pytest.mark.parametrize("D,hq,T,L", FORMS)
+@pytest.mark.parametrize("size", [3e38, -1e36, -3e38])
+def test_windows_whose_first_page_only_some_rows_see(cuda_device, D, hq, T, L, size):
+    """The first row's window starts at the last key of a page, the others' on the
+    next; scores of any size that float32 holds.  Bound as above."""
+    d = _dsb()
+    rng = np.random.default_rng(L)
+    n, w = -(-L // P) + 1, L - T + 1 - 127
+    v = rng.standard_normal((n * P, D))
+    k = np.full((P, D), 2.0 ** -20)
+    pool = np.stack([oq4.pack_block(*oq4.quantise(k), *oq4.quantise(v[a:a + P])) for a in range(0, n * P, P)])[:, None]
+    q = np.zeros((T, hq, D), np.float32)
+    q[..., 3] = size
+    q[..., 5] = -size / 4
+    _, vvals = oq4.pool_values(pool, D)
+    _, vsize = oq4.pool_sizes(pool, D)
+    vvals, vsize = vvals.reshape(-1, D), vsize.reshape(-1, D)
+    got = to_host(d.attention_decode_q4(to_dev(q), d.kv_q4_pages(to_dev(pool), D),
+                                        d.PagedBatch([list(range(n))], [n], [w], [T], [L]), d.Workspace(T, hq, D, L)))
+    for j in range(T):
+        seen = slice(127 + j, L - T + j + 1)
+        assert (np.abs(got[j] - vvals[seen].mean(0)) <= 2.0 ** -20 * vsize[seen].mean(0)).all()
+    d.device_error()
