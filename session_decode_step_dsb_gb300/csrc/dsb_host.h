@@ -27,7 +27,11 @@ inline dsb_status fail(dsb_status st, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  try {
+    g_last_error = buf;
+  } catch (...) {  // no memory for the message: it is called while an entry point reports just that
+    g_last_error.clear();
+  }
   return st;
 }
 

@@ -137,3 +137,43 @@ def test_memory_that_a_call_reads_and_writes_is_apart():
         for k, v in ((o, rows), (rows, o)):
             assert said(lib.dsb_kv_gather_q4(ctypes.byref(kv), b.ref, f.ctypes.data, c.ctypes.data, 0, k, v, ws, None)) == \
                 "k_out / v_out and the page pool overlap"
+
+
+PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+#include "dsb_host.h"
+static bool none = false;
+void* operator new(std::size_t n) {
+  if (none) throw std::bad_alloc();
+  if (void* p = std::malloc(n)) return p;
+  throw std::bad_alloc();
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t) noexcept { std::free(p); }
+int main() {
+  none = true;
+  dsb_status st = dsbh::fail(DSB_ERR_INVALID_ARG, "%s", "a message that is longer than a string holds without memory");
+  none = false;
+  std::printf("%d [%s]\n", (int)st, dsbh::g_last_error.c_str());
+  st = dsbh::fail(DSB_ERR_WORKSPACE, "%s", "a message that is longer than a string holds without memory");
+  std::printf("%d %zu\n", (int)st, dsbh::g_last_error.size());
+}
+"""
+
+
+def test_an_error_without_memory_for_its_message_is_still_a_status(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    from session_decode_step_dsb_gb300 import build
+    cxx, cuda = shutil.which("g++"), os.path.join(os.path.dirname(os.path.dirname(build._nvcc())), "include")
+    if cxx is None or not os.path.exists(os.path.join(cuda, "cuda_runtime.h")):
+        pytest.skip("no host compiler or CUDA headers")
+    src, exe = tmp_path / "m.cpp", tmp_path / "m"
+    src.write_text(PROGRAM)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", build.INCLUDE, "-I", build.CSRC, "-I", cuda, str(src), "-o", str(exe),
+                    "-lpthread"], check=True, capture_output=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0 and got.stdout.splitlines() == ["1 []", "3 59"]
