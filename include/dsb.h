@@ -427,7 +427,9 @@ dsb_status dsb_attention_decode_multi_noalloc(const float* q, int n_q_heads, con
  * stream.  The words of a call: rope_rotary one a
  * token, or two for each run of consecutive positions; append 3 a sequence + 2
  * + the pages its new tokens touch; attention 8 a sequence + 1 + the pages it
- * visits; gather 5 a sequence + 1 + the pages it reads.  The workspace must
+ * visits; gather 5 a sequence + 1 + the pages it reads.  Attention and gather cut
+ * a call of more than 11281 words between its sequences; a sequence that alone
+ * takes more (some 1.4 million keys) is DSB_ERR_UNSUPPORTED.  The workspace must
  * belong to the current device. */
 
 /* Scaling of the rotation's frequencies f_i = theta^(-2i/r) for contexts longer
@@ -459,7 +461,8 @@ typedef struct {
  * each in [0, 2^24)).  q: device float32, row t at q + t * q_stride, heads of
  * head_dim side by side; k alike (NULL with n_kv_heads = 0).  q and k may be
  * parts of the same rows (the strides of a fused projection, q_stride = k_stride
- * then) but share no value.  head_dim even in [2, 1024].  Angles pos[t] f_i, with
+ * then) but share no value, and each starts on 16 bytes: in a fused row k does where
+ * n_q_heads head_dim is a multiple of 4.  head_dim even in [2, 1024].  Angles pos[t] f_i, with
  * f_i in float64, modulo one turn in 64-bit integer arithmetic; c and s the float32
  * nearest to their cosine and sine times the gain (but for one in some thousands at
  * most, at any position); x c - y s and x s + y c with every product and sum rounded

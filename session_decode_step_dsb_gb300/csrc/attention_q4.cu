@@ -18,9 +18,9 @@
 // second's operand layout by an 8 x 8 transpose in the warp.
 //
 // Work: a CTA of four warps takes units of a few pages of one (sequence, kv
-// head, tile of 8 query rows); how many pages a unit has depends on the
-// sequence's own length alone, so a sequence's rows are bitwise the same alone
-// and in a batch.  A warp takes 32 of a page's 128 keys and carries its own
+// head, tile of 4 or 8 query rows); how many pages a unit has depends on the
+// sequence alone (its pages, kv heads and rows), so a sequence's rows are bitwise
+// the same alone and in a batch.  A warp takes 32 of a page's 128 keys and carries its own
 // maximum, sum and output tile through the unit: inside a unit the warps meet at
 // no barrier but those of the copies.  The K and V halves of the pages arrive as
 // bulk copies, four halves ahead.  The four warps' results are joined at the unit's
@@ -33,11 +33,11 @@
 // sums over it are float32.
 //
 // Measured: 4 sequences of 16384 to 65536 keys, 32 kv heads of 128, one row each
-// (820 MB of pages): 193 us with the join, 4.3 TB/s, 0.63 of the copy rate.  Bound by
-// instruction issue and its latencies: some 650 instructions a warp and page, 290 of
-// them the unpacking of the codes, at 16 warps an SM (123 registers), issued in 0.6 of
-// the cycles; an eighth of the waiting is at the units' ends.  16 sequences of up to
-// 4096 keys, 8 kv heads of 128, 5 rows each (39 MB): 20 us for 2 or 4 pages a CTA.
+// (720 MB of pages): 193 us with the join, 3.7 TB/s, 0.55 of the copy rate.  Bound by
+// the latencies of some 640 instructions a warp and page, 290 of them the unpacking of
+// the codes, at 16 warps an SM (124 registers; with 8 rows 128), issued in 0.6 of the
+// cycles; an eighth of the waiting is at the units' ends.  16 sequences of up to
+// 4096 keys, 8 kv heads of 128, 5 rows each (29 MB): 20 us for 2 or 4 pages a CTA.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -23,11 +23,12 @@
 // The unpacking of V runs while the first product does, that of the next K while
 // the second does; two CTAs share an SM.
 //
-// Measured: 8 sequences of 4096 to 16384 keys, 8 kv heads of 128, 40 rows each: 135 us
-// for two tiles of 24 (98 MB of pages, read twice).  Bound by the threads' work on the
-// operands: some 800 instructions a warp and page (codes and weights to fp16, masks,
-// sums), issued in half of the cycles between the barriers of a page; the CTA with the
-// most pages takes a fifth longer than the mean.
+// Measured: 8 sequences of 4096 to 16384 keys (77760 in all), 8 kv heads of 128, 40
+// rows each: 132 us for two tiles of 24 (85 MB of pages, read twice).  Bound by latency:
+// the phases of a page follow one another, some 800 instructions a warp (codes and
+// weights to fp16, masks, sums) issued in half of the cycles by 18 warps an SM with 96
+// registers a thread (8 bytes spilled); the CTA with the most pages takes a fifth longer
+// than the mean.
 //
 // A row's reference is set 2^10 below its largest weight of the unit's first page;
 // a page that brings 2^4 more (any thread sees it) is weighed again with a new one.

@@ -297,11 +297,11 @@ constexpr int kQ4SeqWords = 8;
 // (attention_q4_tc.cu), whose items unpack a page once for three times the rows but take
 // longer to start and to end.
 // Measured at 8 kv heads of 128, warp-level and tcgen05: one sequence of 2048 keys and
-// 64 rows 19 and 24 us; 8 sequences of 4096 to 16384 keys, 16 rows 81 and 82 us, 24 rows
-// 117 and 98, 32 rows 147 and 161, 40 rows 177 and 162, 64 rows 255 and 228: a tile of 24
-// costs 2.2 tiles of 8.  At heads of 64 (12 kv heads), where a page holds half the work,
-// the tcgen05 kernel took longer for all of them (same sequences, 24 rows 120 and 122 us,
-// 40 rows 187 and 207) and is not built.
+// 64 rows 19 and 23 us; 8 sequences of 4096 to 16384 keys (77760 in all), 16 rows 75 and
+// 85 us, 24 rows 103 and 88, 32 rows 133 and 140, 40 rows 159 and 142, 64 rows 224 and
+// 205: a tile of 24 costs 2.2 tiles of 8.  At heads of 64 (12 kv heads), where a page
+// holds half the work, an earlier tcgen05 kernel took longer for all of them (8 sequences
+// of 91559 keys in all, 24 rows 120 and 122 us, 40 rows 187 and 207) and is not built.
 inline int q4_tile_rows(long long rows, int n, int head_dim) {
   if (rows <= 4) return 4;
   return head_dim == 128 && n > 16 && 9 * ((rows + 7) / 8) > 20 * ((rows + 23) / 24) ? 24 : 8;

@@ -3,7 +3,7 @@
 //
 // Bound by its writes: (D + 8) bytes in, 4 D out per key and head.  One CTA per
 // (page, kv head); a thread turns eight codes into one 16-byte store.  8 sequences of
-// 4096 to 16384 keys of 8 heads of 128 (457 MB): 70 us, 6.5 TB/s, 0.96 of the copy
+// 4096 to 16384 keys of 8 heads of 128 (425 MB): 67 us, 6.3 TB/s, 0.93 of the copy
 // rate; 87 us with a head's pages side by side and loads between the stores.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

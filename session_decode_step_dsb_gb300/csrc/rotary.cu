@@ -338,9 +338,10 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&y)[8], float d, float
 // handles the same dimensions of one head after the other, the next one's values on
 // their way, with one set of sines and cosines.  Head h of the row: query heads, then
 // key heads, then value heads.  With many tokens one CTA takes all heads of its token,
-// so the token's set-up is paid once.  Bound by instruction issue: those 5178 tokens
-// move 205 MB (30 us at the copy rate) in 45 us.  16 tokens: 4.5 us, the latency of the
-// chain.
+// so the token's set-up is paid once.  Those 5178 tokens read and write 266 MB (39 us at
+// the copy rate) in 45 us, with 0.71 of the issue slots full: the token's set-up and the
+// shuffles wait.  Into 16-bit pages (276 MB) they take 1 us less.  16 tokens: 4.5 us, the
+// latency of the chain.
 // Metadata: tok_off[n + 1] | pos0[n] | pg_off[n + 1] | pages of every sequence,
 // from the page of its first new key on.
 template <int D, typename Store, int N>
