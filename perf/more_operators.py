@@ -372,7 +372,7 @@ def _run_select(s):
     case = s["case"]
     if own:
         from session_decode_step_dsb_gb300 import dsb
-        dsb.kv_page_bounds(s["kv"], s["batch"], s["bounds"], s["ws"])
+        dsb.kv_page_bounds(s["kv"], s["batch"], s["bounds"])
         got = dsb.kv_select_pages(s["q"], s["kv"], s["bounds"], s["batch"], case["n_select"], s["ws"],
                                   keep_first=case["first"], keep_last=case["last"])
         return {"bounds": s["bounds"], "selected": got}
