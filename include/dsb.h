@@ -556,6 +556,86 @@ dsb_status dsb_attention_decode_q4(const float* q, int64_t q_stride, int n_q_hea
 dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* batch, const int32_t* first,
                             const int32_t* count, int dtype, void* k_out, void* v_out, dsb_workspace* ws, void* stream);
 
+/* ---- whole pages: copies, shared pages, selected pages ---------------------------
+ *
+ * What a server does with the pages of a cache: a session is forked (its full pages
+ * are shared by reference, its last, partly filled one is copied), a pool is compacted
+ * (pages move, block tables follow), sessions that begin alike read the same pages, and
+ * a long context is read in part.  They are no restatement of the pages that the
+ * library was built from.  As above, metadata of up to 4032 words rides in the
+ * launches, which can then be captured into a CUDA graph; under capture a longer call
+ * is cut between sequences where each fits, and DSB_ERR_UNSUPPORTED where one does not. */
+
+/* Copies rows 0 .. keys[i] - 1 of page src[i] to page dst[i], of every kv head, K and V,
+ * in each of n_pools pools (host array, one for each layer; all of one dtype, n_pages,
+ * n_kv_heads and head_dim; 1 to 512).  src, dst, keys: host int32[n_copies], keys in
+ * [0, 128] (0: nothing).  The other rows of dst keep their values.  A page may be the
+ * source of several copies.  One that is written twice, or read and written, is
+ * DSB_ERR_INVALID_ARG (two steps make a chain), and so are pools that share memory.
+ * head_dim 64 or 128.  No workspace; can be captured. */
+dsb_status dsb_kv_copy_pages(const dsb_kv_pages* pools, int n_pools, const int32_t* src, const int32_t* dst,
+                             const int32_t* keys, int n_copies, void* stream);
+
+/* The same of 4-bit pages: codes and numbers of the keys, bit for bit. */
+dsb_status dsb_kv_copy_pages_q4(const dsb_kv_q4_pages* pools, int n_pools, const int32_t* src, const int32_t* dst,
+                                const int32_t* keys, int n_copies, void* stream);
+
+/* Decode attention over 16-bit pages for a ragged batch, in which pages that sequences
+ * have in common are read once for all of them.  Pages are in common where block tables
+ * without a window begin alike, at any depth (a prompt of all, a document of some); a
+ * batch without such pages is served as well.  New token j of sequence s at position p
+ * = seq_lens[s] - new_tokens[s] + j sees keys max(0, p - window[s] + 1) .. p (all up to
+ * p without a window), new tokens having been appended; score = q.k / sqrt(head_dim),
+ * out = softmax(score) V, float32 accuracy.  q: device float32, row t at
+ * q + t * q_stride (a multiple of 4); out: device float32 [tokens][n_q_heads][head_dim],
+ * apart from q's rows and the pools.  Any number of new tokens; a sequence without any
+ * has no rows.  n_q_heads a multiple of n_kv_heads; head_dim 64 or 128.  What lies
+ * behind a sequence's last key, or is hidden from a row, does not reach the row, NaN
+ * and infinities included; a row that sees a NaN or an infinity in K or V has no
+ * finite result where it counts.  Partial sums go to the workspace:
+ * dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest seq_lens) is enough.  No
+ * atomics: the same call gives the same bits (in another batch, sums are cut
+ * elsewhere). */
+dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                                       const dsb_paged_batch* batch, float* out, dsb_workspace* ws, void* stream);
+
+/* Bounds of the pages that the batch's new tokens lie on: bounds (device, the pool's
+ * dtype, [n_pages][n_kv_heads][2][head_dim], 16-byte aligned) gets for each of these
+ * pages, kv heads and dimensions the least and the largest value of K over the
+ * sequence's keys on the page, all of them (so a page that a session took back keys
+ * from is right again).  A NaN makes both NaN.  Bounds of other pages keep their
+ * values.  Call it after an append; a copied page's bounds are made when its session
+ * appends to it.  Two sequences with new tokens on one page are DSB_ERR_INVALID_ARG,
+ * rings (window > 0) DSB_ERR_UNSUPPORTED.  No workspace; can be captured. */
+dsb_status dsb_kv_page_bounds(const dsb_kv_pages* kv, const dsb_paged_batch* batch, void* bounds, void* stream);
+
+/* Selects for every new token and kv head up to n_select of the pages that the token
+ * sees: the first keep_first, the newest keep_last (the token's own among them,
+ * keep_last >= 1), then those of the largest score, ties to the lowest index.  The
+ * score of a page with bounds lo, hi for the query rows r of the head's group is
+ *   sum_d a_d hi_d + b_d lo_d,  a_d = sum_r max(q_rd, 0),  b_d = sum_r min(q_rd, 0),
+ * no key of the page has a larger sum_r q_r . k.  Each product and sum is rounded to
+ * float32; the sums over r (as if zeros followed up to a power of two) and over d are
+ * taken pairwise, neighbours first.  A score that is NaN counts as the largest.
+ * selected: device int32 [tokens][n_kv_heads][n_select], 16-byte aligned, indices of
+ * the sequence's blocks in rising order, -1 behind the last.  The bounds of all pages
+ * of the batch must have been made.  q as in dsb_attention_decode_shared; rings are
+ * DSB_ERR_UNSUPPORTED. */
+dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                               const void* bounds, const dsb_paged_batch* batch, int n_select, int keep_first,
+                               int keep_last, int32_t* selected, dsb_workspace* ws, void* stream);
+
+/* Decode attention over the listed pages alone: a row of token t and kv head h sees the
+ * keys up to its position on the blocks selected[t][h][0 .. n_select - 1] (device int32,
+ * 16-byte aligned; as dsb_kv_select_pages writes them).  Entries that are no block up to
+ * the token's own (-1) are skipped, one that is listed twice counts twice; as many are
+ * read as the call's longest sequence has pages.  A row that sees no key is 0.  Other
+ * arguments and the workspace as dsb_attention_decode_shared; rings are
+ * DSB_ERR_UNSUPPORTED. */
+dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                                         const dsb_paged_batch* batch, const int32_t* selected, int n_select,
+                                         float* out, dsb_workspace* ws, void* stream);
+
 /* ---- measurement probe -------------------------------------------------------
  * The issue rate and latency of the four-way int8 dot product (__dp4a) the
  * narrow q8_0 matmul is built on, so that its arithmetic ceiling comes from a

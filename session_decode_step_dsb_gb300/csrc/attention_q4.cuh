@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "dsb_f32x2.cuh"
 #include "dsb_kernels.h"
 #include "dsb_ptx.cuh"
 #include "dsb_q4.cuh"
@@ -28,33 +29,6 @@ __device__ __forceinline__ float lg2(float x) {
 // most 2^14 over this) whose sums, of p_k z_k too, stay within float32.
 constexpr float kLeastScale = 0x1p-60f;
 
-// Two float32 at once.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack(float a, float b) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 // x0, x1 as hi + lo fp16 pairs.
 __device__ __forceinline__ void split(f2 x, uint32_t& hi, uint32_t& lo) {
   const float2 v = unpack(x);

@@ -1,0 +1,270 @@
+// What the kernels of the attention over shared and over selected pages have in common:
+// the plan that the host lays down and a CTA's walk over it.
+//
+// A plan is a list of segments.  A segment is a run of pages that one or more sequences
+// read: the leading pages that several have in common, or those of one alone.  Its rows
+// are its sequences' query rows on a kv head, one sequence after the other; they are cut
+// into tiles, and a (segment, kv head, tile) is a run of pages to go through.  The runs
+// lie behind each other, counted in pages, and each CTA takes one even share of them,
+// whole or cut: a run has as many parts as CTAs reach into it, and every part leaves its
+// rows' sums in a slot of its own.  The join adds the slots of a row, in order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "dsb_f32x2.cuh"
+#include "dsb_kernels.h"
+#include "dsb_ptx.cuh"
+
+namespace dsbk {
+
+constexpr int kPgKeys = 128;
+// minus the reference of a row that has seen no key: the reference lies below any score
+constexpr float kNoRef = 0x1.fffffep127f;
+// A row's weights are exp2(score - reference), the reference 2^kRoom below its largest
+// score so far; a score that brings 2^kSlack more moves it.
+constexpr float kRoom = 10.0f, kSlack = 4.0f;
+
+__device__ __forceinline__ float exp2_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A float32 pair as two or three pairs of the 16-bit type that add up to it: fp16 to 22
+// bits in two; bf16 to 16 in two, 24 in three.
+template <typename T>
+struct Parts;
+template <>
+struct Parts<__half> {
+  static constexpr int kScore = 2;  // parts of a query value
+  static __device__ __forceinline__ uint32_t take(float& x, float& y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    x -= f.x;
+    y -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <>
+struct Parts<__nv_bfloat16> {
+  static constexpr int kScore = 3;
+  static __device__ __forceinline__ uint32_t take(float& x, float& y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+    x -= __uint_as_float(w << 16);
+    y -= __uint_as_float(w & 0xFFFF0000u);
+    return w;
+  }
+};
+
+// Where sums go: statistics (-reference, sum of weights) and sums of weighted values of
+// [row][slot]; out where a row has one part.  A sum of weights of -1: the row is done.
+struct PartialsOut {
+  float2* stat;
+  float* acc;
+  float* out;
+  int slots;  // of a row
+};
+
+// One row of a tile: its place in q, in out, and the keys that it sees.
+struct RowAt {
+  int tok, row, lo, hi;  // row: token * query heads + head
+};
+
+// Walk over the segments of a plan (all fields alike in the threads that share it).
+struct SharedWalk {
+  const int32_t* meta;
+  int n_seg, hkv, G, rows;  // rows of a tile
+  long long total;
+  // the segment
+  int seg, n_rows, mem_at, n_mem, chunk0, n_pages, pg_at, slot0, cap, first, last, tiles;
+  // the run, and this CTA's part of it
+  int h, tile, at;      // at: pages before the run
+  int i, i_end;         // pages of the run
+  int stop;             // end of this CTA's share
+
+  __device__ __forceinline__ void load() {
+    const int32_t* p = meta + seg * kSharedSegWords;
+    n_rows = p[1];
+    mem_at = p[2];
+    n_mem = p[3];
+    chunk0 = p[4];
+    n_pages = p[5];
+    pg_at = p[6];
+    slot0 = p[7];
+    cap = p[8];
+    first = p[9];
+    last = p[10];
+    tiles = (n_rows + rows - 1) / rows;
+  }
+  __device__ __forceinline__ void begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int cta, int ctas) {
+    meta = m;
+    n_seg = n;
+    hkv = kv_heads;
+    G = group;
+    rows = tile_rows;
+    total = m[n * kSharedSegWords];
+    const int start = (int)(total * cta / ctas);
+    stop = (int)(total * (cta + 1) / ctas);
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (m[mid * kSharedSegWords] <= start)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    seg = lo;
+    load();
+    const int rel = start - m[lo * kSharedSegWords], run = rel / n_pages;
+    h = run / tiles;
+    tile = run - h * tiles;
+    i = rel - run * n_pages;
+    at = start - i;
+    i_end = min(n_pages, stop - at);
+  }
+  // Whether this CTA has a part of another run, and the walk to it.
+  __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
+  __device__ __forceinline__ void next() {
+    at += n_pages;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == hkv) {
+        h = 0;
+        ++seg;
+        load();
+      }
+    }
+    i = 0;
+    i_end = min(n_pages, stop - at);
+  }
+  __device__ __forceinline__ int page(int e) const { return meta[pg_at + e]; }
+  __device__ __forceinline__ int block(int e, int) const { return chunk0 + e; }
+  __device__ __forceinline__ int listed(int) const { return 0; }
+  // whether keys key0 .. key0 + n - 1 can be seen by any row of the segment
+  __device__ __forceinline__ bool seen(int key0, int n) const { return key0 <= last && key0 + n > first; }
+  // The CTA that a page of work lies with, of `ctas`.
+  __device__ __forceinline__ int cta_of(int w, int ctas) const { return (int)(((long long)(w + 1) * ctas - 1) / total); }
+  // Parts of this run before this CTA's, and in all.
+  __device__ __forceinline__ int part(int cta, int ctas) const { return cta - cta_of(at, ctas); }
+  __device__ __forceinline__ int parts(int ctas) const { return cta_of(at + n_pages - 1, ctas) - cta_of(at, ctas) + 1; }
+  __device__ __forceinline__ int slot_base() const { return slot0; }
+  __device__ __forceinline__ int slot_cap() const { return cap; }
+  __device__ __forceinline__ bool alone() const { return slot0 == 0 && meta[seg * kSharedSegWords + 11] == cap; }
+  __device__ __forceinline__ int tile_rows() const { return min(rows, n_rows - tile * rows); }
+  __device__ __forceinline__ RowAt row(int r, int hq) const {
+    r += tile * rows;
+    int lo = 0, hi = n_mem - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (meta[mem_at + mid * kSharedMemWords] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int32_t* m = meta + mem_at + lo * kSharedMemWords;
+    const int rel = r - m[0], j = rel / G, gi = rel - j * G;
+    RowAt a;
+    a.tok = m[1] + j;
+    a.row = a.tok * hq + h * G + gi;
+    a.hi = m[3] - m[2] + j;
+    a.lo = m[4] > 0 ? max(0, a.hi - m[4] + 1) : 0;
+    return a;
+  }
+};
+
+// Walk over the selected pages: a run is the list of a (token, kv head, tile of its group).
+struct SelectedWalk {
+  const int32_t* meta;
+  const int32_t* sel;
+  int n_seg, hkv, G, rows, n_sel, stride, cap;
+  long long total;
+  int seg, tok, tok_end, len0, pg_at, tiles, h, tile, at, i, i_end, stop, last;
+  int n_pages;  // entries of a run
+
+  __device__ __forceinline__ void load() {
+    const int32_t* p = meta + seg * kSelSeqWords;
+    tok_end = p[0] + p[1];
+    len0 = p[2] - p[1] - p[0];  // + token: its position
+    pg_at = p[3];
+  }
+  __device__ __forceinline__ void begin(const int32_t* m, int n, const int32_t* selected, int n_select, int list_stride, int slots,
+                                        int n_tok, int kv_heads, int group, int tile_rows, int cta, int ctas) {
+    meta = m;
+    sel = selected;
+    n_seg = n;
+    hkv = kv_heads;
+    G = group;
+    rows = tile_rows;
+    n_sel = n_pages = n_select;
+    stride = list_stride;
+    cap = slots;
+    tiles = (G + rows - 1) / rows;
+    total = (long long)n_tok * hkv * tiles * n_sel;
+    const int start = (int)(total * cta / ctas);
+    stop = (int)(total * (cta + 1) / ctas);
+    const int run = start / n_sel, th = run / tiles;
+    i = start - run * n_sel;
+    tile = run - th * tiles;
+    tok = th / hkv;
+    h = th - tok * hkv;
+    at = start - i;
+    i_end = min(n_pages, stop - at);
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (m[mid * kSelSeqWords] <= tok)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    seg = lo;
+    load();
+    last = len0 + tok;
+  }
+  __device__ __forceinline__ void next() {
+    at += n_pages;
+    if (++tile == tiles) {
+      tile = 0;
+      if (++h == hkv) {
+        h = 0;
+        if (++tok == tok_end) {
+          ++seg;
+          load();
+        }
+        last = len0 + tok;
+      }
+    }
+    i = 0;
+    i_end = min(n_pages, stop - at);
+  }
+  __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
+  // The block of entry e; one that the token does not see becomes a block behind its last.
+  __device__ __forceinline__ int listed(int e) const {
+    const int b = __ldg(sel + ((size_t)tok * hkv + h) * stride + e);
+    return b >= 0 && b <= last / kPgKeys ? b : last / kPgKeys + 1;
+  }
+  __device__ __forceinline__ int block(int, int got) const { return got; }
+  __device__ __forceinline__ bool seen(int key0, int) const { return key0 <= last; }
+  __device__ __forceinline__ int cta_of(int w, int ctas) const { return (int)(((long long)(w + 1) * ctas - 1) / total); }
+  __device__ __forceinline__ int part(int cta, int ctas) const { return cta - cta_of(at, ctas); }
+  __device__ __forceinline__ int parts(int ctas) const { return cta_of(at + n_pages - 1, ctas) - cta_of(at, ctas) + 1; }
+  __device__ __forceinline__ int slot_base() const { return 0; }
+  __device__ __forceinline__ int slot_cap() const { return cap; }
+  __device__ __forceinline__ bool alone() const { return true; }
+  __device__ __forceinline__ int tile_rows() const { return min(rows, G - tile * rows); }
+  __device__ __forceinline__ RowAt row(int r, int hq) const {
+    RowAt a;
+    a.tok = tok;
+    a.row = tok * hq + h * G + tile * rows + r;
+    a.hi = last;
+    a.lo = 0;
+    return a;
+  }
+};
+
+}  // namespace dsbk

@@ -335,4 +335,61 @@ constexpr int kQ4SpanWords = 5;
 cudaError_t launch_gather_q4(const void* pool, int hkv, int head_dim, int n_seq, long long pages, int dtype, void* k,
                              void* v, const MetaArg& meta, cudaStream_t st);
 
+// ---- whole pages: copies, bounds and selection, attention over shared and selected pages
+// (csrc/copy_pages.cu, csrc/select_pages.cu, csrc/attention_shared.cu)
+
+// Metadata (always in the parameters): the planes' addresses in two words each, then
+// (source page, destination page, keys) of each copy.  A plane: the K or the V pages of a
+// 16-bit pool, or a 4-bit pool.
+cudaError_t launch_copy_pages(int planes, int copies, int hkv, int head_dim, bool q4, const MetaArg& meta, cudaStream_t st);
+
+// Metadata (always in the parameters): (page, keys) of each page; keys >= 1.  bounds:
+// [pages of the pool][hkv][2][head_dim], least values then largest.
+cudaError_t launch_page_bounds(const void* k, int dtype, int hkv, int head_dim, int pages, void* bounds,
+                               const MetaArg& meta, cudaStream_t st);
+
+// Metadata of the selection and of the attention over selected pages: of each sequence its
+// first token, new tokens, length, and where its pages are; then the pages.
+constexpr int kSelSeqWords = 4;
+struct SelectArgs {
+  const float* q;
+  long long q_stride;
+  int hq, hkv;
+  const void* bounds;
+  int n_seq, n_tok, n_select, keep_first, keep_last;
+  int32_t* selected;  // [n_tok][hkv][n_select]
+  int ranks;          // CTAs of a cluster, which share the pages of a (token, kv head)
+  int max_pages;      // of a sequence
+};
+cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
+
+// A plan's metadata: n_seg segments of kSharedSegWords (pages of work before it, rows on a
+// kv head, where its sequences are and how many, block of its first page, pages, where they
+// are, first slot, slots, first and last key that any row sees, slots of its rows in all);
+// the pages of work; sequences of kSharedMemWords (first row, first token, new tokens,
+// length, window); pages.
+constexpr int kSharedSegWords = 12, kSharedMemWords = 5;
+struct PageAttnArgs {
+  const float* q;
+  long long q_stride;
+  int hq, hkv;
+  const void* k;
+  const void* v;
+  int n_seg, n_tok;
+  const int32_t* selected;  // or NULL: a plan of segments
+  int n_select, sel_stride; // entries read of a list, and in it
+  int sel_cap;              // slots of every row of a selection
+  float* stat;              // [n_tok][hq][slots] pairs: reference, sum of weights
+  float* acc;               // [n_tok][hq][slots][head_dim]
+  float* out;               // [n_tok][hq][head_dim]
+  int slots;
+  int ctas;
+};
+// CTAs that the GPU runs at once.
+int page_attn_resident(int sms);
+cudaError_t launch_attention_pages(const PageAttnArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
+// Metadata (always in the parameters): of each sequence its first token and its rows'
+// slots (0: nothing to join).
+cudaError_t launch_attention_join(const PageAttnArgs& a, int n_seq, int head_dim, const MetaArg& meta, cudaStream_t st);
+
 }  // namespace dsbk

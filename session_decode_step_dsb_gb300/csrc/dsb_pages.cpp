@@ -1,0 +1,625 @@
+// C ABI of the calls on whole KV pages (declared in include/dsb.h): copies, bounds and
+// selection, attention over pages that sequences share and over selected pages.  As in
+// dsb.cpp, all arguments are checked on the host before any CUDA call.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+#include <cstring>
+#include <numeric>
+#include <vector>
+
+#include "dsb.h"
+#include "dsb_host.h"
+#include "dsb_kernels.h"
+#include "dsb_paged_host.h"
+
+using namespace dsbh;
+
+namespace {
+
+dsb_status check_pages16(const dsb_kv_pages* kv) {
+  if (!kv) return fail(DSB_ERR_INVALID_ARG, "kv is NULL");
+  if (!kv->k || !kv->v) return fail(DSB_ERR_INVALID_ARG, "kv->k / kv->v is NULL");
+  if (!aligned16(kv->k) || !aligned16(kv->v)) return fail(DSB_ERR_INVALID_ARG, "page pools not 16-byte aligned");
+  if (kv->dtype != DSB_F16 && kv->dtype != DSB_BF16) return fail(DSB_ERR_INVALID_ARG, "dtype must be DSB_F16 or DSB_BF16");
+  if (kv->n_pages < 1 || kv->n_kv_heads < 1) return fail(DSB_ERR_INVALID_ARG, "n_pages / n_kv_heads < 1");
+  if (kv->head_dim != 64 && kv->head_dim != 128)
+    return fail(DSB_ERR_UNSUPPORTED, "head_dim=%d: these calls serve 64 and 128", kv->head_dim);
+  if (kv->n_kv_heads > 65535 || (long long)kv->n_pages * kv->n_kv_heads > (INT_MAX - 128) / DSB_KV_PAGE)
+    return fail(DSB_ERR_UNSUPPORTED, "a pool of %d pages x %d kv heads", kv->n_pages, kv->n_kv_heads);
+  return DSB_OK;
+}
+
+size_t pool16_bytes(const dsb_kv_pages* kv) {
+  return (size_t)kv->n_pages * kv->n_kv_heads * DSB_KV_PAGE * kv->head_dim * 2;
+}
+
+dsb_status check_linear(const dsb_paged_batch* b) {
+  for (int s = 0; s < b->n_seq; ++s)
+    if (b->window[s] != 0) return fail(DSB_ERR_UNSUPPORTED, "sequence %d: pages are selected from linear tables, not rings", s);
+  return DSB_OK;
+}
+
+dsb_status check_q(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv) {
+  if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % kv->n_kv_heads)
+    return fail(DSB_ERR_INVALID_ARG, "n_q_heads=%d is not a positive multiple of n_kv_heads=%d", n_q_heads, kv->n_kv_heads);
+  if (q_stride < (int64_t)n_q_heads * kv->head_dim || q_stride % 4 || q_stride > (1LL << 40))
+    return fail(DSB_ERR_INVALID_ARG, "q_stride=%lld must be a multiple of 4, at least %lld", (long long)q_stride,
+                (long long)n_q_heads * kv->head_dim);
+  return DSB_OK;
+}
+
+// out[n_tok][width] of an attention call, apart from what it reads.
+dsb_status check_out(const float* q, int64_t q_stride, int64_t width, int n_tok, const dsb_kv_pages* kv, const float* out) {
+  const size_t bytes = n_tok * width * sizeof(float);
+  if (overlap(q, ((n_tok - 1) * q_stride + width) * sizeof(float), out, bytes))
+    return fail(DSB_ERR_INVALID_ARG, "out overlaps the rows of q");
+  for (const void* pool : {kv->k, kv->v})
+    if (overlap(pool, pool16_bytes(kv), out, bytes)) return fail(DSB_ERR_INVALID_ARG, "out overlaps the page pools");
+  return DSB_OK;
+}
+
+// Copies within every plane: the sources and destinations of n_copies, one launch for as
+// many as the parameters hold.
+dsb_status copy_common(const std::vector<void*>& planes, size_t plane_bytes, int n_pages, int n_kv_heads, int head_dim,
+                       bool q4, const int32_t* src, const int32_t* dst, const int32_t* keys, int n_copies, void* stream) {
+  if (n_copies < 0) return fail(DSB_ERR_INVALID_ARG, "n_copies=%d < 0", n_copies);
+  if (n_copies > 0 && (!src || !dst || !keys)) return fail(DSB_ERR_INVALID_ARG, "src / dst / keys is NULL");
+  std::vector<void*> sorted(planes);
+  std::sort(sorted.begin(), sorted.end());
+  for (size_t i = 1; i < sorted.size(); ++i)
+    if (overlap(sorted[i - 1], plane_bytes, sorted[i], plane_bytes))
+      return fail(DSB_ERR_INVALID_ARG, "two page pools of the call overlap");
+  std::vector<int> live;
+  std::vector<std::pair<int, int>> used;  // page, copy (destinations), or page, -1 (sources)
+  for (int i = 0; i < n_copies; ++i) {
+    if (src[i] < 0 || src[i] >= n_pages || dst[i] < 0 || dst[i] >= n_pages)
+      return fail(DSB_ERR_INVALID_ARG, "copy %d: pages %d -> %d out of [0, %d)", i, src[i], dst[i], n_pages);
+    if (keys[i] < 0 || keys[i] > DSB_KV_PAGE)
+      return fail(DSB_ERR_INVALID_ARG, "keys[%d]=%d out of [0, %d]", i, keys[i], DSB_KV_PAGE);
+    if (keys[i] == 0) continue;
+    live.push_back(i);
+    used.emplace_back(src[i], -1);
+    used.emplace_back(dst[i], i);
+  }
+  std::sort(used.begin(), used.end());
+  for (size_t i = 1; i < used.size(); ++i)
+    if (used[i].first == used[i - 1].first && used[i].second >= 0)
+      return fail(DSB_ERR_INVALID_ARG, "page %d is written by copy %d and %s", used[i].first, used[i].second,
+                  used[i - 1].second < 0 ? "read by the same call" : "another one");
+  const size_t head = 2 * planes.size(), room = ((size_t)dsbk::kParamWords - head) / 3;
+  std::vector<int32_t> words;
+  for (size_t at = 0; at < live.size(); at += room) {
+    const size_t n = std::min(room, live.size() - at);
+    words.clear();
+    for (void* p : planes) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+      words.push_back((int32_t)(uint32_t)a);
+      words.push_back((int32_t)(uint32_t)((uint64_t)a >> 32));
+    }
+    for (size_t i = at; i < at + n; ++i) words.insert(words.end(), {src[live[i]], dst[live[i]], keys[live[i]]});
+    dsbk::MetaArg meta;
+    meta.host = words.data();
+    meta.n_words = (int)words.size();
+    const cudaError_t e = dsbk::launch_copy_pages((int)planes.size(), (int)n, n_kv_heads, head_dim, q4, meta,
+                                                  static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "copy_pages launch");
+  }
+  return DSB_OK;
+}
+
+constexpr int kMaxPools = 512;
+
+// ---- the plan of an attention over shared pages -------------------------------------
+
+struct Segment {
+  int parent;     // segment of the pages before these, or -1
+  int m0, m1;     // its sequences in Tree::order
+  int b0, n;      // first block, pages
+  int rows = 0;   // query rows on a kv head
+  int slot0 = 0, cap = 0;
+};
+
+struct Tree {
+  const dsb_paged_batch* b;
+  int G;
+  std::vector<int> order;  // sequences with new tokens; a segment's are side by side
+  std::vector<Segment> segs;
+  std::vector<int> end;    // last segment of a sequence's path
+
+  const int32_t* table(int s) const { return b->block_table + (size_t)s * b->max_blocks; }
+  int pages(int s) const { return (b->seq_lens[s] - 1) / DSB_KV_PAGE + 1; }
+  int first_block(int s) const {
+    const int w = b->window[s];
+    return w > 0 ? std::max(0, b->seq_lens[s] - b->new_tokens[s] + 1 - w) / DSB_KV_PAGE : 0;
+  }
+  int rows_of(int m0, int m1) const {
+    int r = 0;
+    for (int m = m0; m < m1; ++m) r += G * b->new_tokens[order[m]];
+    return r;
+  }
+  static int tiles(int rows) { return (rows + 7) / 8; }
+
+  // Whether pages that m1 - m0 sequences have in common are worth a segment: where it has
+  // fewer tiles to take them through than the sequences have apart.
+  bool worth(int m0, int m1, int n) const {
+    int apart = 0;
+    for (int m = m0; m < m1; ++m) apart += tiles(G * b->new_tokens[order[m]]);
+    return n > 0 && tiles(rows_of(m0, m1)) < apart;
+  }
+
+  int add(int parent, int m0, int m1, int b0, int b1) {
+    // a segment's metadata has to fit a launch
+    for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {
+      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0)};
+      s.rows = rows_of(m0, m1);
+      parent = (int)segs.size();
+      segs.push_back(s);
+    }
+    return parent;
+  }
+
+  // Segments of order[m0, m1), which have blocks 0 .. known - 1 in common and those before
+  // `from` in segments already (the last of them `parent`).
+  void split(int m0, int m1, int from, int known, int parent) {
+    if (m1 - m0 == 1) {
+      const int s = order[m0];
+      end[s] = add(parent, m0, m1, std::max(from, first_block(s)), pages(s));
+      return;
+    }
+    const int32_t* lead = table(order[m0]);
+    int e = pages(order[m0]);
+    for (int m = m0 + 1; m < m1; ++m) {
+      const int32_t* t = table(order[m]);
+      const int most = std::min(e, pages(order[m]));
+      e = (int)(std::mismatch(lead + known, lead + most, t + known).first - lead);
+    }
+    if (worth(m0, m1, e - from)) {
+      parent = add(parent, m0, m1, from, e);
+      from = e;
+    }
+    // by the page behind the common ones; sequences that end there come first
+    const auto key = [&](int s) { return pages(s) > e ? table(s)[e] : -1; };
+    std::stable_sort(order.begin() + m0, order.begin() + m1, [&](int x, int y) { return key(x) < key(y); });
+    for (int a = m0; a < m1;) {
+      int z = a + 1;
+      const int k = key(order[a]);
+      while (z < m1 && key(order[z]) == k) ++z;
+      if (k >= 0) {
+        split(a, z, from, e, parent);
+      } else {
+        for (; a < z; ++a) end[order[a]] = from < e ? add(parent, a, a + 1, from, e) : parent;
+      }
+      a = z;
+    }
+  }
+
+  void build() {
+    end.assign(b->n_seq, -1);
+    for (int pass = 0; pass < 2; ++pass)
+      for (int s = 0; s < b->n_seq; ++s)
+        if (b->new_tokens[s] > 0 && (b->window[s] > 0) == (pass == 1)) order.push_back(s);
+    int linear = 0;
+    while (linear < (int)order.size() && b->window[order[linear]] == 0) ++linear;
+    if (linear > 0) {
+      // sequences without a first page in common go apart at once
+      const auto key = [&](int s) { return table(s)[0]; };
+      std::stable_sort(order.begin(), order.begin() + linear, [&](int x, int y) { return key(x) < key(y); });
+      for (int a = 0, z; a < linear; a = z) {
+        for (z = a + 1; z < linear && key(order[z]) == key(order[a]);) ++z;
+        split(a, z, 0, z - a > 1 ? 1 : 0, -1);
+      }
+    }
+    for (int m = linear; m < (int)order.size(); ++m) split(m, m + 1, 0, 0, -1);
+  }
+};
+
+// The largest number of parts that a run of n pages has, where every CTA takes at least
+// `share` pages of work.
+int most_parts(int n, long long share) {
+  return n == 1 ? 1 : (int)std::min<long long>(n, (n - 2) / share + 2);
+}
+
+// Segments of one launch.
+struct Launch {
+  std::vector<int> segs;
+  size_t n_words = 1;
+  long long work = 0;
+  int ctas = 1;
+};
+
+// A launch of a call on selected pages: sequences whose metadata it holds.
+struct SelLaunch {
+  std::vector<int32_t> words;
+  int n_seq = 0, tok0 = 0, n_tok = 0, most = 0;
+};
+
+dsb_status selection_launches(const dsb_paged_batch* b, cudaStream_t cs, std::vector<SelLaunch>* out) {
+  const auto pages = [&](int s) { return b->new_tokens[s] == 0 ? 0 : (b->seq_lens[s] - 1) / DSB_KV_PAGE + 1; };
+  size_t all = 0;
+  for (int s = 0; s < b->n_seq; ++s) all += dsbk::kSelSeqWords + pages(s);
+  size_t room = kMetaWords;
+  if (all > (size_t)dsbk::kParamWords) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(cs, &cap);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (cap != cudaStreamCaptureStatusNone) room = dsbk::kParamWords;
+  }
+  std::vector<int> mine;
+  size_t have = 0;
+  int tok = 0;
+  const auto close = [&]() {
+    SelLaunch l;
+    l.n_seq = (int)mine.size();
+    l.tok0 = tok;
+    int at = l.n_seq * dsbk::kSelSeqWords;
+    for (int s : mine) {
+      l.words.insert(l.words.end(), {l.n_tok, b->new_tokens[s], b->seq_lens[s], at});
+      l.n_tok += b->new_tokens[s];
+      l.most = std::max(l.most, pages(s));
+      at += pages(s);
+    }
+    for (int s : mine)
+      for (int i = 0; i < pages(s); ++i) l.words.push_back(page_of(b, s, i));
+    tok += l.n_tok;
+    out->push_back(std::move(l));
+    mine.clear();
+    have = 0;
+  };
+  for (int s = 0; s < b->n_seq; ++s) {
+    if (b->new_tokens[s] == 0) continue;
+    const size_t need = dsbk::kSelSeqWords + (size_t)pages(s);
+    if (need > room) return fail(DSB_ERR_UNSUPPORTED, "sequence %d: a call holds at most %zu words of metadata", s, room);
+    if (have + need > room) close();
+    mine.push_back(s);
+    have += need;
+  }
+  if (!mine.empty()) close();
+  return DSB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dsb_status dsb_kv_copy_pages(const dsb_kv_pages* pools, int n_pools, const int32_t* src, const int32_t* dst,
+                             const int32_t* keys, int n_copies, void* stream) {
+  return guarded([&]() -> dsb_status {
+    if (!pools) return fail(DSB_ERR_INVALID_ARG, "pools is NULL");
+    if (n_pools < 1 || n_pools > kMaxPools) return fail(DSB_ERR_INVALID_ARG, "n_pools=%d out of [1, %d]", n_pools, kMaxPools);
+    std::vector<void*> planes;
+    for (int i = 0; i < n_pools; ++i) {
+      const dsb_kv_pages& p = pools[i];
+      const dsb_status st = check_pages16(&p);
+      if (st != DSB_OK) return st;
+      if (p.dtype != pools->dtype || p.n_pages != pools->n_pages || p.n_kv_heads != pools->n_kv_heads ||
+          p.head_dim != pools->head_dim)
+        return fail(DSB_ERR_INVALID_ARG, "pool %d differs from the first in dtype, pages, heads or head_dim", i);
+      planes.push_back(p.k);
+      planes.push_back(p.v);
+    }
+    return copy_common(planes, pool16_bytes(pools), pools->n_pages, pools->n_kv_heads, pools->head_dim, false, src, dst,
+                       keys, n_copies, stream);
+  });
+}
+
+dsb_status dsb_kv_copy_pages_q4(const dsb_kv_q4_pages* pools, int n_pools, const int32_t* src, const int32_t* dst,
+                                const int32_t* keys, int n_copies, void* stream) {
+  return guarded([&]() -> dsb_status {
+    if (!pools) return fail(DSB_ERR_INVALID_ARG, "pools is NULL");
+    if (n_pools < 1 || n_pools > kMaxPools) return fail(DSB_ERR_INVALID_ARG, "n_pools=%d out of [1, %d]", n_pools, kMaxPools);
+    std::vector<void*> planes;
+    for (int i = 0; i < n_pools; ++i) {
+      const dsb_kv_q4_pages& p = pools[i];
+      const dsb_status st = check_q4_pages(&p);
+      if (st != DSB_OK) return st;
+      if (p.n_pages != pools->n_pages || p.n_kv_heads != pools->n_kv_heads || p.head_dim != pools->head_dim)
+        return fail(DSB_ERR_INVALID_ARG, "pool %d differs from the first in pages, heads or head_dim", i);
+      planes.push_back(p.blocks);
+    }
+    return copy_common(planes, pool_bytes(pools), pools->n_pages, pools->n_kv_heads, pools->head_dim, true, src, dst,
+                       keys, n_copies, stream);
+  });
+}
+
+dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                                       const dsb_paged_batch* b, float* out, dsb_workspace* ws, void* stream) {
+  return guarded([&]() -> dsb_status {
+    dsb_status st = check_pages16(kv);
+    if (st != DSB_OK) return st;
+    if ((st = check_q(q, q_stride, n_q_heads, kv)) != DSB_OK) return st;
+    int n_tok = 0;
+    if ((st = check_paged_batch(b, kv->n_pages, kMaxLen, &n_tok)) != DSB_OK) return st;
+    if (!ws) return fail(DSB_ERR_WORKSPACE, "workspace is NULL");
+    if (n_tok == 0) return DSB_OK;
+    if (!q || !out) return fail(DSB_ERR_INVALID_ARG, "q / out is NULL");
+    if (!aligned16(q) || !aligned16(out)) return fail(DSB_ERR_INVALID_ARG, "q / out not 16-byte aligned");
+    const int hkv = kv->n_kv_heads, D = kv->head_dim;
+    if ((st = check_out(q, q_stride, (int64_t)n_q_heads * D, n_tok, kv, out)) != DSB_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if ((st = check_workspace(ws)) != DSB_OK) return st;
+
+    Tree tree{b, n_q_heads / hkv, {}, {}, {}};
+    tree.build();
+    std::vector<int> tok0(b->n_seq);
+    for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
+    const auto words_of = [&](const Segment& g) {
+      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords + g.n;
+    };
+
+    // launches: what a captured call keeps has to ride in its parameters
+    size_t all = 1;
+    for (const Segment& g : tree.segs) all += words_of(g);
+    size_t room = kMetaWords;
+    if (all > (size_t)dsbk::kParamWords) {
+      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+      const cudaError_t e = cudaStreamIsCapturing(cs, &cap);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+      if (cap != cudaStreamCaptureStatusNone) room = dsbk::kParamWords;
+    }
+    std::vector<Launch> launches;
+    for (size_t i = 0; i < tree.segs.size(); ++i) {
+      const Segment& g = tree.segs[i];
+      const size_t n = words_of(g);
+      if (1 + n > room)
+        return fail(DSB_ERR_UNSUPPORTED, "a captured call holds at most %d words of metadata for pages of %d sequences", dsbk::kParamWords,
+                    g.m1 - g.m0);
+      const long long work = (long long)hkv * Tree::tiles(g.rows) * g.n;
+      if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+      if (launches.empty() || launches.back().n_words + n > room || launches.back().work + work > INT_MAX / 2)
+        launches.emplace_back();
+      launches.back().segs.push_back((int)i);
+      launches.back().n_words += n;
+      launches.back().work += work;
+    }
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != DSB_OK) return st;
+    const int resident = dsbk::page_attn_resident(dev.sms);
+    int slots = 0;
+    for (Launch& l : launches) {
+      l.ctas = (int)std::min<long long>(resident, l.work);
+      for (int i : l.segs) {
+        Segment& g = tree.segs[i];
+        g.cap = most_parts(g.n, l.work / l.ctas);
+        if (g.parent >= 0) g.slot0 = tree.segs[g.parent].slot0 + tree.segs[g.parent].cap;
+        slots = std::max(slots, g.slot0 + g.cap);
+      }
+    }
+    const auto slots_of = [&](int s) { return tree.segs[tree.end[s]].slot0 + tree.segs[tree.end[s]].cap; };
+    const size_t rows = (size_t)n_tok * n_q_heads;
+    if (slots > 1 && rows * slots * (D + 2) * sizeof(float) > partial_capacity(ws))
+      return fail(DSB_ERR_WORKSPACE, "attention needs %zu workspace bytes for partials, have %zu",
+                  rows * slots * (D + 2) * sizeof(float), partial_capacity(ws));
+
+    dsbk::PageAttnArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.hq = n_q_heads;
+    a.hkv = hkv;
+    a.k = kv->k;
+    a.v = kv->v;
+    a.n_tok = n_tok;
+    a.acc = reinterpret_cast<float*>(partial_base(ws));
+    a.stat = a.acc + rows * slots * D;
+    a.out = out;
+    a.slots = slots;
+    std::vector<int32_t> words;
+    for (const Launch& l : launches) {
+      words.assign(l.segs.size() * dsbk::kSharedSegWords + 1, 0);
+      words.reserve(l.n_words);
+      long long work = 0;
+      for (size_t i = 0; i < l.segs.size(); ++i) {
+        const Segment& g = tree.segs[l.segs[i]];
+        int first = INT_MAX, last = 0, most = 0;
+        const int mem_at = (int)words.size();
+        for (int m = g.m0, row = 0; m < g.m1; ++m) {
+          const int s = tree.order[m], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
+          words.insert(words.end(), {row, tok0[s], n, len, w});
+          row += tree.G * n;
+          first = std::min(first, w > 0 ? std::max(0, len - n + 1 - w) : 0);
+          last = std::max(last, len - 1);
+          most = std::max(most, slots_of(s));
+        }
+        const int pg_at = (int)words.size();
+        for (int p = 0; p < g.n; ++p) words.push_back(page_of(b, tree.order[g.m0], g.b0 + p));
+        const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.m1 - g.m0, g.b0, g.n, pg_at,
+                                                    g.slot0,       g.cap,  first,  last,        most};
+        std::copy(rec, rec + dsbk::kSharedSegWords, words.begin() + i * dsbk::kSharedSegWords);
+        work += (long long)hkv * Tree::tiles(g.rows) * g.n;
+      }
+      words[l.segs.size() * dsbk::kSharedSegWords] = (int32_t)work;
+      dsbk::MetaArg meta;
+      if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
+      a.n_seg = (int)l.segs.size();
+      a.ctas = l.ctas;
+      const cudaError_t e = dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
+      if (e != cudaSuccess) return cuda_fail(e, "attention_decode_shared launch");
+    }
+    // the join, where a row's sums lie in parts
+    words.clear();
+    bool join = false;
+    for (int s = 0; s < b->n_seq; ++s) {
+      if (b->new_tokens[s] == 0) continue;
+      const Segment& g = tree.segs[tree.end[s]];
+      int alone = g.parent < 0 && g.cap == 1;  // written by its one part ..
+      for (int m = g.m0; m < g.m1 && alone; ++m) alone = slots_of(tree.order[m]) == 1;  // .. which serves no longer one
+      words.insert(words.end(), {tok0[s], alone ? 0 : slots_of(s)});
+      join = join || !alone;
+    }
+    if (!join) return DSB_OK;
+    static_assert(2 * DSB_MAX_SEQS <= dsbk::kParamWords, "join metadata");
+    dsbk::MetaArg meta;
+    meta.host = words.data();
+    meta.n_words = (int)words.size();
+    const cudaError_t e = dsbk::launch_attention_join(a, (int)words.size() / 2, D, meta, cs);
+    return e == cudaSuccess ? DSB_OK : cuda_fail(e, "attention_decode_shared join");
+  });
+}
+
+dsb_status dsb_kv_page_bounds(const dsb_kv_pages* kv, const dsb_paged_batch* b, void* bounds, void* stream) {
+  return guarded([&]() -> dsb_status {
+    dsb_status st = check_pages16(kv);
+    if (st != DSB_OK) return st;
+    int n_tok = 0;
+    if ((st = check_paged_batch(b, kv->n_pages, kMaxLen, &n_tok)) != DSB_OK) return st;
+    if ((st = check_linear(b)) != DSB_OK) return st;
+    if (!bounds || !aligned16(bounds)) return fail(DSB_ERR_INVALID_ARG, "bounds is NULL or not 16-byte aligned");
+    const size_t bytes = (size_t)kv->n_pages * kv->n_kv_heads * 2 * kv->head_dim * 2;
+    for (const void* pool : {kv->k, kv->v})
+      if (overlap(pool, pool16_bytes(kv), bounds, bytes)) return fail(DSB_ERR_INVALID_ARG, "bounds overlaps the page pools");
+    std::vector<int32_t> words;
+    std::vector<int> touched;
+    for (int s = 0; s < b->n_seq; ++s) {
+      const int len = b->seq_lens[s], n = b->new_tokens[s];
+      for (int i = (len - n) / DSB_KV_PAGE; n > 0 && i * DSB_KV_PAGE < len; ++i) {
+        words.insert(words.end(), {page_of(b, s, i), std::min(DSB_KV_PAGE, len - i * DSB_KV_PAGE)});
+        touched.push_back(words[words.size() - 2]);
+      }
+    }
+    std::sort(touched.begin(), touched.end());
+    const auto twice = std::adjacent_find(touched.begin(), touched.end());
+    if (twice != touched.end()) return fail(DSB_ERR_INVALID_ARG, "new tokens of the call lie twice on page %d", *twice);
+    for (size_t at = 0; at < words.size(); at += dsbk::kParamWords) {
+      static_assert(dsbk::kParamWords % 2 == 0, "pairs of words");
+      dsbk::MetaArg meta;
+      meta.host = words.data() + at;
+      meta.n_words = (int)std::min<size_t>(dsbk::kParamWords, words.size() - at);
+      const cudaError_t e = dsbk::launch_page_bounds(kv->k, kv->dtype == DSB_F16 ? 0 : 1, kv->n_kv_heads, kv->head_dim,
+                                                     meta.n_words / 2, bounds, meta, static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e, "kv_page_bounds launch");
+    }
+    return DSB_OK;
+  });
+}
+
+dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                               const void* bounds, const dsb_paged_batch* b, int n_select, int keep_first, int keep_last,
+                               int32_t* selected, dsb_workspace* ws, void* stream) {
+  return guarded([&]() -> dsb_status {
+    dsb_status st = check_pages16(kv);
+    if (st != DSB_OK) return st;
+    if ((st = check_q(q, q_stride, n_q_heads, kv)) != DSB_OK) return st;
+    int n_tok = 0;
+    if ((st = check_paged_batch(b, kv->n_pages, kMaxLen, &n_tok)) != DSB_OK) return st;
+    if ((st = check_linear(b)) != DSB_OK) return st;
+    if (keep_first < 0 || keep_last < 1 || keep_first > n_select || keep_last > n_select - keep_first)
+      return fail(DSB_ERR_INVALID_ARG, "keep_first=%d >= 0 and keep_last=%d >= 1 must fit n_select=%d", keep_first, keep_last,
+                  n_select);
+    if (n_select > kMaxLen / DSB_KV_PAGE) return fail(DSB_ERR_INVALID_ARG, "n_select=%d", n_select);
+    if (!ws) return fail(DSB_ERR_WORKSPACE, "workspace is NULL");
+    if (n_tok == 0) return DSB_OK;
+    if (!q || !bounds || !selected) return fail(DSB_ERR_INVALID_ARG, "q / bounds / selected is NULL");
+    if (!aligned16(q) || !aligned16(bounds) || !aligned16(selected))
+      return fail(DSB_ERR_INVALID_ARG, "q / bounds / selected not 16-byte aligned");
+    const int hkv = kv->n_kv_heads, D = kv->head_dim;
+    const size_t out_bytes = (size_t)n_tok * hkv * n_select * sizeof(int32_t);
+    if (overlap(q, ((n_tok - 1) * q_stride + (int64_t)n_q_heads * D) * sizeof(float), selected, out_bytes) ||
+        overlap(bounds, (size_t)kv->n_pages * hkv * 2 * D * 2, selected, out_bytes))
+      return fail(DSB_ERR_INVALID_ARG, "selected overlaps q or bounds");
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if ((st = check_workspace(ws)) != DSB_OK) return st;
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != DSB_OK) return st;
+    std::vector<SelLaunch> launches;
+    if ((st = selection_launches(b, cs, &launches)) != DSB_OK) return st;
+    for (const SelLaunch& l : launches) {
+      dsbk::MetaArg meta;
+      if ((st = meta_arg(ws, l.words, cs, &meta)) != DSB_OK) return st;
+      // CTAs of a cluster: while they find SMs and each has a round of pages of its own
+      int ranks = 1;
+      while (ranks < 8 && (long long)l.n_tok * hkv * ranks * 2 <= 2 * dev.sms && ranks * 128 < l.most) ranks *= 2;
+      const dsbk::SelectArgs a{q + (size_t)l.tok0 * q_stride,
+                               q_stride,
+                               n_q_heads,
+                               hkv,
+                               bounds,
+                               l.n_seq,
+                               l.n_tok,
+                               n_select,
+                               keep_first,
+                               keep_last,
+                               selected + (size_t)l.tok0 * hkv * n_select,
+                               ranks,
+                               l.most};
+      const cudaError_t e = dsbk::launch_select_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
+      if (e != cudaSuccess) return cuda_fail(e, "kv_select_pages launch");
+    }
+    return DSB_OK;
+  });
+}
+
+dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
+                                         const dsb_paged_batch* b, const int32_t* selected, int n_select, float* out,
+                                         dsb_workspace* ws, void* stream) {
+  return guarded([&]() -> dsb_status {
+    dsb_status st = check_pages16(kv);
+    if (st != DSB_OK) return st;
+    if ((st = check_q(q, q_stride, n_q_heads, kv)) != DSB_OK) return st;
+    int n_tok = 0;
+    if ((st = check_paged_batch(b, kv->n_pages, kMaxLen, &n_tok)) != DSB_OK) return st;
+    if ((st = check_linear(b)) != DSB_OK) return st;
+    if (n_select < 1 || n_select > kMaxLen / DSB_KV_PAGE) return fail(DSB_ERR_INVALID_ARG, "n_select=%d", n_select);
+    if (!ws) return fail(DSB_ERR_WORKSPACE, "workspace is NULL");
+    if (n_tok == 0) return DSB_OK;
+    if (!q || !selected || !out) return fail(DSB_ERR_INVALID_ARG, "q / selected / out is NULL");
+    if (!aligned16(q) || !aligned16(selected) || !aligned16(out))
+      return fail(DSB_ERR_INVALID_ARG, "q / selected / out not 16-byte aligned");
+    const int hkv = kv->n_kv_heads, D = kv->head_dim;
+    const int64_t width = (int64_t)n_q_heads * D;
+    if ((st = check_out(q, q_stride, width, n_tok, kv, out)) != DSB_OK) return st;
+    if (overlap(selected, (size_t)n_tok * hkv * n_select * sizeof(int32_t), out, n_tok * width * sizeof(float)))
+      return fail(DSB_ERR_INVALID_ARG, "out overlaps selected");
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if ((st = check_workspace(ws)) != DSB_OK) return st;
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != DSB_OK) return st;
+    std::vector<SelLaunch> launches;
+    if ((st = selection_launches(b, cs, &launches)) != DSB_OK) return st;
+    const int tiles = Tree::tiles(n_q_heads / hkv), resident = dsbk::page_attn_resident(dev.sms);
+    std::vector<dsbk::PageAttnArgs> args;
+    for (const SelLaunch& l : launches) {
+      dsbk::PageAttnArgs a = {};
+      a.n_select = std::min(n_select, l.most);  // a list's pages come first
+      const long long work = (long long)l.n_tok * hkv * tiles * a.n_select;
+      if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+      a.ctas = (int)std::min<long long>(resident, work);
+      a.sel_cap = a.slots = most_parts(a.n_select, work / a.ctas);
+      const size_t need = (size_t)l.n_tok * n_q_heads * a.slots * (D + 2) * sizeof(float);
+      if (a.slots > 1 && need > partial_capacity(ws))
+        return fail(DSB_ERR_WORKSPACE, "attention needs %zu workspace bytes for partials, have %zu", need, partial_capacity(ws));
+      a.q = q + (size_t)l.tok0 * q_stride;
+      a.q_stride = q_stride;
+      a.hq = n_q_heads;
+      a.hkv = hkv;
+      a.k = kv->k;
+      a.v = kv->v;
+      a.n_seg = l.n_seq;
+      a.n_tok = l.n_tok;
+      a.selected = selected + (size_t)l.tok0 * hkv * n_select;
+      a.sel_stride = n_select;
+      a.acc = reinterpret_cast<float*>(partial_base(ws));
+      a.stat = a.acc + (size_t)l.n_tok * n_q_heads * a.slots * D;
+      a.out = out + (size_t)l.tok0 * width;
+      args.push_back(a);
+    }
+    for (size_t i = 0; i < launches.size(); ++i) {
+      const dsbk::PageAttnArgs& a = args[i];
+      dsbk::MetaArg meta;
+      if ((st = meta_arg(ws, launches[i].words, cs, &meta)) != DSB_OK) return st;
+      cudaError_t e = dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
+      if (e != cudaSuccess) return cuda_fail(e, "attention_decode_selected launch");
+      if (a.slots == 1) continue;
+      const int32_t words[2] = {0, a.slots};
+      dsbk::MetaArg one;
+      one.host = words;
+      one.n_words = 2;
+      e = dsbk::launch_attention_join(a, 1, D, one, cs);
+      if (e != cudaSuccess) return cuda_fail(e, "attention_decode_selected join");
+    }
+    return DSB_OK;
+  });
+}
+
+}  // extern "C"

@@ -840,6 +840,126 @@ def kv_gather_q4(kv: KVQ4Pages, batch: PagedBatch, first, count, dtype: int, ws:
     return k, v
 
 
+# ------------------------------------------------------- whole pages
+SIGNATURES.update({
+    "dsb_kv_copy_pages": (_I, [ctypes.POINTER(KVPages), _I, _P, _P, _P, _I, _P]),
+    "dsb_kv_copy_pages_q4": (_I, [ctypes.POINTER(KVQ4Pages), _I, _P, _P, _P, _I, _P]),
+    "dsb_attention_decode_shared": (_I, [_P, _I64, _I, ctypes.POINTER(KVPages), ctypes.POINTER(PagedBatchC), _P, _P,
+                                         _P]),
+    "dsb_kv_page_bounds": (_I, [ctypes.POINTER(KVPages), ctypes.POINTER(PagedBatchC), _P, _P]),
+    "dsb_kv_select_pages": (_I, [_P, _I64, _I, ctypes.POINTER(KVPages), _P, ctypes.POINTER(PagedBatchC), _I, _I, _I,
+                                 _P, _P, _P]),
+    "dsb_attention_decode_selected": (_I, [_P, _I64, _I, ctypes.POINTER(KVPages), ctypes.POINTER(PagedBatchC), _P, _I,
+                                           _P, _P, _P]),
+})
+
+
+def _copy_pages(fn, kind, pools, src, dst, keys, stream):
+    pools = list(pools)
+    if not pools or not all(isinstance(p, kind) for p in pools):
+        raise ValueError(f"pools must be a sequence of {kind.__name__}, one for each layer")
+    sa, ps = _host_i32(src, np.size(src), "src")
+    da, pd = _host_i32(dst, sa.size, "dst")
+    ka, pk = _host_i32(keys, sa.size, "keys")
+    dev = _current_device(pools[0]._tensors[0], "the page pool")
+    for p in pools:
+        for t in p._tensors:
+            _dev_ptr(t, dev, "the page pool")
+    _check(fn((kind * len(pools))(*pools), len(pools), ps, pd, pk, sa.size, _raw_stream(stream, dev)))
+
+
+def kv_copy_pages(pools, src, dst, keys, stream=None):
+    """Copies rows ``0 .. keys[i] - 1`` of page ``src[i]`` to page ``dst[i]``, all
+    heads, K and V, in every pool of ``pools`` (one :class:`KVPages` a layer): a
+    fork's last page, a compaction's moves."""
+    _copy_pages(lib().dsb_kv_copy_pages, KVPages, pools, src, dst, keys, stream)
+
+
+def kv_copy_pages_q4(pools, src, dst, keys, stream=None):
+    """:func:`kv_copy_pages` in 4-bit pools (one :class:`KVQ4Pages` a layer)."""
+    _copy_pages(lib().dsb_kv_copy_pages_q4, KVQ4Pages, pools, src, dst, keys, stream)
+
+
+def _paged_q(q, kv: KVPages, batch: PagedBatch, out, stream):
+    """Stride and device of ``q[n_tok, Hq, D]`` and the output of its shape."""
+    import torch
+    if q.dim() != 3 or q.shape[2] != kv.head_dim:
+        raise ValueError(f"q must be [n_tok, Hq, head_dim={kv.head_dim}], got {tuple(q.shape)}")
+    n_tok, hq, d = q.shape
+    stride = _row_stride(q, batch.n_tok, (hq, d), "q")
+    dev = _current_device(q, "q")
+    for t in kv._tensors:
+        _dev_ptr(t, dev, "the page pool")
+    if out is None:
+        out = _empty_on(stream, (n_tok, hq, d), torch.float32, q.device)
+    elif out is not False:
+        _need(out, 4 * n_tok * hq * d, "out", "f32")
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    return stride, dev, out
+
+
+def attention_decode_shared(q, kv: KVPages, batch: PagedBatch, ws: Workspace, out=None, stream=None):
+    """Decode attention over 16-bit pages for a ragged batch: float32 ``out[n_tok,
+    Hq, D]`` of ``q[n_tok, Hq, D]`` (rows may lie apart).  Leading pages that
+    block tables have in common are read once for all their sequences."""
+    stride, dev, out = _paged_q(q, kv, batch, out, stream)
+    _check(lib().dsb_attention_decode_shared(q.data_ptr(), stride, q.shape[1], ctypes.byref(kv), batch.ref,
+                                             _dev_ptr(out, dev, "out"), ws.handle, _raw_stream(stream, dev)))
+    return out
+
+
+def _bounds(kv: KVPages, bounds, dev: int):
+    k = kv._tensors[0]
+    shape = (kv.n_pages, kv.n_kv_heads, 2, kv.head_dim)
+    if tuple(bounds.shape) != shape or bounds.dtype != k.dtype or not bounds.is_contiguous():
+        raise ValueError(f"bounds must be contiguous {k.dtype} {shape}, got {bounds.dtype} {tuple(bounds.shape)}")
+    return _dev_ptr(bounds, dev, "bounds")
+
+
+def kv_page_bounds(kv: KVPages, batch: PagedBatch, bounds, stream=None):
+    """Least and largest key values, into ``bounds[n_pages, Hkv, 2, D]`` (the pool's
+    type), of the pages that the batch's new tokens lie on."""
+    dev = _current_device(kv._tensors[0], "the page pool")
+    _check(lib().dsb_kv_page_bounds(ctypes.byref(kv), batch.ref, _bounds(kv, bounds, dev), _raw_stream(stream, dev)))
+    return bounds
+
+
+def kv_select_pages(q, kv: KVPages, bounds, batch: PagedBatch, n_select: int, ws: Workspace, keep_first: int = 1,
+                    keep_last: int = 1, selected=None, stream=None):
+    """The pages that each new token and kv head is to read: int32 ``selected[n_tok,
+    Hkv, n_select]``, block indices in rising order, -1 behind the last; the first
+    ``keep_first``, the newest ``keep_last``, then the largest scores."""
+    import torch
+    stride, dev, _ = _paged_q(q, kv, batch, False, stream)
+    shape = (q.shape[0], kv.n_kv_heads, int(n_select))
+    if selected is None:
+        if n_select < 1:
+            raise ValueError(f"n_select must be positive, got {n_select}")
+        selected = _empty_on(stream, shape, torch.int32, q.device)
+    elif tuple(selected.shape) != shape or selected.dtype != torch.int32 or not selected.is_contiguous():
+        raise ValueError(f"selected must be contiguous int32 {shape}")
+    _check(lib().dsb_kv_select_pages(q.data_ptr(), stride, q.shape[1], ctypes.byref(kv), _bounds(kv, bounds, dev),
+                                     batch.ref, n_select, keep_first, keep_last, _dev_ptr(selected, dev, "selected"),
+                                     ws.handle, _raw_stream(stream, dev)))
+    return selected
+
+
+def attention_decode_selected(q, kv: KVPages, batch: PagedBatch, selected, ws: Workspace, out=None, stream=None):
+    """Decode attention over the pages ``selected[n_tok, Hkv, n_select]`` (as
+    :func:`kv_select_pages` gives them) alone."""
+    import torch
+    stride, dev, out = _paged_q(q, kv, batch, out, stream)
+    if selected.dim() != 3 or selected.dtype != torch.int32 or not selected.is_contiguous() or \
+            tuple(selected.shape[:2]) != (q.shape[0], kv.n_kv_heads):
+        raise ValueError(f"selected must be contiguous int32 [{q.shape[0]}, {kv.n_kv_heads}, n_select], got "
+                         f"{selected.dtype} {tuple(selected.shape)}")
+    _check(lib().dsb_attention_decode_selected(q.data_ptr(), stride, q.shape[1], ctypes.byref(kv), batch.ref,
+                                               _dev_ptr(selected, dev, "selected"), selected.shape[2],
+                                               _dev_ptr(out, dev, "out"), ws.handle, _raw_stream(stream, dev)))
+    return out
+
+
 # ---------------------------------------------------------------- decode step
 class ModelShapeC(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),

@@ -1,0 +1,379 @@
+"""GPU parity of the calls on whole pages -- copies, bounds, selection, attention over
+shared and over selected pages -- against the float64 oracle, through the C ABI.
+
+Copies, bounds and selections are exact.  The attention's bound is the oracle's: every
+rounding of a float32 evaluation, and for bf16 caches 2^-18 more of the weighted
+values' magnitudes, the weights being two bf16 (each rounding 2^-9 of what is left)."""
+import numpy as np
+import pytest
+
+from oracle import pages as op
+from tests.gpu_util import to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+P = 128
+
+
+def _dsb():
+    from session_decode_step_dsb_gb300 import dsb
+    return dsb
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _type(kind):
+    d, t = _dsb(), _torch()
+    return (d.DSB_F16, t.float16) if kind == "f16" else (d.DSB_BF16, t.bfloat16)
+
+
+def _pools(rng, n_pages, hkv, D, kind, scale=1.0):
+    """Device K and V pools and their float64 values."""
+    t = _torch()
+    dev = [t.from_numpy(rng.standard_normal((n_pages, hkv, P, D)) * scale).to(_type(kind)[1]).cuda() for _ in "kv"]
+    return dev, [x.double().cpu().numpy() for x in dev]
+
+
+def _tree(rng, groups, per, common, branch, tails, spare=2):
+    """Block table of groups * per sequences over a shuffled pool, its block counts, lengths, page count."""
+    lens = [(common + branch) * P + int(n) for n in tails]
+    blocks = [max(1, -(-n // P)) for n in lens]
+    own = [b - common - branch for b in blocks]
+    total = common + groups * branch + sum(own) + spare
+    order = rng.permutation(total)
+    table, at = np.zeros((len(lens), max(blocks)), np.int32), common + groups * branch
+    for s, b in enumerate(blocks):
+        g = s // per
+        table[s, :b] = np.concatenate([order[:common], order[common + g * branch:common + (g + 1) * branch],
+                                       order[at:at + own[s]]])
+        at += own[s]
+    return table, blocks, lens, total
+
+
+def _attend(q, dev, kind, table, blocks, window, new, lens, **kw):
+    d = _dsb()
+    kv = d.kv_pages(dev[0], dev[1], _type(kind)[0])
+    batch = d.PagedBatch(table, blocks, window, new, lens)
+    ws = d.Workspace(max(batch.n_tok, 1), q.shape[1], q.shape[2], max(lens))
+    if "selected" in kw:
+        return d.attention_decode_selected(q, kv, batch, kw["selected"], ws)
+    return d.attention_decode_shared(q, kv, batch, ws)
+
+
+def _check(got, want, bound, what=""):
+    got = to_host(got).astype(np.float64)
+    assert np.isfinite(got).all(), f"{what}: not finite"
+    bad = np.abs(got - want) > bound
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} outside the bound, worst "
+                           f"{(np.abs(got - want) / np.maximum(bound, 1e-300)).max():.2f} times it at "
+                           f"{np.unravel_index((np.abs(got - want) / np.maximum(bound, 1e-300)).argmax(), bad.shape)}")
+
+
+def _step(kind):
+    return 2.0 ** -20 + (2.0 ** -18 if kind == "bf16" else 0)
+
+
+# --------------------------------------------------------------------- copies
+@pytest.mark.parametrize("kind,D,hkv,layers,keys", [
+    ("f16", 64, 1, 1, [1]), ("bf16", 128, 3, 3, [128, 77, 0, 1]), ("f16", 128, 8, 2, [128] * 5),
+    ("q4", 64, 1, 1, [1]), ("q4", 64, 3, 2, [128, 127, 2, 3, 0]), ("q4", 128, 2, 3, [1, 5, 64, 126, 128, 33]),
+    ("q4", 128, 8, 40, [4, 7]), ("bf16", 64, 2, 512, [9])])
+def test_copies_move_the_keys_and_nothing_else(kind, D, hkv, layers, keys):
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(len(keys) * D + layers)
+    n = 2 * len(keys) + 1
+    order = rng.permutation(n)
+    src, dst = order[:len(keys)].copy(), order[len(keys):2 * len(keys)]
+    if len(keys) > 1:
+        src[1] = src[0]
+    if kind == "q4":
+        host = rng.integers(0, 256, (layers, n, hkv, P * (D + 8)), dtype=np.uint8)
+        dev = to_dev(host)
+        d.kv_copy_pages_q4([d.kv_q4_pages(p, D) for p in dev], src, dst, keys)
+        want = np.stack([op.copy_q4(p, D, src, dst, keys) for p in host]) if layers < 9 else None
+        if want is None:                                     # the first and the last layer
+            want = host.copy()
+            for i in (0, layers - 1):
+                want[i] = op.copy_q4(host[i], D, src, dst, keys)
+                assert np.array_equal(to_host(dev[i]), want[i])
+            return
+    else:
+        host = rng.integers(0, 1 << 16, (layers, 2, n, hkv, P, D), dtype=np.uint16)
+        dev = to_dev(host.view(np.int16))
+        d.kv_copy_pages([d.kv_pages(p[0], p[1], _type(kind)[0]) for p in dev], src, dst, keys)
+        want = np.stack([[op.copy(x, src, dst, keys) for x in p] for p in host]).view(np.int16)
+    assert np.array_equal(to_host(dev), want)
+
+
+def test_more_copies_than_a_launch_holds():
+    d, rng = _dsb(), np.random.default_rng(3)
+    n = 1500
+    host = rng.integers(0, 1 << 16, (2, 2 * n, 1, P, 64), dtype=np.uint16)
+    dev = to_dev(host.view(np.int16))
+    order, keys = rng.permutation(2 * n), rng.integers(0, 4, n)
+    d.kv_copy_pages([d.kv_pages(dev[0], dev[1], d.DSB_F16)], order[:n], order[n:], keys)
+    want = np.stack([op.copy(x, order[:n], order[n:], keys) for x in host]).view(np.int16)
+    assert np.array_equal(to_host(dev), want)
+
+
+# ------------------------------------------------------ attention, shared pages
+SHARED = [
+    # kind, hq, hkv, D, groups, per, common, branch, tails, new
+    ("f16", 1, 1, 64, 1, 1, 0, 0, [1], [1]),
+    ("bf16", 2, 1, 128, 1, 1, 0, 0, [128], [1]),
+    ("f16", 12, 12, 64, 1, 4, 2, 0, [20, 200, 1, 129], [1, 1, 1, 1]),
+    ("bf16", 10, 2, 128, 1, 5, 3, 0, [1, 130, 300, 7, 128], [1, 1, 1, 1, 1]),
+    ("f16", 10, 2, 128, 2, 3, 1, 2, [50, 3, 140, 1, 1, 260], [3, 0, 2, 1, 1, 4]),
+    ("bf16", 8, 1, 64, 3, 2, 0, 2, [5, 6, 7, 8, 9, 300], [5, 6, 1, 2, 0, 40]),
+    ("f16", 3, 3, 128, 1, 9, 5, 0, [11] * 9, [1] * 9),
+    ("bf16", 16, 2, 128, 1, 2, 0, 0, [700, 650], [1, 2]),
+    ("f16", 40, 8, 128, 1, 3, 2, 0, [100, 90, 80], [1, 1, 1]),
+    ("f16", 5, 1, 64, 1, 1, 9, 0, [77], [77]),
+    ("bf16", 5, 1, 128, 1, 1, 0, 0, [300], [300]),
+    ("f16", 64, 1, 128, 1, 2, 3, 0, [3, 2], [1, 1]),
+    ("bf16", 4, 2, 64, 1, 40, 2, 0, list(range(1, 41)), [1] * 40),
+    ("f16", 2, 2, 128, 1, 3, 30, 0, [64, 1, 2], [1, 1, 1]),
+]
+
+
+@pytest.mark.parametrize("kind,hq,hkv,D,groups,per,common,branch,tails,new", SHARED)
+def test_shared_attention_matches_the_oracle(kind, hq, hkv, D, groups, per, common, branch, tails, new):
+    rng = np.random.default_rng(sum(tails) + hq + D)
+    table, blocks, lens, total = _tree(rng, groups, per, common, branch, tails)
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32) * 2
+    window = [0] * len(lens)
+    got = _attend(to_dev(q), dev, kind, table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step(kind))
+    _check(got, want, bound)
+
+
+def test_windows_beside_shared_pages():
+    rng = np.random.default_rng(11)
+    table, blocks, lens, total = _tree(rng, 1, 5, 3, 0, [40, 300, 90, 200, 10])
+    window, new = [0, 130, 0, 1, 500], [2, 3, 1, 2, 1]
+    # rings: as many pages as the window needs
+    for s in (1, 3, 4):
+        blocks[s] = (window[s] + new[s] - 2) // P + 2
+    table = np.pad(table, ((0, 0), (0, 3)))
+    extra = total + 30
+    for s in (1, 3, 4):
+        table[s, :blocks[s]] = np.arange(total + 6 * (s - 1), total + 6 * (s - 1) + blocks[s])
+    dev, (k, v) = _pools(rng, extra, 2, 64, "f16")
+    q = rng.standard_normal((sum(new), 6, 64)).astype(np.float32)
+    got = _attend(to_dev(q), dev, "f16", table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens)
+    _check(got, want, bound)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [[1, 1, 1], [4, 3, 5], [70, 2, 30]])
+def test_what_is_hidden_reaches_no_row(kind, new):
+    t, rng = _torch(), np.random.default_rng(5)
+    table, blocks, lens, total = _tree(rng, 1, 3, 2, 0, [100, 200, 33])
+    dev, (k, v) = _pools(rng, total, 2, 64, kind)
+    q = rng.standard_normal((sum(new), 4, 64)).astype(np.float32)
+    window = [0, 0, 0]
+    clean = to_host(_attend(to_dev(q), dev, kind, table, blocks, window, new, lens))
+    # rows behind the last keys and pages of nobody hold anything
+    used = set()
+    for s, n in enumerate(lens):
+        for p in range(n):
+            used.add((int(table[s, p // P]), p % P))
+    mask = np.array([[(p, r) not in used for r in range(P)] for p in range(total)])
+    for x in dev:
+        x[t.from_numpy(mask).cuda()[:, None].expand(-1, 2, -1)] = float("nan")
+    got = to_host(_attend(to_dev(q), dev, kind, table, blocks, window, new, lens))
+    assert np.array_equal(got, clean)
+    # a draft's key and value seen by the later drafts only
+    last, page, row = lens[0] - 1, int(table[0, (lens[0] - 1) // P]), (lens[0] - 1) % P
+    dev[0][page, :, row] = float("nan")
+    dev[1][page, :, row] = float("inf")
+    got = to_host(_attend(to_dev(q), dev, kind, table, blocks, window, new, lens))
+    row0 = new[0] - 1
+    keep = np.arange(sum(new)) != row0
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step(kind))
+    assert (np.abs(got - want)[keep] <= bound[keep]).all()
+    assert not np.isfinite(got[row0]).any()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e30, 3e38])
+def test_queries_of_any_size(size):
+    rng = np.random.default_rng(8)
+    table, blocks, lens, total = _tree(rng, 1, 2, 1, 0, [30, 90])
+    dev, (k, v) = _pools(rng, total, 1, 64, "bf16", 1.0 / size if size > 1 else 1.0)
+    q = rng.uniform(-1, 1, (2, 2, 64)).astype(np.float32) * np.float32(size)
+    got = _attend(to_dev(q), dev, "bf16", table, blocks, [0, 0], [1, 1], lens)
+    want, bound = op.attention(q, k, v, table, blocks, [0, 0], [1, 1], lens, weight_step=_step("bf16"))
+    _check(got, want, bound + 2e-40)
+
+
+def test_strided_rows_other_streams_and_replays():
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(9)
+    table, blocks, lens, total = _tree(rng, 2, 3, 2, 1, [5, 100, 200, 1, 64, 31])
+    new = [1, 2, 1, 1, 3, 1]
+    dev, _ = _pools(rng, total, 2, 128, "f16")
+    rows = to_dev(rng.standard_normal((sum(new), 10 + 4, 128)).astype(np.float32))
+    q = rows[:, :10]
+    want = _attend(q.contiguous(), dev, "f16", table, blocks, [0] * 6, new, lens)
+    assert t.equal(_attend(q, dev, "f16", table, blocks, [0] * 6, new, lens), want)
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, blocks, [0] * 6, new, lens)
+    ws = d.Workspace(sum(new), 10, 128, max(lens))
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    got = d.attention_decode_shared(q, kv, batch, ws, stream=side)
+    side.synchronize()
+    assert t.equal(got, want)
+    out, graph = t.zeros_like(want), t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        d.attention_decode_shared(q, kv, batch, ws, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        t.cuda.synchronize()
+        assert t.equal(out, want)
+
+
+# ------------------------------------------------------------ bounds, selection
+@pytest.mark.parametrize("kind,D,hkv,new,lens", [
+    ("f16", 64, 1, [1], [1]), ("bf16", 128, 3, [1, 0, 200], [700, 30, 200]), ("f16", 128, 8, [5, 128, 1], [130, 128, 257]),
+    ("bf16", 64, 2, [1000], [5000])])
+def test_bounds_are_the_least_and_largest_keys(kind, D, hkv, new, lens):
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(D + len(new))
+    table, blocks, lens, total = _tree(rng, 1, len(lens), 0, 0, lens)
+    dev, (k, _) = _pools(rng, total, hkv, D, kind)
+    dev[0][table[0, 0], 0, 0, 3] = float("nan")
+    k = dev[0].double().cpu().numpy()
+    before = t.full((total, hkv, 2, D), 7.0, dtype=_type(kind)[1], device="cuda")
+    kv, batch = d.kv_pages(dev[0], dev[1], _type(kind)[0]), d.PagedBatch(table, blocks, [0] * len(lens), new, lens)
+    got = d.kv_page_bounds(kv, batch, before)
+    want = op.bounds(k, table, new, lens, np.full((total, hkv, 2, D), 7.0))
+    assert np.array_equal(to_host(got.double()), want, equal_nan=True)
+
+
+SELECT = [
+    # kind, hq, hkv, D, new, lens, n_select, first, last
+    ("f16", 1, 1, 64, [1], [1], 1, 0, 1),
+    ("bf16", 12, 12, 64, [1], [5000], 8, 1, 1),
+    ("f16", 10, 2, 128, [3, 0, 1], [4000, 300, 129], 5, 1, 2),
+    ("bf16", 8, 1, 128, [1, 200], [20000, 900], 3, 0, 1),
+    ("f16", 7, 1, 64, [2], [2000], 15, 1, 2),
+    ("bf16", 40, 8, 128, [1] * 16, [700 + 100 * i for i in range(16)], 6, 1, 1),
+    ("f16", 24, 1, 64, [1], [70000], 500, 1, 2),
+    ("f16", 17, 1, 128, [1], [3000], 20, 10, 10),
+]
+
+
+@pytest.mark.parametrize("kind,hq,hkv,D,new,lens,n_select,first,last", SELECT)
+@pytest.mark.parametrize("ties", [False, True])
+def test_selection_matches_the_oracle(kind, hq, hkv, D, new, lens, n_select, first, last, ties):
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(n_select + hq + D)
+    table, blocks, lens, total = _tree(rng, 1, len(lens), 0, 0, lens)
+    bnd = rng.standard_normal((total, hkv, 2, D))
+    if ties:
+        bnd = np.round(bnd * 0.7) * (rng.random((total, hkv, 1, 1)) < 0.3)
+    bnd.sort(axis=2)
+    bnd = t.from_numpy(bnd).to(_type(kind)[1])
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32)
+    if ties:
+        q = np.round(q)
+    pool = t.zeros((total, hkv, P, D), dtype=_type(kind)[1], device="cuda")
+    kv, batch = d.kv_pages(pool, t.zeros_like(pool), _type(kind)[0]), d.PagedBatch(table, blocks, [0] * len(lens), new, lens)
+    ws = d.Workspace(sum(new), hq, D, max(lens))
+    got = d.kv_select_pages(to_dev(q), kv, bnd.cuda(), batch, n_select, ws, keep_first=first, keep_last=last)
+    want = op.select(q, bnd.double().numpy(), table, new, lens, n_select, first, last)
+    assert np.array_equal(to_host(got), want)
+
+
+def test_a_page_with_a_nan_is_selected():
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(2)
+    bnd = t.from_numpy(np.sort(rng.standard_normal((40, 1, 2, 64)), 2)).half().cuda()
+    bnd[17] = float("nan")
+    pool = t.zeros((40, 1, P, 64), dtype=t.float16, device="cuda")
+    batch = d.PagedBatch(np.arange(40)[None], [40], [0], [1], [40 * P])
+    got = d.kv_select_pages(t.randn((1, 1, 64), device="cuda"), d.kv_pages(pool, t.zeros_like(pool), d.DSB_F16), bnd,
+                            batch, 2, d.Workspace(1, 1, 64, 40 * P), keep_first=0)
+    assert to_host(got).tolist() == [[[17, 39]]]
+
+
+# ------------------------------------------------------ attention, selected pages
+@pytest.mark.parametrize("kind,hq,hkv,D,new,lens,n", [
+    ("f16", 1, 1, 64, [1], [1], 1), ("bf16", 12, 12, 64, [1], [2000], 4), ("f16", 10, 2, 128, [3, 0, 1], [1500, 300, 129], 3),
+    ("bf16", 18, 2, 128, [1, 2], [900, 640], 40), ("f16", 40, 8, 128, [1, 1], [1000, 130], 2)])
+def test_selected_attention_matches_the_oracle(kind, hq, hkv, D, new, lens, n):
+    rng = np.random.default_rng(hq + n + D)
+    table, blocks, lens, total = _tree(rng, 1, len(lens), 0, 0, lens)
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32)
+    sel = np.full((sum(new), hkv, n), -1, np.int32)
+    row = 0
+    for m, length in zip(new, lens):
+        for j in range(m):
+            mine = (length - m + j) // P
+            for h in range(hkv):
+                pick = np.sort(rng.permutation(mine + 1)[:n])
+                sel[row, h, :len(pick)] = pick
+            row += 1
+    got = _attend(to_dev(q), dev, kind, table, blocks, [0] * len(lens), new, lens, selected=to_dev(sel))
+    want, bound = op.attention(q, k, v, table, blocks, [0] * len(lens), new, lens, sel, weight_step=_step(kind))
+    _check(got, want, bound)
+
+
+def test_lists_of_any_content_stay_within_the_cache():
+    """No block, blocks behind the token's own, the same twice, and nothing at all."""
+    rng = np.random.default_rng(6)
+    table, blocks, lens, total = _tree(rng, 1, 2, 0, 0, [500, 400])
+    dev, (k, v) = _pools(rng, total, 1, 64, "f16")
+    q = rng.standard_normal((3, 2, 64)).astype(np.float32)
+    sel = np.array([[[2, -1, 2, 99]], [[-1, -1, -1, -1]], [[2 ** 31 - 1, -2 ** 31, 1, 3]]], np.int32)
+    got = _attend(to_dev(q), dev, "f16", table, blocks, [0, 0], [2, 1], lens, selected=to_dev(sel))
+    want, bound = op.attention(q, k, v, table, blocks, [0, 0], [2, 1], lens, sel)
+    assert not to_host(got)[1].any()
+    _check(got, want, bound)
+
+
+# ------------------------------------------------------------------- together
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_a_forked_session_goes_on_like_its_parent(kind):
+    """Append a prompt, fork it twice (pages shared, the last copied), append other
+    tokens to each, attend over the shared pages, then select pages and attend over
+    those: every result as the oracle's on the pages that are there."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(12)
+    hq, hkv, D, n0 = 6, 2, 64, 1000
+    dt, tt = _type(kind)
+    pools = [t.zeros((40, hkv, P, D), dtype=tt, device="cuda") for _ in "kv"]
+    kv, bounds = d.kv_pages(pools[0], pools[1], dt), t.zeros((40, hkv, 2, D), dtype=tt, device="cuda")
+    rot, ws = d.Rotary(10000.0), d.Workspace(2000, hq, D, 4096)
+    def step(table, blocks, new, lens, n_select=3):
+        batch = d.PagedBatch(table, blocks, [0] * len(lens), new, lens)
+        qkv = to_dev(rng.standard_normal((sum(new), (hq + 2 * hkv) * D)).astype(np.float32))
+        d.kv_append_paged(qkv, hq, kv, batch, rot, ws)
+        d.kv_page_bounds(kv, batch, bounds)
+        q = qkv.view(sum(new), hq + 2 * hkv, D)[:, :hq]
+        dense = d.attention_decode_shared(q, kv, batch, ws)
+        sel = d.kv_select_pages(q, kv, bounds, batch, n_select, ws)
+        return q, dense, sel, d.attention_decode_selected(q, kv, batch, sel, ws)
+    table = np.zeros((3, 10), np.int32)
+    table[0, :8] = [31, 2, 17, 5, 8, 21, 13, 39]
+    step(table[:1], [8], [n0], [n0])
+    # forks: 7 full pages shared, 104 keys of the eighth copied
+    table[1:, :8] = table[0, :8]
+    table[1:, 7] = [4, 6]
+    d.kv_copy_pages([kv], [39, 39], [4, 6], [n0 % P] * 2)
+    table[0, 8], table[1, 8] = 9, 10
+    lens, new = [n0 + 30, n0 + 25, n0 + 1], [30, 25, 1]
+    q, dense, sel, sparse = step(table, [9, 9, 8], new, lens)
+    k, v = (x.double().cpu().numpy() for x in pools)
+    host = to_host(q).astype(np.float64)
+    want, bound = op.attention(host, k, v, table, [9, 9, 8], [0] * 3, new, lens, weight_step=_step(kind))
+    _check(dense, want, bound, "dense")
+    bnd = np.zeros((40, hkv, 2, D))
+    bnd = op.bounds(k, table, lens, lens, bnd)               # of every page that a sequence has
+    used = sorted({int(x) for s, n in enumerate(lens) for x in table[s, :-(-n // P)]})
+    assert np.array_equal(to_host(bounds.double())[used], bnd[used])
+    want_sel = op.select(to_host(q), bnd, table, new, lens, 3, 1, 1)
+    assert np.array_equal(to_host(sel), want_sel)
+    want, bound = op.attention(host, k, v, table, [9, 9, 8], [0] * 3, new, lens, want_sel, weight_step=_step(kind))
+    _check(sparse, want, bound, "sparse")
