@@ -51,6 +51,7 @@
 #include "dsb_kernels.h"
 #include "dsb_ptx.cuh"
 #include "dsb_q8.cuh"
+#include "kv_tensor_map.h"
 
 namespace dsbk {
 
@@ -885,11 +886,7 @@ size_t partial_smem(int R) {
 // Tensor maps of the K and V caches viewed as [rows][D] 16-bit elements, with
 // 64-column x 64-key boxes and the 128-byte swizzle.  Encoded on the host
 // (no device work) and cached by address and shape.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t kv_tensor_map(const void* base, long long rows, int D, int dtype, CUtensorMap* out) {
+cudaError_t cached_tensor_map(const void* base, long long rows, int D, int dtype, CUtensorMap* out) {
   struct Entry {
     const void* base;
     long long rows;
@@ -899,31 +896,15 @@ cudaError_t kv_tensor_map(const void* base, long long rows, int D, int dtype, CU
   static std::mutex mu;
   static Entry cache[16];
   static int n_cache = 0, next_slot = 0;
-  static EncodeTiledFn encode = nullptr;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n_cache; ++i)
     if (cache[i].base == base && cache[i].rows == rows && cache[i].D == D && cache[i].dtype == dtype) {
       *out = cache[i].map;
       return cudaSuccess;
     }
-  if (!encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-    if (e != cudaSuccess) return e;
-    if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    encode = reinterpret_cast<EncodeTiledFn>(fn);
-  }
-  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBoxCols, (cuuint32_t)kBoxKeys};
-  const cuuint32_t estr[2] = {1, 1};
   CUtensorMap m;
-  const CUresult r = encode(&m, dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  const cudaError_t e = kv_tensor_map(base, rows, D, dtype, kBoxKeys, &m);
+  if (e != cudaSuccess) return e;
   const int slot = n_cache < 16 ? n_cache++ : (next_slot++ & 15);
   cache[slot] = Entry{base, rows, D, dtype, m};
   *out = m;
@@ -940,8 +921,8 @@ cudaError_t launch_partial_merge(Kern kern, size_t smem, const float* q, long lo
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   CUtensorMap tmk, tmv;
-  if ((e = kv_tensor_map(kc, kv_rows, D, dtype, &tmk)) != cudaSuccess) return e;
-  if ((e = kv_tensor_map(vc, kv_rows, D, dtype, &tmv)) != cudaSuccess) return e;
+  if ((e = cached_tensor_map(kc, kv_rows, D, dtype, &tmk)) != cudaSuccess) return e;
+  if ((e = cached_tensor_map(vc, kv_rows, D, dtype, &tmv)) != cudaSuccess) return e;
   const float scale = (float)(1.0 / sqrt((double)D));
   int resident = 0;
   {

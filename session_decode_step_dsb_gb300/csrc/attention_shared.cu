@@ -5,25 +5,21 @@
 //   out = sum_k exp(s_k - max s) v_k / sum_k exp(s_k - max s),  s_k = q . k / sqrt(D)
 //
 // Few rows read every key for little work: bound by memory, 4 D bytes a key and kv head.
-// So the design is about loads in flight and nothing else.  A CTA of four warps walks over
-// pages, each warp over its own 32 keys of every page with its own running reference, sums
-// and output: no barrier until a part ends.  A warp asks for 16 keys of K and V at a time,
-// cp.async into a ring of stages of its own, from which each lane reads only what it
-// asked for itself: the pieces are laid out so that they are the lane's parts of the
-// matrix operands (below), so no lane waits for another.
+// So the design is about bytes on their way and few instructions.  A CTA of four warps walks
+// over pages, each warp over its own 32 keys of every page with its own running reference,
+// sums and output: no barrier until a part ends.  A warp has a ring of three slots of 32 keys
+// of K or V, which one lane fills by TMA tensor copies (128-byte swizzle, so that ldmatrix
+// reads without bank conflicts) as soon as one is free.
 //
 // Products: m16n8k16 in the cache's type, float32 sums.  A tile has 8 query rows; their
 // upper parts are rows 0 to 7 of the left operand and their lower parts rows 8 to 15, so
 // that one product makes both halves of a float32 product, which a lane then holds side by
-// side.  (bf16 queries have a third part, in a product of its own; weights have two.)  The
-// order of the dimensions along a product's sum is free, so lane (g, c) of the K operand
-// takes 16-byte pieces c, c + 4, .. of key g; and the order of the dimensions across the
-// second product's columns is free, so it takes pieces g and g + 8 of keys 2c, 2c + 1, 2c + 8,
-// 2c + 9 of V and pairs up the keys' halves.
+// side.  (bf16 has a third part, in a product of its own.)  The scores of a lane's row and
+// keys are where the left operand of the second product wants their weights.
 //
 // The tensor core's sums round toward zero, which would tell over the pages of a part: each
-// product of weights and V starts from zero, and its two halves are added to the output
-// in float32.
+// page's products of weights and V start from zero, and their halves are added to the
+// output in float32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,6 +32,7 @@
 #include "attention_shared.cuh"
 #include "dsb_kernels.h"
 #include "dsb_ptx.cuh"
+#include "kv_tensor_map.h"
 
 namespace dsbk {
 
@@ -44,52 +41,55 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kRows = 8;
-constexpr int kStep = 16;  // keys of a stage
+
+__device__ unsigned int g_err_attention_pages = 0;
 
 template <int D>
 struct Ring {
-  static constexpr int pieces = D / 8;           // of a lane, 16 bytes each: half of them K
-  static constexpr int stage = pieces * 512;     // bytes
-  static constexpr int stages = 24576 / stage;   // 24 KB a warp
-  static constexpr int bytes = kWarps * stages * stage;
-  static constexpr int join = kWarps * kRows * D * 4;
-  static constexpr int smem = bytes + join + kWarps * kRows * 8;
+  static constexpr int keys = 32;                // of a slot, K or V
+  static constexpr int slab = keys * 128;        // 64 columns of them
+  static constexpr int slot = D / 64 * slab;
+  static constexpr int slots = 24576 / slot;     // 24 KB a warp
+  static constexpr int bytes = kWarps * slots * slot;
+  static constexpr int join = bytes;             // [warp][row][D] sums, [warp][row] statistics
+  static constexpr int stat = join + kWarps * kRows * D * 4;
+  static constexpr int bars = stat + kWarps * kRows * 8;
+  static constexpr int smem = bars + kWarps * slots * 8;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
 }
 
-// d = a b + c, c given or zero
 #define DSB_MMA(TYPE)                                                                                              \
   asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "        \
-      "{%10,%11,%12,%13};"                                                                                         \
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                             \
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3))
+      "{%0,%1,%2,%3};"                                                                                             \
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                             \
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
 template <typename T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1, float c0, float c1, float c2, float c3) {
+                                    uint32_t b1) {
   if constexpr (std::is_same_v<T, __half>)
     DSB_MMA("f16");
   else
     DSB_MMA("bf16");
 }
 #undef DSB_MMA
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  mma<T>(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
-}
 
 template <typename T>
 __device__ __forceinline__ float value(T x);
@@ -104,23 +104,29 @@ __device__ __forceinline__ bool odd(uint32_t w) {
   constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
   return (w & e) == e || (w & e << 16) == e << 16;
 }
-template <typename T>
-__device__ __forceinline__ bool odd(uint4 v) { return odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w); }
 
 template <int D, typename T, typename Walk, int N>
 __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
-    const float* __restrict__ q, long long q_stride, int hq, int hkv, const T* __restrict__ kp, const T* __restrict__ vp,
-    int n_seg, int n_tok, const int32_t* __restrict__ selected, int n_select, int sel_stride, int sel_cap, float scale_log2e,
-    PartialsOut to, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
+    long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, int n_tok,
+    const int32_t* __restrict__ selected, int n_select, int sel_stride, int sel_cap, float scale_log2e, PartialsOut to,
+    const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using R = Ring<D>;
-  constexpr int PG = D / 32, VH = D / 64;  // 16-byte pieces of a lane: of a K row, of a V row
-  extern __shared__ __align__(128) uint8_t smem[];
-  float* joined = reinterpret_cast<float*>(smem + R::bytes);                     // [warp][row][D]
-  float2* joined_stat = reinterpret_cast<float2*>(smem + R::bytes + R::join);    // [warp][row]
+  constexpr int KK = D / 16, NT = D / 8;  // steps of the first product, column tiles of the second
+  constexpr bool kThird = Parts<T>::kMore > 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* joined = reinterpret_cast<float*>(smem + R::join);
+  float2* joined_stat = reinterpret_cast<float2*>(smem + R::stat);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_addr(smem) + warp * R::stages * R::stage + lane * 16;
+  uint8_t* ring = smem + warp * R::slots * R::slot;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::bars) + warp * R::slots;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   const int cta = blockIdx.x, ctas = gridDim.x;
+  if (lane == 0) {
+    for (int i = 0; i < R::slots; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
 
@@ -131,66 +137,75 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     cur.begin(meta, n_seg, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, cta, ctas);
   ahead = cur;
 
-  // ---- asking: entry `e` of ahead's run, its half `half`; 32 entries' blocks and pages
-  // in the lanes
-  int e = ahead.i, half = 0, list_at = 0, list_block = 0, list_page = 0, filled = 0;
-  bool asking = true;
-  const auto list = [&]() {
-    list_at = e;
-    if (e + lane < ahead.n_pages) {
-      const int got = ahead.listed(e + lane);
-      list_block = ahead.block(e + lane, got);
-      if constexpr (std::is_same_v<Walk, SharedWalk>)
-        list_page = ahead.page(e + lane);
-      else
-        list_page = ahead.seen(list_block * kPgKeys, 1) ? meta[ahead.pg_at + got] : 0;
-    }
-  };
-  list();
-  const auto ask = [&]() {
-    if (asking) {
-      const int block = __shfl_sync(0xFFFFFFFFu, list_block, e - list_at);
-      const int page = __shfl_sync(0xFFFFFFFFu, list_page, e - list_at);
-      const int in_page = 32 * warp + kStep * half;
-      if (ahead.seen(block * kPgKeys + in_page, kStep)) {
-        const size_t row0 = ((size_t)page * hkv + ahead.h) * kPgKeys + in_page;
-        const uint32_t dst = ring + filled * R::stage;
-        const T* ks = kp + (row0 + g) * D + 8 * c;
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-          for (int p = 0; p < PG; ++p) cp16(dst + (kt * PG + p) * 512, ks + kt * 8 * D + p * 32);
-        const T* vs = vp + (row0 + 2 * c) * D + 8 * g;
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int v = 0; v < VH; ++v)
-            cp16(dst + (2 * PG + n * VH + v) * 512, vs + ((n >> 1) * 8 + (n & 1)) * D + v * 64);
+  // ---- asking: entry `e` of ahead's run; 32 entries' blocks and pages in the lanes.  Entries
+  // of which no row sees a key of this warp are neither asked for nor gone through.
+  int e = ahead.i - 1, list_at = ahead.i - 32, list_block = 0, list_page = 0, row0 = 0, filled = 0;
+  bool asking = true, value_next = false;
+  const auto find = [&]() {  // the next entry to ask for
+    for (;;) {
+      if (++e == ahead.i_end) {
+        if (!ahead.another()) {
+          asking = false;
+          return;
+        }
+        ahead.next();
+        e = ahead.i;
+        list_at = e - 32;
       }
-      if (++filled == R::stages) filled = 0;
-      if ((half ^= 1) == 0) {
-        if (++e == ahead.i_end) {
-          if (ahead.another()) {
-            ahead.next();
-            e = ahead.i;
-            list();
-          } else {
-            asking = false;
-          }
-        } else if (e - list_at == 32) {
-          list();
+      if (e - list_at == 32) {
+        list_at = e;
+        if (e + lane < ahead.n_pages) {
+          const int got = ahead.listed(e + lane);
+          list_block = ahead.block(e + lane, got);
+          if constexpr (std::is_same_v<Walk, SharedWalk>)
+            list_page = ahead.page(e + lane);
+          else
+            list_page = ahead.seen(list_block * kPgKeys, 1) ? meta[ahead.pg_at + got] : 0;
         }
       }
+      const int block = __shfl_sync(0xFFFFFFFFu, list_block, e - list_at);
+      const int page = __shfl_sync(0xFFFFFFFFu, list_page, e - list_at);
+      if (ahead.seen(block * kPgKeys + 32 * warp, 32)) {
+        row0 = (page * hkv + ahead.h) * kPgKeys + 32 * warp;
+        return;
+      }
     }
-    cp_commit();
   };
+  // One lane asks for 32 keys of K, or then of V, into the slot that is next.
+  const auto ask = [&]() {
+    if (!asking) return;
+    if (lane == 0) {
+      const CUtensorMap* map = value_next ? &tmv : &tmk;
+      mbar_arrive_expect_tx(&full[filled], R::slot);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) tma_box(ring + filled * R::slot + x * R::slab, map, 64 * x, row0, &full[filled]);
+    }
+    if (++filled == R::slots) filled = 0;
+    value_next = !value_next;
+    if (!value_next) find();
+  };
+  find();
 #pragma unroll 1
-  for (int i = 0; i < R::stages; ++i) ask();
+  for (int i = 0; i < R::slots; ++i) ask();
 
-  int stage = 0;
+  // ldmatrix: lane i points at row i % 8 of matrix i / 8.  K: matrices (keys 0-7, dims
+  // 0-7), (keys 0-7, dims 8-15), (keys 8-15, ..); V: (keys 0-7, dims 0-7), (keys 8-15, dims 0-7),
+  // (keys 0-7, dims 8-15), ..
+  // Piece j of a row of 128 bytes lies at piece j ^ (row % 8): steps of two pieces flip
+  // bits 5 and 6 of the address.
+  const uint32_t k_at = smem_addr(ring) + ((lane & 7) + (lane >> 4) * 8) * 128 + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
+  const uint32_t v_at = smem_addr(ring) + ((lane & 7) + (lane >> 3 & 1) * 8) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+  int slot = 0;
+  uint32_t phase = 0;
+  const auto next_slot = [&]() {
+    fence_proxy_async_smem();  // what the lanes have read or cleared precedes the next copy
+    __syncwarp();
+    if (++slot == R::slots) slot = 0, phase ^= 1u;
+    ask();
+  };
+
   for (;;) {
-    // ---- the tile's rows: lane (g, c) holds row g, the pieces of its dimensions that it
-    // has of a key
+    // ---- the tile's rows: lane (g, c) holds row g
     const int live = cur.tile_rows();
     RowAt at{0, 0, 0, 0x7FFFFFFF};
     if (g < live) at = cur.row(g, hq);
@@ -202,27 +217,22 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       min_lo = min(min_lo, __shfl_xor_sync(0xFFFFFFFFu, min_lo, o));
       max_lo = max(max_lo, __shfl_xor_sync(0xFFFFFFFFu, max_lo, o));
     }
-    uint32_t qa[PG][2][4];                                               // upper and lower parts
-    uint32_t qb[Parts<T>::kScore > 2 ? PG : 1][2][2];                    // the third
+    // upper and lower parts of dimensions 16 k + 2c, + 1 and 16 k + 8 + 2c, + 1; the third
+    uint32_t qa[KK][4], qb[kThird ? KK : 1][2];
     float rs;
     {
-      float x[PG][8];
-      const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + 8 * c;
+      float2 x[KK][2];
+      const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + 2 * c;
       float m = 0.0f;
 #pragma unroll
-      for (int p = 0; p < PG; ++p) {
-        float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f), v1 = v0;
-        if (g < live) {
-          v0 = __ldg(reinterpret_cast<const float4*>(src + 32 * p));
-          v1 = __ldg(reinterpret_cast<const float4*>(src + 32 * p + 4));
-        }
-        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      for (int k = 0; k < KK; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[p][i] = v[i] * scale_log2e;
-          m = fmaxf(m, fabsf(x[p][i]));
+        for (int j = 0; j < 2; ++j) {
+          float2 v = make_float2(0.0f, 0.0f);
+          if (g < live) v = __ldg(reinterpret_cast<const float2*>(src + 16 * k + 8 * j));
+          x[k][j] = make_float2(v.x * scale_log2e, v.y * scale_log2e);
+          m = fmaxf(m, fmaxf(fabsf(x[k][j].x), fabsf(x[k][j].y)));
         }
-      }
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
@@ -231,23 +241,19 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
       rs = __uint_as_float((uint32_t)(ex - 10) << 23);
 #pragma unroll
-      for (int p = 0; p < PG; ++p)
+      for (int k = 0; k < KK; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x0 = x[p][4 * j + 2 * k] * inv, x1 = x[p][4 * j + 2 * k + 1] * inv;
-            qa[p][j][2 * k] = Parts<T>::take(x0, x1);
-            qa[p][j][2 * k + 1] = Parts<T>::take(x0, x1);
-            if constexpr (Parts<T>::kScore > 2) qb[p][j][k] = Parts<T>::take(x0, x1);
-          }
+        for (int j = 0; j < 2; ++j) {
+          float x0 = x[k][j].x * inv, x1 = x[k][j].y * inv;
+          qa[k][2 * j] = Parts<T>::take(x0, x1);
+          qa[k][2 * j + 1] = Parts<T>::take(x0, x1);
+          if constexpr (kThird) qb[k][j] = Parts<T>::take(x0, x1);
+        }
     }
 
-    f2 o[VH][8];  // of row g: columns 2c and 2c + 1 of each product
+    f2 o[NT];  // of row g: dimensions 8 t + 2c, + 1
 #pragma unroll
-    for (int v = 0; v < VH; ++v)
-#pragma unroll
-      for (int t = 0; t < 8; ++t) o[v][t] = 0;
+    for (int t = 0; t < NT; ++t) o[t] = 0;
     float minus = kNoRef, l = 0.0f;
 
     int blocks_at = 0, blocks = 0;
@@ -262,146 +268,143 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
         }
         block = __shfl_sync(0xFFFFFFFFu, blocks, i - blocks_at);
       }
+      const int key0 = block * kPgKeys + 32 * warp;
+      if (!cur.seen(key0, 32)) continue;
+
+      // ---- scores of row g with keys 8 t + 2c, + 1
+      float s[4][4], s3[kThird ? 4 : 1][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          s[t][n] = 0.0f;
+          if constexpr (kThird) s3[t][n] = 0.0f;
+        }
+      if (!mbar_wait(&full[slot], phase)) g_err_attention_pages = 1u;
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        uint32_t b[2][4];
+        const uint32_t from = ((k_at + slot * R::slot) ^ (32 * (k & 3))) + (k >> 2) * R::slab;
+        ldsm(b[0], from);
+        ldsm(b[1], from + 16 * 128);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          mma<T>(s[t], qa[k][0], qa[k][1], qa[k][2], qa[k][3], b[t >> 1][2 * (t & 1)], b[t >> 1][2 * (t & 1) + 1]);
+          if constexpr (kThird) mma<T>(s3[t], 0u, qb[k][0], 0u, qb[k][1], b[t >> 1][2 * (t & 1)], b[t >> 1][2 * (t & 1) + 1]);
+        }
+      }
+      next_slot();
+
+      float p[8];  // of keys 8 (n >> 1) + 2c + (n & 1)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        float low = s[n >> 1][2 + (n & 1)];
+        if constexpr (kThird) low += s3[n >> 1][2 + (n & 1)];
+        p[n] = s[n >> 1][n & 1] + low;
+      }
+      const bool whole = key0 >= max_lo && key0 + 31 <= min_hi;
+      unsigned hidden = 0;
+      if (!whole) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int key = key0 + 8 * (n >> 1) + 2 * c + (n & 1);
+          hidden |= (unsigned)(key > at.hi || key < at.lo) << n;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) top = fmaxf(top, hidden >> n & 1u ? -INFINITY : p[n] * rs);
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const bool grown = top + minus > kRoom + kSlack;
+      if (__any_sync(0xFFFFFFFFu, grown)) {
+        const float to_minus = grown ? kRoom - top : minus, f = exp2_of(to_minus - minus);
+        minus = to_minus;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t] = mul2(o[t], pack(f, f));
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        p[n] = hidden >> n & 1u ? 0.0f : exp2_of(fmaf(p[n], rs, minus));
+        l += p[n];
+      }
+
+      if (!mbar_wait(&full[slot], phase)) g_err_attention_pages = 1u;
+      __syncwarp();
+      if (!whole) {
+        // Lane i looks after key i.  One that no row sees may hold anything: cleared.  One
+        // that some rows see, with an infinity or a NaN: 0 times it is no 0, so it is
+        // cleared too, and added to the rows that see it.
+        const int key = key0 + lane;
+        const bool none = key > max_hi || key < min_lo;
+        bool strange = false;
+        uint4* row = reinterpret_cast<uint4*>(ring + slot * R::slot + lane * 128);
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        cp_wait<R::stages - 1>();
-        const int key0 = block * kPgKeys + 32 * warp + kStep * hf;
-        if (cur.seen(key0, kStep)) {
-          const uint32_t from = ring + stage * R::stage;
-          // ---- scores of row g with keys 2c, 2c + 1 of both tiles of eight
-          float s[2][4];
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.0f;
-#pragma unroll
-            for (int p = 0; p < PG; ++p) {
-              const uint4 k = lds16(from + (kt * PG + p) * 512);
-              mma<T>(s[kt], qa[p][0][0], qa[p][0][1], qa[p][0][2], qa[p][0][3], k.x, k.y);
-              mma<T>(s[kt], qa[p][1][0], qa[p][1][1], qa[p][1][2], qa[p][1][3], k.z, k.w);
-              if constexpr (Parts<T>::kScore > 2) {
-                mma<T>(s[kt], 0u, qb[p][0][0], 0u, qb[p][0][1], k.x, k.y);
-                mma<T>(s[kt], 0u, qb[p][1][0], 0u, qb[p][1][1], k.z, k.w);
-              }
-            }
-          }
-          uint4 v[4][VH];
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int h2 = 0; h2 < VH; ++h2) v[n][h2] = lds16(from + (2 * PG + n * VH + h2) * 512);
-          // n: key 8 (n >> 1) + 2c + (n & 1) of the step
-          float x[4], p[4];
-          bool hidden[4] = {false, false, false, false};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) x[n] = s[n >> 1][n & 1] + s[n >> 1][2 + (n & 1)];
-          const bool whole = key0 >= max_lo && key0 + kStep - 1 <= min_hi;
-          unsigned strange = 0;
-          if (!whole) {
-            bool bad[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const int key = key0 + 8 * (n >> 1) + 2 * c + (n & 1);
-              hidden[n] = key > at.hi || key < at.lo;
-              // a key that no row sees may hold anything; nothing of it enters a product
-              const bool none = key > max_hi || key < min_lo;
-              bad[n] = false;
-#pragma unroll
-              for (int h2 = 0; h2 < VH; ++h2) {
-                if (none) v[n][h2] = make_uint4(0, 0, 0, 0);
-                bad[n] = bad[n] || odd<T>(v[n][h2]);
-              }
-            }
-            // one that some rows see, with an infinity or a NaN: 0 times it is no 0, so it
-            // is left out of the product and added below to the rows that see it
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              unsigned b = __ballot_sync(0xFFFFFFFFu, bad[n]);  // any lane (., c): the same keys
-              b |= b >> 4;
-              b |= b >> 8;
-              b |= b >> 16;
-              strange |= (b & 15u) << (4 * n);
-              if (b >> c & 1u) {
-#pragma unroll
-                for (int h2 = 0; h2 < VH; ++h2) v[n][h2] = make_uint4(0, 0, 0, 0);
-              }
-            }
-          }
-          float top = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) top = fmaxf(top, hidden[n] ? -INFINITY : x[n] * rs);
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const bool grown = top + minus > kRoom + kSlack;
-          if (__any_sync(0xFFFFFFFFu, grown)) {
-            const float to_minus = grown ? kRoom - top : minus, f = exp2_of(to_minus - minus);
-            minus = to_minus;
-            l *= f;
-#pragma unroll
-            for (int h2 = 0; h2 < VH; ++h2)
-#pragma unroll
-              for (int t = 0; t < 8; ++t) o[h2][t] = mul2(o[h2][t], pack(f, f));
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            p[n] = hidden[n] ? 0.0f : exp2_of(fmaf(x[n], rs, minus));
-            l += p[n];
-          }
-          if (strange) {
-            // rows 0 to 15 of key n's 4 lanes c: bit 4 n + c
+        for (int x = 0; x < NT; ++x) {
+          const uint4 v = row[(x >> 3) * (R::slab / 16) + (x & 7)];
+          strange = strange || odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w);
+        }
+        if (none || strange) {
 #pragma unroll 1
-            for (int b = 0; b < 16; ++b) {
-              if (!(strange >> b & 1u)) continue;
-              const int n = b >> 2, from_lane = (lane & ~3) | (b & 3);
-              const float pn = n == 0 ? p[0] : n == 1 ? p[1] : n == 2 ? p[2] : p[3];
-              const bool hn = n == 0 ? hidden[0] : n == 1 ? hidden[1] : n == 2 ? hidden[2] : hidden[3];
-              const float w = __shfl_sync(0xFFFFFFFFu, pn, from_lane);
-              const bool no = __shfl_sync(0xFFFFFFFFu, (int)hn, from_lane);
-              const int page = [&] {
-                if constexpr (std::is_same_v<Walk, SharedWalk>)
-                  return cur.page(i);
-                else
-                  return meta[cur.pg_at + block];
-              }();
-              const T* row = vp + (((size_t)page * hkv + cur.h) * kPgKeys + 32 * warp + kStep * hf + 8 * (n >> 1) +
-                                   2 * (b & 3) + (n & 1)) * D;
-              if (!no) {
+          for (int x = 0; x < NT; ++x) row[(x >> 3) * (R::slab / 16) + (x & 7)] = make_uint4(0, 0, 0, 0);
+        }
+        unsigned odd_keys = __ballot_sync(0xFFFFFFFFu, strange && !none);
+        if (odd_keys) {
+          const int page = [&] {
+            if constexpr (std::is_same_v<Walk, SharedWalk>)
+              return cur.page(i);
+            else
+              return meta[cur.pg_at + block];
+          }();
+          const T* rows = vp + (((size_t)page * hkv + cur.h) * kPgKeys + 32 * warp) * D;
+#pragma unroll 1
+          for (; odd_keys; odd_keys &= odd_keys - 1) {
+            const int k = __ffs(odd_keys) - 1, from_lane = (lane & ~3) | (k >> 1 & 3), n = 2 * (k >> 3) + (k & 1);
+            float mine = 0.0f;
 #pragma unroll
-                for (int h2 = 0; h2 < VH; ++h2)
+            for (int m = 0; m < 8; ++m)
+              if (m == n) mine = p[m];
+            const float w = __shfl_sync(0xFFFFFFFFu, mine, from_lane);
+            if (__shfl_sync(0xFFFFFFFFu, hidden, from_lane) >> n & 1u) continue;
 #pragma unroll
-                  for (int t = 0; t < 8; ++t)
-                    o[h2][t] = fma2(pack(w, w), pack(value<T>(row[8 * (2 * c + 8 * h2) + t]),
-                                                     value<T>(row[8 * (2 * c + 1 + 8 * h2) + t])), o[h2][t]);
-              }
-            }
-          }
-          // ---- output: columns t of half h2 are dimensions 8 (n + 8 h2) + t
-          uint32_t a[4];
-          {
-            float p0 = p[0], p1 = p[1], p2 = p[2], p3 = p[3];
-            a[0] = Parts<T>::take(p0, p1);
-            a[1] = Parts<T>::take(p0, p1);
-            a[2] = Parts<T>::take(p2, p3);
-            a[3] = Parts<T>::take(p2, p3);
-          }
-#pragma unroll
-          for (int h2 = 0; h2 < VH; ++h2) {
-            const uint32_t w[4][4] = {{v[0][h2].x, v[0][h2].y, v[0][h2].z, v[0][h2].w},
-                                      {v[1][h2].x, v[1][h2].y, v[1][h2].z, v[1][h2].w},
-                                      {v[2][h2].x, v[2][h2].y, v[2][h2].z, v[2][h2].w},
-                                      {v[3][h2].x, v[3][h2].y, v[3][h2].z, v[3][h2].w}};
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              const uint32_t pick = t & 1 ? 0x7632u : 0x5410u;
-              float d[4];
-              mma<T>(d, a[0], a[1], a[2], a[3], __byte_perm(w[0][t >> 1], w[1][t >> 1], pick),
-                     __byte_perm(w[2][t >> 1], w[3][t >> 1], pick), 0.0f, 0.0f, 0.0f, 0.0f);
-              o[h2][t] = add2(o[h2][t], add2(pack(d[0], d[1]), pack(d[2], d[3])));
-            }
+            for (int t = 0; t < NT; ++t)
+              o[t] = fma2(pack(w, w), pack(value<T>(rows[k * D + 8 * t + 2 * c]), value<T>(rows[k * D + 8 * t + 2 * c + 1])), o[t]);
           }
         }
-        if (++stage == R::stages) stage = 0;
-        ask();
+        __syncwarp();
       }
+      // ---- output
+      uint32_t a[2][4], third[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x0 = p[4 * k + 2 * j], x1 = p[4 * k + 2 * j + 1];
+          a[k][2 * j] = Parts<T>::take(x0, x1);
+          a[k][2 * j + 1] = Parts<T>::take(x0, x1);
+          third[k][j] = Parts<T>::take(x0, x1);
+        }
+#pragma unroll
+      for (int t2 = 0; t2 < NT / 2; ++t2) {
+        uint32_t b[2][4];
+        const uint32_t from = ((v_at + slot * R::slot) ^ (32 * (t2 & 3))) + (t2 >> 2) * R::slab;
+        ldsm_t(b[0], from);
+        ldsm_t(b[1], from + 16 * 128);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (kThird) {
+            mma<T>(d, 0u, third[0][0], 0u, third[0][1], b[0][2 * t], b[0][2 * t + 1]);
+            mma<T>(d, 0u, third[1][0], 0u, third[1][1], b[1][2 * t], b[1][2 * t + 1]);
+          }
+          mma<T>(d, a[0][0], a[0][1], a[0][2], a[0][3], b[0][2 * t], b[0][2 * t + 1]);
+          mma<T>(d, a[1][0], a[1][1], a[1][2], a[1][3], b[1][2 * t], b[1][2 * t + 1]);
+          o[2 * t2 + t] = add2(o[2 * t2 + t], add2(pack(d[0], d[1]), pack(d[2], d[3])));
+        }
+      }
+      next_slot();
     }
 
     // ---- the part's end: the four warps' rows joined
@@ -409,18 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
     __syncthreads();  // the last part's have been read
     {
-      float* row = joined + (warp * kRows + g) * D;
+      float2* row = reinterpret_cast<float2*>(joined + (warp * kRows + g) * D) + c;
 #pragma unroll
-      for (int h2 = 0; h2 < VH; ++h2)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float4* d = reinterpret_cast<float4*>(row + 8 * (2 * c + k + 8 * h2));
-          float x[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) x[t] = k ? unpack(o[h2][t]).y : unpack(o[h2][t]).x;
-          d[0] = make_float4(x[0], x[1], x[2], x[3]);
-          d[1] = make_float4(x[4], x[5], x[6], x[7]);
-        }
+      for (int t = 0; t < NT; ++t) row[4 * t] = unpack(o[t]);
       if (c == 0) joined_stat[warp * kRows + g] = make_float2(-minus, l);
     }
     __syncthreads();
@@ -477,7 +471,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     if (!cur.another()) break;
     cur.next();
   }
-  cp_wait<0>();
 }
 
 // One warp per row: the parts' sums at the largest of their references, in slot order.
@@ -562,11 +555,14 @@ cudaError_t pages_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st
   auto kern = attention_pages_kernel<D, T, Walk, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::smem);
   if (e != cudaSuccess) return e;
+  CUtensorMap tmk, tmv;
+  if ((e = kv_tensor_map(a.k, a.pool_rows, D, std::is_same_v<T, __half> ? 0 : 1, R::keys, &tmk)) != cudaSuccess) return e;
+  if ((e = kv_tensor_map(a.v, a.pool_rows, D, std::is_same_v<T, __half> ? 0 : 1, R::keys, &tmv)) != cudaSuccess) return e;
   ParamWords<N> w;
   fill_words(meta, &w);
   const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
-  return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)R::smem, st, a.q, a.q_stride, a.hq, a.hkv,
-                       static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.n_seg, a.n_tok, a.selected, a.n_select,
+  return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)R::smem, st, tmk, tmv, a.q, a.q_stride, a.hq,
+                       a.hkv, static_cast<const T*>(a.v), a.n_seg, a.n_tok, a.selected, a.n_select,
                        a.sel_stride, a.sel_cap, (float)(1.4426950408889634 / std::sqrt((double)D)), to, w, meta.dev);
 }
 
@@ -586,6 +582,13 @@ cudaError_t launch_attention_pages(const PageAttnArgs& a, int dtype, int head_di
   if (head_dim == 128)
     return dtype == 0 ? pages_walk<128, __half>(a, meta, st) : pages_walk<128, __nv_bfloat16>(a, meta, st);
   return dtype == 0 ? pages_walk<64, __half>(a, meta, st) : pages_walk<64, __nv_bfloat16>(a, meta, st);
+}
+
+unsigned int read_clear_error_attention_pages() {
+  unsigned int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_attention_pages, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  cudaMemcpyToSymbol(g_err_attention_pages, &z, sizeof z);
+  return v;
 }
 
 cudaError_t launch_attention_join(const PageAttnArgs& a, int n_seq, int head_dim, const MetaArg& meta, cudaStream_t st) {

@@ -34,13 +34,14 @@ __device__ __forceinline__ float exp2_of(float x) {
   return y;
 }
 
-// A float32 pair as two or three pairs of the 16-bit type that add up to it: fp16 to 22
-// bits in two; bf16 to 16 in two, 24 in three.
+// A float32 pair as pairs of the 16-bit type that add up to it, largest first: two of fp16
+// hold 22 bits (of values scaled into its range), two of bf16 only 16, three 24.  kMore:
+// products of the warp-level kernel, which holds two parts in one.
 template <typename T>
 struct Parts;
 template <>
 struct Parts<__half> {
-  static constexpr int kScore = 2;  // parts of a query value
+  static constexpr int kMore = 1;
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
     const __half2 h = __floats2half2_rn(x, y);
     const float2 f = __half22float2(h);
@@ -51,7 +52,7 @@ struct Parts<__half> {
 };
 template <>
 struct Parts<__nv_bfloat16> {
-  static constexpr int kScore = 3;
+  static constexpr int kMore = 2;
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);

@@ -375,6 +375,7 @@ struct PageAttnArgs {
   int hq, hkv;
   const void* k;
   const void* v;
+  long long pool_rows;      // pages * kv heads * 128
   int n_seg, n_tok;
   const int32_t* selected;  // or NULL: a plan of segments
   int n_select, sel_stride; // entries read of a list, and in it
@@ -388,6 +389,7 @@ struct PageAttnArgs {
 // CTAs that the GPU runs at once.
 int page_attn_resident(int sms);
 cudaError_t launch_attention_pages(const PageAttnArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
+unsigned int read_clear_error_attention_pages();
 // Metadata (always in the parameters): of each sequence its first token and its rows'
 // slots (0: nothing to join).
 cudaError_t launch_attention_join(const PageAttnArgs& a, int n_seq, int head_dim, const MetaArg& meta, cudaStream_t st);

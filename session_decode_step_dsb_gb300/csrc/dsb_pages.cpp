@@ -400,6 +400,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     a.hkv = hkv;
     a.k = kv->k;
     a.v = kv->v;
+    a.pool_rows = (long long)kv->n_pages * hkv * DSB_KV_PAGE;
     a.n_tok = n_tok;
     a.acc = reinterpret_cast<float*>(partial_base(ws));
     a.stat = a.acc + rows * slots * D;
@@ -595,6 +596,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
       a.hkv = hkv;
       a.k = kv->k;
       a.v = kv->v;
+      a.pool_rows = (long long)kv->n_pages * hkv * DSB_KV_PAGE;
       a.n_seg = l.n_seq;
       a.n_tok = l.n_tok;
       a.selected = selected + (size_t)l.tok0 * hkv * n_select;
