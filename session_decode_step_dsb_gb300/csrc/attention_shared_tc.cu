@@ -1,0 +1,552 @@
+// Decode attention over shared 16-bit pages for many query rows on a kv head (the drafts
+// and sessions of a group together, prompts), on the 5th-generation tensor cores
+// (sm_103a).  The mathematics is that of attention_shared.cu.
+//
+// A CTA takes 128 query rows of a kv head through its share of pages, 128 keys at a time:
+//   S = Q K^T   128 x 128, Q in parts (fp16: two; bf16: three, so that a product keeps
+//               float32's bits) in shared memory, K as it lies in the page
+//   P           a thread has half of a row's scores; weights go back to tensor memory in
+//               as many parts, the first two over the scores that they come from
+//   O = P V     128 x D of one page, V as it lies in the page; added to float32 registers
+//               by the threads (the tensor core's sums round toward zero)
+// The scores of the next page are multiplied while the weights of this one are made, so
+// that the tensor core works without a pause: S(n + 1) lies between P V(n - 1) and P V(n).
+// A warp of its own asks for the pages (TMA, two of K and two of V) and issues the
+// products.  Bound by the products: 32 (fp16) or 48 (bf16) of 128 x 128 x 16 for a page
+// of 128-wide heads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "attention_shared.cuh"
+#include "dsb_kernels.h"
+#include "dsb_ptx.cuh"
+#include "kv_tensor_map.h"
+
+namespace dsbk {
+
+namespace {
+
+constexpr int kWorkers = 256;
+constexpr int kThreads = kWorkers + 128;  // and a warpgroup whose first thread asks and issues
+// Registers of a thread: the launch gives each 168; the issuing warpgroup leaves some to
+// the workers, 256 x 192 + 128 x 120 = 384 x 168.
+constexpr int kWorkerRegs = 192, kIssuerRegs = 120;
+static_assert(kWorkers * kWorkerRegs + 128 * kIssuerRegs <= kThreads * 168, "register split");
+constexpr int kRows = 128;
+
+__device__ unsigned int g_err_attention_shared_tc = 0;
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start, distance of 64-column groups
+// (of an operand whose columns run along its rows), distance of groups of eight rows.
+__device__ __forceinline__ uint64_t desc(uint32_t at, uint32_t groups, uint32_t eights) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(groups >> 4) << 16) | ((uint64_t)(eights >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// kind::f16 with float32 sums, M = 128; trans_b: B's rows run along N.
+template <typename T>
+__device__ __forceinline__ uint32_t idesc(int n, bool trans_b) {
+  const uint32_t type = std::is_same_v<T, __half> ? 0u : 1u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)trans_b << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+// 32 columns of this thread's row.
+__device__ __forceinline__ void tm_ld32(uint32_t at, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t tm_ld1(uint32_t at) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The two warps that share 32 rows; all workers; the latter telling whether any passed true.
+__device__ __forceinline__ void meet_pair(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
+__device__ __forceinline__ bool meet_or(bool x) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 5, 256, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)x)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T>
+__device__ __forceinline__ float half_of(uint32_t w, int which) {
+  const uint16_t h = (uint16_t)(which ? w >> 16 : w);
+  if constexpr (std::is_same_v<T, __half>)
+    return __half2float(__ushort_as_half(h));
+  else
+    return __uint_as_float((uint32_t)h << 16);
+}
+template <typename T>
+__device__ __forceinline__ bool odd(uint32_t w) {  // an infinity or a NaN in a pair
+  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+  return (w & e) == e || (w & e << 16) == e << 16;
+}
+
+template <int D, typename T>
+struct Smem {
+  static constexpr int parts = Parts<T>::kMore + 1;
+  static constexpr int slab = 128 * 128;            // 64 columns of 128 rows
+  static constexpr int tile = D / 64 * slab;        // a part of Q, a page of K or V
+  static constexpr int q = 0;
+  static constexpr int k = q + parts * tile;        // two pages
+  static constexpr int v = k + 2 * tile;            // two pages
+  static constexpr int top = v + 2 * tile;          // [2][2][128] row maxima, sums
+  static constexpr int strange = top + 2 * 2 * 128 * 4;  // [4] words: keys
+  static constexpr int bars = strange + 16;         // K, V [2], scores [2], output, weights, queries
+  static constexpr int base = bars + 9 * 8;
+  static constexpr int bytes = base + 8;
+  // tensor memory: scores and weights of two pages, output, third parts of two pages
+  static constexpr int s_col = 0, o_col = 256, t_col = 384;
+};
+
+template <int D, typename T, int N>
+__global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
+    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
+    long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, float scale_log2e, PartialsOut to,
+    const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+  using S = Smem<D, T>;
+  constexpr int PARTS = S::parts, HD = D / 2;  // dimensions of a thread
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* top = reinterpret_cast<float*>(smem + S::top);
+  unsigned* strange = reinterpret_cast<unsigned*>(smem + S::strange);
+  uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::bars);
+  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *output = scores + 2, *weights = output + 1, *queries = weights + 1;
+  uint32_t* base = reinterpret_cast<uint32_t*>(smem + S::base);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t* meta = N > 1 ? words.w : meta_dev;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  if (tid == 0) {
+    for (int i = 0; i < 7; ++i) mbar_init(&full_k[i], 1);
+    mbar_init(weights, kWorkers / 32);
+    mbar_init(queries, kWorkers / 32);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = *base;
+  pdl_wait();
+  pdl_trigger();
+  SharedWalk cur;
+  cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
+
+  if (warp >= kWorkers / 32) {
+    // ---- the asking and issuing thread; n counts the pages of all its runs
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+    if (tid == kWorkers) {
+      SharedWalk ahead = cur;  // of K; V follows one page later
+      int ek = ahead.i, asked_k = 0, asked_v = 0;
+      int at_row[4];           // rows of the pages asked for in K, until V is
+      bool more = true;
+      const auto ask_k = [&]() {
+        if (!more) return;
+        const int row0 = (ahead.page(ek) * hkv + ahead.h) * kPgKeys, b = asked_k & 1;
+        at_row[asked_k & 3] = row0;
+        mbar_arrive_expect_tx(&full_k[b], S::tile);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) tma_box(smem + S::k + b * S::tile + x * S::slab, &tmk, 64 * x, row0, &full_k[b]);
+        ++asked_k;
+        if (++ek == ahead.i_end) {
+          if (ahead.another()) {
+            ahead.next();
+            ek = ahead.i;
+          } else {
+            more = false;
+          }
+        }
+      };
+      const auto ask_v = [&]() {
+        if (asked_v == asked_k) return;
+        const int row0 = at_row[asked_v & 3], b = asked_v & 1;
+        mbar_arrive_expect_tx(&full_v[b], S::tile);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) tma_box(smem + S::v + b * S::tile + x * S::slab, &tmv, 64 * x, row0, &full_v[b]);
+        ++asked_v;
+      };
+      ask_k();
+      ask_v();
+      ask_k();
+      const uint32_t id_s = idesc<T>(128, false), id_o = idesc<T>(D, true);
+      const uint32_t sq = smem_addr(smem + S::q), sk = smem_addr(smem + S::k), sv = smem_addr(smem + S::v);
+      const auto score = [&](int n) {
+        if (!mbar_wait(&full_k[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+        fence_after();
+        const uint64_t kd = desc(sk + (n & 1) * S::tile, 0, 1024);
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part) {
+          const uint64_t qd = desc(sq + part * S::tile, 0, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t step = (uint64_t)((k >> 2) * (S::slab >> 4) + (k & 3) * 2);
+            mma_ss(tm + S::s_col + 128 * (n & 1), qd + step, kd + step, id_s, part < PARTS - 1 || k > 0);
+          }
+        }
+        commit(&scores[n & 1]);
+      };
+      int n = 0;
+      for (int run = 0;; ++run) {
+        if (!mbar_wait(queries, run & 1)) g_err_attention_shared_tc = 1u;
+        fence_after();
+        score(n);
+        for (int i = cur.i; i < cur.i_end; ++i, ++n) {
+          // K's place is free once the scores are there
+          if (!mbar_wait(&scores[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+          ask_k();
+          if (i + 1 < cur.i_end) score(n + 1);
+          // the weights are there, and the last output has been read, so V's other place is free
+          if (!mbar_wait(weights, n & 1)) g_err_attention_shared_tc = 1u;
+          ask_v();
+          if (!mbar_wait(&full_v[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+          fence_after();
+          const uint64_t vd = desc(sv + (n & 1) * S::tile, S::slab, 1024);
+#pragma unroll
+          for (int part = PARTS - 1; part >= 0; --part) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t a = part == 2 ? tm + S::t_col + 64 * (n & 1) + 8 * k
+                                           : tm + S::s_col + 128 * (n & 1) + 64 * (k >> 2) + 32 * part + 8 * (k & 3);
+              mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0);
+            }
+          }
+          commit(output);
+        }
+        if (!cur.another()) break;
+        cur.next();
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+    return;
+  }
+
+  // ---- workers: thread (row, part) has the row's keys and dimensions of one half
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkerRegs));
+  const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
+  const uint32_t mine = tm + ((uint32_t)(32 * quarter) << 16);
+  int n = 0;
+  for (;;) {
+    const int live = cur.tile_rows();
+    RowAt at{0, 0, 0, 0x7FFFFFFF};
+    if (row < live) at = cur.row(row, hq);
+    float rs;
+    {
+      // q: this thread's dimensions of its row
+      const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + part * HD;
+      float x[HD];
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < HD / 4; ++i) {
+        const float4 v = row < live ? __ldg(reinterpret_cast<const float4*>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
+        x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
+      }
+#pragma unroll
+      for (int i = 0; i < HD; ++i) m = fmaxf(m, fabsf(x[i]));
+      top[part * 128 + row] = m;
+      meet_pair(quarter);
+      m = fmaxf(m, top[(part ^ 1) * 128 + row]);
+      // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
+      // keep their bits whatever q's size
+      const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
+      const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
+      rs = __uint_as_float((uint32_t)(ex - 10) << 23);
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j) {
+        uint32_t w[PARTS][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x0 = x[8 * j + 2 * i] * inv, x1 = x[8 * j + 2 * i + 1] * inv;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) w[p][i] = Parts<T>::take(x0, x1);
+        }
+        const int piece = part * (HD / 8) + j;  // of the row
+        uint8_t* dst = smem + S::q + (piece >> 3) * S::slab + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+          *reinterpret_cast<uint4*>(dst + p * S::tile) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+      }
+    }
+    fence_proxy_async_smem();  // q is the first product's operand
+    __syncwarp();
+    if (lane == 0) arrive(queries);
+    // what the tile's rows see in common, and at all
+    int all_lo, all_hi, any_lo, any_hi;
+    {
+      int* lim = reinterpret_cast<int*>(top) + 2 * 128;  // [8 warps][4]
+      int a = at.lo, b = at.hi, c = row < live ? at.lo : 0x7FFFFFFF, d = row < live ? at.hi : -1;
+      a = __reduce_max_sync(0xFFFFFFFFu, a);
+      b = __reduce_min_sync(0xFFFFFFFFu, b);
+      c = __reduce_min_sync(0xFFFFFFFFu, c);
+      d = __reduce_max_sync(0xFFFFFFFFu, d);
+      if (lane == 0) *reinterpret_cast<int4*>(lim + 4 * warp) = make_int4(a, b, c, d);
+      meet();
+      all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = -1;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int4 v = *reinterpret_cast<const int4*>(lim + 4 * w);
+        all_lo = max(all_lo, v.x), all_hi = min(all_hi, v.y), any_lo = min(any_lo, v.z), any_hi = max(any_hi, v.w);
+      }
+      meet();
+    }
+
+    float acc[HD];
+#pragma unroll
+    for (int i = 0; i < HD; ++i) acc[i] = 0.0f;
+    float minus = kNoRef, l = 0.0f;
+    // adds the output of page m, its products being over
+    const auto drain = [&](int m) {
+      if (!mbar_wait(output, m & 1)) g_err_attention_shared_tc = 1u;
+      __syncwarp();
+      fence_after();
+#pragma unroll
+      for (int x = 0; x < HD / 32; ++x) {
+        float o[32];
+        tm_ld32(mine + S::o_col + part * HD + 32 * x, o);
+        tm_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[32 * x + i] += o[i];
+      }
+      fence_before();
+    };
+    for (int i = cur.i; i < cur.i_end; ++i, ++n) {
+      const int key0 = cur.block(i, 0) * kPgKeys;
+      const bool whole = key0 >= all_lo && key0 + kPgKeys - 1 <= all_hi;
+      const uint32_t s_at = mine + S::s_col + 128 * (n & 1) + 64 * part;
+      if (!mbar_wait(&scores[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+      __syncwarp();
+      fence_after();
+      float x[64];
+      tm_ld32(s_at, x);
+      tm_ld32(s_at + 32, x + 32);
+      tm_ld_wait();
+      if (!whole) {
+        const int from = at.lo - (key0 + 64 * part), upto = at.hi - (key0 + 64 * part);
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (k < from || k > upto) x[k] = -INFINITY;
+      }
+      float most = x[0];
+#pragma unroll
+      for (int k = 1; k < 64; ++k) most = fmaxf(most, x[k]);
+      float* mx = top + (n & 1) * 256;
+      mx[part * 128 + row] = most;
+      meet_pair(quarter);
+      most = fmaxf(most, mx[(part ^ 1) * 128 + row]) * rs;
+      float f = 1.0f;
+      if (most + minus > kRoom + kSlack) {
+        const float to_minus = kRoom - most;
+        f = exp2_of(to_minus - minus);
+        minus = to_minus;
+        l *= f;
+      }
+      // weights; a hidden key's score is -inf here, its weight 0 whatever rs and minus are
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[PARTS][16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float p0 = exp2_of(fmaf(x[32 * c + 2 * k], rs, minus)), p1 = exp2_of(fmaf(x[32 * c + 2 * k + 1], rs, minus));
+          l += p0 + p1;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) w[p][k] = Parts<T>::take(p0, p1);
+        }
+        tm_st16(s_at + 16 * c, w[0]);
+        tm_st16(s_at + 32 + 16 * c, w[1]);
+        if constexpr (PARTS > 2) tm_st16(mine + S::t_col + 64 * (n & 1) + 32 * part + 16 * c, w[PARTS - 1]);
+      }
+      tm_st_wait();
+      bool any_strange = false;
+      if (!whole) {
+        // Two threads to a key of V.  One that no row sees may hold anything: cleared.  One
+        // that some rows see, with an infinity or a NaN: 0 times it is no 0, so it is
+        // cleared too, and added to the rows that see it.
+        if (!mbar_wait(&full_v[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+        const int key = tid >> 1, half = tid & 1;
+        const bool none = key0 + key > any_hi || key0 + key < any_lo;
+        bool is = false;
+        uint4* vrow = reinterpret_cast<uint4*>(smem + S::v + (n & 1) * S::tile + (D == 128 ? half * S::slab : half * 64) + key * 128);
+        // (64-wide heads: a thread's half of the row is four pieces; the swizzle only
+        // permutes the pieces of a row)
+        for (int p = 0; p < D / 16; ++p) {
+          const uint4 v = vrow[p];
+          is = is || odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w);
+        }
+        is = __shfl_xor_sync(0xFFFFFFFFu, (int)is, 1) || is;
+        if (none || is)
+          for (int p = 0; p < D / 16; ++p) vrow[p] = make_uint4(0, 0, 0, 0);
+        is = is && !none;
+        if (tid < 4) strange[tid] = 0;
+        fence_before();
+        any_strange = meet_or(is);
+        if (any_strange) {
+          fence_after();  // the other half's weights are read below
+          if (is && half == 0) atomicOr(&strange[key >> 5], 1u << (key & 31));
+          meet();
+        }
+        fence_proxy_async_smem();
+      }
+      if (i > cur.i) drain(n - 1);
+      if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+#pragma unroll
+        for (int k = 0; k < HD; ++k) acc[k] *= f;
+      }
+      if (any_strange) {
+        const T* page = vp + ((size_t)cur.page(i) * hkv + cur.h) * kPgKeys * D + part * HD;
+        for (int w = 0; w < 4; ++w)
+          for (unsigned left = strange[w]; left; left &= left - 1) {
+            const int key = 32 * w + __ffs(left) - 1;
+            const uint32_t hi_at = mine + S::s_col + 128 * (n & 1) + 64 * (key >> 6) + (key & 63) / 2;
+            // the weight's parts, the smallest first
+            uint32_t got[3] = {tm_ld1(hi_at), tm_ld1(hi_at + 32), 0};
+            if constexpr (PARTS > 2) got[2] = tm_ld1(mine + S::t_col + 64 * (n & 1) + key / 2);
+            tm_ld_wait();
+            const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
+            if (key0 + key >= at.lo && key0 + key <= at.hi) {
+              const T* v = page + (size_t)key * D;
+#pragma unroll
+              for (int k = 0; k < HD; ++k) {
+                const uint32_t bits = *reinterpret_cast<const uint16_t*>(v + k);
+                acc[k] = fmaf(p, half_of<T>(bits, 0), acc[k]);
+              }
+            }
+          }
+        meet();  // the flags have been read
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(weights);
+    }
+    drain(n - 1);
+
+    // ---- the part's end
+    top[part * 128 + row] = l;
+    meet();
+    l += top[(part ^ 1) * 128 + row];
+    if (row < live) {
+      const int cap = cur.slot_cap();
+      float2* stat = to.stat + (size_t)at.row * to.slots + cur.slot_base();
+      float* dst;
+      if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
+        dst = to.out + (size_t)at.row * D;
+#pragma unroll
+        for (int k = 0; k < HD; ++k) acc[k] = __fdiv_rn(acc[k], l);
+        if (cap > 1 && part == 0) stat[0] = make_float2(0.0f, -1.0f);
+      } else {
+        const int p = cur.part(cta, ctas);
+        dst = to.acc + ((size_t)at.row * to.slots + cur.slot_base() + p) * D;
+        if (part == 0) {
+          stat[p] = make_float2(-minus, l);
+          if (p == 0)
+            for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < HD / 4; ++k)
+        reinterpret_cast<float4*>(dst + part * HD)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+    }
+    meet();  // the sums have been read
+    if (!cur.another()) break;
+    cur.next();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  }
+}
+
+template <int D, typename T>
+cudaError_t tc_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st) {
+  using S = Smem<D, T>;
+  static_assert(S::bytes <= 227 * 1024, "shared memory");
+  CUtensorMap tmk, tmv;
+  cudaError_t e = kv_tensor_map(a.k, a.pool_rows, D, std::is_same_v<T, __half> ? 0 : 1, kPgKeys, &tmk);
+  if (e == cudaSuccess) e = kv_tensor_map(a.v, a.pool_rows, D, std::is_same_v<T, __half> ? 0 : 1, kPgKeys, &tmv);
+  if (e != cudaSuccess) return e;
+  return with_words(meta, [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    auto kern = attention_shared_tc_kernel<D, T, N>;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
+    if (err != cudaSuccess) return err;
+    ParamWords<N> w;
+    fill_words(meta, &w);
+    const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
+    return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)S::bytes, st, tmk, tmv, a.q, a.q_stride,
+                         a.hq, a.hkv, static_cast<const T*>(a.v), a.n_seg,
+                         (float)(1.4426950408889634 / std::sqrt((double)D)), to, w, meta.dev);
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_attention_shared_tc(const PageAttnArgs& a, int dtype, int head_dim, const MetaArg& meta,
+                                       cudaStream_t st) {
+  if (head_dim == 128) return dtype == 0 ? tc_go<128, __half>(a, meta, st) : tc_go<128, __nv_bfloat16>(a, meta, st);
+  return dtype == 0 ? tc_go<64, __half>(a, meta, st) : tc_go<64, __nv_bfloat16>(a, meta, st);
+}
+
+unsigned int read_clear_error_attention_shared_tc() {
+  unsigned int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_attention_shared_tc, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  cudaMemcpyToSymbol(g_err_attention_shared_tc, &z, sizeof z);
+  return v;
+}
+
+}  // namespace dsbk

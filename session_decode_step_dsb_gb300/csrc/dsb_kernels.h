@@ -365,10 +365,15 @@ cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, co
 
 // A plan's metadata: n_seg segments of kSharedSegWords (pages of work before it, rows on a
 // kv head, where its sequences are and how many, block of its first page, pages, where they
-// are, first slot, slots, first and last key that any row sees, slots of its rows in all);
-// the pages of work; sequences of kSharedMemWords (first row, first token, new tokens,
-// length, window); pages.
-constexpr int kSharedSegWords = 12, kSharedMemWords = 5;
+// are, first slot, slots, first and last key that any row sees, slots of its rows in all,
+// where its tiles are or 0); the pages of work; sequences of kSharedMemWords (first row,
+// first token, new tokens, length, window); pages; and where tiles of rows see only some of the
+// segment's pages, (pages of the tiles before it, first page) of each tile and the pages of
+// all.
+constexpr int kSharedSegWords = 13, kSharedMemWords = 5;
+// Query rows of a tile of a segment with `rows` of them on a kv head: 8 of the warp-level
+// kernel (attention_shared.cu) or 128 of the tcgen05 one (attention_shared_tc.cu).
+inline int shared_tile_rows(int rows) { return rows > 16 ? 128 : 8; }
 struct PageAttnArgs {
   const float* q;
   long long q_stride;
@@ -390,6 +395,10 @@ struct PageAttnArgs {
 int page_attn_resident(int sms);
 cudaError_t launch_attention_pages(const PageAttnArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
 unsigned int read_clear_error_attention_pages();
+// Tiles of 128 rows; one CTA an SM.
+cudaError_t launch_attention_shared_tc(const PageAttnArgs& a, int dtype, int head_dim, const MetaArg& meta,
+                                       cudaStream_t st);
+unsigned int read_clear_error_attention_shared_tc();
 // Metadata (always in the parameters): of each sequence its first token and its rows'
 // slots (0: nothing to join).
 cudaError_t launch_attention_join(const PageAttnArgs& a, int n_seq, int head_dim, const MetaArg& meta, cudaStream_t st);

@@ -120,6 +120,11 @@ struct Segment {
   int b0, n;      // first block, pages
   int rows = 0;   // query rows on a kv head
   int slot0 = 0, cap = 0;
+  std::vector<int32_t> table;  // of its tiles, where they see only some of its pages
+
+  int tile() const { return dsbk::shared_tile_rows(rows); }
+  int tiles() const { return (rows + tile() - 1) / tile(); }
+  long long pages_a_head() const { return table.empty() ? (long long)tiles() * n : table.back(); }
 };
 
 struct Tree {
@@ -140,21 +145,44 @@ struct Tree {
     for (int m = m0; m < m1; ++m) r += G * b->new_tokens[order[m]];
     return r;
   }
-  static int tiles(int rows) { return (rows + 7) / 8; }
+  // What a page costs a segment of so many rows: tiles of 8, one of 128 as 2.5 of them.
+  static int cost(int rows) {
+    const int tile = dsbk::shared_tile_rows(rows);
+    return (rows + tile - 1) / tile * (tile == 8 ? 2 : 5);
+  }
 
-  // Whether pages that m1 - m0 sequences have in common are worth a segment: where it has
-  // fewer tiles to take them through than the sequences have apart.
+  // Whether pages that m1 - m0 sequences have in common are worth a segment.
   bool worth(int m0, int m1, int n) const {
     int apart = 0;
-    for (int m = m0; m < m1; ++m) apart += tiles(G * b->new_tokens[order[m]]);
-    return n > 0 && tiles(rows_of(m0, m1)) < apart;
+    for (int m = m0; m < m1; ++m) apart += cost(G * b->new_tokens[order[m]]);
+    return n > 0 && cost(rows_of(m0, m1)) < apart;
+  }
+
+  // Pages that each tile of a sequence's rows sees of its segment, where that is not all:
+  // (pages of the tiles before, first page) of each, and the pages of all.
+  void cut_tiles(Segment* g) const {
+    const int s = order[g->m0], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
+    int sum = 0;
+    bool cut = false;
+    for (int r = 0; r < g->rows; r += g->tile()) {
+      const int lo = len - n + r / G, hi = len - n + (std::min(r + g->tile(), g->rows) - 1) / G;
+      const int from = w > 0 ? std::max(0, lo - w + 1) / DSB_KV_PAGE : 0;
+      int a = std::max(from - g->b0, 0), z = std::min(hi / DSB_KV_PAGE - g->b0, g->n - 1);
+      if (a > z) a = z = 0;  // none of them: one page, all hidden
+      g->table.insert(g->table.end(), {sum, a});
+      sum += z - a + 1;
+      cut = cut || z - a + 1 < g->n;
+    }
+    g->table.push_back(sum);
+    if (!cut) g->table.clear();
   }
 
   int add(int parent, int m0, int m1, int b0, int b1) {
     // a segment's metadata has to fit a launch
     for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {
-      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0)};
+      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0), 0, 0, 0, {}};
       s.rows = rows_of(m0, m1);
+      if (m1 - m0 == 1 && s.tiles() > 1) cut_tiles(&s);
       parent = (int)segs.size();
       segs.push_back(s);
     }
@@ -222,8 +250,9 @@ int most_parts(int n, long long share) {
   return n == 1 ? 1 : (int)std::min<long long>(n, (n - 2) / share + 2);
 }
 
-// Segments of one launch.
+// Segments of one launch, all of one height of tiles.
 struct Launch {
+  int tile;
   std::vector<int> segs;
   size_t n_words = 1;
   long long work = 0;
@@ -346,7 +375,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
     const auto words_of = [&](const Segment& g) {
-      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords + g.n;
+      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords + g.n + g.table.size();
     };
 
     // launches: what a captured call keeps has to ride in its parameters
@@ -360,32 +389,37 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
       if (cap != cudaStreamCaptureStatusNone) room = dsbk::kParamWords;
     }
     std::vector<Launch> launches;
-    for (size_t i = 0; i < tree.segs.size(); ++i) {
-      const Segment& g = tree.segs[i];
-      const size_t n = words_of(g);
-      if (1 + n > room)
-        return fail(DSB_ERR_UNSUPPORTED, "a captured call holds at most %d words of metadata for pages of %d sequences", dsbk::kParamWords,
-                    g.m1 - g.m0);
-      const long long work = (long long)hkv * Tree::tiles(g.rows) * g.n;
-      if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
-      if (launches.empty() || launches.back().n_words + n > room || launches.back().work + work > INT_MAX / 2)
-        launches.emplace_back();
-      launches.back().segs.push_back((int)i);
-      launches.back().n_words += n;
-      launches.back().work += work;
+    for (const int tile : {128, 8}) {
+      bool open = false;
+      for (size_t i = 0; i < tree.segs.size(); ++i) {
+        const Segment& g = tree.segs[i];
+        if (g.tile() != tile) continue;
+        const size_t n = words_of(g);
+        if (1 + n > room)
+          return fail(DSB_ERR_UNSUPPORTED, "a call holds at most %zu words of metadata for the pages of %d sequences", room,
+                      g.m1 - g.m0);
+        const long long work = hkv * g.pages_a_head();
+        if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+        if (!open || launches.back().n_words + n > room || launches.back().work + work > INT_MAX / 2) {
+          launches.emplace_back();
+          launches.back().tile = tile;
+          open = true;
+        }
+        launches.back().segs.push_back((int)i);
+        launches.back().n_words += n;
+        launches.back().work += work;
+      }
     }
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
-    const int resident = dsbk::page_attn_resident(dev.sms);
     int slots = 0;
     for (Launch& l : launches) {
-      l.ctas = (int)std::min<long long>(resident, l.work);
-      for (int i : l.segs) {
-        Segment& g = tree.segs[i];
-        g.cap = most_parts(g.n, l.work / l.ctas);
-        if (g.parent >= 0) g.slot0 = tree.segs[g.parent].slot0 + tree.segs[g.parent].cap;
-        slots = std::max(slots, g.slot0 + g.cap);
-      }
+      l.ctas = (int)std::min<long long>(l.tile == 8 ? dsbk::page_attn_resident(dev.sms) : dev.sms, l.work);
+      for (int i : l.segs) tree.segs[i].cap = most_parts(tree.segs[i].n, l.work / l.ctas);
+    }
+    for (Segment& g : tree.segs) {  // a parent comes before its children
+      if (g.parent >= 0) g.slot0 = tree.segs[g.parent].slot0 + tree.segs[g.parent].cap;
+      slots = std::max(slots, g.slot0 + g.cap);
     }
     const auto slots_of = [&](int s) { return tree.segs[tree.end[s]].slot0 + tree.segs[tree.end[s]].cap; };
     const size_t rows = (size_t)n_tok * n_q_heads;
@@ -425,17 +459,20 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         }
         const int pg_at = (int)words.size();
         for (int p = 0; p < g.n; ++p) words.push_back(page_of(b, tree.order[g.m0], g.b0 + p));
+        const int table_at = g.table.empty() ? 0 : (int)words.size();
+        words.insert(words.end(), g.table.begin(), g.table.end());
         const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.m1 - g.m0, g.b0, g.n, pg_at,
-                                                    g.slot0,       g.cap,  first,  last,        most};
+                                                    g.slot0,       g.cap,  first,  last,        most, table_at};
         std::copy(rec, rec + dsbk::kSharedSegWords, words.begin() + i * dsbk::kSharedSegWords);
-        work += (long long)hkv * Tree::tiles(g.rows) * g.n;
+        work += hkv * g.pages_a_head();
       }
       words[l.segs.size() * dsbk::kSharedSegWords] = (int32_t)work;
       dsbk::MetaArg meta;
       if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
       a.n_seg = (int)l.segs.size();
       a.ctas = l.ctas;
-      const cudaError_t e = dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
+      const cudaError_t e = l.tile == 8 ? dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs)
+                                        : dsbk::launch_attention_shared_tc(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
       if (e != cudaSuccess) return cuda_fail(e, "attention_decode_shared launch");
     }
     // the join, where a row's sums lie in parts
@@ -578,7 +615,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
     if ((st = device_info(&dev)) != DSB_OK) return st;
     std::vector<SelLaunch> launches;
     if ((st = selection_launches(b, cs, &launches)) != DSB_OK) return st;
-    const int tiles = Tree::tiles(n_q_heads / hkv), resident = dsbk::page_attn_resident(dev.sms);
+    const int tiles = (n_q_heads / hkv + 7) / 8, resident = dsbk::page_attn_resident(dev.sms);
     std::vector<dsbk::PageAttnArgs> args;
     for (const SelLaunch& l : launches) {
       dsbk::PageAttnArgs a = {};
