@@ -5,15 +5,15 @@
 // A CTA takes 128 query rows of a kv head through its share of pages, 128 keys at a time:
 //   S = Q K^T   128 x 128, Q in parts (fp16: two; bf16: three, so that a product keeps
 //               float32's bits) in shared memory, K as it lies in the page
-//   P           a thread has half of a row's scores; weights go back to tensor memory in
-//               as many parts, the first two over the scores that they come from
-//   O = P V     128 x D of one page, V as it lies in the page; added to float32 registers
-//               by the threads (the tensor core's sums round toward zero)
-// The scores of the next page are multiplied while the weights of this one are made, so
-// that the tensor core works without a pause: S(n + 1) lies between P V(n - 1) and P V(n).
-// A warp of its own asks for the pages (TMA, two of K and two of V) and issues the
-// products.  Bound by the products: 32 (fp16) or 48 (bf16) of 128 x 128 x 16 for a page
-// of 128-wide heads.
+//   P           256 threads, two to a row; weights go back to tensor memory in as many
+//               parts, the first two over the scores that they come from
+//   O = P V     128 x D of one page, V as it lies in the page; 128 more threads, one to
+//               a row, add it to float32 registers (the tensor core's sums round toward
+//               zero) and write the row at the end, while the others begin the next
+// The scores of the next page are multiplied while the weights of this one are made:
+// S(n + 1) lies between P V(n - 1) and P V(n).  A warp of its own asks for the pages (TMA,
+// two of K and two of V) and issues the products.  Bound by the products: 32 (fp16) or 48
+// (bf16) of 128 x 128 x 16 for a page of 128-wide heads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,12 +31,12 @@ namespace dsbk {
 
 namespace {
 
-constexpr int kWorkers = 256;
-constexpr int kThreads = kWorkers + 128;  // and a warpgroup whose first thread asks and issues
-// Registers of a thread: the launch gives each 168; the issuing warpgroup leaves some to
-// the workers, 256 x 192 + 128 x 120 = 384 x 168.
-constexpr int kWorkerRegs = 192, kIssuerRegs = 120;
-static_assert(kWorkers * kWorkerRegs + 128 * kIssuerRegs <= kThreads * 168, "register split");
+// Threads that make weights, that add up the output, and a warpgroup whose first warp asks
+// and issues; and the registers of each (the launch gives every thread 128).
+constexpr int kWeighers = 256, kAdders = 128, kIssuers = 128;
+constexpr int kThreads = kWeighers + kAdders + kIssuers;
+constexpr int kWeigherRegs = 120, kAdderRegs = 192, kIssuerRegs = 80;
+static_assert(kWeighers * kWeigherRegs + kAdders * kAdderRegs + kIssuers * kIssuerRegs <= kThreads * 128, "register split");
 constexpr int kRows = 128;
 
 __device__ unsigned int g_err_attention_shared_tc = 0;
@@ -56,17 +56,26 @@ __device__ __forceinline__ uint32_t idesc(int n, bool trans_b) {
   const uint32_t type = std::is_same_v<T, __half> ? 0u : 1u;
   return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)trans_b << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// The products are issued by a warp whose lanes stay together (the operands' descriptors
+// then live in its uniform registers); `one` is true in one of them.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc), "r"(one)
       : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -93,21 +102,27 @@ __device__ __forceinline__ void tm_ld32(uint32_t at, float* v) {
       : "r"(at)
       : "memory");
 }
+__device__ __forceinline__ void tm_ld16(uint32_t at, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(at)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t tm_ld1(uint32_t at) {
   uint32_t v;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
+__device__ __forceinline__ void tm_st8(uint32_t at, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The two warps that share 32 rows; all workers; the latter telling whether any passed true.
+// The two weighing warps of 32 rows; all of them; the latter telling whether any passed true.
 __device__ __forceinline__ void meet_pair(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 __device__ __forceinline__ bool meet_or(bool x) {
@@ -137,15 +152,17 @@ __device__ __forceinline__ bool odd(uint32_t w) {  // an infinity or a NaN in a 
 template <int D, typename T>
 struct Smem {
   static constexpr int parts = Parts<T>::kMore + 1;
-  static constexpr int slab = 128 * 128;            // 64 columns of 128 rows
-  static constexpr int tile = D / 64 * slab;        // a part of Q, a page of K or V
+  static constexpr int slab = 128 * 128;                // 64 columns of 128 rows
+  static constexpr int tile = D / 64 * slab;            // a part of Q, a page of K or V
   static constexpr int q = 0;
-  static constexpr int k = q + parts * tile;        // two pages
-  static constexpr int v = k + 2 * tile;            // two pages
-  static constexpr int top = v + 2 * tile;          // [2][2][128] row maxima, sums
-  static constexpr int strange = top + 2 * 2 * 128 * 4;  // [4] words: keys
-  static constexpr int bars = strange + 16;         // K, V [2], scores [2], output, weights, queries
-  static constexpr int base = bars + 9 * 8;
+  static constexpr int k = q + parts * tile;            // two pages
+  static constexpr int v = k + 2 * tile;                // two pages
+  static constexpr int top = v + 2 * tile;              // [2][128] row maxima of the halves; limits of rows
+  static constexpr int stat = top + 2 * 128 * 4;        // [128] -reference, sum of weights
+  static constexpr int fac = stat + 128 * 8;            // [3][128] of a page: the sums before it times 2^-fac
+  static constexpr int strange = fac + 3 * 128;         // [3] of a page: keys (4 words), whether any
+  static constexpr int bars = strange + 64;             // see below
+  static constexpr int base = bars + 12 * 8;
   static constexpr int bytes = base + 8;
   // tensor memory: scores and weights of two pages, output, third parts of two pages
   static constexpr int s_col = 0, o_col = 256, t_col = 384;
@@ -157,20 +174,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, float scale_log2e, PartialsOut to,
     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using S = Smem<D, T>;
-  constexpr int PARTS = S::parts, HD = D / 2;  // dimensions of a thread
+  constexpr int PARTS = S::parts, HD = D / 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* top = reinterpret_cast<float*>(smem + S::top);
+  float2* stats = reinterpret_cast<float2*>(smem + S::stat);
+  uint8_t* fac = smem + S::fac;
   unsigned* strange = reinterpret_cast<unsigned*>(smem + S::strange);
+  // pages of K and of V; scores of a page; its output; its weights (by the weighers' warps);
+  // the output has been added (the adders'); a run's queries, its statistics (weighers), and
+  // these have been read (adders)
   uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::bars);
-  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *output = scores + 2, *weights = output + 1, *queries = weights + 1;
+  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *output = scores + 2, *weights = output + 1, *added = weights + 1,
+           *queries = added + 1, *stat_full = queries + 1, *stat_free = stat_full + 1;
   uint32_t* base = reinterpret_cast<uint32_t*>(smem + S::base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
     for (int i = 0; i < 7; ++i) mbar_init(&full_k[i], 1);
-    mbar_init(weights, kWorkers / 32);
-    mbar_init(queries, kWorkers / 32);
+    mbar_init(weights, kWeighers / 32);
+    mbar_init(added, kAdders / 32);
+    mbar_init(queries, kWeighers / 32);
+    mbar_init(stat_full, kWeighers / 32);
+    mbar_init(stat_free, kAdders / 32);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -185,22 +211,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   pdl_trigger();
   SharedWalk cur;
   cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
+  const auto wait = [](uint64_t* bar, int parity) {
+    if (!mbar_wait(bar, (uint32_t)parity)) g_err_attention_shared_tc = 1u;
+  };
 
-  if (warp >= kWorkers / 32) {
-    // ---- the asking and issuing thread; n counts the pages of all its runs
+  if (warp >= (kWeighers + kAdders) / 32) {
+    // ---- the asking and issuing warp; n counts the pages of all its runs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
-    if (tid == kWorkers) {
+    if (warp == (kWeighers + kAdders) / 32) {
+      const uint32_t one = elect();
       SharedWalk ahead = cur;  // of K; V follows one page later
       int ek = ahead.i, asked_k = 0, asked_v = 0;
-      int at_row[4];           // rows of the pages asked for in K, until V is
+      int row_a = 0, row_b = 0;  // rows of the last page asked for in K, and of the one before
       bool more = true;
       const auto ask_k = [&]() {
         if (!more) return;
         const int row0 = (ahead.page(ek) * hkv + ahead.h) * kPgKeys, b = asked_k & 1;
-        at_row[asked_k & 3] = row0;
-        mbar_arrive_expect_tx(&full_k[b], S::tile);
+        row_b = row_a;
+        row_a = row0;
+        if (one) {
+          mbar_arrive_expect_tx(&full_k[b], S::tile);
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) tma_box(smem + S::k + b * S::tile + x * S::slab, &tmk, 64 * x, row0, &full_k[b]);
+          for (int x = 0; x < D / 64; ++x) tma_box(smem + S::k + b * S::tile + x * S::slab, &tmk, 64 * x, row0, &full_k[b]);
+        }
+        __syncwarp();
         ++asked_k;
         if (++ek == ahead.i_end) {
           if (ahead.another()) {
@@ -213,10 +247,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       };
       const auto ask_v = [&]() {
         if (asked_v == asked_k) return;
-        const int row0 = at_row[asked_v & 3], b = asked_v & 1;
-        mbar_arrive_expect_tx(&full_v[b], S::tile);
+        const int row0 = asked_k - asked_v == 1 ? row_a : row_b, b = asked_v & 1;
+        if (one) {
+          mbar_arrive_expect_tx(&full_v[b], S::tile);
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) tma_box(smem + S::v + b * S::tile + x * S::slab, &tmv, 64 * x, row0, &full_v[b]);
+          for (int x = 0; x < D / 64; ++x) tma_box(smem + S::v + b * S::tile + x * S::slab, &tmv, 64 * x, row0, &full_v[b]);
+        }
+        __syncwarp();
         ++asked_v;
       };
       ask_k();
@@ -225,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       const uint32_t id_s = idesc<T>(128, false), id_o = idesc<T>(D, true);
       const uint32_t sq = smem_addr(smem + S::q), sk = smem_addr(smem + S::k), sv = smem_addr(smem + S::v);
       const auto score = [&](int n) {
-        if (!mbar_wait(&full_k[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+        wait(&full_k[n & 1], n >> 1 & 1);
         fence_after();
         const uint64_t kd = desc(sk + (n & 1) * S::tile, 0, 1024);
 #pragma unroll
@@ -234,25 +271,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint64_t step = (uint64_t)((k >> 2) * (S::slab >> 4) + (k & 3) * 2);
-            mma_ss(tm + S::s_col + 128 * (n & 1), qd + step, kd + step, id_s, part < PARTS - 1 || k > 0);
+            mma_ss(tm + S::s_col + 128 * (n & 1), qd + step, kd + step, id_s, part < PARTS - 1 || k > 0, one);
           }
         }
-        commit(&scores[n & 1]);
+        if (one) commit(&scores[n & 1]);
+        __syncwarp();
       };
       int n = 0;
       for (int run = 0;; ++run) {
-        if (!mbar_wait(queries, run & 1)) g_err_attention_shared_tc = 1u;
+        wait(queries, run & 1);
         fence_after();
         score(n);
         for (int i = cur.i; i < cur.i_end; ++i, ++n) {
           // K's place is free once the scores are there
-          if (!mbar_wait(&scores[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+          wait(&scores[n & 1], n >> 1 & 1);
           ask_k();
-          if (i + 1 < cur.i_end) score(n + 1);
-          // the weights are there, and the last output has been read, so V's other place is free
-          if (!mbar_wait(weights, n & 1)) g_err_attention_shared_tc = 1u;
+          if (i + 1 < cur.i_end) {
+            // the next scores take the place of the last weights, which a page of strange values
+            // (see below) needs until it has been added
+            if (n > 0 && strange[5 * ((n - 1) % 3) + 4]) wait(added, (n - 1) & 1);
+            score(n + 1);
+          }
+          wait(weights, n & 1);
+          if (n > 0) wait(added, (n - 1) & 1);  // so is V's other place, and the output's
           ask_v();
-          if (!mbar_wait(&full_v[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+          wait(&full_v[n & 1], n >> 1 & 1);
           fence_after();
           const uint64_t vd = desc(sv + (n & 1) * S::tile, S::slab, 1024);
 #pragma unroll
@@ -261,10 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
             for (int k = 0; k < 8; ++k) {
               const uint32_t a = part == 2 ? tm + S::t_col + 64 * (n & 1) + 8 * k
                                            : tm + S::s_col + 128 * (n & 1) + 64 * (k >> 2) + 32 * part + 8 * (k & 3);
-              mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0);
+              mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0, one);
             }
           }
-          commit(output);
+          if (one) commit(output);
+          __syncwarp();
         }
         if (!cur.another()) break;
         cur.next();
@@ -275,18 +319,112 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     return;
   }
 
-  // ---- workers: thread (row, part) has the row's keys and dimensions of one half
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWorkerRegs));
-  const int quarter = warp & 3, part = warp >> 2, row = 32 * quarter + lane;
+  const int quarter = warp & 3, row = 32 * quarter + lane;
   const uint32_t mine = tm + ((uint32_t)(32 * quarter) << 16);
   int n = 0;
-  for (;;) {
+
+  if (warp >= kWeighers / 32) {
+    // ---- the adders: a thread has a row's output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
+    for (int run = 0;; ++run) {
+      const int live = cur.tile_rows();
+      RowAt at{0, 0, 0, 0x7FFFFFFF};
+      if (row < live) at = cur.row(row, hq);
+      float acc[D];
+#pragma unroll
+      for (int i = 0; i < D; ++i) acc[i] = 0.0f;
+      for (int i = cur.i; i < cur.i_end; ++i, ++n) {
+        wait(output, n & 1);
+        __syncwarp();
+        fence_after();
+        const int down = fac[128 * (n % 3) + row];
+        const float f = down > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - down) << 23);
+        if (__any_sync(0xFFFFFFFFu, down)) {
+#pragma unroll
+          for (int k = 0; k < D; ++k) acc[k] *= f;
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          float o[16];
+          tm_ld16(mine + S::o_col + 16 * x, o);
+          tm_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) acc[16 * x + k] += o[k];
+        }
+        const unsigned* odd_keys = strange + 5 * (n % 3);
+        if (odd_keys[4]) {
+          const int key0 = cur.block(i, 0) * kPgKeys;
+          const T* page = vp + ((size_t)cur.page(i) * hkv + cur.h) * kPgKeys * D;
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+            for (unsigned left = odd_keys[w]; left; left &= left - 1) {
+              const int key = 32 * w + __ffs(left) - 1;
+              const uint32_t hi_at = mine + S::s_col + 128 * (n & 1) + 64 * (key >> 6) + (key & 63) / 2;
+              // the weight's parts, the smallest first
+              uint32_t got[3] = {tm_ld1(hi_at), tm_ld1(hi_at + 32), 0};
+              if constexpr (PARTS > 2) got[2] = tm_ld1(mine + S::t_col + 64 * (n & 1) + key / 2);
+              tm_ld_wait();
+              const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
+              if (key0 + key < at.lo || key0 + key > at.hi) continue;
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(page + (size_t)key * D);
+#pragma unroll
+              for (int k = 0; k < D / 2; ++k) {
+                const uint32_t two = v[k];
+                acc[2 * k] = fmaf(p, half_of<T>(two, 0), acc[2 * k]);
+                acc[2 * k + 1] = fmaf(p, half_of<T>(two, 1), acc[2 * k + 1]);
+              }
+            }
+          __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(added);
+      }
+      // ---- the part's end
+      wait(stat_full, run & 1);
+      const float2 st = stats[row];
+      __syncwarp();
+      if (lane == 0) arrive(stat_free);
+      if (row < live) {
+        const int cap = cur.slot_cap();
+        float2* stat = to.stat + (size_t)at.row * to.slots + cur.slot_base();
+        float* dst;
+        if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
+          dst = to.out + (size_t)at.row * D;
+#pragma unroll
+          for (int k = 0; k < D; ++k) acc[k] = __fdiv_rn(acc[k], st.y);
+          if (cap > 1) stat[0] = make_float2(0.0f, -1.0f);
+        } else {
+          const int p = cur.part(cta, ctas);
+          dst = to.acc + ((size_t)at.row * to.slots + cur.slot_base() + p) * D;
+          stat[p] = make_float2(-st.x, st.y);
+          if (p == 0)
+            for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k)
+          reinterpret_cast<float4*>(dst)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+      }
+      __syncwarp();
+      if (!cur.another()) break;
+      cur.next();
+    }
+    fence_before();
+    __syncthreads();
+    return;
+  }
+
+  // ---- the weighers: thread (row, part) has half of the row's keys
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
+  const int part = warp >> 2;
+  for (int run = 0;; ++run) {
     const int live = cur.tile_rows();
     RowAt at{0, 0, 0, 0x7FFFFFFF};
     if (row < live) at = cur.row(row, hq);
     float rs;
     {
-      // q: this thread's dimensions of its row
+      // q: half of the row's dimensions
       const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + part * HD;
       float x[HD];
       float m = 0.0f;
@@ -326,17 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     __syncwarp();
     if (lane == 0) arrive(queries);
     // what the tile's rows see in common, and at all
-    int all_lo, all_hi, any_lo, any_hi;
+    int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = -1;
     {
-      int* lim = reinterpret_cast<int*>(top) + 2 * 128;  // [8 warps][4]
-      int a = at.lo, b = at.hi, c = row < live ? at.lo : 0x7FFFFFFF, d = row < live ? at.hi : -1;
-      a = __reduce_max_sync(0xFFFFFFFFu, a);
-      b = __reduce_min_sync(0xFFFFFFFFu, b);
-      c = __reduce_min_sync(0xFFFFFFFFu, c);
-      d = __reduce_max_sync(0xFFFFFFFFu, d);
-      if (lane == 0) *reinterpret_cast<int4*>(lim + 4 * warp) = make_int4(a, b, c, d);
+      int* lim = reinterpret_cast<int*>(top);  // [4 quarters][4]
+      const int a = __reduce_max_sync(0xFFFFFFFFu, at.lo), b = __reduce_min_sync(0xFFFFFFFFu, at.hi);
+      const int c = __reduce_min_sync(0xFFFFFFFFu, row < live ? at.lo : 0x7FFFFFFF);
+      const int d = __reduce_max_sync(0xFFFFFFFFu, row < live ? at.hi : -1);
       meet();
-      all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = -1;
+      if (lane == 0 && part == 0) *reinterpret_cast<int4*>(lim + 4 * warp) = make_int4(a, b, c, d);
+      meet();
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const int4 v = *reinterpret_cast<const int4*>(lim + 4 * w);
@@ -345,30 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       meet();
     }
 
-    float acc[HD];
-#pragma unroll
-    for (int i = 0; i < HD; ++i) acc[i] = 0.0f;
-    float minus = kNoRef, l = 0.0f;
-    // adds the output of page m, its products being over
-    const auto drain = [&](int m) {
-      if (!mbar_wait(output, m & 1)) g_err_attention_shared_tc = 1u;
-      __syncwarp();
-      fence_after();
-#pragma unroll
-      for (int x = 0; x < HD / 32; ++x) {
-        float o[32];
-        tm_ld32(mine + S::o_col + part * HD + 32 * x, o);
-        tm_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[32 * x + i] += o[i];
-      }
-      fence_before();
-    };
+    float minus = kNoRef;
+    f2 sum[2] = {0, 0};
     for (int i = cur.i; i < cur.i_end; ++i, ++n) {
       const int key0 = cur.block(i, 0) * kPgKeys;
       const bool whole = key0 >= all_lo && key0 + kPgKeys - 1 <= all_hi;
       const uint32_t s_at = mine + S::s_col + 128 * (n & 1) + 64 * part;
-      if (!mbar_wait(&scores[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+      wait(&scores[n & 1], n >> 1 & 1);
       __syncwarp();
       fence_after();
       float x[64];
@@ -381,42 +500,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         for (int k = 0; k < 64; ++k)
           if (k < from || k > upto) x[k] = -INFINITY;
       }
-      float most = x[0];
+      float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int k = 1; k < 64; ++k) most = fmaxf(most, x[k]);
-      float* mx = top + (n & 1) * 256;
-      mx[part * 128 + row] = most;
+      for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
+      float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      top[part * 128 + row] = most;
       meet_pair(quarter);
-      most = fmaxf(most, mx[(part ^ 1) * 128 + row]) * rs;
-      float f = 1.0f;
+      most = fmaxf(most, top[(part ^ 1) * 128 + row]) * rs;
+      // references are whole numbers, so that a change of one is an exponent
+      int down = 0;
       if (most + minus > kRoom + kSlack) {
-        const float to_minus = kRoom - most;
-        f = exp2_of(to_minus - minus);
+        const float to_minus = rintf(kRoom - most);
+        down = minus - to_minus < 127.0f ? (int)(minus - to_minus) : 127;
+        const float f = down > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - down) << 23);
         minus = to_minus;
-        l *= f;
+        sum[0] = mul2(sum[0], pack(f, f));
+        sum[1] = mul2(sum[1], pack(f, f));
       }
+      if (part == 0) fac[128 * (n % 3) + row] = (uint8_t)down;
       // weights; a hidden key's score is -inf here, its weight 0 whatever rs and minus are
+      const f2 rs2 = pack(rs, rs), minus2 = pack(minus, minus);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[PARTS][16];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[PARTS][8];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float p0 = exp2_of(fmaf(x[32 * c + 2 * k], rs, minus)), p1 = exp2_of(fmaf(x[32 * c + 2 * k + 1], rs, minus));
-          l += p0 + p1;
+        for (int k = 0; k < 8; ++k) {
+          const float2 e = unpack(fma2(pack(x[16 * c + 2 * k], x[16 * c + 2 * k + 1]), rs2, minus2));
+          float p0 = exp2_of(e.x), p1 = exp2_of(e.y);
+          sum[k & 1] = add2(sum[k & 1], pack(p0, p1));
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) w[p][k] = Parts<T>::take(p0, p1);
         }
-        tm_st16(s_at + 16 * c, w[0]);
-        tm_st16(s_at + 32 + 16 * c, w[1]);
-        if constexpr (PARTS > 2) tm_st16(mine + S::t_col + 64 * (n & 1) + 32 * part + 16 * c, w[PARTS - 1]);
+        tm_st8(s_at + 8 * c, w[0]);
+        tm_st8(s_at + 32 + 8 * c, w[1]);
+        if constexpr (PARTS > 2) tm_st8(mine + S::t_col + 64 * (n & 1) + 32 * part + 8 * c, w[PARTS - 1]);
       }
-      tm_st_wait();
-      bool any_strange = false;
-      if (!whole) {
+      unsigned* odd_keys = strange + 5 * (n % 3);
+      if (whole) {
+        if (tid == 0) odd_keys[4] = 0;
+        meet_pair(quarter);  // the maxima have been read
+      } else {
         // Two threads to a key of V.  One that no row sees may hold anything: cleared.  One
         // that some rows see, with an infinity or a NaN: 0 times it is no 0, so it is
         // cleared too, and added to the rows that see it.
-        if (!mbar_wait(&full_v[n & 1], n >> 1 & 1)) g_err_attention_shared_tc = 1u;
+        wait(&full_v[n & 1], n >> 1 & 1);
         const int key = tid >> 1, half = tid & 1;
         const bool none = key0 + key > any_hi || key0 + key < any_lo;
         bool is = false;
@@ -431,80 +558,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         if (none || is)
           for (int p = 0; p < D / 16; ++p) vrow[p] = make_uint4(0, 0, 0, 0);
         is = is && !none;
-        if (tid < 4) strange[tid] = 0;
-        fence_before();
-        any_strange = meet_or(is);
-        if (any_strange) {
-          fence_after();  // the other half's weights are read below
-          if (is && half == 0) atomicOr(&strange[key >> 5], 1u << (key & 31));
-          meet();
+        if (tid < 5) odd_keys[tid] = 0;
+        if (meet_or(is)) {
+          if (is && half == 0) atomicOr(&odd_keys[key >> 5], 1u << (key & 31));
+          if (tid == 0) odd_keys[4] = 1;
         }
         fence_proxy_async_smem();
       }
-      if (i > cur.i) drain(n - 1);
-      if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
-#pragma unroll
-        for (int k = 0; k < HD; ++k) acc[k] *= f;
-      }
-      if (any_strange) {
-        const T* page = vp + ((size_t)cur.page(i) * hkv + cur.h) * kPgKeys * D + part * HD;
-        for (int w = 0; w < 4; ++w)
-          for (unsigned left = strange[w]; left; left &= left - 1) {
-            const int key = 32 * w + __ffs(left) - 1;
-            const uint32_t hi_at = mine + S::s_col + 128 * (n & 1) + 64 * (key >> 6) + (key & 63) / 2;
-            // the weight's parts, the smallest first
-            uint32_t got[3] = {tm_ld1(hi_at), tm_ld1(hi_at + 32), 0};
-            if constexpr (PARTS > 2) got[2] = tm_ld1(mine + S::t_col + 64 * (n & 1) + key / 2);
-            tm_ld_wait();
-            const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
-            if (key0 + key >= at.lo && key0 + key <= at.hi) {
-              const T* v = page + (size_t)key * D;
-#pragma unroll
-              for (int k = 0; k < HD; ++k) {
-                const uint32_t bits = *reinterpret_cast<const uint16_t*>(v + k);
-                acc[k] = fmaf(p, half_of<T>(bits, 0), acc[k]);
-              }
-            }
-          }
-        meet();  // the flags have been read
-      }
+      tm_st_wait();
       fence_before();
       __syncwarp();
       if (lane == 0) arrive(weights);
     }
-    drain(n - 1);
 
     // ---- the part's end
-    top[part * 128 + row] = l;
-    meet();
-    l += top[(part ^ 1) * 128 + row];
-    if (row < live) {
-      const int cap = cur.slot_cap();
-      float2* stat = to.stat + (size_t)at.row * to.slots + cur.slot_base();
-      float* dst;
-      if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
-        dst = to.out + (size_t)at.row * D;
-#pragma unroll
-        for (int k = 0; k < HD; ++k) acc[k] = __fdiv_rn(acc[k], l);
-        if (cap > 1 && part == 0) stat[0] = make_float2(0.0f, -1.0f);
-      } else {
-        const int p = cur.part(cta, ctas);
-        dst = to.acc + ((size_t)at.row * to.slots + cur.slot_base() + p) * D;
-        if (part == 0) {
-          stat[p] = make_float2(-minus, l);
-          if (p == 0)
-            for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < HD / 4; ++k)
-        reinterpret_cast<float4*>(dst + part * HD)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
-    }
-    meet();  // the sums have been read
+    const float2 a = unpack(add2(sum[0], sum[1]));
+    const float l = a.x + a.y;
+    meet_pair(quarter);
+    if (part == 1) top[row] = l;
+    meet_pair(quarter);
+    if (run > 0) wait(stat_free, (run - 1) & 1);
+    if (part == 0) stats[row] = make_float2(minus, l + top[row]);
+    __syncwarp();
+    if (lane == 0) arrive(stat_full);
     if (!cur.another()) break;
+    meet();  // the sums have been read
     cur.next();
   }
-  fence_before();
   __syncthreads();
   if (warp == 0) {
     fence_after();
