@@ -82,40 +82,13 @@ struct SharedWalk {
   int n_seg, hkv, G, rows;  // rows of a tile
   long long total;
   // the segment
-  int seg, n_rows, mem_at, n_mem, chunk0, seg_pages, pg_at, slot0, cap, first, last, tiles_at, tiles;
+  int seg, n_rows, mem_at, n_mem, chunk0, pg_at, slot0, cap, first, last;
   // the run, and this CTA's part of it
   int h, tile, at;     // at: pages before the run
   int page0, n_pages;  // its first page in the segment's, and how many
   int i, i_end;        // pages of the run
   int stop;            // end of this CTA's share
 
-  __device__ __forceinline__ void load() {
-    const int32_t* p = meta + seg * kSharedSegWords;
-    n_rows = p[1];
-    mem_at = p[2];
-    n_mem = p[3];
-    chunk0 = p[4];
-    seg_pages = p[5];
-    pg_at = p[6];
-    slot0 = p[7];
-    cap = p[8];
-    first = p[9];
-    last = p[10];
-    tiles_at = p[12];
-    tiles = (n_rows + rows - 1) / rows;
-  }
-  // Pages of the tile: those of the segment, or where tiles see fewer the table's
-  // (pages of the tiles before it, first page).
-  __device__ __forceinline__ void run() {
-    page0 = 0;
-    n_pages = seg_pages;
-    if (tiles_at) {
-      const int32_t* t = meta + tiles_at + 2 * tile;
-      page0 = t[1];
-      n_pages = t[2] - t[0];
-    }
-    i_end = min(n_pages, stop - at);
-  }
   __device__ __forceinline__ void begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int cta, int ctas) {
     meta = m;
     n_seg = n;
@@ -123,55 +96,64 @@ struct SharedWalk {
     G = group;
     rows = tile_rows;
     total = m[n * kSharedSegWords];
-    const int start = (int)(total * cta / ctas);
     stop = (int)(total * (cta + 1) / ctas);
-    int lo = 0, hi = n - 1;
+    locate((int)(total * cta / ctas));
+  }
+  // The run that page `pos` of the work lies in, from there on.  Found anew for each run:
+  // what a run needs of the plan is not carried through its pages.
+  __device__ __forceinline__ void locate(int pos) {
+    int lo = 0, hi = n_seg - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (m[mid * kSharedSegWords] <= start)
+      if (meta[mid * kSharedSegWords] <= pos)
         lo = mid;
       else
         hi = mid - 1;
     }
     seg = lo;
-    load();
-    int rel = start - m[lo * kSharedSegWords];
-    const int per_head = tiles_at ? m[tiles_at + 2 * tiles] : tiles * seg_pages;
-    h = rel / per_head;
-    rel -= h * per_head;
-    if (tiles_at) {
+    const int32_t* p = meta + seg * kSharedSegWords;
+    n_rows = p[1];
+    mem_at = p[2];
+    n_mem = p[3];
+    chunk0 = p[4];
+    n_pages = p[5];
+    pg_at = p[6];
+    slot0 = p[7];
+    cap = p[8];
+    first = p[9];
+    last = p[10];
+    const int tiles_at = p[12], tiles = (n_rows + rows - 1) / rows;
+    page0 = 0;
+    int rel = pos - p[0];
+    if (tiles_at) {  // tiles that see only some of the pages
+      const int32_t* t = meta + tiles_at;
+      const int per_head = t[2 * tiles];
+      h = rel / per_head;
+      rel -= h * per_head;
       lo = 0, hi = tiles - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (m[tiles_at + 2 * mid] <= rel)
+        if (t[2 * mid] <= rel)
           lo = mid;
         else
           hi = mid - 1;
       }
       tile = lo;
-      i = rel - m[tiles_at + 2 * tile];
+      i = rel - t[2 * tile];
+      page0 = t[2 * tile + 1];
+      n_pages = t[2 * tile + 2] - t[2 * tile];
     } else {
-      tile = rel / seg_pages;
-      i = rel - tile * seg_pages;
+      const int run = rel / n_pages;
+      i = rel - run * n_pages;
+      h = run / tiles;
+      tile = run - h * tiles;
     }
-    at = start - i;
-    run();
+    at = pos - i;
+    i_end = min(n_pages, stop - at);
   }
   // Whether this CTA has a part of another run, and the walk to it.
   __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
-  __device__ __forceinline__ void next() {
-    at += n_pages;
-    if (++tile == tiles) {
-      tile = 0;
-      if (++h == hkv) {
-        h = 0;
-        ++seg;
-        load();
-      }
-    }
-    i = 0;
-    run();
-  }
+  __device__ __forceinline__ void next() { locate(at + n_pages); }
   __device__ __forceinline__ int page(int e) const { return meta[pg_at + page0 + e]; }
   __device__ __forceinline__ int block(int e, int) const { return chunk0 + page0 + e; }
   __device__ __forceinline__ int listed(int) const { return 0; }

@@ -7,12 +7,12 @@
 //               float32's bits) in shared memory, K as it lies in the page
 //   P           256 threads, two to a row; weights go back to tensor memory in as many
 //               parts, the first two over the scores that they come from
-//   O = P V     128 x D of one page, V as it lies in the page; 128 more threads, one to
-//               a row, add it to float32 registers (the tensor core's sums round toward
-//               zero) and write the row at the end, while the others begin the next
+//   O = P V     128 x D of one page, V as it lies in the page; 256 more threads add it to
+//               float32 registers (the tensor core's sums round toward zero) and write
+//               the rows at the end, while the others begin the next
 // The scores of the next page are multiplied while the weights of this one are made:
 // S(n + 1) lies between P V(n - 1) and P V(n).  A warp of its own asks for the pages (TMA,
-// two of K and two of V) and issues the products.  Bound by the products: 32 (fp16) or 48
+// two of K and two of V), another issues the products.  Bound by the products: 32 (fp16) or 48
 // (bf16) of 128 x 128 x 16 for a page of 128-wide heads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,12 +31,12 @@ namespace dsbk {
 
 namespace {
 
-// Threads that make weights, that add up the output, and a warpgroup whose first warp asks
-// and issues; and the registers of each (the launch gives every thread 128).
-constexpr int kWeighers = 256, kAdders = 128, kIssuers = 128;
+// Threads that make weights, that add up the output, and a warpgroup of which one warp asks
+// for pages and one issues products; and the registers of each (the launch gives 96).
+constexpr int kWeighers = 256, kAdders = 256, kIssuers = 128;
 constexpr int kThreads = kWeighers + kAdders + kIssuers;
-constexpr int kWeigherRegs = 120, kAdderRegs = 192, kIssuerRegs = 80;
-static_assert(kWeighers * kWeigherRegs + kAdders * kAdderRegs + kIssuers * kIssuerRegs <= kThreads * 128, "register split");
+constexpr int kWeigherRegs = 112, kAdderRegs = 88, kIssuerRegs = 80;
+static_assert(kWeighers * kWeigherRegs + kAdders * kAdderRegs + kIssuers * kIssuerRegs <= kThreads * 96, "register split");
 constexpr int kRows = 128;
 
 __device__ unsigned int g_err_attention_shared_tc = 0;
@@ -122,8 +122,10 @@ __device__ __forceinline__ void tm_st8(uint32_t at, const uint32_t* v) {
 }
 __device__ __forceinline__ void tm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The two weighing warps of 32 rows; all of them; the latter telling whether any passed true.
+// The two weighing warps of 32 rows; the adders; the weighers; the latter telling whether any
+// passed true.
 __device__ __forceinline__ void meet_pair(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
+__device__ __forceinline__ void meet_adders() { asm volatile("bar.sync 6, 256;" ::: "memory"); }
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 __device__ __forceinline__ bool meet_or(bool x) {
   int r;
@@ -162,7 +164,7 @@ struct Smem {
   static constexpr int fac = stat + 128 * 8;            // [3][128] of a page: the sums before it times 2^-fac
   static constexpr int strange = fac + 3 * 128;         // [3] of a page: keys (4 words), whether any
   static constexpr int bars = strange + 64;             // see below
-  static constexpr int base = bars + 12 * 8;
+  static constexpr int base = bars + 14 * 8;
   static constexpr int bytes = base + 8;
   // tensor memory: scores and weights of two pages, output, third parts of two pages
   static constexpr int s_col = 0, o_col = 256, t_col = 384;
@@ -180,18 +182,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   float2* stats = reinterpret_cast<float2*>(smem + S::stat);
   uint8_t* fac = smem + S::fac;
   unsigned* strange = reinterpret_cast<unsigned*>(smem + S::strange);
-  // pages of K and of V; scores of a page; its output; its weights (by the weighers' warps);
-  // the output has been added (the adders'); a run's queries, its statistics (weighers), and
-  // these have been read (adders)
+  // pages of K and of V; scores of a page; V has been read; a page's output; its weights (by
+  // the weighers' warps); the output has been added (the adders'); a run's queries, its
+  // statistics (weighers), and these have been read (adders)
   uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::bars);
-  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *output = scores + 2, *weights = output + 1, *added = weights + 1,
+  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *free_v = scores + 2, *output = free_v + 2, *weights = output + 1, *added = weights + 1,
            *queries = added + 1, *stat_full = queries + 1, *stat_free = stat_full + 1;
   uint32_t* base = reinterpret_cast<uint32_t*>(smem + S::base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
-    for (int i = 0; i < 7; ++i) mbar_init(&full_k[i], 1);
+    for (int i = 0; i < 9; ++i) mbar_init(&full_k[i], 1);
     mbar_init(weights, kWeighers / 32);
     mbar_init(added, kAdders / 32);
     mbar_init(queries, kWeighers / 32);
@@ -216,98 +218,89 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   };
 
   if (warp >= (kWeighers + kAdders) / 32) {
-    // ---- the asking and issuing warp; n counts the pages of all its runs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+    const uint32_t one = elect();
     if (warp == (kWeighers + kAdders) / 32) {
-      const uint32_t one = elect();
-      SharedWalk ahead = cur;  // of K; V follows one page later
-      int ek = ahead.i, asked_k = 0, asked_v = 0;
-      int row_a = 0, row_b = 0;  // rows of the last page asked for in K, and of the one before
-      bool more = true;
-      const auto ask_k = [&]() {
-        if (!more) return;
-        const int row0 = (ahead.page(ek) * hkv + ahead.h) * kPgKeys, b = asked_k & 1;
-        row_b = row_a;
-        row_a = row0;
+      // ---- the asking warp: pages in the order of all runs, each place as it becomes free
+      const auto ask = [&](int where, const CUtensorMap* map, int row0, uint64_t* bar) {
         if (one) {
-          mbar_arrive_expect_tx(&full_k[b], S::tile);
+          mbar_arrive_expect_tx(bar, S::tile);
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) tma_box(smem + S::k + b * S::tile + x * S::slab, &tmk, 64 * x, row0, &full_k[b]);
+          for (int x = 0; x < D / 64; ++x) tma_box(smem + where + x * S::slab, map, 64 * x, row0, bar);
         }
         __syncwarp();
-        ++asked_k;
-        if (++ek == ahead.i_end) {
-          if (ahead.another()) {
-            ahead.next();
-            ek = ahead.i;
-          } else {
-            more = false;
-          }
-        }
       };
-      const auto ask_v = [&]() {
-        if (asked_v == asked_k) return;
-        const int row0 = asked_k - asked_v == 1 ? row_a : row_b, b = asked_v & 1;
-        if (one) {
-          mbar_arrive_expect_tx(&full_v[b], S::tile);
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x) tma_box(smem + S::v + b * S::tile + x * S::slab, &tmv, 64 * x, row0, &full_v[b]);
+      int i = cur.i;
+      for (int n = 0;; ++n) {
+        const int row0 = (cur.page(i) * hkv + cur.h) * kPgKeys, b = n & 1;
+        if (n > 1) wait(&scores[b], (n >> 1) - 1 & 1);
+        ask(S::k + b * S::tile, &tmk, row0, &full_k[b]);
+        if (n > 1) wait(&free_v[b], (n >> 1) - 1 & 1);
+        ask(S::v + b * S::tile, &tmv, row0, &full_v[b]);
+        if (++i == cur.i_end) {
+          if (!cur.another()) break;
+          cur.next();
+          i = cur.i;
         }
-        __syncwarp();
-        ++asked_v;
-      };
-      ask_k();
-      ask_v();
-      ask_k();
+      }
+    } else if (warp == (kWeighers + kAdders) / 32 + 1) {
+      // ---- the issuing warp; n counts the pages of all its runs.  The tensor core queues a few
+      // products, which cover one wait at a time: the waits of a product of pages lie
+      // within the one before it.
       const uint32_t id_s = idesc<T>(128, false), id_o = idesc<T>(D, true);
       const uint32_t sq = smem_addr(smem + S::q), sk = smem_addr(smem + S::k), sv = smem_addr(smem + S::v);
-      const auto score = [&](int n) {
-        wait(&full_k[n & 1], n >> 1 & 1);
-        fence_after();
-        const uint64_t kd = desc(sk + (n & 1) * S::tile, 0, 1024);
+      const auto score = [&](int n, int part) {  // one part of the scores of page n
+        const uint64_t kd = desc(sk + (n & 1) * S::tile, 0, 1024), qd = desc(sq + part * S::tile, 0, 1024);
 #pragma unroll
-        for (int part = PARTS - 1; part >= 0; --part) {
-          const uint64_t qd = desc(sq + part * S::tile, 0, 1024);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t step = (uint64_t)((k >> 2) * (S::slab >> 4) + (k & 3) * 2);
-            mma_ss(tm + S::s_col + 128 * (n & 1), qd + step, kd + step, id_s, part < PARTS - 1 || k > 0, one);
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)((k >> 2) * (S::slab >> 4) + (k & 3) * 2);
+          mma_ss(tm + S::s_col + 128 * (n & 1), qd + step, kd + step, id_s, part < PARTS - 1 || k > 0, one);
         }
-        if (one) commit(&scores[n & 1]);
-        __syncwarp();
+      };
+      const auto weigh = [&](int n, int part) {  // one part of the output of page n
+        const uint64_t vd = desc(sv + (n & 1) * S::tile, S::slab, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t a = part == 2 ? tm + S::t_col + 64 * (n & 1) + 8 * k
+                                       : tm + S::s_col + 128 * (n & 1) + 64 * (k >> 2) + 32 * part + 8 * (k & 3);
+          mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0, one);
+        }
       };
       int n = 0;
       for (int run = 0;; ++run) {
         wait(queries, run & 1);
+        wait(&full_k[n & 1], n >> 1 & 1);
         fence_after();
-        score(n);
+#pragma unroll
+        for (int part = PARTS - 1; part >= 0; --part) score(n, part);
+        if (one) commit(&scores[n & 1]);
+        __syncwarp();
         for (int i = cur.i; i < cur.i_end; ++i, ++n) {
-          // K's place is free once the scores are there
-          wait(&scores[n & 1], n >> 1 & 1);
-          ask_k();
-          if (i + 1 < cur.i_end) {
+          const bool next = i + 1 < cur.i_end;
+          if (next) {
+            wait(&full_k[(n + 1) & 1], (n + 1) >> 1 & 1);
             // the next scores take the place of the last weights, which a page of strange values
             // (see below) needs until it has been added
             if (n > 0 && strange[5 * ((n - 1) % 3) + 4]) wait(added, (n - 1) & 1);
-            score(n + 1);
+            fence_after();
+            score(n + 1, PARTS - 1);
+          }
+          wait(&full_v[n & 1], n >> 1 & 1);
+          if (next && PARTS > 2) score(n + 1, 1);
+          if (n > 0) wait(added, (n - 1) & 1);  // the output's place is free
+          if (next) {
+            score(n + 1, 0);
+            if (one) commit(&scores[(n + 1) & 1]);
+            __syncwarp();
           }
           wait(weights, n & 1);
-          if (n > 0) wait(added, (n - 1) & 1);  // so is V's other place, and the output's
-          ask_v();
-          wait(&full_v[n & 1], n >> 1 & 1);
           fence_after();
-          const uint64_t vd = desc(sv + (n & 1) * S::tile, S::slab, 1024);
 #pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t a = part == 2 ? tm + S::t_col + 64 * (n & 1) + 8 * k
-                                           : tm + S::s_col + 128 * (n & 1) + 64 * (k >> 2) + 32 * part + 8 * (k & 3);
-              mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0, one);
-            }
+          for (int part = PARTS - 1; part >= 0; --part) weigh(n, part);
+          if (one) {
+            commit(output);
+            if (next) commit(&free_v[n & 1]);  // the last page's place serves the adders first
           }
-          if (one) commit(output);
           __syncwarp();
         }
         if (!cur.another()) break;
@@ -324,15 +317,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   int n = 0;
 
   if (warp >= kWeighers / 32) {
-    // ---- the adders: a thread has a row's output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
+    // ---- the adders: a thread has half of a row's output
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
+    const int d0 = (warp - kWeighers / 32) / 4 * HD;
     for (int run = 0;; ++run) {
       const int live = cur.tile_rows();
       RowAt at{0, 0, 0, 0x7FFFFFFF};
       if (row < live) at = cur.row(row, hq);
-      float acc[D];
+      float acc[HD];
 #pragma unroll
-      for (int i = 0; i < D; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < HD; ++i) acc[i] = 0.0f;
       for (int i = cur.i; i < cur.i_end; ++i, ++n) {
         wait(output, n & 1);
         __syncwarp();
@@ -341,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         const float f = down > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - down) << 23);
         if (__any_sync(0xFFFFFFFFu, down)) {
 #pragma unroll
-          for (int k = 0; k < D; ++k) acc[k] *= f;
+          for (int k = 0; k < HD; ++k) acc[k] *= f;
         }
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
+        for (int x = 0; x < HD / 16; ++x) {
           float o[16];
-          tm_ld16(mine + S::o_col + 16 * x, o);
+          tm_ld16(mine + S::o_col + d0 + 16 * x, o);
           tm_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k) acc[16 * x + k] += o[k];
@@ -367,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
               tm_ld_wait();
               const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
               if (key0 + key < at.lo || key0 + key > at.hi) continue;
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(page + (size_t)key * D);
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(page + (size_t)key * D + d0);
 #pragma unroll
-              for (int k = 0; k < D / 2; ++k) {
+              for (int k = 0; k < HD / 2; ++k) {
                 const uint32_t two = v[k];
                 acc[2 * k] = fmaf(p, half_of<T>(two, 0), acc[2 * k]);
                 acc[2 * k + 1] = fmaf(p, half_of<T>(two, 1), acc[2 * k + 1]);
@@ -382,29 +376,58 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         if (lane == 0) arrive(added);
       }
       // ---- the part's end
+      // (the run found again, so that its place is not carried through its pages)
+      int again = cur.at + cur.i;
+      asm volatile("" : "+r"(again));
+      cur.locate(again);
       wait(stat_full, run & 1);
       const float2 st = stats[row];
       __syncwarp();
       if (lane == 0) arrive(stat_free);
+      // Rows leave through the place of V's last page, 64 dimensions at a time, so that lanes
+      // write along them; the place is free for another page after that.
+      float* dst = nullptr;
       if (row < live) {
         const int cap = cur.slot_cap();
         float2* stat = to.stat + (size_t)at.row * to.slots + cur.slot_base();
-        float* dst;
         if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
           dst = to.out + (size_t)at.row * D;
 #pragma unroll
-          for (int k = 0; k < D; ++k) acc[k] = __fdiv_rn(acc[k], st.y);
-          if (cap > 1) stat[0] = make_float2(0.0f, -1.0f);
+          for (int k = 0; k < HD; ++k) acc[k] = __fdiv_rn(acc[k], st.y);
+          if (cap > 1 && d0 == 0) stat[0] = make_float2(0.0f, -1.0f);
         } else {
           const int p = cur.part(cta, ctas);
           dst = to.acc + ((size_t)at.row * to.slots + cur.slot_base() + p) * D;
-          stat[p] = make_float2(-st.x, st.y);
-          if (p == 0)
-            for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
+          if (d0 == 0) {
+            stat[p] = make_float2(-st.x, st.y);
+            if (p == 0)
+              for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
+          }
         }
+      }
+      {
+        const int b = (n - 1) & 1;
+        float4* stage = reinterpret_cast<float4*>(smem + S::v + b * S::tile);  // [128][HD / 4], pieces turned by row
+        constexpr int P = HD / 4;
+        const int r_out = 16 * (d0 != 0) + lane / P;  // the first row that this lane writes, of its quarter
 #pragma unroll
-        for (int k = 0; k < D / 4; ++k)
-          reinterpret_cast<float4*>(dst)[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+        for (int round = 0; round < 2; ++round) {
+          if ((d0 != 0) == (round == 1)) {
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+              stage[row * P + (k ^ (row & (P - 1)))] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+          }
+          meet_adders();
+#pragma unroll
+          for (int k = 0; k < 16; k += 32 / P) {
+            const int r = r_out + k, rr = 32 * quarter + r;
+            float* out = reinterpret_cast<float*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)dst, r));
+            if (out) reinterpret_cast<float4*>(out + round * HD)[lane % P] = stage[rr * P + ((lane % P) ^ (rr & (P - 1)))];
+          }
+          fence_proxy_async_smem();  // precedes the next page's copy
+          meet_adders();
+        }
+        if (tid == kWeighers) arrive(&free_v[b]);
       }
       __syncwarp();
       if (!cur.another()) break;
@@ -416,48 +439,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   }
 
   // ---- the weighers: thread (row, part) has half of the row's keys
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
   const int part = warp >> 2;
   for (int run = 0;; ++run) {
     const int live = cur.tile_rows();
     RowAt at{0, 0, 0, 0x7FFFFFFF};
     if (row < live) at = cur.row(row, hq);
-    float rs;
     {
-      // q: half of the row's dimensions
-      const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + part * HD;
-      float x[HD];
-      float m = 0.0f;
+      // q: a warp takes 16 rows, lanes along them
+      constexpr int LANES = D / 4, ROWS = 32 / LANES;
+      const int l = lane % LANES;
+      RowAt its{0, 0, 0, 0};
+      const int r0 = 16 * warp, mine_q = r0 + lane % 16;
+      if (mine_q < live) its = cur.row(mine_q, hq);
+      its.row -= its.tok * hq;
+      {
+        float4 x[16 / ROWS];
 #pragma unroll
-      for (int i = 0; i < HD / 4; ++i) {
-        const float4 v = row < live ? __ldg(reinterpret_cast<const float4*>(src) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[4 * i] = v.x * scale_log2e, x[4 * i + 1] = v.y * scale_log2e;
-        x[4 * i + 2] = v.z * scale_log2e, x[4 * i + 3] = v.w * scale_log2e;
-      }
-#pragma unroll
-      for (int i = 0; i < HD; ++i) m = fmaxf(m, fabsf(x[i]));
-      top[part * 128 + row] = m;
-      meet_pair(quarter);
-      m = fmaxf(m, top[(part ^ 1) * 128 + row]);
-      // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
-      // keep their bits whatever q's size
-      const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
-      const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
-      rs = __uint_as_float((uint32_t)(ex - 10) << 23);
-#pragma unroll
-      for (int j = 0; j < HD / 8; ++j) {
-        uint32_t w[PARTS][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x0 = x[8 * j + 2 * i] * inv, x1 = x[8 * j + 2 * i + 1] * inv;
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) w[p][i] = Parts<T>::take(x0, x1);
+        for (int i = 0; i < 16 / ROWS; ++i) {
+          const int r = i * ROWS + lane / LANES;
+          const int tok = __shfl_sync(0xFFFFFFFFu, its.tok, r), head = __shfl_sync(0xFFFFFFFFu, its.row, r);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r0 + r < live) x[i] = __ldg(reinterpret_cast<const float4*>(q + (size_t)tok * q_stride + (size_t)head * D) + l);
         }
-        const int piece = part * (HD / 8) + j;  // of the row
-        uint8_t* dst = smem + S::q + (piece >> 3) * S::slab + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-          *reinterpret_cast<uint4*>(dst + p * S::tile) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        for (int i = 0; i < 16 / ROWS; ++i) {
+          const int r = r0 + i * ROWS + lane / LANES;
+          x[i] = make_float4(x[i].x * scale_log2e, x[i].y * scale_log2e, x[i].z * scale_log2e, x[i].w * scale_log2e);
+          float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+#pragma unroll
+          for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
+          // keep their bits whatever q's size
+          const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
+          const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
+          if (l == 0) top[r] = __uint_as_float((uint32_t)(ex - 10) << 23);
+          float x0 = x[i].x * inv, x1 = x[i].y * inv, x2 = x[i].z * inv, x3 = x[i].w * inv;
+          const int piece = l >> 1;
+          uint8_t* dst = smem + S::q + (piece >> 3) * S::slab + r * 128 + (((piece & 7) ^ (r & 7)) << 4) + (l & 1) * 8;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            const uint32_t w0 = Parts<T>::take(x0, x1), w1 = Parts<T>::take(x2, x3);
+            *reinterpret_cast<uint2*>(dst + p * S::tile) = make_uint2(w0, w1);
+          }
+        }
       }
     }
     fence_proxy_async_smem();  // q is the first product's operand
@@ -465,12 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     if (lane == 0) arrive(queries);
     // what the tile's rows see in common, and at all
     int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = -1;
+    float rs;
     {
-      int* lim = reinterpret_cast<int*>(top);  // [4 quarters][4]
+      int* lim = reinterpret_cast<int*>(top + 128);  // [4 quarters][4]
       const int a = __reduce_max_sync(0xFFFFFFFFu, at.lo), b = __reduce_min_sync(0xFFFFFFFFu, at.hi);
       const int c = __reduce_min_sync(0xFFFFFFFFu, row < live ? at.lo : 0x7FFFFFFF);
       const int d = __reduce_max_sync(0xFFFFFFFFu, row < live ? at.hi : -1);
-      meet();
       if (lane == 0 && part == 0) *reinterpret_cast<int4*>(lim + 4 * warp) = make_int4(a, b, c, d);
       meet();
 #pragma unroll
@@ -478,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         const int4 v = *reinterpret_cast<const int4*>(lim + 4 * w);
         all_lo = max(all_lo, v.x), all_hi = min(all_hi, v.y), any_lo = min(any_lo, v.z), any_hi = max(any_hi, v.w);
       }
+      rs = top[row];
       meet();
     }
 
@@ -550,13 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         uint4* vrow = reinterpret_cast<uint4*>(smem + S::v + (n & 1) * S::tile + (D == 128 ? half * S::slab : half * 64) + key * 128);
         // (64-wide heads: a thread's half of the row is four pieces; the swizzle only
         // permutes the pieces of a row)
-        for (int p = 0; p < D / 16; ++p) {
-          const uint4 v = vrow[p];
+#pragma unroll
+        for (int p = 0; p < D / 16; ++p) {  // (in an order that turns with the key: other banks)
+          const uint4 v = vrow[p ^ (key & (D / 16 - 1))];
           is = is || odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w);
         }
         is = __shfl_xor_sync(0xFFFFFFFFu, (int)is, 1) || is;
         if (none || is)
-          for (int p = 0; p < D / 16; ++p) vrow[p] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int p = 0; p < D / 16; ++p) vrow[p ^ (key & (D / 16 - 1))] = make_uint4(0, 0, 0, 0);
         is = is && !none;
         if (tid < 5) odd_keys[tid] = 0;
         if (meet_or(is)) {

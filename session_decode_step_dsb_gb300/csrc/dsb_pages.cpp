@@ -151,11 +151,14 @@ struct Tree {
     return (rows + tile - 1) / tile * (tile == 8 ? 2 : 5);
   }
 
-  // Whether pages that m1 - m0 sequences have in common are worth a segment.
+  // Whether pages that m1 - m0 sequences have in common are worth a segment: they save the
+  // sequences' own tiles, but a tile that ends there begins once more behind them, which
+  // takes as long as some pages.
   bool worth(int m0, int m1, int n) const {
     int apart = 0;
     for (int m = m0; m < m1; ++m) apart += cost(G * b->new_tokens[order[m]]);
-    return n > 0 && cost(rows_of(m0, m1)) < apart;
+    const int together = cost(rows_of(m0, m1));
+    return (long long)(apart - together) * n > 3LL * together;
   }
 
   // Pages that each tile of a sequence's rows sees of its segment, where that is not all:
