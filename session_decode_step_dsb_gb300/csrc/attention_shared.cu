@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
 
   Walk cur, ahead;
   if constexpr (std::is_same_v<Walk, SharedWalk>)
-    cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
+    cur.locate(cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas));
   else
     cur.begin(meta, n_seg, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, cta, ctas);
   ahead = cur;

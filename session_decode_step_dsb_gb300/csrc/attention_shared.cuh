@@ -89,7 +89,8 @@ struct SharedWalk {
   int i, i_end;        // pages of the run
   int stop;            // end of this CTA's share
 
-  __device__ __forceinline__ void begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int cta, int ctas) {
+  // This CTA's share; returns its start.
+  __device__ __forceinline__ int begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int cta, int ctas) {
     meta = m;
     n_seg = n;
     hkv = kv_heads;
@@ -97,7 +98,7 @@ struct SharedWalk {
     rows = tile_rows;
     total = m[n * kSharedSegWords];
     stop = (int)(total * (cta + 1) / ctas);
-    locate((int)(total * cta / ctas));
+    return (int)(total * cta / ctas);
   }
   // The run that page `pos` of the work lies in, from there on.  Found anew for each run:
   // what a run needs of the plan is not carried through its pages.
@@ -154,6 +155,7 @@ struct SharedWalk {
   // Whether this CTA has a part of another run, and the walk to it.
   __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
   __device__ __forceinline__ void next() { locate(at + n_pages); }
+  __device__ __forceinline__ int here() const { return i_end - i; }  // pages of this CTA's part
   __device__ __forceinline__ int page(int e) const { return meta[pg_at + page0 + e]; }
   __device__ __forceinline__ int block(int e, int) const { return chunk0 + page0 + e; }
   __device__ __forceinline__ int listed(int) const { return 0; }

@@ -35,7 +35,7 @@ namespace {
 // for pages and one issues products; and the registers of each (the launch gives 96).
 constexpr int kWeighers = 256, kAdders = 256, kIssuers = 128;
 constexpr int kThreads = kWeighers + kAdders + kIssuers;
-constexpr int kWeigherRegs = 112, kAdderRegs = 88, kIssuerRegs = 80;
+constexpr int kWeigherRegs = 88, kAdderRegs = 112, kIssuerRegs = 80;
 static_assert(kWeighers * kWeigherRegs + kAdders * kAdderRegs + kIssuers * kIssuerRegs <= kThreads * 96, "register split");
 constexpr int kRows = 128;
 
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   pdl_wait();
   pdl_trigger();
   SharedWalk cur;
-  cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
+  int pos = cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
   const auto wait = [](uint64_t* bar, int parity) {
     if (!mbar_wait(bar, (uint32_t)parity)) g_err_attention_shared_tc = 1u;
   };
@@ -230,17 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         }
         __syncwarp();
       };
-      int i = cur.i;
-      for (int n = 0;; ++n) {
-        const int row0 = (cur.page(i) * hkv + cur.h) * kPgKeys, b = n & 1;
-        if (n > 1) wait(&scores[b], (n >> 1) - 1 & 1);
-        ask(S::k + b * S::tile, &tmk, row0, &full_k[b]);
-        if (n > 1) wait(&free_v[b], (n >> 1) - 1 & 1);
-        ask(S::v + b * S::tile, &tmv, row0, &full_v[b]);
-        if (++i == cur.i_end) {
-          if (!cur.another()) break;
-          cur.next();
-          i = cur.i;
+      for (int n = 0; pos < cur.stop; pos += cur.here()) {
+        cur.locate(pos);
+#pragma unroll 1
+        for (int i = cur.i; i < cur.i_end; ++i, ++n) {
+          const int row0 = (cur.page(i) * hkv + cur.h) * kPgKeys, b = n & 1;
+          if (n > 1) wait(&scores[b], (n >> 1) - 1 & 1);
+          ask(S::k + b * S::tile, &tmk, row0, &full_k[b]);
+          if (n > 1) wait(&free_v[b], (n >> 1) - 1 & 1);
+          ask(S::v + b * S::tile, &tmv, row0, &full_v[b]);
         }
       }
     } else if (warp == (kWeighers + kAdders) / 32 + 1) {
@@ -262,49 +260,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const uint32_t a = part == 2 ? tm + S::t_col + 64 * (n & 1) + 8 * k
-                                       : tm + S::s_col + 128 * (n & 1) + 64 * (k >> 2) + 32 * part + 8 * (k & 3);
+                                       : tm + S::s_col + 128 * (n & 1) + 16 * part + 32 * (k >> 1) + 8 * (k & 1);
           mma_ts(tm + S::o_col, a, vd + (uint64_t)(k * (2048 >> 4)), id_o, part < PARTS - 1 || k > 0, one);
         }
       };
       int n = 0;
-      for (int run = 0;; ++run) {
+      for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+        cur.locate(pos);
+        const int end = n + cur.here();
         wait(queries, run & 1);
-        wait(&full_k[n & 1], n >> 1 & 1);
-        fence_after();
-#pragma unroll
-        for (int part = PARTS - 1; part >= 0; --part) score(n, part);
-        if (one) commit(&scores[n & 1]);
-        __syncwarp();
-        for (int i = cur.i; i < cur.i_end; ++i, ++n) {
-          const bool next = i + 1 < cur.i_end;
+        // the first page's scores alone, then those of a page's next with its output
+#pragma unroll 1
+        for (int m = n - 1; m < end; ++m) {
+          const bool next = m + 1 < end, out = m >= n;
           if (next) {
-            wait(&full_k[(n + 1) & 1], (n + 1) >> 1 & 1);
+            wait(&full_k[(m + 1) & 1], (m + 1) >> 1 & 1);
             // the next scores take the place of the last weights, which a page of strange values
             // (see below) needs until it has been added
-            if (n > 0 && strange[5 * ((n - 1) % 3) + 4]) wait(added, (n - 1) & 1);
+            if (out && m > 0 && strange[5 * ((m - 1) % 3) + 4]) wait(added, (m - 1) & 1);
             fence_after();
-            score(n + 1, PARTS - 1);
+            score(m + 1, PARTS - 1);
           }
-          wait(&full_v[n & 1], n >> 1 & 1);
-          if (next && PARTS > 2) score(n + 1, 1);
-          if (n > 0) wait(added, (n - 1) & 1);  // the output's place is free
+          if (out) wait(&full_v[m & 1], m >> 1 & 1);
+          if (next && PARTS > 2) score(m + 1, 1);
+          if (out && m > 0) wait(added, (m - 1) & 1);  // the output's place is free
           if (next) {
-            score(n + 1, 0);
-            if (one) commit(&scores[(n + 1) & 1]);
+            score(m + 1, 0);
+            if (one) commit(&scores[(m + 1) & 1]);
             __syncwarp();
           }
-          wait(weights, n & 1);
+          if (!out) continue;
+          wait(weights, m & 1);
           fence_after();
-#pragma unroll
-          for (int part = PARTS - 1; part >= 0; --part) weigh(n, part);
+#pragma unroll 1
+          for (int part = PARTS - 1; part >= 0; --part) weigh(m, part);
           if (one) {
             commit(output);
-            if (next) commit(&free_v[n & 1]);  // the last page's place serves the adders first
+            if (next) commit(&free_v[m & 1]);  // the last page's place serves the adders first
           }
           __syncwarp();
         }
-        if (!cur.another()) break;
-        cur.next();
+        n = end;
       }
     }
     __syncwarp();
@@ -318,12 +314,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 
   if (warp >= kWeighers / 32) {
     // ---- the adders: a thread has half of a row's output
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
     const int d0 = (warp - kWeighers / 32) / 4 * HD;
-    for (int run = 0;; ++run) {
-      const int live = cur.tile_rows();
+    for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+      cur.locate(pos);
+      // where the row goes: to the output where this CTA has all of it, else to a slot
       RowAt at{0, 0, 0, 0x7FFFFFFF};
-      if (row < live) at = cur.row(row, hq);
+      float* dst = nullptr;
+      float2* stat = nullptr;
+      int empty = 0;  // slots behind the first part's that the row's parts leave
+      const bool done = cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages;
+      if (row < cur.tile_rows()) {
+        at = cur.row(row, hq);
+        const int part = cur.part(cta, ctas);
+        const size_t slot = (size_t)at.row * to.slots + cur.slot_base() + (done ? 0 : part);
+        dst = done ? to.out + (size_t)at.row * D : to.acc + slot * D;
+        if (d0 == 0 && !(done && cur.slot_cap() == 1)) {
+          stat = to.stat + slot;
+          if (!done && part == 0) empty = cur.slot_cap() - cur.parts(ctas);
+        }
+      }
       float acc[HD];
 #pragma unroll
       for (int i = 0; i < HD; ++i) acc[i] = 0.0f;
@@ -354,9 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 #pragma unroll 1
             for (unsigned left = odd_keys[w]; left; left &= left - 1) {
               const int key = 32 * w + __ffs(left) - 1;
-              const uint32_t hi_at = mine + S::s_col + 128 * (n & 1) + 64 * (key >> 6) + (key & 63) / 2;
+              const uint32_t hi_at = mine + S::s_col + 128 * (n & 1) + 32 * (key >> 5) + (key & 31) / 2;
               // the weight's parts, the smallest first
-              uint32_t got[3] = {tm_ld1(hi_at), tm_ld1(hi_at + 32), 0};
+              uint32_t got[3] = {tm_ld1(hi_at), tm_ld1(hi_at + 16), 0};
               if constexpr (PARTS > 2) got[2] = tm_ld1(mine + S::t_col + 64 * (n & 1) + key / 2);
               tm_ld_wait();
               const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
@@ -375,35 +385,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         __syncwarp();
         if (lane == 0) arrive(added);
       }
-      // ---- the part's end
-      // (the run found again, so that its place is not carried through its pages)
-      int again = cur.at + cur.i;
-      asm volatile("" : "+r"(again));
-      cur.locate(again);
+      // ---- the part's end.  Rows leave through the place of V's last page, 64 dimensions at
+      // a time, so that lanes write along them; the place is free for another page after that.
       wait(stat_full, run & 1);
       const float2 st = stats[row];
       __syncwarp();
       if (lane == 0) arrive(stat_free);
-      // Rows leave through the place of V's last page, 64 dimensions at a time, so that lanes
-      // write along them; the place is free for another page after that.
-      float* dst = nullptr;
-      if (row < live) {
-        const int cap = cur.slot_cap();
-        float2* stat = to.stat + (size_t)at.row * to.slots + cur.slot_base();
-        if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
-          dst = to.out + (size_t)at.row * D;
+      if (stat) {
+        *stat = done ? make_float2(0.0f, -1.0f) : make_float2(-st.x, st.y);
+        for (; empty > 0; --empty) stat[empty + cur.parts(ctas) - 1] = make_float2(0.0f, 0.0f);
+      }
+      if (done) {
+        const float by = __frcp_rn(st.y);
 #pragma unroll
-          for (int k = 0; k < HD; ++k) acc[k] = __fdiv_rn(acc[k], st.y);
-          if (cap > 1 && d0 == 0) stat[0] = make_float2(0.0f, -1.0f);
-        } else {
-          const int p = cur.part(cta, ctas);
-          dst = to.acc + ((size_t)at.row * to.slots + cur.slot_base() + p) * D;
-          if (d0 == 0) {
-            stat[p] = make_float2(-st.x, st.y);
-            if (p == 0)
-              for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
-          }
-        }
+        for (int k = 0; k < HD; ++k) acc[k] *= by;
       }
       {
         const int b = (n - 1) & 1;
@@ -430,8 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         if (tid == kWeighers) arrive(&free_v[b]);
       }
       __syncwarp();
-      if (!cur.another()) break;
-      cur.next();
     }
     fence_before();
     __syncthreads();
@@ -439,12 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   }
 
   // ---- the weighers: thread (row, part) has half of the row's keys
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
   const int part = warp >> 2;
-  for (int run = 0;; ++run) {
+  for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+    cur.locate(pos);
     const int live = cur.tile_rows();
-    RowAt at{0, 0, 0, 0x7FFFFFFF};
-    if (row < live) at = cur.row(row, hq);
     {
       // q: a warp takes 16 rows, lanes along them
       constexpr int LANES = D / 4, ROWS = 32 / LANES;
@@ -488,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     fence_proxy_async_smem();  // q is the first product's operand
     __syncwarp();
     if (lane == 0) arrive(queries);
+    RowAt at{0, 0, 0, 0x7FFFFFFF};
+    if (row < live) at = cur.row(row, hq);
     // what the tile's rows see in common, and at all
     int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = -1;
     float rs;
@@ -516,20 +510,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       wait(&scores[n & 1], n >> 1 & 1);
       __syncwarp();
       fence_after();
-      float x[64];
-      tm_ld32(s_at, x);
-      tm_ld32(s_at + 32, x + 32);
-      tm_ld_wait();
+      // the keys of this half that the row sees, as bits
+      unsigned long long seen = ~0ull;
       if (!whole) {
-        const int from = at.lo - (key0 + 64 * part), upto = at.hi - (key0 + 64 * part);
-#pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (k < from || k > upto) x[k] = -INFINITY;
+        const int from = max(at.lo - (key0 + 64 * part), 0), upto = min(at.hi - (key0 + 64 * part), 63);
+        seen = from > upto ? 0ull : (~0ull >> (63 - upto)) & (~0ull << from);
       }
-      float m4[4] = {x[0], x[1], x[2], x[3]};
+      const auto load = [&](int c, float* x) {
+        tm_ld32(s_at + 32 * c, x);
+        tm_ld_wait();
+        if (!whole) {
+          const uint32_t bits = (uint32_t)(seen >> (32 * c));
 #pragma unroll
-      for (int k = 4; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
-      float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int k = 0; k < 32; ++k) x[k] = bits >> k & 1u ? x[k] : -INFINITY;
+        }
+      };
+      float most = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        float x[32];
+        load(c, x);
+        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int k = 4; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], x[k]);
+        most = fmaxf(most, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+      }
       top[part * 128 + row] = most;
       meet_pair(quarter);
       most = fmaxf(most, top[(part ^ 1) * 128 + row]) * rs;
@@ -546,20 +551,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       if (part == 0) fac[128 * (n % 3) + row] = (uint8_t)down;
       // weights; a hidden key's score is -inf here, its weight 0 whatever rs and minus are
       const f2 rs2 = pack(rs, rs), minus2 = pack(minus, minus);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {  // the weights of 32 keys over their scores
+        float x[32];
+        load(c, x);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[PARTS][8];
+        for (int j = 0; j < 2; ++j) {
+          uint32_t w[PARTS][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 e = unpack(fma2(pack(x[16 * c + 2 * k], x[16 * c + 2 * k + 1]), rs2, minus2));
-          float p0 = exp2_of(e.x), p1 = exp2_of(e.y);
-          sum[k & 1] = add2(sum[k & 1], pack(p0, p1));
+          for (int k = 0; k < 8; ++k) {
+            const float2 e = unpack(fma2(pack(x[16 * j + 2 * k], x[16 * j + 2 * k + 1]), rs2, minus2));
+            float p0 = exp2_of(e.x), p1 = exp2_of(e.y);
+            sum[k & 1] = add2(sum[k & 1], pack(p0, p1));
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) w[p][k] = Parts<T>::take(p0, p1);
+            for (int p = 0; p < PARTS; ++p) w[p][k] = Parts<T>::take(p0, p1);
+          }
+          tm_st8(s_at + 32 * c + 8 * j, w[0]);
+          tm_st8(s_at + 32 * c + 16 + 8 * j, w[1]);
+          if constexpr (PARTS > 2) tm_st8(mine + S::t_col + 64 * (n & 1) + 32 * part + 16 * c + 8 * j, w[PARTS - 1]);
         }
-        tm_st8(s_at + 8 * c, w[0]);
-        tm_st8(s_at + 32 + 8 * c, w[1]);
-        if constexpr (PARTS > 2) tm_st8(mine + S::t_col + 64 * (n & 1) + 32 * part + 8 * c, w[PARTS - 1]);
       }
       unsigned* odd_keys = strange + 5 * (n % 3);
       if (whole) {
@@ -609,9 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     if (part == 0) stats[row] = make_float2(minus, l + top[row]);
     __syncwarp();
     if (lane == 0) arrive(stat_full);
-    if (!cur.another()) break;
     meet();  // the sums have been read
-    cur.next();
   }
   __syncthreads();
   if (warp == 0) {

@@ -227,6 +227,37 @@ struct Tree {
     }
   }
 
+  // Cuts segments of several tiles of 128 rows into pieces of about a CTA's share of the
+  // work: CTAs side by side then take the tiles through the same pages at the same time,
+  // which come from memory once (a CTA that goes through all pages of a tile, and others at
+  // other places of theirs, read 134 MB of pages three times).
+  void cut_shares(int hkv, int sms) {
+    long long work = 0;
+    for (const Segment& g : segs)
+      if (g.tile() == 128) work += hkv * g.pages_a_head();
+    const int share = (int)((work + sms - 1) / sms);
+    std::vector<Segment> out;
+    std::vector<int> last(segs.size());
+    for (size_t i = 0; i < segs.size(); ++i) {
+      const Segment& g = segs[i];
+      const bool cut = g.tile() == 128 && g.tiles() > 1 && g.table.empty() && share > 0;
+      const int pieces = cut ? std::max(1, (g.n + share / 2) / share) : 1;
+      int parent = g.parent >= 0 ? last[g.parent] : -1;
+      for (int k = 0; k < pieces; ++k) {
+        Segment p = g;
+        p.parent = parent;
+        p.b0 = g.b0 + (int)((long long)g.n * k / pieces);
+        p.n = g.b0 + (int)((long long)g.n * (k + 1) / pieces) - p.b0;
+        parent = (int)out.size();
+        out.push_back(std::move(p));
+      }
+      last[i] = parent;
+    }
+    for (int& e : end)
+      if (e >= 0) e = last[e];
+    segs.swap(out);
+  }
+
   void build() {
     end.assign(b->n_seq, -1);
     for (int pass = 0; pass < 2; ++pass)
@@ -375,6 +406,9 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
 
     Tree tree{b, n_q_heads / hkv, {}, {}, {}};
     tree.build();
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != DSB_OK) return st;
+    tree.cut_shares(hkv, dev.sms);
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
     const auto words_of = [&](const Segment& g) {
@@ -413,8 +447,6 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         launches.back().work += work;
       }
     }
-    DeviceInfo dev;
-    if ((st = device_info(&dev)) != DSB_OK) return st;
     int slots = 0;
     for (Launch& l : launches) {
       l.ctas = (int)std::min<long long>(l.tile == 8 ? dsbk::page_attn_resident(dev.sms) : dev.sms, l.work);
