@@ -265,19 +265,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         }
       };
       int n = 0;
+      bool odd_page = false;  // the last page was one
       for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
         cur.locate(pos);
         const int end = n + cur.here();
         wait(queries, run & 1);
+        wait(&full_k[n & 1], n >> 1 & 1);
         // the first page's scores alone, then those of a page's next with its output
 #pragma unroll 1
         for (int m = n - 1; m < end; ++m) {
           const bool next = m + 1 < end, out = m >= n;
           if (next) {
-            wait(&full_k[(m + 1) & 1], (m + 1) >> 1 & 1);
             // the next scores take the place of the last weights, which a page of strange values
             // (see below) needs until it has been added
-            if (out && m > 0 && strange[5 * ((m - 1) % 3) + 4]) wait(added, (m - 1) & 1);
+            if (out && odd_page) wait(added, (m - 1) & 1);
             fence_after();
             score(m + 1, PARTS - 1);
           }
@@ -293,7 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
           wait(weights, m & 1);
           fence_after();
 #pragma unroll 1
-          for (int part = PARTS - 1; part >= 0; --part) weigh(m, part);
+          for (int part = PARTS - 1; part > 0; --part) weigh(m, part);
+          if (m + 2 < end) wait(&full_k[m & 1], (m + 2) >> 1 & 1);
+          odd_page = strange[5 * (m % 3) + 4];
+          weigh(m, 0);
           if (one) {
             commit(output);
             if (next) commit(&free_v[m & 1]);  // the last page's place serves the adders first

@@ -371,9 +371,17 @@ cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, co
 // segment's pages, (pages of the tiles before it, first page) of each tile and the pages of
 // all.
 constexpr int kSharedSegWords = 13, kSharedMemWords = 5;
-// Query rows of a tile of a segment with `rows` of them on a kv head: 8 of the warp-level
-// kernel (attention_shared.cu) or 128 of the tcgen05 one (attention_shared_tc.cu).
-inline int shared_tile_rows(int rows) { return rows > 16 ? 128 : 8; }
+// Query rows of a tile of a segment with `rows` of them on a kv head and n pages: 8 of the
+// warp-level kernel (attention_shared.cu) or 128 of the tcgen05 one
+// (attention_shared_tc.cu), whichever takes less of an SM's time, by what they measured:
+// a page of a tile 0.6 and 1.6 us, and 4 us for a tile of the latter to begin and end.
+inline long long shared_tile_cost(int rows, int n, int tile) {
+  const long long tiles = (rows + tile - 1) / tile;
+  return tile == 8 ? 3 * tiles * n : tiles * (8LL * n + 20);
+}
+inline int shared_tile_rows(int rows, int n) {
+  return shared_tile_cost(rows, n, 128) < shared_tile_cost(rows, n, 8) ? 128 : 8;
+}
 struct PageAttnArgs {
   const float* q;
   long long q_stride;

@@ -119,11 +119,11 @@ struct Segment {
   int m0, m1;     // its sequences in Tree::order
   int b0, n;      // first block, pages
   int rows = 0;   // query rows on a kv head
+  int tile = 8;   // of them go through the pages together
   int slot0 = 0, cap = 0;
   std::vector<int32_t> table;  // of its tiles, where they see only some of its pages
 
-  int tile() const { return dsbk::shared_tile_rows(rows); }
-  int tiles() const { return (rows + tile() - 1) / tile(); }
+  int tiles() const { return (rows + tile - 1) / tile; }
   long long pages_a_head() const { return table.empty() ? (long long)tiles() * n : table.back(); }
 };
 
@@ -145,20 +145,18 @@ struct Tree {
     for (int m = m0; m < m1; ++m) r += G * b->new_tokens[order[m]];
     return r;
   }
-  // What a page costs a segment of so many rows: tiles of 8, one of 128 as 2.5 of them.
-  static int cost(int rows) {
-    const int tile = dsbk::shared_tile_rows(rows);
-    return (rows + tile - 1) / tile * (tile == 8 ? 2 : 5);
-  }
+  // What n pages cost a segment of so many rows.
+  static long long cost(int rows, int n) { return dsbk::shared_tile_cost(rows, n, dsbk::shared_tile_rows(rows, n)); }
 
   // Whether pages that m1 - m0 sequences have in common are worth a segment: they save the
   // sequences' own tiles, but a tile that ends there begins once more behind them, which
   // takes as long as some pages.
   bool worth(int m0, int m1, int n) const {
-    int apart = 0;
-    for (int m = m0; m < m1; ++m) apart += cost(G * b->new_tokens[order[m]]);
-    const int together = cost(rows_of(m0, m1));
-    return (long long)(apart - together) * n > 3LL * together;
+    if (n <= 0) return false;
+    long long apart = 0;
+    for (int m = m0; m < m1; ++m) apart += cost(G * b->new_tokens[order[m]], n);
+    const int rows = rows_of(m0, m1);
+    return apart > cost(rows, n) + cost(rows, 3);
   }
 
   // Pages that each tile of a sequence's rows sees of its segment, where that is not all:
@@ -167,8 +165,8 @@ struct Tree {
     const int s = order[g->m0], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
     int sum = 0;
     bool cut = false;
-    for (int r = 0; r < g->rows; r += g->tile()) {
-      const int lo = len - n + r / G, hi = len - n + (std::min(r + g->tile(), g->rows) - 1) / G;
+    for (int r = 0; r < g->rows; r += g->tile) {
+      const int lo = len - n + r / G, hi = len - n + (std::min(r + g->tile, g->rows) - 1) / G;
       const int from = w > 0 ? std::max(0, lo - w + 1) / DSB_KV_PAGE : 0;
       int a = std::max(from - g->b0, 0), z = std::min(hi / DSB_KV_PAGE - g->b0, g->n - 1);
       if (a > z) a = z = 0;  // none of them: one page, all hidden
@@ -183,8 +181,9 @@ struct Tree {
   int add(int parent, int m0, int m1, int b0, int b1) {
     // a segment's metadata has to fit a launch
     for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {
-      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0), 0, 0, 0, {}};
+      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0)};
       s.rows = rows_of(m0, m1);
+      s.tile = dsbk::shared_tile_rows(s.rows, b1 - b0);
       if (m1 - m0 == 1 && s.tiles() > 1) cut_tiles(&s);
       parent = (int)segs.size();
       segs.push_back(s);
@@ -234,13 +233,13 @@ struct Tree {
   void cut_shares(int hkv, int sms) {
     long long work = 0;
     for (const Segment& g : segs)
-      if (g.tile() == 128) work += hkv * g.pages_a_head();
+      if (g.tile == 128) work += hkv * g.pages_a_head();
     const int share = (int)((work + sms - 1) / sms);
     std::vector<Segment> out;
     std::vector<int> last(segs.size());
     for (size_t i = 0; i < segs.size(); ++i) {
       const Segment& g = segs[i];
-      const bool cut = g.tile() == 128 && g.tiles() > 1 && g.table.empty() && share > 0;
+      const bool cut = g.tile == 128 && g.tiles() > 1 && g.table.empty() && share > 0;
       const int pieces = cut ? std::max(1, (g.n + share / 2) / share) : 1;
       int parent = g.parent >= 0 ? last[g.parent] : -1;
       for (int k = 0; k < pieces; ++k) {
@@ -430,7 +429,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
       bool open = false;
       for (size_t i = 0; i < tree.segs.size(); ++i) {
         const Segment& g = tree.segs[i];
-        if (g.tile() != tile) continue;
+        if (g.tile != tile) continue;
         const size_t n = words_of(g);
         if (1 + n > room)
           return fail(DSB_ERR_UNSUPPORTED, "a call holds at most %zu words of metadata for the pages of %d sequences", room,
