@@ -132,9 +132,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
 
   Walk cur, ahead;
   if constexpr (std::is_same_v<Walk, SharedWalk>)
-    cur.locate(cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas));
+    cur.locate(cur.begin(meta, n_seg, hkv, hq / hkv, kRows, kLead8, cta, ctas));
   else
-    cur.begin(meta, n_seg, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, cta, ctas);
+    cur.locate(cur.begin(meta, n_seg, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, kLead8, cta, ctas));
+  if (!cur.any()) return;
   ahead = cur;
 
   // ---- asking: entry `e` of ahead's run; 32 entries' blocks and pages in the lanes.  Entries
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
           asking = false;
           return;
         }
-        ahead.next();
+        ahead.locate(ahead.following());
         e = ahead.i;
         list_at = e - 32;
       }
@@ -336,19 +337,22 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       if (!whole) {
         // Lane i looks after key i.  One that no row sees may hold anything: cleared.  One
         // that some rows see, with an infinity or a NaN: 0 times it is no 0, so it is
-        // cleared too, and added to the rows that see it.
+        // cleared too, and added to the rows that see it.  (Pieces of a row in an order that
+        // turns with the lane: other banks.)
         const int key = key0 + lane;
         const bool none = key > max_hi || key < min_lo;
         bool strange = false;
         uint4* row = reinterpret_cast<uint4*>(ring + slot * R::slot + lane * 128);
-#pragma unroll 1
-        for (int x = 0; x < NT; ++x) {
-          const uint4 v = row[(x >> 3) * (R::slab / 16) + (x & 7)];
-          strange = strange || odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w);
+        if (min_hi < max_hi || min_lo < max_lo) {
+#pragma unroll 4
+          for (int x = 0; x < NT; ++x) {
+            const uint4 v = row[(x >> 3) * (R::slab / 16) + ((x ^ lane) & 7)];
+            strange = strange || odd<T>(v.x) || odd<T>(v.y) || odd<T>(v.z) || odd<T>(v.w);
+          }
         }
         if (none || strange) {
-#pragma unroll 1
-          for (int x = 0; x < NT; ++x) row[(x >> 3) * (R::slab / 16) + (x & 7)] = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+          for (int x = 0; x < NT; ++x) row[(x >> 3) * (R::slab / 16) + ((x ^ lane) & 7)] = make_uint4(0, 0, 0, 0);
         }
         unsigned odd_keys = __ballot_sync(0xFFFFFFFFu, strange && !none);
         if (odd_keys) {
@@ -455,12 +459,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
           for (int k = 0; k < D / 16; ++k) x[k] = sum == 0.0f ? 0.0f : __fdiv_rn(x[k], sum);
           if (cap > 1 && d0 == 0) stat[0] = make_float2(0.0f, -1.0f);
         } else {
-          const int part = cur.part(cta, ctas);
+          const int part = cur.part(cta);
           dst = to.acc + ((size_t)mine.row * to.slots + cur.slot_base() + part) * D;
           if (d0 == 0) {
             stat[part] = make_float2(ref, sum);
             if (part == 0)
-              for (int k = cur.parts(ctas); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
+              for (int k = cur.parts(); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
           }
         }
 #pragma unroll
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       }
     }
     if (!cur.another()) break;
-    cur.next();
+    cur.locate(cur.following());
   }
 }
 

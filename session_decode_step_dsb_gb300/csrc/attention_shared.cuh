@@ -5,9 +5,11 @@
 // read: the leading pages that several have in common, or those of one alone.  Its rows
 // are its sequences' query rows on a kv head, one sequence after the other; they are cut
 // into tiles, and a (segment, kv head, tile) is a run of pages to go through.  The runs
-// lie behind each other, counted in pages, and each CTA takes one even share of them,
-// whole or cut: a run has as many parts as CTAs reach into it, and every part leaves its
-// rows' sums in a slot of its own.  The join adds the slots of a row, in order.
+// lie behind each other, counted in pages, with a lead before each that stands for what it
+// takes to begin and to end one.  Each CTA takes an even share of all that, and of the runs
+// the pages that lie in it: a run has as many parts as CTAs reach into its pages, and
+// every part leaves its rows' sums in a slot of its own.  The join adds the slots of a
+// row, in order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -76,31 +78,48 @@ struct RowAt {
   int tok, row, lo, hi;  // row: token * query heads + head
 };
 
+// The CTAs' shares of the work, the first `rest` of them one larger.
+struct Shares {
+  int share, rest;
+
+  __device__ __forceinline__ void cut(int total, int ctas) {
+    share = total / ctas;
+    rest = total - share * ctas;
+  }
+  __device__ __forceinline__ int start(int cta) const { return cta * share + min(cta, rest); }
+  __device__ __forceinline__ int cta_of(int at) const {
+    const int large = rest * (share + 1);
+    return at < large ? at / (share + 1) : rest + (at - large) / share;
+  }
+};
+
 // Walk over the segments of a plan (all fields alike in the threads that share it).
 struct SharedWalk {
   const int32_t* meta;
-  int n_seg, hkv, G, rows;  // rows of a tile
-  long long total;
+  int n_seg, hkv, G, rows, lead;  // rows of a tile
+  Shares shares;
   // the segment
   int seg, n_rows, mem_at, n_mem, chunk0, pg_at, slot0, cap, first, last;
   // the run, and this CTA's part of it
-  int h, tile, at;     // at: pages before the run
+  int h, tile, at;     // at: work before the run's pages
   int page0, n_pages;  // its first page in the segment's, and how many
   int i, i_end;        // pages of the run
   int stop;            // end of this CTA's share
 
   // This CTA's share; returns its start.
-  __device__ __forceinline__ int begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int cta, int ctas) {
+  __device__ __forceinline__ int begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int run_lead,
+                                       int cta, int ctas) {
     meta = m;
     n_seg = n;
     hkv = kv_heads;
     G = group;
     rows = tile_rows;
-    total = m[n * kSharedSegWords];
-    stop = (int)(total * (cta + 1) / ctas);
-    return (int)(total * cta / ctas);
+    lead = run_lead;
+    shares.cut(m[n * kSharedSegWords], ctas);
+    stop = shares.start(cta + 1);
+    return shares.start(cta);
   }
-  // The run that page `pos` of the work lies in, from there on.  Found anew for each run:
+  // The run that place `pos` of the work lies in, from there on.  Found anew for each run:
   // what a run needs of the plan is not carried through its pages.
   __device__ __forceinline__ void locate(int pos) {
     int lo = 0, hi = n_seg - 1;
@@ -140,32 +159,33 @@ struct SharedWalk {
           hi = mid - 1;
       }
       tile = lo;
-      i = rel - t[2 * tile];
+      rel -= t[2 * tile];
       page0 = t[2 * tile + 1];
-      n_pages = t[2 * tile + 2] - t[2 * tile];
+      n_pages = t[2 * tile + 2] - t[2 * tile] - lead;
     } else {
-      const int run = rel / n_pages;
-      i = rel - run * n_pages;
+      const int run = rel / (n_pages + lead);
+      rel -= run * (n_pages + lead);
       h = run / tiles;
       tile = run - h * tiles;
     }
-    at = pos - i;
+    at = pos - rel + lead;
+    i = max(rel - lead, 0);
     i_end = min(n_pages, stop - at);
   }
-  // Whether this CTA has a part of another run, and the walk to it.
-  __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
-  __device__ __forceinline__ void next() { locate(at + n_pages); }
+  // Whether any page lies in the share; whether this CTA has a part of another run, and
+  // where that begins.
+  __device__ __forceinline__ bool any() const { return i < i_end; }
+  __device__ __forceinline__ bool another() const { return at + n_pages + lead < stop; }
+  __device__ __forceinline__ int following() const { return at + n_pages; }
   __device__ __forceinline__ int here() const { return i_end - i; }  // pages of this CTA's part
   __device__ __forceinline__ int page(int e) const { return meta[pg_at + page0 + e]; }
   __device__ __forceinline__ int block(int e, int) const { return chunk0 + page0 + e; }
   __device__ __forceinline__ int listed(int) const { return 0; }
   // whether keys key0 .. key0 + n - 1 can be seen by any row of the segment
   __device__ __forceinline__ bool seen(int key0, int n) const { return key0 <= last && key0 + n > first; }
-  // The CTA that a page of work lies with, of `ctas`.
-  __device__ __forceinline__ int cta_of(int w, int ctas) const { return (int)(((long long)(w + 1) * ctas - 1) / total); }
   // Parts of this run before this CTA's, and in all.
-  __device__ __forceinline__ int part(int cta, int ctas) const { return cta - cta_of(at, ctas); }
-  __device__ __forceinline__ int parts(int ctas) const { return cta_of(at + n_pages - 1, ctas) - cta_of(at, ctas) + 1; }
+  __device__ __forceinline__ int part(int cta) const { return cta - shares.cta_of(at); }
+  __device__ __forceinline__ int parts() const { return shares.cta_of(at + n_pages - 1) - shares.cta_of(at) + 1; }
   __device__ __forceinline__ int slot_base() const { return slot0; }
   __device__ __forceinline__ int slot_cap() const { return cap; }
   __device__ __forceinline__ bool alone() const { return slot0 == 0 && meta[seg * kSharedSegWords + 11] == cap; }
@@ -195,68 +215,52 @@ struct SharedWalk {
 struct SelectedWalk {
   const int32_t* meta;
   const int32_t* sel;
-  int n_seg, hkv, G, rows, n_sel, stride, cap;
-  long long total;
-  int seg, tok, tok_end, len0, pg_at, tiles, h, tile, at, i, i_end, stop, last;
+  int n_seg, hkv, G, rows, lead, stride, cap, tiles;
+  Shares shares;
+  int tok, pg_at, h, tile, at, i, i_end, stop, last;
   int n_pages;  // entries of a run
 
-  __device__ __forceinline__ void load() {
-    const int32_t* p = meta + seg * kSelSeqWords;
-    tok_end = p[0] + p[1];
-    len0 = p[2] - p[1] - p[0];  // + token: its position
-    pg_at = p[3];
-  }
-  __device__ __forceinline__ void begin(const int32_t* m, int n, const int32_t* selected, int n_select, int list_stride, int slots,
-                                        int n_tok, int kv_heads, int group, int tile_rows, int cta, int ctas) {
+  __device__ __forceinline__ int begin(const int32_t* m, int n, const int32_t* selected, int n_select, int list_stride,
+                                       int slots, int n_tok, int kv_heads, int group, int tile_rows, int run_lead,
+                                       int cta, int ctas) {
     meta = m;
     sel = selected;
     n_seg = n;
     hkv = kv_heads;
     G = group;
     rows = tile_rows;
-    n_sel = n_pages = n_select;
+    lead = run_lead;
+    n_pages = n_select;
     stride = list_stride;
     cap = slots;
     tiles = (G + rows - 1) / rows;
-    total = (long long)n_tok * hkv * tiles * n_sel;
-    const int start = (int)(total * cta / ctas);
-    stop = (int)(total * (cta + 1) / ctas);
-    const int run = start / n_sel, th = run / tiles;
-    i = start - run * n_sel;
+    shares.cut(n_tok * hkv * tiles * (n_pages + lead), ctas);
+    stop = shares.start(cta + 1);
+    return shares.start(cta);
+  }
+  __device__ __forceinline__ void locate(int pos) {
+    const int run = pos / (n_pages + lead), th = run / tiles, rel = pos - run * (n_pages + lead);
     tile = run - th * tiles;
     tok = th / hkv;
     h = th - tok * hkv;
-    at = start - i;
+    at = pos - rel + lead;
+    i = max(rel - lead, 0);
     i_end = min(n_pages, stop - at);
-    int lo = 0, hi = n - 1;
+    int lo = 0, hi = n_seg - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (m[mid * kSelSeqWords] <= tok)
+      if (meta[mid * kSelSeqWords] <= tok)
         lo = mid;
       else
         hi = mid - 1;
     }
-    seg = lo;
-    load();
-    last = len0 + tok;
+    const int32_t* p = meta + lo * kSelSeqWords;
+    last = p[2] - p[1] + (tok - p[0]);  // the token's position
+    pg_at = p[3];
   }
-  __device__ __forceinline__ void next() {
-    at += n_pages;
-    if (++tile == tiles) {
-      tile = 0;
-      if (++h == hkv) {
-        h = 0;
-        if (++tok == tok_end) {
-          ++seg;
-          load();
-        }
-        last = len0 + tok;
-      }
-    }
-    i = 0;
-    i_end = min(n_pages, stop - at);
-  }
-  __device__ __forceinline__ bool another() const { return at + n_pages < stop; }
+  __device__ __forceinline__ bool any() const { return i < i_end; }
+  __device__ __forceinline__ bool another() const { return at + n_pages + lead < stop; }
+  __device__ __forceinline__ int following() const { return at + n_pages; }
   // The block of entry e; one that the token does not see becomes a block behind its last.
   __device__ __forceinline__ int listed(int e) const {
     const int b = __ldg(sel + ((size_t)tok * hkv + h) * stride + e);
@@ -264,9 +268,8 @@ struct SelectedWalk {
   }
   __device__ __forceinline__ int block(int, int got) const { return got; }
   __device__ __forceinline__ bool seen(int key0, int) const { return key0 <= last; }
-  __device__ __forceinline__ int cta_of(int w, int ctas) const { return (int)(((long long)(w + 1) * ctas - 1) / total); }
-  __device__ __forceinline__ int part(int cta, int ctas) const { return cta - cta_of(at, ctas); }
-  __device__ __forceinline__ int parts(int ctas) const { return cta_of(at + n_pages - 1, ctas) - cta_of(at, ctas) + 1; }
+  __device__ __forceinline__ int part(int cta) const { return cta - shares.cta_of(at); }
+  __device__ __forceinline__ int parts() const { return shares.cta_of(at + n_pages - 1) - shares.cta_of(at) + 1; }
   __device__ __forceinline__ int slot_base() const { return 0; }
   __device__ __forceinline__ int slot_cap() const { return cap; }
   __device__ __forceinline__ bool alone() const { return true; }

@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   const int cta = blockIdx.x, ctas = gridDim.x;
+  SharedWalk cur;  // each role finds its runs anew, so that nothing of them is carried through
+  int pos = cur.begin(meta, n_seg, hkv, hq / hkv, kRows, kLead128, cta, ctas);
   if (tid == 0) {
     for (int i = 0; i < 9; ++i) mbar_init(&full_k[i], 1);
     mbar_init(weights, kWeighers / 32);
@@ -211,8 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   const uint32_t tm = *base;
   pdl_wait();
   pdl_trigger();
-  SharedWalk cur;
-  int pos = cur.begin(meta, n_seg, hkv, hq / hkv, kRows, cta, ctas);
   const auto wait = [](uint64_t* bar, int parity) {
     if (!mbar_wait(bar, (uint32_t)parity)) g_err_attention_shared_tc = 1u;
   };
@@ -230,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         }
         __syncwarp();
       };
-      for (int n = 0; pos < cur.stop; pos += cur.here()) {
+      for (int n = 0;; pos = cur.following()) {
         cur.locate(pos);
+        if (!cur.any()) break;  // a share without a page
 #pragma unroll 1
         for (int i = cur.i; i < cur.i_end; ++i, ++n) {
           const int row0 = (cur.page(i) * hkv + cur.h) * kPgKeys, b = n & 1;
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
           if (n > 1) wait(&free_v[b], (n >> 1) - 1 & 1);
           ask(S::v + b * S::tile, &tmv, row0, &full_v[b]);
         }
+        if (!cur.another()) break;
       }
     } else if (warp == (kWeighers + kAdders) / 32 + 1) {
       // ---- the issuing warp; n counts the pages of all its runs.  The tensor core queues a few
@@ -266,8 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       };
       int n = 0;
       bool odd_page = false;  // the last page was one
-      for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+      for (int run = 0;; ++run, pos = cur.following()) {
         cur.locate(pos);
+        if (!cur.any()) break;  // a share without a page
         const int end = n + cur.here();
         wait(queries, run & 1);
         wait(&full_k[n & 1], n >> 1 & 1);
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
           __syncwarp();
         }
         n = end;
+        if (!cur.another()) break;
       }
     }
     __syncwarp();
@@ -320,8 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     // ---- the adders: a thread has half of a row's output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAdderRegs));
     const int d0 = (warp - kWeighers / 32) / 4 * HD;
-    for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+    for (int run = 0;; ++run, pos = cur.following()) {
       cur.locate(pos);
+      if (!cur.any()) break;  // a share without a page
       // where the row goes: to the output where this CTA has all of it, else to a slot
       RowAt at{0, 0, 0, 0x7FFFFFFF};
       float* dst = nullptr;
@@ -330,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       const bool done = cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages;
       if (row < cur.tile_rows()) {
         at = cur.row(row, hq);
-        const int part = cur.part(cta, ctas);
+        const int part = cur.part(cta);
         const size_t slot = (size_t)at.row * to.slots + cur.slot_base() + (done ? 0 : part);
         dst = done ? to.out + (size_t)at.row * D : to.acc + slot * D;
         if (d0 == 0 && !(done && cur.slot_cap() == 1)) {
           stat = to.stat + slot;
-          if (!done && part == 0) empty = cur.slot_cap() - cur.parts(ctas);
+          if (!done && part == 0) empty = cur.slot_cap() - cur.parts();
         }
       }
       float acc[HD];
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       if (lane == 0) arrive(stat_free);
       if (stat) {
         *stat = done ? make_float2(0.0f, -1.0f) : make_float2(-st.x, st.y);
-        for (; empty > 0; --empty) stat[empty + cur.parts(ctas) - 1] = make_float2(0.0f, 0.0f);
+        for (; empty > 0; --empty) stat[empty + cur.parts() - 1] = make_float2(0.0f, 0.0f);
       }
       if (done) {
         const float by = __frcp_rn(st.y);
@@ -429,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
         if (tid == kWeighers) arrive(&free_v[b]);
       }
       __syncwarp();
+      if (!cur.another()) break;
     }
     fence_before();
     __syncthreads();
@@ -438,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   // ---- the weighers: thread (row, part) has half of the row's keys
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeigherRegs));
   const int part = warp >> 2;
-  for (int run = 0; pos < cur.stop; ++run, pos += cur.here()) {
+  for (int run = 0;; ++run, pos = cur.following()) {
     cur.locate(pos);
+    if (!cur.any()) break;  // a share without a page
     const int live = cur.tile_rows();
     {
       // q: a warp takes 16 rows, lanes along them
@@ -623,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     if (part == 0) stats[row] = make_float2(minus, l + top[row]);
     __syncwarp();
     if (lane == 0) arrive(stat_full);
+    if (!cur.another()) break;
     meet();  // the sums have been read
   }
   __syncthreads();

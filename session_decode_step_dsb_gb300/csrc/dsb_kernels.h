@@ -363,14 +363,16 @@ struct SelectArgs {
 };
 cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
 
-// A plan's metadata: n_seg segments of kSharedSegWords (pages of work before it, rows on a
+// A plan's metadata: n_seg segments of kSharedSegWords (work before it, rows on a
 // kv head, where its sequences are and how many, block of its first page, pages, where they
 // are, first slot, slots, first and last key that any row sees, slots of its rows in all,
-// where its tiles are or 0); the pages of work; sequences of kSharedMemWords (first row,
+// where its tiles are or 0); the work in all; sequences of kSharedMemWords (first row,
 // first token, new tokens, length, window); pages; and where tiles of rows see only some of the
-// segment's pages, (pages of the tiles before it, first page) of each tile and the pages of
-// all.
+// segment's pages, (work of the tiles before it, first page) of each tile and the work of all.
 constexpr int kSharedSegWords = 13, kSharedMemWords = 5;
+// What a run counts for besides its pages, in pages: by what it takes to begin and to end
+// one (attention_shared.cu 2 us beside 1.3 a page, attention_shared_tc.cu 4 beside 1.6).
+constexpr int kLead8 = 2, kLead128 = 3;
 // Query rows of a tile of a segment with `rows` of them on a kv head and n pages: 8 of the
 // warp-level kernel (attention_shared.cu) or 128 of the tcgen05 one
 // (attention_shared_tc.cu), whichever takes less of an SM's time, by what they measured:

@@ -124,7 +124,8 @@ struct Segment {
   std::vector<int32_t> table;  // of its tiles, where they see only some of its pages
 
   int tiles() const { return (rows + tile - 1) / tile; }
-  long long pages_a_head() const { return table.empty() ? (long long)tiles() * n : table.back(); }
+  int lead() const { return tile == 8 ? dsbk::kLead8 : dsbk::kLead128; }
+  long long work_a_head() const { return table.empty() ? (long long)tiles() * (n + lead()) : table.back(); }
 };
 
 struct Tree {
@@ -160,7 +161,7 @@ struct Tree {
   }
 
   // Pages that each tile of a sequence's rows sees of its segment, where that is not all:
-  // (pages of the tiles before, first page) of each, and the pages of all.
+  // (work of the tiles before, first page) of each, and the work of all.
   void cut_tiles(Segment* g) const {
     const int s = order[g->m0], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
     int sum = 0;
@@ -171,7 +172,7 @@ struct Tree {
       int a = std::max(from - g->b0, 0), z = std::min(hi / DSB_KV_PAGE - g->b0, g->n - 1);
       if (a > z) a = z = 0;  // none of them: one page, all hidden
       g->table.insert(g->table.end(), {sum, a});
-      sum += z - a + 1;
+      sum += z - a + 1 + g->lead();
       cut = cut || z - a + 1 < g->n;
     }
     g->table.push_back(sum);
@@ -233,7 +234,7 @@ struct Tree {
   void cut_shares(int hkv, int sms) {
     long long work = 0;
     for (const Segment& g : segs)
-      if (g.tile == 128) work += hkv * g.pages_a_head();
+      if (g.tile == 128) work += hkv * g.work_a_head();
     const int share = (int)((work + sms - 1) / sms);
     std::vector<Segment> out;
     std::vector<int> last(segs.size());
@@ -434,7 +435,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         if (1 + n > room)
           return fail(DSB_ERR_UNSUPPORTED, "a call holds at most %zu words of metadata for the pages of %d sequences", room,
                       g.m1 - g.m0);
-        const long long work = hkv * g.pages_a_head();
+        const long long work = hkv * g.work_a_head();
         if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
         if (!open || launches.back().n_words + n > room || launches.back().work + work > INT_MAX / 2) {
           launches.emplace_back();
@@ -498,7 +499,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.m1 - g.m0, g.b0, g.n, pg_at,
                                                     g.slot0,       g.cap,  first,  last,        most, table_at};
         std::copy(rec, rec + dsbk::kSharedSegWords, words.begin() + i * dsbk::kSharedSegWords);
-        work += hkv * g.pages_a_head();
+        work += hkv * g.work_a_head();
       }
       words[l.segs.size() * dsbk::kSharedSegWords] = (int32_t)work;
       dsbk::MetaArg meta;
@@ -654,7 +655,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
     for (const SelLaunch& l : launches) {
       dsbk::PageAttnArgs a = {};
       a.n_select = std::min(n_select, l.most);  // a list's pages come first
-      const long long work = (long long)l.n_tok * hkv * tiles * a.n_select;
+      const long long work = (long long)l.n_tok * hkv * tiles * (a.n_select + dsbk::kLead8);
       if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
       a.ctas = (int)std::min<long long>(resident, work);
       a.sel_cap = a.slots = most_parts(a.n_select, work / a.ctas);
