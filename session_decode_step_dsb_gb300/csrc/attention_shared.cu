@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
     long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, int n_tok,
     const int32_t* __restrict__ selected, int n_select, int sel_stride, int sel_cap, float scale_log2e, PartialsOut to,
-    const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+    bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using R = Ring<D>;
   constexpr int KK = D / 16, NT = D / 8;  // steps of the first product, column tiles of the second
   constexpr bool kThird = Parts<T>::kMore > 1;
@@ -127,15 +127,20 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     fence_mbar_init();
   }
   __syncwarp();
-  pdl_wait();
+  // beside: launched while the call's kernel before works on, whose results are others than
+  // what this one reads and writes; it has ended before this one does
+  if (!beside) pdl_wait();
   pdl_trigger();
 
   Walk cur, ahead;
   if constexpr (std::is_same_v<Walk, SharedWalk>)
-    cur.locate(cur.begin(meta, n_seg, hkv, hq / hkv, kRows, kLead8, cta, ctas));
+    cur.locate(cur.begin(meta, n_seg, wide, hkv, hq / hkv, kRows, kLead8, cta, ctas));
   else
-    cur.locate(cur.begin(meta, n_seg, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, kLead8, cta, ctas));
-  if (!cur.any()) return;
+    cur.locate(cur.begin(meta, n_seg, wide, selected, n_select, sel_stride, sel_cap, n_tok, hkv, hq / hkv, kRows, kLead8, cta, ctas));
+  if (!cur.any()) {
+    pdl_wait();
+    return;
+  }
   ahead = cur;
 
   // ---- asking: entry `e` of ahead's run; 32 entries' blocks and pages in the lanes.  Entries
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
           if constexpr (std::is_same_v<Walk, SharedWalk>)
             list_page = ahead.page(e + lane);
           else
-            list_page = ahead.seen(list_block * kPgKeys, 1) ? meta[ahead.pg_at + got] : 0;
+            list_page = ahead.seen(list_block * kPgKeys, 1) ? ahead.page(got) : 0;
         }
       }
       const int block = __shfl_sync(0xFFFFFFFFu, list_block, e - list_at);
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
             if constexpr (std::is_same_v<Walk, SharedWalk>)
               return cur.page(i);
             else
-              return meta[cur.pg_at + block];
+              return cur.page(block);
           }();
           const T* rows = vp + (((size_t)page * hkv + cur.h) * kPgKeys + 32 * warp) * D;
 #pragma unroll 1
@@ -475,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     if (!cur.another()) break;
     cur.locate(cur.following());
   }
+  pdl_wait();
 }
 
 // One warp per row: the parts' sums at the largest of their references, in slot order.
@@ -567,7 +573,7 @@ cudaError_t pages_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st
   const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
   return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)R::smem, st, tmk, tmv, a.q, a.q_stride, a.hq,
                        a.hkv, static_cast<const T*>(a.v), a.n_seg, a.n_tok, a.selected, a.n_select,
-                       a.sel_stride, a.sel_cap, (float)(1.4426950408889634 / std::sqrt((double)D)), to, w, meta.dev);
+                       a.sel_stride, a.sel_cap, (float)(1.4426950408889634 / std::sqrt((double)D)), to, a.wide_pages, a.beside, w, meta.dev);
 }
 
 template <int D, typename T>

@@ -73,6 +73,12 @@ struct PartialsOut {
   int slots;  // of a row
 };
 
+// Page e of a list: 32-bit numbers, or where the pool has no more than 2^16 pages two to
+// a word.
+__device__ __forceinline__ int page_at(const int32_t* list, int e, bool wide) {
+  return wide ? list[e] : (int)reinterpret_cast<const uint16_t*>(list)[e];
+}
+
 // One row of a tile: its place in q, in out, and the keys that it sees.
 struct RowAt {
   int tok, row, lo, hi;  // row: token * query heads + head
@@ -97,6 +103,7 @@ struct Shares {
 struct SharedWalk {
   const int32_t* meta;
   int n_seg, hkv, G, rows, lead;  // rows of a tile
+  bool wide;
   Shares shares;
   // the segment
   int seg, n_rows, mem_at, n_mem, chunk0, pg_at, slot0, cap, first, last;
@@ -107,10 +114,11 @@ struct SharedWalk {
   int stop;            // end of this CTA's share
 
   // This CTA's share; returns its start.
-  __device__ __forceinline__ int begin(const int32_t* m, int n, int kv_heads, int group, int tile_rows, int run_lead,
-                                       int cta, int ctas) {
+  __device__ __forceinline__ int begin(const int32_t* m, int n, bool wide_pages, int kv_heads, int group, int tile_rows,
+                                       int run_lead, int cta, int ctas) {
     meta = m;
     n_seg = n;
+    wide = wide_pages;
     hkv = kv_heads;
     G = group;
     rows = tile_rows;
@@ -178,7 +186,7 @@ struct SharedWalk {
   __device__ __forceinline__ bool another() const { return at + n_pages + lead < stop; }
   __device__ __forceinline__ int following() const { return at + n_pages; }
   __device__ __forceinline__ int here() const { return i_end - i; }  // pages of this CTA's part
-  __device__ __forceinline__ int page(int e) const { return meta[pg_at + page0 + e]; }
+  __device__ __forceinline__ int page(int e) const { return page_at(meta + pg_at, page0 + e, wide); }
   __device__ __forceinline__ int block(int e, int) const { return chunk0 + page0 + e; }
   __device__ __forceinline__ int listed(int) const { return 0; }
   // whether keys key0 .. key0 + n - 1 can be seen by any row of the segment
@@ -216,14 +224,16 @@ struct SelectedWalk {
   const int32_t* meta;
   const int32_t* sel;
   int n_seg, hkv, G, rows, lead, stride, cap, tiles;
+  bool wide;
   Shares shares;
   int tok, pg_at, h, tile, at, i, i_end, stop, last;
   int n_pages;  // entries of a run
 
-  __device__ __forceinline__ int begin(const int32_t* m, int n, const int32_t* selected, int n_select, int list_stride,
-                                       int slots, int n_tok, int kv_heads, int group, int tile_rows, int run_lead,
+  __device__ __forceinline__ int begin(const int32_t* m, int n, bool wide_pages, const int32_t* selected, int n_select,
+                                       int list_stride, int slots, int n_tok, int kv_heads, int group, int tile_rows, int run_lead,
                                        int cta, int ctas) {
     meta = m;
+    wide = wide_pages;
     sel = selected;
     n_seg = n;
     hkv = kv_heads;
@@ -266,6 +276,7 @@ struct SelectedWalk {
     const int b = __ldg(sel + ((size_t)tok * hkv + h) * stride + e);
     return b >= 0 && b <= last / kPgKeys ? b : last / kPgKeys + 1;
   }
+  __device__ __forceinline__ int page(int b) const { return page_at(meta + pg_at, b, wide); }
   __device__ __forceinline__ int block(int, int got) const { return got; }
   __device__ __forceinline__ bool seen(int key0, int) const { return key0 <= last; }
   __device__ __forceinline__ int part(int cta) const { return cta - shares.cta_of(at); }

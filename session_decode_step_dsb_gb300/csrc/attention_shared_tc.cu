@@ -174,7 +174,7 @@ template <int D, typename T, int N>
 __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
     long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, float scale_log2e, PartialsOut to,
-    const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+    bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using S = Smem<D, T>;
   constexpr int PARTS = S::parts, HD = D / 2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   const int32_t* meta = N > 1 ? words.w : meta_dev;
   const int cta = blockIdx.x, ctas = gridDim.x;
   SharedWalk cur;  // each role finds its runs anew, so that nothing of them is carried through
-  int pos = cur.begin(meta, n_seg, hkv, hq / hkv, kRows, kLead128, cta, ctas);
+  int pos = cur.begin(meta, n_seg, wide, hkv, hq / hkv, kRows, kLead128, cta, ctas);
   if (tid == 0) {
     for (int i = 0; i < 9; ++i) mbar_init(&full_k[i], 1);
     mbar_init(weights, kWeighers / 32);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   __syncthreads();
   fence_after();
   const uint32_t tm = *base;
-  pdl_wait();
+  if (!beside) pdl_wait();  // as in attention_pages_kernel
   pdl_trigger();
   const auto wait = [](uint64_t* bar, int parity) {
     if (!mbar_wait(bar, (uint32_t)parity)) g_err_attention_shared_tc = 1u;
@@ -637,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   if (warp == 0) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+    pdl_wait();
   }
 }
 
@@ -658,7 +659,7 @@ cudaError_t tc_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st) {
     const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
     return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)S::bytes, st, tmk, tmv, a.q, a.q_stride,
                          a.hq, a.hkv, static_cast<const T*>(a.v), a.n_seg,
-                         (float)(1.4426950408889634 / std::sqrt((double)D)), to, w, meta.dev);
+                         (float)(1.4426950408889634 / std::sqrt((double)D)), to, a.wide_pages, a.beside, w, meta.dev);
   });
 }
 

@@ -349,7 +349,7 @@ cudaError_t launch_page_bounds(const void* k, int dtype, int hkv, int head_dim, 
                                const MetaArg& meta, cudaStream_t st);
 
 // Metadata of the selection and of the attention over selected pages: of each sequence its
-// first token, new tokens, length, and where its pages are; then the pages.
+// first token, new tokens, length, and where its pages are; then the pages (see wide_pages).
 constexpr int kSelSeqWords = 4;
 struct SelectArgs {
   const float* q;
@@ -360,6 +360,7 @@ struct SelectArgs {
   int32_t* selected;  // [n_tok][hkv][n_select]
   int ranks;          // CTAs of a cluster, which share the pages of a (token, kv head)
   int max_pages;      // of a sequence
+  bool wide_pages;    // page numbers of 32 bits, else two to a word
 };
 cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, const MetaArg& meta, cudaStream_t st);
 
@@ -400,6 +401,8 @@ struct PageAttnArgs {
   float* out;               // [n_tok][hq][head_dim]
   int slots;
   int ctas;
+  bool wide_pages;          // page numbers of 32 bits, else two to a word
+  bool beside;              // launched while the call's kernel before works on
 };
 // CTAs that the GPU runs at once.
 int page_attn_resident(int sms);

@@ -112,6 +112,21 @@ dsb_status copy_common(const std::vector<void*>& planes, size_t plane_bytes, int
 
 constexpr int kMaxPools = 512;
 
+// Lists of page numbers take a word each, or where the pool's have 16 bits half of one.
+bool wide_pages(const dsb_kv_pages* kv) { return kv->n_pages > 1 << 16; }
+size_t page_words(int n, bool wide) { return wide ? (size_t)n : ((size_t)n + 1) / 2; }
+template <typename Page>
+void put_pages(std::vector<int32_t>* words, int n, bool wide, Page page) {
+  const size_t at = words->size();
+  words->resize(at + page_words(n, wide));
+  if (wide) {
+    for (int i = 0; i < n; ++i) (*words)[at + i] = page(i);
+  } else {
+    uint16_t* to = reinterpret_cast<uint16_t*>(words->data() + at);
+    for (int i = 0; i < n; ++i) to[i] = (uint16_t)page(i);
+  }
+}
+
 // ---- the plan of an attention over shared pages -------------------------------------
 
 struct Segment {
@@ -284,6 +299,14 @@ int most_parts(int n, long long share) {
   return n == 1 ? 1 : (int)std::min<long long>(n, (n - 2) / share + 2);
 }
 
+// While it lives, launches may start before the stream's kernel before them has ended
+// (they wait for it themselves).
+struct Overlap {
+  const bool was = dsbk::pdl();
+  explicit Overlap(bool on) { dsbk::set_pdl(on || was); }
+  ~Overlap() { dsbk::set_pdl(was); }
+};
+
 // Segments of one launch, all of one height of tiles.
 struct Launch {
   int tile;
@@ -299,10 +322,10 @@ struct SelLaunch {
   int n_seq = 0, tok0 = 0, n_tok = 0, most = 0;
 };
 
-dsb_status selection_launches(const dsb_paged_batch* b, cudaStream_t cs, std::vector<SelLaunch>* out) {
+dsb_status selection_launches(const dsb_paged_batch* b, bool wide, cudaStream_t cs, std::vector<SelLaunch>* out) {
   const auto pages = [&](int s) { return b->new_tokens[s] == 0 ? 0 : (b->seq_lens[s] - 1) / DSB_KV_PAGE + 1; };
   size_t all = 0;
-  for (int s = 0; s < b->n_seq; ++s) all += dsbk::kSelSeqWords + pages(s);
+  for (int s = 0; s < b->n_seq; ++s) all += dsbk::kSelSeqWords + page_words(pages(s), wide);
   size_t room = kMetaWords;
   if (all > (size_t)dsbk::kParamWords) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -322,10 +345,9 @@ dsb_status selection_launches(const dsb_paged_batch* b, cudaStream_t cs, std::ve
       l.words.insert(l.words.end(), {l.n_tok, b->new_tokens[s], b->seq_lens[s], at});
       l.n_tok += b->new_tokens[s];
       l.most = std::max(l.most, pages(s));
-      at += pages(s);
+      at += (int)page_words(pages(s), wide);
     }
-    for (int s : mine)
-      for (int i = 0; i < pages(s); ++i) l.words.push_back(page_of(b, s, i));
+    for (int s : mine) put_pages(&l.words, pages(s), wide, [&](int i) { return page_of(b, s, i); });
     tok += l.n_tok;
     out->push_back(std::move(l));
     mine.clear();
@@ -333,7 +355,7 @@ dsb_status selection_launches(const dsb_paged_batch* b, cudaStream_t cs, std::ve
   };
   for (int s = 0; s < b->n_seq; ++s) {
     if (b->new_tokens[s] == 0) continue;
-    const size_t need = dsbk::kSelSeqWords + (size_t)pages(s);
+    const size_t need = dsbk::kSelSeqWords + page_words(pages(s), wide);
     if (need > room) return fail(DSB_ERR_UNSUPPORTED, "sequence %d: a call holds at most %zu words of metadata", s, room);
     if (have + need > room) close();
     mine.push_back(s);
@@ -411,8 +433,10 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     tree.cut_shares(hkv, dev.sms);
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
+    const bool wide = wide_pages(kv);
     const auto words_of = [&](const Segment& g) {
-      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords + g.n + g.table.size();
+      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords +
+             page_words(g.n, wide) + g.table.size();
     };
 
     // launches: what a captured call keeps has to ride in its parameters
@@ -475,8 +499,13 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     a.stat = a.acc + rows * slots * D;
     a.out = out;
     a.slots = slots;
-    std::vector<int32_t> words;
-    for (const Launch& l : launches) {
+    a.wide_pages = wide;
+    // all metadata before the first launch: a copy between two would keep them apart
+    std::vector<std::vector<int32_t>> metas(launches.size());
+    std::vector<dsbk::MetaArg> args(launches.size());
+    for (size_t li = 0; li < launches.size(); ++li) {
+      const Launch& l = launches[li];
+      std::vector<int32_t>& words = metas[li];
       words.assign(l.segs.size() * dsbk::kSharedSegWords + 1, 0);
       words.reserve(l.n_words);
       long long work = 0;
@@ -493,7 +522,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
           most = std::max(most, slots_of(s));
         }
         const int pg_at = (int)words.size();
-        for (int p = 0; p < g.n; ++p) words.push_back(page_of(b, tree.order[g.m0], g.b0 + p));
+        put_pages(&words, g.n, wide, [&](int p) { return page_of(b, tree.order[g.m0], g.b0 + p); });
         const int table_at = g.table.empty() ? 0 : (int)words.size();
         words.insert(words.end(), g.table.begin(), g.table.end());
         const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.m1 - g.m0, g.b0, g.n, pg_at,
@@ -502,16 +531,20 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         work += hkv * g.work_a_head();
       }
       words[l.segs.size() * dsbk::kSharedSegWords] = (int32_t)work;
-      dsbk::MetaArg meta;
-      if ((st = meta_arg(ws, words, cs, &meta)) != DSB_OK) return st;
+      if ((st = meta_arg(ws, words, cs, &args[li])) != DSB_OK) return st;
+    }
+    for (size_t li = 0; li < launches.size(); ++li) {
+      const Launch& l = launches[li];
       a.n_seg = (int)l.segs.size();
       a.ctas = l.ctas;
-      const cudaError_t e = l.tile == 8 ? dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs)
-                                        : dsbk::launch_attention_shared_tc(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
+      a.beside = li > 0;  // no kernel of the call reads or writes what another one writes
+      const Overlap overlap(a.beside);
+      const cudaError_t e = l.tile == 8 ? dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, args[li], cs)
+                                        : dsbk::launch_attention_shared_tc(a, kv->dtype == DSB_F16 ? 0 : 1, D, args[li], cs);
       if (e != cudaSuccess) return cuda_fail(e, "attention_decode_shared launch");
     }
     // the join, where a row's sums lie in parts
-    words.clear();
+    std::vector<int32_t> words;
     bool join = false;
     for (int s = 0; s < b->n_seq; ++s) {
       if (b->new_tokens[s] == 0) continue;
@@ -526,6 +559,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     dsbk::MetaArg meta;
     meta.host = words.data();
     meta.n_words = (int)words.size();
+    const Overlap overlap(true);
     const cudaError_t e = dsbk::launch_attention_join(a, (int)words.size() / 2, D, meta, cs);
     return e == cudaSuccess ? DSB_OK : cuda_fail(e, "attention_decode_shared join");
   });
@@ -596,13 +630,13 @@ dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, 
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
     std::vector<SelLaunch> launches;
-    if ((st = selection_launches(b, cs, &launches)) != DSB_OK) return st;
+    if ((st = selection_launches(b, wide_pages(kv), cs, &launches)) != DSB_OK) return st;
     for (const SelLaunch& l : launches) {
       dsbk::MetaArg meta;
       if ((st = meta_arg(ws, l.words, cs, &meta)) != DSB_OK) return st;
       // CTAs of a cluster: while they find SMs and each has a round of pages of its own
       int ranks = 1;
-      while (ranks < 8 && (long long)l.n_tok * hkv * ranks * 2 <= 2 * dev.sms && ranks * 128 < l.most) ranks *= 2;
+      while (ranks < 8 && (long long)l.n_tok * hkv * ranks * 2 <= 4 * dev.sms && ranks * 128 < l.most) ranks *= 2;
       const dsbk::SelectArgs a{q + (size_t)l.tok0 * q_stride,
                                q_stride,
                                n_q_heads,
@@ -615,7 +649,8 @@ dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, 
                                keep_last,
                                selected + (size_t)l.tok0 * hkv * n_select,
                                ranks,
-                               l.most};
+                               l.most,
+                               wide_pages(kv)};
       const cudaError_t e = dsbk::launch_select_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, meta, cs);
       if (e != cudaSuccess) return cuda_fail(e, "kv_select_pages launch");
     }
@@ -649,7 +684,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
     std::vector<SelLaunch> launches;
-    if ((st = selection_launches(b, cs, &launches)) != DSB_OK) return st;
+    if ((st = selection_launches(b, wide_pages(kv), cs, &launches)) != DSB_OK) return st;
     const int tiles = (n_q_heads / hkv + 7) / 8, resident = dsbk::page_attn_resident(dev.sms);
     std::vector<dsbk::PageAttnArgs> args;
     for (const SelLaunch& l : launches) {
@@ -676,6 +711,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
       a.acc = reinterpret_cast<float*>(partial_base(ws));
       a.stat = a.acc + (size_t)l.n_tok * n_q_heads * a.slots * D;
       a.out = out + (size_t)l.tok0 * width;
+      a.wide_pages = wide_pages(kv);
       args.push_back(a);
     }
     for (size_t i = 0; i < launches.size(); ++i) {
@@ -689,6 +725,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
       dsbk::MetaArg one;
       one.host = words;
       one.n_words = 2;
+      const Overlap overlap(true);
       e = dsbk::launch_attention_join(a, 1, D, one, cs);
       if (e != cudaSuccess) return cuda_fail(e, "attention_decode_selected join");
     }

@@ -105,46 +105,33 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 constexpr uint32_t kAlways = 0xFFFFFFFFu;
 
-// Pairwise sum, neighbours first, of values that come one after the other, as if zeros
+// Pairwise sum, neighbours first, of values that come eight at a time, as if zeros
 // followed up to a power of two.
 struct Pairwise {
-  float held[16];
-  int n = 0;
-  __device__ __forceinline__ void add(float x) {
+  float held[14];  // sums of 8, 16, .. values that wait for their neighbours
+  int n = 0;       // eights so far
+  __device__ __forceinline__ void add(const float (&v)[8]) {
+    float x = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
+                        __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7])));
     int level = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (!((n >> i) & 1)) break;
-      x = __fadd_rn(held[i], x);
-      level = i + 1;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i == level) held[i] = x;
+#pragma unroll 1
+    for (; n >> level & 1; ++level) x = __fadd_rn(held[level], x);
+    held[level] = x;
     ++n;
   }
   __device__ __forceinline__ float sum() const {
     float x = 0.0f;
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if ((n >> i) & 1) {
-        x = any ? __fadd_rn(held[i], x) : held[i];
-        any = true;
-      }
+#pragma unroll 1
+    for (int level = 0; n >> level; ++level)
+      if (n >> level & 1) x = __fadd_rn(held[level], x);
     return x;
   }
 };
 
-struct SelMeta {
-  int tok0, n_new, len, pg_at;
-};
-static_assert(kSelSeqWords == 4, "SelMeta");
-
 template <int D, typename T, int N>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(
+__global__ void __launch_bounds__(kSelThreads, 4) select_pages_kernel(
     const float* __restrict__ q, long long q_stride, int hq, int hkv, const uint4* __restrict__ bounds, int n_seq,
-    int n_select, int keep_first, int keep_last, int32_t* __restrict__ selected,
+    int n_select, int keep_first, int keep_last, int32_t* __restrict__ selected, bool wide,
     const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   constexpr int L = D / 8;                // lanes to a page
   constexpr int AT = kSelThreads / L;     // pages at a time
@@ -176,6 +163,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(
   const int mine = (rec[2] - rec[1] + (t - rec[0])) / kPageKeys;  // the token's own page
   const int n = mine + 1;                                         // pages that it sees
   const int32_t* pages = meta + rec[3];
+  const auto page_of = [&](int j) { return wide ? pages[j] : (int)reinterpret_cast<const uint16_t*>(pages)[j]; };
   int32_t* out = selected + ((size_t)t * hkv + h) * n_select;
   if (n <= n_select) {  // the same in every CTA of the cluster
     if (rank == 0)
@@ -188,17 +176,18 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(
   if (tid < D) {
     const float* row = q + (size_t)t * q_stride + (size_t)h * G * D + tid;
     Pairwise a, b;
+#pragma unroll 1
     for (int r0 = 0; r0 < G; r0 += 8) {
-      float x[8];
+      float x[8], y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = r0 + i < G ? __ldg(row + (size_t)(r0 + i) * D) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r0 + i < G) {
-          // a NaN stays one in both
-          a.add(x[i] < 0.0f ? 0.0f : x[i]);
-          b.add(x[i] > 0.0f ? 0.0f : x[i]);
-        }
+      for (int i = 0; i < 8; ++i) {  // a NaN stays one in both
+        y[i] = x[i] > 0.0f ? 0.0f : x[i];
+        x[i] = x[i] < 0.0f ? 0.0f : x[i];
+      }
+      a.add(x);
+      b.add(y);
     }
     ab[0][tid] = a.sum();
     ab[1][tid] = b.sum();
@@ -219,7 +208,7 @@ __global__ void __launch_bounds__(kSelThreads) select_pages_kernel(
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * AT + tid / L;
       if (j < n) {
-        const uint4* src = bounds + ((size_t)pages[j] * hkv + h) * 2 * L + part;
+        const uint4* src = bounds + ((size_t)page_of(j) * hkv + h) * 2 * L + part;
         lo[u] = __ldg(src);
         hi[u] = __ldg(src + L);
       } else {
@@ -332,6 +321,11 @@ cudaError_t select_go(const SelectArgs& a, const MetaArg& meta, cudaStream_t st)
     cfg.gridDim = dim3((unsigned)a.ranks, (unsigned)a.hkv, (unsigned)a.n_tok);
     cfg.blockDim = dim3(kSelThreads);
     cfg.dynamicSmemBytes = (size_t)a.max_pages * 4;
+    if (cfg.dynamicSmemBytes > 40 * 1024) {  // past what a launch has without asking (beside 2 KB of static)
+      const cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)cfg.dynamicSmemBytes);
+      if (e != cudaSuccess) return e;
+    }
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -341,7 +335,7 @@ cudaError_t select_go(const SelectArgs& a, const MetaArg& meta, cudaStream_t st)
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, select_pages_kernel<D, T, N>, a.q, a.q_stride, a.hq, a.hkv,
                               static_cast<const uint4*>(a.bounds), a.n_seq, a.n_select, a.keep_first, a.keep_last,
-                              a.selected, w, meta.dev);
+                              a.selected, a.wide_pages, w, meta.dev);
   });
 }
 
