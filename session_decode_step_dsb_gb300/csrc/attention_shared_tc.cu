@@ -456,20 +456,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       const int r0 = 16 * warp, mine_q = r0 + lane % 16;
       if (mine_q < live) its = cur.row(mine_q, hq);
       its.row -= its.tok * hq;
-      {
-        float4 x[16 / ROWS];
+      // four loads on their way while four rows are cut into parts
+      float4 x[4], y[4];
+      const auto load = [&](int j, float4* to) {
 #pragma unroll
-        for (int i = 0; i < 16 / ROWS; ++i) {
-          const int r = i * ROWS + lane / LANES;
+        for (int i = 0; i < 4; ++i) {
+          const int r = (j + i) * ROWS + lane / LANES;
           const int tok = __shfl_sync(0xFFFFFFFFu, its.tok, r), head = __shfl_sync(0xFFFFFFFFu, its.row, r);
-          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r0 + r < live) x[i] = __ldg(reinterpret_cast<const float4*>(q + (size_t)tok * q_stride + (size_t)head * D) + l);
+          to[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r0 + r < live) to[i] = __ldg(reinterpret_cast<const float4*>(q + (size_t)tok * q_stride + (size_t)head * D) + l);
         }
+      };
+      load(0, x);
+#pragma unroll 1
+      for (int j = 0; j < 16 / ROWS; j += 4) {
+        if (j + 4 < 16 / ROWS) load(j + 4, y);
 #pragma unroll
-        for (int i = 0; i < 16 / ROWS; ++i) {
-          const int r = r0 + i * ROWS + lane / LANES;
-          x[i] = make_float4(x[i].x * scale_log2e, x[i].y * scale_log2e, x[i].z * scale_log2e, x[i].w * scale_log2e);
-          float m = fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + (j + i) * ROWS + lane / LANES;
+          float v[4] = {x[i].x * scale_log2e, x[i].y * scale_log2e, x[i].z * scale_log2e, x[i].w * scale_log2e};
+          float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
           for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
           // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
@@ -477,14 +483,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
           const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
           const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
           if (l == 0) top[r] = __uint_as_float((uint32_t)(ex - 10) << 23);
-          float x0 = x[i].x * inv, x1 = x[i].y * inv, x2 = x[i].z * inv, x3 = x[i].w * inv;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] *= inv;
           const int piece = l >> 1;
           uint8_t* dst = smem + S::q + (piece >> 3) * S::slab + r * 128 + (((piece & 7) ^ (r & 7)) << 4) + (l & 1) * 8;
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            const uint32_t w0 = Parts<T>::take(x0, x1), w1 = Parts<T>::take(x2, x3);
+            const uint32_t w0 = Parts<T>::take(v[0], v[1]), w1 = Parts<T>::take(v[2], v[3]);
             *reinterpret_cast<uint2*>(dst + p * S::tile) = make_uint2(w0, w1);
           }
+          x[i] = y[i];
         }
       }
     }
