@@ -97,14 +97,14 @@ def attention(q, k, v, bt, n_blocks, window, new, lens, selected=None, weight_st
         w = int(window[s])
         for h in range(hq):
             if selected is None:
-                keys = range(max(0, p - w + 1) if w else 0, p + 1)
+                keys = np.arange(max(0, p - w + 1) if w else 0, p + 1)
             else:
-                keys = [i for b in selected[t, h // group] if 0 <= b <= p // PAGE
-                        for i in range(b * PAGE, min(p + 1, (b + 1) * PAGE))]
+                keys = np.array([i for b in selected[t, h // group] if 0 <= b <= p // PAGE
+                                 for i in range(b * PAGE, min(p + 1, (b + 1) * PAGE))], int)
             if len(keys) == 0:
                 continue
-            at = [paged.locate(i, bt[s], int(n_blocks[s]), w) for i in keys]
-            pages, rows = np.array([a[0] for a in at]), np.array([a[1] for a in at])
+            block = keys // PAGE % int(n_blocks[s]) if w else keys // PAGE     # as paged.locate
+            pages, rows = np.asarray(bt[s])[block], keys % PAGE
             kk, vv = k[pages, h // group, rows], v[pages, h // group, rows]
             x = q[t, h].astype(np.float64)
             score = kk @ x / math.sqrt(d)

@@ -378,6 +378,9 @@ constexpr int kLead8 = 2, kLead128 = 3;
 // warp-level kernel (attention_shared.cu) or 128 of the tcgen05 one
 // (attention_shared_tc.cu), whichever takes less of an SM's time, by what they measured:
 // a page of a tile 0.6 and 1.6 us, and 4 us for a tile of the latter to begin and end.
+// (The unit is 0.2 us.)  The latter's launch beside the other one takes 10 us longer on
+// every SM, which it has to save.
+constexpr int kWideCost = 50;
 inline long long shared_tile_cost(int rows, int n, int tile) {
   const long long tiles = (rows + tile - 1) / tile;
   return tile == 8 ? 3 * tiles * n : tiles * (8LL * n + 20);

@@ -146,6 +146,7 @@ struct Segment {
 struct Tree {
   const dsb_paged_batch* b;
   int G;
+  bool wide;               // tiles of 128 rows are taken where they cost less
   std::vector<int> order;  // sequences with new tokens; a segment's are side by side
   std::vector<Segment> segs;
   std::vector<int> end;    // last segment of a sequence's path
@@ -162,7 +163,8 @@ struct Tree {
     return r;
   }
   // What n pages cost a segment of so many rows.
-  static long long cost(int rows, int n) { return dsbk::shared_tile_cost(rows, n, dsbk::shared_tile_rows(rows, n)); }
+  int tile_of(int rows, int n) const { return wide ? dsbk::shared_tile_rows(rows, n) : 8; }
+  long long cost(int rows, int n) const { return dsbk::shared_tile_cost(rows, n, tile_of(rows, n)); }
 
   // Whether pages that m1 - m0 sequences have in common are worth a segment: they save the
   // sequences' own tiles, but a tile that ends there begins once more behind them, which
@@ -199,7 +201,7 @@ struct Tree {
     for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {
       Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0)};
       s.rows = rows_of(m0, m1);
-      s.tile = dsbk::shared_tile_rows(s.rows, b1 - b0);
+      s.tile = tile_of(s.rows, b1 - b0);
       if (m1 - m0 == 1 && s.tiles() > 1) cut_tiles(&s);
       parent = (int)segs.size();
       segs.push_back(s);
@@ -250,12 +252,12 @@ struct Tree {
     long long work = 0;
     for (const Segment& g : segs)
       if (g.tile == 128) work += hkv * g.work_a_head();
-    const int share = (int)((work + sms - 1) / sms);
+    const int share = std::max(16, (int)((work + sms - 1) / sms));  // (shorter pieces would be mostly ends)
     std::vector<Segment> out;
     std::vector<int> last(segs.size());
     for (size_t i = 0; i < segs.size(); ++i) {
       const Segment& g = segs[i];
-      const bool cut = g.tile == 128 && g.tiles() > 1 && g.table.empty() && share > 0;
+      const bool cut = g.tile == 128 && g.tiles() > 1 && g.table.empty();
       const int pieces = cut ? std::max(1, (g.n + share / 2) / share) : 1;
       int parent = g.parent >= 0 ? last[g.parent] : -1;
       for (int k = 0; k < pieces; ++k) {
@@ -426,10 +428,18 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = check_workspace(ws)) != DSB_OK) return st;
 
-    Tree tree{b, n_q_heads / hkv, {}, {}, {}};
-    tree.build();
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
+    Tree tree{b, n_q_heads / hkv, true, {}, {}, {}};
+    tree.build();
+    // the tcgen05 kernel's launch has to save what it takes
+    long long saved = 0;
+    for (const Segment& g : tree.segs)
+      saved += dsbk::shared_tile_cost(g.rows, g.n, 8) - dsbk::shared_tile_cost(g.rows, g.n, g.tile);
+    if (saved > 0 && saved * hkv < (long long)dsbk::kWideCost * dev.sms) {
+      tree = Tree{b, n_q_heads / hkv, false, {}, {}, {}};
+      tree.build();
+    }
     tree.cut_shares(hkv, dev.sms);
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;

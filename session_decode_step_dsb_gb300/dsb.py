@@ -497,6 +497,7 @@ def kv_pages(k_pool, v_pool, dtype: int) -> KVPages:
     _need(v_pool, 2 * v_pool.numel(), "v_pool", "16")
     kv = KVPages(_ptr(k_pool), _ptr(v_pool), dtype, n_pages, hkv, d)
     kv._tensors = (k_pool, v_pool)
+    kv._device = k_pool.get_device() if v_pool.get_device() == k_pool.get_device() else -1
     return kv
 
 
@@ -782,6 +783,7 @@ def kv_q4_pages(pool, head_dim: int) -> KVQ4Pages:
         raise ValueError(f"pool must be [n_pages, Hkv, {KV_PAGE * (head_dim + 8)}], got {tuple(pool.shape)}")
     kv = KVQ4Pages(_ptr(pool), pool.shape[0], pool.shape[1], head_dim)
     kv._tensors = (pool,)
+    kv._device = pool.get_device()
     return kv
 
 
@@ -855,17 +857,16 @@ SIGNATURES.update({
 
 
 def _copy_pages(fn, kind, pools, src, dst, keys, stream):
-    pools = list(pools)
-    if not pools or not all(isinstance(p, kind) for p in pools):
+    n = len(pools)
+    if n == 0 or {type(p) for p in pools} != {kind}:
         raise ValueError(f"pools must be a sequence of {kind.__name__}, one for each layer")
     sa, ps = _host_i32(src, np.size(src), "src")
     da, pd = _host_i32(dst, sa.size, "dst")
     ka, pk = _host_i32(keys, sa.size, "keys")
     dev = _current_device(pools[0]._tensors[0], "the page pool")
-    for p in pools:
-        for t in p._tensors:
-            _dev_ptr(t, dev, "the page pool")
-    _check(fn((kind * len(pools))(*pools), len(pools), ps, pd, pk, sa.size, _raw_stream(stream, dev)))
+    if {p._device for p in pools} != {dev}:
+        raise ValueError(f"the page pools must live on cuda:{dev}")
+    _check(fn((kind * n)(*pools), n, ps, pd, pk, sa.size, _raw_stream(stream, dev)))
 
 
 def kv_copy_pages(pools, src, dst, keys, stream=None):
@@ -888,8 +889,8 @@ def _paged_q(q, kv: KVPages, batch: PagedBatch, out, stream):
     n_tok, hq, d = q.shape
     stride = _row_stride(q, batch.n_tok, (hq, d), "q")
     dev = _current_device(q, "q")
-    for t in kv._tensors:
-        _dev_ptr(t, dev, "the page pool")
+    if kv._device != dev:
+        raise ValueError(f"the page pool must live on cuda:{dev}")
     if out is None:
         out = _empty_on(stream, (n_tok, hq, d), torch.float32, q.device)
     elif out is not False:

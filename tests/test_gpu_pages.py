@@ -377,3 +377,204 @@ def test_a_forked_session_goes_on_like_its_parent(kind):
     assert np.array_equal(to_host(sel), want_sel)
     want, bound = op.attention(host, k, v, table, [9, 9, 8], [0] * 3, new, lens, want_sel, weight_step=_step(kind))
     _check(sparse, want, bound, "sparse")
+
+
+# --------------------------- rows enough for the tcgen05 kernel (128 of them to a tile)
+WIDE = [
+    # a prompt on nothing; drafts of 16 sessions behind a prompt; many tiles on pages that are cut by CTAs' shares;
+    # prompts behind a shared prefix, one of a single token
+    ("f16", 10, 2, 128, 1, 1, 0, 0, [600], [600]),
+    ("bf16", 40, 8, 64, 1, 16, 16, 0, [5 + 9 * i for i in range(16)], [4] * 14 + [1, 3]),
+    ("f16", 32, 4, 128, 1, 30, 40, 0, [1 + i for i in range(30)], [1] * 30),
+    ("bf16", 20, 2, 128, 1, 3, 2, 0, [300, 129, 1], [300, 129, 1]),
+    ("f16", 64, 1, 64, 2, 2, 3, 1, [200, 100, 128, 257], [200, 7, 128, 30]),
+]
+
+
+@pytest.mark.parametrize("kind,hq,hkv,D,groups,per,common,branch,tails,new", WIDE)
+def test_wide_tiles_match_the_oracle(kind, hq, hkv, D, groups, per, common, branch, tails, new):
+    d, rng = _dsb(), np.random.default_rng(sum(tails) + hq + D)
+    table, blocks, lens, total = _tree(rng, groups, per, common, branch, tails)
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32) * 2
+    window = [0] * len(lens)
+    got = _attend(to_dev(q), dev, kind, table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step(kind))
+    _check(got, want, bound)
+    again = _attend(to_dev(q), dev, kind, table, blocks, window, new, lens)
+    assert _torch().equal(got, again)
+    d.device_error()
+
+
+def test_wide_tiles_on_rings():
+    """Prompts under a window, and a long one whose tiles see other pages each."""
+    rng = np.random.default_rng(21)
+    new, window, lens = [400, 300, 250], [200, 0, 1], [1500, 700, 250]
+    blocks = [(200 + 400 - 2) // P + 2, 6, 3]
+    table = np.zeros((3, 8), np.int32)
+    order = rng.permutation(20)
+    for s, b in enumerate(blocks):
+        table[s, :b] = order[6 * s:6 * s + b]
+    dev, (k, v) = _pools(rng, 20, 1, 64, "bf16")
+    q = rng.standard_normal((sum(new), 12, 64)).astype(np.float32)
+    got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step("bf16"))
+    _check(got, want, bound)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_wide_tiles_leave_hidden_values_out(kind):
+    """Infinite and NaN values of keys that only later tokens see, several to a page, and of no
+    token's: rows that do not see them are as without."""
+    t, rng = _torch(), np.random.default_rng(22)
+    n, hq, hkv, D = 600, 10, 2, 128
+    table, blocks, lens, total = _tree(rng, 1, 2, 1, 0, [n, n])
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    q = rng.standard_normal((2 * n, hq, D)).astype(np.float32)
+    args = (kind, table, blocks, [0, 0], [n, n], lens)
+    clean = to_host(_attend(to_dev(q), dev, *args))
+    for s in (0, 1):                                         # behind the last keys
+        dev[0][int(table[s, -1]), :, lens[s] % P:] = float("nan")
+        dev[1][int(table[s, -1]), :, lens[s] % P:] = float("-inf")
+    assert np.array_equal(to_host(_attend(to_dev(q), dev, *args)), clean)
+    first = P + 300                                          # sequence 0's keys from position 428 on
+    for p, value in ((first, "inf"), (first + 1, "nan"), (first + 57, "-inf"), (first + 200, "nan"), (lens[0] - 1, "inf")):
+        dev[1][int(table[0, p // P]), :, p % P] = float(value)
+    got = to_host(_attend(to_dev(q), dev, *args))
+    want, bound = op.attention(q, k, v, table, blocks, [0, 0], [n, n], lens, weight_step=_step(kind))
+    keep = np.ones(2 * n, bool)
+    keep[300:n] = False
+    assert (np.abs(got - want)[keep] <= bound[keep]).all()
+    assert not np.isfinite(got[300:n]).any()
+
+
+def test_wide_tiles_on_streams_and_in_graphs():
+    """Calls of both kernels on two streams at once, each with a workspace of its own, and two
+    graphs that share one."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(23)
+    kind, hq, hkv, D = "bf16", 40, 8, 64
+    table, blocks, lens, total = _tree(rng, 1, 16, 16, 0, [5 + 9 * i for i in range(16)])
+    new = [4] * 16
+    dev, _ = _pools(rng, total, hkv, D, kind)
+    qs = [to_dev(rng.standard_normal((64, hq, D)).astype(np.float32)) for _ in range(2)]
+    want = [_attend(q, dev, kind, table, blocks, [0] * 16, new, lens) for q in qs]
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_BF16), d.PagedBatch(table, blocks, [0] * 16, new, lens)
+    spaces = [d.Workspace(64, hq, D, max(lens)) for _ in range(2)]
+    streams = [t.cuda.Stream() for _ in range(2)]
+    t.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            got[i].append(d.attention_decode_shared(qs[i], kv, batch, spaces[i], stream=streams[i]))
+    t.cuda.synchronize()
+    assert all(t.equal(x, want[i]) for i in (0, 1) for x in got[i])
+    outs, graphs = [t.zeros_like(w) for w in want], [t.cuda.CUDAGraph() for _ in want]
+    for q, o, g in zip(qs, outs, graphs):
+        with t.cuda.graph(g):
+            d.attention_decode_shared(q, kv, batch, spaces[0], out=o)
+    for _ in range(3):
+        for o, g in zip(outs, graphs):
+            o.zero_()
+            g.replay()
+        t.cuda.synchronize()
+        assert all(t.equal(o, w) for o, w in zip(outs, want))
+
+
+# ----------------------------------------------------- long contexts, large pools
+def test_a_context_of_more_pages_than_a_segment_holds():
+    rng = np.random.default_rng(24)
+    n = 300_000
+    table, blocks, lens, total = _tree(rng, 1, 1, 0, 0, [n])
+    dev, (k, v) = _pools(rng, total, 1, 64, "f16")
+    q = rng.standard_normal((1, 2, 64)).astype(np.float32)
+    got = _attend(to_dev(q), dev, "f16", table, blocks, [0], [1], lens)
+    want, bound = op.attention(q, k, v, table, blocks, [0], [1], lens)
+    _check(got, want, bound)
+
+
+def test_page_numbers_past_16_bits():
+    """A pool of 70000 pages: numbers of 32 bits in every call, and byte offsets past 2^30."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(25)
+    n_pages, hq, D, lens, new = 70_000, 6, 64, [1000, 700], [2, 1]
+    used = np.sort(rng.permutation(2000)[:16]) + 68_000
+    pools = [t.zeros((n_pages, 1, P, D), dtype=t.float16, device="cuda") for _ in "kv"]
+    small = [t.from_numpy(rng.standard_normal((16, 1, P, D))).half() for _ in "kv"]
+    for x, y in zip(pools, small):
+        x[used] = y.cuda()
+    bt = np.array([[3, 7, 1, 0, 9, 12, 4, 15], [3, 7, 5, 6, 2, 8, 0, 0]])
+    table, blocks = used[bt].astype(np.int32), [8, 6]
+    q = rng.standard_normal((3, hq, D)).astype(np.float32)
+    kv, batch = d.kv_pages(*pools, d.DSB_F16), d.PagedBatch(table, blocks, [0, 0], new, lens)
+    ws, qd = d.Workspace(3, hq, D, 1000), to_dev(q)
+    k, v = (x.double().numpy() for x in small)
+    want, bound = op.attention(q, k, v, bt, blocks, [0, 0], new, lens)
+    _check(d.attention_decode_shared(qd, kv, batch, ws), want, bound)
+    bnd = t.zeros((n_pages, 1, 2, D), dtype=t.float16, device="cuda")
+    d.kv_page_bounds(kv, d.PagedBatch(table[:1], blocks[:1], [0], lens[:1], lens[:1]), bnd)
+    d.kv_page_bounds(kv, d.PagedBatch(table[1:, 2:6], [4], [0], [700 - 2 * P], [700 - 2 * P]), bnd)
+    host = op.bounds(k, bt, [1000, 0], lens, np.zeros((16, 1, 2, D)))
+    host = op.bounds(k, bt[1:, 2:], [700 - 2 * P], [700 - 2 * P], host)
+    assert np.array_equal(to_host(bnd[used].double()), host)
+    sel = d.kv_select_pages(qd, kv, bnd, batch, 3, ws)
+    pick = op.select(q, host, bt, new, lens, 3, 1, 1)
+    assert np.array_equal(to_host(sel), pick)
+    want, bound = op.attention(q, k, v, bt, blocks, [0, 0], new, lens, pick)
+    _check(d.attention_decode_selected(qd, kv, batch, sel, ws), want, bound)
+    d.kv_copy_pages([kv], [int(used[3])], [69_999 if 69_999 not in used else 67_000], [77])
+    at = 69_999 if 69_999 not in used else 67_000
+    assert t.equal(pools[0][at, :, :77].cpu(), small[0][3, :, :77]) and not pools[0][at, :, 77:].any()
+
+
+def test_selection_among_more_pages_than_shared_memory_has_without_asking():
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(26)
+    n = 14_000
+    bnd = np.sort(rng.standard_normal((n, 1, 2, 64)), 2)
+    bnd = t.from_numpy(bnd).half()
+    pool = t.zeros((n, 1, P, 64), dtype=t.float16, device="cuda")
+    batch = d.PagedBatch(rng.permutation(n)[None].astype(np.int32), [n], [0], [1], [n * P - 3])
+    q = rng.standard_normal((1, 3, 64)).astype(np.float32)
+    got = d.kv_select_pages(to_dev(q), d.kv_pages(pool, pool.clone(), d.DSB_F16), bnd.cuda(), batch, 100,
+                            d.Workspace(1, 3, 64, n * P), keep_first=2, keep_last=3)
+    want = op.select(q, bnd.double().numpy(), batch._arrays[0], [1], [n * P - 3], 100, 2, 3)
+    assert np.array_equal(to_host(got), want)
+
+
+# ------------------------------------------------------- memory around the outputs
+def _banded(shape, dtype):
+    """A tensor between two bands of a pattern in one allocation, and the bands."""
+    t = _torch()
+    n = int(np.prod(shape)) * t.empty(0, dtype=dtype).element_size()
+    raw = t.full((n + 16384,), 0xA5, dtype=t.uint8, device="cuda")
+    return raw[8192:8192 + n].view(dtype).view(shape), (raw[:8192], raw[8192 + n:])
+
+
+def test_calls_write_their_outputs_and_nothing_around():
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(27)
+    table, blocks, lens, total = _tree(rng, 1, 3, 2, 0, [5, 131, 70])
+    new, hq, hkv, D = [1, 3, 2], 6, 2, 64
+    bands = []
+    def banded(shape, dtype):
+        x, b = _banded(shape, dtype)
+        bands.extend(b)
+        return x
+    pools = [banded((total, hkv, P, D), t.float16) for _ in "kv"]
+    for x in pools:
+        x.copy_(t.from_numpy(rng.standard_normal(x.shape)))
+    kv, batch = d.kv_pages(*pools, d.DSB_F16), d.PagedBatch(table, blocks, [0] * 3, new, lens)
+    ws, q = d.Workspace(6, hq, D, max(lens)), to_dev(rng.standard_normal((6, hq, D)).astype(np.float32))
+    bnd, sel = banded((total, hkv, 2, D), t.float16), banded((6, hkv, 2), t.int32)
+    outs = [banded((6, hq, D), t.float32) for _ in range(2)]
+    bnd.zero_()
+    d.kv_page_bounds(kv, batch, bnd)
+    d.kv_select_pages(q, kv, bnd, batch, 2, ws, selected=sel)
+    d.attention_decode_shared(q, kv, batch, ws, out=outs[0])
+    d.attention_decode_selected(q, kv, batch, sel, ws, out=outs[1])
+    was = [x.clone() for x in pools]
+    free = [p for p in range(total) if p not in set(table.ravel().tolist())]
+    d.kv_copy_pages([kv], [int(table[0, 0])], free[:1], [33])
+    for x, y in zip(pools, was):
+        y[free[0], :, :33] = y[int(table[0, 0]), :, :33]
+        assert t.equal(x, y)
+    assert t.equal(outs[0], d.attention_decode_shared(q, kv, batch, ws))
+    assert t.equal(outs[1], d.attention_decode_selected(q, kv, batch, sel, ws))
+    assert all(bool((b == 0xA5).all()) for b in bands)
