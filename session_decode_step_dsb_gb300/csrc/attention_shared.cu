@@ -24,9 +24,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 #include <type_traits>
 
 #include "attention_shared.cuh"
@@ -141,6 +141,33 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     pdl_wait();
     return;
   }
+
+  // ---- a tile's rows: lane (g, c) holds row g; what they see in common, and at all
+  int live, min_hi, max_hi, min_lo, max_lo;
+  RowAt at;
+  float2 x[KK][2];
+  const auto fetch = [&]() {
+    live = cur.tile_rows();
+    at = RowAt{0, 0, 0, 0x7FFFFFFF};
+    if (g < live) at = cur.row(g, hq);
+    const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + 2 * c;
+#pragma unroll
+    for (int k = 0; k < KK; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[k][j] = make_float2(0.0f, 0.0f);
+        if (g < live) x[k][j] = __ldg(reinterpret_cast<const float2*>(src + 16 * k + 8 * j));
+      }
+    min_hi = at.hi, max_hi = g < live ? at.hi : -1, min_lo = g < live ? at.lo : 0x7FFFFFFF, max_lo = at.lo;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      min_hi = min(min_hi, __shfl_xor_sync(0xFFFFFFFFu, min_hi, o));
+      max_hi = max(max_hi, __shfl_xor_sync(0xFFFFFFFFu, max_hi, o));
+      min_lo = min(min_lo, __shfl_xor_sync(0xFFFFFFFFu, min_lo, o));
+      max_lo = max(max_lo, __shfl_xor_sync(0xFFFFFFFFu, max_lo, o));
+    }
+  };
+  fetch();
   ahead = cur;
 
   // ---- asking: entry `e` of ahead's run; 32 entries' blocks and pages in the lanes.  Entries
@@ -211,32 +238,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
   };
 
   for (;;) {
-    // ---- the tile's rows: lane (g, c) holds row g
-    const int live = cur.tile_rows();
-    RowAt at{0, 0, 0, 0x7FFFFFFF};
-    if (g < live) at = cur.row(g, hq);
-    int min_hi = at.hi, max_hi = g < live ? at.hi : -1, min_lo = g < live ? at.lo : 0x7FFFFFFF, max_lo = at.lo;
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      min_hi = min(min_hi, __shfl_xor_sync(0xFFFFFFFFu, min_hi, o));
-      max_hi = max(max_hi, __shfl_xor_sync(0xFFFFFFFFu, max_hi, o));
-      min_lo = min(min_lo, __shfl_xor_sync(0xFFFFFFFFu, min_lo, o));
-      max_lo = max(max_lo, __shfl_xor_sync(0xFFFFFFFFu, max_lo, o));
-    }
     // upper and lower parts of dimensions 16 k + 2c, + 1 and 16 k + 8 + 2c, + 1; the third
     uint32_t qa[KK][4], qb[kThird ? KK : 1][2];
     float rs;
     {
-      float2 x[KK][2];
-      const float* src = q + (size_t)at.tok * q_stride + (size_t)(at.row - at.tok * hq) * D + 2 * c;
       float m = 0.0f;
 #pragma unroll
       for (int k = 0; k < KK; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float2 v = make_float2(0.0f, 0.0f);
-          if (g < live) v = __ldg(reinterpret_cast<const float2*>(src + 16 * k + 8 * j));
-          x[k][j] = make_float2(v.x * scale_log2e, v.y * scale_log2e);
+          x[k][j] = make_float2(x[k][j].x * scale_log2e, x[k][j].y * scale_log2e);
           m = fmaxf(m, fmaxf(fabsf(x[k][j].x), fabsf(x[k][j].y)));
         }
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -426,59 +437,72 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       for (int t = 0; t < NT; ++t) row[4 * t] = unpack(o[t]);
       if (c == 0) joined_stat[warp * kRows + g] = make_float2(-minus, l);
     }
-    __syncthreads();
-    {
-      const int r = tid >> 4, d0 = (tid & 15) * (D / 16);
-      if (r < live) {
-        const RowAt mine = cur.row(r, hq);
-        float2 st[kWarps];
-        float ref = -kNoRef;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          st[w] = joined_stat[w * kRows + r];
-          ref = fmaxf(ref, st[w].x);
+    // a thread's share of the rows, and where it goes: to the output where this CTA has all
+    // of the run, else to a slot
+    const int r = tid >> 4, d0 = (tid & 15) * (D / 16);
+    const bool done = cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages;
+    float* dst = nullptr;
+    float2* stat = nullptr;
+    int empty_at = 0, empty = 0;  // slots behind the first part's that the row's parts leave
+    if (r < live) {
+      const size_t row = (size_t)cur.row(r, hq).row;
+      const int part = cur.part(cta);
+      const size_t place = row * to.slots + cur.slot_base() + (done ? 0 : part);
+      dst = done ? to.out + row * D : to.acc + place * D;
+      if (d0 == 0 && !(done && cur.slot_cap() == 1)) {
+        stat = to.stat + place;
+        if (!done && part == 0) {
+          empty_at = cur.parts();
+          empty = cur.slot_cap();
         }
-        float sum = 0.0f, x[D / 16];
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) x[k] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2_of(st[w].x - ref);
-          sum = fmaf(f, st[w].y, sum);
-          const float4* src = reinterpret_cast<const float4*>(joined + (w * kRows + r) * D + d0);
-#pragma unroll
-          for (int k = 0; k < D / 64; ++k) {
-            const float4 y = src[k];
-            x[4 * k] = fmaf(f, y.x, x[4 * k]);
-            x[4 * k + 1] = fmaf(f, y.y, x[4 * k + 1]);
-            x[4 * k + 2] = fmaf(f, y.z, x[4 * k + 2]);
-            x[4 * k + 3] = fmaf(f, y.w, x[4 * k + 3]);
-          }
-        }
-        const int cap = cur.slot_cap();
-        float* dst;
-        float2* stat = to.stat + (size_t)mine.row * to.slots + cur.slot_base();
-        if (cur.alone() && cur.i == 0 && cur.i_end == cur.n_pages) {  // the row is done
-          dst = to.out + (size_t)mine.row * D;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) x[k] = sum == 0.0f ? 0.0f : __fdiv_rn(x[k], sum);
-          if (cap > 1 && d0 == 0) stat[0] = make_float2(0.0f, -1.0f);
-        } else {
-          const int part = cur.part(cta);
-          dst = to.acc + ((size_t)mine.row * to.slots + cur.slot_base() + part) * D;
-          if (d0 == 0) {
-            stat[part] = make_float2(ref, sum);
-            if (part == 0)
-              for (int k = cur.parts(); k < cap; ++k) stat[k] = make_float2(0.0f, 0.0f);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          reinterpret_cast<float4*>(dst + d0)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
       }
     }
-    if (!cur.another()) break;
-    cur.locate(cur.following());
+    // the next run's rows are on their way meanwhile
+    const bool more = cur.another();
+    if (more) {
+      cur.locate(cur.following());
+      fetch();
+    }
+    __syncthreads();
+    if (dst) {
+      float2 st[kWarps];
+      float ref = -kNoRef;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        st[w] = joined_stat[w * kRows + r];
+        ref = fmaxf(ref, st[w].x);
+      }
+      float sum = 0.0f, y[D / 16];
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) y[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_of(st[w].x - ref);
+        sum = fmaf(f, st[w].y, sum);
+        const float4* src = reinterpret_cast<const float4*>(joined + (w * kRows + r) * D + d0);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const float4 z = src[k];
+          y[4 * k] = fmaf(f, z.x, y[4 * k]);
+          y[4 * k + 1] = fmaf(f, z.y, y[4 * k + 1]);
+          y[4 * k + 2] = fmaf(f, z.z, y[4 * k + 2]);
+          y[4 * k + 3] = fmaf(f, z.w, y[4 * k + 3]);
+        }
+      }
+      if (stat) {
+        *stat = done ? make_float2(0.0f, -1.0f) : make_float2(ref, sum);
+        for (; empty_at < empty; ++empty_at) stat[empty_at] = make_float2(0.0f, 0.0f);
+      }
+      if (done) {
+        const float by = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) y[k] *= by;
+      }
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        reinterpret_cast<float4*>(dst + d0)[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    }
+    if (!more) break;
   }
   pdl_wait();
 }
@@ -563,7 +587,8 @@ cudaError_t pages_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st
   using R = Ring<D>;
   static_assert(2 * (R::smem + 1024) <= 228 * 1024, "two CTAs an SM");
   auto kern = attention_pages_kernel<D, T, Walk, N>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::smem);
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = allow_smem(kern, R::smem, &ready);
   if (e != cudaSuccess) return e;
   CUtensorMap tmk, tmv;
   if ((e = kv_tensor_map(a.k, a.pool_rows, D, std::is_same_v<T, __half> ? 0 : 1, R::keys, &tmk)) != cudaSuccess) return e;

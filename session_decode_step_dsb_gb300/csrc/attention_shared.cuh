@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "dsb_f32x2.cuh"
@@ -22,6 +23,19 @@
 #include "dsb_ptx.cuh"
 
 namespace dsbk {
+
+// Lets a kernel have so much dynamic shared memory, once on each device.
+template <typename Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (ready->load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready->fetch_or(bit);
+  return e;
+}
 
 constexpr int kPgKeys = 128;
 // minus the reference of a row that has seen no key: the reference lies below any score

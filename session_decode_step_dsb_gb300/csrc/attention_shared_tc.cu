@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -660,7 +661,8 @@ cudaError_t tc_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st) {
   return with_words(meta, [&](auto n) {
     constexpr int N = decltype(n)::value;
     auto kern = attention_shared_tc_kernel<D, T, N>;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes);
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t err = allow_smem(kern, S::bytes, &ready);
     if (err != cudaSuccess) return err;
     ParamWords<N> w;
     fill_words(meta, &w);

@@ -883,16 +883,16 @@ def kv_copy_pages_q4(pools, src, dst, keys, stream=None):
 
 def _paged_q(q, kv: KVPages, batch: PagedBatch, out, stream):
     """Stride and device of ``q[n_tok, Hq, D]`` and the output of its shape."""
-    import torch
-    if q.dim() != 3 or q.shape[2] != kv.head_dim:
-        raise ValueError(f"q must be [n_tok, Hq, head_dim={kv.head_dim}], got {tuple(q.shape)}")
-    n_tok, hq, d = q.shape
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != kv.head_dim:
+        raise ValueError(f"q must be [n_tok, Hq, head_dim={kv.head_dim}], got {tuple(shape)}")
+    n_tok, hq, d = shape
     stride = _row_stride(q, batch.n_tok, (hq, d), "q")
     dev = _current_device(q, "q")
     if kv._device != dev:
         raise ValueError(f"the page pool must live on cuda:{dev}")
     if out is None:
-        out = _empty_on(stream, (n_tok, hq, d), torch.float32, q.device)
+        out = q.new_empty(shape) if stream is None else _empty_on(stream, shape, q.dtype, q.device)
     elif out is not False:
         _need(out, 4 * n_tok * hq * d, "out", "f32")
         if not out.is_contiguous():
@@ -937,7 +937,8 @@ def kv_select_pages(q, kv: KVPages, bounds, batch: PagedBatch, n_select: int, ws
     if selected is None:
         if n_select < 1:
             raise ValueError(f"n_select must be positive, got {n_select}")
-        selected = _empty_on(stream, shape, torch.int32, q.device)
+        selected = q.new_empty(shape, dtype=torch.int32) if stream is None else \
+            _empty_on(stream, shape, torch.int32, q.device)
     elif tuple(selected.shape) != shape or selected.dtype != torch.int32 or not selected.is_contiguous():
         raise ValueError(f"selected must be contiguous int32 {shape}")
     _check(lib().dsb_kv_select_pages(q.data_ptr(), stride, q.shape[1], ctypes.byref(kv), _bounds(kv, bounds, dev),
