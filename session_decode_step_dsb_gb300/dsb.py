@@ -892,7 +892,7 @@ def _paged_q(q, kv: KVPages, batch: PagedBatch, out, stream):
     if kv._device != dev:
         raise ValueError(f"the page pool must live on cuda:{dev}")
     if out is None:
-        out = q.new_empty(shape) if stream is None else _empty_on(stream, shape, q.dtype, q.device)
+        out = _empty_on(stream, shape, q.dtype, q.device)
     elif out is not False:
         _need(out, 4 * n_tok * hq * d, "out", "f32")
         if not out.is_contiguous():
@@ -937,8 +937,7 @@ def kv_select_pages(q, kv: KVPages, bounds, batch: PagedBatch, n_select: int, ws
     if selected is None:
         if n_select < 1:
             raise ValueError(f"n_select must be positive, got {n_select}")
-        selected = q.new_empty(shape, dtype=torch.int32) if stream is None else \
-            _empty_on(stream, shape, torch.int32, q.device)
+        selected = _empty_on(stream, shape, torch.int32, q.device)
     elif tuple(selected.shape) != shape or selected.dtype != torch.int32 or not selected.is_contiguous():
         raise ValueError(f"selected must be contiguous int32 {shape}")
     _check(lib().dsb_kv_select_pages(q.data_ptr(), stride, q.shape[1], ctypes.byref(kv), _bounds(kv, bounds, dev),
