@@ -510,10 +510,11 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     a.out = out;
     a.slots = slots;
     a.wide_pages = wide;
-    // all metadata before the first launch: a copy between two would keep them apart
+    // Metadata before the launches, as many as there are places for staged ones: a copy
+    // between two would keep them apart.
     std::vector<std::vector<int32_t>> metas(launches.size());
     std::vector<dsbk::MetaArg> args(launches.size());
-    for (size_t li = 0; li < launches.size(); ++li) {
+    const auto lay_out = [&](size_t li) {
       const Launch& l = launches[li];
       std::vector<int32_t>& words = metas[li];
       words.assign(l.segs.size() * dsbk::kSharedSegWords + 1, 0);
@@ -541,13 +542,16 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         work += hkv * g.work_a_head();
       }
       words[l.segs.size() * dsbk::kSharedSegWords] = (int32_t)work;
-      if ((st = meta_arg(ws, words, cs, &args[li])) != DSB_OK) return st;
-    }
+      return meta_arg(ws, words, cs, &args[li]);
+    };
     for (size_t li = 0; li < launches.size(); ++li) {
+      if (li % kSlots == 0)
+        for (size_t i = li; i < std::min(li + kSlots, launches.size()); ++i)
+          if ((st = lay_out(i)) != DSB_OK) return st;
       const Launch& l = launches[li];
       a.n_seg = (int)l.segs.size();
       a.ctas = l.ctas;
-      a.beside = li > 0;  // no kernel of the call reads or writes what another one writes
+      a.beside = li % kSlots > 0;  // no kernel of the call reads or writes what another one writes
       const Overlap overlap(a.beside);
       const cudaError_t e = l.tile == 8 ? dsbk::launch_attention_pages(a, kv->dtype == DSB_F16 ? 0 : 1, D, args[li], cs)
                                         : dsbk::launch_attention_shared_tc(a, kv->dtype == DSB_F16 ? 0 : 1, D, args[li], cs);

@@ -17,8 +17,10 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
+#include "attention_shared.cuh"
 #include "dsb_kernels.h"
 #include "dsb_ptx.cuh"
 
@@ -29,6 +31,8 @@ namespace {
 constexpr int kBoundThreads = 256;
 constexpr int kSelThreads = 256;
 constexpr int kPageKeys = 128;
+// Largest list of scores: a slot of metadata holds 11281 words, two page numbers to one.
+constexpr int kMostOrder = 96 * 1024;
 
 template <typename T>
 struct Two;
@@ -322,8 +326,9 @@ cudaError_t select_go(const SelectArgs& a, const MetaArg& meta, cudaStream_t st)
     cfg.blockDim = dim3(kSelThreads);
     cfg.dynamicSmemBytes = (size_t)a.max_pages * 4;
     if (cfg.dynamicSmemBytes > 40 * 1024) {  // past what a launch has without asking (beside 2 KB of static)
-      const cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)cfg.dynamicSmemBytes);
+      // the same whatever the call needs, so that calls of two threads do not take it from each other
+      static std::atomic<unsigned long long> ready{0};
+      const cudaError_t e = allow_smem(select_pages_kernel<D, T, N>, kMostOrder, &ready);
       if (e != cudaSuccess) return e;
     }
     cfg.stream = st;

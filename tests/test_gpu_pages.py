@@ -3,7 +3,8 @@ shared and over selected pages -- against the float64 oracle, through the C ABI.
 
 Copies, bounds and selections are exact.  The attention's bound is the oracle's: every
 rounding of a float32 evaluation, and for bf16 caches 2^-18 more of the weighted
-values' magnitudes, the weights being two bf16 (each rounding 2^-9 of what is left)."""
+values' magnitudes, which leaves room for weights of two bf16 (each rounding 2^-9 of
+what is left; the kernels take three)."""
 import numpy as np
 import pytest
 
@@ -537,6 +538,70 @@ def test_selection_among_more_pages_than_shared_memory_has_without_asking():
                             d.Workspace(1, 3, 64, n * P), keep_first=2, keep_last=3)
     want = op.select(q, bnd.double().numpy(), batch._arrays[0], [1], [n * P - 3], 100, 2, 3)
     assert np.array_equal(to_host(got), want)
+
+
+def test_more_metadata_than_places_for_it():
+    """1024 sequences of 340 pages each: 18 launches, and 16 places for staged metadata.  Tables
+    repeat the pages of a small pool, so that a key's weight is its own times how often its
+    page is listed."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(28)
+    n_seq, n, total, hq, D = 1024, 340, 64, 2, 64
+    table = rng.integers(0, total, (n_seq, n)).astype(np.int32)
+    dev, _ = _pools(rng, total, 1, D, "f16")
+    q = to_dev(rng.standard_normal((n_seq, hq, D)).astype(np.float32))
+    got = _attend(q, dev, "f16", table, [n] * n_seq, [0] * n_seq, [1] * n_seq, [n * P] * n_seq).double()
+    k, v = (x.double().reshape(total * P, D) for x in dev)
+    often = np.stack([np.bincount(row, minlength=total) for row in table])
+    often = t.from_numpy(np.repeat(often, P, 1)).double().cuda()
+    for s in range(0, n_seq, 32):
+        x, times = q[s:s + 32].double(), often[s:s + 32, None, :]
+        score = x @ k.T / 8
+        size = (x.abs() @ k.abs().T).amax(-1)[..., None] / 8
+        e = t.exp(score - score.amax(-1, keepdim=True))
+        total_e = (e * times).sum(-1, keepdim=True)
+        e, one = e * times / total_e, (e / total_e).amax(-1)[..., None]
+        want = e @ v
+        apart = t.stack([(e[i, :, :, None] * (v[None] - want[i, :, None, :]).abs()).sum(1) for i in range(len(x))])
+        bound = 2.0 ** -20 * 2 * (size + 1) * apart + 2.0 ** -20 * (e @ v.abs())      # the oracle's
+        bound += 2.0 ** -35 * one * (times @ v.abs())
+        assert bool(((got[s:s + 32] - want).abs() <= bound).all()), f"sequences {s} on"
+
+
+def test_selections_of_two_threads():
+    """Lists that need more shared memory than a launch has without asking, beside short ones."""
+    import threading
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(29)
+    n = 14_000
+    bnd = t.from_numpy(np.sort(rng.standard_normal((n, 1, 2, 64)), 2)).half().cuda()
+    pool = t.zeros((n, 1, P, 64), dtype=t.float16, device="cuda")
+    kv = d.kv_pages(pool, pool.clone(), d.DSB_F16)
+    order = rng.permutation(n)[None].astype(np.int32)
+    q = to_dev(rng.standard_normal((1, 3, 64)).astype(np.float32))
+    lens = [n * P - 3, 10_400 * P]
+    want = [None, None]
+    got, errors = [[], []], []
+
+    def run(i, times):
+        try:
+            ws, st = d.Workspace(1, 3, 64, lens[i]), t.cuda.Stream()
+            batch = d.PagedBatch(order, [n], [0], [1], [lens[i]])
+            for _ in range(times):
+                got[i].append(d.kv_select_pages(q, kv, bnd, batch, 100, ws, stream=st))
+            st.synchronize()
+        except Exception as e:  # told by the test's own thread
+            errors.append(e)
+
+    t.cuda.synchronize()
+    for i in (0, 1):
+        run(i, 1)
+        want[i] = got[i].pop()
+    threads = [threading.Thread(target=run, args=(i, 200)) for i in (0, 1)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not errors
+    assert all(len(got[i]) == 200 and all(t.equal(x, want[i]) for x in got[i]) for i in (0, 1))
 
 
 # ------------------------------------------------------- memory around the outputs
