@@ -378,9 +378,11 @@ constexpr int kLead8 = 2, kLead128 = 3;
 // warp-level kernel (attention_shared.cu) or 128 of the tcgen05 one
 // (attention_shared_tc.cu), whichever takes less of an SM's time, by what they measured:
 // a page of a tile 0.6 and 1.6 us, and 4 us for a tile of the latter to begin and end.
-// (The unit is 0.2 us.)  The latter's launch beside the other one takes 10 us longer on
-// every SM, which it has to save.
-constexpr int kWideCost = 50;
+// (The unit is 0.2 us.)  A launch of the latter, beside the other's, has to save 4 us of
+// every SM: 16 sessions of 5 rows behind 4, 8, 16 and 32 common pages take 22, 23, 25 and 26 us with
+// it and 20, 23, 26 and 35 without, 8 sessions behind 16, 32 and 64 pages 21, 24 and 28 for 18, 23
+// and 31 (it saves 8, 17 and 35, and 5, 11 and 22 units), and the host takes 5 us more for it.
+constexpr int kWideCost = 20;
 inline long long shared_tile_cost(int rows, int n, int tile) {
   const long long tiles = (rows + tile - 1) / tile;
   return tile == 8 ? 3 * tiles * n : tiles * (8LL * n + 20);

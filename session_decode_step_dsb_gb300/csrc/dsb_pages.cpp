@@ -18,7 +18,6 @@
 using namespace dsbh;
 
 namespace {
-
 dsb_status check_pages16(const dsb_kv_pages* kv) {
   if (!kv) return fail(DSB_ERR_INVALID_ARG, "kv is NULL");
   if (!kv->k || !kv->v) return fail(DSB_ERR_INVALID_ARG, "kv->k / kv->v is NULL");
@@ -248,11 +247,11 @@ struct Tree {
   // work: CTAs side by side then take the tiles through the same pages at the same time,
   // which come from memory once (a CTA that goes through all pages of a tile, and others at
   // other places of theirs, read 134 MB of pages three times).
-  void cut_shares(int hkv, int sms) {
+  void cut_shares(int hkv, int ctas) {
     long long work = 0;
     for (const Segment& g : segs)
       if (g.tile == 128) work += hkv * g.work_a_head();
-    const int share = std::max(16, (int)((work + sms - 1) / sms));  // (shorter pieces would be mostly ends)
+    const int share = std::max(16, (int)((work + ctas - 1) / ctas));  // (shorter pieces would be mostly ends)
     std::vector<Segment> out;
     std::vector<int> last(segs.size());
     for (size_t i = 0; i < segs.size(); ++i) {
@@ -273,6 +272,24 @@ struct Tree {
     for (int& e : end)
       if (e >= 0) e = last[e];
     segs.swap(out);
+  }
+
+  // SMs for the tiles of 128 rows: all, or where there are tiles of 8 rows too, as many as let
+  // the two kernels end at the same time beside each other (one after the other on all SMs,
+  // each with its beginning and its end: 64 samples 50 us for 46, a document's drafts 109 for
+  // 103).  In units of 0.1 us: a page of a tile 1.4 and 0.7, and 2 us more for the tcgen05 kernel to
+  // begin.
+  int wide_sms(int hkv, int sms) const {
+    long long cost[2] = {0, 0};
+    for (const Segment& g : segs) cost[g.tile == 128] += hkv * g.work_a_head() * (g.tile == 128 ? 14 : 7);
+    if (cost[0] == 0 || cost[1] == 0) return sms;
+    int best = 1;
+    long long least = LLONG_MAX;
+    for (int n = 1; n < sms; ++n) {
+      const long long t = std::max(cost[1] / n + 20, cost[0] / (sms - n));
+      if (t < least) least = t, best = n;
+    }
+    return best;
   }
 
   void build() {
@@ -440,7 +457,8 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
       tree = Tree{b, n_q_heads / hkv, false, {}, {}, {}};
       tree.build();
     }
-    tree.cut_shares(hkv, dev.sms);
+    const int wide_sms = tree.wide_sms(hkv, dev.sms), sms8 = wide_sms < dev.sms ? dev.sms - wide_sms : dev.sms;
+    tree.cut_shares(hkv, wide_sms);
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
     const bool wide = wide_pages(kv);
@@ -483,7 +501,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     }
     int slots = 0;
     for (Launch& l : launches) {
-      l.ctas = (int)std::min<long long>(l.tile == 8 ? dsbk::page_attn_resident(dev.sms) : dev.sms, l.work);
+      l.ctas = (int)std::min<long long>(l.tile == 8 ? dsbk::page_attn_resident(sms8) : wide_sms, l.work);
       for (int i : l.segs) tree.segs[i].cap = most_parts(tree.segs[i].n, l.work / l.ctas);
     }
     for (Segment& g : tree.segs) {  // a parent comes before its children
