@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -507,79 +508,89 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
   pdl_wait();
 }
 
-// One warp per row: the parts' sums at the largest of their references, in slot order.
+// The parts' sums of a row at the largest of their references, in slot order, by a warp.  It
+// takes one row of a few, and of many up to 32, of which it finds those that are in parts by
+// one load: rows beyond what the GPU holds warps would wait their turn to find that there is
+// nothing to join (prompts of 160000 rows:
+// 712 us a call with a row to a warp, 683 so).
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(int n_seq, int rows, int hq, PartialsOut from,
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(int n_seq, int rows, int per, int hq, PartialsOut from,
                                                                   const __grid_constant__ ParamWords<N> words) {
   constexpr int V = D / 32;  // dimensions of a lane
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int tok = row / hq;
-  int s = 0, hi = n_seq - 1;
-  while (s < hi) {
-    const int mid = (s + hi + 1) >> 1;
-    if (words.w[2 * mid] <= tok)
-      s = mid;
-    else
-      hi = mid - 1;
-  }
-  const int n = words.w[2 * s + 1];
-  if (n == 0) return;
-  const float2* stat = from.stat + (size_t)row * from.slots;
-  const float* acc = from.acc + (size_t)row * from.slots * D + lane * V;
-  float2 mine = make_float2(0.0f, 0.0f);
-  if (lane < n) mine = __ldcg(stat + lane);
-  if (__shfl_sync(0xFFFFFFFFu, mine.y, 0) == -1.0f) return;
-  float ref = mine.y == 0.0f ? -kNoRef : mine.x;
-  for (int i = lane + 32; i < n; i += 32) {
-    const float2 x = __ldcg(stat + i);
-    if (x.y != 0.0f) ref = fmaxf(ref, x.x);
-  }
+  const int row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * per, lane = threadIdx.x & 31;
+  if (row0 >= rows) return;
+  unsigned todo = 1;
+  if (per > 1)
+    todo = __ballot_sync(0xFFFFFFFFu, lane < min(per, rows - row0) &&
+                                          __ldcg(&from.stat[(size_t)(row0 + lane) * from.slots].y) != -1.0f);
+  for (; todo; todo &= todo - 1) {
+    const int row = row0 + __ffs(todo) - 1, tok = row / hq;
+    int s = 0, hi = n_seq - 1;
+    while (s < hi) {
+      const int mid = (s + hi + 1) >> 1;
+      if (words.w[2 * mid] <= tok)
+        s = mid;
+      else
+        hi = mid - 1;
+    }
+    const int n = words.w[2 * s + 1];
+    if (n == 0) continue;
+    const float2* stat = from.stat + (size_t)row * from.slots;
+    const float* acc = from.acc + (size_t)row * from.slots * D + lane * V;
+    float2 mine = make_float2(0.0f, 0.0f);
+    if (lane < n) mine = __ldcg(stat + lane);
+    if (__shfl_sync(0xFFFFFFFFu, mine.y, 0) == -1.0f) continue;
+    float ref = mine.y == 0.0f ? -kNoRef : mine.x;
+    for (int i = lane + 32; i < n; i += 32) {
+      const float2 x = __ldcg(stat + i);
+      if (x.y != 0.0f) ref = fmaxf(ref, x.x);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
-  float sum = 0.0f, x[V];
+    for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
+    float sum = 0.0f, x[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) x[k] = 0.0f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    if (i0 > 0) mine = i0 + lane < n ? __ldcg(stat + i0 + lane) : make_float2(0.0f, 0.0f);
-    const float f = mine.y == 0.0f ? 0.0f : exp2_of(mine.x - ref);
-    const float fl = mine.y == 0.0f ? 0.0f : f * mine.y;
-    const unsigned there = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
-    const int m = min(32, n - i0);
-    for (int j0 = 0; j0 < m; j0 += 8) {
-      float y[8][V];
+    for (int k = 0; k < V; ++k) x[k] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      if (i0 > 0) mine = i0 + lane < n ? __ldcg(stat + i0 + lane) : make_float2(0.0f, 0.0f);
+      const float f = mine.y == 0.0f ? 0.0f : exp2_of(mine.x - ref);
+      const float fl = mine.y == 0.0f ? 0.0f : f * mine.y;
+      const unsigned there = __ballot_sync(0xFFFFFFFFu, mine.y != 0.0f);
+      const int m = min(32, n - i0);
+      for (int j0 = 0; j0 < m; j0 += 8) {
+        float y[8][V];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (there >> (j0 + j) & 1u) {
-          const float* src = acc + (size_t)(i0 + j0 + j) * D;
-          if constexpr (V == 4) {
-            const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-            y[j][0] = z.x, y[j][1] = z.y, y[j][2] = z.z, y[j][3] = z.w;
-          } else {
-            const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-            y[j][0] = z.x, y[j][1] = z.y;
+        for (int j = 0; j < 8; ++j)
+          if (there >> (j0 + j) & 1u) {
+            const float* src = acc + (size_t)(i0 + j0 + j) * D;
+            if constexpr (V == 4) {
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+              y[j][0] = z.x, y[j][1] = z.y, y[j][2] = z.z, y[j][3] = z.w;
+            } else {
+              const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+              y[j][0] = z.x, y[j][1] = z.y;
+            }
           }
-        }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float fj = __shfl_sync(0xFFFFFFFFu, f, j0 + j), lj = __shfl_sync(0xFFFFFFFFu, fl, j0 + j);
-        if (there >> (j0 + j) & 1u) {
-          sum += lj;
+        for (int j = 0; j < 8; ++j) {
+          const float fj = __shfl_sync(0xFFFFFFFFu, f, j0 + j), lj = __shfl_sync(0xFFFFFFFFu, fl, j0 + j);
+          if (there >> (j0 + j) & 1u) {
+            sum += lj;
 #pragma unroll
-          for (int k = 0; k < V; ++k) x[k] = fmaf(fj, y[j][k], x[k]);
+            for (int k = 0; k < V; ++k) x[k] = fmaf(fj, y[j][k], x[k]);
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < V; ++k) x[k] = sum == 0.0f ? 0.0f : __fdiv_rn(x[k], sum);
-  float* out = from.out + (size_t)row * D + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
-  else
-    *reinterpret_cast<float2*>(out) = make_float2(x[0], x[1]);
+    for (int k = 0; k < V; ++k) x[k] = sum == 0.0f ? 0.0f : __fdiv_rn(x[k], sum);
+    float* out = from.out + (size_t)row * D + lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<float2*>(out) = make_float2(x[0], x[1]);
+  }
 }
 
 template <int D, typename T, typename Walk, int N>
@@ -628,14 +639,14 @@ unsigned int read_clear_error_attention_pages() {
 
 cudaError_t launch_attention_join(const PageAttnArgs& a, int n_seq, int head_dim, const MetaArg& meta, cudaStream_t st) {
   const PartialsOut from{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
-  const int rows = a.n_tok * a.hq;
-  const dim3 grid((unsigned)((rows + kWarps - 1) / kWarps));
+  const int rows = a.n_tok * a.hq, per = std::min(std::max(rows / 8192, 1), 32);
+  const dim3 grid((unsigned)((rows + kWarps * per - 1) / (kWarps * per)));
   const auto go = [&](auto n) {
     constexpr int N = decltype(n)::value;
     ParamWords<N> w;
     fill_words(meta, &w);
-    return head_dim == 128 ? launch_kernel(attention_join_kernel<128, N>, grid, dim3(kThreads), 0, st, n_seq, rows, a.hq, from, w)
-                           : launch_kernel(attention_join_kernel<64, N>, grid, dim3(kThreads), 0, st, n_seq, rows, a.hq, from, w);
+    return head_dim == 128 ? launch_kernel(attention_join_kernel<128, N>, grid, dim3(kThreads), 0, st, n_seq, rows, per, a.hq, from, w)
+                           : launch_kernel(attention_join_kernel<64, N>, grid, dim3(kThreads), 0, st, n_seq, rows, per, a.hq, from, w);
   };
   if (meta.n_words <= kParamFew) return go(std::integral_constant<int, kParamFew>{});
   return go(std::integral_constant<int, kParamWords>{});

@@ -540,6 +540,20 @@ def test_selection_among_more_pages_than_shared_memory_has_without_asking():
     assert np.array_equal(to_host(got), want)
 
 
+def test_more_rows_than_the_gpu_holds_warps():
+    """Prompts beside single tokens: rows in one part and in several, several to a warp of the join."""
+    rng = np.random.default_rng(30)
+    kind, hq, hkv, D = "f16", 40, 2, 64
+    table, blocks, lens, total = _tree(rng, 1, 5, 1, 0, [260, 5, 131, 400, 60])
+    new = [250, 1, 128, 90, 0]
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32)
+    assert len(q) * hq > 16384
+    got = _attend(to_dev(q), dev, kind, table, blocks, [0] * 5, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, [0] * 5, new, lens)
+    _check(got, want, bound)
+
+
 def test_more_metadata_than_places_for_it():
     """1024 sequences of 340 pages each: 18 launches, and 16 places for staged metadata.  Tables
     repeat the pages of a small pool, so that a key's weight is its own times how often its
