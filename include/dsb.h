@@ -593,9 +593,8 @@ dsb_status dsb_kv_copy_pages_q4(const dsb_kv_q4_pages* pools, int n_pools, const
  * behind a sequence's last key, or is hidden from a row, does not reach the row, NaN
  * and infinities included; a row that sees a NaN or an infinity in K or V has no
  * finite result where it counts.  Partial sums go to the workspace:
- * dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest seq_lens) is enough.  No
- * atomics: the same call gives the same bits (in another batch, sums are cut
- * elsewhere). */
+ * dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest seq_lens) is enough.  The
+ * same call gives the same bits (in another batch, sums are cut elsewhere). */
 dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
                                        const dsb_paged_batch* batch, float* out, dsb_workspace* ws, void* stream);
 

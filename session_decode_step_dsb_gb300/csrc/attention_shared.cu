@@ -20,6 +20,12 @@
 // The tensor core's sums round toward zero, which would tell over the pages of a part: each
 // page's products of weights and V start from zero, and their halves are added to the
 // output in float32.
+//
+// Measured (GB300): 64 selected pages of bf16 for each of 16 sessions and 8 kv heads of 128,
+// 537 MB: 92 us, 0.86 of the copy rate; two CTAs an SM take 1.3 us for a page each, and 5 us
+// until their first.  What is left are latencies of eight warps an SM (issue slots 0.25 full,
+// the tensor pipe 0.36); a third CTA has no room, 255 registers a thread being in use.  16
+// sessions of 5 rows behind 16 common pages (bf16, 76 MB): 26 us, 3 of them the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -511,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
 // The parts' sums of a row at the largest of their references, in slot order, by a warp.  It
 // takes one row of a few, and of many up to 32, of which it finds those that are in parts by
 // one load: rows beyond what the GPU holds warps would wait their turn to find that there is
-// nothing to join (prompts of 160000 rows:
-// 712 us a call with a row to a warp, 683 so).
+// nothing to join (prompts of 160000 rows: 712 us a call with a row to a warp, 683 so).
 template <int D, int N>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(int n_seq, int rows, int per, int hq, PartialsOut from,
                                                                   const __grid_constant__ ParamWords<N> words) {

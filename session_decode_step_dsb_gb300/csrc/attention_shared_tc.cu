@@ -14,6 +14,14 @@
 // S(n + 1) lies between P V(n - 1) and P V(n).  A warp of its own asks for the pages (TMA,
 // two of K and two of V), another issues the products.  Bound by the products: 32 (fp16) or 48
 // (bf16) of 128 x 128 x 16 for a page of 128-wide heads.
+//
+// Measured (GB300), 128-wide heads, 40 on 8: prompts of 4 x 1000 tokens behind 4096 keys, bf16,
+// 683 us with the join, 0.55 PFLOP/s, in three parts 1.65 (tensor pipe active 0.74 of the
+// time); drafts of 32 sessions on 32768 keys, fp16, 97 us on 123 SMs (0.59).  A page takes
+// 2800 cycles (fp16) or 4000 (bf16): a product with both operands in shared memory 106, one
+// with its left operand in tensor memory 73, which makes 2860 and 4300 one after the other.
+// With the fp16 Q in tensor memory too (2340) a page took as long: the weights then do.
+// A change of runs takes 5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -5,6 +5,10 @@
 // a page side by side; a plane is a pool's K or V pages, or a 4-bit pool.  A thread asks
 // for all its 16-byte pieces before it stores the first, so that a CTA has up to 32 KB
 // on their way.
+//
+// Measured (GB300), 40 layers of 8 kv heads of 128: the last pages of 16 forks, bf16, 376 MB
+// read and written: 57 us, 0.98 of the copy rate; 50 whole 4-bit pages, 557 MB: 81 us, 1.0.
+// A fork of three sessions in two layers: 2 us, a launch.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -372,7 +372,7 @@ cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, co
 // segment's pages, (work of the tiles before it, first page) of each tile and the work of all.
 constexpr int kSharedSegWords = 13, kSharedMemWords = 5;
 // What a run counts for besides its pages, in pages: by what it takes to begin and to end
-// one (attention_shared.cu 2 us beside 1.3 a page, attention_shared_tc.cu 4 beside 1.6).
+// one (attention_shared.cu 2 us beside 1.3 a page, attention_shared_tc.cu 5 beside 1.5 to 2).
 constexpr int kLead8 = 2, kLead128 = 3;
 // Query rows of a tile of a segment with `rows` of them on a kv head and n pages: 8 of the
 // warp-level kernel (attention_shared.cu) or 128 of the tcgen05 one
