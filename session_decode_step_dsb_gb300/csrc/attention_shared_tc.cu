@@ -173,7 +173,7 @@ struct Smem {
   static constexpr int fac = stat + 128 * 8;            // [3][128] of a page: the sums before it times 2^-fac
   static constexpr int strange = fac + 3 * 128;         // [3] of a page: keys (4 words), whether any
   static constexpr int bars = strange + 64;             // see below
-  static constexpr int base = bars + 14 * 8;
+  static constexpr int base = bars + 15 * 8;
   static constexpr int bytes = base + 8;
   // tensor memory: scores and weights of two pages, output, third parts of two pages
   static constexpr int s_col = 0, o_col = 256, t_col = 384;
@@ -192,10 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   uint8_t* fac = smem + S::fac;
   unsigned* strange = reinterpret_cast<unsigned*>(smem + S::strange);
   // pages of K and of V; scores of a page; V has been read; a page's output; its weights (by
-  // the weighers' warps); the output has been added (the adders'); a run's queries, its
-  // statistics (weighers), and these have been read (adders)
+  // the weighers' warps; of two pages, since those of the next may be there before the issuer
+  // has seen that these are); the output has been added (the adders'); a run's queries, its
+  // statistics (weighers), and these have been read (adders).  No barrier completes a phase
+  // before the one ahead of it has been seen by all that wait for it.
   uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + S::bars);
-  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *free_v = scores + 2, *output = free_v + 2, *weights = output + 1, *added = weights + 1,
+  uint64_t *full_v = full_k + 2, *scores = full_v + 2, *free_v = scores + 2, *output = free_v + 2, *weights = output + 1, *added = weights + 2,
            *queries = added + 1, *stat_full = queries + 1, *stat_free = stat_full + 1;
   uint32_t* base = reinterpret_cast<uint32_t*>(smem + S::base);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   int pos = cur.begin(meta, n_seg, wide, hkv, hq / hkv, kRows, kLead128, cta, ctas);
   if (tid == 0) {
     for (int i = 0; i < 9; ++i) mbar_init(&full_k[i], 1);
-    mbar_init(weights, kWeighers / 32);
+    mbar_init(&weights[0], kWeighers / 32);
+    mbar_init(&weights[1], kWeighers / 32);
     mbar_init(added, kAdders / 32);
     mbar_init(queries, kWeighers / 32);
     mbar_init(stat_full, kWeighers / 32);
@@ -222,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
   const uint32_t tm = *base;
   if (!beside) pdl_wait();  // as in attention_pages_kernel
   pdl_trigger();
-  const auto wait = [](uint64_t* bar, int parity) {
-    if (!mbar_wait(bar, (uint32_t)parity)) g_err_attention_shared_tc = 1u;
+  const auto wait = [&](uint64_t* bar, int parity) {  // tells which barrier it was that did not come
+    if (!mbar_wait(bar, (uint32_t)parity)) atomicOr(&g_err_attention_shared_tc, 2u << (int)(bar - full_k));
   };
 
   if (warp >= (kWeighers + kAdders) / 32) {
@@ -302,12 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
             if (one) commit(&scores[(m + 1) & 1]);
             __syncwarp();
           }
-          if (!out) continue;
-          wait(weights, m & 1);
+          if (!out) {
+            if (n + 1 < end) wait(&full_k[(n + 1) & 1], (n + 1) >> 1 & 1);
+            continue;
+          }
+          wait(&weights[m & 1], m >> 1 & 1);
           fence_after();
 #pragma unroll 1
           for (int part = PARTS - 1; part > 0; --part) weigh(m, part);
-          if (m + 2 < end) wait(&full_k[m & 1], (m + 2) >> 1 & 1);
+          if (m + 2 < end) wait(&full_k[m & 1], (m + 2) >> 1 & 1);  // (the first two pages': above)
           odd_page = strange[5 * (m % 3) + 4];
           weigh(m, 0);
           if (one) {
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       tm_st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) arrive(weights);
+      if (lane == 0) arrive(&weights[n & 1]);
     }
 
     // ---- the part's end

@@ -482,6 +482,25 @@ def test_wide_tiles_on_streams_and_in_graphs():
 
 
 # ----------------------------------------------------- long contexts, large pools
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_many_calls_give_the_same_bits(kind):
+    """Samples of eight prompts: both kernels beside each other, short runs of tiles of 128 rows.
+    A wait that could miss what it waits for would, in one of so many calls, run out."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(31)
+    table, blocks, lens, total = _tree(rng, 8, 8, 8, 9, rng.integers(1, 700, 64))
+    dev, _ = _pools(rng, total, 8, 128, kind)
+    kv, batch = d.kv_pages(dev[0], dev[1], _type(kind)[0]), d.PagedBatch(table, blocks, [0] * 64, [1] * 64, lens)
+    q, ws = to_dev(rng.standard_normal((64, 40, 128)).astype(np.float32)), d.Workspace(64, 40, 128, max(lens))
+    want, out = d.attention_decode_shared(q, kv, batch, ws), t.empty_like(q)
+    wrong = t.zeros((), dtype=t.int64, device="cuda")
+    for i in range(20_000):
+        d.attention_decode_shared(q, kv, batch, ws, out=out)
+        if i % 20 == 0:
+            wrong += (out != want).sum()
+    assert int(wrong) == 0
+    d.device_error()
+
+
 def test_a_context_of_more_pages_than_a_segment_holds():
     rng = np.random.default_rng(24)
     n = 300_000
