@@ -16,7 +16,7 @@
 // (bf16) of 128 x 128 x 16 for a page of 128-wide heads.
 //
 // Measured (GB300), 128-wide heads, 40 on 8: prompts of 4 x 1000 tokens behind 4096 keys, bf16,
-// 683 us with the join, 0.55 PFLOP/s, in three parts 1.65 (tensor pipe active 0.74 of the
+// 689 us with the join, 0.55 PFLOP/s, in three parts 1.64 (tensor pipe active 0.74 of the
 // time); drafts of 32 sessions on 32768 keys, fp16, 97 us on 123 SMs (0.59).  A page takes
 // 2800 cycles (fp16) or 4000 (bf16): a product with both operands in shared memory 106, one
 // with its left operand in tensor memory 73, which makes 2860 and 4300 one after the other.
