@@ -290,8 +290,19 @@ def prepare(case, seed):
         from session_decode_step_dsb_gb300 import dsb
         dt = dsb.DSB_F16 if case["kind"] == "f16" else dsb.DSB_BF16
         s["kv"] = dsb.kv_pages(k, v if op != "select" else torch.empty_like(k), dt)
-        s["batch"] = dsb.PagedBatch(table.numpy(), blocks, [0] * len(lens), fresh, lens)
-        s["ws"] = dsb.Workspace(max(n_tok, 1), hq, d, max(lens))
+        # a call serves up to 8192 new tokens: larger batches go in several, sequence by sequence
+        at, s["calls"] = 0, []
+        while at < len(lens):
+            end, rows = at, 0
+            while end < len(lens) and rows + fresh[end] <= 8192:
+                rows, end = rows + fresh[end], end + 1
+            first = sum(fresh[:at])
+            s["calls"].append((s["q"][first:first + rows], slice(first, first + rows),
+                               dsb.PagedBatch(table[at:end].numpy(), blocks[at:end], [0] * (end - at), fresh[at:end],
+                                              lens[at:end])))
+            at = end
+        s["batch"] = s["calls"][0][2]
+        s["ws"] = dsb.Workspace(max(max(len(q) for q, _, _ in s["calls"]), 1), hq, d, max(lens))
     return s
 
 
@@ -335,7 +346,12 @@ def _grid(s):
 def _run_shared(s):
     if own:
         from session_decode_step_dsb_gb300 import dsb
-        return dsb.attention_decode_shared(s["q"], s["kv"], s["batch"], s["ws"])
+        if len(s["calls"]) == 1:
+            return dsb.attention_decode_shared(s["q"], s["kv"], s["batch"], s["ws"])
+        out = torch.empty_like(s["q"])
+        for q, rows, batch in s["calls"]:
+            dsb.attention_decode_shared(q, s["kv"], batch, s["ws"], out=out[rows])
+        return out
     case, new = s["case"], s["new"]
     n, hkv, hq, d = len(s["lens"]), case["hkv"], case["hq"], case["d"]
     key, val = (x[s["table_dev"]].transpose(1, 2).reshape(n, hkv, -1, d).float() for x in (s["k"], s["v"]))
