@@ -892,7 +892,11 @@ def _paged_q(q, kv: KVPages, batch: PagedBatch, out, stream):
     if kv._device != dev:
         raise ValueError(f"the page pool must live on cuda:{dev}")
     if out is None:
-        out = _empty_on(stream, shape, q.dtype, q.device)
+        if stream is None and q.is_contiguous():
+            import torch
+            out = torch.empty_like(q)      # 2 us less of the host's time than a shape's
+        else:
+            out = _empty_on(stream, shape, q.dtype, q.device)
     elif out is not False:
         _need(out, 4 * n_tok * hq * d, "out", "f32")
         if not out.is_contiguous():
