@@ -718,10 +718,13 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
     std::vector<SelLaunch> launches;
     if ((st = selection_launches(b, wide_pages(kv), cs, &launches)) != DSB_OK) return st;
     const int tiles = (n_q_heads / hkv + 7) / 8, resident = dsbk::page_attn_resident(dev.sms);
+    // entries read of every list: of the call, however it is cut into launches
+    const int longest = *std::max_element(b->seq_lens, b->seq_lens + b->n_seq);
+    const int read = std::min(n_select, (longest - 1) / DSB_KV_PAGE + 1);
     std::vector<dsbk::PageAttnArgs> args;
     for (const SelLaunch& l : launches) {
       dsbk::PageAttnArgs a = {};
-      a.n_select = std::min(n_select, l.most);  // a list's pages come first
+      a.n_select = read;
       const long long work = (long long)l.n_tok * hkv * tiles * (a.n_select + dsbk::kLead8);
       if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
       a.ctas = (int)std::min<long long>(resident, work);
