@@ -312,6 +312,9 @@ struct Tree {
   }
 };
 
+// Work of a launch, in pages, counts in 32 bits.
+constexpr int kMostWork = INT_MAX / 2;
+
 // The largest number of parts that a run of n pages has, where every CTA takes at least
 // `share` pages of work.
 int most_parts(int n, long long share) {
@@ -335,13 +338,15 @@ struct Launch {
   int ctas = 1;
 };
 
-// A launch of a call on selected pages: sequences whose metadata it holds.
+// A launch of a call on selected pages: sequences, or tokens of them, whose metadata it holds.
 struct SelLaunch {
   std::vector<int32_t> words;
   int n_seq = 0, tok0 = 0, n_tok = 0, most = 0;
 };
 
-dsb_status selection_launches(const dsb_paged_batch* b, bool wide, cudaStream_t cs, std::vector<SelLaunch>* out) {
+// most_tok: new tokens of a launch; a sequence with more of them is cut.
+dsb_status selection_launches(const dsb_paged_batch* b, bool wide, int most_tok, cudaStream_t cs,
+                              std::vector<SelLaunch>* out) {
   const auto pages = [&](int s) { return b->new_tokens[s] == 0 ? 0 : (b->seq_lens[s] - 1) / DSB_KV_PAGE + 1; };
   size_t all = 0;
   for (int s = 0; s < b->n_seq; ++s) all += dsbk::kSelSeqWords + page_words(pages(s), wide);
@@ -352,33 +357,41 @@ dsb_status selection_launches(const dsb_paged_batch* b, bool wide, cudaStream_t 
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
     if (cap != cudaStreamCaptureStatusNone) room = dsbk::kParamWords;
   }
-  std::vector<int> mine;
+  struct Tokens {
+    int s, n, len;  // sequence, new tokens, keys up to the last of them
+  };
+  std::vector<Tokens> mine;
   size_t have = 0;
-  int tok = 0;
+  int tok = 0, taken = 0;
   const auto close = [&]() {
     SelLaunch l;
     l.n_seq = (int)mine.size();
     l.tok0 = tok;
     int at = l.n_seq * dsbk::kSelSeqWords;
-    for (int s : mine) {
-      l.words.insert(l.words.end(), {l.n_tok, b->new_tokens[s], b->seq_lens[s], at});
-      l.n_tok += b->new_tokens[s];
-      l.most = std::max(l.most, pages(s));
-      at += (int)page_words(pages(s), wide);
+    for (const Tokens& t : mine) {
+      l.words.insert(l.words.end(), {l.n_tok, t.n, t.len, at});
+      l.n_tok += t.n;
+      l.most = std::max(l.most, pages(t.s));
+      at += (int)page_words(pages(t.s), wide);
     }
-    for (int s : mine) put_pages(&l.words, pages(s), wide, [&](int i) { return page_of(b, s, i); });
+    for (const Tokens& t : mine) put_pages(&l.words, pages(t.s), wide, [&](int i) { return page_of(b, t.s, i); });
     tok += l.n_tok;
     out->push_back(std::move(l));
     mine.clear();
     have = 0;
+    taken = 0;
   };
   for (int s = 0; s < b->n_seq; ++s) {
-    if (b->new_tokens[s] == 0) continue;
     const size_t need = dsbk::kSelSeqWords + page_words(pages(s), wide);
-    if (need > room) return fail(DSB_ERR_UNSUPPORTED, "sequence %d: a call holds at most %zu words of metadata", s, room);
-    if (have + need > room) close();
-    mine.push_back(s);
-    have += need;
+    if (b->new_tokens[s] > 0 && need > room)
+      return fail(DSB_ERR_UNSUPPORTED, "sequence %d: a call holds at most %zu words of metadata", s, room);
+    for (int j = 0, n; j < b->new_tokens[s]; j += n) {
+      if (have + need > room || taken == most_tok) close();
+      n = std::min(b->new_tokens[s] - j, most_tok - taken);
+      mine.push_back({s, n, b->seq_lens[s] - b->new_tokens[s] + j + n});
+      have += need;
+      taken += n;
+    }
   }
   if (!mine.empty()) close();
   return DSB_OK;
@@ -488,8 +501,8 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
           return fail(DSB_ERR_UNSUPPORTED, "a call holds at most %zu words of metadata for the pages of %d sequences", room,
                       g.m1 - g.m0);
         const long long work = hkv * g.work_a_head();
-        if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
-        if (!open || launches.back().n_words + n > room || launches.back().work + work > INT_MAX / 2) {
+        if (work > kMostWork) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+        if (!open || launches.back().n_words + n > room || launches.back().work + work > kMostWork) {
           launches.emplace_back();
           launches.back().tile = tile;
           open = true;
@@ -662,7 +675,7 @@ dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, 
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
     std::vector<SelLaunch> launches;
-    if ((st = selection_launches(b, wide_pages(kv), cs, &launches)) != DSB_OK) return st;
+    if ((st = selection_launches(b, wide_pages(kv), n_tok, cs, &launches)) != DSB_OK) return st;
     for (const SelLaunch& l : launches) {
       dsbk::MetaArg meta;
       if ((st = meta_arg(ws, l.words, cs, &meta)) != DSB_OK) return st;
@@ -715,18 +728,20 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
     if ((st = check_workspace(ws)) != DSB_OK) return st;
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
-    std::vector<SelLaunch> launches;
-    if ((st = selection_launches(b, wide_pages(kv), cs, &launches)) != DSB_OK) return st;
     const int tiles = (n_q_heads / hkv + 7) / 8, resident = dsbk::page_attn_resident(dev.sms);
     // entries read of every list: of the call, however it is cut into launches
     const int longest = *std::max_element(b->seq_lens, b->seq_lens + b->n_seq);
     const int read = std::min(n_select, (longest - 1) / DSB_KV_PAGE + 1);
+    const long long work_a_token = (long long)hkv * tiles * (read + dsbk::kLead8);
+    if (work_a_token > kMostWork) return fail(DSB_ERR_UNSUPPORTED, "%d listed pages for %d query heads", read, n_q_heads);
+    std::vector<SelLaunch> launches;
+    const int most_tok = (int)std::min<long long>(n_tok, kMostWork / work_a_token);
+    if ((st = selection_launches(b, wide_pages(kv), most_tok, cs, &launches)) != DSB_OK) return st;
     std::vector<dsbk::PageAttnArgs> args;
     for (const SelLaunch& l : launches) {
       dsbk::PageAttnArgs a = {};
       a.n_select = read;
-      const long long work = (long long)l.n_tok * hkv * tiles * (a.n_select + dsbk::kLead8);
-      if (work > INT_MAX / 2) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
+      const long long work = l.n_tok * work_a_token;
       a.ctas = (int)std::min<long long>(resident, work);
       a.sel_cap = a.slots = most_parts(a.n_select, work / a.ctas);
       const size_t need = (size_t)l.n_tok * n_q_heads * a.slots * (D + 2) * sizeof(float);

@@ -52,3 +52,23 @@ def test_lists_are_read_alike_in_every_launch(long, short):
     call = lambda: d.attention_decode_selected(qd, kv, batch, sd, ws)
     _check(call(), want, bound, "called")
     _check(_captured(call), want, bound, "captured")
+
+
+def test_selected_pages_of_long_prompts_and_many_heads():
+    """More rows times listed pages than a launch counts: a prompt of 8192 tokens, 64 heads, 2100 pages
+    of a small pool."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(41)
+    new, h, D, n, total = 8192, 64, 64, 2100, 8
+    table = rng.integers(0, total, (1, n)).astype(np.int32)
+    dev, (k, v) = _pools(rng, total, h, D, "f16")
+    q = t.from_numpy(rng.standard_normal((1, h, D)).astype(np.float32)).cuda().expand(new, h, D).contiguous()
+    sel = t.full((new, h, n), -1, dtype=t.int32, device="cuda")
+    sel[:, :, n - 2] = t.arange(new, device="cuda")[:, None] % (n - new // P)       # a page that every token sees
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, [n], [0], [new], [n * P])
+    got = d.attention_decode_selected(q, kv, batch, sel, d.Workspace(64, h, D, n * P))
+    one = q[:1].double().cpu().numpy()
+    for b in range(total):                                   # the rows of a page are all alike
+        at = np.flatnonzero(table[0, np.arange(new) % (n - new // P)] == b)
+        want, bound = op.attention(one, k, v, np.array([[b]]), [1], [0], [1], [P])
+        x = to_host(got[t.from_numpy(at).cuda()]).astype(np.float64)
+        assert (np.abs(x - want) <= bound).all(), f"page {b}"
