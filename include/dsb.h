@@ -563,8 +563,10 @@ dsb_status dsb_kv_gather_q4(const dsb_kv_q4_pages* kv, const dsb_paged_batch* ba
  * (pages move, block tables follow), sessions that begin alike read the same pages, and
  * a long context is read in part.  They are no restatement of the pages that the
  * library was built from.  As above, metadata of up to 4032 words rides in the
- * launches, which can then be captured into a CUDA graph; under capture a longer call
- * is cut between sequences where each fits, and DSB_ERR_UNSUPPORTED where one does not. */
+ * launches, which can then be captured into a CUDA graph; a longer call is cut into
+ * several launches.  What is not cut are the page numbers of a sequence whose pages are
+ * selected: a call serves up to 22554 pages of each (11277 in a pool of more than
+ * 65536), under capture 8056 (4028), and more are DSB_ERR_UNSUPPORTED. */
 
 /* Copies rows 0 .. keys[i] - 1 of page src[i] to page dst[i], of every kv head, K and V,
  * in each of n_pools pools (host array, one for each layer; all of one dtype, n_pages,

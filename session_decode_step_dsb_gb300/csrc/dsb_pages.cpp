@@ -126,25 +126,36 @@ void put_pages(std::vector<int32_t>* words, int n, bool wide, Page page) {
   }
 }
 
+// Work of a launch, in pages, counts in 32 bits.
+constexpr int kMostWork = INT_MAX / 2;
+
 // ---- the plan of an attention over shared pages -------------------------------------
 
+// Where a segment's metadata or work would not fit a launch, its sequences' tokens are
+// divided between several, a group: beside each other in Tree::segs, of the same pages,
+// sequences and slots.
 struct Segment {
-  int parent;     // segment of the pages before these, or -1
-  int m0, m1;     // its sequences in Tree::order
+  int parent;     // a segment of the pages before these (any of a group), or -1
+  int group;      // the first one of its group
+  int m0, m1;     // the group's sequences in Tree::order
+  int t0, t1;     // its own of their new tokens, counted one sequence after the other
+  int members;    // sequences that it has tokens of
   int b0, n;      // first block, pages
-  int rows = 0;   // query rows on a kv head
-  int tile = 8;   // of them go through the pages together
+  int rows;       // query rows on a kv head
+  int tile;       // of them go through the pages together
   int slot0 = 0, cap = 0;
   std::vector<int32_t> table;  // of its tiles, where they see only some of its pages
 
   int tiles() const { return (rows + tile - 1) / tile; }
-  int lead() const { return tile == 8 ? dsbk::kLead8 : dsbk::kLead128; }
+  static int lead_of(int tile) { return tile == 8 ? dsbk::kLead8 : dsbk::kLead128; }
+  int lead() const { return lead_of(tile); }
   long long work_a_head() const { return table.empty() ? (long long)tiles() * (n + lead()) : table.back(); }
 };
 
 struct Tree {
   const dsb_paged_batch* b;
-  int G;
+  int G, hkv;
+  bool wide_numbers;       // of pages
   bool wide;               // tiles of 128 rows are taken where they cost less
   std::vector<int> order;  // sequences with new tokens; a segment's are side by side
   std::vector<Segment> segs;
@@ -156,10 +167,10 @@ struct Tree {
     const int w = b->window[s];
     return w > 0 ? std::max(0, b->seq_lens[s] - b->new_tokens[s] + 1 - w) / DSB_KV_PAGE : 0;
   }
-  int rows_of(int m0, int m1) const {
-    int r = 0;
-    for (int m = m0; m < m1; ++m) r += G * b->new_tokens[order[m]];
-    return r;
+  int tokens_of(int m0, int m1) const {
+    int n = 0;
+    for (int m = m0; m < m1; ++m) n += b->new_tokens[order[m]];
+    return n;
   }
   // What n pages cost a segment of so many rows.
   int tile_of(int rows, int n) const { return wide ? dsbk::shared_tile_rows(rows, n) : 8; }
@@ -172,18 +183,18 @@ struct Tree {
     if (n <= 0) return false;
     long long apart = 0;
     for (int m = m0; m < m1; ++m) apart += cost(G * b->new_tokens[order[m]], n);
-    const int rows = rows_of(m0, m1);
+    const int rows = G * tokens_of(m0, m1);
     return apart > cost(rows, n) + cost(rows, 3);
   }
 
   // Pages that each tile of a sequence's rows sees of its segment, where that is not all:
   // (work of the tiles before, first page) of each, and the work of all.
   void cut_tiles(Segment* g) const {
-    const int s = order[g->m0], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
+    const int s = order[g->m0], pos0 = b->seq_lens[s] - b->new_tokens[s] + g->t0, w = b->window[s];
     int sum = 0;
     bool cut = false;
     for (int r = 0; r < g->rows; r += g->tile) {
-      const int lo = len - n + r / G, hi = len - n + (std::min(r + g->tile, g->rows) - 1) / G;
+      const int lo = pos0 + r / G, hi = pos0 + (std::min(r + g->tile, g->rows) - 1) / G;
       const int from = w > 0 ? std::max(0, lo - w + 1) / DSB_KV_PAGE : 0;
       int a = std::max(from - g->b0, 0), z = std::min(hi / DSB_KV_PAGE - g->b0, g->n - 1);
       if (a > z) a = z = 0;  // none of them: one page, all hidden
@@ -196,14 +207,29 @@ struct Tree {
   }
 
   int add(int parent, int m0, int m1, int b0, int b1) {
-    // a segment's metadata has to fit a launch
-    for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {
-      Segment s{parent, m0, m1, b0, std::min(kMost, b1 - b0)};
-      s.rows = rows_of(m0, m1);
-      s.tile = tile_of(s.rows, b1 - b0);
-      if (m1 - m0 == 1 && s.tiles() > 1) cut_tiles(&s);
-      parent = (int)segs.size();
-      segs.push_back(s);
+    const int tokens = tokens_of(m0, m1);
+    for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {  // pages of a segment
+      const int n = std::min(kMost, b1 - b0), tile = tile_of(G * tokens, b1 - b0), group = (int)segs.size();
+      // Words that a launch's parameters have for sequences and the tiles' table; the tokens whose tiles
+      // such a table holds, and whose work is counted; the sequences.
+      const int room = dsbk::kParamWords - 1 - dsbk::kSharedSegWords - (int)page_words(n, wide_numbers);
+      const int places = (room - dsbk::kSharedMemWords - 1) / 2;
+      long long most = kMostWork / ((long long)hkv * (n + Segment::lead_of(tile))) * tile / G;
+      if (m1 - m0 == 1) most = std::min(most, std::max(1LL, (long long)places * tile / G));
+      const int share = (int)((tokens + (tokens + most - 1) / most - 1) / ((tokens + most - 1) / most));
+      for (int t0 = 0, m = m0, m_end = 0; t0 < tokens;) {  // m: the sequence of t0, whose tokens end at m_end
+        Segment g{parent, group, m0, m1, t0, t0, 0, b0, n, 0, tile};
+        while (g.t1 < std::min(t0 + share, tokens) && g.members < room / dsbk::kSharedMemWords) {
+          while (m_end <= g.t1) m_end += b->new_tokens[order[m++]];
+          g.t1 = std::min({t0 + share, tokens, m_end});
+          ++g.members;
+        }
+        g.rows = G * (g.t1 - t0);
+        if (m1 - m0 == 1 && g.tiles() > 1 && g.tiles() <= places) cut_tiles(&g);  // (more: one token's, which see the same)
+        t0 = g.t1;
+        segs.push_back(std::move(g));
+      }
+      parent = group;
     }
     return parent;
   }
@@ -247,27 +273,32 @@ struct Tree {
   // work: CTAs side by side then take the tiles through the same pages at the same time,
   // which come from memory once (a CTA that goes through all pages of a tile, and others at
   // other places of theirs, read 134 MB of pages three times).
-  void cut_shares(int hkv, int ctas) {
+  void cut_shares(int ctas) {
     long long work = 0;
     for (const Segment& g : segs)
       if (g.tile == 128) work += hkv * g.work_a_head();
     const int share = std::max(16, (int)((work + ctas - 1) / ctas));  // (shorter pieces would be mostly ends)
     std::vector<Segment> out;
     std::vector<int> last(segs.size());
-    for (size_t i = 0; i < segs.size(); ++i) {
-      const Segment& g = segs[i];
-      const bool cut = g.tile == 128 && g.tiles() > 1 && g.table.empty();
-      const int pieces = cut ? std::max(1, (g.n + share / 2) / share) : 1;
-      int parent = g.parent >= 0 ? last[g.parent] : -1;
+    for (size_t i = 0, z; i < segs.size(); i = z) {  // a group alike
+      bool cut = true;
+      for (z = i; z < segs.size() && segs[z].group == (int)i; ++z)
+        cut = cut && segs[z].tile == 128 && segs[z].tiles() > 1 && segs[z].table.empty();
+      const int n = segs[i].n, pieces = cut ? std::max(1, (n + share / 2) / share) : 1;
+      int parent = segs[i].parent >= 0 ? last[segs[i].parent] : -1;
       for (int k = 0; k < pieces; ++k) {
-        Segment p = g;
-        p.parent = parent;
-        p.b0 = g.b0 + (int)((long long)g.n * k / pieces);
-        p.n = g.b0 + (int)((long long)g.n * (k + 1) / pieces) - p.b0;
-        parent = (int)out.size();
-        out.push_back(std::move(p));
+        const int group = (int)out.size(), from = (int)((long long)n * k / pieces), upto = (int)((long long)n * (k + 1) / pieces);
+        for (size_t g = i; g < z; ++g) {
+          Segment p = segs[g];
+          p.parent = parent;
+          p.group = group;
+          p.b0 += from;
+          p.n = upto - from;
+          out.push_back(std::move(p));
+        }
+        parent = group;
       }
-      last[i] = parent;
+      last[i] = parent;  // (a group's first one is what others name)
     }
     for (int& e : end)
       if (e >= 0) e = last[e];
@@ -279,7 +310,7 @@ struct Tree {
   // each with its beginning and its end: 64 samples 50 us for 46, a document's drafts 109 for
   // 103).  In units of 0.1 us: a page of a tile 1.4 and 0.7, and 2 us more for the tcgen05 kernel to
   // begin.
-  int wide_sms(int hkv, int sms) const {
+  int wide_sms(int sms) const {
     long long cost[2] = {0, 0};
     for (const Segment& g : segs) cost[g.tile == 128] += hkv * g.work_a_head() * (g.tile == 128 ? 14 : 7);
     if (cost[0] == 0 || cost[1] == 0) return sms;
@@ -311,9 +342,6 @@ struct Tree {
     for (int m = linear; m < (int)order.size(); ++m) split(m, m + 1, 0, 0, -1);
   }
 };
-
-// Work of a launch, in pages, counts in 32 bits.
-constexpr int kMostWork = INT_MAX / 2;
 
 // The largest number of parts that a run of n pages has, where every CTA takes at least
 // `share` pages of work.
@@ -460,24 +488,24 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
 
     DeviceInfo dev;
     if ((st = device_info(&dev)) != DSB_OK) return st;
-    Tree tree{b, n_q_heads / hkv, true, {}, {}, {}};
+    const bool wide = wide_pages(kv);
+    Tree tree{b, n_q_heads / hkv, hkv, wide, true, {}, {}, {}};
     tree.build();
     // the tcgen05 kernel's launch has to save what it takes
     long long saved = 0;
     for (const Segment& g : tree.segs)
       saved += dsbk::shared_tile_cost(g.rows, g.n, 8) - dsbk::shared_tile_cost(g.rows, g.n, g.tile);
     if (saved > 0 && saved * hkv < (long long)dsbk::kWideCost * dev.sms) {
-      tree = Tree{b, n_q_heads / hkv, false, {}, {}, {}};
+      tree = Tree{b, n_q_heads / hkv, hkv, wide, false, {}, {}, {}};
       tree.build();
     }
-    const int wide_sms = tree.wide_sms(hkv, dev.sms), sms8 = wide_sms < dev.sms ? dev.sms - wide_sms : dev.sms;
-    tree.cut_shares(hkv, wide_sms);
+    const int wide_sms = tree.wide_sms(dev.sms), sms8 = wide_sms < dev.sms ? dev.sms - wide_sms : dev.sms;
+    tree.cut_shares(wide_sms);
     std::vector<int> tok0(b->n_seq);
     for (int s = 0, t = 0; s < b->n_seq; t += b->new_tokens[s], ++s) tok0[s] = t;
-    const bool wide = wide_pages(kv);
     const auto words_of = [&](const Segment& g) {
-      return (size_t)dsbk::kSharedSegWords + (size_t)(g.m1 - g.m0) * dsbk::kSharedMemWords +
-             page_words(g.n, wide) + g.table.size();
+      return (size_t)dsbk::kSharedSegWords + (size_t)g.members * dsbk::kSharedMemWords + page_words(g.n, wide) +
+             g.table.size();
     };
 
     // launches: what a captured call keeps has to ride in its parameters
@@ -497,11 +525,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         const Segment& g = tree.segs[i];
         if (g.tile != tile) continue;
         const size_t n = words_of(g);
-        if (1 + n > room)
-          return fail(DSB_ERR_UNSUPPORTED, "a call holds at most %zu words of metadata for the pages of %d sequences", room,
-                      g.m1 - g.m0);
         const long long work = hkv * g.work_a_head();
-        if (work > kMostWork) return fail(DSB_ERR_UNSUPPORTED, "too many attention items");
         if (!open || launches.back().n_words + n > room || launches.back().work + work > kMostWork) {
           launches.emplace_back();
           launches.back().tile = tile;
@@ -517,7 +541,9 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
       l.ctas = (int)std::min<long long>(l.tile == 8 ? dsbk::page_attn_resident(sms8) : wide_sms, l.work);
       for (int i : l.segs) tree.segs[i].cap = most_parts(tree.segs[i].n, l.work / l.ctas);
     }
+    for (Segment& g : tree.segs) tree.segs[g.group].cap = std::max(tree.segs[g.group].cap, g.cap);
     for (Segment& g : tree.segs) {  // a parent comes before its children
+      g.cap = tree.segs[g.group].cap;
       if (g.parent >= 0) g.slot0 = tree.segs[g.parent].slot0 + tree.segs[g.parent].cap;
       slots = std::max(slots, g.slot0 + g.cap);
     }
@@ -555,19 +581,21 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
         const Segment& g = tree.segs[l.segs[i]];
         int first = INT_MAX, last = 0, most = 0;
         const int mem_at = (int)words.size();
-        for (int m = g.m0, row = 0; m < g.m1; ++m) {
-          const int s = tree.order[m], len = b->seq_lens[s], n = b->new_tokens[s], w = b->window[s];
-          words.insert(words.end(), {row, tok0[s], n, len, w});
-          row += tree.G * n;
-          first = std::min(first, w > 0 ? std::max(0, len - n + 1 - w) : 0);
-          last = std::max(last, len - 1);
+        for (int m = g.m0, row = 0, at = 0; m < g.m1; at += b->new_tokens[tree.order[m++]]) {
+          const int s = tree.order[m], pos0 = b->seq_lens[s] - b->new_tokens[s], w = b->window[s];
           most = std::max(most, slots_of(s));
+          const int j = std::max(g.t0 - at, 0), j_end = std::min(g.t1 - at, b->new_tokens[s]);
+          if (j >= j_end) continue;  // another segment's of the group
+          words.insert(words.end(), {row, tok0[s] + j, j_end - j, pos0 + j_end, w});
+          row += tree.G * (j_end - j);
+          first = std::min(first, w > 0 ? std::max(0, pos0 + j + 1 - w) : 0);
+          last = std::max(last, pos0 + j_end - 1);
         }
         const int pg_at = (int)words.size();
         put_pages(&words, g.n, wide, [&](int p) { return page_of(b, tree.order[g.m0], g.b0 + p); });
         const int table_at = g.table.empty() ? 0 : (int)words.size();
         words.insert(words.end(), g.table.begin(), g.table.end());
-        const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.m1 - g.m0, g.b0, g.n, pg_at,
+        const int32_t rec[dsbk::kSharedSegWords] = {(int32_t)work, g.rows, mem_at, g.members, g.b0, g.n, pg_at,
                                                     g.slot0,       g.cap,  first,  last,        most, table_at};
         std::copy(rec, rec + dsbk::kSharedSegWords, words.begin() + i * dsbk::kSharedSegWords);
         work += hkv * g.work_a_head();

@@ -72,3 +72,62 @@ def test_selected_pages_of_long_prompts_and_many_heads():
         want, bound = op.attention(one, k, v, np.array([[b]]), [1], [0], [1], [P])
         x = to_host(got[t.from_numpy(at).cuda()]).astype(np.float64)
         assert (np.abs(x - want) <= bound).all(), f"page {b}"
+
+
+# ------------------------------------------------- many sessions, large groups
+@pytest.mark.parametrize("groups,per,branch", [(1, 1024, 0), (128, 8, 3)])
+def test_a_thousand_sessions_behind_one_prompt(groups, per, branch):
+    """More sessions on the same pages than one launch's metadata holds, called and captured."""
+    d, rng = _dsb(), np.random.default_rng(per)
+    n, hq, D = 1024, 2, 64
+    table, blocks, lens, total = _tree(rng, groups, per, 2, branch, rng.integers(1, 200, n))
+    dev, (k, v) = _pools(rng, total, 1, D, "f16")
+    q = rng.standard_normal((n, hq, D)).astype(np.float32)
+    want, bound = op.attention(q, k, v, table, blocks, [0] * n, [1] * n, lens)
+    qd, kv, batch = to_dev(q), d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, blocks, [0] * n, [1] * n, lens)
+    ws = d.Workspace(n, hq, D, max(lens))
+    call = lambda: d.attention_decode_shared(qd, kv, batch, ws)
+    _check(call(), want, bound, "called")
+    _check(_captured(call), want, bound, "captured")
+
+
+def _prompt_errors(got, q, k, v, pages, len_, window=0):
+    """Largest error of a prompt's rows over the oracle's bound, in which |v - out| is no more than
+    |v| + |out|: got, q [tokens, hq, D] of the last tokens of len_ keys, one kv head, device tensors."""
+    t = _torch()
+    n, hq, D = got.shape
+    key, val = (x[pages, 0].double().reshape(-1, D)[:len_] for x in (k, v))
+    at, worst = t.arange(len_, device="cuda"), 0.0
+    p = t.arange(len_ - n, len_, device="cuda")[:, None]
+    hidden = (at > p) | (at <= p - window if window else at < 0)
+    for h in range(hq):
+        x = q[:, h].double()
+        score = (x @ key.T / D ** 0.5).masked_fill_(hidden, -np.inf)
+        size = (x.abs() @ key.abs().T).masked_fill_(hidden, 0).amax(-1, keepdim=True) / D ** 0.5
+        e = t.softmax(score, -1)
+        want, mag = e @ val, e @ val.abs()
+        bound = 2.0 ** -20 * 2 * (size + 1) * (mag + want.abs()) + 2.0 ** -20 * mag
+        bound += 2.0 ** -35 * e.amax(-1, keepdim=True) * ((~hidden).double() @ val.abs())
+        worst = max(worst, float(((got[:, h].double() - want).abs() / bound).max()))
+    return worst
+
+
+@pytest.mark.parametrize("hq,new,before,window,captured", [
+    (64, 4096, 0, 0, True), (128, 8192, 0, 0, False), (128, 8192, 0, 0, True), (80, 4000, 500, 300, True), (5, 8192, 300, 0, True)])
+def test_prompts_of_many_rows(hq, new, before, window, captured):
+    """More tiles of rows than one launch's metadata has places for what each sees."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(hq)
+    D, len_ = 64, new + before
+    n = -(-len_ // P)
+    nb = -(-(window + new - 1) // P) + 1 if window else n
+    order = rng.permutation(n + 2)
+    dev = [t.randn((n + 2, 1, P, D), device="cuda", generator=t.Generator("cuda").manual_seed(i)).half() for i in (1, 2)]
+    table = order[:nb] if window else order[:n]
+    pages = [int(table[i % nb]) for i in range(n)]           # (what a ring's older blocks held, no row sees)
+    q = t.randn((new, hq, D), device="cuda", generator=t.Generator("cuda").manual_seed(3))
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table[None].astype(np.int32), [nb], [window], [new], [len_])
+    ws = d.Workspace(new, hq, D, len_)
+    call = lambda: d.attention_decode_shared(q, kv, batch, ws)
+    got = _captured(call) if captured else call()
+    assert _prompt_errors(got, q, dev[0], dev[1], pages, len_, window) <= 1
+    d.device_error()
