@@ -253,22 +253,17 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
 #pragma unroll
       for (int k = 0; k < KK; ++k)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[k][j] = make_float2(x[k][j].x * scale_log2e, x[k][j].y * scale_log2e);
-          m = fmaxf(m, fmaxf(fabsf(x[k][j].x), fabsf(x[k][j].y)));
-        }
+        for (int j = 0; j < 2; ++j) m = fmaxf(m, fmaxf(fabsf(x[k][j].x), fabsf(x[k][j].y)));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
-      // keep their bits whatever q's size
-      const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
-      const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
-      rs = __uint_as_float((uint32_t)(ex - 10) << 23);
+      float by;
+      row_powers<T>(m, by, rs);
+      by *= scale_log2e;
 #pragma unroll
       for (int k = 0; k < KK; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float x0 = x[k][j].x * inv, x1 = x[k][j].y * inv;
+          float x0 = x[k][j].x * by, x1 = x[k][j].y * by;
           qa[k][2 * j] = Parts<T>::take(x0, x1);
           qa[k][2 * j + 1] = Parts<T>::take(x0, x1);
           if constexpr (kThird) qb[k][j] = Parts<T>::take(x0, x1);

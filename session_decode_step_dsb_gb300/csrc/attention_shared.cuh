@@ -17,6 +17,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include "dsb_f32x2.cuh"
 #include "dsb_kernels.h"
@@ -77,6 +78,21 @@ struct Parts<__nv_bfloat16> {
     return w;
   }
 };
+
+// The powers of two that a query row, with m its largest value, is multiplied by before it
+// is cut into parts, and its scores after.  fp16: m goes to [2^13, 2^14), and with the
+// scores' factor to [2^10, 2^12): the parts keep their bits whatever q's size, and no key makes
+// more than 2^35.  bf16 has float32's range, and its keys too: a row stays as it is, and its
+// products are finite where float32's own are.  Only one below 2^-60, whose third parts could
+// lie below the type's least value, is lifted there.
+template <typename T>
+__device__ __forceinline__ void row_powers(float m, float& before, float& after) {
+  const int ex = (int)(__float_as_uint(m) >> 23);
+  const int to = std::is_same_v<T, __half> ? 140 : 67;
+  const int up = to - (std::is_same_v<T, __half> ? min(max(ex, 14), 254) : min(max(ex, 1), 67));
+  before = __uint_as_float((uint32_t)(127 + up) << 23);
+  after = __uint_as_float((uint32_t)(127 - up) << 23);
+}
 
 // Where sums go: statistics (-reference, sum of weights) and sums of weighted values of
 // [row][slot]; out where a row has one part.  A sum of weights of -1: the row is done.

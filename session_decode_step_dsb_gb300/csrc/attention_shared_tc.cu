@@ -489,17 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + (j + i) * ROWS + lane / LANES;
-          float v[4] = {x[i].x * scale_log2e, x[i].y * scale_log2e, x[i].z * scale_log2e, x[i].w * scale_log2e};
+          float v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
           for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          // the row over a power of two that brings its largest value to [2^10, 2^11): the parts
-          // keep their bits whatever q's size
-          const int ex = min(max((int)(__float_as_uint(m) >> 23), 11), 254);
-          const float inv = __uint_as_float((uint32_t)(264 - ex) << 23);
-          if (l == 0) top[r] = __uint_as_float((uint32_t)(ex - 10) << 23);
+          float by, after;
+          row_powers<T>(m, by, after);
+          if (l == 0) top[r] = after;
+          by *= scale_log2e;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] *= inv;
+          for (int k = 0; k < 4; ++k) v[k] *= by;
           const int piece = l >> 1;
           uint8_t* dst = smem + S::q + (piece >> 3) * S::slab + r * 128 + (((piece & 7) ^ (r & 7)) << 4) + (l & 1) * 8;
 #pragma unroll

@@ -131,3 +131,29 @@ def test_prompts_of_many_rows(hq, new, before, window, captured):
     got = _captured(call) if captured else call()
     assert _prompt_errors(got, q, dev[0], dev[1], pages, len_, window) <= 1
     d.device_error()
+
+
+# ------------------------------------------------------ the ends of a type's range
+FORMS = [
+    # hq, hkv, tails, new: rows for the warp-level kernel, and for the tcgen05 one
+    (4, 2, [30, 500], [1, 2]), (2, 1, [40_000], [1]), (20, 2, [600, 300], [600, 2])]
+
+
+def _far(rng, hq, hkv, tails, new, ksize, vsize, qsize, D=64):
+    table, blocks, lens, total = _tree(rng, 1, len(tails), 1, 0, tails)
+    t = _torch()
+    host = [np.clip(rng.standard_normal((total, hkv, P, D)), -3, 3) * x for x in (ksize, vsize)]
+    dev = [t.from_numpy(x).bfloat16().cuda() for x in host]
+    q = (rng.standard_normal((sum(new), hq, D)) * qsize).astype(np.float32)
+    return dev, [x.double().cpu().numpy() for x in dev], q, table, blocks, [0] * len(lens), lens
+
+
+@pytest.mark.parametrize("hq,hkv,tails,new", FORMS)
+@pytest.mark.parametrize("ksize,qsize", [(2.0 ** 100, 2.0 ** -100), (2.0 ** 118, 2.0 ** -117), (2.0 ** 126, 2.0 ** -124),
+                                         (2.0 ** -100, 2.0 ** 100)])
+def test_bf16_keys_of_any_size(hq, hkv, tails, new, ksize, qsize):
+    rng = np.random.default_rng(hq)
+    dev, (k, v), q, table, blocks, window, lens = _far(rng, hq, hkv, tails, new, ksize, 1.0, qsize)
+    got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step("bf16"))
+    _check(got, want, bound)
