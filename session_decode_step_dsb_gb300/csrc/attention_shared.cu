@@ -116,8 +116,8 @@ template <int D, typename T, typename Walk, int N>
 __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
     long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, int n_tok,
-    const int32_t* __restrict__ selected, int n_select, int sel_stride, int sel_cap, float scale_log2e, PartialsOut to,
-    bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+    const int32_t* __restrict__ selected, int n_select, int sel_stride, int sel_cap, float scale_log2e, float unit,
+    PartialsOut to, bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using R = Ring<D>;
   constexpr int KK = D / 16, NT = D / 8;  // steps of the first product, column tiles of the second
   constexpr bool kThird = Parts<T>::kMore > 1;
@@ -336,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
       for (int n = 0; n < 8; ++n) top = fmaxf(top, hidden >> n & 1u ? -INFINITY : p[n] * rs);
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const bool grown = top + minus > kRoom + kSlack;
+      const bool grown = top + minus > Parts<T>::kRoom + kSlack;
       if (__any_sync(0xFFFFFFFFu, grown)) {
-        const float to_minus = grown ? kRoom - top : minus, f = exp2_of(to_minus - minus);
+        const float to_minus = grown ? Parts<T>::kRoom - top : minus, f = exp2_of(to_minus - minus);
         minus = to_minus;
         l *= f;
 #pragma unroll
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         p[n] = hidden >> n & 1u ? 0.0f : exp2_of(fmaf(p[n], rs, minus));
+        if constexpr (kThird) p[n] *= unit;
         l += p[n];
       }
 
@@ -609,7 +610,8 @@ cudaError_t pages_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st
   const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
   return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)R::smem, st, tmk, tmv, a.q, a.q_stride, a.hq,
                        a.hkv, static_cast<const T*>(a.v), a.n_seg, a.n_tok, a.selected, a.n_select,
-                       a.sel_stride, a.sel_cap, (float)(1.4426950408889634 / std::sqrt((double)D)), to, a.wide_pages, a.beside, w, meta.dev);
+                       a.sel_stride, a.sel_cap, (float)(1.4426950408889634 / std::sqrt((double)D)), a.unit, to, a.wide_pages, a.beside, w,
+                       meta.dev);
 }
 
 template <int D, typename T>

@@ -41,9 +41,9 @@ inline cudaError_t allow_smem(Kern kern, int bytes, std::atomic<unsigned long lo
 constexpr int kPgKeys = 128;
 // minus the reference of a row that has seen no key: the reference lies below any score
 constexpr float kNoRef = 0x1.fffffep127f;
-// A row's weights are exp2(score - reference), the reference 2^kRoom below its largest
+// A row's weights are exp2(score - reference), the reference 2^kRoom (of Parts) below its largest
 // score so far; a score that brings 2^kSlack more moves it.
-constexpr float kRoom = 10.0f, kSlack = 4.0f;
+constexpr float kSlack = 4.0f;
 
 __device__ __forceinline__ float exp2_of(float x) {
   float y;
@@ -53,12 +53,16 @@ __device__ __forceinline__ float exp2_of(float x) {
 
 // A float32 pair as pairs of the 16-bit type that add up to it, largest first: two of fp16
 // hold 22 bits (of values scaled into its range), two of bf16 only 16, three 24.  kMore:
-// products of the warp-level kernel, which holds two parts in one.
+// products of the warp-level kernel, which holds two parts in one.  kRoom: the largest weights
+// are 2^10 in fp16, whose range that uses; values up to 2^16 then add up to 2^60 at most.  In
+// bf16 they are 1 times the call's unit, by which weighted values of the type's largest
+// size add up to less than that (see PageAttnArgs).
 template <typename T>
 struct Parts;
 template <>
 struct Parts<__half> {
   static constexpr int kMore = 1;
+  static constexpr float kRoom = 10.0f;
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
     const __half2 h = __floats2half2_rn(x, y);
     const float2 f = __half22float2(h);
@@ -70,6 +74,7 @@ struct Parts<__half> {
 template <>
 struct Parts<__nv_bfloat16> {
   static constexpr int kMore = 2;
+  static constexpr float kRoom = 0.0f;
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);

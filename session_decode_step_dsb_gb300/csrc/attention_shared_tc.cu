@@ -182,8 +182,8 @@ struct Smem {
 template <int D, typename T, int N>
 __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const float* __restrict__ q,
-    long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, float scale_log2e, PartialsOut to,
-    bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
+    long long q_stride, int hq, int hkv, const T* __restrict__ vp, int n_seg, float scale_log2e, float unit,
+    PartialsOut to, bool wide, bool beside, const __grid_constant__ ParamWords<N> words, const int32_t* __restrict__ meta_dev) {
   using S = Smem<D, T>;
   constexpr int PARTS = S::parts, HD = D / 2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -573,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       most = fmaxf(most, top[(part ^ 1) * 128 + row]) * rs;
       // references are whole numbers, so that a change of one is an exponent
       int down = 0;
-      if (most + minus > kRoom + kSlack) {
-        const float to_minus = rintf(kRoom - most);
+      if (most + minus > Parts<T>::kRoom + kSlack) {
+        const float to_minus = rintf(Parts<T>::kRoom - most);
         down = minus - to_minus < 127.0f ? (int)(minus - to_minus) : 127;
         const float f = down > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - down) << 23);
         minus = to_minus;
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
       }
       if (part == 0) fac[128 * (n % 3) + row] = (uint8_t)down;
       // weights; a hidden key's score is -inf here, its weight 0 whatever rs and minus are
-      const f2 rs2 = pack(rs, rs), minus2 = pack(minus, minus);
+      const f2 rs2 = pack(rs, rs), minus2 = pack(minus, minus), unit2 = pack(unit, unit);
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {  // the weights of 32 keys over their scores
         float x[32];
@@ -594,8 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float2 e = unpack(fma2(pack(x[16 * j + 2 * k], x[16 * j + 2 * k + 1]), rs2, minus2));
-            float p0 = exp2_of(e.x), p1 = exp2_of(e.y);
-            sum[k & 1] = add2(sum[k & 1], pack(p0, p1));
+            f2 two = pack(exp2_of(e.x), exp2_of(e.y));
+            if constexpr (PARTS > 2) two = mul2(two, unit2);
+            sum[k & 1] = add2(sum[k & 1], two);
+            float p0 = unpack(two).x, p1 = unpack(two).y;
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) w[p][k] = Parts<T>::take(p0, p1);
           }
@@ -682,7 +684,7 @@ cudaError_t tc_go(const PageAttnArgs& a, const MetaArg& meta, cudaStream_t st) {
     const PartialsOut to{reinterpret_cast<float2*>(a.stat), a.acc, a.out, a.slots};
     return launch_kernel(kern, dim3((unsigned)a.ctas), dim3(kThreads), (size_t)S::bytes, st, tmk, tmv, a.q, a.q_stride,
                          a.hq, a.hkv, static_cast<const T*>(a.v), a.n_seg,
-                         (float)(1.4426950408889634 / std::sqrt((double)D)), to, a.wide_pages, a.beside, w, meta.dev);
+                         (float)(1.4426950408889634 / std::sqrt((double)D)), a.unit, to, a.wide_pages, a.beside, w, meta.dev);
   });
 }
 

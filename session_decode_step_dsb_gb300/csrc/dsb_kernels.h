@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
@@ -390,6 +391,15 @@ inline long long shared_tile_cost(int rows, int n, int tile) {
 inline int shared_tile_rows(int rows, int n) {
   return shared_tile_cost(rows, n, 128) < shared_tile_cost(rows, n, 8) ? 128 : 8;
 }
+// A power of two for weights of up to 2^4 (kSlack of attention_shared.cuh), of which a row of the call
+// has no more than `keys`: together they are no more than 1/2, and bf16 values of any size under
+// them, in whatever parts and in the join of these, add up to less than the largest float32.
+// (float32's least values lie so far below that a value of 2^-100 keeps 24 bits under 2^20 keys.)
+inline float weight_unit(long long keys) {
+  int bits = 0;
+  while (1LL << bits < keys) ++bits;
+  return std::ldexp(1.0f, -(bits + 5));
+}
 struct PageAttnArgs {
   const float* q;
   long long q_stride;
@@ -406,6 +416,7 @@ struct PageAttnArgs {
   float* out;               // [n_tok][hq][head_dim]
   int slots;
   int ctas;
+  float unit;               // of bf16 caches' weights, see weight_unit
   bool wide_pages;          // page numbers of 32 bits, else two to a word
   bool beside;              // launched while the call's kernel before works on
 };

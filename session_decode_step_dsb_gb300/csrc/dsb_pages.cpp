@@ -566,6 +566,7 @@ dsb_status dsb_attention_decode_shared(const float* q, int64_t q_stride, int n_q
     a.stat = a.acc + rows * slots * D;
     a.out = out;
     a.slots = slots;
+    a.unit = dsbk::weight_unit(*std::max_element(b->seq_lens, b->seq_lens + b->n_seq));
     a.wide_pages = wide;
     // Metadata before the launches, as many as there are places for staged ones: a copy
     // between two would keep them apart.
@@ -789,6 +790,7 @@ dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n
       a.acc = reinterpret_cast<float*>(partial_base(ws));
       a.stat = a.acc + (size_t)l.n_tok * n_q_heads * a.slots * D;
       a.out = out + (size_t)l.tok0 * width;
+      a.unit = dsbk::weight_unit((long long)read * DSB_KV_PAGE);
       a.wide_pages = wide_pages(kv);
       args.push_back(a);
     }

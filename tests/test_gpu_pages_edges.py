@@ -157,3 +157,38 @@ def test_bf16_keys_of_any_size(hq, hkv, tails, new, ksize, qsize):
     got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens)
     want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step("bf16"))
     _check(got, want, bound)
+
+
+@pytest.mark.parametrize("hq,hkv,tails,new", FORMS)
+@pytest.mark.parametrize("vsize", [2.0 ** 100, 2.0 ** 118, 2.0 ** 126, 2.0 ** -90])
+def test_bf16_values_of_any_size(hq, hkv, tails, new, vsize):
+    rng = np.random.default_rng(hq)
+    dev, (k, v), q, table, blocks, window, lens = _far(rng, hq, hkv, tails, new, 1.0, vsize, 1.0)
+    got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, weight_step=_step("bf16"))
+    _check(got, want, bound)
+
+
+@pytest.mark.parametrize("hq,hkv,tails,new", FORMS)
+def test_the_largest_bf16_values(hq, hkv, tails, new):
+    """Every value the type's largest, every score alike: a row's result is that value, to the rounding
+    of a sum of weights and of one quotient."""
+    rng, t = np.random.default_rng(hq), _torch()
+    dev, _, q, table, blocks, window, lens = _far(rng, hq, hkv, tails, new, 0.0, 0.0, 1.0)
+    most = t.finfo(t.bfloat16).max
+    dev[1].fill_(most)
+    got = to_host(_attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens)).astype(np.float64)
+    assert (np.abs(got - most) <= most * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("ksize,qsize,vsize", [(2.0 ** 118, 2.0 ** -117, 1.0), (1.0, 1.0, 2.0 ** 126)])
+def test_selected_pages_of_any_size(ksize, qsize, vsize):
+    rng = np.random.default_rng(51)
+    hkv, new = 2, [1, 3]
+    dev, (k, v), q, table, blocks, window, lens = _far(rng, 10, hkv, [3000, 5000], new, ksize, vsize, qsize)
+    sel = np.full((4, hkv, 45), -1, np.int32)
+    for i, (s, p) in enumerate([(0, lens[0] - 1)] + [(1, lens[1] - 3 + j) for j in range(3)]):
+        sel[i, :, :p // P + 1] = np.arange(p // P + 1)
+    got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens, selected=to_dev(sel))
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, sel, weight_step=_step("bf16"))
+    _check(got, want, bound)
