@@ -78,8 +78,11 @@ struct Parts<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t take(float& x, float& y) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-    x -= __uint_as_float(w << 16);
-    y -= __uint_as_float(w & 0xFFFF0000u);
+    // (both at once: the tcgen05 kernel's weights hold its products up; prompts 706 -> 688 us)
+    const float2 left = unpack(fma2(pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)),
+                                    pack(-1.0f, -1.0f), pack(x, y)));
+    x = left.x;
+    y = left.y;
     return w;
   }
 };
