@@ -214,9 +214,14 @@ struct Tree {
       // such a table holds, and whose work is counted; the sequences.
       const int room = dsbk::kParamWords - 1 - dsbk::kSharedSegWords - (int)page_words(n, wide_numbers);
       const int places = (room - dsbk::kSharedMemWords - 1) / 2;
-      long long most = kMostWork / ((long long)hkv * (n + Segment::lead_of(tile))) * tile / G;
-      if (m1 - m0 == 1) most = std::min(most, std::max(1LL, (long long)places * tile / G));
-      const int share = (int)((tokens + (tokens + most - 1) / most - 1) / ((tokens + most - 1) / most));
+      int share = tokens;  // of a segment of the group
+      const int tiles = (G * tokens + tile - 1) / tile, a_tile = n + Segment::lead_of(tile);
+      if ((long long)hkv * tiles * a_tile > kMostWork || (m1 - m0 == 1 && tiles > places)) {
+        long long most = kMostWork / ((long long)hkv * a_tile) * tile / G;
+        if (m1 - m0 == 1) most = std::min(most, std::max(1LL, (long long)places * tile / G));
+        const int parts = (int)((tokens + most - 1) / most);
+        share = (tokens + parts - 1) / parts;
+      }
       for (int t0 = 0, m = m0, m_end = 0; t0 < tokens;) {  // m: the sequence of t0, whose tokens end at m_end
         Segment g{parent, group, m0, m1, t0, t0, 0, b0, n, 0, tile};
         while (g.t1 < std::min(t0 + share, tokens) && g.members < room / dsbk::kSharedMemWords) {
@@ -279,6 +284,7 @@ struct Tree {
       if (g.tile == 128) work += hkv * g.work_a_head();
     const int share = std::max(16, (int)((work + ctas - 1) / ctas));  // (shorter pieces would be mostly ends)
     std::vector<Segment> out;
+    out.reserve(2 * segs.size());
     std::vector<int> last(segs.size());
     for (size_t i = 0, z; i < segs.size(); i = z) {  // a group alike
       bool cut = true;
@@ -289,7 +295,7 @@ struct Tree {
       for (int k = 0; k < pieces; ++k) {
         const int group = (int)out.size(), from = (int)((long long)n * k / pieces), upto = (int)((long long)n * (k + 1) / pieces);
         for (size_t g = i; g < z; ++g) {
-          Segment p = segs[g];
+          Segment p = k + 1 < pieces ? segs[g] : std::move(segs[g]);
           p.parent = parent;
           p.group = group;
           p.b0 += from;
@@ -325,6 +331,7 @@ struct Tree {
 
   void build() {
     end.assign(b->n_seq, -1);
+    segs.reserve(2 * b->n_seq);
     for (int pass = 0; pass < 2; ++pass)
       for (int s = 0; s < b->n_seq; ++s)
         if (b->new_tokens[s] > 0 && (b->window[s] > 0) == (pass == 1)) order.push_back(s);
