@@ -394,16 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_shared_tc_kernel(
               if constexpr (PARTS > 2) got[2] = tm_ld1(mine + S::t_col + 64 * (n & 1) + key / 2);
               tm_ld_wait();
               const float p = (half_of<T>(got[2], key & 1) + half_of<T>(got[1], key & 1)) + half_of<T>(got[0], key & 1);
-              if (key0 + key < at.lo || key0 + key > at.hi) continue;
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(page + (size_t)key * D + d0);
+              if (key0 + key >= at.lo && key0 + key <= at.hi) {
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(page + (size_t)key * D + d0);
 #pragma unroll
-              for (int k = 0; k < HD / 2; ++k) {
-                const uint32_t two = v[k];
-                acc[2 * k] = fmaf(p, half_of<T>(two, 0), acc[2 * k]);
-                acc[2 * k + 1] = fmaf(p, half_of<T>(two, 1), acc[2 * k + 1]);
+                for (int k = 0; k < HD / 2; ++k) {
+                  const uint32_t two = v[k];
+                  acc[2 * k] = fmaf(p, half_of<T>(two, 0), acc[2 * k]);
+                  acc[2 * k + 1] = fmaf(p, half_of<T>(two, 1), acc[2 * k + 1]);
+                }
               }
+              __syncwarp();  // rows that see the key and others load the next one's weight together
             }
-          __syncwarp();
         }
         fence_before();
         __syncwarp();
