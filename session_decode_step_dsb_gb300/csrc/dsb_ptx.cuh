@@ -128,9 +128,17 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 // Programmatic dependent launch.  pdl_wait() blocks until the grid this one
 // depends on has completed and its writes are visible (a no-op when the launch
 // carries no programmatic dependency); pdl_trigger() lets the dependent grid be
-// scheduled once every CTA of this grid has issued it or exited.  Every kernel
+// scheduled once every CTA of this grid has issued it or exited.  A kernel
 // calls pdl_trigger() only after its pdl_wait(), so at most two grids of a
 // chain overlap, and writes no global memory before its pdl_wait().
+// The one exception are the launches of one call that work beside each other
+// (`beside` of attention_shared.cu and attention_shared_tc.cu, which see): the
+// first waits and then triggers as above, the others trigger at once, read and
+// write, and wait before they end.  So a grid has ended only after all grids
+// ahead of it have, and what waits for the last of them (the join, the next call)
+// waits for all.  This holds because what they read (queries, pages, lists,
+// staged metadata) was complete before the first one's wait returned, and because no two
+// of them write, or one writes and another reads, the same memory.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
