@@ -192,3 +192,134 @@ def test_selected_pages_of_any_size(ksize, qsize, vsize):
     got = _attend(to_dev(q), dev, "bf16", table, blocks, window, new, lens, selected=to_dev(sel))
     want, bound = op.attention(q, k, v, table, blocks, window, new, lens, sel, weight_step=_step("bf16"))
     _check(got, want, bound)
+
+
+# ----------------------------------------------- lists and calls of every length
+@pytest.mark.parametrize("kind,hq,hkv,D,n", [("f16", 5, 1, 64, 33), ("bf16", 16, 2, 128, 32), ("f16", 8, 1, 128, 97),
+                                             ("bf16", 3, 3, 64, 200)])
+def test_lists_of_any_length(kind, hq, hkv, D, n):
+    """Lists past the 32 entries that a warp's lanes hold, NaN behind the last keys and on pages of nobody."""
+    t, rng = _torch(), np.random.default_rng(n)
+    lens, new = [29_000, 9_000, 200], [2, 1, 3]
+    table, blocks, _, total = _tree(rng, 1, 3, 0, 0, lens)
+    dev, (k, v) = _pools(rng, total, hkv, D, kind)
+    for x in dev:
+        for s, m in enumerate(lens):
+            x[int(table[s, blocks[s] - 1]), :, (m - 1) % P + 1:] = float("nan")
+        x[t.tensor(sorted(set(range(total)) - {int(b) for s in range(3) for b in table[s, :blocks[s]]})).cuda()] = float("inf")
+    q = rng.standard_normal((6, hq, D)).astype(np.float32)
+    sel = np.full((6, hkv, n), -1, np.int32)
+    for row, (s, p) in enumerate([(0, 28_998), (0, 28_999), (1, 8_999), (2, 197), (2, 198), (2, 199)]):
+        for h in range(hkv):
+            pick = np.sort(np.append(rng.permutation(p // P)[:n - 1 - row % 2], p // P))
+            sel[row, h, :len(pick)] = pick
+    sel[1] = sel[1, :, ::-1]                                 # in another order, behind what is no block
+    got = _attend(to_dev(q), dev, kind, table, blocks, [0] * 3, new, lens, selected=to_dev(sel))
+    want, bound = op.attention(q, k, v, table, blocks, [0] * 3, new, lens, sel, weight_step=_step(kind))
+    _check(got, want, bound)
+
+
+@pytest.mark.parametrize("n_seq,pages", [(3, 3500), (90, 500), (1000, 8)])
+def test_selections_of_several_launches(n_seq, pages):
+    """Metadata beyond a launch's parameters and beyond a place for staged words, called and captured: the
+    selection, and the attention over what it selects."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(n_seq)
+    hq, hkv, D, total, n_select = 4, 2, 64, 48, 6
+    table = rng.integers(0, total, (n_seq, pages)).astype(np.int32)
+    lens = [int(x) for x in rng.integers(pages * P // 2, pages * P, n_seq)]
+    new = [int(x) for x in rng.integers(0, 3, n_seq)]
+    blocks, window = [pages] * n_seq, [0] * n_seq
+    dev, (k, v) = _pools(rng, total, hkv, D, "f16")
+    bnd = np.sort(rng.standard_normal((total, hkv, 2, D)), 2)
+    bnd = t.from_numpy(bnd).half()
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32)
+    qd, bd = to_dev(q), bnd.cuda()
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, blocks, window, new, lens)
+    ws = d.Workspace(sum(new), hq, D, max(lens))
+    pick = lambda: d.kv_select_pages(qd, kv, bd, batch, n_select, ws, keep_first=1, keep_last=2)
+    want_sel = op.select(q, bnd.double().numpy(), table, new, lens, n_select, 1, 2)
+    sel = pick()
+    assert np.array_equal(to_host(sel), want_sel)
+    assert np.array_equal(to_host(_captured(pick)), want_sel)
+    want, bound = op.attention(q, k, v, table, blocks, window, new, lens, want_sel)
+    call = lambda: d.attention_decode_selected(qd, kv, batch, sel, ws)
+    _check(call(), want, bound, "called")
+    _check(_captured(call), want, bound, "captured")
+
+
+def test_copies_and_bounds_in_a_graph():
+    """A fork's copy and the bounds of the pages that new tokens lie on, captured and replayed on other
+    contents."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(43)
+    table, blocks, lens, total = _tree(rng, 1, 3, 2, 0, [5, 131, 70], spare=4)
+    new, hkv, D = [1, 140, 2], 2, 64
+    dev, _ = _pools(rng, total, hkv, D, "bf16")
+    q4 = to_dev(rng.integers(0, 256, (total, hkv, P * (D + 8)), dtype=np.uint8))
+    bnd = t.zeros((total, hkv, 2, D), dtype=t.bfloat16, device="cuda")
+    kv, batch = d.kv_pages(dev[0], dev[1], d.DSB_BF16), d.PagedBatch(table, blocks, [0] * 3, new, lens)
+    free = [p for p in range(total) if p not in set(table.ravel().tolist())]
+    src, dst, keys = [int(table[0, 2]), int(table[1, 0])], free[:2], [5, 128]
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        d.kv_copy_pages([kv], src, dst, keys)
+        d.kv_copy_pages_q4([d.kv_q4_pages(q4, D)], src, dst, keys)
+        d.kv_page_bounds(kv, batch, bnd)
+    for seed in (1, 2):
+        for x in dev:
+            x.copy_(t.from_numpy(np.random.default_rng(seed).standard_normal(x.shape)))
+        q4.copy_(to_dev(np.random.default_rng(seed).integers(0, 256, q4.shape, dtype=np.uint8)))
+        was = [x.view(t.int16).cpu().numpy() for x in dev] + [to_host(q4)]
+        graph.replay()
+        t.cuda.synchronize()
+        for x, y in zip(dev, was):
+            assert np.array_equal(to_host(x.view(t.int16)), op.copy(y, src, dst, keys))
+        assert np.array_equal(to_host(q4), op.copy_q4(was[2], D, src, dst, keys))
+        want = op.bounds(dev[0].double().cpu().numpy(), table, new, lens, np.zeros((total, hkv, 2, D)))
+        assert np.array_equal(to_host(bnd.double()), want)
+
+
+def test_4bit_copies_in_every_layer():
+    """All 40 layers' pools, whole: of the keys that are copied the source's bytes, of the others their own."""
+    d, rng = _dsb(), np.random.default_rng(44)
+    layers, n, hkv, D = 40, 5, 8, 128
+    host = rng.integers(0, 256, (layers, n, hkv, P * (D + 8)), dtype=np.uint8)
+    dev = to_dev(host)
+    src, dst, keys = [3, 3], [0, 4], [4, 7]
+    d.kv_copy_pages_q4([d.kv_q4_pages(p, D) for p in dev], src, dst, keys)
+    # which key a byte belongs to: the oracle's copy of one key's bytes onto zeros, key by key
+    owner = np.full(P * (D + 8), -1)
+    for key in range(P):
+        ones = np.full((2, 1, P * (D + 8)), 255, np.uint8)
+        ones[1] = 0
+        whole, less = (op.copy_q4(ones, D, [0], [1], [m])[1, 0] for m in (key + 1, key))
+        owner[whole != less] = key
+    assert (owner >= 0).all()
+    want = host.copy()
+    for a, b, m in zip(src, dst, keys):
+        want[:, b] = np.where(owner < m, host[:, a], host[:, b])
+    assert np.array_equal(to_host(dev), want)
+
+
+@pytest.mark.parametrize("hq,new,D", [(20, 7, 64), (20, 7, 128), (20, 600, 64), (20, 600, 128)])
+def test_bf16_weights_keep_float32s_bits(hq, new, D):
+    """A prompt whose first key is the only one with a value (1) and a score: token p's result is w / (w + p)
+    with w = exp(score) in (1/2, 1].  Off by: the score (below 1 in powers of two; the factor, q's product and
+    parts, the products' sum, the reference) 2^-22, exp2 2^-22, the sum of the weight's parts 2^-22, the sum of
+    up to 64 weights, the quotient and a join 2^-22; together 2^-20, half of the bound.  A weight as two
+    bf16 is up to 2^-18 off."""
+    d, t, rng = _dsb(), _torch(), np.random.default_rng(new + D)
+    n, rows = -(-new // P), min(new, 64)
+    k, v = (t.zeros((n, 1, P, D), dtype=t.bfloat16, device="cuda") for _ in "kv")
+    k[0, 0, 0, 0], v[0, 0, 0] = 1, 1
+    q = np.zeros((new, hq, D), np.float32)
+    q[..., 0] = rng.uniform(-np.log(2), 0, (new, hq)) * D ** 0.5
+    got = to_host(_attend(to_dev(q), [k, v], "bf16", np.arange(n, dtype=np.int32)[None], [n], [0], [new], [new]))[:rows]
+    w = np.exp(q[:rows, :, 0].astype(np.float64) / D ** 0.5)
+    want = w / (w + np.arange(rows)[:, None])
+    off = np.abs(got - want[..., None]) / want[..., None]
+    assert off.max() <= 2.0 ** -19, off.max() * 2 ** 19
+    # the same with a mistake: weights of two bf16 leave the bound
+    def bf16(x):
+        return t.from_numpy(x).bfloat16().double().numpy()
+    wrong = (bf16(w) + bf16(w - bf16(w))) / (w + np.arange(rows)[:, None])
+    assert (np.abs(wrong - want) / want).max() > 2.0 ** -19
