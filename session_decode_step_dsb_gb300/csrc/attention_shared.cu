@@ -64,12 +64,6 @@ struct Ring {
   static constexpr int smem = bars + kWarps * slots * 8;
 };
 
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -104,13 +98,6 @@ template <>
 __device__ __forceinline__ float value<__half>(__half x) { return __half2float(x); }
 template <>
 __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Whether a pair of 16-bit values holds an infinity or a NaN.
-template <typename T>
-__device__ __forceinline__ bool odd(uint32_t w) {
-  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || (w & e << 16) == e << 16;
-}
 
 template <int D, typename T, typename Walk, int N>
 __global__ void __launch_bounds__(kThreads, 2) attention_pages_kernel(

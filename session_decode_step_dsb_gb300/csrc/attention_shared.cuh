@@ -3,14 +3,15 @@
 //
 // A plan is a list of segments.  A segment is a run of pages that one or more sequences
 // read: the leading pages that several have in common, or those of one alone.  Its rows
-// are its sequences' query rows on a kv head, one sequence after the other; they are cut
-// into tiles, and a (segment, kv head, tile) is a run of pages to go through.  The runs
+// are its sequences' query rows on a kv head, one sequence after the other (of some of
+// their tokens, where all would not fit a launch); they are cut into tiles, and a (segment, kv head, tile) is a run of pages to go through.  The runs
 // lie behind each other, counted in pages, with a lead before each that stands for what it
 // takes to begin and to end one.  Each CTA takes an even share of all that, and of the runs
 // the pages that lie in it: a run has as many parts as CTAs reach into its pages, and
 // every part leaves its rows' sums in a slot of its own.  The join adds the slots of a
 // row, in order.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,6 +50,20 @@ __device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A box of a tensor map (64 columns of some keys) into shared memory; bar counts its bytes.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+// Whether a pair of 16-bit values holds an infinity or a NaN.
+template <typename T>
+__device__ __forceinline__ bool odd(uint32_t w) {
+  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
+  return (w & e) == e || (w & e << 16) == e << 16;
 }
 
 // A float32 pair as pairs of the 16-bit type that add up to it, largest first: two of fp16

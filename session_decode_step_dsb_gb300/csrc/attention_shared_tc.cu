@@ -93,12 +93,6 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
-}
 // 32 columns of this thread's row.
 __device__ __forceinline__ void tm_ld32(uint32_t at, float* v) {
   asm volatile(
@@ -153,11 +147,6 @@ __device__ __forceinline__ float half_of(uint32_t w, int which) {
     return __half2float(__ushort_as_half(h));
   else
     return __uint_as_float((uint32_t)h << 16);
-}
-template <typename T>
-__device__ __forceinline__ bool odd(uint32_t w) {  // an infinity or a NaN in a pair
-  constexpr uint32_t e = std::is_same_v<T, __half> ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || (w & e << 16) == e << 16;
 }
 
 template <int D, typename T>

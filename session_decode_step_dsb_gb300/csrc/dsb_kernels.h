@@ -369,7 +369,7 @@ cudaError_t launch_select_pages(const SelectArgs& a, int dtype, int head_dim, co
 // kv head, where its sequences are and how many, block of its first page, pages, where they
 // are, first slot, slots, first and last key that any row sees, slots of its rows in all,
 // where its tiles are or 0); the work in all; sequences of kSharedMemWords (first row,
-// first token, new tokens, length, window); pages; and where tiles of rows see only some of the
+// first token, new tokens, length up to the last of these, window); pages; and where tiles of rows see only some of the
 // segment's pages, (work of the tiles before it, first page) of each tile and the work of all.
 constexpr int kSharedSegWords = 13, kSharedMemWords = 5;
 // What a run counts for besides its pages, in pages: by what it takes to begin and to end
