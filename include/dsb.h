@@ -588,9 +588,11 @@ dsb_status dsb_kv_copy_pages_q4(const dsb_kv_q4_pages* pools, int n_pools, const
  * batch without such pages is served as well.  New token j of sequence s at position p
  * = seq_lens[s] - new_tokens[s] + j sees keys max(0, p - window[s] + 1) .. p (all up to
  * p without a window), new tokens having been appended; score = q.k / sqrt(head_dim),
- * out = softmax(score) V, float32 accuracy.  q: device float32, row t at
+ * out = softmax(score) V, float32 accuracy (where q.k is within float32's range, for
+ * keys and values up to their type's largest).  q: device float32, row t at
  * q + t * q_stride (a multiple of 4); out: device float32 [tokens][n_q_heads][head_dim],
- * apart from q's rows and the pools.  Any number of new tokens; a sequence without any
+ * apart from q's rows and the pools.  Any number of new tokens and of sequences on the
+ * same pages, under capture too; a sequence without new tokens
  * has no rows.  n_q_heads a multiple of n_kv_heads; head_dim 64 or 128.  What lies
  * behind a sequence's last key, or is hidden from a row, does not reach the row, NaN
  * and infinities included; a row that sees a NaN or an infinity in K or V has no
@@ -629,8 +631,8 @@ dsb_status dsb_kv_select_pages(const float* q, int64_t q_stride, int n_q_heads, 
 /* Decode attention over the listed pages alone: a row of token t and kv head h sees the
  * keys up to its position on the blocks selected[t][h][0 .. n_select - 1] (device int32,
  * 16-byte aligned; as dsb_kv_select_pages writes them).  Entries that are no block up to
- * the token's own (-1) are skipped, one that is listed twice counts twice; as many are
- * read as the call's longest sequence has pages.  A row that sees no key is 0.  Other
+ * the token's own (-1) are skipped, one that is listed twice counts twice; of every list
+ * as many are read as the call's longest sequence has pages.  A row that sees no key is 0.  Other
  * arguments and the workspace as dsb_attention_decode_shared; rings are
  * DSB_ERR_UNSUPPORTED. */
 dsb_status dsb_attention_decode_selected(const float* q, int64_t q_stride, int n_q_heads, const dsb_kv_pages* kv,
