@@ -160,6 +160,7 @@ struct Tree {
   std::vector<int> order;  // sequences with new tokens; a segment's are side by side
   std::vector<Segment> segs;
   std::vector<int> end;    // last segment of a sequence's path
+  bool divided = false;    // a segment does not fit a launch
 
   const int32_t* table(int s) const { return b->block_table + (size_t)s * b->max_blocks; }
   int pages(int s) const { return (b->seq_lens[s] - 1) / DSB_KV_PAGE + 1; }
@@ -206,37 +207,67 @@ struct Tree {
     if (!cut) g->table.clear();
   }
 
+  // Words that a launch's parameters have for a segment's sequences and its tiles' table, beside
+  // its pages; and of how many tiles such a table holds.
+  int room_of(int n) const { return dsbk::kParamWords - 1 - dsbk::kSharedSegWords - (int)page_words(n, wide_numbers); }
+  int places_of(int n) const { return (room_of(n) - dsbk::kSharedMemWords - 1) / 2; }
+
   int add(int parent, int m0, int m1, int b0, int b1) {
     const int tokens = tokens_of(m0, m1);
     for (constexpr int kMost = 2048; b0 < b1; b0 += kMost) {  // pages of a segment
-      const int n = std::min(kMost, b1 - b0), tile = tile_of(G * tokens, b1 - b0), group = (int)segs.size();
-      // Words that a launch's parameters have for sequences and the tiles' table; the tokens whose tiles
-      // such a table holds, and whose work is counted; the sequences.
-      const int room = dsbk::kParamWords - 1 - dsbk::kSharedSegWords - (int)page_words(n, wide_numbers);
-      const int places = (room - dsbk::kSharedMemWords - 1) / 2;
-      int share = tokens;  // of a segment of the group
-      const int tiles = (G * tokens + tile - 1) / tile, a_tile = n + Segment::lead_of(tile);
-      if ((long long)hkv * tiles * a_tile > kMostWork || (m1 - m0 == 1 && tiles > places)) {
-        long long most = kMostWork / ((long long)hkv * a_tile) * tile / G;
-        if (m1 - m0 == 1) most = std::min(most, std::max(1LL, (long long)places * tile / G));
-        const int parts = (int)((tokens + most - 1) / most);
-        share = (tokens + parts - 1) / parts;
+      Segment g{parent,       (int)segs.size(), m0, m1, 0, tokens, m1 - m0, b0, std::min(kMost, b1 - b0),
+                G * tokens, tile_of(G * tokens, b1 - b0)};
+      if (g.members == 1 && g.tiles() > 1 && g.tiles() <= places_of(g.n)) cut_tiles(&g);
+      divided = divided || !fits(g);
+      parent = g.group;
+      segs.push_back(std::move(g));
+    }
+    return parent;
+  }
+
+  bool fits(const Segment& g) const {
+    if ((long long)hkv * g.tiles() * (g.n + g.lead()) > kMostWork) return false;
+    return g.members == 1 ? g.tiles() <= places_of(g.n) : g.members <= room_of(g.n) / dsbk::kSharedMemWords;
+  }
+
+  // Groups of segments for those that do not fit a launch (once all sequences have their places
+  // in `order`).
+  void divide() {
+    std::vector<Segment> out;
+    std::vector<int> to(segs.size());
+    for (size_t i = 0; i < segs.size(); ++i) {
+      Segment& whole = segs[i];
+      if (whole.parent >= 0) whole.parent = to[whole.parent];
+      whole.group = to[i] = (int)out.size();
+      if (fits(whole)) {
+        out.push_back(std::move(whole));
+        continue;
       }
-      for (int t0 = 0, m = m0, m_end = 0; t0 < tokens;) {  // m: the sequence of t0, whose tokens end at m_end
-        Segment g{parent, group, m0, m1, t0, t0, 0, b0, n, 0, tile};
-        while (g.t1 < std::min(t0 + share, tokens) && g.members < room / dsbk::kSharedMemWords) {
+      // tokens of a segment: whose work counts, and whose tiles a table holds
+      const int tokens = whole.t1, places = places_of(whole.n), most_members = room_of(whole.n) / dsbk::kSharedMemWords;
+      long long most = kMostWork / ((long long)hkv * (whole.n + whole.lead())) * whole.tile / G;
+      if (whole.members == 1) most = std::min(most, std::max(1LL, (long long)places * whole.tile / G));
+      const int parts = (int)((tokens + most - 1) / most), share = (tokens + parts - 1) / parts;
+      for (int t0 = 0, m = whole.m0, m_end = 0; t0 < tokens;) {  // m_end: of the tokens of sequences before m
+        Segment g = whole;
+        g.t0 = g.t1 = t0;
+        g.members = 0;
+        g.table.clear();
+        while (g.t1 < std::min(t0 + share, tokens) && g.members < most_members) {
           while (m_end <= g.t1) m_end += b->new_tokens[order[m++]];
           g.t1 = std::min({t0 + share, tokens, m_end});
           ++g.members;
         }
         g.rows = G * (g.t1 - t0);
-        if (m1 - m0 == 1 && g.tiles() > 1 && g.tiles() <= places) cut_tiles(&g);  // (more: one token's, which see the same)
+        // (more tiles than that are one token's, which see the same)
+        if (whole.members == 1 && g.tiles() > 1 && g.tiles() <= places) cut_tiles(&g);
         t0 = g.t1;
-        segs.push_back(std::move(g));
+        out.push_back(std::move(g));
       }
-      parent = group;
     }
-    return parent;
+    for (int& e : end)
+      if (e >= 0) e = to[e];
+    segs.swap(out);
   }
 
   // Segments of order[m0, m1), which have blocks 0 .. known - 1 in common and those before
@@ -347,6 +378,7 @@ struct Tree {
       }
     }
     for (int m = linear; m < (int)order.size(); ++m) split(m, m + 1, 0, 0, -1);
+    if (divided) divide();
   }
 };
 

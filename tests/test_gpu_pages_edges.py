@@ -75,17 +75,19 @@ def test_selected_pages_of_long_prompts_and_many_heads():
 
 
 # ------------------------------------------------- many sessions, large groups
-@pytest.mark.parametrize("groups,per,branch", [(1, 1024, 0), (128, 8, 3)])
-def test_a_thousand_sessions_behind_one_prompt(groups, per, branch):
-    """More sessions on the same pages than one launch's metadata holds, called and captured."""
-    d, rng = _dsb(), np.random.default_rng(per)
+@pytest.mark.parametrize("groups,per,branch,most", [(1, 1024, 0, 1), (128, 8, 3, 1), (1, 1024, 0, 4), (4, 256, 1, 3)])
+def test_a_thousand_sessions_behind_one_prompt(groups, per, branch, most):
+    """More sessions on the same pages than one launch's metadata holds, of one or of up to `most` new
+    tokens each, called and captured."""
+    d, rng = _dsb(), np.random.default_rng(per + most)
     n, hq, D = 1024, 2, 64
-    table, blocks, lens, total = _tree(rng, groups, per, 2, branch, rng.integers(1, 200, n))
+    table, blocks, lens, total = _tree(rng, groups, per, 2, branch, rng.integers(most, 200, n))
+    new = [1] * n if most == 1 else rng.integers(0, most + 1, n).tolist()
     dev, (k, v) = _pools(rng, total, 1, D, "f16")
-    q = rng.standard_normal((n, hq, D)).astype(np.float32)
-    want, bound = op.attention(q, k, v, table, blocks, [0] * n, [1] * n, lens)
-    qd, kv, batch = to_dev(q), d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, blocks, [0] * n, [1] * n, lens)
-    ws = d.Workspace(n, hq, D, max(lens))
+    q = rng.standard_normal((sum(new), hq, D)).astype(np.float32)
+    want, bound = op.attention(q, k, v, table, blocks, [0] * n, new, lens)
+    qd, kv, batch = to_dev(q), d.kv_pages(dev[0], dev[1], d.DSB_F16), d.PagedBatch(table, blocks, [0] * n, new, lens)
+    ws = d.Workspace(sum(new), hq, D, max(lens))
     call = lambda: d.attention_decode_shared(qd, kv, batch, ws)
     _check(call(), want, bound, "called")
     _check(_captured(call), want, bound, "captured")
