@@ -589,12 +589,12 @@ dsb_status dsb_kv_copy_pages_q4(const dsb_kv_q4_pages* pools, int n_pools, const
  * = seq_lens[s] - new_tokens[s] + j sees keys max(0, p - window[s] + 1) .. p (all up to
  * p without a window), new tokens having been appended; score = q.k / sqrt(head_dim),
  * out = softmax(score) V, float32 accuracy (where q.k is within float32's range, for
- * keys and values up to their type's largest).  q: device float32, row t at
- * q + t * q_stride (a multiple of 4); out: device float32 [tokens][n_q_heads][head_dim],
- * apart from q's rows and the pools.  Any number of new tokens and of sequences on the
- * same pages, under capture too; a sequence without new tokens
- * has no rows.  n_q_heads a multiple of n_kv_heads; head_dim 64 or 128.  What lies
- * behind a sequence's last key, or is hidden from a row, does not reach the row, NaN
+ * keys and values up to their type's largest; of bf16 values below 2^-100 long sequences
+ * keep fewer bits).  q: device float32, row t at q + t * q_stride (a multiple of 4); out:
+ * device float32 [tokens][n_q_heads][head_dim], apart from q's rows and the pools.  Any
+ * number of new tokens and of sequences on the same pages, under capture too; a sequence
+ * without new tokens has no rows.  n_q_heads a multiple of n_kv_heads; head_dim 64 or 128.
+ * What lies behind a sequence's last key, or is hidden from a row, does not reach the row, NaN
  * and infinities included; a row that sees a NaN or an infinity in K or V has no
  * finite result where it counts.  Partial sums go to the workspace:
  * dsb_workspace_bytes(tokens, n_q_heads, head_dim, longest seq_lens) is enough.  The
